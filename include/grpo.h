@@ -61,7 +61,9 @@ typedef enum {
     GRPO_ERR_CUDA = 5,         /* a CUDA runtime call or kernel launch failed */
     GRPO_ERR_TOKEN_RANGE = 6,  /* a scored token id was outside [0, V)        */
     GRPO_ERR_LENGTH_RANGE = 7, /* a completion length was outside [0, C]      */
-    GRPO_ERR_TIMEOUT = 8       /* a bounded device-side wait gave up          */
+    GRPO_ERR_TIMEOUT = 8,      /* a bounded device-side wait gave up          */
+    GRPO_ERR_VALUE = 9         /* a gradient norm is not finite, or a row of
+                                  probabilities (or a temperature) is undefined */
 } grpo_status;
 
 typedef enum { GRPO_F32 = 0, GRPO_BF16 = 1 } grpo_dtype;
@@ -454,11 +456,145 @@ grpo_status grpo_lmhead_loss_bwd_ex(const void *hidden, const void *weight, int6
                                     grpo_stream_t stream);
 
 /*
+ * grpo_embed_fwd -- embedding lookup with scaling, the way into the model that
+ * the LM head above is the way out of:
+ *   out[i, :] = scale * weight[ids[i], :]
+ * ids [n] int64; weight: V rows of d elements of `wdtype`, ldw >= d elements
+ * apart; out: n rows of d elements of `odtype`, ldo >= d apart (float32 or
+ * bfloat16 each, aligned to their element).  The product is taken in float32
+ * and rounded once.  An id outside [0, V) gives a row of NaN.  scale is
+ * finite; n and V below 2^31 - 2^16; d at most 2^24.  Rows whose address and
+ * pitch are multiples of 16 bytes (and d of 8) move in 16-byte accesses.
+ */
+grpo_status grpo_embed_fwd(const int64_t *ids, int64_t n, const void *weight, grpo_dtype wdtype,
+                           int64_t V, int64_t d, int64_t ldw, float scale, void *out,
+                           grpo_dtype odtype, int64_t ldo, grpo_stream_t stream);
+
+/*
+ * grpo_embed_bwd -- the lookup's gradient:
+ *   dweight[v, :] = scale * sum over { i : ids[i] = v } of dout[i, :]
+ * or, with accumulate != 0, dweight[v, :] += the same: for tied weights, into
+ * the dweight that grpo_lmhead_loss_bwd wrote.  Without accumulate every row
+ * is written (zeros for ids that do not occur); with it the rows of ids that
+ * do not occur are neither read nor written.  Tokens whose id is pad_id (a
+ * negative pad_id: none) and ids outside [0, V) contribute nothing, and their
+ * dout rows are not read; the latter are reported by grpo_check_error as
+ * GRPO_ERR_TOKEN_RANGE.
+ *
+ * dout: n rows of d elements of `ddtype`, ldd apart; dweight: V rows of
+ * `wdtype`, ldw apart.  The tokens are sorted by id (stable) and each id's
+ * rows added in float32 in a fixed order that depends on the ids alone, so
+ * results are bitwise reproducible; one rounding to `wdtype`.
+ * workspace: at least grpo_embed_workspace_size(n, V, d) bytes (about 16
+ * bytes per token, 2 * d * 4 / 32 bytes per token of partial sums, one byte
+ * per id).
+ */
+grpo_status grpo_embed_workspace_size(int64_t n, int64_t V, int64_t d, size_t *bytes);
+grpo_status grpo_embed_bwd(const int64_t *ids, int64_t n, const void *dout, grpo_dtype ddtype,
+                           int64_t V, int64_t d, int64_t ldd, float scale, int64_t pad_id,
+                           void *dweight, grpo_dtype wdtype, int64_t ldw, int accumulate,
+                           void *workspace, size_t workspace_bytes, grpo_stream_t stream);
+
+/* One dense tensor of the gradient calls below.  out: where the clipped values
+ * go; NULL or data itself: in place (then out_dtype == dtype). */
+typedef struct {
+    const void *data;
+    void *out;
+    int64_t numel;
+    grpo_dtype dtype;
+    grpo_dtype out_dtype;
+} grpo_tensor;
+
+typedef enum {
+    GRPO_NORM_L2 = 0, /* sqrt of the sum of squares over all tensors */
+    GRPO_NORM_MAX = 1 /* largest absolute value                      */
+} grpo_norm_type;
+
+/*
+ * grpo_clip_grad_norm -- the gradients' global norm, and clipping by it (the
+ * step between the backward and the optimizer):
+ *   norm = over all `count` tensors together
+ *   coef = min(1, max_norm / (norm + eps))
+ *   out  = coef * data, element by element (float32 product, one rounding)
+ * tensors: HOST array (read before the call returns; the pointers in it are
+ * device pointers, aligned to their element, dense, not overlapping one
+ * another except out == data).  stats: two float32 in device memory, norm and
+ * coef.  In place with coef = 1 nothing is written; with another output
+ * everything is.  max_norm >= 0 (infinity: no limit), eps >= 0.
+ * Squares are summed in float32 per thread and batch and in float64 beyond,
+ * scaled by a power of two where they would leave float32's range, in a fixed
+ * order: results are bitwise reproducible.  A norm that is not finite is
+ * reported by grpo_check_error as GRPO_ERR_VALUE; the formula is followed
+ * (an infinite norm gives coef 0, NaN stays NaN).
+ * workspace: at least grpo_grad_norm_workspace_size(count) bytes.
+ *
+ * grpo_grad_norm -- the norm alone (coef = 1): out pointers are not used.
+ */
+grpo_status grpo_grad_norm_workspace_size(int64_t count, size_t *bytes);
+grpo_status grpo_clip_grad_norm(const grpo_tensor *tensors, int64_t count, grpo_norm_type type,
+                                float max_norm, float eps, float *stats, void *workspace,
+                                size_t workspace_bytes, grpo_stream_t stream);
+grpo_status grpo_grad_norm(const grpo_tensor *tensors, int64_t count, grpo_norm_type type,
+                           float *stats, void *workspace, size_t workspace_bytes,
+                           grpo_stream_t stream);
+
+/*
+ * grpo_verify_drafts -- verification of drafted tokens against the target
+ * policy, from random numbers that the caller gives: the rollout's step that
+ * makes the completions and their log-probs (old_logp of the loss at
+ * temperature 1).
+ *
+ * For sequence i with L_i = draft_len[i] (NULL: K) drafted tokens x_j, target
+ * logits rows z_j (the logits after j drafted tokens; j = 0 .. L_i), draft
+ * logits rows y_j (j < L_i) and T = temperature[i] (NULL: 1):
+ *   p_j = softmax(z_j / T); q_j = softmax(y_j / T), or without draft logits
+ *   (draft_logits NULL: tokens copied from elsewhere) all mass on x_j;
+ *   x_j is accepted while u_j * q_j(x_j) < p_j(x_j);
+ *   a = n_accepted[i]: the first j not accepted, or L_i;
+ *   the emitted token is argmax_v of
+ *       max(p_a(v) - q_a(v), 0) / noise[i, v]   if a < L_i (of p_a(v) / noise
+ *                                               if no such term is positive),
+ *       p_a(v) / noise[i, v]                    if a = L_i,
+ *   the lowest v of equal ones.  With u uniform in [0, 1) and noise
+ *   exponential the accepted and emitted tokens are distributed as the
+ *   target's samples.  T = 0 (below 1e-6): x_j is accepted while it is the
+ *   lowest argmax of z_j, and that argmax is emitted; u and noise of the
+ *   sequence are not read, and its log-probs are those of T = 1.
+ * L_i = 0 (or K = 0) samples one token.  Rows after the first rejection are
+ * not read.
+ *
+ * target_logits: row j of sequence i starts at element i * target_seq + j *
+ * target_row; draft_logits the same with its strides (ignored when NULL);
+ * both of `dtype`, aligned to their element.  draft_tokens [N, K] int64, u
+ * [N, K] float32, noise float32 rows noise_row apart, positive and finite.
+ * Outputs: tokens [N, K+1] int64 (the accepted ones, the emitted one, then
+ * -1), n_accepted [N] int32, logp [N, K+1] float32 (log p_j of tokens[i, j],
+ * then 0).
+ * A row whose distribution is undefined (NaN or +inf in it, nothing but -inf;
+ * a temperature that is negative, NaN or infinite) stops its sequence there
+ * with token -1 and logp NaN, GRPO_ERR_VALUE by grpo_check_error; a drafted
+ * id outside [0, V) is not accepted (GRPO_ERR_TOKEN_RANGE), a length outside
+ * [0, K] clamped (GRPO_ERR_LENGTH_RANGE).
+ * Decisions are made in float64 from float32 sums, bitwise reproducibly.
+ * K <= 2^20.  workspace: at least grpo_verify_workspace_size(N) bytes.
+ */
+grpo_status grpo_verify_workspace_size(int64_t N, size_t *bytes);
+grpo_status grpo_verify_drafts(const void *target_logits, const void *draft_logits,
+                               grpo_dtype dtype, int64_t N, int64_t K, int64_t V,
+                               int64_t target_seq, int64_t target_row, int64_t draft_seq,
+                               int64_t draft_row, const int64_t *draft_tokens,
+                               const int32_t *draft_len, const float *u, const float *noise,
+                               int64_t noise_row, const float *temperature, int64_t *tokens,
+                               int32_t *n_accepted, float *logp, void *workspace,
+                               size_t workspace_bytes, grpo_stream_t stream);
+
+/*
  * grpo_check_error -- synchronises `stream`, then reports what the kernels of
- * the most recent grpo_loss_fwd on `workspace` recorded: GRPO_OK,
+ * the most recent call on `workspace` (grpo_loss_fwd and its relatives,
+ * grpo_embed_bwd, grpo_clip_grad_norm, grpo_verify_drafts) recorded: GRPO_OK,
  * GRPO_ERR_TOKEN_RANGE (a scored id outside [0, V); its logp and lse are NaN),
- * GRPO_ERR_LENGTH_RANGE (a length outside [0, C]; it was clamped), or
- * GRPO_ERR_TIMEOUT.  GRPO_ERR_CUDA if the synchronisation itself failed.
+ * GRPO_ERR_LENGTH_RANGE (a length outside [0, C]; it was clamped),
+ * GRPO_ERR_TIMEOUT, or GRPO_ERR_VALUE.  GRPO_ERR_CUDA if the synchronisation itself failed.
  */
 grpo_status grpo_check_error(const void *workspace, grpo_stream_t stream);
 

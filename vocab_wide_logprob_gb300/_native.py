@@ -21,11 +21,13 @@ STATUS_NAMES = {
     0: "GRPO_OK", 1: "GRPO_ERR_INVALID_ARG", 2: "GRPO_ERR_UNSUPPORTED",
     3: "GRPO_ERR_WORKSPACE", 4: "GRPO_ERR_MISALIGNED", 5: "GRPO_ERR_CUDA",
     6: "GRPO_ERR_TOKEN_RANGE", 7: "GRPO_ERR_LENGTH_RANGE", 8: "GRPO_ERR_TIMEOUT",
+    9: "GRPO_ERR_VALUE",
 }
 GRPO_F32, GRPO_BF16 = 0, 1
 GRPO_ADV_DR, GRPO_ADV_STD = 0, 1
 GRPO_AGG_TOKEN_SUM, GRPO_AGG_SEQ_MEAN = 0, 1
 GRPO_BWD_SKIP_ZERO_WEIGHT = 1
+GRPO_NORM_L2, GRPO_NORM_MAX = 0, 1
 
 
 class GrpoError(RuntimeError):
@@ -80,6 +82,16 @@ def _load():
                                                 INT),
         "grpo_lmhead_loss_bwd_ex": ([P, P, I64, I64, I64, I64, I64, P, P, P, P, P, P, P,
                                      ctypes.c_uint32, P, SZ, P], INT),
+        "grpo_embed_fwd": ([P, I64, P, INT, I64, I64, I64, F, P, INT, I64, P], INT),
+        "grpo_embed_workspace_size": ([I64, I64, I64, ctypes.POINTER(SZ)], INT),
+        "grpo_embed_bwd": ([P, I64, P, INT, I64, I64, I64, F, I64, P, INT, I64, INT, P, SZ, P],
+                           INT),
+        "grpo_grad_norm_workspace_size": ([I64, ctypes.POINTER(SZ)], INT),
+        "grpo_clip_grad_norm": ([P, I64, INT, F, F, P, P, SZ, P], INT),
+        "grpo_grad_norm": ([P, I64, INT, P, P, SZ, P], INT),
+        "grpo_verify_workspace_size": ([I64, ctypes.POINTER(SZ)], INT),
+        "grpo_verify_drafts": ([P, P, INT, I64, I64, I64, I64, I64, I64, I64, P, P, P, P, I64, P,
+                                P, P, P, P, SZ, P], INT),
         "grpo_lmhead_loss_bwd": ([P, P, I64, I64, I64, I64, I64, P, P, P, P, P, P, P, P, SZ, P],
                                  INT),
     }
@@ -509,6 +521,247 @@ def grpo_lmhead_loss_bwd(hidden, weight, P, input_ids, lens, lse, w, grad_loss=N
     else:
         _check(_lib.grpo_lmhead_loss_bwd_ex(*head, int(flags), *tail), "grpo_lmhead_loss_bwd_ex")
     return out[0], out[1], workspace
+
+
+def _rows(t, name, device=None):
+    """Dtype code and row pitch of a matrix whose rows are dense (a view of
+    wider rows is taken as it is)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype not in _CODE:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    r, c = t.shape
+    pitch = t.stride(0) if r > 1 else max(t.stride(0), c)
+    if (c > 1 and t.stride(1) != 1) or pitch < c:
+        raise ValueError(f"{name} must have dense rows")
+    return _CODE[t.dtype], pitch
+
+
+_CODE = {torch.float32: GRPO_F32, torch.bfloat16: GRPO_BF16}
+
+
+def grpo_embed_fwd(ids, weight, scale=1.0, out=None, out_dtype=None, stream=None):
+    """``scale * weight[ids]``: ids int64 of any shape, weight [V, d] float32
+    or bfloat16 (rows may be part of wider ones).  Returns ``out`` [*ids.shape,
+    d] in ``out_dtype`` (the weight's when None); a given ``out`` may be a view
+    [n, d] of wider rows.  An id outside [0, V) gives a row of NaN."""
+    _dev(ids, "ids", torch.int64)
+    wcode, ldw = _rows(weight, "weight", ids.device)
+    V, d = weight.shape
+    n = ids.numel()
+    if out is None:
+        out = torch.empty((*ids.shape, d), dtype=out_dtype or weight.dtype, device=ids.device)
+        flat = out.view(n, d)
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
+        if tuple(out.shape) not in ((*ids.shape, d), (n, d)):
+            raise ValueError("out must be [*ids.shape, d]")
+        flat = out if out.dim() == 2 else out.view(n, d)
+    ocode, ldo = _rows(flat, "out", ids.device)
+    _check(_lib.grpo_embed_fwd(_ptr(ids), n, _ptr(weight), wcode, V, d, ldw, float(scale),
+                               _ptr(flat), ocode, ldo, _stream(stream)), "grpo_embed_fwd")
+    return out
+
+
+def grpo_embed_workspace_size(n: int, V: int, d: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(_lib.grpo_embed_workspace_size(n, V, d, ctypes.byref(out)),
+           "grpo_embed_workspace_size")
+    return int(out.value)
+
+
+def grpo_embed_bwd(ids, dout, V, scale=1.0, pad_id=None, dweight=None, accumulate=False,
+                   out_dtype=None, workspace=None, stream=None):
+    """Gradient of :func:`grpo_embed_fwd` with respect to the weight: ``dout``
+    [*ids.shape, d] float32 or bfloat16 -> ``(dweight [V, d], workspace)``,
+    dweight in ``out_dtype`` (float32 when None).  With ``accumulate`` the
+    gradient is added to the given ``dweight`` (for example the LM head's, with
+    tied weights).  Tokens equal to ``pad_id`` contribute nothing."""
+    _dev(ids, "ids", torch.int64)
+    n = ids.numel()
+    if dout.shape[:-1] != ids.shape and tuple(dout.shape[:-1]) != (n,):
+        raise ValueError("dout must be [*ids.shape, d]")
+    d = dout.shape[-1]
+    flat = dout if dout.dim() == 2 else dout.view(n, d)
+    dcode, ldd = _rows(flat, "dout", ids.device)
+    if dweight is None:
+        if accumulate:
+            raise ValueError("accumulate needs a dweight")
+        dweight = torch.empty((V, d), dtype=out_dtype or torch.float32, device=ids.device)
+    elif out_dtype is not None and dweight.dtype != out_dtype:
+        raise TypeError(f"dweight must be {out_dtype}, got {dweight.dtype}")
+    if tuple(dweight.shape) != (V, d):
+        raise ValueError("dweight must be [V, d]")
+    wcode, ldw = _rows(dweight, "dweight", ids.device)
+    need = grpo_embed_workspace_size(n, V, d)
+    if workspace is None or workspace.numel() < need:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=ids.device)
+    pad = -1 if pad_id is None else int(pad_id)
+    _check(_lib.grpo_embed_bwd(_ptr(ids), n, _ptr(flat), dcode, V, d, ldd, float(scale), pad,
+                               _ptr(dweight), wcode, ldw, 1 if accumulate else 0, _ptr(workspace),
+                               workspace.numel(), _stream(stream)), "grpo_embed_bwd")
+    return dweight, workspace
+
+
+class _Tensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int)]
+
+
+def _tensor_table(grads, outs):
+    """The grpo_tensor array of a list of dense tensors (and their outputs)."""
+    if not all([t.is_cuda and t.is_contiguous() for t in grads]):
+        raise ValueError("every gradient must be a contiguous CUDA tensor")
+    codes = [_CODE.get(t.dtype) for t in grads]
+    if None in codes:
+        raise TypeError("gradients must be float32 or bfloat16")
+    n = len(grads)
+    table = (_Tensor * n)()
+    if outs is None:
+        rows = [(t.data_ptr(), None, t.numel(), c, c) for t, c in zip(grads, codes)]
+    else:
+        if len(outs) != n:
+            raise ValueError("out must have one tensor per gradient")
+        if not all([o.is_cuda and o.is_contiguous() and o.numel() == t.numel()
+                    for o, t in zip(outs, grads)]):
+            raise ValueError("every out must be a contiguous CUDA tensor of its gradient's size")
+        ocodes = [_CODE.get(o.dtype) for o in outs]
+        if None in ocodes:
+            raise TypeError("outputs must be float32 or bfloat16")
+        rows = [(t.data_ptr(), o.data_ptr(), t.numel(), c, oc)
+                for t, o, c, oc in zip(grads, outs, codes, ocodes)]
+    for k, r in enumerate(rows):
+        table[k] = r
+    return table
+
+
+def grpo_grad_norm_workspace_size(count: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(_lib.grpo_grad_norm_workspace_size(count, ctypes.byref(out)),
+           "grpo_grad_norm_workspace_size")
+    return int(out.value)
+
+
+def _clip_buffers(grads, stats, workspace):
+    dev = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
+    if stats is None:
+        stats = torch.empty((2,), dtype=torch.float32, device=dev)
+    _dev(stats, "stats", torch.float32)
+    if stats.numel() < 2:
+        raise ValueError("stats must hold two values")
+    need = grpo_grad_norm_workspace_size(len(grads))
+    if workspace is None or workspace.numel() < need:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    return stats, workspace
+
+
+def grpo_clip_grad_norm(grads, max_norm, out=None, norm_type=GRPO_NORM_L2, eps=1e-6, stats=None,
+                        workspace=None, stream=None):
+    """Clips the list of gradients ``grads`` (dense float32 or bfloat16, any
+    mixture) by their global norm, in place or into the tensors of ``out``.
+    Returns ``(stats, workspace)``, stats = [norm, coefficient] float32 on the
+    device."""
+    grads = list(grads)
+    stats, workspace = _clip_buffers(grads, stats, workspace)
+    table = _tensor_table(grads, out)
+    _check(_lib.grpo_clip_grad_norm(table, len(grads), int(norm_type), float(max_norm), float(eps),
+                                    _ptr(stats), _ptr(workspace), workspace.numel(),
+                                    _stream(stream)), "grpo_clip_grad_norm")
+    return stats, workspace
+
+
+def grpo_grad_norm(grads, norm_type=GRPO_NORM_L2, stats=None, workspace=None, stream=None):
+    """The global norm of ``grads`` alone: ``(stats, workspace)``, stats =
+    [norm, 1]."""
+    grads = list(grads)
+    stats, workspace = _clip_buffers(grads, stats, workspace)
+    table = _tensor_table(grads, None)
+    _check(_lib.grpo_grad_norm(table, len(grads), int(norm_type), _ptr(stats), _ptr(workspace),
+                               workspace.numel(), _stream(stream)), "grpo_grad_norm")
+    return stats, workspace
+
+
+def grpo_verify_workspace_size(N: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(_lib.grpo_verify_workspace_size(N, ctypes.byref(out)), "grpo_verify_workspace_size")
+    return int(out.value)
+
+
+def _logit_rows(t, name, shape):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    N, R, V = shape
+    row = t.stride(1) if R > 1 else max(t.stride(1), V)
+    seq = t.stride(0) if N > 1 else max(t.stride(0), R * row)
+    if (V > 1 and t.stride(2) != 1) or row < V or (N > 1 and seq < (R - 1) * row + V):
+        raise ValueError(f"{name} must have dense rows that do not overlap")
+    return seq, row
+
+
+def grpo_verify_drafts(target_logits, draft_tokens, u, noise, draft_logits=None, draft_lens=None,
+                       temperature=None, out=None, workspace=None, stream=None):
+    """Verifies drafted tokens against the target policy.  ``target_logits``
+    [N, K+1, V] and ``draft_logits`` [N, K, V] (None: copied drafts without
+    probabilities) float32 or bfloat16, views of padded rows included;
+    ``draft_tokens`` [N, K] int64, ``u`` [N, K] uniform and ``noise`` [N, V]
+    exponential float32 random numbers, ``draft_lens`` [N] int32 (None: K each),
+    ``temperature`` [N] float32 (None: 1; 0: greedy).  Returns a dict with
+    ``tokens`` [N, K+1] int64 (accepted, emitted, then -1), ``n_accepted`` [N]
+    int32, ``logp`` [N, K+1] float32 and ``workspace``; pass it as ``out`` to
+    reuse the buffers."""
+    if target_logits.dim() != 3:
+        raise ValueError("target_logits must be [N, K+1, V]")
+    N, K, V = target_logits.shape[0], target_logits.shape[1] - 1, target_logits.shape[2]
+    if K < 0:
+        raise ValueError("target_logits must have at least one row per sequence")
+    if target_logits.dtype not in _CODE:
+        raise TypeError(f"target_logits must be float32 or bfloat16, got {target_logits.dtype}")
+    tseq, trow = _logit_rows(target_logits, "target_logits", (N, K + 1, V))
+    dseq = drow = 0
+    if draft_logits is not None:
+        if draft_logits.dtype != target_logits.dtype:
+            raise TypeError("draft_logits must have target_logits' dtype")
+        dseq, drow = _logit_rows(draft_logits, "draft_logits", (N, K, V))
+    for name, t, dt, shape in (("draft_tokens", draft_tokens, torch.int64, (N, K)),
+                               ("u", u, torch.float32, (N, K)),
+                               ("draft_lens", draft_lens, torch.int32, (N,)),
+                               ("temperature", temperature, torch.float32, (N,))):
+        _dev(t, name, dt)
+        if t is not None and tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if noise.dtype != torch.float32 or tuple(noise.shape) != (N, V):
+        raise ValueError("noise must be float32 [N, V]")
+    _, nrow = _rows(noise, "noise", target_logits.device)
+    dev = target_logits.device
+    if out is None:
+        out = {"tokens": torch.empty((N, K + 1), dtype=torch.int64, device=dev),
+               "n_accepted": torch.empty((N,), dtype=torch.int32, device=dev),
+               "logp": torch.empty((N, K + 1), dtype=torch.float32, device=dev)}
+    else:
+        for name, dt, shape in (("tokens", torch.int64, (N, K + 1)),
+                                ("n_accepted", torch.int32, (N,)),
+                                ("logp", torch.float32, (N, K + 1))):
+            _dev(out[name], name, dt)
+            if tuple(out[name].shape) != shape:
+                raise ValueError(f"{name} must be {list(shape)}")
+        workspace = out.get("workspace") if workspace is None else workspace
+    need = grpo_verify_workspace_size(N)
+    if workspace is None or workspace.numel() < need:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    out["workspace"] = workspace
+    _check(_lib.grpo_verify_drafts(
+        _ptr(target_logits), _ptr(draft_logits), _CODE[target_logits.dtype], N, K, V, tseq, trow,
+        dseq, drow, _ptr(draft_tokens), _ptr(draft_lens), _ptr(u), _ptr(noise), nrow,
+        _ptr(temperature), _ptr(out["tokens"]), _ptr(out["n_accepted"]), _ptr(out["logp"]),
+        _ptr(workspace), workspace.numel(), _stream(stream)), "grpo_verify_drafts")
+    return out
 
 
 def grpo_set_early_start(enable: bool) -> None:

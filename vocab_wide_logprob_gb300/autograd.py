@@ -2,9 +2,10 @@
 backward grpo_loss_bwd (d loss / d logits, "loss.backward()" of "Making Dr
 GRPO go brrr", salahadawi.com), both through the C ABI; torch only holds
 the tensors.  GRPOLMHeadLoss does the same from hidden states and the LM head
-(grpo_lmhead_loss_fwd / grpo_lmhead_loss_bwd).
+(grpo_lmhead_loss_fwd / grpo_lmhead_loss_bwd).  GRPOEmbedding is the
+embedding lookup (grpo_embed_fwd / grpo_embed_bwd).
 
-Only the logits (or the hidden states and the LM head) receive a gradient.  The advantages, old and reference
+Of the losses, only the logits (or the hidden states and the LM head) receive a gradient.  The advantages, old and reference
 log-probs are constants of the update step (the advantage comes from the
 rewards, the old and reference log-probs from no-grad passes), so their
 gradients are None.
@@ -44,6 +45,34 @@ def grpo_loss(logits, P, input_ids, lens, adv, old_logp=None, ref_logp=None, eps
     """Functional form of :class:`GRPOLoss` (differentiable in ``logits``)."""
     return GRPOLoss.apply(logits, P, input_ids, lens, adv, old_logp, ref_logp, eps, beta, norm,
                           agg)
+
+
+class GRPOEmbedding(torch.autograd.Function):
+    """out = GRPOEmbedding.apply(ids, weight, scale, pad_id, out_dtype):
+    grpo_embed_fwd, differentiable in ``weight`` [V, d]; the backward is
+    grpo_embed_bwd (summed in float32, handed over in the weight's dtype).
+    Tokens equal to ``pad_id`` give no gradient."""
+
+    @staticmethod
+    def forward(ctx, ids, weight, scale=1.0, pad_id=None, out_dtype=None):
+        ids = ids.contiguous()
+        ctx.save_for_backward(ids)
+        ctx.V, ctx.scale, ctx.pad_id, ctx.wdtype = weight.shape[0], scale, pad_id, weight.dtype
+        return g.grpo_embed_fwd(ids, weight, scale, out_dtype=out_dtype)
+
+    @staticmethod
+    def backward(ctx, dout):
+        (ids,) = ctx.saved_tensors
+        # (the gradient of a broadcast or transposed use arrives with other strides)
+        dw, _ = g.grpo_embed_bwd(ids, dout.contiguous(), ctx.V, ctx.scale, ctx.pad_id,
+                                 out_dtype=ctx.wdtype)
+        return None, dw, None, None, None
+
+
+def grpo_embed(ids, weight, scale=1.0, pad_id=None, out_dtype=None):
+    """Functional form of :class:`GRPOEmbedding` (differentiable in
+    ``weight``)."""
+    return GRPOEmbedding.apply(ids, weight, scale, pad_id, out_dtype)
 
 
 class GRPOLMHeadLoss(torch.autograd.Function):

@@ -6,12 +6,15 @@
 
 #include <atomic>
 #include <map>
+#include <memory>
 #include <mutex>
+#include <new>
 #include <utility>
 
 #include "common.cuh"
 #include "host_ctx.cuh"
 #include "lmhead.cuh"
+#include "ops.cuh"
 #include "host_rows.cuh"
 #include "selftest.cuh"
 #include "grpo.h"
@@ -188,6 +191,8 @@ const char* grpo_status_string(grpo_status s) {
       return "a completion length is outside [0, C]";
     case GRPO_ERR_TIMEOUT:
       return "a device-side wait timed out";
+    case GRPO_ERR_VALUE:
+      return "a norm is not finite, or a row of probabilities is undefined";
   }
   return "unknown status";
 }
@@ -895,17 +900,304 @@ grpo_status grpo_lmhead_loss_bwd_ex(const void* hidden, const void* weight, int6
   return GRPO_OK;
 }
 
+// ---- the operators around the loss ----------------------------------------------
+
+}  // extern "C"
+
+namespace {
+
+// A matrix of `rows` rows of d elements, `ld` apart: fits int64 bytes.
+bool matrix_fits(int64_t rows, int64_t ld) { return mul3(rows, ld, 8) >= 0; }
+size_t matrix_bytes(int64_t rows, int64_t d, int64_t ld, grpo_dtype t) {
+  return rows < 1 ? 0 : ((size_t)(rows - 1) * (size_t)ld + (size_t)d) * (t == GRPO_F32 ? 4 : 2);
+}
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return na > 0 && nb > 0 && x < y + nb && y < x + na;
+}
+bool known_dtype(grpo_dtype t) { return t == GRPO_F32 || t == GRPO_BF16; }
+size_t esize_of(grpo_dtype t) { return t == GRPO_F32 ? 4 : 2; }
+
+constexpr int64_t kMaxEmbedDim = (int64_t)1 << 24;
+
+// Shape checks shared by the embedding calls.
+grpo_status check_embed(int64_t n, int64_t V, int64_t d, int64_t ldw, int64_t ldx) {
+  if (n < 0 || V < 1 || d < 1 || ldw < d || ldx < d) return GRPO_ERR_INVALID_ARG;
+  if (n > INT32_MAX - 65536 || V > INT32_MAX - 65536 || d > kMaxEmbedDim ||
+      !matrix_fits(V, ldw) || !matrix_fits(n, ldx))
+    return GRPO_ERR_UNSUPPORTED;
+  return GRPO_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+grpo_status grpo_embed_fwd(const int64_t* ids, int64_t n, const void* weight, grpo_dtype wdtype,
+                           int64_t V, int64_t d, int64_t ldw, float scale, void* out,
+                           grpo_dtype odtype, int64_t ldo, grpo_stream_t stream) {
+  if (!known_dtype(wdtype) || !known_dtype(odtype)) return GRPO_ERR_UNSUPPORTED;
+  const grpo_status s = check_embed(n, V, d, ldw, ldo);
+  if (s != GRPO_OK) return s;
+  if (isnan(scale) || isinf(scale)) return GRPO_ERR_INVALID_ARG;
+  if (n == 0) return GRPO_OK;
+  if (ids == nullptr || weight == nullptr || out == nullptr) return GRPO_ERR_INVALID_ARG;
+  if (!aligned(ids, 8) || !aligned(weight, esize_of(wdtype)) || !aligned(out, esize_of(odtype)))
+    return GRPO_ERR_MISALIGNED;
+  const size_t ob = matrix_bytes(n, d, ldo, odtype);
+  if (overlap(out, ob, weight, matrix_bytes(V, d, ldw, wdtype)) ||
+      overlap(out, ob, ids, 8 * (size_t)n))
+    return GRPO_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  if (current_device(&dev) != cudaSuccess) return GRPO_ERR_CUDA;
+  stream_take_last(stream);
+  EmbedFwdArgs a;
+  a.ids = ids;
+  a.n = n;
+  a.weight = weight;
+  a.wdtype = wdtype == GRPO_F32 ? 0 : 1;
+  a.V = V;
+  a.d = d;
+  a.ldw = ldw;
+  a.scale = scale;
+  a.out = out;
+  a.odtype = odtype == GRPO_F32 ? 0 : 1;
+  a.ldo = ldo;
+  return from_cuda(launch_embed_fwd(a, dev, (cudaStream_t)stream));
+}
+
+grpo_status grpo_embed_workspace_size(int64_t n, int64_t V, int64_t d, size_t* bytes) {
+  if (bytes == nullptr) return GRPO_ERR_INVALID_ARG;
+  const grpo_status s = check_embed(n, V, d, d, d);
+  if (s != GRPO_OK) return s;
+  *bytes = embed_workspace_bytes(n, V, d);
+  return GRPO_OK;
+}
+
+grpo_status grpo_embed_bwd(const int64_t* ids, int64_t n, const void* dout, grpo_dtype ddtype,
+                           int64_t V, int64_t d, int64_t ldd, float scale, int64_t pad_id,
+                           void* dweight, grpo_dtype wdtype, int64_t ldw, int accumulate,
+                           void* workspace, size_t workspace_bytes, grpo_stream_t stream) {
+  if (!known_dtype(ddtype) || !known_dtype(wdtype)) return GRPO_ERR_UNSUPPORTED;
+  const grpo_status s = check_embed(n, V, d, ldw, ldd);
+  if (s != GRPO_OK) return s;
+  if (isnan(scale) || isinf(scale)) return GRPO_ERR_INVALID_ARG;
+  if (dweight == nullptr || workspace == nullptr) return GRPO_ERR_INVALID_ARG;
+  if (n > 0 && (ids == nullptr || dout == nullptr)) return GRPO_ERR_INVALID_ARG;
+  if (!aligned(ids, 8) || !aligned(dout, esize_of(ddtype)) ||
+      !aligned(dweight, esize_of(wdtype)) || !aligned(workspace, 256))
+    return GRPO_ERR_MISALIGNED;
+  if (workspace_bytes < embed_workspace_bytes(n, V, d)) return GRPO_ERR_WORKSPACE;
+  const size_t wb = matrix_bytes(V, d, ldw, wdtype);
+  const size_t db = matrix_bytes(n, d, ldd, ddtype);
+  if (overlap(dweight, wb, dout, db) || overlap(dweight, wb, ids, 8 * (size_t)n) ||
+      overlap(dweight, wb, workspace, workspace_bytes) ||
+      overlap(workspace, workspace_bytes, dout, db) ||
+      overlap(workspace, workspace_bytes, ids, 8 * (size_t)n))
+    return GRPO_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  if (current_device(&dev) != cudaSuccess) return GRPO_ERR_CUDA;
+  stream_take_last(stream);
+  EmbedBwdArgs a;
+  a.ids = ids;
+  a.n = n;
+  a.dout = dout;
+  a.ddtype = ddtype == GRPO_F32 ? 0 : 1;
+  a.V = V;
+  a.d = d;
+  a.ldd = ldd;
+  a.scale = scale;
+  a.pad_id = pad_id;
+  a.dweight = dweight;
+  a.wdtype = wdtype == GRPO_F32 ? 0 : 1;
+  a.ldw = ldw;
+  a.accumulate = accumulate != 0;
+  a.ws = workspace;
+  return from_cuda(launch_embed_bwd(a, dev, (cudaStream_t)stream));
+}
+
+grpo_status grpo_grad_norm_workspace_size(int64_t count, size_t* bytes) {
+  if (bytes == nullptr || count < 0) return GRPO_ERR_INVALID_ARG;
+  if (count > INT32_MAX) return GRPO_ERR_UNSUPPORTED;
+  *bytes = grad_norm_workspace_bytes(count);
+  return GRPO_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+grpo_status clip_impl(const grpo_tensor* tensors, int64_t count, grpo_norm_type type,
+                      float max_norm, float eps, bool norm_only, float* stats, void* workspace,
+                      size_t workspace_bytes, grpo_stream_t stream) {
+  if (type != GRPO_NORM_L2 && type != GRPO_NORM_MAX) return GRPO_ERR_UNSUPPORTED;
+  if (count < 0 || !(max_norm >= 0.f) || !(eps >= 0.f) || isinf(eps)) return GRPO_ERR_INVALID_ARG;
+  if (count > INT32_MAX) return GRPO_ERR_UNSUPPORTED;
+  if ((count > 0 && tensors == nullptr) || stats == nullptr || workspace == nullptr)
+    return GRPO_ERR_INVALID_ARG;
+  if (!aligned(stats, 4) || !aligned(workspace, 256)) return GRPO_ERR_MISALIGNED;
+  if (workspace_bytes < grad_norm_workspace_bytes(count)) return GRPO_ERR_WORKSPACE;
+  GradTensor* g = nullptr;
+  GradTensor few[64];
+  std::unique_ptr<GradTensor[]> many;
+  if (count <= 64) {
+    g = few;
+  } else {
+    many.reset(new (std::nothrow) GradTensor[(size_t)count]);
+    if (!many) return GRPO_ERR_UNSUPPORTED;
+    g = many.get();
+  }
+  int64_t all = 0;
+  for (int64_t k = 0; k < count; ++k) {
+    const grpo_tensor& t = tensors[k];
+    if (!known_dtype(t.dtype) || !known_dtype(t.out_dtype)) return GRPO_ERR_UNSUPPORTED;
+    if (t.numel < 0 || (t.numel > 0 && t.data == nullptr)) return GRPO_ERR_INVALID_ARG;
+    if (t.numel > INT64_MAX / 16 - all) return GRPO_ERR_UNSUPPORTED;
+    all += t.numel;
+    void* out = t.out == nullptr ? const_cast<void*>(t.data) : t.out;
+    // in place: no other type; elsewhere: not over part of the input
+    if (out == t.data && t.out_dtype != t.dtype) return GRPO_ERR_INVALID_ARG;
+    if (!aligned(t.data, esize_of(t.dtype)) || !aligned(out, esize_of(t.out_dtype)))
+      return GRPO_ERR_MISALIGNED;
+    const size_t nb = (size_t)t.numel * esize_of(t.dtype);
+    const size_t no = (size_t)t.numel * esize_of(t.out_dtype);
+    if (!norm_only && ((out != t.data && overlap(out, no, t.data, nb)) ||
+                       overlap(out, no, workspace, workspace_bytes)))
+      return GRPO_ERR_INVALID_ARG;
+    g[k].data = t.data;
+    g[k].out = out;
+    g[k].numel = t.numel;
+    g[k].dt = (t.dtype == GRPO_BF16 ? 1 : 0) | (t.out_dtype == GRPO_BF16 ? 2 : 0);
+  }
+  DeviceInfo dev;
+  if (current_device(&dev) != cudaSuccess) return GRPO_ERR_CUDA;
+  stream_take_last(stream);
+  ClipArgs a;
+  a.tensors = g;
+  a.count = count;
+  a.type = type == GRPO_NORM_L2 ? 0 : 1;
+  a.max_norm = max_norm;
+  a.eps = eps;
+  a.norm_only = norm_only;
+  a.stats = stats;
+  a.ws = workspace;
+  return from_cuda(launch_clip(a, dev, (cudaStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+grpo_status grpo_clip_grad_norm(const grpo_tensor* tensors, int64_t count, grpo_norm_type type,
+                                float max_norm, float eps, float* stats, void* workspace,
+                                size_t workspace_bytes, grpo_stream_t stream) {
+  return clip_impl(tensors, count, type, max_norm, eps, false, stats, workspace, workspace_bytes,
+                   stream);
+}
+
+grpo_status grpo_grad_norm(const grpo_tensor* tensors, int64_t count, grpo_norm_type type,
+                           float* stats, void* workspace, size_t workspace_bytes,
+                           grpo_stream_t stream) {
+  return clip_impl(tensors, count, type, INFINITY, 0.f, true, stats, workspace, workspace_bytes,
+                   stream);
+}
+
+grpo_status grpo_verify_workspace_size(int64_t N, size_t* bytes) {
+  if (bytes == nullptr || N < 0) return GRPO_ERR_INVALID_ARG;
+  if (N > INT32_MAX) return GRPO_ERR_UNSUPPORTED;
+  *bytes = verify_workspace_bytes(N);
+  return GRPO_OK;
+}
+
+grpo_status grpo_verify_drafts(const void* target_logits, const void* draft_logits,
+                               grpo_dtype dtype, int64_t N, int64_t K, int64_t V,
+                               int64_t target_seq, int64_t target_row, int64_t draft_seq,
+                               int64_t draft_row, const int64_t* draft_tokens,
+                               const int32_t* draft_len, const float* u, const float* noise,
+                               int64_t noise_row, const float* temperature, int64_t* tokens,
+                               int32_t* n_accepted, float* logp, void* workspace,
+                               size_t workspace_bytes, grpo_stream_t stream) {
+  if (!known_dtype(dtype)) return GRPO_ERR_UNSUPPORTED;
+  if (N < 0 || K < 0 || V < 1) return GRPO_ERR_INVALID_ARG;
+  if (N > INT32_MAX || K > (int64_t)1 << 20 || V > INT32_MAX - 65536) return GRPO_ERR_UNSUPPORTED;
+  const bool has_draft = draft_logits != nullptr && K > 0;
+  if (target_row < V || target_seq < 0 || noise_row < V) return GRPO_ERR_INVALID_ARG;
+  if (mul3(K + 1, target_row, 8) < 0 || mul3(N, target_seq, 8) < 0 || mul3(N, noise_row, 8) < 0)
+    return GRPO_ERR_UNSUPPORTED;
+  if (N > 1 && target_seq < K * target_row + V) return GRPO_ERR_INVALID_ARG;
+  if (has_draft) {
+    if (draft_row < V || draft_seq < 0) return GRPO_ERR_INVALID_ARG;
+    if (mul3(K, draft_row, 8) < 0 || mul3(N, draft_seq, 8) < 0) return GRPO_ERR_UNSUPPORTED;
+    if (N > 1 && draft_seq < (K - 1) * draft_row + V) return GRPO_ERR_INVALID_ARG;
+  }
+  if (workspace == nullptr) return GRPO_ERR_INVALID_ARG;
+  if (N > 0) {
+    if (target_logits == nullptr || noise == nullptr || tokens == nullptr ||
+        n_accepted == nullptr || logp == nullptr)
+      return GRPO_ERR_INVALID_ARG;
+    if (K > 0 && (draft_tokens == nullptr || u == nullptr)) return GRPO_ERR_INVALID_ARG;
+  }
+  if (!aligned(target_logits, esize_of(dtype)) || !aligned(draft_logits, esize_of(dtype)) ||
+      !aligned(draft_tokens, 8) || !aligned(draft_len, 4) || !aligned(u, 4) ||
+      !aligned(noise, 4) || !aligned(temperature, 4) || !aligned(tokens, 8) ||
+      !aligned(n_accepted, 4) || !aligned(logp, 4) || !aligned(workspace, 256))
+    return GRPO_ERR_MISALIGNED;
+  if (workspace_bytes < verify_workspace_bytes(N)) return GRPO_ERR_WORKSPACE;
+  DeviceInfo dev;
+  if (current_device(&dev) != cudaSuccess) return GRPO_ERR_CUDA;
+  stream_take_last(stream);
+  VerifyArgs a;
+  a.target = target_logits;
+  a.draft = has_draft ? draft_logits : nullptr;
+  a.dtype = dtype == GRPO_F32 ? 0 : 1;
+  a.N = N;
+  a.K = K;
+  a.V = V;
+  a.tld = target_row;
+  a.tls = target_seq;
+  a.dld = has_draft ? draft_row : 0;
+  a.dls = has_draft ? draft_seq : 0;
+  a.tokens = draft_tokens;
+  a.lens = draft_len;
+  a.u = u;
+  a.noise = noise;
+  a.nld = noise_row;
+  a.temperature = temperature;
+  a.out_tokens = tokens;
+  a.n_accepted = n_accepted;
+  a.logp = logp;
+  a.ws = workspace;
+  return from_cuda(launch_verify(a, dev, (cudaStream_t)stream));
+}
+
 grpo_status grpo_check_error(const void* workspace, grpo_stream_t stream) {
   if (workspace == nullptr) return GRPO_ERR_INVALID_ARG;
-  uint32_t flags = 0;
+  WsHeader hdr = {};
   const cudaStream_t st = (cudaStream_t)stream;
   stream_take_after_fwd(st);
-  if (cudaMemcpyAsync(&flags, workspace, sizeof flags, cudaMemcpyDeviceToHost, st) != cudaSuccess)
+  if (cudaMemcpyAsync(&hdr, workspace, sizeof hdr, cudaMemcpyDeviceToHost, st) != cudaSuccess)
     return GRPO_ERR_CUDA;
   if (cudaStreamSynchronize(st) != cudaSuccess) return GRPO_ERR_CUDA;
+  uint32_t flags = hdr.flags;
+  if (flags == kFlagIndirect && hdr.status_check == ~hdr.status_count) {
+    // the flags of every item, a block at a time
+    const uint32_t n = hdr.status_count;
+    uint32_t buf[1024];
+    const char* ws = static_cast<const char*>(workspace);
+    flags = 0;
+    for (uint32_t k = 0; k < n; k += 1024) {
+      const uint32_t c = n - k < 1024 ? n - k : 1024;
+      if (cudaMemcpyAsync(buf, ws + 256 + 4 * (size_t)k, 4 * (size_t)c, cudaMemcpyDeviceToHost,
+                          st) != cudaSuccess ||
+          cudaStreamSynchronize(st) != cudaSuccess)
+        return GRPO_ERR_CUDA;
+      for (uint32_t j = 0; j < c; ++j) flags |= buf[j];
+    }
+  }
   if (flags & kFlagTokenRange) return GRPO_ERR_TOKEN_RANGE;
   if (flags & kFlagLengthRange) return GRPO_ERR_LENGTH_RANGE;
   if (flags & kFlagTimeout) return GRPO_ERR_TIMEOUT;
+  if (flags & kFlagValue) return GRPO_ERR_VALUE;
   return GRPO_OK;
 }
 

@@ -20,6 +20,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kFlagTokenRange = 1u;
 constexpr uint32_t kFlagLengthRange = 2u;
 constexpr uint32_t kFlagTimeout = 4u;
+constexpr uint32_t kFlagValue = 8u;
+// The header's flags word refers to `status_count` more words of flags, one
+// per item of the call, at byte 256 of the workspace (each written by its
+// item, so no kernel has to reset them first).
+constexpr uint32_t kFlagIndirect = 0x80000000u;
 
 // Workspace: a 256-byte header, then the exclusive prefix sums of the
 // clamped lengths (offsets[i] = sum of len[0..i), offsets[N] = number of
@@ -28,7 +33,8 @@ constexpr uint32_t kFlagTimeout = 4u;
 struct WsHeader {
   uint32_t flags;   // kFlag* bits of the most recent forward call
   uint32_t ticket;  // arrival counter of the loss reduction's last-block step
-  uint32_t pad[2];
+  uint32_t status_count;  // with kFlagIndirect
+  uint32_t status_check;  // ~status_count: the two are not left-over bytes
 };
 constexpr int kMaxLossBlocks = 1024;
 

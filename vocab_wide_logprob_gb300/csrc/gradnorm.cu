@@ -1,0 +1,368 @@
+// Global norm of many gradient tensors, and clipping.
+//
+//   norm = sqrt(sum over all tensors and elements of g^2)   (or max |g|)
+//   coef = min(1, max_norm / (norm + eps))
+//   out  = coef * g                                          (per element)
+//
+// Two launches for any number of tensors up to kMaxTensors each: the norm
+// kernel reads every element once and leaves one float64 partial per CTA; the
+// scaling kernel adds the partials in CTA order (every CTA the same sum), and
+// scales.  The table of tensors travels in the kernel's parameters, so a call
+// needs no copy, no device table and no synchronisation, and can be captured.
+#include <math.h>
+
+#include "ops.cuh"
+
+namespace grpo {
+namespace {
+
+constexpr int kVecs = 8;  // 16-byte loads in flight per thread
+constexpr int64_t kChunkBytes = (int64_t)kThreads * kVecs * 16;  // 32 KiB of one tensor
+
+// What a launch knows about its tensors.  first[k] is the chunk that tensor k
+// begins with; first[count] the number of chunks.
+template <int CAP>
+struct Table {
+  const void* data[CAP];
+  void* out[CAP];
+  int64_t numel[CAP];
+  int64_t first[CAP + 1];
+  uint8_t dt[CAP];  // bit 0: data is bf16, bit 1: out is bf16
+  int count;
+};
+
+template <int CAP>
+__device__ __forceinline__ int find_tensor(const Table<CAP>& t, int64_t chunk) {
+  int lo = 0, hi = t.count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (t.first[mid] <= chunk)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// ---------------------------------------------------------------------------
+// norm
+// ---------------------------------------------------------------------------
+
+// Squares of values above 2^60 or (all of them) below 2^-50 leave float32's
+// range: such a batch is scaled by a power of two first, which is exact.
+template <int N>
+__device__ __forceinline__ double sum_squares(const float* x, float top) {
+  float sc = 1.f;
+  double back = 1.0;
+  if (top > 0x1p60f) {
+    sc = 0x1p-80f;
+    back = 0x1p160;
+  } else if (top < 0x1p-50f) {
+    sc = 0x1p100f;
+    back = 0x1p-200;
+  }
+  float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+  if (sc == 1.f) {
+#pragma unroll
+    for (int k = 0; k < N; k += 4) {
+      s0 = fmaf(x[k], x[k], s0);
+      s1 = fmaf(x[k + 1], x[k + 1], s1);
+      s2 = fmaf(x[k + 2], x[k + 2], s2);
+      s3 = fmaf(x[k + 3], x[k + 3], s3);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) s0 = fmaf(x[k] * sc, x[k] * sc, s0);
+  }
+  return (double)((s0 + s1) + (s2 + s3)) * back;
+}
+
+// max that keeps NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  return a != a ? a : (b != b ? b : fmaxf(a, b));
+}
+
+template <typename T, bool kMax>
+__device__ __forceinline__ double chunk_norm(const T* data, int64_t numel, int64_t e0) {
+  using E = Elt<T>;
+  constexpr int EPV = E::kPerVec;
+  constexpr int kElems = (int)(kChunkBytes / sizeof(T));
+  const int64_t e1 = min(e0 + kElems, numel);
+  const int tid = threadIdx.x;
+  // 16-byte aligned interior [a, b); ragged ends are scalar
+  const uintptr_t addr = reinterpret_cast<uintptr_t>(data + e0);
+  const int64_t a = min(e0 + (int64_t)(((16u - (unsigned)(addr & 15u)) & 15u) / sizeof(T)), e1);
+  const int nvec = (int)((e1 - a) / EPV);
+  const int64_t b = a + (int64_t)nvec * EPV;
+  uint4 d[kVecs];
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) {
+    const int k = tid + u * kThreads;
+    d[u] = k < nvec ? ld_stream(data + a + (int64_t)k * EPV) : make_uint4(0, 0, 0, 0);
+  }
+  float edge = 0.f;
+  if (tid < a - e0) edge = E::load1(data + e0 + tid);
+  if (tid >= 32 && tid - 32 < e1 - b) edge = E::load1(data + b + tid - 32);
+  double s = 0.0;
+  float m = fabsf(edge);
+  if (!kMax) {
+    const float ed[4] = {edge, 0.f, 0.f, 0.f};
+    s = edge != 0.f ? sum_squares<4>(ed, fabsf(edge)) : 0.0;
+  }
+  // halves of the loads at a time, to bound the registers
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float x[kVecs / 2 * EPV];
+#pragma unroll
+    for (int u = 0; u < kVecs / 2; ++u) E::unpack(d[h * (kVecs / 2) + u], x + u * EPV);
+    if (kMax) {
+#pragma unroll
+      for (int k = 0; k < kVecs / 2 * EPV; ++k) m = max_nan(m, fabsf(x[k]));
+    } else {
+      float top = 0.f;
+#pragma unroll
+      for (int k = 0; k < kVecs / 2 * EPV; ++k) top = fmaxf(top, fabsf(x[k]));
+      s += sum_squares<kVecs / 2 * EPV>(x, top);
+    }
+  }
+  return kMax ? (double)m : s;
+}
+
+__device__ __forceinline__ double combine(double a, double b, bool is_max) {
+  if (!is_max) return a + b;
+  return a != a ? a : (b != b ? b : fmax(a, b));
+}
+
+// Sum (or maximum) over the CTA in a fixed tree; every thread gets it.
+template <bool kMax>
+__device__ __forceinline__ double block_reduce(double v, double* s_red) {
+  for (int o = 16; o > 0; o >>= 1) v = combine(v, __shfl_xor_sync(0xffffffffu, v, o), kMax);
+  if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double t = s_red[0];
+#pragma unroll
+  for (int k = 1; k < kWarps; ++k) t = combine(t, s_red[k], kMax);
+  __syncthreads();
+  return t;
+}
+
+template <int CAP, bool kMax>
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ Table<CAP> t,
+                                                             double* partial) {
+  __shared__ double s_red[kWarps];
+  pdl_wait();
+  pdl_trigger();
+  const int64_t chunks = t.first[t.count];
+  double s = 0.0;
+  for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+    const int k = find_tensor(t, c);
+    double v;
+    if (t.dt[k] & 1)
+      v = chunk_norm<uint16_t, kMax>(static_cast<const uint16_t*>(t.data[k]), t.numel[k],
+                                     (c - t.first[k]) * (kChunkBytes / 2));
+    else
+      v = chunk_norm<float, kMax>(static_cast<const float*>(t.data[k]), t.numel[k],
+                                  (c - t.first[k]) * (kChunkBytes / 4));
+    s = combine(s, v, kMax);
+  }
+  s = block_reduce<kMax>(s, s_red);
+  if (threadIdx.x == 0) partial[blockIdx.x] = s;
+}
+
+// ---------------------------------------------------------------------------
+// clip
+// ---------------------------------------------------------------------------
+
+template <typename TI, typename TO>
+__device__ __forceinline__ void chunk_scale(const TI* data, TO* out, int64_t numel, int64_t e0,
+                                            float coef) {
+  constexpr int kElems = (int)(kChunkBytes / sizeof(TI));
+  const int64_t e1 = min(e0 + kElems, numel);
+  const int tid = threadIdx.x;
+  const bool vec = reinterpret_cast<uintptr_t>(data) % 16 == 0 &&
+                   reinterpret_cast<uintptr_t>(out) % (8 * sizeof(TO)) % 16 == 0;
+  if (vec) {  // 8 elements a step
+    const int n8 = (int)((e1 - e0) / 8);
+    constexpr int U = kElems / 8 / kThreads;
+#pragma unroll
+    for (int h = 0; h < U; h += 4) {
+      float x[4][8];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int k = tid + (h + u) * kThreads;
+        if (k < n8) {
+          const char* p = reinterpret_cast<const char*>(data + e0 + (int64_t)k * 8);
+          Elt<TI>::unpack(*reinterpret_cast<const uint4*>(p), x[u]);
+          if (sizeof(TI) == 4)
+            Elt<TI>::unpack(*reinterpret_cast<const uint4*>(p + 16), x[u] + (sizeof(TI) == 4 ? 4 : 0));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int k = tid + (h + u) * kThreads;
+        if (k < n8) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[u][e] *= coef;
+          char* q = reinterpret_cast<char*>(out + e0 + (int64_t)k * 8);
+          *reinterpret_cast<uint4*>(q) = Elt<TO>::pack(x[u]);
+          if (sizeof(TO) == 4)
+            *reinterpret_cast<uint4*>(q + 16) = Elt<TO>::pack(x[u] + (sizeof(TO) == 4 ? 4 : 0));
+        }
+      }
+    }
+    e0 += (int64_t)n8 * 8;
+  }
+  for (int64_t e = e0 + tid; e < e1; e += kThreads) {
+    float x;
+    if constexpr (sizeof(TI) == 4)
+      x = data[e];
+    else
+      x = bf16_bits_to_float(data[e]);
+    Elt<TO>::store1(out + e, x * coef);
+  }
+}
+
+// Adds the norm kernel's partials (the same fixed tree in every CTA), forms
+// the coefficient, and scales the chunks last to first: the chunks the norm
+// kernel read last are the ones still in L2.  In place and under the limit
+// there is nothing to write.
+template <int CAP, bool kMax>
+__global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ Table<CAP> t,
+                                                              const double* partial, int npartial,
+                                                              float max_norm, float eps,
+                                                              int copies, float* stats,
+                                                              WsHeader* hdr) {
+  __shared__ double s_red[kWarps];
+  pdl_wait();
+  pdl_trigger();
+  double s = 0.0;
+  for (int k = threadIdx.x; k < npartial; k += kThreads) s = combine(s, partial[k], kMax);
+  s = block_reduce<kMax>(s, s_red);
+  const double norm = kMax ? s : sqrt(s);
+  double c = (double)max_norm / (norm + (double)eps);
+  c = c > 1.0 ? 1.0 : c;                     // keeps NaN
+  if (isinf(max_norm)) c = 1.0;              // no limit
+  const float coef = (float)c;
+  if (stats != nullptr && blockIdx.x == 0 && threadIdx.x == 0) {
+    stats[0] = (float)norm;
+    stats[1] = coef;
+    hdr->flags = isfinite(norm) ? 0u : kFlagValue;
+  }
+  if (coef == 1.f && !copies) return;
+  const int64_t chunks = t.first[t.count];
+  for (int64_t r = blockIdx.x; r < chunks; r += gridDim.x) {
+    const int64_t ch = chunks - 1 - r;
+    const int k = find_tensor(t, ch);
+    if (coef == 1.f && t.out[k] == t.data[k]) continue;
+    const int64_t n = t.numel[k], j = ch - t.first[k];
+    switch (t.dt[k]) {
+      case 0:
+        chunk_scale(static_cast<const float*>(t.data[k]), static_cast<float*>(t.out[k]), n,
+                    j * (kChunkBytes / 4), coef);
+        break;
+      case 1:
+        chunk_scale(static_cast<const uint16_t*>(t.data[k]), static_cast<float*>(t.out[k]), n,
+                    j * (kChunkBytes / 2), coef);
+        break;
+      case 2:
+        chunk_scale(static_cast<const float*>(t.data[k]), static_cast<uint16_t*>(t.out[k]), n,
+                    j * (kChunkBytes / 4), coef);
+        break;
+      default:
+        chunk_scale(static_cast<const uint16_t*>(t.data[k]), static_cast<uint16_t*>(t.out[k]), n,
+                    j * (kChunkBytes / 2), coef);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// launch
+// ---------------------------------------------------------------------------
+
+constexpr int kMaxTensors = 768;     // tensors of one launch: the parameters stay below 32 KiB
+constexpr int kMaxPartials = 152 * 8;  // CTAs of one norm launch
+static_assert(sizeof(Table<kMaxTensors>) < 32000, "kernel parameters");
+
+template <int CAP>
+void fill(Table<CAP>* t, const GradTensor* g, int count) {
+  t->count = count;
+  int64_t at = 0;
+  for (int k = 0; k < count; ++k) {
+    t->data[k] = g[k].data;
+    t->out[k] = g[k].out;
+    t->numel[k] = g[k].numel;
+    t->dt[k] = (uint8_t)g[k].dt;
+    t->first[k] = at;
+    const int64_t per = kChunkBytes / ((g[k].dt & 1) ? 2 : 4);
+    at += (g[k].numel + per - 1) / per;
+  }
+  t->first[count] = at;
+}
+
+template <int CAP, bool kMax>
+cudaError_t clip_launch(const ClipArgs& a, const GradTensor* g, int count, int part0, int nparts,
+                        bool norm_step, bool first, const DeviceInfo& d, cudaStream_t st) {
+  Table<CAP> t;
+  fill(&t, g, count);
+  double* partial = reinterpret_cast<double*>(static_cast<char*>(a.ws) + 256);
+  const int64_t chunks = t.first[count];
+  if (norm_step)
+    return launch_pdl(grad_norm_kernel<CAP, kMax>, dim3((unsigned)nparts), dim3(kThreads), 0, st,
+                      1, t, partial + part0);
+  bool copies = false;
+  for (int k = 0; k < count; ++k) copies |= g[k].out != g[k].data;
+  int64_t grid = 8 * (int64_t)d.sms;
+  if (grid > chunks) grid = chunks;
+  if (grid < 1 || a.norm_only) grid = 1;
+  if (a.norm_only) t.first[count] = 0;
+  return launch_pdl(grad_scale_kernel<CAP, kMax>, dim3((unsigned)grid), dim3(kThreads), 0, st, 1,
+                    t, (const double*)partial, nparts, a.max_norm, a.eps, (int)(copies && !a.norm_only),
+                    first ? a.stats : (float*)nullptr, static_cast<WsHeader*>(a.ws));
+}
+
+template <bool kMax>
+cudaError_t clip_run(const ClipArgs& a, const DeviceInfo& d, cudaStream_t st) {
+  // the norm of every group of tensors, then the scaling of every group
+  int parts = 0;
+  for (int step = 0; step < 2; ++step) {
+    int part0 = 0;
+    for (int64_t k = 0; k == 0 || k < a.count; k += kMaxTensors) {
+      const int cnt = (int)(a.count - k < kMaxTensors ? a.count - k : kMaxTensors);
+      int64_t chunks = 0;
+      for (int j = 0; j < cnt; ++j) {
+        const int64_t per = kChunkBytes / ((a.tensors[k + j].dt & 1) ? 2 : 4);
+        chunks += (a.tensors[k + j].numel + per - 1) / per;
+      }
+      int np = (int)(chunks < 8 * (int64_t)d.sms ? chunks : 8 * (int64_t)d.sms);
+      if (np > kMaxPartials) np = kMaxPartials;
+      if (np < 1) np = 1;
+      const int n = step == 0 ? np : parts;
+      const GradTensor* g = a.tensors + k;
+      cudaError_t e;
+      if (cnt <= 32)
+        e = clip_launch<32, kMax>(a, g, cnt, part0, n, step == 0, k == 0, d, st);
+      else if (cnt <= 192)
+        e = clip_launch<192, kMax>(a, g, cnt, part0, n, step == 0, k == 0, d, st);
+      else
+        e = clip_launch<kMaxTensors, kMax>(a, g, cnt, part0, n, step == 0, k == 0, d, st);
+      if (e != cudaSuccess) return e;
+      part0 += np;
+      if (step == 1 && a.norm_only) break;
+    }
+    parts = part0;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+size_t grad_norm_workspace_bytes(int64_t count) {
+  const size_t groups = count < 1 ? 1 : (size_t)((count + kMaxTensors - 1) / kMaxTensors);
+  return 256 + align_up(groups * kMaxPartials * sizeof(double), 256);
+}
+
+cudaError_t launch_clip(const ClipArgs& a, const DeviceInfo& d, cudaStream_t st) {
+  return a.type == 0 ? clip_run<false>(a, d, st) : clip_run<true>(a, d, st);
+}
+
+}  // namespace grpo

@@ -1,0 +1,83 @@
+// Launchers of the operators around the loss (embedding, gradient clipping,
+// draft verification); defined in embed.cu, gradnorm.cu and verify.cu, called
+// by api.cu.  Internal header.
+#pragma once
+
+#include "common.cuh"
+
+namespace grpo {
+
+// ---- embedding lookup and its gradient (embed.cu) ---------------------------
+
+struct EmbedFwdArgs {
+  const int64_t* ids;
+  int64_t n;
+  const void* weight;
+  int wdtype;  // 0 f32, 1 bf16
+  int64_t V, d, ldw;
+  float scale;
+  void* out;
+  int odtype;
+  int64_t ldo;
+};
+cudaError_t launch_embed_fwd(const EmbedFwdArgs& a, const DeviceInfo& d, cudaStream_t st);
+
+struct EmbedBwdArgs {
+  const int64_t* ids;
+  int64_t n;
+  const void* dout;
+  int ddtype;
+  int64_t V, d, ldd;
+  float scale;
+  int64_t pad_id;  // negative: none
+  void* dweight;
+  int wdtype;
+  int64_t ldw;
+  bool accumulate;
+  void* ws;
+};
+size_t embed_workspace_bytes(int64_t n, int64_t V, int64_t d);
+cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, const DeviceInfo& d, cudaStream_t st);
+
+// ---- gradient norm and clipping (gradnorm.cu) --------------------------------
+
+struct GradTensor {
+  const void* data;
+  void* out;
+  int64_t numel;
+  int dt;  // bit 0: data is bf16, bit 1: out is bf16
+};
+struct ClipArgs {
+  const GradTensor* tensors;  // host
+  int64_t count;
+  int type;  // 0: L2, 1: max |g|
+  float max_norm, eps;
+  bool norm_only;
+  float* stats;  // norm, coefficient
+  void* ws;
+};
+size_t grad_norm_workspace_bytes(int64_t count);
+cudaError_t launch_clip(const ClipArgs& a, const DeviceInfo& d, cudaStream_t st);
+
+// ---- verification of drafted tokens (verify.cu) -------------------------------
+
+struct VerifyArgs {
+  const void* target;  // [N, K + 1, V], row pitch tld, sequence pitch tls
+  const void* draft;   // [N, K, V] or null
+  int dtype;
+  int64_t N, K, V, tld, tls, dld, dls;
+  const int64_t* tokens;  // [N, K]
+  const int32_t* lens;    // [N] or null (K each)
+  const float* u;         // [N, K]
+  const float* noise;     // [N, V], row pitch nld
+  int64_t nld;
+  const float* temperature;  // [N] or null (1)
+  int64_t* out_tokens;       // [N, K + 1]
+  int32_t* n_accepted;       // [N]
+  float* logp;               // [N, K + 1]
+  void* ws;
+};
+size_t verify_workspace_bytes(int64_t N);
+cudaError_t launch_verify(const VerifyArgs& a, const DeviceInfo& d, cudaStream_t st);
+
+}  // namespace grpo
