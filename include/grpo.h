@@ -560,8 +560,8 @@ grpo_status grpo_grad_norm(const grpo_tensor *tensors, int64_t count, grpo_norm_
  *   target's samples.  T = 0 (below 1e-6): x_j is accepted while it is the
  *   lowest argmax of z_j, and that argmax is emitted; u and noise of the
  *   sequence are not read, and its log-probs are those of T = 1.
- * L_i = 0 (or K = 0) samples one token.  Rows after the first rejection are
- * not read.
+ * L_i = 0 (or K = 0) samples one token.  No result depends on rows after the
+ * first rejection.
  *
  * target_logits: row j of sequence i starts at element i * target_seq + j *
  * target_row; draft_logits the same with its strides (ignored when NULL);
@@ -576,9 +576,10 @@ grpo_status grpo_grad_norm(const grpo_tensor *tensors, int64_t count, grpo_norm_
  * id outside [0, V) is not accepted (GRPO_ERR_TOKEN_RANGE), a length outside
  * [0, K] clamped (GRPO_ERR_LENGTH_RANGE).
  * Decisions are made in float64 from float32 sums, bitwise reproducibly.
- * K <= 2^20.  workspace: at least grpo_verify_workspace_size(N) bytes.
+ * K <= 2^20, N * (K+1) <= 2^26.  workspace: at least
+ * grpo_verify_workspace_size(N, K) bytes (about 400 bytes per row).
  */
-grpo_status grpo_verify_workspace_size(int64_t N, size_t *bytes);
+grpo_status grpo_verify_workspace_size(int64_t N, int64_t K, size_t *bytes);
 grpo_status grpo_verify_drafts(const void *target_logits, const void *draft_logits,
                                grpo_dtype dtype, int64_t N, int64_t K, int64_t V,
                                int64_t target_seq, int64_t target_row, int64_t draft_seq,

@@ -121,6 +121,9 @@ def test_squares_outside_float32(scale, dt):
     for grads in (t[:1], t):
         stats, ws = n.grpo_grad_norm(grads)
         want = norm64(grads)
+        if want > torch.finfo(F32).max:  # the float32 result is infinite, and said to be
+            assert math.isinf(float(stats[0])) and n.grpo_check_error(ws) == 9
+            continue
         # a subnormal result is rounded to a step of 2^-149
         assert abs(float(stats[0]) - want) <= 12 * U * want + 2.0 ** -149
         assert n.grpo_check_error(ws) == 0

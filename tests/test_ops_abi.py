@@ -89,9 +89,8 @@ def test_embed_bwd_refusals(lib):
 
 
 def _clip(lib, n, rows=((0x10000, 0, 16, 0, 0),), **kw):
-    table = (n._Tensor * max(1, len(rows)))()
-    for k, r in enumerate(rows):
-        table[k] = (r[0] or None, r[1] or None, *r[2:])
+    words = [w for r in rows for w in (r[0], r[1], r[2], r[3] | r[4] << 32)]
+    table = (ctypes.c_int64 * max(1, len(words)))(*words)
     a = dict(tensors=table, count=len(rows), type=0, max_norm=1.0, eps=1e-6, stats=A(0x90000),
              ws=A(0x100000), ws_bytes=1 << 20, stream=None)
     a.update(kw)
@@ -140,6 +139,7 @@ def test_verify_refusals(lib):
     assert _verify(lib, K=-1) == INVALID
     assert _verify(lib, V=0) == INVALID
     assert _verify(lib, K=(1 << 20) + 1) == UNSUPPORTED
+    assert _verify(lib, N=1 << 25) == UNSUPPORTED
     assert _verify(lib, V=1 << 31, trow=1 << 31, tseq=1 << 34, nrow=1 << 31) == UNSUPPORTED
     assert _verify(lib, trow=99) == INVALID
     assert _verify(lib, tseq=399) == INVALID      # sequences overlap
@@ -154,9 +154,9 @@ def test_verify_refusals(lib):
         assert _verify(lib, **{name: A(bad)}) == MISALIGNED, name
     assert _verify(lib, ws_bytes=256) == WORKSPACE
     out = ctypes.c_size_t(0)
-    assert lib.grpo_verify_workspace_size(4, ctypes.byref(out)) == OK
-    assert lib.grpo_verify_workspace_size(-1, ctypes.byref(out)) == INVALID
-    assert lib.grpo_verify_workspace_size(4, None) == INVALID
+    assert lib.grpo_verify_workspace_size(4, 3, ctypes.byref(out)) == OK
+    assert lib.grpo_verify_workspace_size(-1, 3, ctypes.byref(out)) == INVALID
+    assert lib.grpo_verify_workspace_size(4, 3, None) == INVALID
 
 
 def test_status_string(lib):

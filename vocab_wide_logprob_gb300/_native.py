@@ -8,7 +8,9 @@ fallback: importing this module fails loudly when the library is missing.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
 import os
 
 import torch
@@ -89,7 +91,7 @@ def _load():
         "grpo_grad_norm_workspace_size": ([I64, ctypes.POINTER(SZ)], INT),
         "grpo_clip_grad_norm": ([P, I64, INT, F, F, P, P, SZ, P], INT),
         "grpo_grad_norm": ([P, I64, INT, P, P, SZ, P], INT),
-        "grpo_verify_workspace_size": ([I64, ctypes.POINTER(SZ)], INT),
+        "grpo_verify_workspace_size": ([I64, I64, ctypes.POINTER(SZ)], INT),
         "grpo_verify_drafts": ([P, P, INT, I64, I64, I64, I64, I64, I64, I64, P, P, P, P, I64, P,
                                 P, P, P, P, SZ, P], INT),
         "grpo_lmhead_loss_bwd": ([P, P, I64, I64, I64, I64, I64, P, P, P, P, P, P, P, P, SZ, P],
@@ -103,6 +105,7 @@ def _load():
 
 
 _lib = _load()
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def library() -> ctypes.CDLL:
@@ -110,13 +113,14 @@ def library() -> ctypes.CDLL:
 
 
 def _stream(stream=None):
+    """Handle of ``stream``, or of the current device's current stream."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return _raw_stream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _check(status: int, where: str):
@@ -608,36 +612,39 @@ def grpo_embed_bwd(ids, dout, V, scale=1.0, pad_id=None, dweight=None, accumulat
     return dweight, workspace
 
 
-class _Tensor(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
-                ("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int)]
+def _columns(tensors, name):
+    """Addresses, sizes and dtype codes of a list of dense tensors.  (A model
+    has hundreds: the attributes are read by C-level maps.)"""
+    T = torch.Tensor
+    if not (all(map(_is_cuda, tensors)) and all(map(T.is_contiguous, tensors))):
+        raise ValueError(f"every {name} must be a contiguous CUDA tensor")
+    try:
+        codes = list(map(_CODE.__getitem__, map(_dtype, tensors)))
+    except KeyError:
+        raise TypeError(f"every {name} must be float32 or bfloat16") from None
+    return list(map(T.data_ptr, tensors)), list(map(T.numel, tensors)), codes
+
+
+_is_cuda, _dtype = operator.attrgetter("is_cuda"), operator.attrgetter("dtype")
 
 
 def _tensor_table(grads, outs):
-    """The grpo_tensor array of a list of dense tensors (and their outputs)."""
-    if not all([t.is_cuda and t.is_contiguous() for t in grads]):
-        raise ValueError("every gradient must be a contiguous CUDA tensor")
-    codes = [_CODE.get(t.dtype) for t in grads]
-    if None in codes:
-        raise TypeError("gradients must be float32 or bfloat16")
-    n = len(grads)
-    table = (_Tensor * n)()
+    """The grpo_tensor array (four 8-byte words each) of a list of gradients
+    and their outputs, as an array the caller keeps while the C call reads it."""
+    data, numel, codes = _columns(grads, "gradient")
+    n = len(data)
+    flat = [0] * (4 * n)
     if outs is None:
-        rows = [(t.data_ptr(), None, t.numel(), c, c) for t, c in zip(grads, codes)]
+        ocodes = codes
     else:
         if len(outs) != n:
             raise ValueError("out must have one tensor per gradient")
-        if not all([o.is_cuda and o.is_contiguous() and o.numel() == t.numel()
-                    for o, t in zip(outs, grads)]):
-            raise ValueError("every out must be a contiguous CUDA tensor of its gradient's size")
-        ocodes = [_CODE.get(o.dtype) for o in outs]
-        if None in ocodes:
-            raise TypeError("outputs must be float32 or bfloat16")
-        rows = [(t.data_ptr(), o.data_ptr(), t.numel(), c, oc)
-                for t, o, c, oc in zip(grads, outs, codes, ocodes)]
-    for k, r in enumerate(rows):
-        table[k] = r
-    return table
+        flat[1::4], onumel, ocodes = _columns(outs, "out")
+        if onumel != numel:
+            raise ValueError("every out must have its gradient's size")
+    flat[0::4], flat[2::4] = data, numel
+    flat[3::4] = [c | o << 32 for c, o in zip(codes, ocodes)]
+    return array.array("Q", flat)
 
 
 def grpo_grad_norm_workspace_size(count: int) -> int:
@@ -669,7 +676,7 @@ def grpo_clip_grad_norm(grads, max_norm, out=None, norm_type=GRPO_NORM_L2, eps=1
     grads = list(grads)
     stats, workspace = _clip_buffers(grads, stats, workspace)
     table = _tensor_table(grads, out)
-    _check(_lib.grpo_clip_grad_norm(table, len(grads), int(norm_type), float(max_norm), float(eps),
+    _check(_lib.grpo_clip_grad_norm(table.buffer_info()[0], len(grads), int(norm_type), float(max_norm), float(eps),
                                     _ptr(stats), _ptr(workspace), workspace.numel(),
                                     _stream(stream)), "grpo_clip_grad_norm")
     return stats, workspace
@@ -681,14 +688,14 @@ def grpo_grad_norm(grads, norm_type=GRPO_NORM_L2, stats=None, workspace=None, st
     grads = list(grads)
     stats, workspace = _clip_buffers(grads, stats, workspace)
     table = _tensor_table(grads, None)
-    _check(_lib.grpo_grad_norm(table, len(grads), int(norm_type), _ptr(stats), _ptr(workspace),
+    _check(_lib.grpo_grad_norm(table.buffer_info()[0], len(grads), int(norm_type), _ptr(stats), _ptr(workspace),
                                workspace.numel(), _stream(stream)), "grpo_grad_norm")
     return stats, workspace
 
 
-def grpo_verify_workspace_size(N: int) -> int:
+def grpo_verify_workspace_size(N: int, K: int) -> int:
     out = ctypes.c_size_t(0)
-    _check(_lib.grpo_verify_workspace_size(N, ctypes.byref(out)), "grpo_verify_workspace_size")
+    _check(_lib.grpo_verify_workspace_size(N, K, ctypes.byref(out)), "grpo_verify_workspace_size")
     return int(out.value)
 
 
@@ -752,7 +759,7 @@ def grpo_verify_drafts(target_logits, draft_tokens, u, noise, draft_logits=None,
             if tuple(out[name].shape) != shape:
                 raise ValueError(f"{name} must be {list(shape)}")
         workspace = out.get("workspace") if workspace is None else workspace
-    need = grpo_verify_workspace_size(N)
+    need = grpo_verify_workspace_size(N, K)
     if workspace is None or workspace.numel() < need:
         workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
     out["workspace"] = workspace

@@ -918,6 +918,11 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 bool known_dtype(grpo_dtype t) { return t == GRPO_F32 || t == GRPO_BF16; }
 size_t esize_of(grpo_dtype t) { return t == GRPO_F32 ? 4 : 2; }
 
+// Rows of a verification: a grid of up to 32 CTAs per row stays below 2^31.
+bool verify_fits(int64_t N, int64_t K) {
+  return K <= (int64_t)1 << 20 && N <= ((int64_t)1 << 26) / (K + 1);
+}
+
 constexpr int64_t kMaxEmbedDim = (int64_t)1 << 24;
 
 // Shape checks shared by the embedding calls.
@@ -1052,6 +1057,12 @@ grpo_status clip_impl(const grpo_tensor* tensors, int64_t count, grpo_norm_type 
     const grpo_tensor& t = tensors[k];
     if (!known_dtype(t.dtype) || !known_dtype(t.out_dtype)) return GRPO_ERR_UNSUPPORTED;
     if (t.numel < 0 || (t.numel > 0 && t.data == nullptr)) return GRPO_ERR_INVALID_ARG;
+    if (t.numel == 0) {  // nothing behind its pointers
+      g[k].data = g[k].out = nullptr;
+      g[k].numel = 0;
+      g[k].dt = 0;
+      continue;
+    }
     if (t.numel > INT64_MAX / 16 - all) return GRPO_ERR_UNSUPPORTED;
     all += t.numel;
     void* out = t.out == nullptr ? const_cast<void*>(t.data) : t.out;
@@ -1102,10 +1113,10 @@ grpo_status grpo_grad_norm(const grpo_tensor* tensors, int64_t count, grpo_norm_
                    stream);
 }
 
-grpo_status grpo_verify_workspace_size(int64_t N, size_t* bytes) {
-  if (bytes == nullptr || N < 0) return GRPO_ERR_INVALID_ARG;
-  if (N > INT32_MAX) return GRPO_ERR_UNSUPPORTED;
-  *bytes = verify_workspace_bytes(N);
+grpo_status grpo_verify_workspace_size(int64_t N, int64_t K, size_t* bytes) {
+  if (bytes == nullptr || N < 0 || K < 0) return GRPO_ERR_INVALID_ARG;
+  if (!verify_fits(N, K)) return GRPO_ERR_UNSUPPORTED;
+  *bytes = verify_workspace_bytes(N, K);
   return GRPO_OK;
 }
 
@@ -1119,7 +1130,7 @@ grpo_status grpo_verify_drafts(const void* target_logits, const void* draft_logi
                                size_t workspace_bytes, grpo_stream_t stream) {
   if (!known_dtype(dtype)) return GRPO_ERR_UNSUPPORTED;
   if (N < 0 || K < 0 || V < 1) return GRPO_ERR_INVALID_ARG;
-  if (N > INT32_MAX || K > (int64_t)1 << 20 || V > INT32_MAX - 65536) return GRPO_ERR_UNSUPPORTED;
+  if (!verify_fits(N, K) || V > INT32_MAX - 65536) return GRPO_ERR_UNSUPPORTED;
   const bool has_draft = draft_logits != nullptr && K > 0;
   if (target_row < V || target_seq < 0 || noise_row < V) return GRPO_ERR_INVALID_ARG;
   if (mul3(K + 1, target_row, 8) < 0 || mul3(N, target_seq, 8) < 0 || mul3(N, noise_row, 8) < 0)
@@ -1142,7 +1153,7 @@ grpo_status grpo_verify_drafts(const void* target_logits, const void* draft_logi
       !aligned(noise, 4) || !aligned(temperature, 4) || !aligned(tokens, 8) ||
       !aligned(n_accepted, 4) || !aligned(logp, 4) || !aligned(workspace, 256))
     return GRPO_ERR_MISALIGNED;
-  if (workspace_bytes < verify_workspace_bytes(N)) return GRPO_ERR_WORKSPACE;
+  if (workspace_bytes < verify_workspace_bytes(N, K)) return GRPO_ERR_WORKSPACE;
   DeviceInfo dev;
   if (current_device(&dev) != cudaSuccess) return GRPO_ERR_CUDA;
   stream_take_last(stream);

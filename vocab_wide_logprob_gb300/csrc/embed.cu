@@ -8,6 +8,7 @@
 // order and writes every row of dW once: a sum of tokens' rows, or zeros for
 // an id that does not occur.  No floating-point atomics: the order of every
 // sum is fixed by n and the ids, so results are bitwise reproducible.
+#include "host_ctx.cuh"
 #include "ops.cuh"
 
 namespace grpo {
@@ -85,11 +86,10 @@ struct Cols8<T, false> {
 // forward
 // ---------------------------------------------------------------------------
 
-constexpr int kFwdUnroll = 4;  // 8-column units in flight per thread
-
-// One CTA copies `rows` rows; its threads walk the rows' units of 8 columns.
-// A strided unit u of a row is columns u, u + nu, ... u + 7 nu.
-template <typename TW, typename TO, bool kVec>
+// One CTA copies `rows` rows; its threads walk the rows' units of 8 columns, U
+// of them in flight each: first the units' ids, then the rows, then the
+// stores.  A strided unit u of a row is columns u, u + nu, ... u + 7 nu.
+template <typename TW, typename TO, bool kVec, int U>
 __global__ void __launch_bounds__(kThreads) embed_fwd_kernel(
     const int64_t* __restrict__ ids, int64_t n, const TW* __restrict__ w, int64_t V, int64_t d,
     int64_t ldw, float scale, TO* __restrict__ out, int64_t ldo, int rows, int nu) {
@@ -97,37 +97,57 @@ __global__ void __launch_bounds__(kThreads) embed_fwd_kernel(
   pdl_trigger();
   const int64_t row0 = (int64_t)blockIdx.x * rows;
   const int nrows = (int)min((int64_t)rows, n - row0);
-  const int64_t total = (int64_t)nrows * nu;
-  for (int64_t base = threadIdx.x; base < total; base += kThreads * kFwdUnroll) {
-    float x[kFwdUnroll][8];
-    int64_t dst[kFwdUnroll];
-    int left[kFwdUnroll];
+  int r = threadIdx.x / nu, c = threadIdx.x - r * nu;
+  const int dr = kThreads / nu, dc = kThreads - dr * nu;
+  while (r < nrows) {
+    int64_t id[U];
+    int rr[U], cc[U];
 #pragma unroll
-    for (int u = 0; u < kFwdUnroll; ++u) {
-      const int64_t k = base + u * kThreads;
-      dst[u] = -1;
-      if (k < total) {
-        const int r = nrows == 1 ? 0 : (int)((uint32_t)k / (uint32_t)nu);
-        const int64_t c = k - (int64_t)r * nu;
-        const int64_t id = __ldg(ids + row0 + r);
-        const int64_t col = kVec ? 8 * c : c;
-        left[u] = (int)(d - col);
-        dst[u] = (row0 + r) * ldo + col;
-        if (id >= 0 && id < V) {
-          Cols8<TW, kVec>::load(w + id * ldw + col, nu, left[u], x[u]);
+    for (int u = 0; u < U; ++u) {
+      rr[u] = r;
+      cc[u] = c;
+      id[u] = r < nrows ? __ldg(ids + row0 + r) : 0;
+      c += dc;
+      r += dr;
+      if (c >= nu) {
+        c -= nu;
+        ++r;
+      }
+    }
+    if constexpr (kVec) {
+      Vec8<TW> x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (rr[u] >= nrows) continue;
+        if (id[u] >= 0 && id[u] < V)
+          x[u].load_stream(w + id[u] * ldw + 8 * cc[u]);
+        else
+          x[u].fill(sizeof(TW) == 4 ? 0x7fc00000u : 0x7fc07fc0u);  // NaN
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (rr[u] < nrows)
+          x[u].template store<false>(out + (row0 + rr[u]) * ldo + 8 * cc[u], scale);
+    } else {
+      float x[U][8];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (rr[u] >= nrows) continue;
+        if (id[u] >= 0 && id[u] < V) {
+          Cols8<TW, false>::load(w + id[u] * ldw + cc[u], nu, (int)d - cc[u], x[u]);
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[u][e] = __int_as_float(0x7fc00000);
         }
       }
-    }
 #pragma unroll
-    for (int u = 0; u < kFwdUnroll; ++u)
-      if (dst[u] >= 0) {
+      for (int u = 0; u < U; ++u) {
+        if (rr[u] >= nrows) continue;
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[u][e] *= scale;
-        Cols8<TO, kVec>::store(out + dst[u], nu, left[u], x[u]);
+        Cols8<TO, false>::store(out + (row0 + rr[u]) * ldo + cc[u], nu, (int)d - cc[u], x[u]);
       }
+    }
   }
 }
 
@@ -136,14 +156,18 @@ bool rows_aligned16(const void* p, int64_t ld, size_t esize) {
 }
 
 template <typename TW, typename TO>
-cudaError_t launch_fwd_t(const EmbedFwdArgs& a, cudaStream_t st) {
+cudaError_t launch_fwd_t(const EmbedFwdArgs& a, const DeviceInfo& dev, cudaStream_t st) {
   const bool vec = a.d % 8 == 0 && rows_aligned16(a.weight, a.ldw, sizeof(TW)) &&
                    rows_aligned16(a.out, a.ldo, sizeof(TO));
+  constexpr int U = sizeof(TW) == 4 ? 4 : 8;
   const int nu = (int)((a.d + 7) / 8);
-  // a CTA's units fill one unrolled step of its threads
-  int64_t rows = kThreads * kFwdUnroll / nu;
+  // a CTA's units fill one unrolled step of its threads, unless that leaves
+  // SMs without a CTA
+  int64_t rows = kThreads * (vec ? U : 4) / nu;
+  const int64_t spread = a.n / (2 * (int64_t)dev.sms);
+  if (rows > spread) rows = spread;
   if (rows < 1) rows = 1;
-  auto kern = vec ? embed_fwd_kernel<TW, TO, true> : embed_fwd_kernel<TW, TO, false>;
+  auto kern = vec ? embed_fwd_kernel<TW, TO, true, U> : embed_fwd_kernel<TW, TO, false, 4>;
   return launch_pdl(kern, dim3((unsigned)((a.n + rows - 1) / rows)), dim3(kThreads), 0, st, 1,
                     a.ids, a.n, static_cast<const TW*>(a.weight), a.V, a.d, a.ldw, a.scale,
                     static_cast<TO*>(a.out), a.ldo, (int)rows, nu);
@@ -199,11 +223,11 @@ int64_t padded_cols(int64_t d) {
 }
 
 struct BwdLayout {
-  size_t key[2], pos[2], hist[kMaxPasses], bad, present, list, part, total;
+  size_t key[2], pos[2], hist[kMaxPasses], bad, list, part, total;
   int64_t dpad;
 };
 
-// header | keys and positions, twice | histograms | flags | ...
+// header | keys and positions, twice | histograms | flags | partial sums
 BwdLayout bwd_layout(int64_t n, int64_t V, int64_t d) {
   const SortPlan s = sort_plan(n, V);
   BwdLayout l;
@@ -218,7 +242,6 @@ BwdLayout bwd_layout(int64_t n, int64_t V, int64_t d) {
   for (int k = 0; k < kMaxPasses; ++k)
     l.hist[k] = take(k < s.passes ? 4 * (size_t)kMaxBins * s.tiles : 0);
   l.bad = take(4 * (size_t)s.tiles);
-  l.present = take((size_t)V);
   l.list = take(4 * (size_t)(s.seg_tiles + 1));
   l.dpad = padded_cols(d);
   l.part = take(2 * (size_t)s.seg_tiles * (size_t)l.dpad * 4);
@@ -226,35 +249,79 @@ BwdLayout bwd_layout(int64_t n, int64_t V, int64_t d) {
   return l;
 }
 
-// First pass over the ids: 32-bit keys (ignored tokens sort behind every id),
-// the histogram of each tile's first digit, and everything the later kernels
-// add to is cleared.
+// The rows of dW that the sort's kernels clear beside their own work.  The
+// sort is a chain of small latency-bound steps on few SMs, the clearing a
+// stream of stores: each kernel of the chain gets CTAs that write its share
+// of the zeros.  Every row is cleared (which ids occur is not known yet); the
+// rows that occur are written over by the sums.
+struct Clear {
+  char* base;      // dense rows: one run of bytes
+  int64_t bytes;   // of this kernel's share
+  int64_t rows;    // pitched rows: count, width and pitch in bytes
+  int64_t width, pitch;
+  unsigned first;  // CTAs below it belong to the sort
+};
+constexpr int64_t kClearBytes = 131072;  // per CTA
+
+__device__ __forceinline__ void clear_rows(const Clear& c) {
+  const int64_t k = blockIdx.x - c.first;
+  const int nt = blockDim.x;
+  if (c.rows == 0) {
+    const int64_t a = k * kClearBytes;
+    const int64_t n = min(kClearBytes, c.bytes - a);
+    char* p = c.base + a;
+    // (base is 16-byte aligned; only the last run has a ragged end)
+    for (int64_t i = 16 * (int64_t)threadIdx.x; i + 16 <= n; i += 16 * nt)
+      st_stream(p + i, make_uint4(0, 0, 0, 0));
+    for (int64_t i = n / 16 * 16 + 2 * (int64_t)threadIdx.x; i < n; i += 2 * nt)
+      *reinterpret_cast<uint16_t*>(p + i) = 0;
+    return;
+  }
+  const int64_t per = max((int64_t)1, kClearBytes / c.width);
+  const int64_t r1 = min(c.rows, (k + 1) * per);
+  const uintptr_t any = reinterpret_cast<uintptr_t>(c.base) | (uintptr_t)c.width | (uintptr_t)c.pitch;
+  for (int64_t r = k * per; r < r1; ++r) {
+    char* row = c.base + r * c.pitch;
+    if (any % 16 == 0)
+      for (int64_t i = threadIdx.x; i < c.width / 16; i += nt)
+        st_stream(row + 16 * i, make_uint4(0, 0, 0, 0));
+    else if (any % 4 == 0)
+      for (int64_t i = threadIdx.x; i < c.width / 4; i += nt) reinterpret_cast<uint32_t*>(row)[i] = 0;
+    else
+      for (int64_t i = threadIdx.x; i < c.width / 2; i += nt) reinterpret_cast<uint16_t*>(row)[i] = 0;
+  }
+}
+
+// Key of an id: ignored tokens sort behind every id.
+__device__ __forceinline__ int32_t key_of(int64_t id, int64_t V, int64_t pad_id, int* outside) {
+  const bool in = id >= 0 && id < V;
+  *outside |= !in && !(pad_id >= 0 && id == pad_id);
+  return !in || id == pad_id ? (int32_t)V : (int32_t)id;
+}
+
+// First pass over the ids: 32-bit keys, the histogram of each tile's first
+// digit, and what the later kernels add to is cleared.
 __global__ void __launch_bounds__(kSortThreads) embed_keys_kernel(
     const int64_t* __restrict__ ids, int64_t n, int64_t V, int64_t pad_id, int64_t tile, int dbits,
-    int32_t* __restrict__ key, int32_t* __restrict__ hist0, int32_t* __restrict__ hist_rest,
-    int64_t n_rest, uint32_t* __restrict__ bad, uint8_t* __restrict__ present, int64_t n_present,
-    int32_t* __restrict__ list) {
+    int32_t* key, int32_t* hist0, int32_t* hist_rest, int64_t n_rest, uint32_t* bad, int32_t* list,
+    const Clear clr) {
   __shared__ int32_t h[kMaxBins];
   pdl_wait();
   pdl_trigger();
+  if (blockIdx.x >= clr.first) return clear_rows(clr);
   const int tid = threadIdx.x;
   h[tid] = 0;
   __syncthreads();
-  const int64_t all = (int64_t)gridDim.x * kSortThreads;
+  const int64_t all = (int64_t)clr.first * kSortThreads;
   const int64_t me = (int64_t)blockIdx.x * kSortThreads + tid;
   for (int64_t k = me; k < n_rest; k += all) hist_rest[k] = 0;
-  for (int64_t k = me; k < (n_present + 15) / 16; k += all)
-    reinterpret_cast<uint4*>(present)[k] = make_uint4(0, 0, 0, 0);
   if (me == 0) list[0] = 0;
   const int64_t a = (int64_t)blockIdx.x * tile, b = min(a + tile, n);
   const uint32_t mask = (1u << dbits) - 1u;
   int outside = 0;
+#pragma unroll 4
   for (int64_t i = a + tid; i < b; i += kSortThreads) {
-    const int64_t id = __ldg(ids + i);
-    const bool in = id >= 0 && id < V;
-    const bool skip = !in || id == pad_id;
-    outside |= !in && !(pad_id >= 0 && id == pad_id);
-    const int32_t k = skip ? (int32_t)V : (int32_t)id;
+    const int32_t k = key_of(__ldg(ids + i), V, pad_id, &outside);
     key[i] = k;
     atomicAdd(&h[(uint32_t)k & mask], 1);
   }
@@ -263,31 +330,97 @@ __global__ void __launch_bounds__(kSortThreads) embed_keys_kernel(
   if (tid == 0) bad[blockIdx.x] = any ? kFlagTokenRange : 0u;
 }
 
+struct SortShared {
+  int32_t base[kMaxBins];
+  int32_t wh[kSortWarps][kMaxBins];
+  int32_t wsum[kSortWarps];
+};
+
+// Exclusive prefix over the bins of `total` (one per thread), plus `before`.
+__device__ __forceinline__ void bin_bases(SortShared& sh, int32_t total, int32_t before) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int32_t x = total;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sh.wsum[warp] = x;
+  __syncthreads();
+  int32_t run = x - total + before;
+  for (int k = 0; k < warp; ++k) run += sh.wsum[k];
+  sh.base[tid] = run;
+}
+
+// Ranks the elements [at, at + kBatch) below b in order (warp match, then a
+// prefix over the warps) and hands each its output position; sh.base moves on.
+template <typename Load, typename Emit>
+__device__ __forceinline__ void scatter_batch(SortShared& sh, int64_t at, int64_t b, int shift,
+                                              uint32_t mask, Load load, Emit emit) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int R = kPerWarp / 32;
+#pragma unroll
+  for (int k = 0; k < kSortWarps; ++k) sh.wh[k][tid] = 0;
+  int32_t kk[R], pp[R], rank[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t i = at + warp * kPerWarp + r * 32 + lane;
+    kk[r] = -1;
+    pp[r] = 0;
+    if (i < b) load(i, kk[r], pp[r]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const bool live = kk[r] >= 0;
+    const uint32_t dg = live ? ((uint32_t)kk[r] >> shift) & mask : 0xffffffffu;
+    const uint32_t same = __match_any_sync(0xffffffffu, dg);
+    const uint32_t below = same & ((1u << lane) - 1u);
+    const int32_t old = live ? sh.wh[warp][dg] : 0;
+    __syncwarp();
+    if (live && below == 0) sh.wh[warp][dg] = old + __popc(same);
+    __syncwarp();
+    rank[r] = old + __popc(below);
+  }
+  __syncthreads();
+  {
+    int32_t first = sh.base[tid];
+#pragma unroll
+    for (int k = 0; k < kSortWarps; ++k) {
+      const int32_t c = sh.wh[k][tid];
+      sh.wh[k][tid] = first;
+      first += c;
+    }
+    sh.base[tid] = first;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (kk[r] >= 0) emit(kk[r], pp[r], sh.wh[warp][((uint32_t)kk[r] >> shift) & mask] + rank[r]);
+  __syncthreads();
+}
+
 // One stable radix pass.  Each CTA derives its tile's first output position
 // of every digit from the tiles' histograms (all digits below it, then the
-// same digit in earlier tiles), ranks its elements in order (warp match, then
-// a prefix over the warps) and scatters them.  While it does, it counts the
-// next pass's digit per destination tile (integer atomics: any order gives
-// the same counts).
+// same digit in earlier tiles) and scatters its elements in order.  While it
+// does, it counts the next pass's digit per destination tile (integer
+// atomics: any order gives the same counts).
 __global__ void __launch_bounds__(kSortThreads) embed_scatter_kernel(
     const int32_t* key, const int32_t* pos, int64_t n, int64_t tile, int shift, int dbits,
     const int32_t* hist, int32_t* hist_next, int32_t* key_out, int32_t* pos_out,
-    const uint32_t* bad, WsHeader* hdr, uint8_t* present, int32_t V) {
-  __shared__ int32_t base[kMaxBins];
-  __shared__ int32_t wh[kSortWarps][kMaxBins];
-  __shared__ int32_t wsum[kSortWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int tiles = gridDim.x;
+    const uint32_t* bad, WsHeader* hdr, const Clear clr) {
+  __shared__ SortShared sh;
+  const int tid = threadIdx.x;
+  const int tiles = (int)clr.first;
   const uint32_t mask = (1u << dbits) - 1u;
   pdl_wait();
   pdl_trigger();
+  if (blockIdx.x >= clr.first) return clear_rows(clr);
   if (bad != nullptr && blockIdx.x == 0) {
     uint32_t f = 0;
     for (int t = tid; t < tiles; t += kSortThreads) f |= bad[t];
     const int any = __syncthreads_or((int)f);
     if (tid == 0) hdr->flags = any ? kFlagTokenRange : 0u;
   }
-  // first output position of digit `tid` in this tile
   int32_t before = 0, total = 0;
 #pragma unroll 8
   for (int t = 0; t < tiles; ++t) {
@@ -295,67 +428,76 @@ __global__ void __launch_bounds__(kSortThreads) embed_scatter_kernel(
     before += t < (int)blockIdx.x ? c : 0;
     total += c;
   }
-  int32_t x = total;
-  for (int o = 1; o < 32; o <<= 1) {
-    const int32_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) wsum[warp] = x;
-  __syncthreads();
-  int32_t run = x - total + before;
-  for (int k = 0; k < warp; ++k) run += wsum[k];
-  base[tid] = run;
-
+  bin_bases(sh, total, before);
   const int64_t a = (int64_t)blockIdx.x * tile, b = min(a + tile, n);
-  for (int64_t at = a; at < b; at += kBatch) {
-#pragma unroll
-    for (int k = 0; k < kSortWarps; ++k) wh[k][tid] = 0;
+  for (int64_t at = a; at < b; at += kBatch)
+    scatter_batch(
+        sh, at, b, shift, mask,
+        [&](int64_t i, int32_t& k, int32_t& p) {
+          k = key[i];
+          p = pos != nullptr ? pos[i] : (int32_t)i;
+        },
+        [&](int32_t k, int32_t p, int32_t to) {
+          key_out[to] = k;
+          pos_out[to] = p;
+          if (hist_next != nullptr)
+            atomicAdd(hist_next + (int64_t)(to / tile) * kMaxBins +
+                          (((uint32_t)k >> (shift + dbits)) & mask),
+                      1);
+        });
+}
+
+// The whole sort of up to kOneCta tokens by one CTA: every pass counts and
+// scatters between shared-memory arrays.
+constexpr int kOneCta = 4096;
+struct OneShared {
+  SortShared s;
+  int32_t key[2][kOneCta], pos[2][kOneCta];
+  int32_t hist[kMaxBins];
+};
+__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(
+    const int64_t* __restrict__ ids, int n, int64_t V, int64_t pad_id, int passes, int dbits,
+    int32_t* key_out, int32_t* pos_out, int32_t* list, WsHeader* hdr, const Clear clr) {
+  extern __shared__ __align__(16) unsigned char one_raw[];
+  OneShared& o = *reinterpret_cast<OneShared*>(one_raw);
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x >= clr.first) return clear_rows(clr);
+  const int tid = threadIdx.x;
+  const uint32_t mask = (1u << dbits) - 1u;
+  int outside = 0;
+#pragma unroll 4
+  for (int i = tid; i < n; i += kSortThreads) {
+    o.key[0][i] = key_of(__ldg(ids + i), V, pad_id, &outside);
+    o.pos[0][i] = i;
+  }
+  const int any = __syncthreads_or(outside);
+  if (tid == 0) {
+    hdr->flags = any ? kFlagTokenRange : 0u;
+    list[0] = 0;
+  }
+  for (int p = 0; p < passes; ++p) {
+    const int shift = p * dbits, from = p & 1;
+    o.hist[tid] = 0;
     __syncthreads();
-    int32_t kk[kPerWarp / 32], pp[kPerWarp / 32], rank[kPerWarp / 32];
-#pragma unroll
-    for (int r = 0; r < kPerWarp / 32; ++r) {
-      const int64_t i = at + warp * kPerWarp + r * 32 + lane;
-      kk[r] = i < b ? key[i] : -1;
-      pp[r] = i < b ? (pos != nullptr ? pos[i] : (int32_t)i) : 0;
-    }
-#pragma unroll
-    for (int r = 0; r < kPerWarp / 32; ++r) {
-      const bool live = kk[r] >= 0;
-      const uint32_t dg = live ? ((uint32_t)kk[r] >> shift) & mask : 0xffffffffu;
-      const uint32_t same = __match_any_sync(0xffffffffu, dg);
-      const uint32_t below = same & ((1u << lane) - 1u);
-      const int32_t old = live ? wh[warp][dg] : 0;
-      __syncwarp();
-      if (live && below == 0) wh[warp][dg] = old + __popc(same);
-      __syncwarp();
-      rank[r] = old + __popc(below);
-    }
+    for (int i = tid; i < n; i += kSortThreads)
+      atomicAdd(&o.hist[((uint32_t)o.key[from][i] >> shift) & mask], 1);
     __syncthreads();
-    {
-      int32_t first = base[tid];
-#pragma unroll
-      for (int k = 0; k < kSortWarps; ++k) {
-        const int32_t c = wh[k][tid];
-        wh[k][tid] = first;
-        first += c;
-      }
-      base[tid] = first;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kPerWarp / 32; ++r) {
-      if (kk[r] < 0) continue;
-      const uint32_t dg = ((uint32_t)kk[r] >> shift) & mask;
-      const int32_t to = wh[warp][dg] + rank[r];
-      key_out[to] = kk[r];
-      pos_out[to] = pp[r];
-      if (hist_next != nullptr)
-        atomicAdd(hist_next + (int64_t)(to / tile) * kMaxBins +
-                      (((uint32_t)kk[r] >> (shift + dbits)) & mask),
-                  1);
-      if (present != nullptr && kk[r] < V) present[kk[r]] = 1;
-    }
-    __syncthreads();
+    bin_bases(o.s, o.hist[tid], 0);
+    const bool last = p + 1 == passes;
+    int32_t* ko = last ? key_out : o.key[from ^ 1];
+    int32_t* po = last ? pos_out : o.pos[from ^ 1];
+    for (int at = 0; at < n; at += kBatch)
+      scatter_batch(
+          o.s, at, n, shift, mask,
+          [&](int64_t i, int32_t& k, int32_t& q) {
+            k = o.key[from][i];
+            q = o.pos[from][i];
+          },
+          [&](int32_t k, int32_t q, int32_t to) {
+            ko[to] = k;
+            po[to] = q;
+          });
   }
 }
 
@@ -368,10 +510,8 @@ struct SegParams {
   const int32_t* pos;
   int64_t n, V, d, ldd, ldw, dpad;
   float scale;
-  const uint8_t* present;
-  float* part;    // [seg tiles][2][dpad]: an id's rows in a tile that begins / ends inside the id
-  int32_t* list;  // count, then the tiles in which an id begins that ends in a later one
-  int64_t seg_blocks;
+  float* part;    // [seg tiles][2][dpad]: an id's rows in a tile that it began before (0), goes on after (1)
+  int32_t* list;  // count, then the tiles in which a split id begins
   int tpr, groups;  // threads per row, rows side by side in a CTA
   int cols;         // columns of one CTA in y (8 per thread of a row)
 };
@@ -391,52 +531,79 @@ __device__ __forceinline__ void write_row(TW* row, int step, int left, bool accu
   Cols8<TW, kVec>::store(row, step, left, x);
 }
 
-constexpr int kSegUnroll = 8;
-constexpr int kZeroRows = 16;  // rows of dW one CTA clears
+// One thread's 8 columns of a token's row, as loaded.
+template <typename T, bool kVec>
+struct RowPart;
+template <typename T>
+struct RowPart<T, true> {
+  Vec8<T> v;
+  __device__ __forceinline__ void load(const T* p, int, int) { v.load_stream(p); }
+  __device__ __forceinline__ void get(float* x) const { v.unpack(x); }
+};
+template <typename T>
+struct RowPart<T, false> {
+  float v[8];
+  __device__ __forceinline__ void load(const T* p, int step, int left) {
+    Cols8<T, false>::load(p, step, left, v);
+  }
+  __device__ __forceinline__ void get(float* x) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = v[k];
+  }
+};
 
-// A group of `tpr` threads sums kSegEntries sorted entries, 8 columns per
-// thread, and writes a row whenever the id changes.  Ids that begin before
-// or end after the group's entries leave partial sums for
-// embed_join_kernel.  CTAs past seg_blocks write the zero rows.
+constexpr int kSegUnroll = 8;
+
+// A group of `tpr` threads takes kSegEntries sorted entries (a tile), 8
+// columns per thread, and writes a row whenever the id changes.  An id that
+// goes on past its tile is finished by the group it began in, unless it fills
+// a whole further tile: then it is split at the tiles, every tile leaves its
+// partial sum, and embed_join_kernel adds them.  Both neighbours decide that
+// from the same keys: the id at a tile's first entry a is split iff it began
+// before the previous tile (key[a - Q - 1]) or reaches past this one
+// (key[a + Q]).
 template <typename TD, typename TW, bool kVec, bool kAcc>
-__global__ void __launch_bounds__(kThreads) embed_sum_kernel(const SegParams p,
-                                                             const TD* __restrict__ dout,
-                                                             TW* __restrict__ dw) {
+__global__ void __launch_bounds__(kThreads, 2) embed_sum_kernel(const SegParams p,
+                                                                const TD* __restrict__ dout,
+                                                                TW* dw) {
+  constexpr int Q = kSegEntries;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
-  if ((int64_t)blockIdx.x >= p.seg_blocks) {
-    const int64_t r0 = ((int64_t)blockIdx.x - p.seg_blocks) * kZeroRows;
-    const int nr = (int)min((int64_t)kZeroRows, p.V - r0);
-    const int64_t c0 = (int64_t)blockIdx.y * p.cols;
-    const int nc = (int)min((int64_t)p.cols, p.d - c0);
-    for (int r = 0; r < nr; ++r) {
-      if (p.present[r0 + r]) continue;
-      TW* row = dw + (r0 + r) * p.ldw + c0;
-      if (kVec) {
-        for (int k = tid; k < nc * (int)sizeof(TW) / 16; k += kThreads)
-          st_stream(reinterpret_cast<char*>(row) + 16 * k, make_uint4(0, 0, 0, 0));
-      } else {
-        for (int k = tid; k < nc; k += kThreads) row[k] = 0;
-      }
-    }
-    return;
-  }
   const int grp = tid / p.tpr, l = tid - grp * p.tpr;
   if (grp >= p.groups) return;
   const int64_t t = (int64_t)blockIdx.x * p.groups + grp;
-  const int64_t a = t * kSegEntries, b = min(a + kSegEntries, p.n);
+  const int64_t a = t * Q, b = min(a + Q, p.n);
   if (a >= p.n) return;
-  int32_t cur = p.key[a];
-  if (cur >= p.V) return;  // ignored tokens from here on
   const int64_t c0 = (int64_t)blockIdx.y * p.cols + (kVec ? 8 * l : l);
   const int left = (int)min((int64_t)p.cols, p.d - (int64_t)blockIdx.y * p.cols) - (kVec ? 8 * l : l);
   const int step = p.tpr;
   if (left <= 0) return;
-  bool open = a > 0 && p.key[a - 1] == cur;
+  // the keys that decide about the tile's ends (and the first entries') in
+  // one round of loads
+  const int32_t first = p.key[a];
+  const int32_t prev = a > 0 ? p.key[a - 1] : -1;
+  const int32_t prev2 = a > Q ? p.key[a - Q - 1] : -1;
+  const int32_t last = p.key[b - 1];
+  const int32_t next = b < p.n ? p.key[b] : -1;
+  const int32_t next2 = b + Q < p.n ? p.key[b + Q] : -1;
+  int32_t k[kSegUnroll], at[kSegUnroll];
+#pragma unroll
+  for (int u = 0; u < kSegUnroll; ++u) {
+    k[u] = a + u < p.n ? p.key[a + u] : INT32_MAX;
+    at[u] = a + u < p.n ? p.pos[a + u] : 0;
+  }
+  if (first >= p.V) return;  // ignored tokens from here on
+  const bool head = prev == first;
+  bool open = head && (prev2 == first || next == first);  // split: this tile's share of it
+  const bool skip = head && !open;                         // the tile before finishes it
+  const bool goes_on = next == last && last < p.V;
+  const bool split = goes_on && (next2 == last || (open && last == first));
+  const bool extend = goes_on && !split;
   // partial sums keep the thread's 8 columns side by side
   float* part = p.part + 2 * t * p.dpad + (int64_t)blockIdx.y * p.cols + 8 * l;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  int32_t cur = -1;
   auto flush_part = [&](int which) {
     float4* q = reinterpret_cast<float4*>(part + which * p.dpad);
     q[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
@@ -448,32 +615,46 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const SegParams p,
     else
       write_row<TW, kVec>(dw + cur * p.ldw + c0, step, left, kAcc, p.scale, acc);
   };
-  for (int64_t e = a; e < b && cur < p.V; e += kSegUnroll) {
-    int32_t k[kSegUnroll];
-    float x[kSegUnroll][8];
+  const int64_t stop = extend ? min(b + Q, p.n) : b;
+  for (int64_t e = a; e < stop; e += kSegUnroll) {
+    RowPart<TD, kVec> x[kSegUnroll];
+    bool use[kSegUnroll];
 #pragma unroll
     for (int u = 0; u < kSegUnroll; ++u) {
-      k[u] = e + u < b ? p.key[e + u] : INT32_MAX;
-      if (k[u] < p.V)
-        Cols8<TD, kVec>::load(dout + (int64_t)p.pos[e + u] * p.ldd + c0, step, left, x[u]);
+      use[u] = k[u] < p.V && (e + u < b || (extend && k[u] == last)) && !(skip && k[u] == first);
+      if (use[u]) x[u].load(dout + (int64_t)at[u] * p.ldd + c0, step, left);
+    }
+    int32_t kn[kSegUnroll];
+    const bool more = e + kSegUnroll < stop;
+#pragma unroll
+    for (int u = 0; u < kSegUnroll; ++u) {
+      const int64_t i = e + kSegUnroll + u;
+      kn[u] = more && i < p.n ? p.key[i] : INT32_MAX;
+      at[u] = more && i < p.n ? p.pos[i] : 0;
     }
 #pragma unroll
     for (int u = 0; u < kSegUnroll; ++u) {
-      if (k[u] == INT32_MAX || cur >= p.V) continue;
-      if (k[u] != cur) {
-        flush();
-        open = false;
-        cur = k[u];
+      if (use[u]) {
+        float v[8];
+        x[u].get(v);
+        if (k[u] != cur) {
+          if (cur >= 0) {
+            flush();
+            open = false;
+          }
+          cur = k[u];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) acc[c] = 0.f;
-        if (cur >= p.V) continue;
+          for (int c = 0; c < 8; ++c) acc[c] = v[c];
+        } else {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) acc[c] += v[c];
+        }
       }
-#pragma unroll
-      for (int c = 0; c < 8; ++c) acc[c] += x[u][c];
+      k[u] = kn[u];
     }
   }
-  if (cur >= p.V) return;
-  if (b < p.n && p.key[b] == cur) {  // the id goes on in the next tile
+  if (cur < 0) return;
+  if (split && cur == last) {
     flush_part(open ? 0 : 1);
     if (!open && l == 0 && blockIdx.y == 0) p.list[1 + atomicAdd(p.list, 1)] = (int32_t)t;
   } else {
@@ -483,11 +664,10 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const SegParams p,
 
 constexpr int kJoinCols = 128;  // columns of one join item (float4 per lane)
 
-// Ids that span several tiles: the partial sums of their tiles, added per
-// warp over every kWarps-th tile and then over the warps, both in order.
+// Split ids: the partial sums of their tiles, added per warp over every
+// kWarps-th tile and then over the warps, both in order.
 template <typename TW, bool kVec, bool kAcc>
-__global__ void __launch_bounds__(kThreads) embed_join_kernel(const SegParams p,
-                                                              TW* __restrict__ dw) {
+__global__ void __launch_bounds__(kThreads) embed_join_kernel(const SegParams p, TW* dw) {
   __shared__ float4 s_acc[kWarps][32];
   pdl_wait();
   pdl_trigger();
@@ -498,18 +678,16 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const SegParams p,
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
     const int64_t t = p.list[1 + it / ny];
     const int64_t c = (it % ny) * kJoinCols + 4 * lane;
-    const int64_t next = (t + 1) * kSegEntries;
-    const int32_t v = p.key[next];
-    // end of the id's entries
-    int64_t lo = next + 1, hi = p.n;
-    while (lo < hi) {
-      const int64_t mid = (lo + hi) >> 1;
-      if (p.key[mid] <= v)
-        lo = mid + 1;
-      else
-        hi = mid;
+    const int32_t v = p.key[(t + 1) * kSegEntries];
+    // the last tile that begins with the id
+    int64_t last = t + 1;
+    for (;;) {
+      const int64_t e = (last + 1 + lane) * kSegEntries;
+      const uint32_t same = __ballot_sync(0xffffffffu, e < p.n && p.key[e < p.n ? e : 0] == v);
+      const int run = same == 0xffffffffu ? 32 : __ffs(~same) - 1;
+      last += run;
+      if (run < 32) break;
     }
-    const int64_t last = (lo - 1) / kSegEntries;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (c < p.dpad) {
 #pragma unroll 4
@@ -562,10 +740,9 @@ cudaError_t launch_sums(const EmbedBwdArgs& a, SegParams p, const DeviceInfo& de
                         cudaStream_t st) {
   const unsigned ny = (unsigned)((p.d + p.cols - 1) / p.cols);
   const int64_t seg_tiles = (p.n + kSegEntries - 1) / kSegEntries;
-  p.seg_blocks = (seg_tiles + p.groups - 1) / p.groups;
-  const int64_t zero_blocks = kAcc ? 0 : (p.V + kZeroRows - 1) / kZeroRows;
+  const int64_t blocks = (seg_tiles + p.groups - 1) / p.groups;
   cudaError_t e = launch_pdl(embed_sum_kernel<TD, TW, kVec, kAcc>,
-                             dim3((unsigned)(p.seg_blocks + zero_blocks), ny), dim3(kThreads), 0,
+                             dim3((unsigned)blocks, ny), dim3(kThreads), 0,
                              st, 1, p, static_cast<const TD*>(a.dout), static_cast<TW*>(a.dweight));
   if (e != cudaSuccess || seg_tiles < 2) return e;
   const int64_t items = seg_tiles * ((p.dpad + kJoinCols - 1) / kJoinCols);
@@ -586,12 +763,12 @@ cudaError_t launch_sums_t(const EmbedBwdArgs& a, const SegParams& p, bool vec,
 
 }  // namespace
 
-cudaError_t launch_embed_fwd(const EmbedFwdArgs& a, const DeviceInfo&, cudaStream_t st) {
+cudaError_t launch_embed_fwd(const EmbedFwdArgs& a, const DeviceInfo& dev, cudaStream_t st) {
   if (a.n == 0) return cudaSuccess;
   if (a.wdtype == 0)
-    return a.odtype == 0 ? launch_fwd_t<float, float>(a, st) : launch_fwd_t<float, uint16_t>(a, st);
-  return a.odtype == 0 ? launch_fwd_t<uint16_t, float>(a, st)
-                       : launch_fwd_t<uint16_t, uint16_t>(a, st);
+    return a.odtype == 0 ? launch_fwd_t<float, float>(a, dev, st) : launch_fwd_t<float, uint16_t>(a, dev, st);
+  return a.odtype == 0 ? launch_fwd_t<uint16_t, float>(a, dev, st)
+                       : launch_fwd_t<uint16_t, uint16_t>(a, dev, st);
 }
 
 size_t embed_workspace_bytes(int64_t n, int64_t V, int64_t d) { return bwd_layout(n, V, d).total; }
@@ -601,7 +778,6 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, const DeviceInfo& dev, cudaS
   const BwdLayout l = bwd_layout(a.n, a.V, a.d);
   char* ws = static_cast<char*>(a.ws);
   auto i32 = [&](size_t off) { return reinterpret_cast<int32_t*>(ws + off); };
-  uint8_t* present = reinterpret_cast<uint8_t*>(ws + l.present);
   uint32_t* bad = reinterpret_cast<uint32_t*>(ws + l.bad);
   WsHeader* hdr = reinterpret_cast<WsHeader*>(ws);
   if (a.n == 0) {
@@ -610,27 +786,69 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, const DeviceInfo& dev, cudaS
     const size_t es = a.wdtype == 0 ? 4 : 2;
     return cudaMemset2DAsync(a.dweight, (size_t)a.ldw * es, 0, (size_t)a.d * es, (size_t)a.V, st);
   }
-  const int64_t n_rest =
-      s.passes > 1 ? (int64_t)(l.hist[s.passes - 1] - l.hist[1]) / 4 + (int64_t)kMaxBins * s.tiles
-                   : 0;
-  cudaError_t e = launch_pdl(embed_keys_kernel, dim3((unsigned)s.tiles), dim3(kSortThreads), 0, st,
-                             1, a.ids, a.n, a.V, a.pad_id, s.tile, s.dbits, i32(l.key[0]),
-                             i32(l.hist[0]), i32(l.hist[1]), n_rest, bad, present,
-                             a.accumulate ? (int64_t)0 : a.V, i32(l.list));
-  for (int k = 0; k < s.passes && e == cudaSuccess; ++k) {
-    e = launch_pdl(embed_scatter_kernel, dim3((unsigned)s.tiles), dim3(kSortThreads), 0, st, 1,
-                   (const int32_t*)i32(l.key[k & 1]),
-                   k == 0 ? (const int32_t*)nullptr : (const int32_t*)i32(l.pos[k & 1]), a.n,
-                   s.tile, k * s.dbits, s.dbits, (const int32_t*)i32(l.hist[k]),
-                   k + 1 < s.passes ? i32(l.hist[k + 1]) : (int32_t*)nullptr,
-                   i32(l.key[(k + 1) & 1]), i32(l.pos[(k + 1) & 1]),
-                   k == 0 ? (const uint32_t*)bad : (const uint32_t*)nullptr, hdr,
-                   k == 0 && !a.accumulate ? present : (uint8_t*)nullptr, (int32_t)a.V);
+  // the clearing, in equal shares over the sort's kernels
+  const size_t we = a.wdtype == 0 ? 4 : 2;
+  const bool one = a.n <= kOneCta;
+  const int shares = one ? 1 : s.passes + 1;
+  const bool dense = a.ldw == a.d && reinterpret_cast<uintptr_t>(a.dweight) % 16 == 0;
+  int64_t clear_ctas = 0;
+  auto clear_share = [&](int k, unsigned first) {
+    Clear c = {};
+    c.first = first;
+    clear_ctas = 0;
+    if (a.accumulate) return c;
+    char* base = static_cast<char*>(a.dweight);
+    if (dense) {
+      const int64_t total = a.V * a.d * (int64_t)we;
+      const int64_t runs = (total + kClearBytes - 1) / kClearBytes;
+      const int64_t r0 = runs * k / shares, r1 = runs * (k + 1) / shares;
+      c.base = base + r0 * kClearBytes;
+      c.bytes = (k + 1 == shares ? total : r1 * kClearBytes) - r0 * kClearBytes;
+      clear_ctas = r1 - r0;
+    } else {
+      const int64_t r0 = a.V * k / shares, r1 = a.V * (k + 1) / shares;
+      c.base = base + r0 * a.ldw * (int64_t)we;
+      c.rows = r1 - r0;
+      c.width = a.d * (int64_t)we;
+      c.pitch = a.ldw * (int64_t)we;
+      const int64_t per = kClearBytes / c.width > 0 ? kClearBytes / c.width : 1;
+      clear_ctas = (c.rows + per - 1) / per;
+      if (c.rows == 0) c.bytes = 0;
+    }
+    return c;
+  };
+  cudaError_t e;
+  int out = s.passes & 1;
+  if (one) {
+    const Clear c = clear_share(0, 1);
+    e = ensure_dynamic_smem((const void*)embed_sort_kernel, (int)sizeof(OneShared));
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(embed_sort_kernel, dim3((unsigned)(1 + clear_ctas)), dim3(kSortThreads),
+                   sizeof(OneShared), st, 1, a.ids, (int)a.n, a.V, a.pad_id, s.passes, s.dbits,
+                   i32(l.key[out]), i32(l.pos[out]), i32(l.list), hdr, c);
+  } else {
+    const int64_t n_rest =
+        s.passes > 1 ? (int64_t)(l.hist[s.passes - 1] - l.hist[1]) / 4 + (int64_t)kMaxBins * s.tiles
+                     : 0;
+    const Clear c = clear_share(0, (unsigned)s.tiles);
+    e = launch_pdl(embed_keys_kernel, dim3((unsigned)(s.tiles + clear_ctas)), dim3(kSortThreads), 0,
+                   st, 1, a.ids, a.n, a.V, a.pad_id, s.tile, s.dbits, i32(l.key[0]), i32(l.hist[0]),
+                   i32(l.hist[1]), n_rest, bad, i32(l.list), c);
+    for (int k = 0; k < s.passes && e == cudaSuccess; ++k) {
+      const Clear ck = clear_share(k + 1, (unsigned)s.tiles);
+      e = launch_pdl(embed_scatter_kernel, dim3((unsigned)(s.tiles + clear_ctas)),
+                     dim3(kSortThreads), 0, st, 1, (const int32_t*)i32(l.key[k & 1]),
+                     k == 0 ? (const int32_t*)nullptr : (const int32_t*)i32(l.pos[k & 1]), a.n,
+                     s.tile, k * s.dbits, s.dbits, (const int32_t*)i32(l.hist[k]),
+                     k + 1 < s.passes ? i32(l.hist[k + 1]) : (int32_t*)nullptr,
+                     i32(l.key[(k + 1) & 1]), i32(l.pos[(k + 1) & 1]),
+                     k == 0 ? (const uint32_t*)bad : (const uint32_t*)nullptr, hdr, ck);
+    }
   }
   if (e != cudaSuccess) return e;
   SegParams p = {};
-  p.key = i32(l.key[s.passes & 1]);
-  p.pos = i32(l.pos[s.passes & 1]);
+  p.key = i32(l.key[out]);
+  p.pos = i32(l.pos[out]);
   p.n = a.n;
   p.V = a.V;
   p.d = a.d;
@@ -638,13 +856,12 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, const DeviceInfo& dev, cudaS
   p.ldw = a.ldw;
   p.dpad = l.dpad;
   p.scale = a.scale;
-  p.present = present;
   p.part = reinterpret_cast<float*>(ws + l.part);
   p.list = i32(l.list);
   p.tpr = row_threads(a.d);
   p.groups = kThreads / p.tpr;
   p.cols = 8 * p.tpr;
-  const size_t de = a.ddtype == 0 ? 4 : 2, we = a.wdtype == 0 ? 4 : 2;
+  const size_t de = a.ddtype == 0 ? 4 : 2;
   const bool vec = a.d % 8 == 0 && rows_aligned16(a.dout, a.ldd, de) &&
                    rows_aligned16(a.dweight, a.ldw, we);
   if (a.ddtype == 0)

@@ -174,45 +174,43 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
 // ---------------------------------------------------------------------------
 
 template <typename TI, typename TO>
-__device__ __forceinline__ void chunk_scale(const TI* data, TO* out, int64_t numel, int64_t e0,
-                                            float coef) {
+__device__ __forceinline__ void chunk_scale(const void* data_, void* out_, int64_t numel,
+                                            int64_t chunk, float coef) {
   constexpr int kElems = (int)(kChunkBytes / sizeof(TI));
-  const int64_t e1 = min(e0 + kElems, numel);
+  constexpr int kUnits = kElems / 8 / kThreads;  // of 8 elements, per thread
+  const int64_t e0 = chunk * kElems;
+  const TI* data = static_cast<const TI*>(data_) + e0;
+  TO* out = static_cast<TO*>(out_) + e0;
+  const int n = (int)min((int64_t)kElems, numel - e0);
   const int tid = threadIdx.x;
-  const bool vec = reinterpret_cast<uintptr_t>(data) % 16 == 0 &&
-                   reinterpret_cast<uintptr_t>(out) % (8 * sizeof(TO)) % 16 == 0;
-  if (vec) {  // 8 elements a step
-    const int n8 = (int)((e1 - e0) / 8);
-    constexpr int U = kElems / 8 / kThreads;
+  const bool vec = (reinterpret_cast<uintptr_t>(data) | reinterpret_cast<uintptr_t>(out)) % 16 == 0;
+  int done = 0;
+  if (vec && n == kElems) {
+    constexpr int U = 4;  // units in flight
+    const TI* p = data + 8 * tid;
+    TO* q = out + 8 * tid;
 #pragma unroll
-    for (int h = 0; h < U; h += 4) {
-      float x[4][8];
+    for (int h = 0; h < kUnits; h += U) {
+      Vec8<TI> v[U];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int k = tid + (h + u) * kThreads;
-        if (k < n8) {
-          const char* p = reinterpret_cast<const char*>(data + e0 + (int64_t)k * 8);
-          Elt<TI>::unpack(*reinterpret_cast<const uint4*>(p), x[u]);
-          if (sizeof(TI) == 4)
-            Elt<TI>::unpack(*reinterpret_cast<const uint4*>(p + 16), x[u] + (sizeof(TI) == 4 ? 4 : 0));
-        }
-      }
+      for (int u = 0; u < U; ++u) v[u].load(p + (h + u) * kThreads * 8);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int k = tid + (h + u) * kThreads;
-        if (k < n8) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[u][e] *= coef;
-          char* q = reinterpret_cast<char*>(out + e0 + (int64_t)k * 8);
-          *reinterpret_cast<uint4*>(q) = Elt<TO>::pack(x[u]);
-          if (sizeof(TO) == 4)
-            *reinterpret_cast<uint4*>(q + 16) = Elt<TO>::pack(x[u] + (sizeof(TO) == 4 ? 4 : 0));
-        }
-      }
+      for (int u = 0; u < U; ++u) v[u].template store<true>(q + (h + u) * kThreads * 8, coef);
     }
-    e0 += (int64_t)n8 * 8;
+    return;
   }
-  for (int64_t e = e0 + tid; e < e1; e += kThreads) {
+  if (vec) {
+    const int n8 = n / 8;
+#pragma unroll 1
+    for (int k = tid; k < n8; k += kThreads) {
+      Vec8<TI> v;
+      v.load(data + 8 * k);
+      v.template store<true>(out + 8 * k, coef);
+    }
+    done = 8 * n8;
+  }
+#pragma unroll 4
+  for (int e = done + tid; e < n; e += kThreads) {
     float x;
     if constexpr (sizeof(TI) == 4)
       x = data[e];
@@ -227,7 +225,7 @@ __device__ __forceinline__ void chunk_scale(const TI* data, TO* out, int64_t num
 // kernel read last are the ones still in L2.  In place and under the limit
 // there is nothing to write.
 template <int CAP, bool kMax>
-__global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ Table<CAP> t,
+__global__ void __launch_bounds__(kThreads, 4) grad_scale_kernel(const __grid_constant__ Table<CAP> t,
                                                               const double* partial, int npartial,
                                                               float max_norm, float eps,
                                                               int copies, float* stats,
@@ -246,7 +244,7 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
   if (stats != nullptr && blockIdx.x == 0 && threadIdx.x == 0) {
     stats[0] = (float)norm;
     stats[1] = coef;
-    hdr->flags = isfinite(norm) ? 0u : kFlagValue;
+    hdr->flags = isfinite((float)norm) ? 0u : kFlagValue;
   }
   if (coef == 1.f && !copies) return;
   const int64_t chunks = t.first[t.count];
@@ -257,20 +255,16 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
     const int64_t n = t.numel[k], j = ch - t.first[k];
     switch (t.dt[k]) {
       case 0:
-        chunk_scale(static_cast<const float*>(t.data[k]), static_cast<float*>(t.out[k]), n,
-                    j * (kChunkBytes / 4), coef);
+        chunk_scale<float, float>(t.data[k], t.out[k], n, j, coef);
         break;
       case 1:
-        chunk_scale(static_cast<const uint16_t*>(t.data[k]), static_cast<float*>(t.out[k]), n,
-                    j * (kChunkBytes / 2), coef);
+        chunk_scale<uint16_t, float>(t.data[k], t.out[k], n, j, coef);
         break;
       case 2:
-        chunk_scale(static_cast<const float*>(t.data[k]), static_cast<uint16_t*>(t.out[k]), n,
-                    j * (kChunkBytes / 4), coef);
+        chunk_scale<float, uint16_t>(t.data[k], t.out[k], n, j, coef);
         break;
       default:
-        chunk_scale(static_cast<const uint16_t*>(t.data[k]), static_cast<uint16_t*>(t.out[k]), n,
-                    j * (kChunkBytes / 2), coef);
+        chunk_scale<uint16_t, uint16_t>(t.data[k], t.out[k], n, j, coef);
     }
   }
 }

@@ -7,6 +7,46 @@
 
 namespace grpo {
 
+// 8 consecutive elements (16-byte aligned) as they are stored, in registers.
+template <typename TI>
+struct Vec8 {
+  static constexpr int kWords = sizeof(TI) / 2;  // of 16 bytes
+  uint4 v[kWords];
+  __device__ __forceinline__ void load(const TI* p) {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) v[k] = reinterpret_cast<const uint4*>(p)[k];
+  }
+  // through the read-only path, not kept in L1
+  __device__ __forceinline__ void load_stream(const TI* p) {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) v[k] = ld_stream(reinterpret_cast<const uint4*>(p) + k);
+  }
+  __device__ __forceinline__ void fill(uint32_t word) {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) v[k] = make_uint4(word, word, word, word);
+  }
+  __device__ __forceinline__ void unpack(float* x) const {
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) Elt<TI>::unpack(v[k], x + k * Elt<TI>::kPerVec);
+  }
+  // times coef, rounded to TO; kStream: evict-first stores
+  template <bool kStream, typename TO>
+  __device__ __forceinline__ void store(TO* q, float coef) const {
+    float x[8];
+    unpack(x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] *= coef;
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(TO) / 2; ++k) {
+      const uint4 w = Elt<TO>::pack(x + k * Elt<TO>::kPerVec);
+      if (kStream)
+        st_stream(reinterpret_cast<uint4*>(q) + k, w);
+      else
+        reinterpret_cast<uint4*>(q)[k] = w;
+    }
+  }
+};
+
 // ---- embedding lookup and its gradient (embed.cu) ---------------------------
 
 struct EmbedFwdArgs {
@@ -77,7 +117,7 @@ struct VerifyArgs {
   float* logp;               // [N, K + 1]
   void* ws;
 };
-size_t verify_workspace_bytes(int64_t N);
+size_t verify_workspace_bytes(int64_t N, int64_t K);
 cudaError_t launch_verify(const VerifyArgs& a, const DeviceInfo& d, cudaStream_t st);
 
 }  // namespace grpo

@@ -10,12 +10,15 @@
 //   and argmax_v p_a(v) / e_v on the row after the last drafted token;
 //   with T = 0: x_j is accepted while it is argmax z_j, and argmax z_a emitted.
 //
-// One thread block cluster walks one sequence: every CTA streams its slice of
-// a row and keeps a running (max, sum of exponentials), the cluster's CTAs
-// exchange their partials through distributed shared memory, and all of them
-// take the same decision from the same bits.  Rows after the first rejection
-// are never read; the rejected row's second reading (for the race) comes out
-// of L2.  One launch, no atomics between sequences.
+// Two kernels.  verify_rows_kernel computes (max, sum of exponentials) of every
+// target and draft row, each row split over CTAs that work on their own; with
+// more rows than the GPU takes at once it runs position by position and leaves
+// out rows behind a rejection that is already known (the last CTA of a
+// position's rows decides it and publishes it; nothing waits for anything, and
+// a row that was read in vain changes no result).  verify_emit_kernel, one
+// thread block cluster per sequence, takes every position's decision at once,
+// one position per lane, and runs the race over the row that the sequence
+// stops at.
 //
 // Whole-number outputs must not depend on float32 rounding where a decision
 // is close, so the tests are made in float64 from float32 sums, and the race
@@ -23,17 +26,16 @@
 // best lower bound (a handful of a row) are compared in float64.
 #include <math.h>
 
-#include <map>
-#include <mutex>
-#include <tuple>
-
-#include "host_ctx.cuh"
 #include "ops.cuh"
 
 namespace grpo {
 namespace {
 
+constexpr int kRaceThreads = 512;
+constexpr int kRaceWarps = kRaceThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kMaxSplit = 16;          // CTAs per row of the rows kernel
+constexpr int64_t kMinPartBytes = 16384;  // of a row, when it is split
 constexpr int kCandidates = 1024;      // race candidates a CTA can hold
 constexpr float kMinTemperature = 1e-6f;  // below it a temperature counts as 0
 constexpr float kBig = 1e30f;          // maxima beyond it take the subtracting form below
@@ -100,21 +102,29 @@ struct VerifyParams {
   int32_t* n_accepted;
   float* logp;
   WsHeader* hdr;
-  uint32_t* status;  // [N]
-  int64_t chunk;     // elements of a row per CTA of the cluster
+  uint32_t* status;   // [N]
+  // (max, sum) of part s of target row (j, i) at [(j * N + i) * split + s]; the
+  // draft rows' after all of those.  arg: where a greedy target row has its
+  // maximum first.
+  float2* part;
+  int64_t* arg;
+  int32_t* rejected;  // [N]: a position at which the sequence is known to stop
+  uint32_t* ticket;   // [K * N]: CTAs done with a position's rows
+  int split;          // CTAs per row
+  int64_t part_elems; // elements of a row per CTA
+  int lazy;           // rows behind a known rejection are left out
+  int64_t chunk;      // elements of a row per CTA of the emitting cluster
 };
 
-// What a CTA tells the others about its slice of a row (rank 0 adds what the
-// decision needs, so that every CTA decides from the same bits).
-struct Part {
-  float mt, st, md, sd;      // target and draft: max, sum
-  int64_t arg;               // lowest index of the target's maximum (T = 0)
-  float u, temperature;
-  float xt, xd;              // logits of the drafted token
-  int64_t token;
-  int32_t bonus, flags, pad[2];
-};
-static_assert(sizeof(Part) == 64, "four 16-byte stores");
+__device__ __forceinline__ int32_t clamped_len(const VerifyParams& p, int64_t i, uint32_t* flags) {
+  const int32_t len = p.lens != nullptr ? p.lens[i] : (int32_t)p.K;
+  if (len >= 0 && len <= p.K) return len;
+  *flags |= kFlagLengthRange;
+  return len < 0 ? 0 : (int32_t)p.K;
+}
+__device__ __forceinline__ float temperature_of(const VerifyParams& p, int64_t i) {
+  return p.temperature != nullptr ? p.temperature[i] : 1.f;
+}
 
 struct Decision {
   int accept, emit;  // go on; or emit by race (1), argmax (2), nothing (3)
@@ -229,44 +239,156 @@ __device__ __forceinline__ RowStat row_stats(const T* row, int64_t v0, int64_t v
   return r;
 }
 
-struct Shared {
-  Part part[2][kMaxCluster];
-  float4 red[kWarps];     // (mt, st, md, sd) per warp
-  int64_t red_arg[kWarps];
-  Decision dec;
-  double win[2][kMaxCluster];
-  int64_t win_at[2][kMaxCluster];
-  double wred[kWarps];
-  int64_t wred_at[kWarps];
-  int best, count;
-  int32_t cand[kCandidates];
-  float cand_hi[kCandidates];
-};
+// Position j of sequence i: merge the parts of its rows in order, and decide.
+template <typename T>
+__device__ __forceinline__ void decide(const VerifyParams& p, const T* target, const T* draft,
+                                       int64_t i, int64_t j, int32_t len, float Ti, Decision& d) {
+  const bool greedy = Ti < kMinTemperature, bonus = j >= len;
+  const bool use_draft = draft != nullptr && !bonus && !greedy;
+  const Temper t = temper(greedy ? 1.f : Ti);
+  d.flags = 0;
+  d.accept = 0;
+  d.lp = 0.0;
+  d.token = -1;
+  d.arg = INT64_MAX;
+  int64_t x = -1;
+  float xt = 0.f, xd = 0.f, u = 0.f;
+  if (!bonus) {
+    x = p.tokens[i * p.K + j];
+    u = p.u[i * p.K + j];
+    if (x >= 0 && x < p.V) {
+      d.token = x;
+      xt = Elt<T>::load1(target + i * p.tls + j * p.tld + x);
+      if (use_draft) xd = Elt<T>::load1(draft + i * p.dls + j * p.dld + x);
+    } else {
+      d.flags |= kFlagTokenRange;
+    }
+  }
+  const volatile float2* tp = p.part + (j * p.N + i) * p.split;
+  const volatile int64_t* ta = p.arg + (j * p.N + i) * p.split;
+  const volatile float2* dp = p.part + ((p.K + 1 + j) * p.N + i) * p.split;
+  float mt = -INFINITY, st = 0.f, md = -INFINITY, sd = 0.f;
+  for (int k = 0; k < p.split; ++k) {
+    const float m2 = tp[k].x, s2 = tp[k].y;
+    if (greedy) {
+      const int64_t a2 = ta[k];
+      d.arg = m2 > mt ? a2 : (m2 == mt ? min(d.arg, a2) : d.arg);
+    }
+    merge(mt, st, m2, s2, t);
+    if (use_draft) {
+      const float m3 = dp[k].x, s3 = dp[k].y;
+      merge(md, sd, m3, s3, t);
+    }
+  }
+  d.mt = mt;
+  d.st = (double)st;
+  d.md = md;
+  d.sd = (double)sd;
+  bool defined = Ti >= 0.f && Ti <= 3.4e38f && mt > -INFINITY && mt < INFINITY && st > 0.f &&
+                 st < INFINITY;
+  if (use_draft) defined = defined && md > -INFINITY && md < INFINITY && sd > 0.f && sd < INFINITY;
+  if (!defined) {
+    d.emit = 3;
+    d.flags |= kFlagValue;
+    return;
+  }
+  d.emit = greedy ? 2 : 1;
+  if (d.token < 0) return;  // after the last draft, or an id outside [0, V)
+  d.lp = log_prob(xt, mt, d.st, t);
+  if (greedy) {
+    d.accept = d.token == d.arg;
+  } else {
+    const double lq = use_draft ? log_prob(xd, md, d.sd, t) : 0.0;
+    d.accept = xt > -INFINITY && (double)u * exp(lq - d.lp) < 1.0;
+  }
+}
 
-// The CTA's statistic of a row, left per warp in sh.red (x, y or z, w).
-template <bool kArg>
-__device__ __forceinline__ void warp_stats(RowStat r, const Temper& t, Shared& sh, bool draft) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// One row part per CTA.  Grid order: positions, then kinds (target, draft),
+// then sequences, then parts.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4) verify_rows_kernel(const VerifyParams p,
+                                                                  const T* __restrict__ target,
+                                                                  const T* __restrict__ draft) {
+  __shared__ float2 s_red[kWarps];
+  __shared__ int64_t s_arg[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_trigger();
+  const int s = (int)(blockIdx.x % (unsigned)p.split);
+  int64_t q = blockIdx.x / (unsigned)p.split;
+  const int64_t i = q % p.N;
+  q /= p.N;
+  const int kinds = draft != nullptr ? 2 : 1;
+  const int64_t j = q / kinds;
+  const bool is_draft = q % kinds == 1;
+  uint32_t flags = 0;
+  const int32_t len = clamped_len(p, i, &flags);
+  const float Ti = temperature_of(p, i);
+  const bool greedy = Ti < kMinTemperature;
+  if (j > len || (is_draft && (j == len || greedy))) return;
+  if (p.lazy && *(volatile int32_t*)(p.rejected + i) < j) return;
+  const Temper t = temper(greedy ? 1.f : Ti);
+  const int64_t v0 = min(p.V, s * p.part_elems), v1 = min(p.V, v0 + p.part_elems);
+  const T* row = is_draft ? draft + i * p.dls + j * p.dld : target + i * p.tls + j * p.tld;
+  RowStat r = greedy ? row_stats<T, true>(row, v0, v1, t) : row_stats<T, false>(row, v0, v1, t);
   for (int o = 16; o > 0; o >>= 1) {
     const float m2 = __shfl_xor_sync(0xffffffffu, r.m, o);
     const float s2 = __shfl_xor_sync(0xffffffffu, r.s, o);
-    if (kArg) {
+    if (greedy) {
       const int64_t a2 = __shfl_xor_sync(0xffffffffu, r.arg, o);
       r.arg = m2 > r.m ? a2 : (m2 == r.m ? min(r.arg, a2) : r.arg);
     }
     merge(r.m, r.s, m2, s2, t);
   }
   if (lane == 0) {
-    if (draft) {
-      sh.red[warp].z = r.m;
-      sh.red[warp].w = r.s;
-    } else {
-      sh.red[warp].x = r.m;
-      sh.red[warp].y = r.s;
-      sh.red_arg[warp] = r.arg;
-    }
+    s_red[warp] = make_float2(r.m, r.s);
+    s_arg[warp] = r.arg;
   }
+  __syncthreads();
+  if (tid != 0) return;
+  float m = s_red[0].x, sum = s_red[0].y;
+  int64_t arg = s_arg[0];
+  for (int k = 1; k < kWarps; ++k) {
+    const float2 o = s_red[k];
+    arg = o.x > m ? s_arg[k] : (o.x == m ? min(arg, s_arg[k]) : arg);
+    merge(m, sum, o.x, o.y, t);
+  }
+  const int64_t row_at = ((is_draft ? p.K + 1 : 0) + j) * p.N + i;
+  p.part[row_at * p.split + s] = make_float2(m, sum);
+  if (greedy) p.arg[row_at * p.split + s] = arg;
+  if (!p.lazy || j >= len) return;
+  __threadfence();
+  const uint32_t expect = (uint32_t)(p.split * (draft != nullptr && !greedy ? 2 : 1));
+  if (atomicAdd(p.ticket + j * p.N + i, 1u) + 1u != expect) return;
+  __threadfence();
+  Decision d;
+  decide<T>(p, target, draft, i, j, len, Ti, d);
+  if (!d.accept) atomicMin(p.rejected + i, (int32_t)j);
 }
+
+__global__ void __launch_bounds__(kThreads) verify_init_kernel(int32_t* rejected, int64_t n,
+                                                               uint32_t* ticket, int64_t m) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t all = (int64_t)gridDim.x * kThreads;
+  for (int64_t k = (int64_t)blockIdx.x * kThreads + threadIdx.x; k < n; k += all)
+    rejected[k] = INT32_MAX;
+  for (int64_t k = (int64_t)blockIdx.x * kThreads + threadIdx.x; k < m; k += all) ticket[k] = 0;
+}
+
+struct Shared {
+  Decision dec;
+  int stop;            // the position that the sequence stops at
+  uint32_t flags;
+  double win[2][kMaxCluster];
+  int64_t win_at[2][kMaxCluster];
+  int again[2][kMaxCluster];
+  double wred[kRaceWarps];
+  int64_t wred_at[kRaceWarps];
+  int best, count;
+  int32_t cand[kCandidates];
+  float cand_hi[kCandidates];
+};
 
 // The row's race in this CTA's slice: best score and its lowest index.
 struct Racer {
@@ -308,71 +430,103 @@ __device__ void race(const Racer& c, const T* tr, const T* dr, const float* nr, 
                      int64_t v1, Shared& sh, double& score, int64_t& at) {
   using E = Elt<T>;
   constexpr int EPV = E::kPerVec;
+  constexpr int U = 16 / EPV;  // vectors per thread and step: 16 elements
+  constexpr int kNoiseVecs = EPV / 4;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     sh.best = 0;
     sh.count = 0;
   }
   __syncthreads();
-  // one batch of a warp: raise the CTA's best lower bound, keep the elements
-  // that may still beat it
-  auto batch = [&](const float* lo, const float* hi, const int64_t* v, int n) {
-    float top = 0.f;
-    for (int k = 0; k < n; ++k) top = fmaxf(top, lo[k]);
+  // the CTA's best lower bound, raised by this warp's
+  auto raise = [&](float top) -> float {
     const unsigned wtop = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-    float bar = __int_as_float(*(volatile int*)&sh.best);
-    if (__uint_as_float(wtop) > bar) {
-      if (lane == 0) atomicMax(&sh.best, (int)wtop);
-      bar = __uint_as_float(wtop);
-    }
-    for (int k = 0; k < n; ++k)
-      if (hi[k] >= bar && hi[k] > 0.f && bar > 0.f) {
-        const int s = atomicAdd(&sh.count, 1);
-        if (s < kCandidates) {
-          sh.cand[s] = (int32_t)v[k];
-          sh.cand_hi[s] = hi[k];
-        }
+    const float bar = __int_as_float(*(volatile int*)&sh.best);
+    if (__uint_as_float(wtop) <= bar) return bar;
+    if (lane == 0) atomicMax(&sh.best, (int)wtop);
+    return __uint_as_float(wtop);
+  };
+  auto keep = [&](float hi, float bar, int64_t v) {
+    if (hi >= bar && hi > 0.f && bar > 0.f) {
+      const int s = atomicAdd(&sh.count, 1);
+      if (s < kCandidates) {
+        sh.cand[s] = (int32_t)v;
+        sh.cand_hi[s] = hi;
       }
+    }
   };
   const bool vec = reinterpret_cast<uintptr_t>(tr) % 16 == 0 && v0 % EPV == 0 &&
                    reinterpret_cast<uintptr_t>(nr) % 16 == 0 &&
                    (!c.has_draft || reinterpret_cast<uintptr_t>(dr) % 16 == 0);
   int64_t from = v0;
   if (vec) {
-    const int64_t nvec = (v1 - v0) / EPV;
-    for (int64_t base = 0; base < nvec; base += kThreads) {
-      const int64_t k = base + tid;
-      float lo[EPV], hi[EPV];
-      int64_t v[EPV];
+    const int nvec = (int)((v1 - v0) / EPV);
+    for (int base = 0; base < nvec; base += kRaceThreads * U) {
+      uint4 dx[U], dy[U], de[U][kNoiseVecs];
 #pragma unroll
-      for (int j = 0; j < EPV; ++j) {
-        lo[j] = hi[j] = 0.f;
-        v[j] = v0 + k * EPV + j;
-      }
-      if (k < nvec) {
-        float x[EPV], y[EPV], e[EPV];
-        E::unpack(ld_stream(tr + v0 + k * EPV), x);
-        if (c.has_draft) E::unpack(ld_stream(dr + v0 + k * EPV), y);
+      for (int w = 0; w < U; ++w) {
+        const int k = base + w * kRaceThreads + tid;
+        if (k < nvec) {
+          const int64_t v = v0 + (int64_t)k * EPV;
+          dx[w] = ld_stream(tr + v);
+          if (c.has_draft) dy[w] = ld_stream(dr + v);
 #pragma unroll
-        for (int j = 0; j < EPV; j += 4)
-          Elt<float>::unpack(ld_stream(nr + v0 + k * EPV + j), e + j);
-#pragma unroll
-        for (int j = 0; j < EPV; ++j) {
-          race_bounds(c, x[j], c.has_draft ? y[j] : 0.f, e[j], lo[j], hi[j]);
-          if (v[j] == c.skip) lo[j] = hi[j] = 0.f;
+          for (int h = 0; h < kNoiseVecs; ++h) de[w][h] = ld_stream(nr + v + 4 * h);
         }
       }
-      batch(lo, hi, v, EPV);
+      float hi[U][EPV], top = 0.f;
+#pragma unroll
+      for (int w = 0; w < U; ++w) {
+        const int k = base + w * kRaceThreads + tid;
+        float x[EPV], y[EPV], e[EPV];
+        E::unpack(dx[w], x);
+        if (c.has_draft) E::unpack(dy[w], y);
+#pragma unroll
+        for (int h = 0; h < kNoiseVecs; ++h) Elt<float>::unpack(de[w][h], e + 4 * h);
+#pragma unroll
+        for (int l = 0; l < EPV; ++l) {
+          hi[w][l] = 0.f;
+          if (k < nvec && v0 + (int64_t)k * EPV + l != c.skip) {
+            float lo;
+            race_bounds(c, x[l], c.has_draft ? y[l] : 0.f, e[l], lo, hi[w][l]);
+            top = fmaxf(top, lo);
+          }
+        }
+      }
+      const float bar = raise(top);
+#pragma unroll
+      for (int w = 0; w < U; ++w)
+#pragma unroll
+        for (int l = 0; l < EPV; ++l)
+          keep(hi[w][l], bar, v0 + (int64_t)(base + w * kRaceThreads + tid) * EPV + l);
     }
-    from = v0 + nvec * EPV;
+    from = v0 + (int64_t)nvec * EPV;
   }
-  for (int64_t base = from; base < v1; base += kThreads) {
-    float lo = 0.f, hi = 0.f;
-    const int64_t v = base + tid;
-    if (v < v1 && v != c.skip)
-      race_bounds(c, E::load1(tr + v), c.has_draft ? E::load1(dr + v) : 0.f, __ldg(nr + v), lo,
-                  hi);
-    batch(&lo, &hi, &v, 1);
+  constexpr int W = 8;
+  for (int64_t base = from; base < v1; base += kRaceThreads * W) {
+    float hi[W], top = 0.f, x[W], y[W], e[W];
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const int64_t v = base + w * kRaceThreads + tid;
+      if (v < v1) {
+        x[w] = E::load1(tr + v);
+        y[w] = c.has_draft ? E::load1(dr + v) : 0.f;
+        e[w] = __ldg(nr + v);
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const int64_t v = base + w * kRaceThreads + tid;
+      hi[w] = 0.f;
+      if (v < v1 && v != c.skip) {
+        float lo;
+        race_bounds(c, x[w], y[w], e[w], lo, hi[w]);
+        top = fmaxf(top, lo);
+      }
+    }
+    const float bar = raise(top);
+#pragma unroll
+    for (int w = 0; w < W; ++w) keep(hi[w], bar, base + w * kRaceThreads + tid);
   }
   __syncthreads();
   const float bar = __int_as_float(sh.best);
@@ -380,13 +534,13 @@ __device__ void race(const Racer& c, const T* tr, const T* dr, const float* nr, 
   score = 0.0;
   at = INT64_MAX;
   if (bar > 0.f && count <= kCandidates) {
-    for (int k = tid; k < count; k += kThreads)
+    for (int k = tid; k < count; k += kRaceThreads)
       if (sh.cand_hi[k] >= bar)
         better(score, at, race_score64(c, tr, dr, nr, sh.cand[k]), sh.cand[k]);
   } else {
     // bounds that do not separate anything (residuals at the level of the
     // rounding): every element in float64
-    for (int64_t v = v0 + tid; v < v1; v += kThreads)
+    for (int64_t v = v0 + tid; v < v1; v += kRaceThreads)
       better(score, at, race_score64(c, tr, dr, nr, v), v);
   }
   for (int o = 16; o > 0; o >>= 1) {
@@ -401,7 +555,7 @@ __device__ void race(const Racer& c, const T* tr, const T* dr, const float* nr, 
   __syncthreads();
   score = sh.wred[0];
   at = sh.wred_at[0];
-  for (int k = 1; k < kWarps; ++k) better(score, at, sh.wred[k], sh.wred_at[k]);
+  for (int k = 1; k < kRaceWarps; ++k) better(score, at, sh.wred[k], sh.wred_at[k]);
 }
 
 __device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v) {
@@ -410,232 +564,168 @@ __device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v) {
 __device__ __forceinline__ void st_cluster_s64(uint32_t addr, int64_t v) {
   asm volatile("st.shared::cluster.s64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
+__device__ __forceinline__ void st_cluster_s32(uint32_t addr, int v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
 
-// Thread 0 of each CTA: merge the ranks' parts in rank order and decide.
-__device__ __forceinline__ void decide(const Part* part, int ranks, bool has_draft, Decision& d) {
-  const Part& h = part[0];
-  d.flags = (uint32_t)h.flags;
-  d.token = h.token;
-  d.accept = 0;
-  d.lp = 0.0;
-  const bool greedy = h.temperature < kMinTemperature;
-  const Temper t = temper(greedy ? 1.f : h.temperature);
-  float mt = h.mt, st = h.st, md = h.md, sd = h.sd;
-  int64_t arg = h.arg;
-  for (int k = 1; k < ranks; ++k) {
-    const Part& o = part[k];
-    arg = o.mt > mt ? o.arg : (o.mt == mt ? min(arg, o.arg) : arg);
-    merge(mt, st, o.mt, o.st, t);
-    if (has_draft) merge(md, sd, o.md, o.sd, t);
-  }
-  d.mt = mt;
-  d.st = (double)st;
-  d.md = md;
-  d.sd = (double)sd;
-  d.arg = arg;
-  const bool use_draft = has_draft && !h.bonus && !greedy;
-  bool defined = h.temperature >= 0.f && h.temperature <= 3.4e38f && mt > -INFINITY &&
-                 mt < INFINITY && st > 0.f && st < INFINITY;
-  if (use_draft) defined = defined && md > -INFINITY && md < INFINITY && sd > 0.f && sd < INFINITY;
-  if (!defined) {
-    d.emit = 3;
-    d.flags |= kFlagValue;
-    return;
-  }
-  d.emit = greedy ? 2 : 1;
-  if (h.bonus || d.token < 0) return;  // (-1: a drafted token outside [0, V) is not accepted)
-  d.lp = log_prob(h.xt, mt, d.st, t);
-  if (greedy) {
-    d.accept = d.token == arg;
-  } else {
-    const double lq = use_draft ? log_prob(h.xd, md, d.sd, t) : 0.0;
-    d.accept = h.xt > -INFINITY && (double)h.u * exp(lq - d.lp) < 1.0;
-  }
-}
-
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) verify_kernel(const VerifyParams p,
-                                                             const T* __restrict__ target,
-                                                             const T* __restrict__ draft) {
+__global__ void __launch_bounds__(kRaceThreads, 2) verify_emit_kernel(
+    const VerifyParams p, const T* __restrict__ target, const T* __restrict__ draft) {
   __shared__ __align__(16) Shared sh;
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
   const uint32_t rank = cluster_ctarank(), ranks = cluster_size();
-  const bool has_draft = draft != nullptr;
   pdl_wait();
   pdl_trigger();
-  // every CTA of the cluster runs before the first distributed store
-  if (ranks > 1) cluster_sync();
+  const int64_t i = cluster_id_x();
+  uint32_t flags = 0;
+  const int32_t len = clamped_len(p, i, &flags);
+  const float Ti = temperature_of(p, i);
+  const Temper t = temper(Ti < kMinTemperature ? 1.f : Ti);
   if (blockIdx.x == 0 && tid == 0) {
     p.hdr->flags = kFlagIndirect;
     p.hdr->status_count = (uint32_t)p.N;
     p.hdr->status_check = ~(uint32_t)p.N;
   }
-  const int64_t v0 = min(p.V, (int64_t)rank * p.chunk), v1 = min(p.V, v0 + p.chunk);
-  int slot = 0, wslot = 0;
-  for (int64_t i = cluster_id_x(); i < p.N; i += nclusters_x()) {
-    int32_t len = p.lens != nullptr ? p.lens[i] : (int32_t)p.K;
-    uint32_t flags = 0;
-    if (len < 0 || len > p.K) {
-      flags = kFlagLengthRange;
-      len = len < 0 ? 0 : (int32_t)p.K;
+  // every position's decision, one per lane; the first that is not accepted
+  // is where the sequence stops (a row that was left out lies behind it)
+  // (a published rejection is taken over as it is: rows behind it are missing)
+  const int32_t known = p.lazy ? p.rejected[i] : INT32_MAX;
+  if (tid < 32) {
+    for (int64_t base = 0; base <= len; base += 32) {
+      const int64_t j = base + lane;
+      Decision d;
+      d.accept = 0;
+      d.flags = 0;
+      if (j <= len) decide<T>(p, target, draft, i, j, len, Ti, d);
+      if (j >= known) d.accept = 0;
+      const uint32_t stops = __ballot_sync(0xffffffffu, !d.accept);
+      const int first = stops ? __ffs(stops) - 1 : 32;
+      if (lane <= first) flags |= d.flags;
+      if (rank == 0 && lane < first) {
+        p.out_tokens[i * (p.K + 1) + j] = d.token;
+        p.logp[i * (p.K + 1) + j] = (float)d.lp;
+      }
+      if (lane == first) {
+        sh.dec = d;
+        sh.stop = (int)j;
+      }
+      if (stops) break;
     }
-    const float Ti = p.temperature != nullptr ? p.temperature[i] : 1.f;
-    const bool greedy = Ti < kMinTemperature;
-    const Temper t = temper(greedy ? 1.f : Ti);
-    int64_t j = 0;
-    const T* trow = nullptr;
-    const T* drow = nullptr;
-    for (;; ++j) {
-      const bool bonus = j >= len;
-      trow = target + i * p.tls + j * p.tld;
-      drow = has_draft && !bonus ? draft + i * p.dls + j * p.dld : nullptr;
-      if (greedy)
-        warp_stats<true>(row_stats<T, true>(trow, v0, v1, t), t, sh, false);
-      else
-        warp_stats<false>(row_stats<T, false>(trow, v0, v1, t), t, sh, false);
-      const bool read_draft = drow != nullptr && !greedy;
-      if (read_draft)
-        warp_stats<false>(row_stats<T, false>(drow, v0, v1, t), t, sh, true);
-      __syncthreads();
-      if (tid < (int)ranks) {
-        union {
-          Part part;
-          float4 f[4];
-        } o;
-        Part& a = o.part;
-        a.mt = sh.red[0].x;
-        a.st = sh.red[0].y;
-        a.arg = sh.red_arg[0];
-        a.md = read_draft ? sh.red[0].z : -INFINITY;
-        a.sd = read_draft ? sh.red[0].w : 0.f;
-        for (int k = 1; k < kWarps; ++k) {
-          const float4 r = sh.red[k];
-          a.arg = r.x > a.mt ? sh.red_arg[k] : (r.x == a.mt ? min(a.arg, sh.red_arg[k]) : a.arg);
-          merge(a.mt, a.st, r.x, r.y, t);
-          if (read_draft) merge(a.md, a.sd, r.z, r.w, t);
-        }
-        a.u = 0.f;
-        a.temperature = Ti;
-        a.xt = a.xd = 0.f;
-        a.token = -1;
-        a.bonus = bonus;
-        a.flags = 0;
-        a.pad[0] = a.pad[1] = 0;
-        if (rank == 0) {
-          a.flags = (int32_t)flags;
-          if (!bonus) {
-            const int64_t x = p.tokens[i * p.K + j];
-            a.u = p.u[i * p.K + j];
-            if (x >= 0 && x < p.V) {
-              a.token = x;
-              a.xt = Elt<T>::load1(trow + x);
-              if (read_draft) a.xd = Elt<T>::load1(drow + x);
-            } else {
-              a.flags |= (int32_t)kFlagTokenRange;
-            }
-          }
-        }
-        const uint32_t dst = map_to_rank(smem_u32(&sh.part[slot][rank]), (uint32_t)tid);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) st_cluster_f32x4(dst + 16 * k, o.f[k]);
-      }
-      __syncwarp();  // the cluster barrier instructions are warp-aligned
-      if (ranks > 1)
-        cluster_sync();
-      else
-        __syncthreads();
-      if (tid == 0) decide(sh.part[slot], (int)ranks, has_draft, sh.dec);
-      __syncthreads();
-      // (the part slots alternate: this one is rewritten two rows on, after a
-      // barrier that every CTA reaches only when it has decided here)
-      slot ^= 1;
-      flags |= sh.dec.flags;
-      // (a row after the last drafted token is never accepted: rank 0 says so)
-      if (!sh.dec.accept || j >= p.K) break;
-      if (rank == 0 && tid == 0) {
-        p.out_tokens[i * (p.K + 1) + j] = sh.dec.token;
-        p.logp[i * (p.K + 1) + j] = (float)sh.dec.lp;
-      }
-    }
-    // the emitted token
-    const Decision d = sh.dec;
-    int64_t token = -1;
-    if (d.emit == 2) {
-      token = d.arg;
-    } else if (d.emit == 1) {
-      Racer c;
-      c.t = t;
-      c.mt = d.mt;
-      c.rt = ref_of(d.mt, t);
-      c.bigt = is_big(d.mt);
-      c.it = (float)(1.0 / d.st);
-      c.st = d.st;
-      c.md = d.md;
-      c.rd = ref_of(d.md, t);
-      c.bigd = is_big(d.md);
-      c.sd = d.sd;
-      c.id = d.sd > 0.0 ? (float)(1.0 / d.sd) : 0.f;
-      const bool bonus = sh.part[slot ^ 1][0].bonus != 0;
-      c.has_draft = has_draft && !bonus;
-      c.skip = !has_draft && !bonus ? d.token : -1;
-      for (int mode = 0; mode < 2; ++mode) {
-        double s;
-        int64_t at;
-        race(c, trow, drow, p.noise + i * p.nld, v0, v1, sh, s, at);
-        if (tid < (int)ranks) {
-          st_cluster_f64(map_to_rank(smem_u32(&sh.win[wslot][rank]), (uint32_t)tid), s);
-          st_cluster_s64(map_to_rank(smem_u32(&sh.win_at[wslot][rank]), (uint32_t)tid), at);
-        }
-        __syncwarp();
-        if (ranks > 1)
-          cluster_sync();
-        else
-          __syncthreads();
-        s = sh.win[wslot][0];
-        at = sh.win_at[wslot][0];
-        for (uint32_t k = 1; k < ranks; ++k) better(s, at, sh.win[wslot][k], sh.win_at[wslot][k]);
-        wslot ^= 1;
-        token = s > 0.0 ? at : -1;
-        // nothing left in the residual (p = q up to rounding): the target's own race
-        if (s > 0.0 || (!c.has_draft && c.skip < 0)) break;
-        c.has_draft = false;
-        c.skip = -1;
-      }
-      if (token < 0) flags |= kFlagValue;  // no positive finite score
-    }
-    if (rank == 0) {
-      const int64_t o = i * (p.K + 1);
-      if (tid == 0) {
-        p.out_tokens[o + j] = token;
-        p.logp[o + j] = token >= 0 ? (float)log_prob(Elt<T>::load1(trow + token), d.mt, d.st, t)
-                                   : __int_as_float(0x7fc00000);
-        p.n_accepted[i] = (int32_t)j;
-        p.status[i] = flags & ~kFlagIndirect;
-      }
-      for (int64_t k = j + 1 + tid; k <= p.K; k += kThreads) {
-        p.out_tokens[o + k] = -1;
-        p.logp[o + k] = 0.f;
-      }
-    }
-    __syncthreads();  // sh.dec and the race's arrays are free
+    flags = __reduce_or_sync(0xffffffffu, flags);
+    if (lane == 0) sh.flags = flags;
   }
-  // no CTA leaves while another may still store into it
-  if (ranks > 1) cluster_sync();
+  // (also: every CTA of the cluster runs before the first distributed store)
+  if (ranks > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  const Decision d = sh.dec;
+  const int64_t j = sh.stop;
+  const bool bonus = j >= len;
+  flags = sh.flags;
+  const T* trow = target + i * p.tls + j * p.tld;
+  const T* drow = draft != nullptr && !bonus ? draft + i * p.dls + j * p.dld : nullptr;
+  const int64_t v0 = min(p.V, (int64_t)rank * p.chunk), v1 = min(p.V, v0 + p.chunk);
+  Racer c;
+  c.t = t;
+  c.mt = d.mt;
+  c.rt = ref_of(d.mt, t);
+  c.bigt = is_big(d.mt);
+  c.it = (float)(1.0 / d.st);
+  c.st = d.st;
+  c.md = d.md;
+  c.rd = ref_of(d.md, t);
+  c.bigd = is_big(d.md);
+  c.sd = d.sd;
+  c.has_draft = drow != nullptr;
+  c.id = c.has_draft ? (float)(1.0 / d.sd) : 0.f;
+  c.skip = draft == nullptr && !bonus ? d.token : -1;
+  int64_t token = d.emit == 2 ? d.arg : -1;
+  // The CTAs of the cluster pass the same barriers: what a further round
+  // depends on comes from what rank 0 sent.
+  for (int round = 0; round < 2; ++round) {
+    double s = 0.0;
+    int64_t at = INT64_MAX;
+    if (d.emit == 1) race(c, trow, drow, p.noise + i * p.nld, v0, v1, sh, s, at);
+    const int again = d.emit == 1 && (c.has_draft || c.skip >= 0);
+    if (tid < (int)ranks) {
+      const uint32_t to = (uint32_t)tid;
+      st_cluster_f64(map_to_rank(smem_u32(&sh.win[round][rank]), to), s);
+      st_cluster_s64(map_to_rank(smem_u32(&sh.win_at[round][rank]), to), at);
+      st_cluster_s32(map_to_rank(smem_u32(&sh.again[round][rank]), to), again);
+    }
+    __syncwarp();  // the cluster barrier instructions are warp-aligned
+    if (ranks > 1)
+      cluster_sync();
+    else
+      __syncthreads();
+    s = sh.win[round][0];
+    at = sh.win_at[round][0];
+    for (uint32_t k = 1; k < ranks; ++k) better(s, at, sh.win[round][k], sh.win_at[round][k]);
+    if (d.emit == 1 && s > 0.0) token = at;
+    // nothing left in the residual (p = q up to rounding): the target's own race
+    if (s > 0.0 || !sh.again[round][0]) break;
+    c.has_draft = false;
+    c.skip = -1;
+  }
+  if (rank != 0) return;
+  if (token < 0) flags |= kFlagValue;
+  const int64_t o = i * (p.K + 1);
+  if (tid == 0) {
+    p.out_tokens[o + j] = token;
+    p.logp[o + j] = token >= 0 ? (float)log_prob(Elt<T>::load1(trow + token), d.mt, d.st, t)
+                               : __int_as_float(0x7fc00000);
+    p.n_accepted[i] = (int32_t)j;
+    p.status[i] = flags & ~kFlagIndirect;
+  }
+  for (int64_t k = j + 1 + tid; k <= p.K; k += kRaceThreads) {
+    p.out_tokens[o + k] = -1;
+    p.logp[o + k] = 0.f;
+  }
 }
 
-std::mutex g_occ_mutex;
-std::map<std::tuple<int, int, int>, int> g_occ;  // (device, dtype, cluster) -> clusters at once
+struct VerifyLayout {
+  size_t status, part, arg, rejected, ticket, total;
+};
+VerifyLayout verify_layout(int64_t N, int64_t K) {
+  VerifyLayout l;
+  const size_t n = (size_t)(N < 1 ? 1 : N), rows = n * (size_t)(K + 1);
+  size_t at = 256;
+  auto take = [&](size_t bytes) {
+    const size_t p = at;
+    at = align_up(at + bytes, 256);
+    return p;
+  };
+  l.status = take(4 * n);
+  l.part = take(2 * rows * kMaxSplit * sizeof(float2));
+  l.arg = take(rows * kMaxSplit * sizeof(int64_t));
+  l.rejected = take(4 * n);
+  l.ticket = take(4 * rows);
+  l.total = at;
+  return l;
+}
 
 template <typename T>
 cudaError_t launch_t(const VerifyArgs& a, const DeviceInfo& d, cudaStream_t st) {
   constexpr int EPV = Elt<T>::kPerVec;
-  const int K = lse_split(a.V * (int64_t)sizeof(T), a.N, d.sms, "GRPO_VERIFY_CLUSTER");
-  VerifyParams p;
+  const VerifyLayout l = verify_layout(a.N, a.K);
+  char* ws = static_cast<char*>(a.ws);
+  const int64_t row_bytes = a.V * (int64_t)sizeof(T);
+  const int kinds = a.draft != nullptr ? 2 : 1;
+  // parts of a row: enough that the first position's rows occupy every SM
+  // four times over, of at least 16 KiB
+  int split = 1;
+  while (split < kMaxSplit && a.N * kinds * split < 4 * (int64_t)d.sms &&
+         row_bytes / (2 * split) >= kMinPartBytes)
+    split *= 2;
+  const int64_t rows = a.N * (a.K + 1) + (kinds == 2 ? a.N * a.K : 0);
+  if (rows > INT32_MAX / split) return cudaErrorInvalidValue;  // (refused by api.cu)
+  VerifyParams p = {};
   p.N = a.N;
   p.K = a.K;
   p.V = a.V;
@@ -652,49 +742,41 @@ cudaError_t launch_t(const VerifyArgs& a, const DeviceInfo& d, cudaStream_t st) 
   p.out_tokens = a.out_tokens;
   p.n_accepted = a.n_accepted;
   p.logp = a.logp;
-  p.hdr = static_cast<WsHeader*>(a.ws);
-  p.status = reinterpret_cast<uint32_t*>(static_cast<char*>(a.ws) + 256);
-  p.chunk = ((a.V + K - 1) / K + EPV - 1) / EPV * EPV;
-  auto kern = verify_kernel<T>;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = K;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3(K);
-  int clusters = 0;
-  const auto key = std::make_tuple(d.device, (int)sizeof(T), K);
-  {
-    std::lock_guard<std::mutex> g(g_occ_mutex);
-    const auto it = g_occ.find(key);
-    if (it != g_occ.end()) clusters = it->second;
-  }
-  if (clusters == 0) {
-    const cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
+  p.hdr = reinterpret_cast<WsHeader*>(ws);
+  p.status = reinterpret_cast<uint32_t*>(ws + l.status);
+  p.part = reinterpret_cast<float2*>(ws + l.part);
+  p.arg = reinterpret_cast<int64_t*>(ws + l.arg);
+  p.rejected = reinterpret_cast<int32_t*>(ws + l.rejected);
+  p.ticket = reinterpret_cast<uint32_t*>(ws + l.ticket);
+  p.split = split;
+  p.part_elems = ((a.V + split - 1) / split + EPV - 1) / EPV * EPV;
+  // all rows at once when the GPU takes them at once
+  p.lazy = a.K > 0 && rows * split > 4 * (int64_t)d.sms;
+  cudaError_t e;
+  if (p.lazy) {
+    const int64_t words = a.N * (a.K + 1);
+    const int64_t grid = (words + kThreads - 1) / kThreads;
+    e = launch_pdl(verify_init_kernel, dim3((unsigned)(grid < d.sms ? grid : d.sms)),
+                   dim3(kThreads), 0, st, 1, p.rejected, a.N, p.ticket, a.N * a.K);
     if (e != cudaSuccess) return e;
-    if (clusters < 1) clusters = 1;
-    std::lock_guard<std::mutex> g(g_occ_mutex);
-    g_occ[key] = clusters;
   }
-  const int64_t nq = clusters < a.N ? clusters : a.N;
-  cfg.gridDim = dim3((unsigned)(nq * K));
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, p, static_cast<const T*>(a.target),
-                            static_cast<const T*>(a.draft));
+  const T* target = static_cast<const T*>(a.target);
+  const T* draft = static_cast<const T*>(a.draft);
+  e = launch_pdl(verify_rows_kernel<T>, dim3((unsigned)(rows * split)), dim3(kThreads), 0, st, 1,
+                 p, target, draft);
+  if (e != cudaSuccess) return e;
+  // the emitting cluster: twice every SM, at least 16 KiB of logits per CTA
+  int C = 1;
+  while (C < kMaxCluster && a.N * C < 2 * (int64_t)d.sms && row_bytes / (2 * C) >= kMinPartBytes)
+    C *= 2;
+  p.chunk = ((a.V + C - 1) / C + EPV - 1) / EPV * EPV;
+  return launch_pdl(verify_emit_kernel<T>, dim3((unsigned)(a.N * C)), dim3(kRaceThreads), 0, st,
+                    (unsigned)C, p, target, draft);
 }
 
 }  // namespace
 
-size_t verify_workspace_bytes(int64_t N) {
-  return 256 + align_up(sizeof(uint32_t) * (size_t)(N < 1 ? 1 : N), 256);
-}
+size_t verify_workspace_bytes(int64_t N, int64_t K) { return verify_layout(N, K).total; }
 
 cudaError_t launch_verify(const VerifyArgs& a, const DeviceInfo& d, cudaStream_t st) {
   if (a.N == 0) return cudaMemsetAsync(a.ws, 0, sizeof(WsHeader), st);
