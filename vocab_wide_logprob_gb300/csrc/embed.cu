@@ -86,11 +86,11 @@ struct Cols8<T, false> {
 // forward
 // ---------------------------------------------------------------------------
 
-// One CTA copies `rows` rows; its threads walk the rows' units of 8 columns, U
-// of them in flight each: first the units' ids, then the rows, then the
-// stores.  A strided unit u of a row is columns u, u + nu, ... u + 7 nu.
-template <typename TW, typename TO, bool kVec, int U>
-__global__ void __launch_bounds__(kThreads) embed_fwd_kernel(
+// Any alignment: one CTA copies `rows` rows; its threads walk the rows' units
+// of 8 columns (unit c of a row: columns c, c + nu, ... c + 7 nu), U of them
+// in flight each: first the units' ids, then the rows, then the stores.
+template <typename TW, typename TO, int U>
+__global__ void __launch_bounds__(kThreads) embed_fwd_any_kernel(
     const int64_t* __restrict__ ids, int64_t n, const TW* __restrict__ w, int64_t V, int64_t d,
     int64_t ldw, float scale, TO* __restrict__ out, int64_t ldo, int rows, int nu) {
   pdl_wait();
@@ -114,41 +114,100 @@ __global__ void __launch_bounds__(kThreads) embed_fwd_kernel(
         ++r;
       }
     }
-    if constexpr (kVec) {
-      Vec8<TW> x[U];
+    float x[U][8];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (rr[u] >= nrows) continue;
-        if (id[u] >= 0 && id[u] < V)
-          x[u].load_stream(w + id[u] * ldw + 8 * cc[u]);
-        else
-          x[u].fill(sizeof(TW) == 4 ? 0x7fc00000u : 0x7fc07fc0u);  // NaN
-      }
+    for (int u = 0; u < U; ++u) {
+      if (rr[u] >= nrows) continue;
+      if (id[u] >= 0 && id[u] < V) {
+        Cols8<TW, false>::load(w + id[u] * ldw + cc[u], nu, (int)d - cc[u], x[u]);
+      } else {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (rr[u] < nrows)
-          x[u].template store<false>(out + (row0 + rr[u]) * ldo + 8 * cc[u], scale);
-    } else {
-      float x[U][8];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (rr[u] >= nrows) continue;
-        if (id[u] >= 0 && id[u] < V) {
-          Cols8<TW, false>::load(w + id[u] * ldw + cc[u], nu, (int)d - cc[u], x[u]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[u][e] = __int_as_float(0x7fc00000);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (rr[u] >= nrows) continue;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[u][e] *= scale;
-        Cols8<TO, false>::store(out + (row0 + rr[u]) * ldo + cc[u], nu, (int)d - cc[u], x[u]);
+        for (int e = 0; e < 8; ++e) x[u][e] = __int_as_float(0x7fc00000);
       }
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (rr[u] >= nrows) continue;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[u][e] *= scale;
+      Cols8<TO, false>::store(out + (row0 + rr[u]) * ldo + cc[u], nu, (int)d - cc[u], x[u]);
+    }
   }
+}
+
+constexpr int kFwdIds = 512;  // rows of a CTA whose ids wait in shared memory
+// units (8 columns) a thread has on their way: 128 bytes
+template <typename TW>
+__host__ __device__ constexpr int fwd_depth() {
+  return sizeof(TW) == 4 ? 4 : 8;
+}
+
+// 16-byte aligned rows.  A CTA takes a run of rows; their ids are loaded
+// first, and then every thread streams its units of 8 columns through a ring
+// of its own in shared memory, kDepth asynchronous copies ahead of its stores.
+// The ring costs no registers and needs no barrier (a thread reads back what
+// it copied itself), so loads and stores of a CTA overlap all the way.
+template <typename TW, typename TO, bool kStream>
+__global__ void __launch_bounds__(kThreads) embed_fwd_kernel(
+    const int64_t* __restrict__ ids, int64_t n, const TW* __restrict__ w, int64_t V, int64_t ldw,
+    float scale, TO* __restrict__ out, int64_t ldo, int rows, int nu) {
+  constexpr int kDepth = fwd_depth<TW>();
+  constexpr int kUnit = 8 * (int)sizeof(TW);
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ int32_t s_id[kFwdIds];
+  const int tid = threadIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  const int64_t row0 = (int64_t)blockIdx.x * rows;
+  const int nrows = (int)min((int64_t)rows, n - row0);
+  for (int k = tid; k < nrows; k += kThreads) {
+    const int64_t id = __ldg(ids + row0 + k);
+    s_id[k] = id >= 0 && id < V ? (int32_t)id : -1;
+  }
+  __syncthreads();
+  const int dr = kThreads / nu, dc = kThreads - dr * nu;
+  struct At {
+    int r, c;
+  };
+  auto step = [&](At& a) {
+    a.c += dc;
+    a.r += dr;
+    if (a.c >= nu) {
+      a.c -= nu;
+      ++a.r;
+    }
+  };
+  At get = {tid / nu, tid - tid / nu * nu}, put = get;
+  const uint32_t mine = smem_u32(ring) + tid * kUnit;  // slot k: + k * kThreads * kUnit
+  auto issue = [&](int slot) {
+    if (get.r < nrows) {
+      const int32_t id = s_id[get.r];
+      if (id >= 0) {
+        const char* src = reinterpret_cast<const char*>(w + id * ldw + 8 * get.c);
+        const uint32_t dst = mine + slot * (kThreads * kUnit);
+#pragma unroll
+        for (int b = 0; b < kUnit; b += 16) cp_async16(dst + b, src + b);
+      }
+    }
+    cp_async_commit();
+    step(get);
+  };
+#pragma unroll
+  for (int k = 0; k < kDepth; ++k) issue(k);
+  int slot = 0;
+  while (put.r < nrows) {
+    cp_async_wait<kDepth - 1>();
+    Vec8<TW> x;
+#pragma unroll
+    for (int k = 0; k < Vec8<TW>::kWords; ++k)
+      x.v[k] = ld_shared_v4(mine + slot * (kThreads * kUnit) + 16 * k);
+    if (s_id[put.r] < 0) x.fill(sizeof(TW) == 4 ? 0x7fc00000u : 0x7fc07fc0u);  // NaN
+    x.template store<kStream>(out + (row0 + put.r) * ldo + 8 * put.c, scale);
+    step(put);
+    issue(slot);
+    slot = slot + 1 == kDepth ? 0 : slot + 1;
+  }
+  cp_async_wait<0>();
 }
 
 bool rows_aligned16(const void* p, int64_t ld, size_t esize) {
@@ -159,18 +218,30 @@ template <typename TW, typename TO>
 cudaError_t launch_fwd_t(const EmbedFwdArgs& a, const DeviceInfo& dev, cudaStream_t st) {
   const bool vec = a.d % 8 == 0 && rows_aligned16(a.weight, a.ldw, sizeof(TW)) &&
                    rows_aligned16(a.out, a.ldo, sizeof(TO));
-  constexpr int U = sizeof(TW) == 4 ? 4 : 8;
   const int nu = (int)((a.d + 7) / 8);
-  // a CTA's units fill one unrolled step of its threads, unless that leaves
-  // SMs without a CTA
-  int64_t rows = kThreads * (vec ? U : 4) / nu;
-  const int64_t spread = a.n / (2 * (int64_t)dev.sms);
-  if (rows > spread) rows = spread;
-  if (rows < 1) rows = 1;
-  auto kern = vec ? embed_fwd_kernel<TW, TO, true, U> : embed_fwd_kernel<TW, TO, false, 4>;
-  return launch_pdl(kern, dim3((unsigned)((a.n + rows - 1) / rows)), dim3(kThreads), 0, st, 1,
-                    a.ids, a.n, static_cast<const TW*>(a.weight), a.V, a.d, a.ldw, a.scale,
-                    static_cast<TO*>(a.out), a.ldo, (int)rows, nu);
+  const TW* w = static_cast<const TW*>(a.weight);
+  TO* out = static_cast<TO*>(a.out);
+  if (!vec) {
+    constexpr int U = 4;
+    // a CTA's units fill one unrolled step of its threads, unless that leaves
+    // SMs without a CTA
+    int64_t rows = kThreads * U / nu;
+    const int64_t spread = a.n / (2 * (int64_t)dev.sms);
+    if (rows > spread) rows = spread;
+    if (rows < 1) rows = 1;
+    return launch_pdl(embed_fwd_any_kernel<TW, TO, U>, dim3((unsigned)((a.n + rows - 1) / rows)),
+                      dim3(kThreads), 0, st, 1, a.ids, a.n, w, a.V, a.d, a.ldw, a.scale, out, a.ldo,
+                      (int)rows, nu);
+  }
+  // runs of rows: six CTAs per SM at once
+  int64_t rows = (a.n + 6 * (int64_t)dev.sms - 1) / (6 * (int64_t)dev.sms);
+  if (rows > kFwdIds) rows = kFwdIds;
+  // an output larger than half of L2 is not kept there for its reader
+  const bool stream = (size_t)a.n * (size_t)a.d * sizeof(TO) > ((size_t)64 << 20);
+  auto kern = stream ? embed_fwd_kernel<TW, TO, true> : embed_fwd_kernel<TW, TO, false>;
+  const size_t smem = (size_t)fwd_depth<TW>() * kThreads * 8 * sizeof(TW);
+  return launch_pdl(kern, dim3((unsigned)((a.n + rows - 1) / rows)), dim3(kThreads), smem, st, 1,
+                    a.ids, a.n, w, a.V, a.ldw, a.scale, out, a.ldo, (int)rows, nu);
 }
 
 // ---------------------------------------------------------------------------
@@ -186,7 +257,8 @@ constexpr int kMaxTiles = 304;                  // CTAs of a sort pass (two per 
 constexpr int kMaxPasses = 4;
 static_assert(kMaxBins == kSortThreads, "one thread per bin");
 
-constexpr int kSegEntries = 32;  // sorted entries summed by one group of threads
+constexpr int kSegUnroll = 8;
+constexpr int kMaxSegEntries = 32;
 
 struct SortPlan {
   int bits;       // key bits: ids 0 .. V-1 and the key V of ignored tokens
@@ -194,22 +266,9 @@ struct SortPlan {
   int dbits;      // bits per digit
   int64_t tile;   // elements per CTA, a multiple of kBatch
   int tiles;
-  int64_t seg_tiles;
+  int seg;            // sorted entries summed by one group of threads
+  int64_t seg_tiles;  // such groups
 };
-
-SortPlan sort_plan(int64_t n, int64_t V) {
-  SortPlan s;
-  s.bits = 1;
-  while (s.bits < 31 && ((int64_t)1 << s.bits) <= V) ++s.bits;
-  s.passes = (s.bits + 8) / 9;
-  s.dbits = (s.bits + s.passes - 1) / s.passes;
-  int64_t per = (n + kMaxTiles - 1) / kMaxTiles;
-  s.tile = (per + kBatch - 1) / kBatch * kBatch;
-  if (s.tile < kBatch) s.tile = kBatch;
-  s.tiles = (int)((n + s.tile - 1) / s.tile);
-  s.seg_tiles = (n + kSegEntries - 1) / kSegEntries;
-  return s;
-}
 
 // Threads per row (8 columns each) of the summing kernel, and the columns of
 // its rows of partial sums: whole CTAs of threads.
@@ -222,6 +281,24 @@ int64_t padded_cols(int64_t d) {
   return (d + cols - 1) / cols * cols;
 }
 
+SortPlan sort_plan(int64_t n, int64_t V, int64_t d) {
+  SortPlan s;
+  s.bits = 1;
+  while (s.bits < 31 && ((int64_t)1 << s.bits) <= V) ++s.bits;
+  s.passes = (s.bits + 8) / 9;
+  s.dbits = (s.bits + s.passes - 1) / s.passes;
+  int64_t per = (n + kMaxTiles - 1) / kMaxTiles;
+  s.tile = (per + kBatch - 1) / kBatch * kBatch;
+  if (s.tile < kBatch) s.tile = kBatch;
+  s.tiles = (int)((n + s.tile - 1) / s.tile);
+  // few tokens: shorter groups, so that there are enough of them (about 512
+  // threads on each of 152 SMs)
+  s.seg = kMaxSegEntries;
+  while (s.seg > kSegUnroll && (n + s.seg - 1) / s.seg * (padded_cols(d) / 8) < 152 * 512) s.seg /= 2;
+  s.seg_tiles = (n + s.seg - 1) / s.seg;
+  return s;
+}
+
 struct BwdLayout {
   size_t key[2], pos[2], hist[kMaxPasses], bad, list, part, total;
   int64_t dpad;
@@ -229,7 +306,7 @@ struct BwdLayout {
 
 // header | keys and positions, twice | histograms | flags | partial sums
 BwdLayout bwd_layout(int64_t n, int64_t V, int64_t d) {
-  const SortPlan s = sort_plan(n, V);
+  const SortPlan s = sort_plan(n, V, d);
   BwdLayout l;
   size_t at = 256;
   auto take = [&](size_t bytes) {
@@ -512,6 +589,7 @@ struct SegParams {
   float scale;
   float* part;    // [seg tiles][2][dpad]: an id's rows in a tile that it began before (0), goes on after (1)
   int32_t* list;  // count, then the tiles in which a split id begins
+  int seg;          // sorted entries per tile
   int tpr, groups;  // threads per row, rows side by side in a CTA
   int cols;         // columns of one CTA in y (8 per thread of a row)
 };
@@ -552,9 +630,7 @@ struct RowPart<T, false> {
   }
 };
 
-constexpr int kSegUnroll = 8;
-
-// A group of `tpr` threads takes kSegEntries sorted entries (a tile), 8
+// A group of `tpr` threads takes Q sorted entries (a tile), 8
 // columns per thread, and writes a row whenever the id changes.  An id that
 // goes on past its tile is finished by the group it began in, unless it fills
 // a whole further tile: then it is split at the tiles, every tile leaves its
@@ -562,11 +638,12 @@ constexpr int kSegUnroll = 8;
 // from the same keys: the id at a tile's first entry a is split iff it began
 // before the previous tile (key[a - Q - 1]) or reaches past this one
 // (key[a + Q]).
-template <typename TD, typename TW, bool kVec, bool kAcc>
+// U rows are in flight per thread: 8 of bfloat16, 4 of float32.
+template <typename TD, typename TW, bool kVec, bool kAcc, int U>
 __global__ void __launch_bounds__(kThreads, 2) embed_sum_kernel(const SegParams p,
                                                                 const TD* __restrict__ dout,
                                                                 TW* dw) {
-  constexpr int Q = kSegEntries;
+  const int Q = p.seg;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
@@ -587,9 +664,9 @@ __global__ void __launch_bounds__(kThreads, 2) embed_sum_kernel(const SegParams 
   const int32_t last = p.key[b - 1];
   const int32_t next = b < p.n ? p.key[b] : -1;
   const int32_t next2 = b + Q < p.n ? p.key[b + Q] : -1;
-  int32_t k[kSegUnroll], at[kSegUnroll];
+  int32_t k[U], at[U];
 #pragma unroll
-  for (int u = 0; u < kSegUnroll; ++u) {
+  for (int u = 0; u < U; ++u) {
     k[u] = a + u < p.n ? p.key[a + u] : INT32_MAX;
     at[u] = a + u < p.n ? p.pos[a + u] : 0;
   }
@@ -616,24 +693,24 @@ __global__ void __launch_bounds__(kThreads, 2) embed_sum_kernel(const SegParams 
       write_row<TW, kVec>(dw + cur * p.ldw + c0, step, left, kAcc, p.scale, acc);
   };
   const int64_t stop = extend ? min(b + Q, p.n) : b;
-  for (int64_t e = a; e < stop; e += kSegUnroll) {
-    RowPart<TD, kVec> x[kSegUnroll];
-    bool use[kSegUnroll];
+  for (int64_t e = a; e < stop; e += U) {
+    RowPart<TD, kVec> x[U];
+    bool use[U];
 #pragma unroll
-    for (int u = 0; u < kSegUnroll; ++u) {
+    for (int u = 0; u < U; ++u) {
       use[u] = k[u] < p.V && (e + u < b || (extend && k[u] == last)) && !(skip && k[u] == first);
       if (use[u]) x[u].load(dout + (int64_t)at[u] * p.ldd + c0, step, left);
     }
-    int32_t kn[kSegUnroll];
-    const bool more = e + kSegUnroll < stop;
+    int32_t kn[U];
+    const bool more = e + U < stop;
 #pragma unroll
-    for (int u = 0; u < kSegUnroll; ++u) {
-      const int64_t i = e + kSegUnroll + u;
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = e + U + u;
       kn[u] = more && i < p.n ? p.key[i] : INT32_MAX;
       at[u] = more && i < p.n ? p.pos[i] : 0;
     }
 #pragma unroll
-    for (int u = 0; u < kSegUnroll; ++u) {
+    for (int u = 0; u < U; ++u) {
       if (use[u]) {
         float v[8];
         x[u].get(v);
@@ -678,11 +755,11 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const SegParams p,
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
     const int64_t t = p.list[1 + it / ny];
     const int64_t c = (it % ny) * kJoinCols + 4 * lane;
-    const int32_t v = p.key[(t + 1) * kSegEntries];
+    const int32_t v = p.key[(t + 1) * p.seg];
     // the last tile that begins with the id
     int64_t last = t + 1;
     for (;;) {
-      const int64_t e = (last + 1 + lane) * kSegEntries;
+      const int64_t e = (last + 1 + lane) * p.seg;
       const uint32_t same = __ballot_sync(0xffffffffu, e < p.n && p.key[e < p.n ? e : 0] == v);
       const int run = same == 0xffffffffu ? 32 : __ffs(~same) - 1;
       last += run;
@@ -739,9 +816,10 @@ template <typename TD, typename TW, bool kVec, bool kAcc>
 cudaError_t launch_sums(const EmbedBwdArgs& a, SegParams p, const DeviceInfo& dev,
                         cudaStream_t st) {
   const unsigned ny = (unsigned)((p.d + p.cols - 1) / p.cols);
-  const int64_t seg_tiles = (p.n + kSegEntries - 1) / kSegEntries;
+  const int64_t seg_tiles = (p.n + p.seg - 1) / p.seg;
+  constexpr int U = sizeof(TD) == 4 ? 4 : 8;
   const int64_t blocks = (seg_tiles + p.groups - 1) / p.groups;
-  cudaError_t e = launch_pdl(embed_sum_kernel<TD, TW, kVec, kAcc>,
+  cudaError_t e = launch_pdl(embed_sum_kernel<TD, TW, kVec, kAcc, U>,
                              dim3((unsigned)blocks, ny), dim3(kThreads), 0,
                              st, 1, p, static_cast<const TD*>(a.dout), static_cast<TW*>(a.dweight));
   if (e != cudaSuccess || seg_tiles < 2) return e;
@@ -774,7 +852,7 @@ cudaError_t launch_embed_fwd(const EmbedFwdArgs& a, const DeviceInfo& dev, cudaS
 size_t embed_workspace_bytes(int64_t n, int64_t V, int64_t d) { return bwd_layout(n, V, d).total; }
 
 cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, const DeviceInfo& dev, cudaStream_t st) {
-  const SortPlan s = sort_plan(a.n, a.V);
+  const SortPlan s = sort_plan(a.n, a.V, a.d);
   const BwdLayout l = bwd_layout(a.n, a.V, a.d);
   char* ws = static_cast<char*>(a.ws);
   auto i32 = [&](size_t off) { return reinterpret_cast<int32_t*>(ws + off); };
@@ -859,7 +937,11 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, const DeviceInfo& dev, cudaS
   p.part = reinterpret_cast<float*>(ws + l.part);
   p.list = i32(l.list);
   p.tpr = row_threads(a.d);
+  p.seg = s.seg;
+  // rows side by side in a CTA, unless that leaves SMs without one
+  const int64_t per = s.seg_tiles / (2 * (int64_t)dev.sms);
   p.groups = kThreads / p.tpr;
+  if (p.groups > per) p.groups = per < 1 ? 1 : (int)per;
   p.cols = 8 * p.tpr;
   const size_t de = a.ddtype == 0 ? 4 : 2;
   const bool vec = a.d % 8 == 0 && rows_aligned16(a.dout, a.ldd, de) &&

@@ -7,6 +7,19 @@
 
 namespace grpo {
 
+// Asynchronous 16-byte copies global -> shared memory (past L1), by thread.
+__device__ __forceinline__ void cp_async16(uint32_t smem_dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// At most N of this thread's groups still on their way.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // 8 consecutive elements (16-byte aligned) as they are stored, in registers.
 template <typename TI>
 struct Vec8 {

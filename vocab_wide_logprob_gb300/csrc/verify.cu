@@ -17,7 +17,7 @@
 // position's rows decides it and publishes it; nothing waits for anything, and
 // a row that was read in vain changes no result).  verify_emit_kernel, one
 // thread block cluster per sequence, takes every position's decision at once,
-// one position per lane, and runs the race over the row that the sequence
+// one position per warp, and runs the race over the row that the sequence
 // stops at.
 //
 // Whole-number outputs must not depend on float32 rounding where a decision
@@ -25,6 +25,7 @@
 // keeps in float32 only bounds: the candidates whose upper bound reaches the
 // best lower bound (a handful of a row) are compared in float64.
 #include <math.h>
+#include <stddef.h>
 
 #include "ops.cuh"
 
@@ -34,8 +35,8 @@ namespace {
 constexpr int kRaceThreads = 512;
 constexpr int kRaceWarps = kRaceThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxSplit = 16;          // CTAs per row of the rows kernel
-constexpr int64_t kMinPartBytes = 16384;  // of a row, when it is split
+constexpr int kMaxSplit = 32;          // CTAs per row of the rows kernel (one lane each when merged)
+constexpr int64_t kMinPartBytes = 8192;  // of a row, when it is split
 constexpr int kCandidates = 1024;      // race candidates a CTA can hold
 constexpr float kMinTemperature = 1e-6f;  // below it a temperature counts as 0
 constexpr float kBig = 1e30f;          // maxima beyond it take the subtracting form below
@@ -46,17 +47,19 @@ constexpr float kRaceMargin = 1e-5f;
 
 // exp(x / T) = 2^(x c), c = log2(e) / T kept as c_hi + c_lo with c_lo > 0 (so
 // that -inf stays -inf in both steps).
+// The split is made in float32 (this GPU has few float64 units): the quotient
+// of log2(e)'s leading part rounded down, and what is left of it.
 struct Temper {
   float hi, lo;
-  double c;
 };
 __device__ __forceinline__ Temper temper(float T) {
+  constexpr float kHead = 1.44269502162933349609375f, kTail = 1.92596299112661746887e-8f;
   Temper t;
-  t.c = 1.4426950408889634074 / (double)T;
-  t.hi = __double2float_rd(t.c);
-  t.lo = fmaxf((float)(t.c - (double)t.hi), 1e-37f);
+  t.hi = __fdiv_rd(kHead, T);
+  t.lo = fmaxf((fmaf(-t.hi, T, kHead) + kTail) / T, 1e-37f);
   return t;
 }
+__device__ __forceinline__ double temper64(const Temper& t) { return (double)t.hi + (double)t.lo; }
 
 // Reference exponent of a row (or part of one) with maximum m: weights are
 // 2^(x c - r).  With r the rounded product, x c - r is rounded once, at its
@@ -84,12 +87,15 @@ __device__ __forceinline__ void merge(float& m, float& s, float m2, float s2, co
   s = s * rescale(m, M, t) + s2 * rescale(m2, M, t);
   m = M;
 }
-// natural log of p(x) in float64
-__device__ __forceinline__ double log_prob(float x, float m, double s, const Temper& t) {
-  const double e = is_big(m) ? ((double)x - (double)m) * t.c
-                             : (double)x * t.c - (double)ref_of(m, t);
-  return e * kLn2 - log(s);
+// natural log of a weight in float64 (p is weight / sum)
+__device__ __forceinline__ double log_weight(float x, float m, const Temper& t) {
+  const double c = temper64(t);
+  const double e = is_big(m) ? ((double)x - (double)m) * c : (double)x * c - (double)ref_of(m, t);
+  return e * kLn2;
 }
+// Acceptance and log-probs within this of a border are looked at in float64
+// (logf and the differences of float32 logs are good to about 2e-6 here).
+constexpr float kClose = 1e-4f;
 
 struct VerifyParams {
   int64_t N, K, V, tld, tls, dld, dls, nld;
@@ -108,6 +114,7 @@ struct VerifyParams {
   // maximum first.
   float2* part;
   int64_t* arg;
+  float* picked;      // the drafted tokens' logits, in the order of the rows
   int32_t* rejected;  // [N]: a position at which the sequence is known to stop
   uint32_t* ticket;   // [K * N]: CTAs done with a position's rows
   int split;          // CTAs per row
@@ -128,10 +135,9 @@ __device__ __forceinline__ float temperature_of(const VerifyParams& p, int64_t i
 
 struct Decision {
   int accept, emit;  // go on; or emit by race (1), argmax (2), nothing (3)
-  float mt, md;
-  double st, sd;
+  float mt, md, st, sd;  // maxima and sums of the rows
   int64_t arg, token;
-  double lp;  // log-prob of the drafted token
+  float lp;  // log-prob of the drafted token
   uint32_t flags;
 };
 
@@ -239,54 +245,64 @@ __device__ __forceinline__ RowStat row_stats(const T* row, int64_t v0, int64_t v
   return r;
 }
 
-// Position j of sequence i: merge the parts of its rows in order, and decide.
-template <typename T>
-__device__ __forceinline__ void decide(const VerifyParams& p, const T* target, const T* draft,
-                                       int64_t i, int64_t j, int32_t len, float Ti, Decision& d) {
+// Position j of sequence i, by one warp: the lanes take the parts of the
+// target's and the draft's row, a tree of shuffles merges them, and every lane
+// decides.  The results are every lane's.
+__device__ __forceinline__ void decide(const VerifyParams& p, bool has_draft, int64_t i, int64_t j,
+                                       int32_t len, float Ti, Decision& d) {
+  const int lane = threadIdx.x & 31;
   const bool greedy = Ti < kMinTemperature, bonus = j >= len;
-  const bool use_draft = draft != nullptr && !bonus && !greedy;
+  const bool use_draft = has_draft && !bonus && !greedy;
   const Temper t = temper(greedy ? 1.f : Ti);
   d.flags = 0;
   d.accept = 0;
-  d.lp = 0.0;
+  d.lp = 0.f;
   d.token = -1;
+  const int64_t trow = j * p.N + i, drow = (p.K + 1 + j) * p.N + i;
+  d.mt = d.md = -INFINITY;
+  d.st = d.sd = 0.f;
   d.arg = INT64_MAX;
-  int64_t x = -1;
+  if (lane < p.split) {
+    const float2 v = __ldcg(p.part + trow * p.split + lane);
+    d.mt = v.x;
+    d.st = v.y;
+    if (use_draft) {
+      const float2 w = __ldcg(p.part + drow * p.split + lane);
+      d.md = w.x;
+      d.sd = w.y;
+    }
+    if (greedy) d.arg = __ldcg(p.arg + trow * p.split + lane);
+  }
   float xt = 0.f, xd = 0.f, u = 0.f;
   if (!bonus) {
-    x = p.tokens[i * p.K + j];
+    const int64_t x = p.tokens[i * p.K + j];
     u = p.u[i * p.K + j];
-    if (x >= 0 && x < p.V) {
+    xt = __ldcg(p.picked + trow);
+    if (use_draft) xd = __ldcg(p.picked + drow);
+    if (x >= 0 && x < p.V)
       d.token = x;
-      xt = Elt<T>::load1(target + i * p.tls + j * p.tld + x);
-      if (use_draft) xd = Elt<T>::load1(draft + i * p.dls + j * p.dld + x);
-    } else {
+    else
       d.flags |= kFlagTokenRange;
-    }
   }
-  const volatile float2* tp = p.part + (j * p.N + i) * p.split;
-  const volatile int64_t* ta = p.arg + (j * p.N + i) * p.split;
-  const volatile float2* dp = p.part + ((p.K + 1 + j) * p.N + i) * p.split;
-  float mt = -INFINITY, st = 0.f, md = -INFINITY, sd = 0.f;
-  for (int k = 0; k < p.split; ++k) {
-    const float m2 = tp[k].x, s2 = tp[k].y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, d.mt, o);
+    const float s2 = __shfl_xor_sync(0xffffffffu, d.st, o);
     if (greedy) {
-      const int64_t a2 = ta[k];
-      d.arg = m2 > mt ? a2 : (m2 == mt ? min(d.arg, a2) : d.arg);
+      const int64_t a2 = __shfl_xor_sync(0xffffffffu, d.arg, o);
+      d.arg = m2 > d.mt ? a2 : (m2 == d.mt ? min(d.arg, a2) : d.arg);
     }
-    merge(mt, st, m2, s2, t);
+    merge(d.mt, d.st, m2, s2, t);
     if (use_draft) {
-      const float m3 = dp[k].x, s3 = dp[k].y;
-      merge(md, sd, m3, s3, t);
+      const float m3 = __shfl_xor_sync(0xffffffffu, d.md, o);
+      const float s3 = __shfl_xor_sync(0xffffffffu, d.sd, o);
+      merge(d.md, d.sd, m3, s3, t);
     }
   }
-  d.mt = mt;
-  d.st = (double)st;
-  d.md = md;
-  d.sd = (double)sd;
-  bool defined = Ti >= 0.f && Ti <= 3.4e38f && mt > -INFINITY && mt < INFINITY && st > 0.f &&
-                 st < INFINITY;
-  if (use_draft) defined = defined && md > -INFINITY && md < INFINITY && sd > 0.f && sd < INFINITY;
+  bool defined = Ti >= 0.f && Ti <= 3.4e38f && d.mt > -INFINITY && d.mt < INFINITY &&
+                 d.st > 0.f && d.st < INFINITY;
+  if (use_draft)
+    defined = defined && d.md > -INFINITY && d.md < INFINITY && d.sd > 0.f && d.sd < INFINITY;
   if (!defined) {
     d.emit = 3;
     d.flags |= kFlagValue;
@@ -294,12 +310,23 @@ __device__ __forceinline__ void decide(const VerifyParams& p, const T* target, c
   }
   d.emit = greedy ? 2 : 1;
   if (d.token < 0) return;  // after the last draft, or an id outside [0, V)
-  d.lp = log_prob(xt, mt, d.st, t);
+  // (differences of the exponents in float64, the sums' logs in float32)
+  const double wt = log_weight(xt, d.mt, t);
+  d.lp = (float)(wt - (double)logf(d.st));
   if (greedy) {
     d.accept = d.token == d.arg;
-  } else {
-    const double lq = use_draft ? log_prob(xd, md, d.sd, t) : 0.0;
-    d.accept = xt > -INFINITY && (double)u * exp(lq - d.lp) < 1.0;
+    return;
+  }
+  if (!(xt > -INFINITY)) return;
+  const double wd = use_draft ? log_weight(xd, d.md, t) : 0.0;
+  // log(q / p) and its border -log(u)
+  const float ratio = (float)(wd - wt) + (logf(d.st) - (use_draft ? logf(d.sd) : 0.f));
+  const float border = -logf(u);
+  if (fabsf(ratio - border) > kClose * fmaxf(1.f, fabsf(border))) {
+    d.accept = ratio < border;
+  } else {  // also NaN, u = 0 against q = 0 and u < 0
+    const double lq = use_draft ? wd - log((double)d.sd) : 0.0;
+    d.accept = (double)u * exp(lq - (wt - log((double)d.st))) < 1.0;
   }
 }
 
@@ -330,7 +357,11 @@ __global__ void __launch_bounds__(kThreads, 4) verify_rows_kernel(const VerifyPa
   const Temper t = temper(greedy ? 1.f : Ti);
   const int64_t v0 = min(p.V, s * p.part_elems), v1 = min(p.V, v0 + p.part_elems);
   const T* row = is_draft ? draft + i * p.dls + j * p.dld : target + i * p.tls + j * p.tld;
+  int64_t x = -1;  // the drafted token, if this part holds its logit
+  if (tid == 0 && j < len) x = p.tokens[i * p.K + j];
   RowStat r = greedy ? row_stats<T, true>(row, v0, v1, t) : row_stats<T, false>(row, v0, v1, t);
+  float picked = 0.f;
+  if (x >= v0 && x < v1) picked = Elt<T>::load1(row + x);
   for (int o = 16; o > 0; o >>= 1) {
     const float m2 = __shfl_xor_sync(0xffffffffu, r.m, o);
     const float s2 = __shfl_xor_sync(0xffffffffu, r.s, o);
@@ -345,25 +376,31 @@ __global__ void __launch_bounds__(kThreads, 4) verify_rows_kernel(const VerifyPa
     s_arg[warp] = r.arg;
   }
   __syncthreads();
-  if (tid != 0) return;
-  float m = s_red[0].x, sum = s_red[0].y;
-  int64_t arg = s_arg[0];
-  for (int k = 1; k < kWarps; ++k) {
-    const float2 o = s_red[k];
-    arg = o.x > m ? s_arg[k] : (o.x == m ? min(arg, s_arg[k]) : arg);
-    merge(m, sum, o.x, o.y, t);
+  if (warp != 0) return;
+  uint32_t last = 0;
+  if (lane == 0) {
+    float m = s_red[0].x, sum = s_red[0].y;
+    int64_t arg = s_arg[0];
+    for (int k = 1; k < kWarps; ++k) {
+      const float2 o = s_red[k];
+      arg = o.x > m ? s_arg[k] : (o.x == m ? min(arg, s_arg[k]) : arg);
+      merge(m, sum, o.x, o.y, t);
+    }
+    const int64_t row_at = ((is_draft ? p.K + 1 : 0) + j) * p.N + i;
+    p.part[row_at * p.split + s] = make_float2(m, sum);
+    if (greedy) p.arg[row_at * p.split + s] = arg;
+    if (x >= v0 && x < v1) p.picked[row_at] = picked;
+    if (p.lazy && j < len) {
+      const uint32_t expect = (uint32_t)(p.split * (draft != nullptr && !greedy ? 2 : 1));
+      __threadfence();
+      last = atomicAdd(p.ticket + j * p.N + i, 1u) + 1u == expect;
+      __threadfence();
+    }
   }
-  const int64_t row_at = ((is_draft ? p.K + 1 : 0) + j) * p.N + i;
-  p.part[row_at * p.split + s] = make_float2(m, sum);
-  if (greedy) p.arg[row_at * p.split + s] = arg;
-  if (!p.lazy || j >= len) return;
-  __threadfence();
-  const uint32_t expect = (uint32_t)(p.split * (draft != nullptr && !greedy ? 2 : 1));
-  if (atomicAdd(p.ticket + j * p.N + i, 1u) + 1u != expect) return;
-  __threadfence();
+  if (!__shfl_sync(0xffffffffu, last, 0)) return;
   Decision d;
-  decide<T>(p, target, draft, i, j, len, Ti, d);
-  if (!d.accept) atomicMin(p.rejected + i, (int32_t)j);
+  decide(p, draft != nullptr, i, j, len, Ti, d);
+  if (lane == 0 && !d.accept) atomicMin(p.rejected + i, (int32_t)j);
 }
 
 __global__ void __launch_bounds__(kThreads) verify_init_kernel(int32_t* rejected, int64_t n,
@@ -376,16 +413,25 @@ __global__ void __launch_bounds__(kThreads) verify_init_kernel(int32_t* rejected
   for (int64_t k = (int64_t)blockIdx.x * kThreads + threadIdx.x; k < m; k += all) ticket[k] = 0;
 }
 
+// What the float32 bounds say about a slice: its best lower bound, and the
+// largest upper bound and the token of the elements that reach it.
+struct __align__(16) Bounds {  // (one 16-byte store into another CTA)
+  float lo, hi;
+  int32_t token, count;  // count: elements that reach the lower bound; -1: not separated
+};
+
 struct Shared {
   Decision dec;
-  int stop;            // the position that the sequence stops at
+  int stop;  // the position that the sequence stops at
   uint32_t flags;
+  // what the CTAs of the cluster tell one another, per round
+  Bounds bounds[2][kMaxCluster];
   double win[2][kMaxCluster];
   int64_t win_at[2][kMaxCluster];
-  int again[2][kMaxCluster];
+  int again[2][kMaxCluster];  // rank 0's: 1 a race is run, 2 and a second one may follow
   double wred[kRaceWarps];
   int64_t wred_at[kRaceWarps];
-  int best, count;
+  int best, top, count;
   int32_t cand[kCandidates];
   float cand_hi[kCandidates];
 };
@@ -394,7 +440,7 @@ struct Shared {
 struct Racer {
   Temper t;
   float mt, rt, it, md, rd, id;  // max, reference exponent, 1 / sum
-  double st, sd;
+  float st, sd;                  // the sums
   bool bigt, bigd, has_draft;
   int64_t skip;  // token without mass in the residual (drafts without logits), or -1
 };
@@ -403,8 +449,8 @@ template <typename T>
 __device__ __forceinline__ double race_score64(const Racer& c, const T* tr, const T* dr,
                                                const float* nr, int64_t v) {
   if (v == c.skip) return 0.0;
-  double p = exp(log_prob(Elt<T>::load1(tr + v), c.mt, c.st, c.t));
-  if (c.has_draft) p -= exp(log_prob(Elt<T>::load1(dr + v), c.md, c.sd, c.t));
+  double p = exp(log_weight(Elt<T>::load1(tr + v), c.mt, c.t)) / (double)c.st;
+  if (c.has_draft) p -= exp(log_weight(Elt<T>::load1(dr + v), c.md, c.t)) / (double)c.sd;
   return p > 0.0 ? p / (double)__ldg(nr + v) : 0.0;
 }
 
@@ -426,8 +472,8 @@ __device__ __forceinline__ void race_bounds(const Racer& c, float x, float y, fl
 }
 
 template <typename T>
-__device__ void race(const Racer& c, const T* tr, const T* dr, const float* nr, int64_t v0,
-                     int64_t v1, Shared& sh, double& score, int64_t& at) {
+__device__ Bounds race_bounds_of(const Racer& c, const T* tr, const T* dr, const float* nr,
+                                 int64_t v0, int64_t v1, Shared& sh) {
   using E = Elt<T>;
   constexpr int EPV = E::kPerVec;
   constexpr int U = 16 / EPV;  // vectors per thread and step: 16 elements
@@ -435,9 +481,11 @@ __device__ void race(const Racer& c, const T* tr, const T* dr, const float* nr, 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     sh.best = 0;
+    sh.top = 0;
     sh.count = 0;
   }
   __syncthreads();
+  float largest = 0.f;  // upper bound
   // the CTA's best lower bound, raised by this warp's
   auto raise = [&](float top) -> float {
     const unsigned wtop = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
@@ -447,6 +495,7 @@ __device__ void race(const Racer& c, const T* tr, const T* dr, const float* nr, 
     return __uint_as_float(wtop);
   };
   auto keep = [&](float hi, float bar, int64_t v) {
+    largest = fmaxf(largest, hi);
     if (hi >= bar && hi > 0.f && bar > 0.f) {
       const int s = atomicAdd(&sh.count, 1);
       if (s < kCandidates) {
@@ -528,18 +577,53 @@ __device__ void race(const Racer& c, const T* tr, const T* dr, const float* nr, 
 #pragma unroll
     for (int w = 0; w < W; ++w) keep(hi[w], bar, base + w * kRaceThreads + tid);
   }
+  const unsigned wlargest = __reduce_max_sync(0xffffffffu, __float_as_uint(largest));
+  if (lane == 0) atomicMax(&sh.top, (int)wlargest);
   __syncthreads();
-  const float bar = __int_as_float(sh.best);
+  Bounds r;
+  r.lo = __int_as_float(sh.best);
+  r.hi = __int_as_float(sh.top);
+  r.token = -1;
+  r.count = r.hi > 0.f ? -1 : 0;  // nothing with mass here, or nothing separated (yet)
   const int count = sh.count;
+  if (warp == 0 && r.lo > 0.f && count <= kCandidates) {
+    // the candidates that reach the final bound, to the front of the list
+    int kept = 0;
+    float hi = 0.f;
+    for (int k0 = 0; k0 < count; k0 += 32) {
+      const int k = k0 + lane;
+      const float h = k < count ? sh.cand_hi[k] : 0.f;
+      const int32_t v = k < count ? sh.cand[k] : 0;
+      const uint32_t in = __ballot_sync(0xffffffffu, k < count && h >= r.lo);
+      if (k < count && h >= r.lo) {
+        sh.cand[kept + __popc(in & ((1u << lane) - 1u))] = v;
+        hi = fmaxf(hi, h);
+      }
+      kept += __popc(in);
+      __syncwarp();
+    }
+    r.hi = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(hi)));
+    r.count = kept;
+    r.token = sh.cand[0];
+    if (lane == 0) sh.count = kept;
+  }
+  return r;  // warp 0's
+}
+
+// The slice's best score in float64 and its lowest index: of the candidates
+// kept, or (bounds that do not separate anything, residuals at the level of
+// the rounding) of every element.
+template <typename T>
+__device__ void race_exact(const Racer& c, const T* tr, const T* dr, const float* nr, int64_t v0,
+                           int64_t v1, bool separated, Shared& sh, double& score, int64_t& at) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   score = 0.0;
   at = INT64_MAX;
-  if (bar > 0.f && count <= kCandidates) {
-    for (int k = tid; k < count; k += kRaceThreads)
-      if (sh.cand_hi[k] >= bar)
+  if (separated) {
+    if (warp == 0)
+      for (int k = lane; k < sh.count; k += 32)
         better(score, at, race_score64(c, tr, dr, nr, sh.cand[k]), sh.cand[k]);
   } else {
-    // bounds that do not separate anything (residuals at the level of the
-    // rounding): every element in float64
     for (int64_t v = v0 + tid; v < v1; v += kRaceThreads)
       better(score, at, race_score64(c, tr, dr, nr, v), v);
   }
@@ -558,6 +642,10 @@ __device__ void race(const Racer& c, const T* tr, const T* dr, const float* nr, 
   for (int k = 1; k < kRaceWarps; ++k) better(score, at, sh.wred[k], sh.wred_at[k]);
 }
 
+// A line on its way into L2.
+__device__ __forceinline__ void prefetch_l2(const void* q) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+}
 __device__ __forceinline__ void st_cluster_f64(uint32_t addr, double v) {
   asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
 }
@@ -573,103 +661,145 @@ __device__ __forceinline__ uint32_t cluster_size() {
   return r;
 }
 
+static_assert(sizeof(Bounds) == 16 && offsetof(Shared, bounds) % 16 == 0, "16-byte stores");
+static_assert(offsetof(Shared, win) % 8 == 0 && offsetof(Shared, win_at) % 8 == 0 &&
+                  offsetof(Shared, again) % 4 == 0,
+              "stores into other CTAs");
+
+__device__ __forceinline__ void cluster_or_cta_sync(uint32_t ranks) {
+  __syncwarp();  // the cluster barrier instructions are warp-aligned
+  if (ranks > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kRaceThreads, 2) verify_emit_kernel(
     const VerifyParams p, const T* __restrict__ target, const T* __restrict__ draft) {
   __shared__ __align__(16) Shared sh;
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_ctarank(), ranks = cluster_size();
-  pdl_wait();
-  pdl_trigger();
   const int64_t i = cluster_id_x();
+  const int64_t v0 = min(p.V, (int64_t)rank * p.chunk), v1 = min(p.V, v0 + p.chunk);
+  const float* noise = p.noise + i * p.nld;
+  // The kernel before this one waited before it let this one start, so the
+  // caller's inputs are complete: the lengths, temperatures and the noise (on
+  // its way into L2) need no wait.
   uint32_t flags = 0;
   const int32_t len = clamped_len(p, i, &flags);
   const float Ti = temperature_of(p, i);
-  const Temper t = temper(Ti < kMinTemperature ? 1.f : Ti);
+  const bool greedy = Ti < kMinTemperature;
+  if (!greedy)
+    for (int64_t v = v0 + 32 * (int64_t)tid; v < v1; v += 32 * kRaceThreads) prefetch_l2(noise + v);
+  const Temper t = temper(greedy ? 1.f : Ti);
+  pdl_wait();
+  pdl_trigger();
   if (blockIdx.x == 0 && tid == 0) {
     p.hdr->flags = kFlagIndirect;
     p.hdr->status_count = (uint32_t)p.N;
     p.hdr->status_check = ~(uint32_t)p.N;
   }
-  // every position's decision, one per lane; the first that is not accepted
-  // is where the sequence stops (a row that was left out lies behind it)
-  // (a published rejection is taken over as it is: rows behind it are missing)
+  // every position's decision, one per warp; the first that is not accepted
+  // is where the sequence stops (a row that was left out lies behind it, and
+  // a published rejection is taken over as it is)
   const int32_t known = p.lazy ? p.rejected[i] : INT32_MAX;
-  if (tid < 32) {
-    for (int64_t base = 0; base <= len; base += 32) {
-      const int64_t j = base + lane;
-      Decision d;
-      d.accept = 0;
-      d.flags = 0;
-      if (j <= len) decide<T>(p, target, draft, i, j, len, Ti, d);
-      if (j >= known) d.accept = 0;
-      const uint32_t stops = __ballot_sync(0xffffffffu, !d.accept);
-      const int first = stops ? __ffs(stops) - 1 : 32;
-      if (lane <= first) flags |= d.flags;
-      if (rank == 0 && lane < first) {
-        p.out_tokens[i * (p.K + 1) + j] = d.token;
-        p.logp[i * (p.K + 1) + j] = (float)d.lp;
-      }
-      if (lane == first) {
-        sh.dec = d;
-        sh.stop = (int)j;
-      }
-      if (stops) break;
+  if (tid == 0) {
+    sh.stop = INT32_MAX;
+    sh.flags = flags;
+  }
+  for (int64_t base = 0; base <= len; base += kRaceWarps) {
+    __syncthreads();
+    const int64_t j = base + warp;
+    Decision d;
+    d.accept = 0;
+    if (j <= len && j <= known) {
+      decide(p, draft != nullptr, i, j, len, Ti, d);
+      if (j == known) d.accept = 0;
+      if (lane == 0 && !d.accept) atomicMin(&sh.stop, (int)j);
     }
-    flags = __reduce_or_sync(0xffffffffu, flags);
-    if (lane == 0) sh.flags = flags;
+    __syncthreads();
+    const int stop = sh.stop;
+    if (lane == 0 && j <= stop && j <= len) {
+      if (d.flags) atomicOr(&sh.flags, d.flags);
+      if (j == stop) {
+        sh.dec = d;
+      } else if (rank == 0) {
+        p.out_tokens[i * (p.K + 1) + j] = d.token;
+        p.logp[i * (p.K + 1) + j] = d.lp;
+      }
+    }
+    if (stop != INT32_MAX) break;
   }
   // (also: every CTA of the cluster runs before the first distributed store)
-  if (ranks > 1)
-    cluster_sync();
-  else
-    __syncthreads();
+  cluster_or_cta_sync(ranks);
   const Decision d = sh.dec;
   const int64_t j = sh.stop;
   const bool bonus = j >= len;
   flags = sh.flags;
   const T* trow = target + i * p.tls + j * p.tld;
   const T* drow = draft != nullptr && !bonus ? draft + i * p.dls + j * p.dld : nullptr;
-  const int64_t v0 = min(p.V, (int64_t)rank * p.chunk), v1 = min(p.V, v0 + p.chunk);
   Racer c;
   c.t = t;
   c.mt = d.mt;
   c.rt = ref_of(d.mt, t);
   c.bigt = is_big(d.mt);
-  c.it = (float)(1.0 / d.st);
+  c.it = 1.f / d.st;
   c.st = d.st;
   c.md = d.md;
   c.rd = ref_of(d.md, t);
   c.bigd = is_big(d.md);
   c.sd = d.sd;
   c.has_draft = drow != nullptr;
-  c.id = c.has_draft ? (float)(1.0 / d.sd) : 0.f;
+  c.id = 1.f / d.sd;
   c.skip = draft == nullptr && !bonus ? d.token : -1;
   int64_t token = d.emit == 2 ? d.arg : -1;
-  // The CTAs of the cluster pass the same barriers: what a further round
-  // depends on comes from what rank 0 sent.
+  // The CTAs of the cluster pass the same barriers: what a further step
+  // depends on comes from what they sent one another.
   for (int round = 0; round < 2; ++round) {
-    double s = 0.0;
-    int64_t at = INT64_MAX;
-    if (d.emit == 1) race(c, trow, drow, p.noise + i * p.nld, v0, v1, sh, s, at);
-    const int again = d.emit == 1 && (c.has_draft || c.skip >= 0);
+    Bounds own = {0.f, 0.f, -1, 0};
+    if (d.emit == 1) own = race_bounds_of(c, trow, drow, noise, v0, v1, sh);
+    if (tid < (int)ranks) {
+      const uint32_t to = (uint32_t)tid;
+      const float4 f = make_float4(own.lo, own.hi, __int_as_float(own.token), __int_as_float(own.count));
+      st_cluster_f32x4(map_to_rank(smem_u32(&sh.bounds[round][rank]), to), f);
+      st_cluster_s32(map_to_rank(smem_u32(&sh.again[round][rank]), to),
+                     d.emit != 1 ? 0 : (c.has_draft || c.skip >= 0 ? 2 : 1));
+    }
+    cluster_or_cta_sync(ranks);
+    const int again = sh.again[round][0];
+    if (again == 0) break;
+    float bar = 0.f;
+    for (uint32_t k = 0; k < ranks; ++k) bar = fmaxf(bar, sh.bounds[round][k].lo);
+    int rivals = 0;
+    int32_t winner = -1;
+    for (uint32_t k = 0; k < ranks; ++k) {
+      const Bounds b = sh.bounds[round][k];
+      if (b.count != 0 && b.hi >= bar) {
+        rivals += b.count < 0 ? 2 : b.count;
+        winner = b.token;
+      }
+    }
+    if (rivals == 1 && bar > 0.f) {  // nothing else comes near
+      token = winner;
+      break;
+    }
+    const Bounds mine = sh.bounds[round][rank];
+    double s;
+    int64_t at;
+    race_exact(c, trow, drow, noise, v0, v1, mine.count >= 0, sh, s, at);
     if (tid < (int)ranks) {
       const uint32_t to = (uint32_t)tid;
       st_cluster_f64(map_to_rank(smem_u32(&sh.win[round][rank]), to), s);
       st_cluster_s64(map_to_rank(smem_u32(&sh.win_at[round][rank]), to), at);
-      st_cluster_s32(map_to_rank(smem_u32(&sh.again[round][rank]), to), again);
     }
-    __syncwarp();  // the cluster barrier instructions are warp-aligned
-    if (ranks > 1)
-      cluster_sync();
-    else
-      __syncthreads();
+    cluster_or_cta_sync(ranks);
     s = sh.win[round][0];
     at = sh.win_at[round][0];
     for (uint32_t k = 1; k < ranks; ++k) better(s, at, sh.win[round][k], sh.win_at[round][k]);
-    if (d.emit == 1 && s > 0.0) token = at;
+    token = s > 0.0 ? at : -1;
     // nothing left in the residual (p = q up to rounding): the target's own race
-    if (s > 0.0 || !sh.again[round][0]) break;
+    if (s > 0.0 || again == 1) break;
     c.has_draft = false;
     c.skip = -1;
   }
@@ -678,7 +808,8 @@ __global__ void __launch_bounds__(kRaceThreads, 2) verify_emit_kernel(
   const int64_t o = i * (p.K + 1);
   if (tid == 0) {
     p.out_tokens[o + j] = token;
-    p.logp[o + j] = token >= 0 ? (float)log_prob(Elt<T>::load1(trow + token), d.mt, d.st, t)
+    p.logp[o + j] = token >= 0 ? (float)(log_weight(Elt<T>::load1(trow + token), d.mt, t) -
+                                         (double)logf(d.st))
                                : __int_as_float(0x7fc00000);
     p.n_accepted[i] = (int32_t)j;
     p.status[i] = flags & ~kFlagIndirect;
@@ -690,7 +821,7 @@ __global__ void __launch_bounds__(kRaceThreads, 2) verify_emit_kernel(
 }
 
 struct VerifyLayout {
-  size_t status, part, arg, rejected, ticket, total;
+  size_t status, part, arg, picked, rejected, ticket, total;
 };
 VerifyLayout verify_layout(int64_t N, int64_t K) {
   VerifyLayout l;
@@ -704,6 +835,7 @@ VerifyLayout verify_layout(int64_t N, int64_t K) {
   l.status = take(4 * n);
   l.part = take(2 * rows * kMaxSplit * sizeof(float2));
   l.arg = take(rows * kMaxSplit * sizeof(int64_t));
+  l.picked = take(2 * rows * sizeof(float));
   l.rejected = take(4 * n);
   l.ticket = take(4 * rows);
   l.total = at;
@@ -718,7 +850,7 @@ cudaError_t launch_t(const VerifyArgs& a, const DeviceInfo& d, cudaStream_t st) 
   const int64_t row_bytes = a.V * (int64_t)sizeof(T);
   const int kinds = a.draft != nullptr ? 2 : 1;
   // parts of a row: enough that the first position's rows occupy every SM
-  // four times over, of at least 16 KiB
+  // four times over, of at least 8 KiB
   int split = 1;
   while (split < kMaxSplit && a.N * kinds * split < 4 * (int64_t)d.sms &&
          row_bytes / (2 * split) >= kMinPartBytes)
@@ -746,6 +878,7 @@ cudaError_t launch_t(const VerifyArgs& a, const DeviceInfo& d, cudaStream_t st) 
   p.status = reinterpret_cast<uint32_t*>(ws + l.status);
   p.part = reinterpret_cast<float2*>(ws + l.part);
   p.arg = reinterpret_cast<int64_t*>(ws + l.arg);
+  p.picked = reinterpret_cast<float*>(ws + l.picked);
   p.rejected = reinterpret_cast<int32_t*>(ws + l.rejected);
   p.ticket = reinterpret_cast<uint32_t*>(ws + l.ticket);
   p.split = split;
@@ -765,7 +898,7 @@ cudaError_t launch_t(const VerifyArgs& a, const DeviceInfo& d, cudaStream_t st) 
   e = launch_pdl(verify_rows_kernel<T>, dim3((unsigned)(rows * split)), dim3(kThreads), 0, st, 1,
                  p, target, draft);
   if (e != cudaSuccess) return e;
-  // the emitting cluster: twice every SM, at least 16 KiB of logits per CTA
+  // the emitting cluster: twice every SM, at least 8 KiB of logits per CTA
   int C = 1;
   while (C < kMaxCluster && a.N * C < 2 * (int64_t)d.sms && row_bytes / (2 * C) >= kMinPartBytes)
     C *= 2;
