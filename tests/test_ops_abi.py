@@ -171,7 +171,7 @@ def test_binding_refuses_cpu_tensors_and_wrong_types(n):
     with pytest.raises(ValueError):
         n.grpo_embed_bwd(ids, torch.zeros(4, 16), 8)
     with pytest.raises(ValueError):
-        n._rows(w, "w")
+        n._rows(w, "w", w.device)
     with pytest.raises(ValueError):
         n._tensor_table([w], None)
     with pytest.raises(ValueError):

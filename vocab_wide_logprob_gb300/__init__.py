@@ -19,9 +19,10 @@ _NAMES = ("grpo_mask", "grpo_advantage", "grpo_advantage_ex", "grpo_workspace_si
 
 def __getattr__(name):
     if name in _NAMES:
-        from . import _native
-        return getattr(_native, name)
-    if name in ("GRPOLoss", "grpo_loss"):
-        from . import autograd
-        return getattr(autograd, name)
-    raise AttributeError(name)
+        from . import _native as module
+    elif name in ("GRPOLoss", "grpo_loss", "GRPOEmbedding", "grpo_embed"):
+        from . import autograd as module
+    else:
+        raise AttributeError(name)
+    value = globals()[name] = getattr(module, name)  # the next access is a plain one
+    return value

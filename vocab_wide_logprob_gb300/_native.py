@@ -527,25 +527,35 @@ def grpo_lmhead_loss_bwd(hidden, weight, P, input_ids, lens, lse, w, grad_loss=N
     return out[0], out[1], workspace
 
 
-def _rows(t, name, device=None):
-    """Dtype code and row pitch of a matrix whose rows are dense (a view of
-    wider rows is taken as it is)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dtype not in _CODE:
+def _rows(t, name, device):
+    """Dtype code and row pitch of a matrix on ``device`` whose rows are dense
+    (a view of wider rows is taken as it is)."""
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
+    code = _CODE.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must have two dimensions")
-    r, c = t.shape
-    pitch = t.stride(0) if r > 1 else max(t.stride(0), c)
-    if (c > 1 and t.stride(1) != 1) or pitch < c:
+    r, c = shape
+    pitch, inner = t.stride()
+    if r <= 1 and pitch < c:
+        pitch = c
+    if (c > 1 and inner != 1) or pitch < c:
         raise ValueError(f"{name} must have dense rows")
-    return _CODE[t.dtype], pitch
+    return code, pitch
 
 
 _CODE = {torch.float32: GRPO_F32, torch.bfloat16: GRPO_BF16}
+
+
+def _empty_rows(shape, dtype, name, device):
+    """A new dense tensor and its dtype code."""
+    code = _CODE.get(dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
+    return torch.empty(shape, dtype=dtype, device=device), code
 
 
 def grpo_embed_fwd(ids, weight, scale=1.0, out=None, out_dtype=None, stream=None):
@@ -554,21 +564,21 @@ def grpo_embed_fwd(ids, weight, scale=1.0, out=None, out_dtype=None, stream=None
     d] in ``out_dtype`` (the weight's when None); a given ``out`` may be a view
     [n, d] of wider rows.  An id outside [0, V) gives a row of NaN."""
     _dev(ids, "ids", torch.int64)
-    wcode, ldw = _rows(weight, "weight", ids.device)
+    dev = ids.device
+    wcode, ldw = _rows(weight, "weight", dev)
     V, d = weight.shape
     n = ids.numel()
     if out is None:
-        out = torch.empty((*ids.shape, d), dtype=out_dtype or weight.dtype, device=ids.device)
-        flat = out.view(n, d)
+        out, ocode = _empty_rows(ids.shape + (d,), out_dtype or weight.dtype, "out", dev)
+        ldo = d
     else:
         if out_dtype is not None and out.dtype != out_dtype:
             raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
-        if tuple(out.shape) not in ((*ids.shape, d), (n, d)):
+        if out.shape != ids.shape + (d,) and out.shape != (n, d):
             raise ValueError("out must be [*ids.shape, d]")
-        flat = out if out.dim() == 2 else out.view(n, d)
-    ocode, ldo = _rows(flat, "out", ids.device)
-    _check(_lib.grpo_embed_fwd(_ptr(ids), n, _ptr(weight), wcode, V, d, ldw, float(scale),
-                               _ptr(flat), ocode, ldo, _stream(stream)), "grpo_embed_fwd")
+        ocode, ldo = _rows(out if out.dim() == 2 else out.view(n, d), "out", dev)
+    _check(_lib.grpo_embed_fwd(ids.data_ptr(), n, weight.data_ptr(), wcode, V, d, ldw, float(scale),
+                               out.data_ptr(), ocode, ldo, _stream(stream)), "grpo_embed_fwd")
     return out
 
 
@@ -587,27 +597,29 @@ def grpo_embed_bwd(ids, dout, V, scale=1.0, pad_id=None, dweight=None, accumulat
     gradient is added to the given ``dweight`` (for example the LM head's, with
     tied weights).  Tokens equal to ``pad_id`` contribute nothing."""
     _dev(ids, "ids", torch.int64)
+    dev = ids.device
     n = ids.numel()
-    if dout.shape[:-1] != ids.shape and tuple(dout.shape[:-1]) != (n,):
+    if dout.shape[:-1] != ids.shape and dout.shape[:-1] != (n,):
         raise ValueError("dout must be [*ids.shape, d]")
     d = dout.shape[-1]
-    flat = dout if dout.dim() == 2 else dout.view(n, d)
-    dcode, ldd = _rows(flat, "dout", ids.device)
+    dcode, ldd = _rows(dout if dout.dim() == 2 else dout.view(n, d), "dout", dev)
     if dweight is None:
         if accumulate:
             raise ValueError("accumulate needs a dweight")
-        dweight = torch.empty((V, d), dtype=out_dtype or torch.float32, device=ids.device)
-    elif out_dtype is not None and dweight.dtype != out_dtype:
-        raise TypeError(f"dweight must be {out_dtype}, got {dweight.dtype}")
-    if tuple(dweight.shape) != (V, d):
-        raise ValueError("dweight must be [V, d]")
-    wcode, ldw = _rows(dweight, "dweight", ids.device)
+        dweight, wcode = _empty_rows((V, d), out_dtype or torch.float32, "dweight", dev)
+        ldw = d
+    else:
+        if out_dtype is not None and dweight.dtype != out_dtype:
+            raise TypeError(f"dweight must be {out_dtype}, got {dweight.dtype}")
+        if dweight.shape != (V, d):
+            raise ValueError("dweight must be [V, d]")
+        wcode, ldw = _rows(dweight, "dweight", dev)
     need = grpo_embed_workspace_size(n, V, d)
     if workspace is None or workspace.numel() < need:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=ids.device)
-    pad = -1 if pad_id is None else int(pad_id)
-    _check(_lib.grpo_embed_bwd(_ptr(ids), n, _ptr(flat), dcode, V, d, ldd, float(scale), pad,
-                               _ptr(dweight), wcode, ldw, 1 if accumulate else 0, _ptr(workspace),
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    _check(_lib.grpo_embed_bwd(ids.data_ptr(), n, dout.data_ptr(), dcode, V, d, ldd, float(scale),
+                               -1 if pad_id is None else int(pad_id), dweight.data_ptr(), wcode,
+                               ldw, 1 if accumulate else 0, workspace.data_ptr(),
                                workspace.numel(), _stream(stream)), "grpo_embed_bwd")
     return dweight, workspace
 
@@ -658,9 +670,10 @@ def _clip_buffers(grads, stats, workspace):
     dev = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
     if stats is None:
         stats = torch.empty((2,), dtype=torch.float32, device=dev)
-    _dev(stats, "stats", torch.float32)
-    if stats.numel() < 2:
-        raise ValueError("stats must hold two values")
+    else:
+        _dev(stats, "stats", torch.float32)
+        if stats.numel() < 2:
+            raise ValueError("stats must hold two values")
     need = grpo_grad_norm_workspace_size(len(grads))
     if workspace is None or workspace.numel() < need:
         workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
@@ -676,8 +689,8 @@ def grpo_clip_grad_norm(grads, max_norm, out=None, norm_type=GRPO_NORM_L2, eps=1
     grads = list(grads)
     stats, workspace = _clip_buffers(grads, stats, workspace)
     table = _tensor_table(grads, out)
-    _check(_lib.grpo_clip_grad_norm(table.buffer_info()[0], len(grads), int(norm_type), float(max_norm), float(eps),
-                                    _ptr(stats), _ptr(workspace), workspace.numel(),
+    _check(_lib.grpo_clip_grad_norm(table.buffer_info()[0], len(grads), norm_type, float(max_norm), eps,
+                                    stats.data_ptr(), workspace.data_ptr(), workspace.numel(),
                                     _stream(stream)), "grpo_clip_grad_norm")
     return stats, workspace
 
@@ -688,8 +701,9 @@ def grpo_grad_norm(grads, norm_type=GRPO_NORM_L2, stats=None, workspace=None, st
     grads = list(grads)
     stats, workspace = _clip_buffers(grads, stats, workspace)
     table = _tensor_table(grads, None)
-    _check(_lib.grpo_grad_norm(table.buffer_info()[0], len(grads), int(norm_type), _ptr(stats), _ptr(workspace),
-                               workspace.numel(), _stream(stream)), "grpo_grad_norm")
+    _check(_lib.grpo_grad_norm(table.buffer_info()[0], len(grads), norm_type, stats.data_ptr(),
+                               workspace.data_ptr(), workspace.numel(), _stream(stream)),
+           "grpo_grad_norm")
     return stats, workspace
 
 
@@ -699,17 +713,33 @@ def grpo_verify_workspace_size(N: int, K: int) -> int:
     return int(out.value)
 
 
-def _logit_rows(t, name, shape):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3 or tuple(t.shape) != shape:
+def _logit_rows(t, name, shape, device):
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     N, R, V = shape
-    row = t.stride(1) if R > 1 else max(t.stride(1), V)
-    seq = t.stride(0) if N > 1 else max(t.stride(0), R * row)
-    if (V > 1 and t.stride(2) != 1) or row < V or (N > 1 and seq < (R - 1) * row + V):
+    seq, row, inner = t.stride()
+    if R <= 1 and row < V:
+        row = V
+    if N <= 1 and seq < R * row:
+        seq = R * row
+    if (V > 1 and inner != 1) or row < V or seq < (R - 1) * row + V:
         raise ValueError(f"{name} must have dense rows that do not overlap")
     return seq, row
+
+
+def _vector(t, name, dtype, shape, device):
+    """Address of a contiguous tensor of that type and shape (None: none)."""
+    if t is None:
+        return None
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
 
 
 def grpo_verify_drafts(target_logits, draft_tokens, u, noise, draft_logits=None, draft_lens=None,
@@ -725,49 +755,44 @@ def grpo_verify_drafts(target_logits, draft_tokens, u, noise, draft_logits=None,
     reuse the buffers."""
     if target_logits.dim() != 3:
         raise ValueError("target_logits must be [N, K+1, V]")
-    N, K, V = target_logits.shape[0], target_logits.shape[1] - 1, target_logits.shape[2]
+    N, rows, V = target_logits.shape
+    K = rows - 1
     if K < 0:
         raise ValueError("target_logits must have at least one row per sequence")
-    if target_logits.dtype not in _CODE:
-        raise TypeError(f"target_logits must be float32 or bfloat16, got {target_logits.dtype}")
-    tseq, trow = _logit_rows(target_logits, "target_logits", (N, K + 1, V))
+    dev, dtype = target_logits.device, target_logits.dtype
+    if dtype not in _CODE:
+        raise TypeError(f"target_logits must be float32 or bfloat16, got {dtype}")
+    tseq, trow = _logit_rows(target_logits, "target_logits", (N, rows, V), dev)
     dseq = drow = 0
     if draft_logits is not None:
-        if draft_logits.dtype != target_logits.dtype:
+        if draft_logits.dtype != dtype:
             raise TypeError("draft_logits must have target_logits' dtype")
-        dseq, drow = _logit_rows(draft_logits, "draft_logits", (N, K, V))
-    for name, t, dt, shape in (("draft_tokens", draft_tokens, torch.int64, (N, K)),
-                               ("u", u, torch.float32, (N, K)),
-                               ("draft_lens", draft_lens, torch.int32, (N,)),
-                               ("temperature", temperature, torch.float32, (N,))):
-        _dev(t, name, dt)
-        if t is not None and tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if noise.dtype != torch.float32 or tuple(noise.shape) != (N, V):
+        dseq, drow = _logit_rows(draft_logits, "draft_logits", (N, K, V), dev)
+    if noise.dtype != torch.float32 or noise.shape != (N, V):
         raise ValueError("noise must be float32 [N, V]")
-    _, nrow = _rows(noise, "noise", target_logits.device)
-    dev = target_logits.device
+    nrow = _rows(noise, "noise", dev)[1]
+    given = (_vector(draft_tokens, "draft_tokens", torch.int64, (N, K), dev),
+             _vector(draft_lens, "draft_lens", torch.int32, (N,), dev),
+             _vector(u, "u", torch.float32, (N, K), dev), noise.data_ptr(), nrow,
+             _vector(temperature, "temperature", torch.float32, (N,), dev))
     if out is None:
-        out = {"tokens": torch.empty((N, K + 1), dtype=torch.int64, device=dev),
+        out = {"tokens": torch.empty((N, rows), dtype=torch.int64, device=dev),
                "n_accepted": torch.empty((N,), dtype=torch.int32, device=dev),
-               "logp": torch.empty((N, K + 1), dtype=torch.float32, device=dev)}
+               "logp": torch.empty((N, rows), dtype=torch.float32, device=dev)}
+        made = (out["tokens"].data_ptr(), out["n_accepted"].data_ptr(), out["logp"].data_ptr())
     else:
-        for name, dt, shape in (("tokens", torch.int64, (N, K + 1)),
-                                ("n_accepted", torch.int32, (N,)),
-                                ("logp", torch.float32, (N, K + 1))):
-            _dev(out[name], name, dt)
-            if tuple(out[name].shape) != shape:
-                raise ValueError(f"{name} must be {list(shape)}")
+        made = (_vector(out["tokens"], "tokens", torch.int64, (N, rows), dev),
+                _vector(out["n_accepted"], "n_accepted", torch.int32, (N,), dev),
+                _vector(out["logp"], "logp", torch.float32, (N, rows), dev))
         workspace = out.get("workspace") if workspace is None else workspace
     need = grpo_verify_workspace_size(N, K)
     if workspace is None or workspace.numel() < need:
         workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
     out["workspace"] = workspace
     _check(_lib.grpo_verify_drafts(
-        _ptr(target_logits), _ptr(draft_logits), _CODE[target_logits.dtype], N, K, V, tseq, trow,
-        dseq, drow, _ptr(draft_tokens), _ptr(draft_lens), _ptr(u), _ptr(noise), nrow,
-        _ptr(temperature), _ptr(out["tokens"]), _ptr(out["n_accepted"]), _ptr(out["logp"]),
-        _ptr(workspace), workspace.numel(), _stream(stream)), "grpo_verify_drafts")
+        target_logits.data_ptr(), _ptr(draft_logits), _CODE[dtype], N, K, V, tseq, trow, dseq,
+        drow, *given, *made, workspace.data_ptr(), workspace.numel(), _stream(stream)),
+        "grpo_verify_drafts")
     return out
 
 

@@ -257,7 +257,7 @@ constexpr int kMaxTiles = 304;                  // CTAs of a sort pass (two per 
 constexpr int kMaxPasses = 4;
 static_assert(kMaxBins == kSortThreads, "one thread per bin");
 
-constexpr int kSegUnroll = 8;
+constexpr int kMinSegEntries = 8;
 constexpr int kMaxSegEntries = 32;
 
 struct SortPlan {
@@ -294,7 +294,7 @@ SortPlan sort_plan(int64_t n, int64_t V, int64_t d) {
   // few tokens: shorter groups, so that there are enough of them (about 512
   // threads on each of 152 SMs)
   s.seg = kMaxSegEntries;
-  while (s.seg > kSegUnroll && (n + s.seg - 1) / s.seg * (padded_cols(d) / 8) < 152 * 512) s.seg /= 2;
+  while (s.seg > kMinSegEntries && (n + s.seg - 1) / s.seg * (padded_cols(d) / 8) < 152 * 512) s.seg /= 2;
   s.seg_tiles = (n + s.seg - 1) / s.seg;
   return s;
 }
@@ -609,128 +609,146 @@ __device__ __forceinline__ void write_row(TW* row, int step, int left, bool accu
   Cols8<TW, kVec>::store(row, step, left, x);
 }
 
-// One thread's 8 columns of a token's row, as loaded.
-template <typename T, bool kVec>
-struct RowPart;
-template <typename T>
-struct RowPart<T, true> {
-  Vec8<T> v;
-  __device__ __forceinline__ void load(const T* p, int, int) { v.load_stream(p); }
-  __device__ __forceinline__ void get(float* x) const { v.unpack(x); }
-};
-template <typename T>
-struct RowPart<T, false> {
-  float v[8];
-  __device__ __forceinline__ void load(const T* p, int step, int left) {
-    Cols8<T, false>::load(p, step, left, v);
-  }
-  __device__ __forceinline__ void get(float* x) const {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = v[k];
-  }
-};
+// Bytes a thread of the summing kernel has on their way: kSumDepth rows of 8
+// columns, asynchronous copies through a ring of its own in shared memory
+// (rows of any alignment: kSumRegs rows in registers instead).
+template <typename TD>
+__host__ __device__ constexpr int sum_depth() {
+  return sizeof(TD) == 4 ? 4 : 8;
+}
+constexpr int kSumRegs = 4;
+constexpr int kMaxGroups = 32;
 
-// A group of `tpr` threads takes Q sorted entries (a tile), 8
-// columns per thread, and writes a row whenever the id changes.  An id that
-// goes on past its tile is finished by the group it began in, unless it fills
-// a whole further tile: then it is split at the tiles, every tile leaves its
-// partial sum, and embed_join_kernel adds them.  Both neighbours decide that
-// from the same keys: the id at a tile's first entry a is split iff it began
-// before the previous tile (key[a - Q - 1]) or reaches past this one
-// (key[a + Q]).
-// U rows are in flight per thread: 8 of bfloat16, 4 of float32.
-template <typename TD, typename TW, bool kVec, bool kAcc, int U>
-__global__ void __launch_bounds__(kThreads, 2) embed_sum_kernel(const SegParams p,
+// A group of `tpr` threads takes Q sorted entries (a tile), 8 columns per
+// thread, and writes a row whenever the id changes.  An id that goes on past
+// its tile is finished by the group it began in, unless it fills a whole
+// further tile: then it is split at the tiles, every tile leaves its partial
+// sum, and embed_join_kernel adds them.  Both neighbours decide that from the
+// same keys: the id at a tile's first entry a is split iff it began before the
+// previous tile (key[a - Q - 1]) or reaches past this one (key[a + Q]).
+template <typename TD, typename TW, bool kVec, bool kAcc>
+__global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const SegParams p,
                                                                 const TD* __restrict__ dout,
                                                                 TW* dw) {
+  extern __shared__ __align__(16) unsigned char sum_ring[];
+  __shared__ int32_t s_key[(kMaxGroups + 1) * kMaxSegEntries];
+  __shared__ int32_t s_pos[(kMaxGroups + 1) * kMaxSegEntries];
   const int Q = p.seg;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
+  // keys and positions of the CTA's tiles and of one tile more (for the last
+  // one's extension)
+  const int64_t base = (int64_t)blockIdx.x * p.groups * Q;
+  const int have = (int)min((int64_t)(p.groups + 1) * Q, p.n - base);
+  for (int k = tid; k < have; k += kThreads) {
+    s_key[k] = p.key[base + k];
+    s_pos[k] = p.pos[base + k];
+  }
   const int grp = tid / p.tpr, l = tid - grp * p.tpr;
-  if (grp >= p.groups) return;
   const int64_t t = (int64_t)blockIdx.x * p.groups + grp;
   const int64_t a = t * Q, b = min(a + Q, p.n);
-  if (a >= p.n) return;
+  const bool live = grp < p.groups && a < p.n;
+  const int32_t prev = live && a > 0 ? p.key[a - 1] : -1;
+  const int32_t prev2 = live && a > Q ? p.key[a - Q - 1] : -1;
+  const int32_t next2 = live && b + Q < p.n ? p.key[b + Q] : -1;
+  __syncthreads();
+  if (!live) return;
   const int64_t c0 = (int64_t)blockIdx.y * p.cols + (kVec ? 8 * l : l);
   const int left = (int)min((int64_t)p.cols, p.d - (int64_t)blockIdx.y * p.cols) - (kVec ? 8 * l : l);
   const int step = p.tpr;
   if (left <= 0) return;
-  // the keys that decide about the tile's ends (and the first entries') in
-  // one round of loads
-  const int32_t first = p.key[a];
-  const int32_t prev = a > 0 ? p.key[a - 1] : -1;
-  const int32_t prev2 = a > Q ? p.key[a - Q - 1] : -1;
-  const int32_t last = p.key[b - 1];
-  const int32_t next = b < p.n ? p.key[b] : -1;
-  const int32_t next2 = b + Q < p.n ? p.key[b + Q] : -1;
-  int32_t k[U], at[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    k[u] = a + u < p.n ? p.key[a + u] : INT32_MAX;
-    at[u] = a + u < p.n ? p.pos[a + u] : 0;
-  }
+  const int32_t* key = s_key + grp * Q;
+  const int32_t* pos = s_pos + grp * Q;
+  const int nb = (int)(b - a);  // entries of the tile
+  const int32_t first = key[0];
   if (first >= p.V) return;  // ignored tokens from here on
+  const int32_t last = key[nb - 1];
+  const int32_t next = b < p.n ? key[nb] : -1;
   const bool head = prev == first;
   bool open = head && (prev2 == first || next == first);  // split: this tile's share of it
-  const bool skip = head && !open;                         // the tile before finishes it
   const bool goes_on = next == last && last < p.V;
   const bool split = goes_on && (next2 == last || (open && last == first));
-  const bool extend = goes_on && !split;
+  // entries [e0, e1) are this group's: not the ones the tile before finishes,
+  // not the ignored ones, and of the next tile those that finish `last`
+  int e0 = 0, e1 = nb;
+  if (head && !open)
+    while (e0 < nb && key[e0] == first) ++e0;
+  while (e1 > e0 && key[e1 - 1] >= p.V) --e1;
+  if (goes_on && !split)
+    while (e1 < nb + Q && a + e1 < p.n && key[e1] == last) ++e1;
+  if (e0 >= e1) return;
   // partial sums keep the thread's 8 columns side by side
   float* part = p.part + 2 * t * p.dpad + (int64_t)blockIdx.y * p.cols + 8 * l;
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  int32_t cur = -1;
+  float acc[8];
   auto flush_part = [&](int which) {
     float4* q = reinterpret_cast<float4*>(part + which * p.dpad);
     q[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     q[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
   };
+  int32_t cur = -1;
   auto flush = [&]() {
     if (open)
       flush_part(0);
     else
       write_row<TW, kVec>(dw + cur * p.ldw + c0, step, left, kAcc, p.scale, acc);
   };
-  const int64_t stop = extend ? min(b + Q, p.n) : b;
-  for (int64_t e = a; e < stop; e += U) {
-    RowPart<TD, kVec> x[U];
-    bool use[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      use[u] = k[u] < p.V && (e + u < b || (extend && k[u] == last)) && !(skip && k[u] == first);
-      if (use[u]) x[u].load(dout + (int64_t)at[u] * p.ldd + c0, step, left);
-    }
-    int32_t kn[U];
-    const bool more = e + U < stop;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t i = e + U + u;
-      kn[u] = more && i < p.n ? p.key[i] : INT32_MAX;
-      at[u] = more && i < p.n ? p.pos[i] : 0;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (use[u]) {
-        float v[8];
-        x[u].get(v);
-        if (k[u] != cur) {
-          if (cur >= 0) {
-            flush();
-            open = false;
-          }
-          cur = k[u];
-#pragma unroll
-          for (int c = 0; c < 8; ++c) acc[c] = v[c];
-        } else {
-#pragma unroll
-          for (int c = 0; c < 8; ++c) acc[c] += v[c];
-        }
+  auto take = [&](int e, const float* v) {
+    const int32_t k = key[e];
+    if (k != cur) {
+      if (cur >= 0) {
+        flush();
+        open = false;
       }
-      k[u] = kn[u];
+      cur = k;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) acc[c] = v[c];
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) acc[c] += v[c];
+    }
+  };
+  if constexpr (kVec) {
+    constexpr int kDepth = sum_depth<TD>(), kUnit = 8 * (int)sizeof(TD);
+    const uint32_t mine = smem_u32(sum_ring) + tid * kUnit;  // slot k: + k * kThreads * kUnit
+    auto issue = [&](int e, int slot) {
+      if (e < e1) {
+        const char* src = reinterpret_cast<const char*>(dout + (int64_t)pos[e] * p.ldd + c0);
+#pragma unroll
+        for (int q = 0; q < kUnit; q += 16)
+          cp_async16(mine + slot * (kThreads * kUnit) + q, src + q);
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < kDepth; ++k) issue(e0 + k, k);
+    int slot = 0;
+#pragma unroll 1
+    for (int e = e0; e < e1; ++e) {
+      cp_async_wait<kDepth - 1>();
+      Vec8<TD> x;
+#pragma unroll
+      for (int k = 0; k < Vec8<TD>::kWords; ++k)
+        x.v[k] = ld_shared_v4(mine + slot * (kThreads * kUnit) + 16 * k);
+      float v[8];
+      x.unpack(v);
+      take(e, v);
+      issue(e + kDepth, slot);
+      slot = slot + 1 == kDepth ? 0 : slot + 1;
+    }
+    cp_async_wait<0>();
+  } else {
+#pragma unroll 1
+    for (int e = e0; e < e1; e += kSumRegs) {
+      float v[kSumRegs][8];
+#pragma unroll
+      for (int u = 0; u < kSumRegs; ++u)
+        if (e + u < e1) Cols8<TD, false>::load(dout + (int64_t)pos[e + u] * p.ldd + c0, step, left, v[u]);
+#pragma unroll
+      for (int u = 0; u < kSumRegs; ++u)
+        if (e + u < e1) take(e + u, v[u]);
     }
   }
-  if (cur < 0) return;
   if (split && cur == last) {
     flush_part(open ? 0 : 1);
     if (!open && l == 0 && blockIdx.y == 0) p.list[1 + atomicAdd(p.list, 1)] = (int32_t)t;
@@ -817,11 +835,12 @@ cudaError_t launch_sums(const EmbedBwdArgs& a, SegParams p, const DeviceInfo& de
                         cudaStream_t st) {
   const unsigned ny = (unsigned)((p.d + p.cols - 1) / p.cols);
   const int64_t seg_tiles = (p.n + p.seg - 1) / p.seg;
-  constexpr int U = sizeof(TD) == 4 ? 4 : 8;
   const int64_t blocks = (seg_tiles + p.groups - 1) / p.groups;
-  cudaError_t e = launch_pdl(embed_sum_kernel<TD, TW, kVec, kAcc, U>,
-                             dim3((unsigned)blocks, ny), dim3(kThreads), 0,
-                             st, 1, p, static_cast<const TD*>(a.dout), static_cast<TW*>(a.dweight));
+  const size_t ring = kVec ? (size_t)sum_depth<TD>() * kThreads * 8 * sizeof(TD) : 0;
+  cudaError_t e = ensure_dynamic_smem((const void*)embed_sum_kernel<TD, TW, kVec, kAcc>, (int)ring);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(embed_sum_kernel<TD, TW, kVec, kAcc>, dim3((unsigned)blocks, ny), dim3(kThreads),
+                 ring, st, 1, p, static_cast<const TD*>(a.dout), static_cast<TW*>(a.dweight));
   if (e != cudaSuccess || seg_tiles < 2) return e;
   const int64_t items = seg_tiles * ((p.dpad + kJoinCols - 1) / kJoinCols);
   const int64_t grid = items < 4 * (int64_t)dev.sms ? items : 4 * (int64_t)dev.sms;
@@ -941,6 +960,7 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, const DeviceInfo& dev, cudaS
   // rows side by side in a CTA, unless that leaves SMs without one
   const int64_t per = s.seg_tiles / (2 * (int64_t)dev.sms);
   p.groups = kThreads / p.tpr;
+  if (p.groups > kMaxGroups) p.groups = kMaxGroups;
   if (p.groups > per) p.groups = per < 1 ? 1 : (int)per;
   p.cols = 8 * p.tpr;
   const size_t de = a.ddtype == 0 ? 4 : 2;

@@ -27,6 +27,7 @@
 #include <math.h>
 #include <stddef.h>
 
+#include "host_ctx.cuh"
 #include "ops.cuh"
 
 namespace grpo {
@@ -146,14 +147,21 @@ struct RowStat {
   int64_t arg;
 };
 
+// The rows kernel streams a row through shared memory: every thread copies its
+// own 16-byte vectors kRowStages batches ahead (asynchronous copies, read back
+// by the thread that issued them: no barrier, no registers).
+constexpr int kRowVecs = 4;  // vectors of a batch, per thread
+constexpr int kRowStages = 3;
+constexpr size_t kRowRing = (size_t)kRowStages * kRowVecs * kThreads * 16;
+
 // (max, sum) of one CTA's slice [v0, v1) of a row, per thread; with kArg also
 // where the thread saw its maximum first.
 template <typename T, bool kArg>
 __device__ __forceinline__ RowStat row_stats(const T* row, int64_t v0, int64_t v1,
-                                             const Temper& t) {
+                                             const Temper& t, uint32_t ring) {
   using E = Elt<T>;
   constexpr int EPV = E::kPerVec;
-  constexpr int U = 4;
+  constexpr int U = kRowVecs;
   const int tid = threadIdx.x;
   RowStat r;
   r.m = -INFINITY;
@@ -163,10 +171,10 @@ __device__ __forceinline__ RowStat row_stats(const T* row, int64_t v0, int64_t v
   const uintptr_t addr = reinterpret_cast<uintptr_t>(row + v0);
   const int64_t a =
       min(v0 + (int64_t)(((16u - (unsigned)(addr & 15u)) & 15u) / sizeof(T)), v1);
-  const int64_t nvec = (v1 - a) / EPV;
-  const int64_t b = a + nvec * EPV;
+  const int nvec = (int)((v1 - a) / EPV);
+  const int64_t b = a + (int64_t)nvec * EPV;
   float m = -INFINITY, edge_s = 0.f;
-  int64_t where = -1;  // first vector of the batch that holds the maximum
+  int where = -1;  // first vector of the batch that holds the maximum
   uint64_t acc01 = f2_pack(0.f, 0.f), acc23 = f2_pack(0.f, 0.f);
   const uint64_t hi2 = f2_pack(t.hi, t.hi), lo2 = f2_pack(t.lo, t.lo);
   // the ragged head and tail, at most one element of each per thread
@@ -187,15 +195,29 @@ __device__ __forceinline__ RowStat row_stats(const T* row, int64_t v0, int64_t v
     }
     if (x != -INFINITY) edge_s += ex2(exponent(x, m, ref_of(m, t), is_big(m), t));
   };
-  if (he >= 0) one(he);
-  for (int64_t base = tid; base < nvec; base += kThreads * U) {
-    uint4 d[U];
+  const uint32_t mine = ring + 16 * tid;  // vector u of stage s: + (s * U + u) * kThreads * 16
+  int ahead = tid;
+  auto issue = [&](int stage) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t k = base + u * kThreads;
-      d[u] = k < nvec ? ld_stream(row + a + k * EPV)
-                      : make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf);
+      const int k = ahead + u * kThreads;
+      if (k < nvec) cp_async16(mine + (stage * U + u) * (kThreads * 16), row + a + (int64_t)k * EPV);
     }
+    cp_async_commit();
+    ahead += kThreads * U;
+  };
+#pragma unroll
+  for (int k = 0; k < kRowStages; ++k) issue(k);
+  if (he >= 0) one(he);
+  int stage = 0;
+  for (int base = tid; base < nvec; base += kThreads * U) {
+    cp_async_wait<kRowStages - 1>();
+    uint4 d[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      d[u] = base + u * kThreads < nvec
+                 ? ld_shared_v4(mine + (stage * U + u) * (kThreads * 16))
+                 : make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf);
     const float bm = E::template batch_max<U>(d);
     if (bm > m) {
       const float sc = rescale(m, bm, t);
@@ -226,15 +248,18 @@ __device__ __forceinline__ RowStat row_stats(const T* row, int64_t v0, int64_t v
 #pragma unroll
       for (int k = 0; k < U * EPV; ++k) edge_s += ex2(exponent(x[k], m, 0.f, true, t));
     }
+    issue(stage);  // (the batch is in registers)
+    stage = stage + 1 == kRowStages ? 0 : stage + 1;
   }
+  cp_async_wait<0>();
   if (te >= 0) one(te);
   if (kArg && where >= 0) {  // the batch's first element at the maximum
     r.arg = INT64_MAX;
     for (int u = U - 1; u >= 0; --u) {
-      const int64_t k = where + u * kThreads;
+      const int k = where + u * kThreads;
       if (k < nvec)
         for (int e = EPV - 1; e >= 0; --e)
-          if (E::load1(row + a + k * EPV + e) == m) r.arg = a + k * EPV + e;
+          if (E::load1(row + a + (int64_t)k * EPV + e) == m) r.arg = a + (int64_t)k * EPV + e;
     }
   }
   float a0, a1, a2, a3;
@@ -336,6 +361,7 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) verify_rows_kernel(const VerifyParams p,
                                                                   const T* __restrict__ target,
                                                                   const T* __restrict__ draft) {
+  extern __shared__ __align__(16) unsigned char row_ring[];
   __shared__ float2 s_red[kWarps];
   __shared__ int64_t s_arg[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -359,7 +385,9 @@ __global__ void __launch_bounds__(kThreads, 4) verify_rows_kernel(const VerifyPa
   const T* row = is_draft ? draft + i * p.dls + j * p.dld : target + i * p.tls + j * p.tld;
   int64_t x = -1;  // the drafted token, if this part holds its logit
   if (tid == 0 && j < len) x = p.tokens[i * p.K + j];
-  RowStat r = greedy ? row_stats<T, true>(row, v0, v1, t) : row_stats<T, false>(row, v0, v1, t);
+  const uint32_t ring = smem_u32(row_ring);
+  RowStat r = greedy ? row_stats<T, true>(row, v0, v1, t, ring)
+                     : row_stats<T, false>(row, v0, v1, t, ring);
   float picked = 0.f;
   if (x >= v0 && x < v1) picked = Elt<T>::load1(row + x);
   for (int o = 16; o > 0; o >>= 1) {
@@ -439,8 +467,8 @@ struct Shared {
 // The row's race in this CTA's slice: best score and its lowest index.
 struct Racer {
   Temper t;
-  float mt, rt, it, md, rd, id;  // max, reference exponent, 1 / sum
-  float st, sd;                  // the sums
+  float mt, rt, md, rd;      // maxima and reference exponents
+  float st, sd, lst, lsd;    // the sums and their log2
   bool bigt, bigd, has_draft;
   int64_t skip;  // token without mass in the residual (drafts without logits), or -1
 };
@@ -461,23 +489,55 @@ __device__ __forceinline__ void better(double& s, int64_t& at, double s2, int64_
   }
 }
 
-// lower and upper bound of a score
+// Lower and upper bound of a score, any row.
 __device__ __forceinline__ void race_bounds(const Racer& c, float x, float y, float e, float& lo,
                                             float& hi) {
-  const float p = ex2(exponent(x, c.mt, c.rt, c.bigt, c.t)) * c.it;
-  const float q = c.has_draft ? ex2(exponent(y, c.md, c.rd, c.bigd, c.t)) * c.id : 0.f;
-  const float w = __fdividef(1.f, e), d = p - q, b = kRaceMargin * (p + q);
-  lo = (d - b) * w;
-  hi = (d + b) * w;
+  const float p = ex2(exponent(x, c.mt, c.rt, c.bigt, c.t) - c.lst);
+  const float q = c.has_draft ? ex2(exponent(y, c.md, c.rd, c.bigd, c.t) - c.lsd) : 0.f;
+  const float w = __fdividef(1.f, e), d = p - q, s = p + q;
+  lo = fmaf(s, -kRaceMargin, d) * w;
+  hi = fmaf(s, kRaceMargin, d) * w;
+}
+// The same for a pair of elements of rows whose maxima are not extreme:
+// nt and nd are minus the reference exponents and the log2 of the sums.
+template <bool kDraft>
+__device__ __forceinline__ void race_bounds2(uint64_t hi2, uint64_t lo2, uint64_t nt, uint64_t nd,
+                                             float x0, float x1, float y0, float y1, float e0,
+                                             float e1, uint64_t& lo, uint64_t& hi) {
+  const uint64_t x = f2_pack(x0, x1);
+  const uint64_t p = f2_ex2(f2_fma(x, lo2, f2_fma(x, hi2, nt)));
+  const uint64_t w = f2_pack(__fdividef(1.f, e0), __fdividef(1.f, e1));
+  const uint64_t up = f2_pack(kRaceMargin, kRaceMargin), dn = f2_pack(-kRaceMargin, -kRaceMargin);
+  uint64_t d = p, s = p;
+  if (kDraft) {
+    const uint64_t y = f2_pack(y0, y1);
+    const uint64_t q = f2_ex2(f2_fma(y, lo2, f2_fma(y, hi2, nd)));
+    d = f2_fma(q, f2_pack(-1.f, -1.f), p);
+    s = f2_add(p, q);
+  }
+  lo = f2_mul(f2_fma(s, dn, d), w);
+  hi = f2_mul(f2_fma(s, up, d), w);
+}
+
+// The race streams its rows as the rows kernel does: 8 elements per thread and
+// step of target, draft and noise, kRaceStages steps ahead.
+template <typename T>
+__host__ __device__ constexpr int race_stages() {
+  return sizeof(T) == 4 ? 2 : 3;
+}
+template <typename T>
+__host__ __device__ constexpr int race_vecs() {  // 16-byte vectors of a step, per thread
+  return 2 * (int)sizeof(T) / 2 + 2;
+}
+template <typename T>
+__host__ __device__ constexpr size_t race_ring() {
+  return (size_t)race_stages<T>() * race_vecs<T>() * kRaceThreads * 16;
 }
 
 template <typename T>
 __device__ Bounds race_bounds_of(const Racer& c, const T* tr, const T* dr, const float* nr,
-                                 int64_t v0, int64_t v1, Shared& sh) {
+                                 int64_t v0, int64_t v1, Shared& sh, uint32_t ring) {
   using E = Elt<T>;
-  constexpr int EPV = E::kPerVec;
-  constexpr int U = 16 / EPV;  // vectors per thread and step: 16 elements
-  constexpr int kNoiseVecs = EPV / 4;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     sh.best = 0;
@@ -495,7 +555,6 @@ __device__ Bounds race_bounds_of(const Racer& c, const T* tr, const T* dr, const
     return __uint_as_float(wtop);
   };
   auto keep = [&](float hi, float bar, int64_t v) {
-    largest = fmaxf(largest, hi);
     if (hi >= bar && hi > 0.f && bar > 0.f) {
       const int s = atomicAdd(&sh.count, 1);
       if (s < kCandidates) {
@@ -504,58 +563,99 @@ __device__ Bounds race_bounds_of(const Racer& c, const T* tr, const T* dr, const
       }
     }
   };
-  const bool vec = reinterpret_cast<uintptr_t>(tr) % 16 == 0 && v0 % EPV == 0 &&
-                   reinterpret_cast<uintptr_t>(nr) % 16 == 0 &&
-                   (!c.has_draft || reinterpret_cast<uintptr_t>(dr) % 16 == 0);
   int64_t from = v0;
+  // 16-byte aligned rows with maxima of ordinary size: pairs, through the ring
+  constexpr int W = E::kPerVec == 8 ? 1 : 2;  // vectors of 8 logits
+  constexpr int S = race_stages<T>(), R = race_vecs<T>();
+  const bool vec = (reinterpret_cast<uintptr_t>(tr + v0) | reinterpret_cast<uintptr_t>(nr + v0) |
+                    (c.has_draft ? reinterpret_cast<uintptr_t>(dr + v0) : 0)) % 16 == 0 &&
+                   !c.bigt && !(c.has_draft && c.bigd);
   if (vec) {
-    const int nvec = (int)((v1 - v0) / EPV);
-    for (int base = 0; base < nvec; base += kRaceThreads * U) {
-      uint4 dx[U], dy[U], de[U][kNoiseVecs];
+    const int n8 = (int)((v1 - v0) / 8);
+    const uint32_t mine = ring + 16 * tid;  // vector r of stage s: + (s * R + r) * kRaceThreads * 16
+    const T* tp = tr + v0;
+    const T* dp = c.has_draft ? dr + v0 : nullptr;
+    const float* np = nr + v0;
+    int ahead = tid;
+    auto issue = [&](int stage) {
+      if (ahead < n8) {
+        const uint32_t to = mine + stage * (R * kRaceThreads * 16);
 #pragma unroll
-      for (int w = 0; w < U; ++w) {
-        const int k = base + w * kRaceThreads + tid;
-        if (k < nvec) {
-          const int64_t v = v0 + (int64_t)k * EPV;
-          dx[w] = ld_stream(tr + v);
-          if (c.has_draft) dy[w] = ld_stream(dr + v);
-#pragma unroll
-          for (int h = 0; h < kNoiseVecs; ++h) de[w][h] = ld_stream(nr + v + 4 * h);
+        for (int k = 0; k < W; ++k) {
+          cp_async16(to + k * (kRaceThreads * 16), tp + (int64_t)ahead * 8 + k * E::kPerVec);
+          if (c.has_draft)
+            cp_async16(to + (W + k) * (kRaceThreads * 16), dp + (int64_t)ahead * 8 + k * E::kPerVec);
         }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          cp_async16(to + (2 * W + k) * (kRaceThreads * 16), np + (int64_t)ahead * 8 + 4 * k);
       }
-      float hi[U][EPV], top = 0.f;
+      cp_async_commit();
+      ahead += kRaceThreads;
+    };
+    auto at = [&](int stage, int r) {
+      return ld_shared_v4(mine + (stage * R + r) * (kRaceThreads * 16));
+    };
 #pragma unroll
-      for (int w = 0; w < U; ++w) {
-        const int k = base + w * kRaceThreads + tid;
-        float x[EPV], y[EPV], e[EPV];
-        E::unpack(dx[w], x);
-        if (c.has_draft) E::unpack(dy[w], y);
+    for (int k = 0; k < S; ++k) issue(k);
+    const uint64_t hi2 = f2_pack(c.t.hi, c.t.hi), lo2 = f2_pack(c.t.lo, c.t.lo);
+    const float nt1 = -(c.rt + c.lst), nd1 = -(c.rd + c.lsd);
+    const uint64_t nt = f2_pack(nt1, nt1), nd = f2_pack(nd1, nd1);
+    const int64_t skip = c.skip >= 0 ? c.skip - v0 : -1;
+    const int steps = (n8 + kRaceThreads - 1) / kRaceThreads;
+    int stage = 0;
+    for (int step = 0; step < steps; ++step) {
+      const int k = step * kRaceThreads + tid;
+      cp_async_wait<S - 1>();
+      float hi[8], top = 0.f, most = 0.f;
+      if (k < n8) {
+        float x[8], y[8], e[8];
 #pragma unroll
-        for (int h = 0; h < kNoiseVecs; ++h) Elt<float>::unpack(de[w][h], e + 4 * h);
-#pragma unroll
-        for (int l = 0; l < EPV; ++l) {
-          hi[w][l] = 0.f;
-          if (k < nvec && v0 + (int64_t)k * EPV + l != c.skip) {
-            float lo;
-            race_bounds(c, x[l], c.has_draft ? y[l] : 0.f, e[l], lo, hi[w][l]);
-            top = fmaxf(top, lo);
-          }
+        for (int q = 0; q < W; ++q) {
+          E::unpack(at(stage, q), x + q * E::kPerVec);
+          if (c.has_draft) E::unpack(at(stage, W + q), y + q * E::kPerVec);
         }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) Elt<float>::unpack(at(stage, 2 * W + q), e + 4 * q);
+        float lo[8];
+#pragma unroll
+        for (int q = 0; q < 8; q += 2) {
+          uint64_t l, h;
+          if (c.has_draft)
+            race_bounds2<true>(hi2, lo2, nt, nd, x[q], x[q + 1], y[q], y[q + 1], e[q], e[q + 1], l, h);
+          else
+            race_bounds2<false>(hi2, lo2, nt, nd, x[q], x[q + 1], 0.f, 0.f, e[q], e[q + 1], l, h);
+          f2_unpack(l, lo[q], lo[q + 1]);
+          f2_unpack(h, hi[q], hi[q + 1]);
+        }
+        if (skip >= 0 && skip / 8 == k) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (8 * (int64_t)k + q == skip) lo[q] = hi[q] = 0.f;
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          top = fmaxf(top, lo[q]);
+          most = fmaxf(most, hi[q]);
+        }
+        largest = fmaxf(largest, most);
       }
       const float bar = raise(top);
+      if (most >= bar) {
 #pragma unroll
-      for (int w = 0; w < U; ++w)
-#pragma unroll
-        for (int l = 0; l < EPV; ++l)
-          keep(hi[w][l], bar, v0 + (int64_t)(base + w * kRaceThreads + tid) * EPV + l);
+        for (int q = 0; q < 8; ++q) keep(hi[q], bar, v0 + 8 * (int64_t)k + q);
+      }
+      issue(stage);
+      stage = stage + 1 == S ? 0 : stage + 1;
     }
-    from = v0 + (int64_t)nvec * EPV;
+    cp_async_wait<0>();
+    from = v0 + (int64_t)n8 * 8;
   }
-  constexpr int W = 8;
-  for (int64_t base = from; base < v1; base += kRaceThreads * W) {
-    float hi[W], top = 0.f, x[W], y[W], e[W];
+  constexpr int M = 4;
+  for (int64_t base = from; base < v1; base += kRaceThreads * M) {
+    float hi[M], top = 0.f, x[M], y[M], e[M];
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
+    for (int w = 0; w < M; ++w) {
       const int64_t v = base + w * kRaceThreads + tid;
       if (v < v1) {
         x[w] = E::load1(tr + v);
@@ -564,7 +664,7 @@ __device__ Bounds race_bounds_of(const Racer& c, const T* tr, const T* dr, const
       }
     }
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
+    for (int w = 0; w < M; ++w) {
       const int64_t v = base + w * kRaceThreads + tid;
       hi[w] = 0.f;
       if (v < v1 && v != c.skip) {
@@ -572,10 +672,11 @@ __device__ Bounds race_bounds_of(const Racer& c, const T* tr, const T* dr, const
         race_bounds(c, x[w], y[w], e[w], lo, hi[w]);
         top = fmaxf(top, lo);
       }
+      largest = fmaxf(largest, hi[w]);
     }
     const float bar = raise(top);
 #pragma unroll
-    for (int w = 0; w < W; ++w) keep(hi[w], bar, base + w * kRaceThreads + tid);
+    for (int w = 0; w < M; ++w) keep(hi[w], bar, base + w * kRaceThreads + tid);
   }
   const unsigned wlargest = __reduce_max_sync(0xffffffffu, __float_as_uint(largest));
   if (lane == 0) atomicMax(&sh.top, (int)wlargest);
@@ -677,6 +778,7 @@ __device__ __forceinline__ void cluster_or_cta_sync(uint32_t ranks) {
 template <typename T>
 __global__ void __launch_bounds__(kRaceThreads, 2) verify_emit_kernel(
     const VerifyParams p, const T* __restrict__ target, const T* __restrict__ draft) {
+  extern __shared__ __align__(16) unsigned char emit_ring[];
   __shared__ __align__(16) Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_ctarank(), ranks = cluster_size();
@@ -744,21 +846,21 @@ __global__ void __launch_bounds__(kRaceThreads, 2) verify_emit_kernel(
   c.mt = d.mt;
   c.rt = ref_of(d.mt, t);
   c.bigt = is_big(d.mt);
-  c.it = 1.f / d.st;
+  c.lst = __log2f(d.st);
   c.st = d.st;
   c.md = d.md;
   c.rd = ref_of(d.md, t);
   c.bigd = is_big(d.md);
   c.sd = d.sd;
   c.has_draft = drow != nullptr;
-  c.id = 1.f / d.sd;
+  c.lsd = __log2f(d.sd);
   c.skip = draft == nullptr && !bonus ? d.token : -1;
   int64_t token = d.emit == 2 ? d.arg : -1;
   // The CTAs of the cluster pass the same barriers: what a further step
   // depends on comes from what they sent one another.
   for (int round = 0; round < 2; ++round) {
     Bounds own = {0.f, 0.f, -1, 0};
-    if (d.emit == 1) own = race_bounds_of(c, trow, drow, noise, v0, v1, sh);
+    if (d.emit == 1) own = race_bounds_of(c, trow, drow, noise, v0, v1, sh, smem_u32(emit_ring));
     if (tid < (int)ranks) {
       const uint32_t to = (uint32_t)tid;
       const float4 f = make_float4(own.lo, own.hi, __int_as_float(own.token), __int_as_float(own.count));
@@ -895,16 +997,20 @@ cudaError_t launch_t(const VerifyArgs& a, const DeviceInfo& d, cudaStream_t st) 
   }
   const T* target = static_cast<const T*>(a.target);
   const T* draft = static_cast<const T*>(a.draft);
-  e = launch_pdl(verify_rows_kernel<T>, dim3((unsigned)(rows * split)), dim3(kThreads), 0, st, 1,
-                 p, target, draft);
+  e = ensure_dynamic_smem((const void*)verify_rows_kernel<T>, (int)kRowRing);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(verify_rows_kernel<T>, dim3((unsigned)(rows * split)), dim3(kThreads), kRowRing,
+                 st, 1, p, target, draft);
   if (e != cudaSuccess) return e;
   // the emitting cluster: twice every SM, at least 8 KiB of logits per CTA
   int C = 1;
   while (C < kMaxCluster && a.N * C < 2 * (int64_t)d.sms && row_bytes / (2 * C) >= kMinPartBytes)
     C *= 2;
   p.chunk = ((a.V + C - 1) / C + EPV - 1) / EPV * EPV;
-  return launch_pdl(verify_emit_kernel<T>, dim3((unsigned)(a.N * C)), dim3(kRaceThreads), 0, st,
-                    (unsigned)C, p, target, draft);
+  e = ensure_dynamic_smem((const void*)verify_emit_kernel<T>, (int)race_ring<T>());
+  if (e != cudaSuccess) return e;
+  return launch_pdl(verify_emit_kernel<T>, dim3((unsigned)(a.N * C)), dim3(kRaceThreads),
+                    race_ring<T>(), st, (unsigned)C, p, target, draft);
 }
 
 }  // namespace
