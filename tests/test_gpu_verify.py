@@ -203,6 +203,28 @@ def test_residual_at_the_level_of_rounding():
     assert (out["n_accepted"] == 0).all()
 
 
+@pytest.mark.parametrize("V,at", [(64, 0), (5003, 17), (40000, 39999), (151936, 100)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_winner_with_a_residual_inside_the_bounds(V, at, sign):
+    """A token whose p and q differ by 4e-6 of themselves, which float32 bounds
+    cannot tell from 0, and whose noise makes it the winner by far (or, with
+    q above p, not a candidate at all)."""
+    c = case(3, 1, V, F32, 31, err=0.0)
+    c["z"].mul_(0.5)
+    c["y"] = c["z"][:, :1].clone()
+    c["y"][:, 0, at] -= sign * 4e-6
+    # the residual's ordinary mass, and the rejected token that pays for it:
+    # 2 exp(2) = exp(1) + exp(2.48988), so the sums stay equal
+    up, paid = (at + 3) % V, (at + 5) % V
+    c["z"][:, 0, up] = c["z"][:, 0, paid] = 2.0
+    c["y"][:, 0, up] = 1.0
+    c["y"][:, 0, paid] = 2.48988012564475
+    c["x"].fill_(paid)
+    c["u"].fill_(0.999)
+    c["noise"][:, at] = 1e-12
+    both(c)
+
+
 def test_no_residual_falls_back_to_the_target():
     """Copied draft of the only possible token, rejected by a NaN random number."""
     z = torch.full((2, 2, 64), -math.inf, device="cuda")

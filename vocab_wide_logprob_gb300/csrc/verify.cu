@@ -82,10 +82,26 @@ __device__ __forceinline__ float rescale(float m1, float m2, const Temper& t) {
   if (is_big(m1) || is_big(m2)) return ex2((m1 - m2) * t.hi);
   return ex2(ref_of(m1, t) - ref_of(m2, t));
 }
-__device__ __forceinline__ void merge(float& m, float& s, float m2, float s2, const Temper& t) {
-  const float M = fmaxf(m, m2);
-  // a NaN sum stays; an empty part (max -inf) has sum 0 or NaN
-  s = s * rescale(m, M, t) + s2 * rescale(m2, M, t);
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ int64_t warp_min(int64_t x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = min(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+// The lanes' parts (m, s) of a row as one, in every lane.  A NaN sum stays; an
+// empty part has m = -inf and s = 0.
+__device__ __forceinline__ void warp_merge(float& m, float& s, const Temper& t) {
+  const float M = warp_max(m);
+  s = warp_sum(s * rescale(m, M, t));
   m = M;
 }
 // natural log of a weight in float64 (p is weight / sum)
@@ -110,10 +126,11 @@ struct VerifyParams {
   float* logp;
   WsHeader* hdr;
   uint32_t* status;   // [N]
-  // (max, sum) of part s of target row (j, i) at [(j * N + i) * split + s]; the
-  // draft rows' after all of those.  arg: where a greedy target row has its
-  // maximum first.
+  // (reference, sum) of part s of target row (j, i) at [(j * N + i) * split + s];
+  // the draft rows' after all of those.  top, arg: a greedy target row's
+  // maximum and where it is first.
   float2* part;
+  float* top;
   int64_t* arg;
   float* picked;      // the drafted tokens' logits, in the order of the rows
   int32_t* rejected;  // [N]: a position at which the sequence is known to stop
@@ -142,132 +159,166 @@ struct Decision {
   uint32_t flags;
 };
 
-struct RowStat {
-  float m, s;
-  int64_t arg;
-};
-
 // The rows kernel streams a row through shared memory: every thread copies its
 // own 16-byte vectors kRowStages batches ahead (asynchronous copies, read back
 // by the thread that issued them: no barrier, no registers).
 constexpr int kRowVecs = 4;  // vectors of a batch, per thread
 constexpr int kRowStages = 3;
 constexpr size_t kRowRing = (size_t)kRowStages * kRowVecs * kThreads * 16;
+// A warp's reference follows its maximum only when a value is this much above
+// it (as an exponent of 2: weights up to 16, no loss): nearly never after the
+// first batch.
+constexpr float kRefSlack = 4.f;
 
-// (max, sum) of one CTA's slice [v0, v1) of a row, per thread; with kArg also
-// where the thread saw its maximum first.
+// One warp's share of a row: reference m and sum, in every lane; with kArg
+// also the exact maximum and its lowest index.
+struct RowStat {
+  float m, s, top;
+  int64_t arg;
+};
+
+// Over the slice [v0, v1) of a row, by all warps of the CTA.
 template <typename T, bool kArg>
 __device__ __forceinline__ RowStat row_stats(const T* row, int64_t v0, int64_t v1,
                                              const Temper& t, uint32_t ring) {
   using E = Elt<T>;
   constexpr int EPV = E::kPerVec;
   constexpr int U = kRowVecs;
+  constexpr uint32_t kAll = 0xffffffffu;
   const int tid = threadIdx.x;
-  RowStat r;
-  r.m = -INFINITY;
-  r.s = 0.f;
-  r.arg = INT64_MAX;
-  if (v0 >= v1) return r;
   const uintptr_t addr = reinterpret_cast<uintptr_t>(row + v0);
   const int64_t a =
-      min(v0 + (int64_t)(((16u - (unsigned)(addr & 15u)) & 15u) / sizeof(T)), v1);
-  const int nvec = (int)((v1 - a) / EPV);
+      min(v0 + (int64_t)(((16u - (unsigned)(addr & 15u)) & 15u) / sizeof(T)), max(v0, v1));
+  const int nvec = (int)((max(a, v1) - a) / EPV);
   const int64_t b = a + (int64_t)nvec * EPV;
-  float m = -INFINITY, edge_s = 0.f;
-  int where = -1;  // first vector of the batch that holds the maximum
+  const int batches = (nvec + kThreads * U - 1) / (kThreads * U);
+
+  float m = -INFINITY, above = -INFINITY;  // the warp's reference; what moves it
+  float edge_s = 0.f, top = -INFINITY;
+  int where = -1;  // first vector of the batch that holds the thread's maximum
   uint64_t acc01 = f2_pack(0.f, 0.f), acc23 = f2_pack(0.f, 0.f);
   const uint64_t hi2 = f2_pack(t.hi, t.hi), lo2 = f2_pack(t.lo, t.lo);
-  // the ragged head and tail, at most one element of each per thread
-  int64_t he = -1, te = -1;
-  if (tid < a - v0) he = v0 + tid;
-  if (tid < v1 - b) te = b + tid;
-  auto one = [&](int64_t e) {
-    const float x = E::load1(row + e);
-    if (x > m) {
-      const float sc = rescale(m, x, t);
-      const uint64_t sc2 = f2_pack(sc, sc);
-      acc01 = f2_mul(acc01, sc2);
-      acc23 = f2_mul(acc23, sc2);
-      edge_s *= sc;
-      m = x;
-      if (kArg) r.arg = e;
-      where = -1;
-    }
-    if (x != -INFINITY) edge_s += ex2(exponent(x, m, ref_of(m, t), is_big(m), t));
+  auto adopt = [&](float x) {  // the whole warp
+    const float M = warp_max(fmaxf(x, m));
+    const float sc = rescale(m, M, t);
+    acc01 = f2_mul(acc01, f2_pack(sc, sc));
+    acc23 = f2_mul(acc23, f2_pack(sc, sc));
+    edge_s *= sc;
+    m = M;
+    above = is_big(M) ? M : M + __fdividef(kRefSlack, t.hi);
   };
-  const uint32_t mine = ring + 16 * tid;  // vector u of stage s: + (s * U + u) * kThreads * 16
-  int ahead = tid;
-  auto issue = [&](int stage) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = ahead + u * kThreads;
-      if (k < nvec) cp_async16(mine + (stage * U + u) * (kThreads * 16), row + a + (int64_t)k * EPV);
-    }
-    cp_async_commit();
-    ahead += kThreads * U;
-  };
-#pragma unroll
-  for (int k = 0; k < kRowStages; ++k) issue(k);
-  if (he >= 0) one(he);
-  int stage = 0;
-  for (int base = tid; base < nvec; base += kThreads * U) {
-    cp_async_wait<kRowStages - 1>();
-    uint4 d[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      d[u] = base + u * kThreads < nvec
-                 ? ld_shared_v4(mine + (stage * U + u) * (kThreads * 16))
-                 : make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf);
+  auto consume = [&](const uint4* d, int base) {
     const float bm = E::template batch_max<U>(d);
-    if (bm > m) {
-      const float sc = rescale(m, bm, t);
-      const uint64_t sc2 = f2_pack(sc, sc);
-      acc01 = f2_mul(acc01, sc2);
-      acc23 = f2_mul(acc23, sc2);
-      edge_s *= sc;
-      m = bm;
+    if (__any_sync(kAll, bm > above)) adopt(bm);
+    if (kArg && bm > top) {
+      top = bm;
       where = base;
     }
-    float x[U * EPV];
-#pragma unroll
-    for (int u = 0; u < U; ++u) E::unpack(d[u], x + u * EPV);
     if (!is_big(m)) {
       const float nr = -ref_of(m, t);
       const uint64_t nr2 = f2_pack(nr, nr);
 #pragma unroll
-      for (int k = 0; k < U * EPV; k += 4) {
-        const uint64_t x01 = f2_pack(x[k], x[k + 1]), x23 = f2_pack(x[k + 2], x[k + 3]);
-        acc01 = f2_add(acc01, f2_ex2(f2_fma(x01, lo2, f2_fma(x01, hi2, nr2))));
-        acc23 = f2_add(acc23, f2_ex2(f2_fma(x23, lo2, f2_fma(x23, hi2, nr2))));
-      }
-    } else if (m == -INFINITY) {  // nothing but -inf so far, or NaN
+      for (int u = 0; u < U; ++u) {
+        float x[EPV];
+        E::unpack(d[u], x);
 #pragma unroll
-      for (int k = 0; k < U * EPV; ++k)
-        if (x[k] != x[k]) edge_s = x[k];
+        for (int k = 0; k < EPV; k += 4) {
+          const uint64_t x01 = f2_pack(x[k], x[k + 1]), x23 = f2_pack(x[k + 2], x[k + 3]);
+          acc01 = f2_add(acc01, f2_ex2(f2_fma(x01, lo2, f2_fma(x01, hi2, nr2))));
+          acc23 = f2_add(acc23, f2_ex2(f2_fma(x23, lo2, f2_fma(x23, hi2, nr2))));
+        }
+      }
+    } else {  // extreme values, or nothing but -inf and NaN so far
+#pragma unroll 1
+      for (int u = 0; u < U; ++u) {
+        float x[EPV];
+        E::unpack(u == 0 ? d[0] : u == 1 ? d[1] : u == 2 ? d[2] : d[3], x);
+#pragma unroll
+        for (int k = 0; k < EPV; ++k)
+          if (x[k] != -INFINITY) edge_s += ex2(exponent(x[k], m, 0.f, true, t));
+      }
+    }
+  };
+  static_assert(U == 4, "the slow path names the vectors");
+
+  const uint32_t mine = ring + 16 * tid;  // vector u of stage s: + (s * U + u) * kThreads * 16
+  const T* src = row + a + (int64_t)tid * EPV;
+  int ahead = 0;  // batches issued
+  auto issue = [&](int stage) {
+    const int base = ahead * (kThreads * U) + tid;
+    const T* q = src + (int64_t)ahead * (kThreads * U * EPV);
+    const uint32_t to = mine + stage * (U * kThreads * 16);
+    if (base - tid + kThreads * U <= nvec) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) cp_async16(to + u * (kThreads * 16), q + u * (kThreads * EPV));
     } else {
 #pragma unroll
-      for (int k = 0; k < U * EPV; ++k) edge_s += ex2(exponent(x[k], m, 0.f, true, t));
+      for (int u = 0; u < U; ++u)
+        if (base + u * kThreads < nvec) cp_async16(to + u * (kThreads * 16), q + u * (kThreads * EPV));
     }
-    issue(stage);  // (the batch is in registers)
+    cp_async_commit();
+    ++ahead;
+  };
+#pragma unroll
+  for (int k = 0; k < kRowStages; ++k) issue(k);
+  int stage = 0;
+  for (int n = 0; n < batches; ++n) {
+    cp_async_wait<kRowStages - 1>();
+    const int base = n * (kThreads * U) + tid;
+    const uint32_t at = mine + stage * (U * kThreads * 16);
+    uint4 d[U];
+    if (base - tid + kThreads * U <= nvec) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) d[u] = ld_shared_v4(at + u * (kThreads * 16));
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        d[u] = base + u * kThreads < nvec
+                   ? ld_shared_v4(at + u * (kThreads * 16))
+                   : make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf);
+    }
+    consume(d, base);
+    issue(stage);  // (the batch was in registers)
     stage = stage + 1 == kRowStages ? 0 : stage + 1;
   }
   cp_async_wait<0>();
-  if (te >= 0) one(te);
-  if (kArg && where >= 0) {  // the batch's first element at the maximum
-    r.arg = INT64_MAX;
-    for (int u = U - 1; u >= 0; --u) {
-      const int k = where + u * kThreads;
-      if (k < nvec)
-        for (int e = EPV - 1; e >= 0; --e)
-          if (E::load1(row + a + (int64_t)k * EPV + e) == m) r.arg = a + (int64_t)k * EPV + e;
+
+  // the ragged ends: the first warp, at most one element of each per lane
+  float xh = -INFINITY, xt = -INFINITY;
+  if (tid < 32) {
+    if (v0 + tid < a) xh = E::load1(row + v0 + tid);
+    if (b + tid < v1) xt = E::load1(row + b + tid);
+    const float bm = fmaxf(xh, xt);
+    if (__any_sync(kAll, bm > above)) adopt(bm);
+    const float r = ref_of(m, t);
+    if (xh != -INFINITY) edge_s += ex2(exponent(xh, m, r, is_big(m), t));
+    if (xt != -INFINITY) edge_s += ex2(exponent(xt, m, r, is_big(m), t));
+  }
+  RowStat out;
+  out.arg = INT64_MAX;
+  out.top = top;
+  if (kArg) {
+    out.top = warp_max(fmaxf(top, fmaxf(xh, xt)));
+    if (out.top > -INFINITY) {  // the thread's first element at the maximum
+      if (xt == out.top) out.arg = b + tid;
+      if (where >= 0 && top == out.top)
+        for (int u = U - 1; u >= 0; --u) {
+          const int k = where + u * kThreads;
+          if (k < nvec)
+            for (int e = EPV - 1; e >= 0; --e)
+              if (E::load1(row + a + (int64_t)k * EPV + e) == out.top)
+                out.arg = a + (int64_t)k * EPV + e;
+        }
+      if (xh == out.top) out.arg = v0 + tid;
     }
+    out.arg = warp_min(out.arg);
   }
   float a0, a1, a2, a3;
   f2_unpack(acc01, a0, a1);
   f2_unpack(acc23, a2, a3);
-  r.m = m;
-  r.s = edge_s + ((a0 + a1) + (a2 + a3));
-  return r;
+  out.m = m;
+  out.s = warp_sum(edge_s + ((a0 + a1) + (a2 + a3)));
+  return out;
 }
 
 // Position j of sequence i, by one warp: the lanes take the parts of the
@@ -287,6 +338,7 @@ __device__ __forceinline__ void decide(const VerifyParams& p, bool has_draft, in
   d.mt = d.md = -INFINITY;
   d.st = d.sd = 0.f;
   d.arg = INT64_MAX;
+  float top = -INFINITY;
   if (lane < p.split) {
     const float2 v = __ldcg(p.part + trow * p.split + lane);
     d.mt = v.x;
@@ -296,7 +348,10 @@ __device__ __forceinline__ void decide(const VerifyParams& p, bool has_draft, in
       d.md = w.x;
       d.sd = w.y;
     }
-    if (greedy) d.arg = __ldcg(p.arg + trow * p.split + lane);
+    if (greedy) {
+      top = __ldcg(p.top + trow * p.split + lane);
+      d.arg = __ldcg(p.arg + trow * p.split + lane);
+    }
   }
   float xt = 0.f, xd = 0.f, u = 0.f;
   if (!bonus) {
@@ -309,21 +364,9 @@ __device__ __forceinline__ void decide(const VerifyParams& p, bool has_draft, in
     else
       d.flags |= kFlagTokenRange;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, d.mt, o);
-    const float s2 = __shfl_xor_sync(0xffffffffu, d.st, o);
-    if (greedy) {
-      const int64_t a2 = __shfl_xor_sync(0xffffffffu, d.arg, o);
-      d.arg = m2 > d.mt ? a2 : (m2 == d.mt ? min(d.arg, a2) : d.arg);
-    }
-    merge(d.mt, d.st, m2, s2, t);
-    if (use_draft) {
-      const float m3 = __shfl_xor_sync(0xffffffffu, d.md, o);
-      const float s3 = __shfl_xor_sync(0xffffffffu, d.sd, o);
-      merge(d.md, d.sd, m3, s3, t);
-    }
-  }
+  warp_merge(d.mt, d.st, t);
+  if (use_draft) warp_merge(d.md, d.sd, t);
+  if (greedy) d.arg = warp_min(top == warp_max(top) ? d.arg : INT64_MAX);
   bool defined = Ti >= 0.f && Ti <= 3.4e38f && d.mt > -INFINITY && d.mt < INFINITY &&
                  d.st > 0.f && d.st < INFINITY;
   if (use_draft)
@@ -355,25 +398,35 @@ __device__ __forceinline__ void decide(const VerifyParams& p, bool has_draft, in
   }
 }
 
-// One row part per CTA.  Grid order: positions, then kinds (target, draft),
-// then sequences, then parts.
+// One row part per CTA.  Grid order: positions, then sequences, then kinds
+// (target, draft), then parts, so that a position's decision is known before
+// the next position's CTAs begin.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) verify_rows_kernel(const VerifyParams p,
                                                                   const T* __restrict__ target,
                                                                   const T* __restrict__ draft) {
   extern __shared__ __align__(16) unsigned char row_ring[];
   __shared__ float2 s_red[kWarps];
+  __shared__ float s_top[kWarps];
   __shared__ int64_t s_arg[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
-  const int s = (int)(blockIdx.x % (unsigned)p.split);
-  int64_t q = blockIdx.x / (unsigned)p.split;
-  const int64_t i = q % p.N;
-  q /= p.N;
-  const int kinds = draft != nullptr ? 2 : 1;
-  const int64_t j = q / kinds;
-  const bool is_draft = q % kinds == 1;
+  unsigned q = blockIdx.x;
+  const int s = (int)(q % (unsigned)p.split);
+  q /= (unsigned)p.split;
+  bool is_draft = false;
+  if (draft != nullptr) {
+    // (the last position has no draft rows)
+    const unsigned pairs = (unsigned)(2 * p.N * p.K);
+    if (q < pairs) {
+      is_draft = q & 1;
+      q >>= 1;
+    } else {
+      q -= pairs / 2;
+    }
+  }
+  const int64_t j = q / (unsigned)p.N, i = q % (unsigned)p.N;
   uint32_t flags = 0;
   const int32_t len = clamped_len(p, i, &flags);
   const float Ti = temperature_of(p, i);
@@ -386,38 +439,33 @@ __global__ void __launch_bounds__(kThreads, 4) verify_rows_kernel(const VerifyPa
   int64_t x = -1;  // the drafted token, if this part holds its logit
   if (tid == 0 && j < len) x = p.tokens[i * p.K + j];
   const uint32_t ring = smem_u32(row_ring);
-  RowStat r = greedy ? row_stats<T, true>(row, v0, v1, t, ring)
-                     : row_stats<T, false>(row, v0, v1, t, ring);
+  const RowStat r = greedy ? row_stats<T, true>(row, v0, v1, t, ring)
+                           : row_stats<T, false>(row, v0, v1, t, ring);
   float picked = 0.f;
   if (x >= v0 && x < v1) picked = Elt<T>::load1(row + x);
-  for (int o = 16; o > 0; o >>= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, r.m, o);
-    const float s2 = __shfl_xor_sync(0xffffffffu, r.s, o);
-    if (greedy) {
-      const int64_t a2 = __shfl_xor_sync(0xffffffffu, r.arg, o);
-      r.arg = m2 > r.m ? a2 : (m2 == r.m ? min(r.arg, a2) : r.arg);
-    }
-    merge(r.m, r.s, m2, s2, t);
-  }
   if (lane == 0) {
     s_red[warp] = make_float2(r.m, r.s);
+    s_top[warp] = r.top;
     s_arg[warp] = r.arg;
   }
   __syncthreads();
   if (warp != 0) return;
+  float m = lane < kWarps ? s_red[lane].x : -INFINITY;
+  float sum = lane < kWarps ? s_red[lane].y : 0.f;
+  warp_merge(m, sum, t);
+  const int64_t at = (((is_draft ? p.K + 1 : 0) + j) * p.N + i) * p.split + s;
+  if (greedy) {
+    const float top = lane < kWarps ? s_top[lane] : -INFINITY, M = warp_max(top);
+    const int64_t arg = warp_min(lane < kWarps && top == M ? s_arg[lane] : INT64_MAX);
+    if (lane == 0) {
+      p.top[at] = M;
+      p.arg[at] = arg;
+    }
+  }
   uint32_t last = 0;
   if (lane == 0) {
-    float m = s_red[0].x, sum = s_red[0].y;
-    int64_t arg = s_arg[0];
-    for (int k = 1; k < kWarps; ++k) {
-      const float2 o = s_red[k];
-      arg = o.x > m ? s_arg[k] : (o.x == m ? min(arg, s_arg[k]) : arg);
-      merge(m, sum, o.x, o.y, t);
-    }
-    const int64_t row_at = ((is_draft ? p.K + 1 : 0) + j) * p.N + i;
-    p.part[row_at * p.split + s] = make_float2(m, sum);
-    if (greedy) p.arg[row_at * p.split + s] = arg;
-    if (x >= v0 && x < v1) p.picked[row_at] = picked;
+    p.part[at] = make_float2(m, sum);
+    if (x >= v0 && x < v1) p.picked[at / p.split] = picked;
     if (p.lazy && j < len) {
       const uint32_t expect = (uint32_t)(p.split * (draft != nullptr && !greedy ? 2 : 1));
       __threadfence();
@@ -489,34 +537,38 @@ __device__ __forceinline__ void better(double& s, int64_t& at, double s2, int64_
   }
 }
 
+// 1 / x on the special-function unit (2^-23; infinite for 0).
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // Lower and upper bound of a score, any row.
 __device__ __forceinline__ void race_bounds(const Racer& c, float x, float y, float e, float& lo,
                                             float& hi) {
   const float p = ex2(exponent(x, c.mt, c.rt, c.bigt, c.t) - c.lst);
   const float q = c.has_draft ? ex2(exponent(y, c.md, c.rd, c.bigd, c.t) - c.lsd) : 0.f;
-  const float w = __fdividef(1.f, e), d = p - q, s = p + q;
+  const float w = rcp(e), d = p - q, s = p + q;
   lo = fmaf(s, -kRaceMargin, d) * w;
   hi = fmaf(s, kRaceMargin, d) * w;
 }
-// The same for a pair of elements of rows whose maxima are not extreme:
+// The upper bounds of a pair of elements of rows whose maxima are not extreme:
 // nt and nd are minus the reference exponents and the log2 of the sums.
 template <bool kDraft>
-__device__ __forceinline__ void race_bounds2(uint64_t hi2, uint64_t lo2, uint64_t nt, uint64_t nd,
-                                             float x0, float x1, float y0, float y1, float e0,
-                                             float e1, uint64_t& lo, uint64_t& hi) {
+__device__ __forceinline__ uint64_t race_upper2(uint64_t hi2, uint64_t lo2, uint64_t nt,
+                                                uint64_t nd, float x0, float x1, float y0,
+                                                float y1, float e0, float e1) {
   const uint64_t x = f2_pack(x0, x1);
   const uint64_t p = f2_ex2(f2_fma(x, lo2, f2_fma(x, hi2, nt)));
-  const uint64_t w = f2_pack(__fdividef(1.f, e0), __fdividef(1.f, e1));
-  const uint64_t up = f2_pack(kRaceMargin, kRaceMargin), dn = f2_pack(-kRaceMargin, -kRaceMargin);
-  uint64_t d = p, s = p;
+  const uint64_t w = f2_pack(rcp(e0), rcp(e1));
+  const uint64_t up = f2_pack(1.f + kRaceMargin, 1.f + kRaceMargin);
+  uint64_t h = f2_mul(p, up);  // p (1 + margin) - q (1 - margin)
   if (kDraft) {
     const uint64_t y = f2_pack(y0, y1);
     const uint64_t q = f2_ex2(f2_fma(y, lo2, f2_fma(y, hi2, nd)));
-    d = f2_fma(q, f2_pack(-1.f, -1.f), p);
-    s = f2_add(p, q);
+    h = f2_fma(q, f2_pack(kRaceMargin - 1.f, kRaceMargin - 1.f), h);
   }
-  lo = f2_mul(f2_fma(s, dn, d), w);
-  hi = f2_mul(f2_fma(s, up, d), w);
+  return f2_mul(h, w);
 }
 
 // The race streams its rows as the rows kernel does: 8 elements per thread and
@@ -545,7 +597,7 @@ __device__ Bounds race_bounds_of(const Racer& c, const T* tr, const T* dr, const
     sh.count = 0;
   }
   __syncthreads();
-  float largest = 0.f;  // upper bound
+  float largest = 0.f;  // upper bound (that of a skipped token too: it only asks for the exact race)
   // the CTA's best lower bound, raised by this warp's
   auto raise = [&](float top) -> float {
     const unsigned wtop = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
@@ -555,7 +607,9 @@ __device__ Bounds race_bounds_of(const Racer& c, const T* tr, const T* dr, const
     return __uint_as_float(wtop);
   };
   auto keep = [&](float hi, float bar, int64_t v) {
-    if (hi >= bar && hi > 0.f && bar > 0.f) {
+    // (with no lower bound yet, everything that may have mass: its own lower
+    // bound may be 0 where p and q are close, and its score still the largest)
+    if (hi >= bar && hi > 0.f) {
       const int s = atomicAdd(&sh.count, 1);
       if (s < kCandidates) {
         sh.cand[s] = (int32_t)v;
@@ -604,12 +658,13 @@ __device__ Bounds race_bounds_of(const Racer& c, const T* tr, const T* dr, const
     const int64_t skip = c.skip >= 0 ? c.skip - v0 : -1;
     const int steps = (n8 + kRaceThreads - 1) / kRaceThreads;
     int stage = 0;
+    float bar = 0.f;
     for (int step = 0; step < steps; ++step) {
       const int k = step * kRaceThreads + tid;
       cp_async_wait<S - 1>();
-      float hi[8], top = 0.f, most = 0.f;
+      float most = 0.f;
+      float x[8], y[8], e[8];
       if (k < n8) {
-        float x[8], y[8], e[8];
 #pragma unroll
         for (int q = 0; q < W; ++q) {
           E::unpack(at(stage, q), x + q * E::kPerVec);
@@ -617,33 +672,36 @@ __device__ Bounds race_bounds_of(const Racer& c, const T* tr, const T* dr, const
         }
 #pragma unroll
         for (int q = 0; q < 2; ++q) Elt<float>::unpack(at(stage, 2 * W + q), e + 4 * q);
-        float lo[8];
 #pragma unroll
         for (int q = 0; q < 8; q += 2) {
-          uint64_t l, h;
-          if (c.has_draft)
-            race_bounds2<true>(hi2, lo2, nt, nd, x[q], x[q + 1], y[q], y[q + 1], e[q], e[q + 1], l, h);
-          else
-            race_bounds2<false>(hi2, lo2, nt, nd, x[q], x[q + 1], 0.f, 0.f, e[q], e[q + 1], l, h);
-          f2_unpack(l, lo[q], lo[q + 1]);
-          f2_unpack(h, hi[q], hi[q + 1]);
-        }
-        if (skip >= 0 && skip / 8 == k) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            if (8 * (int64_t)k + q == skip) lo[q] = hi[q] = 0.f;
-        }
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          top = fmaxf(top, lo[q]);
-          most = fmaxf(most, hi[q]);
+          const uint64_t h = c.has_draft
+                                 ? race_upper2<true>(hi2, lo2, nt, nd, x[q], x[q + 1], y[q],
+                                                     y[q + 1], e[q], e[q + 1])
+                                 : race_upper2<false>(hi2, lo2, nt, nd, x[q], x[q + 1], 0.f, 0.f,
+                                                      e[q], e[q + 1]);
+          float h0, h1;
+          f2_unpack(h, h0, h1);
+          most = fmaxf(most, fmaxf(h0, h1));
         }
         largest = fmaxf(largest, most);
       }
-      const float bar = raise(top);
-      if (most >= bar) {
+      // an upper bound above everything so far: both bounds, one by one
+      if (__any_sync(0xffffffffu, most > 0.f && most >= bar)) {
+        float hi[8], top = 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          hi[q] = 0.f;
+          if (k < n8 && 8 * (int64_t)k + q != skip) {
+            float lo;
+            race_bounds(c, x[q], c.has_draft ? y[q] : 0.f, e[q], lo, hi[q]);
+            top = fmaxf(top, lo);
+          }
+        }
+        bar = raise(top);
 #pragma unroll
         for (int q = 0; q < 8; ++q) keep(hi[q], bar, v0 + 8 * (int64_t)k + q);
+      } else {
+        bar = fmaxf(bar, __int_as_float(*(volatile int*)&sh.best));
       }
       issue(stage);
       stage = stage + 1 == S ? 0 : stage + 1;
@@ -923,7 +981,7 @@ __global__ void __launch_bounds__(kRaceThreads, 2) verify_emit_kernel(
 }
 
 struct VerifyLayout {
-  size_t status, part, arg, picked, rejected, ticket, total;
+  size_t status, part, top, arg, picked, rejected, ticket, total;
 };
 VerifyLayout verify_layout(int64_t N, int64_t K) {
   VerifyLayout l;
@@ -936,6 +994,7 @@ VerifyLayout verify_layout(int64_t N, int64_t K) {
   };
   l.status = take(4 * n);
   l.part = take(2 * rows * kMaxSplit * sizeof(float2));
+  l.top = take(rows * kMaxSplit * sizeof(float));
   l.arg = take(rows * kMaxSplit * sizeof(int64_t));
   l.picked = take(2 * rows * sizeof(float));
   l.rejected = take(4 * n);
@@ -979,6 +1038,7 @@ cudaError_t launch_t(const VerifyArgs& a, const DeviceInfo& d, cudaStream_t st) 
   p.hdr = reinterpret_cast<WsHeader*>(ws);
   p.status = reinterpret_cast<uint32_t*>(ws + l.status);
   p.part = reinterpret_cast<float2*>(ws + l.part);
+  p.top = reinterpret_cast<float*>(ws + l.top);
   p.arg = reinterpret_cast<int64_t*>(ws + l.arg);
   p.picked = reinterpret_cast<float*>(ws + l.picked);
   p.rejected = reinterpret_cast<int32_t*>(ws + l.rejected);
@@ -1002,9 +1062,11 @@ cudaError_t launch_t(const VerifyArgs& a, const DeviceInfo& d, cudaStream_t st) 
   e = launch_pdl(verify_rows_kernel<T>, dim3((unsigned)(rows * split)), dim3(kThreads), kRowRing,
                  st, 1, p, target, draft);
   if (e != cudaSuccess) return e;
-  // the emitting cluster: twice every SM, at least 8 KiB of logits per CTA
+  // the emitting cluster: as many CTAs as the GPU takes at once (two per SM),
+  // of at least 8 KiB of logits each
   int C = 1;
-  while (C < kMaxCluster && a.N * C < 2 * (int64_t)d.sms && row_bytes / (2 * C) >= kMinPartBytes)
+  while (C < kMaxCluster && a.N * 2 * C <= 2 * (int64_t)d.sms &&
+         row_bytes / (2 * C) >= kMinPartBytes)
     C *= 2;
   p.chunk = ((a.V + C - 1) / C + EPV - 1) / EPV * EPV;
   e = ensure_dynamic_smem((const void*)verify_emit_kernel<T>, (int)race_ring<T>());
