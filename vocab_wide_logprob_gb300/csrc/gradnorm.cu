@@ -230,22 +230,31 @@ __global__ void __launch_bounds__(kThreads, 4) grad_scale_kernel(const __grid_co
                                                               float max_norm, float eps,
                                                               int copies, float* stats,
                                                               WsHeader* hdr) {
-  __shared__ double s_red[kWarps];
+  __shared__ float s_coef;
   pdl_wait();
   pdl_trigger();
-  double s = 0.0;
-  for (int k = threadIdx.x; k < npartial; k += kThreads) s = combine(s, partial[k], kMax);
-  s = block_reduce<kMax>(s, s_red);
-  const double norm = kMax ? s : sqrt(s);
-  double c = (double)max_norm / (norm + (double)eps);
-  c = c > 1.0 ? 1.0 : c;                     // keeps NaN
-  if (isinf(max_norm)) c = 1.0;              // no limit
-  const float coef = (float)c;
-  if (stats != nullptr && blockIdx.x == 0 && threadIdx.x == 0) {
-    stats[0] = (float)norm;
-    stats[1] = coef;
-    hdr->flags = isfinite((float)norm) ? 0u : kFlagValue;
+  // one warp: a float64 instruction occupies its pipe for many cycles here,
+  // whatever the number of warps that issue it
+  if (threadIdx.x < 32) {
+    double s = 0.0;
+#pragma unroll 8
+    for (int k = threadIdx.x; k < npartial; k += 32) s = combine(s, partial[k], kMax);
+    for (int o = 16; o > 0; o >>= 1) s = combine(s, __shfl_xor_sync(0xffffffffu, s, o), kMax);
+    const double norm = kMax ? s : sqrt(s);
+    double c = (double)max_norm / (norm + (double)eps);
+    c = c > 1.0 ? 1.0 : c;         // keeps NaN
+    if (isinf(max_norm)) c = 1.0;  // no limit
+    if (threadIdx.x == 0) {
+      s_coef = (float)c;
+      if (stats != nullptr && blockIdx.x == 0) {
+        stats[0] = (float)norm;
+        stats[1] = (float)c;
+        hdr->flags = isfinite((float)norm) ? 0u : kFlagValue;
+      }
+    }
   }
+  __syncthreads();
+  const float coef = s_coef;
   if (coef == 1.f && !copies) return;
   const int64_t chunks = t.first[t.count];
   for (int64_t r = blockIdx.x; r < chunks; r += gridDim.x) {
@@ -305,7 +314,7 @@ cudaError_t clip_launch(const ClipArgs& a, const GradTensor* g, int count, int p
                       1, t, partial + part0);
   bool copies = false;
   for (int k = 0; k < count; ++k) copies |= g[k].out != g[k].data;
-  int64_t grid = 8 * (int64_t)d.sms;
+  int64_t grid = 4 * (int64_t)d.sms;  // as many as are resident
   if (grid > chunks) grid = chunks;
   if (grid < 1 || a.norm_only) grid = 1;
   if (a.norm_only) t.first[count] = 0;

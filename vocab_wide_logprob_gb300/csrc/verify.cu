@@ -46,18 +46,25 @@ constexpr double kLn2 = 0.69314718055994530942;
 // from the exponent's rounding at 60 bits, ex2 and the products), with room
 constexpr float kRaceMargin = 1e-5f;
 
+// 1 / x on the special-function unit (2^-23; infinite for 0).
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // exp(x / T) = 2^(x c), c = log2(e) / T kept as c_hi + c_lo with c_lo > 0 (so
 // that -inf stays -inf in both steps).
-// The split is made in float32 (this GPU has few float64 units): the quotient
-// of log2(e)'s leading part rounded down, and what is left of it.
+// The split is made in float32 (this GPU has few float64 units): a quotient
+// of log2(e)'s leading part that is a little too small, and what is left.
 struct Temper {
   float hi, lo;
 };
 __device__ __forceinline__ Temper temper(float T) {
   constexpr float kHead = 1.44269502162933349609375f, kTail = 1.92596299112661746887e-8f;
   Temper t;
-  t.hi = __fdiv_rd(kHead, T);
-  t.lo = fmaxf((fmaf(-t.hi, T, kHead) + kTail) / T, 1e-37f);
+  const float inv = rcp(T);  // good to 2^-23
+  t.hi = kHead * inv * (1.f - 0x1p-21f);
+  t.lo = fmaxf((fmaf(-t.hi, T, kHead) + kTail) * inv, 1e-37f);
   return t;
 }
 __device__ __forceinline__ double temper64(const Temper& t) { return (double)t.hi + (double)t.lo; }
@@ -135,7 +142,7 @@ struct VerifyParams {
   float* picked;      // the drafted tokens' logits, in the order of the rows
   int32_t* rejected;  // [N]: a position at which the sequence is known to stop
   uint32_t* ticket;   // [K * N]: CTAs done with a position's rows
-  int split;          // CTAs per row
+  int split, split_log2;  // CTAs per row, a power of two
   int64_t part_elems; // elements of a row per CTA
   int lazy;           // rows behind a known rejection are left out
   int64_t chunk;      // elements of a row per CTA of the emitting cluster
@@ -413,8 +420,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_rows_kernel(const VerifyPa
   pdl_wait();
   pdl_trigger();
   unsigned q = blockIdx.x;
-  const int s = (int)(q % (unsigned)p.split);
-  q /= (unsigned)p.split;
+  const int s = (int)(q & (unsigned)(p.split - 1));  // (a power of two)
+  q >>= p.split_log2;
   bool is_draft = false;
   if (draft != nullptr) {
     // (the last position has no draft rows)
@@ -426,7 +433,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_rows_kernel(const VerifyPa
       q -= pairs / 2;
     }
   }
-  const int64_t j = q / (unsigned)p.N, i = q % (unsigned)p.N;
+  const unsigned jq = q / (unsigned)p.N;
+  const int64_t j = jq, i = q - jq * (unsigned)p.N;
   uint32_t flags = 0;
   const int32_t len = clamped_len(p, i, &flags);
   const float Ti = temperature_of(p, i);
@@ -453,7 +461,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_rows_kernel(const VerifyPa
   float m = lane < kWarps ? s_red[lane].x : -INFINITY;
   float sum = lane < kWarps ? s_red[lane].y : 0.f;
   warp_merge(m, sum, t);
-  const int64_t at = (((is_draft ? p.K + 1 : 0) + j) * p.N + i) * p.split + s;
+  const int64_t row_at = ((is_draft ? p.K + 1 : 0) + j) * p.N + i;
+  const int64_t at = (row_at << p.split_log2) + s;
   if (greedy) {
     const float top = lane < kWarps ? s_top[lane] : -INFINITY, M = warp_max(top);
     const int64_t arg = warp_min(lane < kWarps && top == M ? s_arg[lane] : INT64_MAX);
@@ -465,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_rows_kernel(const VerifyPa
   uint32_t last = 0;
   if (lane == 0) {
     p.part[at] = make_float2(m, sum);
-    if (x >= v0 && x < v1) p.picked[at / p.split] = picked;
+    if (x >= v0 && x < v1) p.picked[row_at] = picked;
     if (p.lazy && j < len) {
       const uint32_t expect = (uint32_t)(p.split * (draft != nullptr && !greedy ? 2 : 1));
       __threadfence();
@@ -537,12 +546,6 @@ __device__ __forceinline__ void better(double& s, int64_t& at, double s2, int64_
   }
 }
 
-// 1 / x on the special-function unit (2^-23; infinite for 0).
-__device__ __forceinline__ float rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // Lower and upper bound of a score, any row.
 __device__ __forceinline__ void race_bounds(const Racer& c, float x, float y, float e, float& lo,
                                             float& hi) {
@@ -1012,10 +1015,12 @@ cudaError_t launch_t(const VerifyArgs& a, const DeviceInfo& d, cudaStream_t st) 
   const int kinds = a.draft != nullptr ? 2 : 1;
   // parts of a row: enough that the first position's rows occupy every SM
   // four times over, of at least 8 KiB
-  int split = 1;
+  int split = 1, split_log2 = 0;
   while (split < kMaxSplit && a.N * kinds * split < 4 * (int64_t)d.sms &&
-         row_bytes / (2 * split) >= kMinPartBytes)
+         row_bytes / (2 * split) >= kMinPartBytes) {
     split *= 2;
+    ++split_log2;
+  }
   const int64_t rows = a.N * (a.K + 1) + (kinds == 2 ? a.N * a.K : 0);
   if (rows > INT32_MAX / split) return cudaErrorInvalidValue;  // (refused by api.cu)
   VerifyParams p = {};
@@ -1044,6 +1049,7 @@ cudaError_t launch_t(const VerifyArgs& a, const DeviceInfo& d, cudaStream_t st) 
   p.rejected = reinterpret_cast<int32_t*>(ws + l.rejected);
   p.ticket = reinterpret_cast<uint32_t*>(ws + l.ticket);
   p.split = split;
+  p.split_log2 = split_log2;
   p.part_elems = ((a.V + split - 1) / split + EPV - 1) / EPV * EPV;
   // all rows at once when the GPU takes them at once
   p.lazy = a.K > 0 && rows * split > 4 * (int64_t)d.sms;
