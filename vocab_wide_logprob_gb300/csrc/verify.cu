@@ -589,6 +589,117 @@ __host__ __device__ constexpr size_t race_ring() {
   return (size_t)race_stages<T>() * race_vecs<T>() * kRaceThreads * 16;
 }
 
+// The CTA's best lower bound, raised by this warp's.
+__device__ __forceinline__ float race_raise(Shared& sh, float top) {
+  const unsigned wtop = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+  const float bar = __int_as_float(*(volatile int*)&sh.best);
+  if (__uint_as_float(wtop) <= bar) return bar;
+  if ((threadIdx.x & 31) == 0) atomicMax(&sh.best, (int)wtop);
+  return __uint_as_float(wtop);
+}
+__device__ __forceinline__ void race_keep(Shared& sh, float hi, float bar, int64_t v) {
+  // (with no lower bound yet, everything that may have mass: its own lower
+  // bound may be 0 where p and q are close, and its score still the largest)
+  if (hi >= bar && hi > 0.f) {
+    const int s = atomicAdd(&sh.count, 1);
+    if (s < kCandidates) {
+      sh.cand[s] = (int32_t)v;
+      sh.cand_hi[s] = hi;
+    }
+  }
+}
+
+// 16-byte aligned rows with maxima of ordinary size: n8 groups of 8 elements
+// from v0 on, pairs of them through packed arithmetic.  Returns the largest
+// upper bound.
+template <typename T, bool kDraft>
+__device__ __forceinline__ float race_stream(const Racer& c, const T* tr, const T* dr,
+                                             const float* nr, int64_t v0, int n8, Shared& sh,
+                                             uint32_t ring) {
+  using E = Elt<T>;
+  constexpr int W = E::kPerVec == 8 ? 1 : 2;  // vectors of 8 logits
+  constexpr int S = race_stages<T>(), R = race_vecs<T>();
+  constexpr uint32_t kSlot = kRaceThreads * 16;
+  const int tid = threadIdx.x;
+  const uint32_t mine = ring + 16 * tid;  // vector r of stage s: + (s * R + r) * kSlot
+  const T* tp = tr + v0 + 8 * tid;
+  const T* dp = kDraft ? dr + v0 + 8 * tid : nullptr;
+  const float* np = nr + v0 + 8 * tid;
+  int ahead = tid;
+  auto issue = [&](uint32_t to) {
+    if (ahead < n8) {
+#pragma unroll
+      for (int k = 0; k < W; ++k) {
+        cp_async16(to + k * kSlot, tp + k * E::kPerVec);
+        if (kDraft) cp_async16(to + (W + k) * kSlot, dp + k * E::kPerVec);
+      }
+      cp_async16(to + 2 * W * kSlot, np);
+      cp_async16(to + (2 * W + 1) * kSlot, np + 4);
+    }
+    cp_async_commit();
+    ahead += kRaceThreads;
+    tp += 8 * kRaceThreads;
+    if (kDraft) dp += 8 * kRaceThreads;
+    np += 8 * kRaceThreads;
+  };
+#pragma unroll
+  for (int k = 0; k < S; ++k) issue(mine + k * R * kSlot);
+  const uint64_t hi2 = f2_pack(c.t.hi, c.t.hi), lo2 = f2_pack(c.t.lo, c.t.lo);
+  const float nt1 = -(c.rt + c.lst), nd1 = -(c.rd + c.lsd);
+  const uint64_t nt = f2_pack(nt1, nt1), nd = f2_pack(nd1, nd1);
+  const int64_t in = c.skip - v0;  // the token left out, if it is here
+  const int skip = c.skip >= 0 && in >= 0 && in < 8 * (int64_t)n8 ? (int)in : -1;
+  const int steps = (n8 + kRaceThreads - 1) / kRaceThreads;
+  uint32_t at = mine;
+  float bar = 0.f, largest = 0.f;
+#pragma unroll 1
+  for (int step = 0, k = tid; step < steps; ++step, k += kRaceThreads) {
+    cp_async_wait<S - 1>();
+    float most = 0.f;
+    float x[8], y[8], e[8];
+    if (k < n8) {
+#pragma unroll
+      for (int q = 0; q < W; ++q) {
+        E::unpack(ld_shared_v4(at + q * kSlot), x + q * E::kPerVec);
+        if (kDraft) E::unpack(ld_shared_v4(at + (W + q) * kSlot), y + q * E::kPerVec);
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) Elt<float>::unpack(ld_shared_v4(at + (2 * W + q) * kSlot), e + 4 * q);
+#pragma unroll
+      for (int q = 0; q < 8; q += 2) {
+        const uint64_t h =
+            kDraft ? race_upper2<true>(hi2, lo2, nt, nd, x[q], x[q + 1], y[q], y[q + 1], e[q], e[q + 1])
+                   : race_upper2<false>(hi2, lo2, nt, nd, x[q], x[q + 1], 0.f, 0.f, e[q], e[q + 1]);
+        float h0, h1;
+        f2_unpack(h, h0, h1);
+        most = fmaxf(most, fmaxf(h0, h1));
+      }
+      largest = fmaxf(largest, most);
+    }
+    // an upper bound above everything so far: both bounds, one by one
+    bar = fmaxf(bar, __int_as_float(*(volatile int*)&sh.best));
+    if (__any_sync(0xffffffffu, most > 0.f && most >= bar)) {
+      float hi[8], top = 0.f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        hi[q] = 0.f;
+        if (k < n8 && 8 * k + q != skip) {
+          float lo;
+          race_bounds(c, x[q], kDraft ? y[q] : 0.f, e[q], lo, hi[q]);
+          top = fmaxf(top, lo);
+        }
+      }
+      bar = race_raise(sh, top);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) race_keep(sh, hi[q], bar, v0 + 8 * (int64_t)k + q);
+    }
+    issue(at);
+    at = at == mine + (S - 1) * R * kSlot ? mine : at + R * kSlot;
+  }
+  cp_async_wait<0>();
+  return largest;
+}
+
 template <typename T>
 __device__ Bounds race_bounds_of(const Racer& c, const T* tr, const T* dr, const float* nr,
                                  int64_t v0, int64_t v1, Shared& sh, uint32_t ring) {
@@ -600,116 +711,16 @@ __device__ Bounds race_bounds_of(const Racer& c, const T* tr, const T* dr, const
     sh.count = 0;
   }
   __syncthreads();
-  float largest = 0.f;  // upper bound (that of a skipped token too: it only asks for the exact race)
-  // the CTA's best lower bound, raised by this warp's
-  auto raise = [&](float top) -> float {
-    const unsigned wtop = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-    const float bar = __int_as_float(*(volatile int*)&sh.best);
-    if (__uint_as_float(wtop) <= bar) return bar;
-    if (lane == 0) atomicMax(&sh.best, (int)wtop);
-    return __uint_as_float(wtop);
-  };
-  auto keep = [&](float hi, float bar, int64_t v) {
-    // (with no lower bound yet, everything that may have mass: its own lower
-    // bound may be 0 where p and q are close, and its score still the largest)
-    if (hi >= bar && hi > 0.f) {
-      const int s = atomicAdd(&sh.count, 1);
-      if (s < kCandidates) {
-        sh.cand[s] = (int32_t)v;
-        sh.cand_hi[s] = hi;
-      }
-    }
-  };
+  // upper bound (that of a skipped token too: it only asks for the exact race)
+  float largest = 0.f;
   int64_t from = v0;
-  // 16-byte aligned rows with maxima of ordinary size: pairs, through the ring
-  constexpr int W = E::kPerVec == 8 ? 1 : 2;  // vectors of 8 logits
-  constexpr int S = race_stages<T>(), R = race_vecs<T>();
   const bool vec = (reinterpret_cast<uintptr_t>(tr + v0) | reinterpret_cast<uintptr_t>(nr + v0) |
                     (c.has_draft ? reinterpret_cast<uintptr_t>(dr + v0) : 0)) % 16 == 0 &&
                    !c.bigt && !(c.has_draft && c.bigd);
   if (vec) {
     const int n8 = (int)((v1 - v0) / 8);
-    const uint32_t mine = ring + 16 * tid;  // vector r of stage s: + (s * R + r) * kRaceThreads * 16
-    const T* tp = tr + v0;
-    const T* dp = c.has_draft ? dr + v0 : nullptr;
-    const float* np = nr + v0;
-    int ahead = tid;
-    auto issue = [&](int stage) {
-      if (ahead < n8) {
-        const uint32_t to = mine + stage * (R * kRaceThreads * 16);
-#pragma unroll
-        for (int k = 0; k < W; ++k) {
-          cp_async16(to + k * (kRaceThreads * 16), tp + (int64_t)ahead * 8 + k * E::kPerVec);
-          if (c.has_draft)
-            cp_async16(to + (W + k) * (kRaceThreads * 16), dp + (int64_t)ahead * 8 + k * E::kPerVec);
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          cp_async16(to + (2 * W + k) * (kRaceThreads * 16), np + (int64_t)ahead * 8 + 4 * k);
-      }
-      cp_async_commit();
-      ahead += kRaceThreads;
-    };
-    auto at = [&](int stage, int r) {
-      return ld_shared_v4(mine + (stage * R + r) * (kRaceThreads * 16));
-    };
-#pragma unroll
-    for (int k = 0; k < S; ++k) issue(k);
-    const uint64_t hi2 = f2_pack(c.t.hi, c.t.hi), lo2 = f2_pack(c.t.lo, c.t.lo);
-    const float nt1 = -(c.rt + c.lst), nd1 = -(c.rd + c.lsd);
-    const uint64_t nt = f2_pack(nt1, nt1), nd = f2_pack(nd1, nd1);
-    const int64_t skip = c.skip >= 0 ? c.skip - v0 : -1;
-    const int steps = (n8 + kRaceThreads - 1) / kRaceThreads;
-    int stage = 0;
-    float bar = 0.f;
-    for (int step = 0; step < steps; ++step) {
-      const int k = step * kRaceThreads + tid;
-      cp_async_wait<S - 1>();
-      float most = 0.f;
-      float x[8], y[8], e[8];
-      if (k < n8) {
-#pragma unroll
-        for (int q = 0; q < W; ++q) {
-          E::unpack(at(stage, q), x + q * E::kPerVec);
-          if (c.has_draft) E::unpack(at(stage, W + q), y + q * E::kPerVec);
-        }
-#pragma unroll
-        for (int q = 0; q < 2; ++q) Elt<float>::unpack(at(stage, 2 * W + q), e + 4 * q);
-#pragma unroll
-        for (int q = 0; q < 8; q += 2) {
-          const uint64_t h = c.has_draft
-                                 ? race_upper2<true>(hi2, lo2, nt, nd, x[q], x[q + 1], y[q],
-                                                     y[q + 1], e[q], e[q + 1])
-                                 : race_upper2<false>(hi2, lo2, nt, nd, x[q], x[q + 1], 0.f, 0.f,
-                                                      e[q], e[q + 1]);
-          float h0, h1;
-          f2_unpack(h, h0, h1);
-          most = fmaxf(most, fmaxf(h0, h1));
-        }
-        largest = fmaxf(largest, most);
-      }
-      // an upper bound above everything so far: both bounds, one by one
-      if (__any_sync(0xffffffffu, most > 0.f && most >= bar)) {
-        float hi[8], top = 0.f;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          hi[q] = 0.f;
-          if (k < n8 && 8 * (int64_t)k + q != skip) {
-            float lo;
-            race_bounds(c, x[q], c.has_draft ? y[q] : 0.f, e[q], lo, hi[q]);
-            top = fmaxf(top, lo);
-          }
-        }
-        bar = raise(top);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) keep(hi[q], bar, v0 + 8 * (int64_t)k + q);
-      } else {
-        bar = fmaxf(bar, __int_as_float(*(volatile int*)&sh.best));
-      }
-      issue(stage);
-      stage = stage + 1 == S ? 0 : stage + 1;
-    }
-    cp_async_wait<0>();
+    largest = c.has_draft ? race_stream<T, true>(c, tr, dr, nr, v0, n8, sh, ring)
+                          : race_stream<T, false>(c, tr, dr, nr, v0, n8, sh, ring);
     from = v0 + (int64_t)n8 * 8;
   }
   constexpr int M = 4;
@@ -735,9 +746,9 @@ __device__ Bounds race_bounds_of(const Racer& c, const T* tr, const T* dr, const
       }
       largest = fmaxf(largest, hi[w]);
     }
-    const float bar = raise(top);
+    const float bar = race_raise(sh, top);
 #pragma unroll
-    for (int w = 0; w < M; ++w) keep(hi[w], bar, base + w * kRaceThreads + tid);
+    for (int w = 0; w < M; ++w) race_keep(sh, hi[w], bar, base + w * kRaceThreads + tid);
   }
   const unsigned wlargest = __reduce_max_sync(0xffffffffu, __float_as_uint(largest));
   if (lane == 0) atomicMax(&sh.top, (int)wlargest);
