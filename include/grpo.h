@@ -576,8 +576,8 @@ grpo_status grpo_grad_norm(const grpo_tensor *tensors, int64_t count, grpo_norm_
  * id outside [0, V) is not accepted (GRPO_ERR_TOKEN_RANGE), a length outside
  * [0, K] clamped (GRPO_ERR_LENGTH_RANGE).
  * Decisions are made in float64 from float32 sums, bitwise reproducibly.
- * K <= 2^20, N * (K+1) <= 2^26.  workspace: at least
- * grpo_verify_workspace_size(N, K) bytes (about 400 bytes per row).
+ * K <= 2^20, N * (K+1) <= 2^26, V < 2^29.  workspace: at least
+ * grpo_verify_workspace_size(N, K) bytes (about 1 KB per row).
  */
 grpo_status grpo_verify_workspace_size(int64_t N, int64_t K, size_t *bytes);
 grpo_status grpo_verify_drafts(const void *target_logits, const void *draft_logits,

@@ -1130,7 +1130,7 @@ grpo_status grpo_verify_drafts(const void* target_logits, const void* draft_logi
                                size_t workspace_bytes, grpo_stream_t stream) {
   if (!known_dtype(dtype)) return GRPO_ERR_UNSUPPORTED;
   if (N < 0 || K < 0 || V < 1) return GRPO_ERR_INVALID_ARG;
-  if (!verify_fits(N, K) || V > INT32_MAX - 65536) return GRPO_ERR_UNSUPPORTED;
+  if (!verify_fits(N, K) || V >= (int64_t)1 << 29) return GRPO_ERR_UNSUPPORTED;
   const bool has_draft = draft_logits != nullptr && K > 0;
   if (target_row < V || target_seq < 0 || noise_row < V) return GRPO_ERR_INVALID_ARG;
   if (mul3(K + 1, target_row, 8) < 0 || mul3(N, target_seq, 8) < 0 || mul3(N, noise_row, 8) < 0)

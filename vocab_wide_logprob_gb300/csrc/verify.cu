@@ -52,41 +52,32 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// exp(x / T) = 2^(x c), c = log2(e) / T kept as c_hi + c_lo with c_lo > 0 (so
-// that -inf stays -inf in both steps).
-// The split is made in float32 (this GPU has few float64 units): a quotient
-// of log2(e)'s leading part that is a little too small, and what is left.
+// exp(x / T) = 2^(x c) with c = log2(e) / T rounded to float32 once, for the
+// target and the draft alike and in every step: the distributions are those of
+// a temperature that differs from T by at most 2^-23 of itself, which moves a
+// ratio p / q by 2^-23 of its own logarithm.
 struct Temper {
-  float hi, lo;
+  float c;
 };
-__device__ __forceinline__ Temper temper(float T) {
-  constexpr float kHead = 1.44269502162933349609375f, kTail = 1.92596299112661746887e-8f;
-  Temper t;
-  const float inv = rcp(T);  // good to 2^-23
-  t.hi = kHead * inv * (1.f - 0x1p-21f);
-  t.lo = fmaxf((fmaf(-t.hi, T, kHead) + kTail) * inv, 1e-37f);
-  return t;
-}
-__device__ __forceinline__ double temper64(const Temper& t) { return (double)t.hi + (double)t.lo; }
+__device__ __forceinline__ Temper temper(float T) { return {__fdiv_rn(1.44269504f, T)}; }
 
 // Reference exponent of a row (or part of one) with maximum m: weights are
 // 2^(x c - r).  With r the rounded product, x c - r is rounded once, at its
 // own size: near the maximum, where the weights matter, it is exact to 2^-24.
 // Where the product would leave float32's range, weights are 2^((x - m) c).
-__device__ __forceinline__ float ref_of(float m, const Temper& t) { return m * t.hi; }
+__device__ __forceinline__ float ref_of(float m, const Temper& t) { return m * t.c; }
 __device__ __forceinline__ bool is_big(float m) { return !(fabsf(m) < kBig); }
 __device__ __forceinline__ float exponent(float x, float m, float r, bool big, const Temper& t) {
   if (big) {
-    const float s = x - m;
-    return fmaf(s, t.hi, s * t.lo);
+    return (x - m) * t.c;
   }
-  return fmaf(x, t.lo, fmaf(x, t.hi, -r));
+  return fmaf(x, t.c, -r);
 }
 // 2^(reference m1 - reference m2): moves a sum from one reference to a larger one
 __device__ __forceinline__ float rescale(float m1, float m2, const Temper& t) {
   if (m1 == m2) return 1.f;
   if (m1 == -INFINITY) return 0.f;
-  if (is_big(m1) || is_big(m2)) return ex2((m1 - m2) * t.hi);
+  if (is_big(m1) || is_big(m2)) return ex2((m1 - m2) * t.c);
   return ex2(ref_of(m1, t) - ref_of(m2, t));
 }
 __device__ __forceinline__ float warp_max(float x) {
@@ -113,7 +104,7 @@ __device__ __forceinline__ void warp_merge(float& m, float& s, const Temper& t) 
 }
 // natural log of a weight in float64 (p is weight / sum)
 __device__ __forceinline__ double log_weight(float x, float m, const Temper& t) {
-  const double c = temper64(t);
+  const double c = (double)t.c;
   const double e = is_big(m) ? ((double)x - (double)m) * c : (double)x * c - (double)ref_of(m, t);
   return e * kLn2;
 }
@@ -204,7 +195,7 @@ __device__ __forceinline__ RowStat row_stats(const T* row, int64_t v0, int64_t v
   float edge_s = 0.f, top = -INFINITY;
   int where = -1;  // first vector of the batch that holds the thread's maximum
   uint64_t acc01 = f2_pack(0.f, 0.f), acc23 = f2_pack(0.f, 0.f);
-  const uint64_t hi2 = f2_pack(t.hi, t.hi), lo2 = f2_pack(t.lo, t.lo);
+  const uint64_t c2 = f2_pack(t.c, t.c);
   auto adopt = [&](float x) {  // the whole warp
     const float M = warp_max(fmaxf(x, m));
     const float sc = rescale(m, M, t);
@@ -212,7 +203,7 @@ __device__ __forceinline__ RowStat row_stats(const T* row, int64_t v0, int64_t v
     acc23 = f2_mul(acc23, f2_pack(sc, sc));
     edge_s *= sc;
     m = M;
-    above = is_big(M) ? M : M + __fdividef(kRefSlack, t.hi);
+    above = is_big(M) ? M : M + __fdividef(kRefSlack, t.c);
   };
   auto consume = [&](const uint4* d, int base) {
     const float bm = E::template batch_max<U>(d);
@@ -231,8 +222,8 @@ __device__ __forceinline__ RowStat row_stats(const T* row, int64_t v0, int64_t v
 #pragma unroll
         for (int k = 0; k < EPV; k += 4) {
           const uint64_t x01 = f2_pack(x[k], x[k + 1]), x23 = f2_pack(x[k + 2], x[k + 3]);
-          acc01 = f2_add(acc01, f2_ex2(f2_fma(x01, lo2, f2_fma(x01, hi2, nr2))));
-          acc23 = f2_add(acc23, f2_ex2(f2_fma(x23, lo2, f2_fma(x23, hi2, nr2))));
+          acc01 = f2_add(acc01, f2_ex2(f2_fma(x01, c2, nr2)));
+          acc23 = f2_add(acc23, f2_ex2(f2_fma(x23, c2, nr2)));
         }
       }
     } else {  // extreme values, or nothing but -inf and NaN so far
@@ -513,10 +504,13 @@ struct Shared {
   Bounds bounds[2][kMaxCluster];
   double win[2][kMaxCluster];
   int64_t win_at[2][kMaxCluster];
-  int again[2][kMaxCluster];  // rank 0's: 1 a race is run, 2 and a second one may follow
+  int again[2][kMaxCluster];  // rank 0's: 1 a race is run, 2 and a second one may follow; + 4: a wait gave up
   double wred[kRaceWarps];
   int64_t wred_at[kRaceWarps];
   int best, top, count;
+  int abort;        // a bounded wait gave up
+  uint32_t issued;  // steps of the ring that were copied
+  uint64_t full[3], empty[3];
   int32_t cand[kCandidates];
   float cand_hi[kCandidates];
 };
@@ -558,35 +552,37 @@ __device__ __forceinline__ void race_bounds(const Racer& c, float x, float y, fl
 // The upper bounds of a pair of elements of rows whose maxima are not extreme:
 // nt and nd are minus the reference exponents and the log2 of the sums.
 template <bool kDraft>
-__device__ __forceinline__ uint64_t race_upper2(uint64_t hi2, uint64_t lo2, uint64_t nt,
-                                                uint64_t nd, float x0, float x1, float y0,
+__device__ __forceinline__ uint64_t race_upper2(uint64_t c2, uint64_t nt, uint64_t nd,
+                                                float x0, float x1, float y0,
                                                 float y1, float e0, float e1) {
   const uint64_t x = f2_pack(x0, x1);
-  const uint64_t p = f2_ex2(f2_fma(x, lo2, f2_fma(x, hi2, nt)));
+  const uint64_t p = f2_ex2(f2_fma(x, c2, nt));
   const uint64_t w = f2_pack(rcp(e0), rcp(e1));
   const uint64_t up = f2_pack(1.f + kRaceMargin, 1.f + kRaceMargin);
   uint64_t h = f2_mul(p, up);  // p (1 + margin) - q (1 - margin)
   if (kDraft) {
     const uint64_t y = f2_pack(y0, y1);
-    const uint64_t q = f2_ex2(f2_fma(y, lo2, f2_fma(y, hi2, nd)));
+    const uint64_t q = f2_ex2(f2_fma(y, c2, nd));
     h = f2_fma(q, f2_pack(kRaceMargin - 1.f, kRaceMargin - 1.f), h);
   }
   return f2_mul(h, w);
 }
 
-// The race streams its rows as the rows kernel does: 8 elements per thread and
-// step of target, draft and noise, kRaceStages steps ahead.
+// The race streams its rows in steps of 8 elements per thread of target, draft
+// and noise: bulk copies (TMA), kRaceStages steps ahead, issued by thread 0
+// when every warp has released the stage.
+constexpr int kRaceElems = 8 * kRaceThreads;
 template <typename T>
 __host__ __device__ constexpr int race_stages() {
   return sizeof(T) == 4 ? 2 : 3;
 }
 template <typename T>
-__host__ __device__ constexpr int race_vecs() {  // 16-byte vectors of a step, per thread
-  return 2 * (int)sizeof(T) / 2 + 2;
+__host__ __device__ constexpr uint32_t race_stage_bytes() {
+  return (uint32_t)kRaceElems * (2 * (uint32_t)sizeof(T) + 4);
 }
 template <typename T>
 __host__ __device__ constexpr size_t race_ring() {
-  return (size_t)race_stages<T>() * race_vecs<T>() * kRaceThreads * 16;
+  return (size_t)race_stages<T>() * race_stage_bytes<T>();
 }
 
 // The CTA's best lower bound, raised by this warp's.
@@ -610,66 +606,76 @@ __device__ __forceinline__ void race_keep(Shared& sh, float hi, float bar, int64
 }
 
 // 16-byte aligned rows with maxima of ordinary size: n8 groups of 8 elements
-// from v0 on, pairs of them through packed arithmetic.  Returns the largest
+// from v0 on, pairs of them through packed arithmetic.  `used` counts the
+// ring's steps over all calls (every thread the same).  Returns the largest
 // upper bound.
 template <typename T, bool kDraft>
 __device__ __forceinline__ float race_stream(const Racer& c, const T* tr, const T* dr,
                                              const float* nr, int64_t v0, int n8, Shared& sh,
-                                             uint32_t ring) {
+                                             uint32_t ring, uint32_t& used) {
   using E = Elt<T>;
   constexpr int W = E::kPerVec == 8 ? 1 : 2;  // vectors of 8 logits
-  constexpr int S = race_stages<T>(), R = race_vecs<T>();
-  constexpr uint32_t kSlot = kRaceThreads * 16;
-  const int tid = threadIdx.x;
-  const uint32_t mine = ring + 16 * tid;  // vector r of stage s: + (s * R + r) * kSlot
-  const T* tp = tr + v0 + 8 * tid;
-  const T* dp = kDraft ? dr + v0 + 8 * tid : nullptr;
-  const float* np = nr + v0 + 8 * tid;
-  int ahead = tid;
-  auto issue = [&](uint32_t to) {
-    if (ahead < n8) {
-#pragma unroll
-      for (int k = 0; k < W; ++k) {
-        cp_async16(to + k * kSlot, tp + k * E::kPerVec);
-        if (kDraft) cp_async16(to + (W + k) * kSlot, dp + k * E::kPerVec);
-      }
-      cp_async16(to + 2 * W * kSlot, np);
-      cp_async16(to + (2 * W + 1) * kSlot, np + 4);
-    }
-    cp_async_commit();
-    ahead += kRaceThreads;
-    tp += 8 * kRaceThreads;
-    if (kDraft) dp += 8 * kRaceThreads;
-    np += 8 * kRaceThreads;
+  constexpr uint32_t S = race_stages<T>(), kLogits = kRaceElems * sizeof(T);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int steps = (n8 + kRaceThreads - 1) / kRaceThreads;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (*(volatile int*)&sh.abort) return;
+    if (!mbar_wait(smem_u32(bar), parity)) *(volatile int*)&sh.abort = 1;
   };
-#pragma unroll
-  for (int k = 0; k < S; ++k) issue(mine + k * R * kSlot);
-  const uint64_t hi2 = f2_pack(c.t.hi, c.t.hi), lo2 = f2_pack(c.t.lo, c.t.lo);
+  auto issue = [&](int step) {  // thread 0
+    const uint32_t n = used + (uint32_t)step, st = n % S;
+    wait(&sh.empty[st], ((n / S) & 1u) ^ 1u);
+    if (*(volatile int*)&sh.abort) return;
+    const uint32_t to = ring + st * race_stage_bytes<T>(), full = smem_u32(&sh.full[st]);
+    const uint32_t count = (uint32_t)min(kRaceElems, 8 * (n8 - step * kRaceThreads));
+    const int64_t v = v0 + (int64_t)step * kRaceElems;
+    mbar_arrive_expect_tx(full, count * ((kDraft ? 2 : 1) * (uint32_t)sizeof(T) + 4));
+    bulk_g2s(to, tr + v, count * (uint32_t)sizeof(T), full);
+    if (kDraft) bulk_g2s(to + kLogits, dr + v, count * (uint32_t)sizeof(T), full);
+    bulk_g2s(to + 2 * kLogits, nr + v, count * 4, full);
+    sh.issued = n + 1;
+  };
+  if (tid == 0)
+    for (int k = 0; k < (int)S && k < steps; ++k) issue(k);
+  const uint64_t c2 = f2_pack(c.t.c, c.t.c);
   const float nt1 = -(c.rt + c.lst), nd1 = -(c.rd + c.lsd);
   const uint64_t nt = f2_pack(nt1, nt1), nd = f2_pack(nd1, nd1);
   const int64_t in = c.skip - v0;  // the token left out, if it is here
   const int skip = c.skip >= 0 && in >= 0 && in < 8 * (int64_t)n8 ? (int)in : -1;
-  const int steps = (n8 + kRaceThreads - 1) / kRaceThreads;
-  uint32_t at = mine;
   float bar = 0.f, largest = 0.f;
 #pragma unroll 1
   for (int step = 0, k = tid; step < steps; ++step, k += kRaceThreads) {
-    cp_async_wait<S - 1>();
+    const uint32_t n = used + (uint32_t)step, st = n % S;
+    // the stage of the step before, once every warp has released it
+    if (tid == 0 && step > 0 && step - 1 + (int)S < steps) issue(step - 1 + (int)S);
+    __syncwarp();
+    wait(&sh.full[st], (n / S) & 1u);
     float most = 0.f;
     float x[8], y[8], e[8];
+    const uint32_t at = ring + st * race_stage_bytes<T>();
     if (k < n8) {
+      if (W == 1) {
+        E::unpack(ld_shared_v4(at + 16 * tid), x);
+        if (kDraft) E::unpack(ld_shared_v4(at + kLogits + 16 * tid), y);
+      } else {
 #pragma unroll
-      for (int q = 0; q < W; ++q) {
-        E::unpack(ld_shared_v4(at + q * kSlot), x + q * E::kPerVec);
-        if (kDraft) E::unpack(ld_shared_v4(at + (W + q) * kSlot), y + q * E::kPerVec);
+        for (int q = 0; q < W; ++q) {
+          E::unpack(ld_shared_v4(at + 32 * tid + 16 * q), x + q * E::kPerVec);
+          if (kDraft) E::unpack(ld_shared_v4(at + kLogits + 32 * tid + 16 * q), y + q * E::kPerVec);
+        }
       }
 #pragma unroll
-      for (int q = 0; q < 2; ++q) Elt<float>::unpack(ld_shared_v4(at + (2 * W + q) * kSlot), e + 4 * q);
+      for (int q = 0; q < 2; ++q)
+        Elt<float>::unpack(ld_shared_v4(at + 2 * kLogits + 32 * tid + 16 * q), e + 4 * q);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh.empty[st]));
+    if (k < n8) {
 #pragma unroll
       for (int q = 0; q < 8; q += 2) {
         const uint64_t h =
-            kDraft ? race_upper2<true>(hi2, lo2, nt, nd, x[q], x[q + 1], y[q], y[q + 1], e[q], e[q + 1])
-                   : race_upper2<false>(hi2, lo2, nt, nd, x[q], x[q + 1], 0.f, 0.f, e[q], e[q + 1]);
+            kDraft ? race_upper2<true>(c2, nt, nd, x[q], x[q + 1], y[q], y[q + 1], e[q], e[q + 1])
+                   : race_upper2<false>(c2, nt, nd, x[q], x[q + 1], 0.f, 0.f, e[q], e[q + 1]);
         float h0, h1;
         f2_unpack(h, h0, h1);
         most = fmaxf(most, fmaxf(h0, h1));
@@ -693,16 +699,15 @@ __device__ __forceinline__ float race_stream(const Racer& c, const T* tr, const 
 #pragma unroll
       for (int q = 0; q < 8; ++q) race_keep(sh, hi[q], bar, v0 + 8 * (int64_t)k + q);
     }
-    issue(at);
-    at = at == mine + (S - 1) * R * kSlot ? mine : at + R * kSlot;
   }
-  cp_async_wait<0>();
+  used += (uint32_t)steps;
   return largest;
 }
 
 template <typename T>
 __device__ Bounds race_bounds_of(const Racer& c, const T* tr, const T* dr, const float* nr,
-                                 int64_t v0, int64_t v1, Shared& sh, uint32_t ring) {
+                                 int64_t v0, int64_t v1, Shared& sh, uint32_t ring,
+                                 uint32_t& used) {
   using E = Elt<T>;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
@@ -719,8 +724,8 @@ __device__ Bounds race_bounds_of(const Racer& c, const T* tr, const T* dr, const
                    !c.bigt && !(c.has_draft && c.bigd);
   if (vec) {
     const int n8 = (int)((v1 - v0) / 8);
-    largest = c.has_draft ? race_stream<T, true>(c, tr, dr, nr, v0, n8, sh, ring)
-                          : race_stream<T, false>(c, tr, dr, nr, v0, n8, sh, ring);
+    largest = c.has_draft ? race_stream<T, true>(c, tr, dr, nr, v0, n8, sh, ring, used)
+                          : race_stream<T, false>(c, tr, dr, nr, v0, n8, sh, ring, used);
     from = v0 + (int64_t)n8 * 8;
   }
   constexpr int M = 4;
@@ -758,6 +763,12 @@ __device__ Bounds race_bounds_of(const Racer& c, const T* tr, const T* dr, const
   r.hi = __int_as_float(sh.top);
   r.token = -1;
   r.count = r.hi > 0.f ? -1 : 0;  // nothing with mass here, or nothing separated (yet)
+  if (*(volatile int*)&sh.abort) {  // a wait gave up: the exact race, which needs no ring
+    r.lo = 0.f;
+    r.hi = INFINITY;
+    r.count = -1;
+    return r;
+  }
   const int count = sh.count;
   if (warp == 0 && r.lo > 0.f && count <= kCandidates) {
     // the candidates that reach the final bound, to the front of the list
@@ -881,6 +892,13 @@ __global__ void __launch_bounds__(kRaceThreads, 2) verify_emit_kernel(
   if (tid == 0) {
     sh.stop = INT32_MAX;
     sh.flags = flags;
+    sh.abort = 0;
+    sh.issued = 0;
+    for (int k = 0; k < 3; ++k) {
+      mbar_init(smem_u32(&sh.full[k]), 1);
+      mbar_init(smem_u32(&sh.empty[k]), kRaceWarps);
+    }
+    mbar_init_fence();
   }
   for (int64_t base = 0; base <= len; base += kRaceWarps) {
     __syncthreads();
@@ -928,20 +946,24 @@ __global__ void __launch_bounds__(kRaceThreads, 2) verify_emit_kernel(
   c.lsd = __log2f(d.sd);
   c.skip = draft == nullptr && !bonus ? d.token : -1;
   int64_t token = d.emit == 2 ? d.arg : -1;
+  uint32_t used = 0;
   // The CTAs of the cluster pass the same barriers: what a further step
   // depends on comes from what they sent one another.
   for (int round = 0; round < 2; ++round) {
     Bounds own = {0.f, 0.f, -1, 0};
-    if (d.emit == 1) own = race_bounds_of(c, trow, drow, noise, v0, v1, sh, smem_u32(emit_ring));
+    if (d.emit == 1) own = race_bounds_of(c, trow, drow, noise, v0, v1, sh, smem_u32(emit_ring), used);
     if (tid < (int)ranks) {
       const uint32_t to = (uint32_t)tid;
       const float4 f = make_float4(own.lo, own.hi, __int_as_float(own.token), __int_as_float(own.count));
       st_cluster_f32x4(map_to_rank(smem_u32(&sh.bounds[round][rank]), to), f);
       st_cluster_s32(map_to_rank(smem_u32(&sh.again[round][rank]), to),
-                     d.emit != 1 ? 0 : (c.has_draft || c.skip >= 0 ? 2 : 1));
+                     (d.emit != 1 ? 0 : (c.has_draft || c.skip >= 0 ? 2 : 1)) +
+                         (*(volatile int*)&sh.abort ? 4 : 0));
     }
     cluster_or_cta_sync(ranks);
-    const int again = sh.again[round][0];
+    const int again = sh.again[round][0] & 3;
+    for (uint32_t k = 0; k < ranks; ++k)
+      if (sh.again[round][k] & 4) flags |= kFlagTimeout;
     if (again == 0) break;
     float bar = 0.f;
     for (uint32_t k = 0; k < ranks; ++k) bar = fmaxf(bar, sh.bounds[round][k].lo);
@@ -977,6 +999,14 @@ __global__ void __launch_bounds__(kRaceThreads, 2) verify_emit_kernel(
     c.has_draft = false;
     c.skip = -1;
   }
+  // After a wait that gave up: the copies on their way end first.
+  if (tid == 0 && *(volatile int*)&sh.abort) {
+    constexpr uint32_t S = race_stages<T>();
+    for (uint32_t k = 0; k < S && k < sh.issued; ++k) {
+      const uint32_t n = sh.issued - 1 - k;
+      mbar_wait(smem_u32(&sh.full[n % S]), (n / S) & 1u);
+    }
+  }
   if (rank != 0) return;
   if (token < 0) flags |= kFlagValue;
   const int64_t o = i * (p.K + 1);
@@ -986,7 +1016,7 @@ __global__ void __launch_bounds__(kRaceThreads, 2) verify_emit_kernel(
                                          (double)logf(d.st))
                                : __int_as_float(0x7fc00000);
     p.n_accepted[i] = (int32_t)j;
-    p.status[i] = flags & ~kFlagIndirect;
+    p.status[i] = flags;
   }
   for (int64_t k = j + 1 + tid; k <= p.K; k += kRaceThreads) {
     p.out_tokens[o + k] = -1;
