@@ -168,12 +168,18 @@ def test_binding_refuses_cpu_tensors_and_wrong_types(n):
     w = torch.zeros(8, 16)
     with pytest.raises(ValueError):
         n.grpo_embed_fwd(ids, w)
+    with pytest.raises(TypeError):
+        n.grpo_embed_fwd([1, 2], w)
     with pytest.raises(ValueError):
         n.grpo_embed_bwd(ids, torch.zeros(4, 16), 8)
     with pytest.raises(ValueError):
-        n._rows(w, "w", w.device)
-    with pytest.raises(ValueError):
-        n._tensor_table([w], None)
+        n.grpo_clip_grad_norm([w], 1.0)
+    with pytest.raises(TypeError):
+        n.grpo_clip_grad_norm([w.tolist()], 1.0)
+    with pytest.raises(TypeError):
+        n.grpo_clip_grad_norm(7, 1.0)
+    with pytest.raises(TypeError):
+        n.grpo_clip_grad_norm([], "one")
     with pytest.raises(ValueError):
         n.grpo_verify_drafts(torch.zeros(2, 3), ids, w, w)
     with pytest.raises(ValueError):

@@ -8,9 +8,7 @@ fallback: importing this module fails loudly when the library is missing.
 """
 from __future__ import annotations
 
-import array
 import ctypes
-import operator
 import os
 
 import torch
@@ -105,6 +103,10 @@ def _load():
 
 
 _lib = _load()
+
+from . import _ops  # noqa: E402  (the operators around the loss; linked to libgrpo.so)
+
+_ops.set_error(GrpoError)
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -527,35 +529,10 @@ def grpo_lmhead_loss_bwd(hidden, weight, P, input_ids, lens, lse, w, grad_loss=N
     return out[0], out[1], workspace
 
 
-def _rows(t, name, device):
-    """Dtype code and row pitch of a matrix on ``device`` whose rows are dense
-    (a view of wider rows is taken as it is)."""
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
-    code = _CODE.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    shape = t.shape
-    if len(shape) != 2:
-        raise ValueError(f"{name} must have two dimensions")
-    r, c = shape
-    pitch, inner = t.stride()
-    if r <= 1 and pitch < c:
-        pitch = c
-    if (c > 1 and inner != 1) or pitch < c:
-        raise ValueError(f"{name} must have dense rows")
-    return code, pitch
-
-
-_CODE = {torch.float32: GRPO_F32, torch.bfloat16: GRPO_BF16}
-
-
-def _empty_rows(shape, dtype, name, device):
-    """A new dense tensor and its dtype code."""
-    code = _CODE.get(dtype)
-    if code is None:
-        raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
-    return torch.empty(shape, dtype=dtype, device=device), code
+# The operators around the loss.  Their tensors are checked and marshalled in
+# C++ (csrc/binding.cpp, module _ops): these calls are short, or take hundreds
+# of tensors.  A tensor of the wrong type raises TypeError, one of the wrong
+# shape, layout or device ValueError, a refused call GrpoError.
 
 
 def grpo_embed_fwd(ids, weight, scale=1.0, out=None, out_dtype=None, stream=None):
@@ -563,23 +540,7 @@ def grpo_embed_fwd(ids, weight, scale=1.0, out=None, out_dtype=None, stream=None
     or bfloat16 (rows may be part of wider ones).  Returns ``out`` [*ids.shape,
     d] in ``out_dtype`` (the weight's when None); a given ``out`` may be a view
     [n, d] of wider rows.  An id outside [0, V) gives a row of NaN."""
-    _dev(ids, "ids", torch.int64)
-    dev = ids.device
-    wcode, ldw = _rows(weight, "weight", dev)
-    V, d = weight.shape
-    n = ids.numel()
-    if out is None:
-        out, ocode = _empty_rows(ids.shape + (d,), out_dtype or weight.dtype, "out", dev)
-        ldo = d
-    else:
-        if out_dtype is not None and out.dtype != out_dtype:
-            raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
-        if out.shape != ids.shape + (d,) and out.shape != (n, d):
-            raise ValueError("out must be [*ids.shape, d]")
-        ocode, ldo = _rows(out if out.dim() == 2 else out.view(n, d), "out", dev)
-    _check(_lib.grpo_embed_fwd(ids.data_ptr(), n, weight.data_ptr(), wcode, V, d, ldw, float(scale),
-                               out.data_ptr(), ocode, ldo, _stream(stream)), "grpo_embed_fwd")
-    return out
+    return _ops.embed_fwd(ids, weight, scale, out, out_dtype, stream)
 
 
 def grpo_embed_workspace_size(n: int, V: int, d: int) -> int:
@@ -596,67 +557,8 @@ def grpo_embed_bwd(ids, dout, V, scale=1.0, pad_id=None, dweight=None, accumulat
     dweight in ``out_dtype`` (float32 when None).  With ``accumulate`` the
     gradient is added to the given ``dweight`` (for example the LM head's, with
     tied weights).  Tokens equal to ``pad_id`` contribute nothing."""
-    _dev(ids, "ids", torch.int64)
-    dev = ids.device
-    n = ids.numel()
-    if dout.shape[:-1] != ids.shape and dout.shape[:-1] != (n,):
-        raise ValueError("dout must be [*ids.shape, d]")
-    d = dout.shape[-1]
-    dcode, ldd = _rows(dout if dout.dim() == 2 else dout.view(n, d), "dout", dev)
-    if dweight is None:
-        if accumulate:
-            raise ValueError("accumulate needs a dweight")
-        dweight, wcode = _empty_rows((V, d), out_dtype or torch.float32, "dweight", dev)
-        ldw = d
-    else:
-        if out_dtype is not None and dweight.dtype != out_dtype:
-            raise TypeError(f"dweight must be {out_dtype}, got {dweight.dtype}")
-        if dweight.shape != (V, d):
-            raise ValueError("dweight must be [V, d]")
-        wcode, ldw = _rows(dweight, "dweight", dev)
-    need = grpo_embed_workspace_size(n, V, d)
-    if workspace is None or workspace.numel() < need:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-    _check(_lib.grpo_embed_bwd(ids.data_ptr(), n, dout.data_ptr(), dcode, V, d, ldd, float(scale),
-                               -1 if pad_id is None else int(pad_id), dweight.data_ptr(), wcode,
-                               ldw, 1 if accumulate else 0, workspace.data_ptr(),
-                               workspace.numel(), _stream(stream)), "grpo_embed_bwd")
-    return dweight, workspace
-
-
-def _columns(tensors, name):
-    """Addresses, sizes and dtype codes of a list of dense tensors.  (A model
-    has hundreds: the attributes are read by C-level maps.)"""
-    T = torch.Tensor
-    if not (all(map(_is_cuda, tensors)) and all(map(T.is_contiguous, tensors))):
-        raise ValueError(f"every {name} must be a contiguous CUDA tensor")
-    try:
-        codes = list(map(_CODE.__getitem__, map(_dtype, tensors)))
-    except KeyError:
-        raise TypeError(f"every {name} must be float32 or bfloat16") from None
-    return list(map(T.data_ptr, tensors)), list(map(T.numel, tensors)), codes
-
-
-_is_cuda, _dtype = operator.attrgetter("is_cuda"), operator.attrgetter("dtype")
-
-
-def _tensor_table(grads, outs):
-    """The grpo_tensor array (four 8-byte words each) of a list of gradients
-    and their outputs, as an array the caller keeps while the C call reads it."""
-    data, numel, codes = _columns(grads, "gradient")
-    n = len(data)
-    flat = [0] * (4 * n)
-    if outs is None:
-        ocodes = codes
-    else:
-        if len(outs) != n:
-            raise ValueError("out must have one tensor per gradient")
-        flat[1::4], onumel, ocodes = _columns(outs, "out")
-        if onumel != numel:
-            raise ValueError("every out must have its gradient's size")
-    flat[0::4], flat[2::4] = data, numel
-    flat[3::4] = [c | o << 32 for c, o in zip(codes, ocodes)]
-    return array.array("Q", flat)
+    return _ops.embed_bwd(ids, dout, V, scale, pad_id, dweight, accumulate, out_dtype, workspace,
+                          stream)
 
 
 def grpo_grad_norm_workspace_size(count: int) -> int:
@@ -666,80 +568,25 @@ def grpo_grad_norm_workspace_size(count: int) -> int:
     return int(out.value)
 
 
-def _clip_buffers(grads, stats, workspace):
-    dev = grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
-    if stats is None:
-        stats = torch.empty((2,), dtype=torch.float32, device=dev)
-    else:
-        _dev(stats, "stats", torch.float32)
-        if stats.numel() < 2:
-            raise ValueError("stats must hold two values")
-    need = grpo_grad_norm_workspace_size(len(grads))
-    if workspace is None or workspace.numel() < need:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-    return stats, workspace
-
-
 def grpo_clip_grad_norm(grads, max_norm, out=None, norm_type=GRPO_NORM_L2, eps=1e-6, stats=None,
                         workspace=None, stream=None):
     """Clips the list of gradients ``grads`` (dense float32 or bfloat16, any
     mixture) by their global norm, in place or into the tensors of ``out``.
     Returns ``(stats, workspace)``, stats = [norm, coefficient] float32 on the
     device."""
-    grads = list(grads)
-    stats, workspace = _clip_buffers(grads, stats, workspace)
-    table = _tensor_table(grads, out)
-    _check(_lib.grpo_clip_grad_norm(table.buffer_info()[0], len(grads), norm_type, float(max_norm), eps,
-                                    stats.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                    _stream(stream)), "grpo_clip_grad_norm")
-    return stats, workspace
+    return _ops.clip(grads, max_norm, out, norm_type, eps, stats, workspace, stream, False)
 
 
 def grpo_grad_norm(grads, norm_type=GRPO_NORM_L2, stats=None, workspace=None, stream=None):
     """The global norm of ``grads`` alone: ``(stats, workspace)``, stats =
     [norm, 1]."""
-    grads = list(grads)
-    stats, workspace = _clip_buffers(grads, stats, workspace)
-    table = _tensor_table(grads, None)
-    _check(_lib.grpo_grad_norm(table.buffer_info()[0], len(grads), norm_type, stats.data_ptr(),
-                               workspace.data_ptr(), workspace.numel(), _stream(stream)),
-           "grpo_grad_norm")
-    return stats, workspace
+    return _ops.clip(grads, None, None, norm_type, None, stats, workspace, stream, True)
 
 
 def grpo_verify_workspace_size(N: int, K: int) -> int:
     out = ctypes.c_size_t(0)
     _check(_lib.grpo_verify_workspace_size(N, K, ctypes.byref(out)), "grpo_verify_workspace_size")
     return int(out.value)
-
-
-def _logit_rows(t, name, shape, device):
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}, got {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    N, R, V = shape
-    seq, row, inner = t.stride()
-    if R <= 1 and row < V:
-        row = V
-    if N <= 1 and seq < R * row:
-        seq = R * row
-    if (V > 1 and inner != 1) or row < V or seq < (R - 1) * row + V:
-        raise ValueError(f"{name} must have dense rows that do not overlap")
-    return seq, row
-
-
-def _vector(t, name, dtype, shape, device):
-    """Address of a contiguous tensor of that type and shape (None: none)."""
-    if t is None:
-        return None
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor on {device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return t.data_ptr()
 
 
 def grpo_verify_drafts(target_logits, draft_tokens, u, noise, draft_logits=None, draft_lens=None,
@@ -753,47 +600,8 @@ def grpo_verify_drafts(target_logits, draft_tokens, u, noise, draft_logits=None,
     ``tokens`` [N, K+1] int64 (accepted, emitted, then -1), ``n_accepted`` [N]
     int32, ``logp`` [N, K+1] float32 and ``workspace``; pass it as ``out`` to
     reuse the buffers."""
-    if target_logits.dim() != 3:
-        raise ValueError("target_logits must be [N, K+1, V]")
-    N, rows, V = target_logits.shape
-    K = rows - 1
-    if K < 0:
-        raise ValueError("target_logits must have at least one row per sequence")
-    dev, dtype = target_logits.device, target_logits.dtype
-    if dtype not in _CODE:
-        raise TypeError(f"target_logits must be float32 or bfloat16, got {dtype}")
-    tseq, trow = _logit_rows(target_logits, "target_logits", (N, rows, V), dev)
-    dseq = drow = 0
-    if draft_logits is not None:
-        if draft_logits.dtype != dtype:
-            raise TypeError("draft_logits must have target_logits' dtype")
-        dseq, drow = _logit_rows(draft_logits, "draft_logits", (N, K, V), dev)
-    if noise.dtype != torch.float32 or noise.shape != (N, V):
-        raise ValueError("noise must be float32 [N, V]")
-    nrow = _rows(noise, "noise", dev)[1]
-    given = (_vector(draft_tokens, "draft_tokens", torch.int64, (N, K), dev),
-             _vector(draft_lens, "draft_lens", torch.int32, (N,), dev),
-             _vector(u, "u", torch.float32, (N, K), dev), noise.data_ptr(), nrow,
-             _vector(temperature, "temperature", torch.float32, (N,), dev))
-    if out is None:
-        out = {"tokens": torch.empty((N, rows), dtype=torch.int64, device=dev),
-               "n_accepted": torch.empty((N,), dtype=torch.int32, device=dev),
-               "logp": torch.empty((N, rows), dtype=torch.float32, device=dev)}
-        made = (out["tokens"].data_ptr(), out["n_accepted"].data_ptr(), out["logp"].data_ptr())
-    else:
-        made = (_vector(out["tokens"], "tokens", torch.int64, (N, rows), dev),
-                _vector(out["n_accepted"], "n_accepted", torch.int32, (N,), dev),
-                _vector(out["logp"], "logp", torch.float32, (N, rows), dev))
-        workspace = out.get("workspace") if workspace is None else workspace
-    need = grpo_verify_workspace_size(N, K)
-    if workspace is None or workspace.numel() < need:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-    out["workspace"] = workspace
-    _check(_lib.grpo_verify_drafts(
-        target_logits.data_ptr(), _ptr(draft_logits), _CODE[dtype], N, K, V, tseq, trow, dseq,
-        drow, *given, *made, workspace.data_ptr(), workspace.numel(), _stream(stream)),
-        "grpo_verify_drafts")
-    return out
+    return _ops.verify(target_logits, draft_tokens, u, noise, draft_logits, draft_lens,
+                       temperature, out, workspace, stream)
 
 
 def grpo_set_early_start(enable: bool) -> None:

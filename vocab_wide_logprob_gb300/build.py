@@ -1,4 +1,6 @@
-"""Builds ``libgrpo.so`` (the C-ABI CUDA library) in-tree for sm_103a.
+"""Builds ``libgrpo.so`` (the C-ABI CUDA library) in-tree for sm_103a, and
+``_ops.so`` (the marshalling of PyTorch tensors for the operators around the
+loss, host code linked to it).
 
 Each ``csrc/*.cu`` file is compiled to an object in ``_build/`` in parallel,
 then linked into ``vocab_wide_logprob_gb300/libgrpo.so`` against the shared
@@ -13,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIBRARY = os.path.join(PKG, "libgrpo.so")
+BINDING = os.path.join(PKG, "_ops.so")
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -72,6 +77,39 @@ def _compile(src: str, verbose_ptxas: bool) -> tuple[str, str]:
     return obj, ""
 
 
+def _torch_dir() -> str:
+    import importlib.util
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def _compile_binding() -> str:
+    obj = os.path.join(BUILD, "binding.o")
+    if _stale(obj, [BINDING_SOURCE, *glob.glob(os.path.join(INCLUDE, "*.h"))]):
+        inc = os.path.join(_torch_dir(), "include")
+        dirs = [INCLUDE, inc, os.path.join(inc, "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(cuda_home(), "include")]
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+               *[x for d in dirs for x in ("-isystem" if d != INCLUDE else "-I", d)],
+               "-c", BINDING_SOURCE, "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on {BINDING_SOURCE}:\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str, force: bool) -> None:
+    if not force and not _stale(BINDING, [obj, LIBRARY]):
+        return
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libgrpo.so",
+           "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda", "-L", os.path.join(cuda_home(), "lib64"), "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of {BINDING} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True) -> str:
     """Compiles the library if any source is newer than it; returns its path."""
     os.makedirs(BUILD, exist_ok=True)
@@ -79,8 +117,10 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True) 
     if force:
         for o in glob.glob(os.path.join(BUILD, "*.o")):
             os.remove(o)
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(9, len(srcs) + 1)) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
+        binding = binding.result()
     objs = [o for o, _ in results]
     if verbose_ptxas and not quiet:
         for _, log in results:
@@ -94,6 +134,7 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True) 
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIBRARY)
+    _link_binding(binding, force)
     return LIBRARY
 
 
