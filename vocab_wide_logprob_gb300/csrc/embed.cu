@@ -18,62 +18,13 @@ namespace {
 // element access: 8 columns per thread
 // ---------------------------------------------------------------------------
 
-// A thread's 8 columns of a row: contiguous (kVec: 16-byte loads and stores,
-// every row 16-byte aligned) or strided by the threads of the row (any
-// alignment; neighbouring threads still touch neighbouring elements).
-template <typename T, bool kVec>
-struct Cols8;
-
-template <>
-struct Cols8<uint16_t, true> {
-  __device__ static void load(const uint16_t* p, int, int, float* x) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-    Elt<uint16_t>::unpack(v, x);
-  }
-  __device__ static void store(uint16_t* p, int, int, const float* x) {
-    *reinterpret_cast<uint4*>(p) = Elt<uint16_t>::pack(x);
-  }
-  __device__ static void load_rw(const uint16_t* p, int, int, float* x) {
-    Elt<uint16_t>::unpack(*reinterpret_cast<const uint4*>(p), x);
-  }
-};
-template <>
-struct Cols8<float, true> {
-  __device__ static void load(const float* p, int, int, float* x) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint4 b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
-    Elt<float>::unpack(a, x);
-    Elt<float>::unpack(b, x + 4);
-  }
-  __device__ static void store(float* p, int, int, const float* x) {
-    reinterpret_cast<uint4*>(p)[0] = Elt<float>::pack(x);
-    reinterpret_cast<uint4*>(p)[1] = Elt<float>::pack(x + 4);
-  }
-  __device__ static void load_rw(const float* p, int, int, float* x) {
-    Elt<float>::unpack(reinterpret_cast<const uint4*>(p)[0], x);
-    Elt<float>::unpack(reinterpret_cast<const uint4*>(p)[1], x + 4);
-  }
-};
-// strided: p points at the thread's first column, `step` apart, `left` columns
-// of the row from p on
+// A thread's 8 columns of a row of any alignment: the first at p, `step` apart,
+// `left` columns of the row from p on.
 template <typename T>
-struct Cols8<T, false> {
+struct Cols8 {
   __device__ static void load(const T* p, int step, int left, float* x) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) x[k] = k * step < left ? Elt<T>::load1(p + k * step) : 0.f;
-  }
-  __device__ static void load_rw(const T* p, int step, int left, float* x) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      x[k] = 0.f;
-      if (k * step < left) {
-        const T v = p[k * step];
-        if constexpr (sizeof(T) == 4)
-          x[k] = v;
-        else
-          x[k] = bf16_bits_to_float(v);
-      }
-    }
   }
   __device__ static void store(T* p, int step, int left, const float* x) {
 #pragma unroll
@@ -119,7 +70,7 @@ __global__ void __launch_bounds__(kThreads) embed_fwd_any_kernel(
     for (int u = 0; u < U; ++u) {
       if (rr[u] >= nrows) continue;
       if (id[u] >= 0 && id[u] < V) {
-        Cols8<TW, false>::load(w + id[u] * ldw + cc[u], nu, (int)d - cc[u], x[u]);
+        Cols8<TW>::load(w + id[u] * ldw + cc[u], nu, (int)d - cc[u], x[u]);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[u][e] = __int_as_float(0x7fc00000);
@@ -130,7 +81,7 @@ __global__ void __launch_bounds__(kThreads) embed_fwd_any_kernel(
       if (rr[u] >= nrows) continue;
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[u][e] *= scale;
-      Cols8<TO, false>::store(out + (row0 + rr[u]) * ldo + cc[u], nu, (int)d - cc[u], x[u]);
+      Cols8<TO>::store(out + (row0 + rr[u]) * ldo + cc[u], nu, (int)d - cc[u], x[u]);
     }
   }
 }
@@ -270,14 +221,18 @@ struct SortPlan {
   int64_t seg_tiles;  // such groups
 };
 
-// Threads per row (8 columns each) of the summing kernel, and the columns of
-// its rows of partial sums: whole CTAs of threads.
-int row_threads(int64_t d) {
-  const int64_t units = (d + 7) / 8;
+// Columns per thread of the summing kernel: 8 side by side of 16-byte aligned
+// rows; else 4, a row's threads apart, so that neighbours read neighbouring
+// elements.
+__host__ __device__ constexpr int sum_cols(bool vec) { return vec ? 8 : 4; }
+// Threads per row, and the columns of a row of partial sums: whole CTAs of
+// threads.
+int row_threads(int64_t d, bool vec) {
+  const int64_t units = (d + sum_cols(vec) - 1) / sum_cols(vec);
   return (int)(units < kThreads ? units : kThreads);
 }
-int64_t padded_cols(int64_t d) {
-  const int64_t cols = 8 * (int64_t)row_threads(d);
+int64_t padded_cols(int64_t d, bool vec) {
+  const int64_t cols = sum_cols(vec) * (int64_t)row_threads(d, vec);
   return (d + cols - 1) / cols * cols;
 }
 
@@ -294,14 +249,13 @@ SortPlan sort_plan(int64_t n, int64_t V, int64_t d) {
   // few tokens: shorter groups, so that there are enough of them (about 512
   // threads on each of 152 SMs)
   s.seg = kMaxSegEntries;
-  while (s.seg > kMinSegEntries && (n + s.seg - 1) / s.seg * (padded_cols(d) / 8) < 152 * 512) s.seg /= 2;
+  while (s.seg > kMinSegEntries && (n + s.seg - 1) / s.seg * (padded_cols(d, true) / 8) < 152 * 512) s.seg /= 2;
   s.seg_tiles = (n + s.seg - 1) / s.seg;
   return s;
 }
 
 struct BwdLayout {
   size_t key[2], pos[2], hist[kMaxPasses], bad, list, part, total;
-  int64_t dpad;
 };
 
 // header | keys and positions, twice | histograms | flags | partial sums
@@ -320,8 +274,8 @@ BwdLayout bwd_layout(int64_t n, int64_t V, int64_t d) {
     l.hist[k] = take(k < s.passes ? 4 * (size_t)kMaxBins * s.tiles : 0);
   l.bad = take(4 * (size_t)s.tiles);
   l.list = take(4 * (size_t)(s.seg_tiles + 1));
-  l.dpad = padded_cols(d);
-  l.part = take(2 * (size_t)s.seg_tiles * (size_t)l.dpad * 4);
+  const int64_t pv = padded_cols(d, true), ps = padded_cols(d, false);
+  l.part = take(2 * (size_t)s.seg_tiles * (size_t)(pv > ps ? pv : ps) * 4);
   l.total = at;
   return l;
 }
@@ -591,22 +545,42 @@ struct SegParams {
   int32_t* list;  // count, then the tiles in which a split id begins
   int seg;          // sorted entries per tile
   int tpr, groups;  // threads per row, rows side by side in a CTA
-  int cols;         // columns of one CTA in y (8 per thread of a row)
+  int cols;         // columns of one CTA in y
 };
 
+// A thread's C columns of a row of dW: contiguous (8) or `step` apart (4).
 template <typename TW, bool kVec>
 __device__ __forceinline__ void write_row(TW* row, int step, int left, bool accumulate,
                                           float scale, const float* acc) {
+  constexpr int C = sum_cols(kVec);
   float x[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) x[k] = acc[k] * scale;
-  if (accumulate) {
-    float o[8];
-    Cols8<TW, kVec>::load_rw(row, step, left, o);
+  for (int k = 0; k < C; ++k) x[k] = acc[k] * scale;
+  if constexpr (kVec) {
+    if (accumulate) {
+      Vec8<TW> old;
+      old.load(row);
+      float o[8];
+      old.unpack(o);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] += o[k];
+      for (int k = 0; k < 8; ++k) x[k] += o[k];
+    }
+#pragma unroll
+    for (int k = 0; k < Vec8<TW>::kWords; ++k)
+      reinterpret_cast<uint4*>(row)[k] = Elt<TW>::pack(x + k * Elt<TW>::kPerVec);
+  } else {
+#pragma unroll
+    for (int k = 0; k < C; ++k) {
+      if (k * step >= left) break;
+      if (accumulate) {
+        if constexpr (sizeof(TW) == 4)
+          x[k] += row[k * step];
+        else
+          x[k] += bf16_bits_to_float(row[k * step]);
+      }
+      Elt<TW>::store1(row + k * step, x[k]);
+    }
   }
-  Cols8<TW, kVec>::store(row, step, left, x);
 }
 
 // Bytes a thread of the summing kernel has on their way: kSumDepth rows of 8
@@ -616,10 +590,10 @@ template <typename TD>
 __host__ __device__ constexpr int sum_depth() {
   return sizeof(TD) == 4 ? 4 : 8;
 }
-constexpr int kSumRegs = 4;
+constexpr int kSumRegs = 8;
 constexpr int kMaxGroups = 32;
 
-// A group of `tpr` threads takes Q sorted entries (a tile), 8 columns per
+// A group of `tpr` threads takes Q sorted entries (a tile), C columns per
 // thread, and writes a row whenever the id changes.  An id that goes on past
 // its tile is finished by the group it began in, unless it fills a whole
 // further tile: then it is split at the tiles, every tile leaves its partial
@@ -633,6 +607,7 @@ __global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const SegParams 
   extern __shared__ __align__(16) unsigned char sum_ring[];
   __shared__ int32_t s_key[(kMaxGroups + 1) * kMaxSegEntries];
   __shared__ int32_t s_pos[(kMaxGroups + 1) * kMaxSegEntries];
+  constexpr int C = sum_cols(kVec);
   const int Q = p.seg;
   pdl_wait();
   pdl_trigger();
@@ -678,13 +653,14 @@ __global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const SegParams 
   if (goes_on && !split)
     while (e1 < nb + Q && a + e1 < p.n && key[e1] == last) ++e1;
   if (e0 >= e1) return;
-  // partial sums keep the thread's 8 columns side by side
-  float* part = p.part + 2 * t * p.dpad + (int64_t)blockIdx.y * p.cols + 8 * l;
-  float acc[8];
+  // partial sums keep the thread's columns side by side
+  float* part = p.part + 2 * t * p.dpad + (int64_t)blockIdx.y * p.cols + C * l;
+  float acc[C];
   auto flush_part = [&](int which) {
     float4* q = reinterpret_cast<float4*>(part + which * p.dpad);
-    q[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    q[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+#pragma unroll
+    for (int c = 0; c < C; c += 4)
+      q[c / 4] = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
   };
   int32_t cur = -1;
   auto flush = [&]() {
@@ -702,10 +678,10 @@ __global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const SegParams 
       }
       cur = k;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) acc[c] = v[c];
+      for (int c = 0; c < C; ++c) acc[c] = v[c];
     } else {
 #pragma unroll
-      for (int c = 0; c < 8; ++c) acc[c] += v[c];
+      for (int c = 0; c < C; ++c) acc[c] += v[c];
     }
   };
   if constexpr (kVec) {
@@ -740,10 +716,14 @@ __global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const SegParams 
   } else {
 #pragma unroll 1
     for (int e = e0; e < e1; e += kSumRegs) {
-      float v[kSumRegs][8];
+      float v[kSumRegs][C];
 #pragma unroll
-      for (int u = 0; u < kSumRegs; ++u)
-        if (e + u < e1) Cols8<TD, false>::load(dout + (int64_t)pos[e + u] * p.ldd + c0, step, left, v[u]);
+      for (int u = 0; u < kSumRegs; ++u) {
+        if (e + u >= e1) continue;
+        const TD* row = dout + (int64_t)pos[e + u] * p.ldd + c0;
+#pragma unroll
+        for (int c = 0; c < C; ++c) v[u][c] = c * step < left ? Elt<TD>::load1(row + c * step) : 0.f;
+      }
 #pragma unroll
       for (int u = 0; u < kSumRegs; ++u)
         if (e + u < e1) take(e + u, v[u]);
@@ -806,14 +786,15 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const SegParams p,
         s.w += q.w;
       }
       const float x[4] = {s.x, s.y, s.z, s.w};
+      constexpr int C = sum_cols(kVec);
       const int64_t cy = c / p.cols;               // the CTA column of embed_sum_kernel
-      const int64_t unit = (c - cy * p.cols) / 8;  // its thread
-      const int o = (int)(c & 7);
+      const int64_t unit = (c - cy * p.cols) / C;  // its thread
+      const int o = (int)(c % C);
       const int64_t ncy = min((int64_t)p.cols, p.d - cy * p.cols);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        // the partial sums hold each thread's 8 columns side by side
-        const int64_t in = kVec ? 8 * unit + o + k : unit + (int64_t)(o + k) * p.tpr;
+        // the partial sums hold each thread's columns side by side
+        const int64_t in = kVec ? C * unit + o + k : unit + (int64_t)(o + k) * p.tpr;
         if (in < ncy && unit < p.tpr) {
           TW* q = dw + v * p.ldw + cy * p.cols + in;
           float y = x[k] * p.scale;
@@ -951,21 +932,21 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, const DeviceInfo& dev, cudaS
   p.d = a.d;
   p.ldd = a.ldd;
   p.ldw = a.ldw;
-  p.dpad = l.dpad;
   p.scale = a.scale;
   p.part = reinterpret_cast<float*>(ws + l.part);
   p.list = i32(l.list);
-  p.tpr = row_threads(a.d);
+  const size_t de = a.ddtype == 0 ? 4 : 2;
+  const bool vec = a.d % 8 == 0 && rows_aligned16(a.dout, a.ldd, de) &&
+                   rows_aligned16(a.dweight, a.ldw, we);
+  p.dpad = padded_cols(a.d, vec);
+  p.tpr = row_threads(a.d, vec);
   p.seg = s.seg;
   // rows side by side in a CTA, unless that leaves SMs without one
   const int64_t per = s.seg_tiles / (2 * (int64_t)dev.sms);
   p.groups = kThreads / p.tpr;
   if (p.groups > kMaxGroups) p.groups = kMaxGroups;
   if (p.groups > per) p.groups = per < 1 ? 1 : (int)per;
-  p.cols = 8 * p.tpr;
-  const size_t de = a.ddtype == 0 ? 4 : 2;
-  const bool vec = a.d % 8 == 0 && rows_aligned16(a.dout, a.ldd, de) &&
-                   rows_aligned16(a.dweight, a.ldw, we);
+  p.cols = sum_cols(vec) * p.tpr;
   if (a.ddtype == 0)
     return a.wdtype == 0 ? launch_sums_t<float, float>(a, p, vec, dev, st)
                          : launch_sums_t<float, uint16_t>(a, p, vec, dev, st);
