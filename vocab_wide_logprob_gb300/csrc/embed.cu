@@ -292,7 +292,7 @@ struct Clear {
   int64_t width, pitch;
   unsigned first;  // CTAs below it belong to the sort
 };
-constexpr int64_t kClearBytes = 131072;  // per CTA
+constexpr int64_t kClearBytes = 32768;  // per CTA
 
 __device__ __forceinline__ void clear_rows(const Clear& c) {
   const int64_t k = blockIdx.x - c.first;
