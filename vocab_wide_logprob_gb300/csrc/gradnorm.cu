@@ -48,33 +48,41 @@ __device__ __forceinline__ int find_tensor(const Table<CAP>& t, int64_t chunk) {
 // norm
 // ---------------------------------------------------------------------------
 
-// Squares of values above 2^60 or (all of them) below 2^-50 leave float32's
-// range: such a batch is scaled by a power of two first, which is exact.
+// A sum of squares, or a maximum.  This GPU has few float64 units (a warp's
+// float64 instruction holds the pipe for 16 cycles), so sums are kept as an
+// unevaluated pair of floats, hi + lo, exact to 2^-47 of themselves; float64
+// takes the batches whose squares leave float32's range, and the CTAs' totals.
+struct Acc {
+  float hi, lo;  // kMax: hi alone
+  double rare;
+};
+// hi + lo += x (x of any size): the rounding error of each sum is kept.
+__device__ __forceinline__ void pair_add(float& hi, float& lo, float x) {
+  const float s = hi + x, t = s - hi;
+  lo += (hi - (s - t)) + (x - t);
+  hi = s;
+}
+// Squares of values above 2^40 or (all of a batch) below 2^-50 are taken
+// apart: scaled by a power of two, which is exact.
 template <int N>
-__device__ __forceinline__ double sum_squares(const float* x, float top) {
-  float sc = 1.f;
-  double back = 1.0;
-  if (top > 0x1p60f) {
-    sc = 0x1p-80f;
-    back = 0x1p160;
-  } else if (top < 0x1p-50f) {
-    sc = 0x1p100f;
-    back = 0x1p-200;
+__device__ __forceinline__ void add_squares(Acc& a, const float* x, float top) {
+  if (top > 0x1p40f || (top < 0x1p-50f && top > 0.f)) {
+    const float sc = top > 1.f ? 0x1p-80f : 0x1p100f;
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) s = fmaf(x[k] * sc, x[k] * sc, s);
+    a.rare += (double)s * (top > 1.f ? 0x1p160 : 0x1p-200);
+    return;
   }
   float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-  if (sc == 1.f) {
 #pragma unroll
-    for (int k = 0; k < N; k += 4) {
-      s0 = fmaf(x[k], x[k], s0);
-      s1 = fmaf(x[k + 1], x[k + 1], s1);
-      s2 = fmaf(x[k + 2], x[k + 2], s2);
-      s3 = fmaf(x[k + 3], x[k + 3], s3);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < N; ++k) s0 = fmaf(x[k] * sc, x[k] * sc, s0);
+  for (int k = 0; k < N; k += 4) {
+    s0 = fmaf(x[k], x[k], s0);
+    s1 = fmaf(x[k + 1], x[k + 1], s1);
+    s2 = fmaf(x[k + 2], x[k + 2], s2);
+    s3 = fmaf(x[k + 3], x[k + 3], s3);
   }
-  return (double)((s0 + s1) + (s2 + s3)) * back;
+  pair_add(a.hi, a.lo, (s0 + s1) + (s2 + s3));
 }
 
 // max that keeps NaN
@@ -83,7 +91,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 
 template <typename T, bool kMax>
-__device__ __forceinline__ double chunk_norm(const T* data, int64_t numel, int64_t e0) {
+__device__ __forceinline__ void chunk_norm(Acc& acc, const T* data, int64_t numel, int64_t e0) {
   using E = Elt<T>;
   constexpr int EPV = E::kPerVec;
   constexpr int kElems = (int)(kChunkBytes / sizeof(T));
@@ -103,11 +111,11 @@ __device__ __forceinline__ double chunk_norm(const T* data, int64_t numel, int64
   float edge = 0.f;
   if (tid < a - e0) edge = E::load1(data + e0 + tid);
   if (tid >= 32 && tid - 32 < e1 - b) edge = E::load1(data + b + tid - 32);
-  double s = 0.0;
-  float m = fabsf(edge);
-  if (!kMax) {
+  if (kMax) {
+    acc.hi = max_nan(acc.hi, fabsf(edge));
+  } else if (edge != 0.f) {
     const float ed[4] = {edge, 0.f, 0.f, 0.f};
-    s = edge != 0.f ? sum_squares<4>(ed, fabsf(edge)) : 0.0;
+    add_squares<4>(acc, ed, fabsf(edge));
   }
   // halves of the loads at a time, to bound the registers
 #pragma unroll
@@ -117,15 +125,14 @@ __device__ __forceinline__ double chunk_norm(const T* data, int64_t numel, int64
     for (int u = 0; u < kVecs / 2; ++u) E::unpack(d[h * (kVecs / 2) + u], x + u * EPV);
     if (kMax) {
 #pragma unroll
-      for (int k = 0; k < kVecs / 2 * EPV; ++k) m = max_nan(m, fabsf(x[k]));
+      for (int k = 0; k < kVecs / 2 * EPV; ++k) acc.hi = max_nan(acc.hi, fabsf(x[k]));
     } else {
       float top = 0.f;
 #pragma unroll
       for (int k = 0; k < kVecs / 2 * EPV; ++k) top = fmaxf(top, fabsf(x[k]));
-      s += sum_squares<kVecs / 2 * EPV>(x, top);
+      add_squares<kVecs / 2 * EPV>(acc, x, top);
     }
   }
-  return kMax ? (double)m : s;
 }
 
 __device__ __forceinline__ double combine(double a, double b, bool is_max) {
@@ -133,40 +140,66 @@ __device__ __forceinline__ double combine(double a, double b, bool is_max) {
   return a != a ? a : (b != b ? b : fmax(a, b));
 }
 
-// Sum (or maximum) over the CTA in a fixed tree; every thread gets it.
+// Sum (or maximum) over the CTA in a fixed tree, in thread 0.
 template <bool kMax>
-__device__ __forceinline__ double block_reduce(double v, double* s_red) {
-  for (int o = 16; o > 0; o >>= 1) v = combine(v, __shfl_xor_sync(0xffffffffu, v, o), kMax);
-  if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = v;
+__device__ __forceinline__ double block_total(Acc a) {
+  __shared__ float s_hi[kWarps], s_lo[kWarps];
+  __shared__ double s_rare[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto tree = [&](int width) {
+    for (int o = width / 2; o > 0; o >>= 1) {
+      const float hi = __shfl_xor_sync(0xffffffffu, a.hi, o);
+      const float lo = __shfl_xor_sync(0xffffffffu, a.lo, o);
+      if (kMax) {
+        a.hi = max_nan(a.hi, hi);
+      } else {
+        // (the smaller lane's value first in both, so that both get the same bits)
+        float h = (lane & o) ? hi : a.hi, l = ((lane & o) ? lo : a.lo) + ((lane & o) ? a.lo : lo);
+        pair_add(h, l, (lane & o) ? a.hi : hi);
+        a.hi = h;
+        a.lo = l;
+      }
+    }
+  };
+  tree(32);
+  // (0, or not a number: the rare batches of any thread)
+  const bool rare = !kMax && __any_sync(0xffffffffu, !(a.rare == 0.0));
+  if (rare)
+    for (int o = 16; o > 0; o >>= 1) a.rare += __shfl_xor_sync(0xffffffffu, a.rare, o);
+  if (lane == 0) {
+    s_hi[warp] = a.hi;
+    s_lo[warp] = a.lo;
+    s_rare[warp] = a.rare;
+  }
   __syncthreads();
-  double t = s_red[0];
-#pragma unroll
-  for (int k = 1; k < kWarps; ++k) t = combine(t, s_red[k], kMax);
-  __syncthreads();
-  return t;
+  if (warp != 0) return 0.0;
+  a.hi = lane < kWarps ? s_hi[lane] : 0.f;
+  a.lo = lane < kWarps ? s_lo[lane] : 0.f;
+  a.rare = lane < kWarps ? s_rare[lane] : 0.0;
+  tree(kWarps);
+  if (!kMax && __any_sync(0xffffffffu, !(a.rare == 0.0)))
+    for (int o = kWarps / 2; o > 0; o >>= 1) a.rare += __shfl_xor_sync(0xffffffffu, a.rare, o);
+  return kMax ? (double)a.hi : (double)a.hi + (double)a.lo + a.rare;
 }
 
 template <int CAP, bool kMax>
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ Table<CAP> t,
                                                              double* partial) {
-  __shared__ double s_red[kWarps];
   pdl_wait();
   pdl_trigger();
   const int64_t chunks = t.first[t.count];
-  double s = 0.0;
+  Acc a = {0.f, 0.f, 0.0};
   for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
     const int k = find_tensor(t, c);
-    double v;
     if (t.dt[k] & 1)
-      v = chunk_norm<uint16_t, kMax>(static_cast<const uint16_t*>(t.data[k]), t.numel[k],
-                                     (c - t.first[k]) * (kChunkBytes / 2));
+      chunk_norm<uint16_t, kMax>(a, static_cast<const uint16_t*>(t.data[k]), t.numel[k],
+                                 (c - t.first[k]) * (kChunkBytes / 2));
     else
-      v = chunk_norm<float, kMax>(static_cast<const float*>(t.data[k]), t.numel[k],
-                                  (c - t.first[k]) * (kChunkBytes / 4));
-    s = combine(s, v, kMax);
+      chunk_norm<float, kMax>(a, static_cast<const float*>(t.data[k]), t.numel[k],
+                              (c - t.first[k]) * (kChunkBytes / 4));
   }
-  s = block_reduce<kMax>(s, s_red);
-  if (threadIdx.x == 0) partial[blockIdx.x] = s;
+  const double total = block_total<kMax>(a);
+  if (threadIdx.x == 0) partial[blockIdx.x] = total;
 }
 
 // ---------------------------------------------------------------------------
@@ -186,7 +219,7 @@ __device__ __forceinline__ void chunk_scale(const void* data_, void* out_, int64
   const bool vec = (reinterpret_cast<uintptr_t>(data) | reinterpret_cast<uintptr_t>(out)) % 16 == 0;
   int done = 0;
   if (vec && n == kElems) {
-    constexpr int U = 4;  // units in flight
+    constexpr int U = kUnits < 4 ? kUnits : 4;  // units in flight
     const TI* p = data + 8 * tid;
     TO* q = out + 8 * tid;
 #pragma unroll
