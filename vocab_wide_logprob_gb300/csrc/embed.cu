@@ -738,12 +738,13 @@ __global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const SegParams 
 }
 
 constexpr int kJoinCols = 128;  // columns of one join item (float4 per lane)
+constexpr int kJoinWarps = 16;
 
 // Split ids: the partial sums of their tiles, added per warp over every
-// kWarps-th tile and then over the warps, both in order.
+// kJoinWarps-th tile and then over the warps, both in order.
 template <typename TW, bool kVec, bool kAcc>
-__global__ void __launch_bounds__(kThreads) embed_join_kernel(const SegParams p, TW* dw) {
-  __shared__ float4 s_acc[kWarps][32];
+__global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(const SegParams p, TW* dw) {
+  __shared__ float4 s_acc[kJoinWarps][32];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -754,19 +755,23 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const SegParams p,
     const int64_t t = p.list[1 + it / ny];
     const int64_t c = (it % ny) * kJoinCols + 4 * lane;
     const int32_t v = p.key[(t + 1) * p.seg];
-    // the last tile that begins with the id
-    int64_t last = t + 1;
+    // the last tile that begins with the id: the next 32 at once, then by
+    // 32-way search (the keys are sorted)
+    int64_t last = t + 1, beyond = (p.n + p.seg - 1) / p.seg, stride = 1;
     for (;;) {
-      const int64_t e = (last + 1 + lane) * p.seg;
-      const uint32_t same = __ballot_sync(0xffffffffu, e < p.n && p.key[e < p.n ? e : 0] == v);
-      const int run = same == 0xffffffffu ? 32 : __ffs(~same) - 1;
-      last += run;
-      if (run < 32) break;
+      const int64_t k = last + stride * (lane + 1);
+      const uint32_t same =
+          __ballot_sync(0xffffffffu, k < beyond && p.key[k < beyond ? k * p.seg : 0] == v);
+      const int run = __popc(same);
+      last += stride * run;
+      if (run < 32) beyond = min(beyond, last + stride);
+      if (beyond - last <= 1) break;
+      stride = max((int64_t)1, (beyond - last) / 32);
     }
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (c < p.dpad) {
-#pragma unroll 4
-      for (int64_t k = t + warp; k <= last; k += kWarps) {
+#pragma unroll 8
+      for (int64_t k = t + warp; k <= last; k += kJoinWarps) {
         const float4 q = *reinterpret_cast<const float4*>(p.part + (2 * k + (k == t)) * p.dpad + c);
         s.x += q.x;
         s.y += q.y;
@@ -778,7 +783,7 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const SegParams p,
     s_acc[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && c < p.dpad) {
-      for (int k = 1; k < kWarps; ++k) {
+      for (int k = 1; k < kJoinWarps; ++k) {
         const float4 q = s_acc[k][lane];
         s.x += q.x;
         s.y += q.y;
@@ -825,7 +830,7 @@ cudaError_t launch_sums(const EmbedBwdArgs& a, SegParams p, const DeviceInfo& de
   if (e != cudaSuccess || seg_tiles < 2) return e;
   const int64_t items = seg_tiles * ((p.dpad + kJoinCols - 1) / kJoinCols);
   const int64_t grid = items < 4 * (int64_t)dev.sms ? items : 4 * (int64_t)dev.sms;
-  return launch_pdl(embed_join_kernel<TW, kVec, kAcc>, dim3((unsigned)grid), dim3(kThreads), 0, st,
+  return launch_pdl(embed_join_kernel<TW, kVec, kAcc>, dim3((unsigned)grid), dim3(32 * kJoinWarps), 0, st,
                     1, p, static_cast<TW*>(a.dweight));
 }
 
