@@ -13,6 +13,10 @@
  *                   term, token-sum aggregation divided by a constant
  *   grpo_loss_bwd   "loss.backward()": d loss / d logits
  *
+ * and the operators that a policy update has around the loss: the embedding
+ * (grpo_embed_*), the gradients' norm and clipping (grpo_clip_grad_norm) and
+ * the verification of drafted tokens (grpo_verify_drafts).
+ *
  * Shapes: N = B*G completions (completions b*G .. b*G+G-1 answer prompt b),
  * P prompt tokens, C completion tokens, T = P + C, vocabulary V.  Completion
  * token t of sequence i is input_ids[i, P+t]; it is scored by logits row

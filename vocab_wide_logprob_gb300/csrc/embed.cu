@@ -8,6 +8,11 @@
 // order and writes every row of dW once: a sum of tokens' rows, or zeros for
 // an id that does not occur.  No floating-point atomics: the order of every
 // sum is fixed by n and the ids, so results are bitwise reproducible.
+//
+// Both are HBM-bound copies but for the sort, whose kernels wait on latency:
+// 81,920 rows of 896 bfloat16 looked up in 31 us (147 MB written, 46 MB of
+// distinct rows read); the gradient of 131,072 tokens (half of them padding)
+// over 151,936 ids in 140 us, 82 us of it the zeros of the 545 MB result.
 #include "host_ctx.cuh"
 #include "ops.cuh"
 
@@ -37,7 +42,8 @@ struct Cols8 {
 // forward
 // ---------------------------------------------------------------------------
 
-// Any alignment: one CTA copies `rows` rows; its threads walk the rows' units
+// Any alignment (5,001 rows of 901 elements, float32 to bfloat16: 6 us): one
+// CTA copies `rows` rows; its threads walk the rows' units
 // of 8 columns (unit c of a row: columns c, c + nu, ... c + 7 nu), U of them
 // in flight each: first the units' ids, then the rows, then the stores.
 template <typename TW, typename TO, int U>
@@ -97,7 +103,9 @@ __host__ __device__ constexpr int fwd_depth() {
 // first, and then every thread streams its units of 8 columns through a ring
 // of its own in shared memory, kDepth asynchronous copies ahead of its stores.
 // The ring costs no registers and needs no barrier (a thread reads back what
-// it copied itself), so loads and stores of a CTA overlap all the way.
+// it copied itself), so loads and stores of a CTA overlap all the way: 81,920
+// rows of 896 bfloat16 in 31 us; with a CTA's loads in registers, its ids, rows
+// and stores one after the other, 55 us.
 template <typename TW, typename TO, bool kStream>
 __global__ void __launch_bounds__(kThreads) embed_fwd_kernel(
     const int64_t* __restrict__ ids, int64_t n, const TW* __restrict__ w, int64_t V, int64_t ldw,
@@ -283,8 +291,9 @@ BwdLayout bwd_layout(int64_t n, int64_t V, int64_t d) {
 // The rows of dW that the sort's kernels clear beside their own work.  The
 // sort is a chain of small latency-bound steps on few SMs, the clearing a
 // stream of stores: each kernel of the chain gets CTAs that write its share
-// of the zeros.  Every row is cleared (which ids occur is not known yet); the
-// rows that occur are written over by the sums.
+// of the zeros, 6.7 TB/s of them.  Every row is cleared (which ids occur is not
+// known yet); the rows that occur are written over by the sums.  12,288 tokens
+// of 151,936 ids: 88 us a call, 125 us when the rest was cleared after the sort.
 struct Clear {
   char* base;      // dense rows: one run of bytes
   int64_t bytes;   // of this kernel's share
@@ -479,7 +488,8 @@ __global__ void __launch_bounds__(kSortThreads) embed_scatter_kernel(
 }
 
 // The whole sort of up to kOneCta tokens by one CTA: every pass counts and
-// scatters between shared-memory arrays.
+// scatters between shared-memory arrays (777 tokens: 7 us in one launch, where
+// the passes' kernels take three launches of 4 us).
 constexpr int kOneCta = 4096;
 struct OneShared {
   SortShared s;
@@ -600,6 +610,8 @@ constexpr int kMaxGroups = 32;
 // sum, and embed_join_kernel adds them.  Both neighbours decide that from the
 // same keys: the id at a tile's first entry a is split iff it began before the
 // previous tile (key[a - Q - 1]) or reaches past this one (key[a + Q]).
+// HBM-bound at many tokens: 65,536 rows of 896 float32 (235 MB) in 50 us, with
+// 8 rows in registers 62 us.
 template <typename TD, typename TW, bool kVec, bool kAcc>
 __global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const SegParams p,
                                                                 const TD* __restrict__ dout,
@@ -741,7 +753,9 @@ constexpr int kJoinCols = 128;  // columns of one join item (float4 per lane)
 constexpr int kJoinWarps = 16;
 
 // Split ids: the partial sums of their tiles, added per warp over every
-// kJoinWarps-th tile and then over the warps, both in order.
+// kJoinWarps-th tile and then over the warps, both in order.  A few us as a
+// rule; 131,072 tokens of one id (4,096 tiles) take the whole call from 70 us
+// (their rows alone) to 143 us.
 template <typename TW, bool kVec, bool kAcc>
 __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(const SegParams p, TW* dw) {
   __shared__ float4 s_acc[kJoinWarps][32];

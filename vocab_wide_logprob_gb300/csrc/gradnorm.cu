@@ -9,6 +9,10 @@
 // scaling kernel adds the partials in CTA order (every CTA the same sum), and
 // scales.  The table of tensors travels in the kernel's parameters, so a call
 // needs no copy, no device table and no synchronisation, and can be captured.
+//
+// HBM-bound: the norm of 988 MB reads at 7.0 TB/s (141 us), the scaling of it
+// into another buffer moves 6.5 TB/s (300 us); a call on 290 tensors takes 455
+// us, the norm of 64 MB 12.7 us, 26 small tensors 9 us (the host's part).
 #include <math.h>
 
 #include "ops.cuh"
@@ -254,9 +258,9 @@ __device__ __forceinline__ void chunk_scale(const void* data_, void* out_, int64
 }
 
 // Adds the norm kernel's partials (the same fixed tree in every CTA), forms
-// the coefficient, and scales the chunks last to first: the chunks the norm
-// kernel read last are the ones still in L2.  In place and under the limit
-// there is nothing to write.
+// the coefficient, and scales the chunks last to first (what the norm kernel
+// read last may still be in L2; at 988 MB 1% of it is).  In place and under the
+// limit there is nothing to write.
 template <int CAP, bool kMax>
 __global__ void __launch_bounds__(kThreads, 4) grad_scale_kernel(const __grid_constant__ Table<CAP> t,
                                                               const double* partial, int npartial,

@@ -159,7 +159,11 @@ struct Decision {
 
 // The rows kernel streams a row through shared memory: every thread copies its
 // own 16-byte vectors kRowStages batches ahead (asynchronous copies, read back
-// by the thread that issued them: no barrier, no registers).
+// by the thread that issued them: no barrier, no registers).  The ring alone
+// reads 6.2 TB/s; with the exponentials 4.6 TB/s (242 MB in 52 us at 128
+// sequences of 5 rows of 151,936 bfloat16 and their drafts), bound by issue
+// slots: one unpack, half a packed FMA and one ex2 per element, and some 600
+// instructions per warp and part around them.
 constexpr int kRowVecs = 4;  // vectors of a batch, per thread
 constexpr int kRowStages = 3;
 constexpr size_t kRowRing = (size_t)kRowStages * kRowVecs * kThreads * 16;
@@ -398,7 +402,8 @@ __device__ __forceinline__ void decide(const VerifyParams& p, bool has_draft, in
 
 // One row part per CTA.  Grid order: positions, then sequences, then kinds
 // (target, draft), then parts, so that a position's decision is known before
-// the next position's CTAs begin.
+// most of the next position's CTAs begin: 242 of 350 MB are read at 128 x 4
+// drafts of which 73% are accepted, where 207 MB are needed.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) verify_rows_kernel(const VerifyParams p,
                                                                   const T* __restrict__ target,
@@ -569,8 +574,9 @@ __device__ __forceinline__ uint64_t race_upper2(uint64_t c2, uint64_t nt, uint64
 }
 
 // The race streams its rows in steps of 8 elements per thread of target, draft
-// and noise: bulk copies (TMA), kRaceStages steps ahead, issued by thread 0
-// when every warp has released the stage.
+// and noise: bulk copies (TMA), race_stages() steps ahead, issued by thread 0
+// when every warp has released the stage.  156 MB in 28 us of the emitting
+// kernel's 44 (128 sequences); with per-thread copies the call took 5 us more.
 constexpr int kRaceElems = 8 * kRaceThreads;
 template <typename T>
 __host__ __device__ constexpr int race_stages() {
