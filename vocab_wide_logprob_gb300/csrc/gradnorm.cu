@@ -4,14 +4,14 @@
 //   coef = min(1, max_norm / (norm + eps))
 //   out  = coef * g                                          (per element)
 //
-// Two launches for any number of tensors up to kMaxTensors each: the norm
-// kernel reads every element once and leaves one float64 partial per CTA; the
-// scaling kernel adds the partials in CTA order (every CTA the same sum), and
-// scales.  The table of tensors travels in the kernel's parameters, so a call
-// needs no copy, no device table and no synchronisation, and can be captured.
+// Two launches, or three: the norm kernel reads every element once and leaves
+// one float64 partial per CTA; one warp adds the partials in a fixed order; the
+// scaling kernel scales.  The table of tensors travels in the kernels'
+// parameters (kMaxTensors of them a launch), so a call needs no copy, no device
+// table and no synchronisation, and can be captured.
 //
 // HBM-bound: the norm of 988 MB reads at 7.0 TB/s (141 us), the scaling of it
-// into another buffer moves 6.5 TB/s (300 us); a call on 290 tensors takes 455
+// into another buffer moves 6.6 TB/s (298 us); a call on 290 tensors takes 440
 // us, the norm of 64 MB 12.7 us, 26 small tensors 9 us (the host's part).
 #include <math.h>
 
@@ -257,41 +257,64 @@ __device__ __forceinline__ void chunk_scale(const void* data_, void* out_, int64
   }
 }
 
-// Adds the norm kernel's partials (the same fixed tree in every CTA), forms
-// the coefficient, and scales the chunks last to first (what the norm kernel
-// read last may still be in L2; at 988 MB 1% of it is).  In place and under the
-// limit there is nothing to write.
+// The partials added by one warp in a fixed order (one, since a float64
+// instruction occupies its pipe for many cycles here whatever the number of
+// warps that issue it), and the coefficient from their sum.
+template <bool kMax>
+__device__ __forceinline__ float coefficient(const double* partial, int npartial, float max_norm,
+                                             float eps, float* stats, WsHeader* hdr) {
+  double s = 0.0;
+#pragma unroll 8
+  for (int k = threadIdx.x; k < npartial; k += 32) s = combine(s, partial[k], kMax);
+  for (int o = 16; o > 0; o >>= 1) s = combine(s, __shfl_xor_sync(0xffffffffu, s, o), kMax);
+  const double norm = kMax ? s : sqrt(s);
+  double c = (double)max_norm / (norm + (double)eps);
+  c = c > 1.0 ? 1.0 : c;         // keeps NaN
+  if (isinf(max_norm)) c = 1.0;  // no limit
+  if (stats != nullptr && threadIdx.x == 0) {
+    stats[0] = (float)norm;
+    stats[1] = (float)c;
+    hdr->flags = isfinite((float)norm) ? 0u : kFlagValue;
+  }
+  return (float)c;
+}
+
+// The norm and the coefficient alone (one warp): the whole second step of
+// grpo_grad_norm, and for many chunks the scaling kernel's first.
+template <bool kMax>
+__global__ void __launch_bounds__(32) grad_coef_kernel(const double* partial, int npartial,
+                                                       float max_norm, float eps, float* stats,
+                                                       WsHeader* hdr) {
+  pdl_wait();
+  pdl_trigger();
+  coefficient<kMax>(partial, npartial, max_norm, eps, stats, hdr);
+}
+
+// Scales the chunks last to first (what the norm kernel read last may still be
+// in L2; at 988 MB 1% of it is).  In place and under the limit there is nothing
+// to write.  npartial: the partials to form the coefficient from (the same sum
+// in every CTA), or 0: it is in stats already.
 template <int CAP, bool kMax>
 __global__ void __launch_bounds__(kThreads, 4) grad_scale_kernel(const __grid_constant__ Table<CAP> t,
                                                               const double* partial, int npartial,
                                                               float max_norm, float eps,
                                                               int copies, float* stats,
-                                                              WsHeader* hdr) {
+                                                              WsHeader* hdr, int first) {
   __shared__ float s_coef;
   pdl_wait();
   pdl_trigger();
-  // one warp: a float64 instruction occupies its pipe for many cycles here,
-  // whatever the number of warps that issue it
-  if (threadIdx.x < 32) {
-    double s = 0.0;
-#pragma unroll 8
-    for (int k = threadIdx.x; k < npartial; k += 32) s = combine(s, partial[k], kMax);
-    for (int o = 16; o > 0; o >>= 1) s = combine(s, __shfl_xor_sync(0xffffffffu, s, o), kMax);
-    const double norm = kMax ? s : sqrt(s);
-    double c = (double)max_norm / (norm + (double)eps);
-    c = c > 1.0 ? 1.0 : c;         // keeps NaN
-    if (isinf(max_norm)) c = 1.0;  // no limit
-    if (threadIdx.x == 0) {
-      s_coef = (float)c;
-      if (stats != nullptr && blockIdx.x == 0) {
-        stats[0] = (float)norm;
-        stats[1] = (float)c;
-        hdr->flags = isfinite((float)norm) ? 0u : kFlagValue;
-      }
+  float coef;
+  if (npartial == 0) {
+    coef = stats[1];
+  } else {
+    if (threadIdx.x < 32) {
+      const float c = coefficient<kMax>(partial, npartial, max_norm, eps,
+                                        first && blockIdx.x == 0 ? stats : nullptr, hdr);
+      if (threadIdx.x == 0) s_coef = c;
     }
+    __syncthreads();
+    coef = s_coef;
   }
-  __syncthreads();
-  const float coef = s_coef;
   if (coef == 1.f && !copies) return;
   const int64_t chunks = t.first[t.count];
   for (int64_t r = blockIdx.x; r < chunks; r += gridDim.x) {
@@ -339,59 +362,78 @@ void fill(Table<CAP>* t, const GradTensor* g, int count) {
   t->first[count] = at;
 }
 
+int64_t chunks_of(const GradTensor& g) {
+  const int64_t per = kChunkBytes / ((g.dt & 1) ? 2 : 4);
+  return (g.numel + per - 1) / per;
+}
+
+// One group of tensors.  step 0: its norm kernel, nparts partials from part0
+// on; step 2: its scaling kernel (nparts partials in all, or 0 when the
+// coefficient is known).
 template <int CAP, bool kMax>
 cudaError_t clip_launch(const ClipArgs& a, const GradTensor* g, int count, int part0, int nparts,
-                        bool norm_step, bool first, const DeviceInfo& d, cudaStream_t st) {
+                        int step, bool first, const DeviceInfo& d, cudaStream_t st) {
   Table<CAP> t;
   fill(&t, g, count);
   double* partial = reinterpret_cast<double*>(static_cast<char*>(a.ws) + 256);
-  const int64_t chunks = t.first[count];
-  if (norm_step)
+  if (step == 0)
     return launch_pdl(grad_norm_kernel<CAP, kMax>, dim3((unsigned)nparts), dim3(kThreads), 0, st,
                       1, t, partial + part0);
   bool copies = false;
   for (int k = 0; k < count; ++k) copies |= g[k].out != g[k].data;
-  int64_t grid = 4 * (int64_t)d.sms;  // as many as are resident
+  // into other tensors: 64 CTAs per SM one after the other (442 us for 988 MB,
+  // norm included; 4 per SM, all at once, 463); in place, where there may be
+  // nothing to do, those that are resident at once
+  int64_t grid = (copies ? 64 : 4) * (int64_t)d.sms;
+  const int64_t chunks = t.first[count];
   if (grid > chunks) grid = chunks;
-  if (grid < 1 || a.norm_only) grid = 1;
-  if (a.norm_only) t.first[count] = 0;
+  if (grid < 1) grid = 1;
   return launch_pdl(grad_scale_kernel<CAP, kMax>, dim3((unsigned)grid), dim3(kThreads), 0, st, 1,
-                    t, (const double*)partial, nparts, a.max_norm, a.eps, (int)(copies && !a.norm_only),
-                    first ? a.stats : (float*)nullptr, static_cast<WsHeader*>(a.ws));
+                    t, (const double*)partial, nparts, a.max_norm, a.eps, (int)copies, a.stats,
+                    static_cast<WsHeader*>(a.ws), (int)first);
 }
 
 template <bool kMax>
 cudaError_t clip_run(const ClipArgs& a, const DeviceInfo& d, cudaStream_t st) {
-  // the norm of every group of tensors, then the scaling of every group
+  // the norm of every group of tensors, the coefficient, the scaling of every
+  // group.  With few chunks the scaling kernel's CTAs form the coefficient
+  // themselves (a launch less); with many a kernel of its own does it once.
+  int64_t all = 0;
+  for (int64_t k = 0; k < a.count; ++k) all += chunks_of(a.tensors[k]);
+  const bool apart = a.norm_only || all > 4 * (int64_t)d.sms;
   int parts = 0;
-  for (int step = 0; step < 2; ++step) {
+  cudaError_t e = cudaSuccess;
+  for (int step = 0; step < 3; ++step) {
+    if (step == 1) {
+      if (apart)
+        e = launch_pdl(grad_coef_kernel<kMax>, dim3(1), dim3(32), 0, st, 1,
+                       (const double*)(static_cast<char*>(a.ws) + 256), parts, a.max_norm, a.eps,
+                       a.stats, static_cast<WsHeader*>(a.ws));
+      if (e != cudaSuccess || a.norm_only) return e;
+      continue;
+    }
     int part0 = 0;
     for (int64_t k = 0; k == 0 || k < a.count; k += kMaxTensors) {
       const int cnt = (int)(a.count - k < kMaxTensors ? a.count - k : kMaxTensors);
-      int64_t chunks = 0;
-      for (int j = 0; j < cnt; ++j) {
-        const int64_t per = kChunkBytes / ((a.tensors[k + j].dt & 1) ? 2 : 4);
-        chunks += (a.tensors[k + j].numel + per - 1) / per;
-      }
-      int np = (int)(chunks < 8 * (int64_t)d.sms ? chunks : 8 * (int64_t)d.sms);
+      const GradTensor* g = a.tensors + k;
+      int64_t np = 0;
+      for (int j = 0; j < cnt; ++j) np += chunks_of(g[j]);
+      if (np > 8 * (int64_t)d.sms) np = 8 * (int64_t)d.sms;
       if (np > kMaxPartials) np = kMaxPartials;
       if (np < 1) np = 1;
-      const int n = step == 0 ? np : parts;
-      const GradTensor* g = a.tensors + k;
-      cudaError_t e;
+      const int n = step == 0 ? (int)np : (apart ? 0 : parts);
       if (cnt <= 32)
-        e = clip_launch<32, kMax>(a, g, cnt, part0, n, step == 0, k == 0, d, st);
+        e = clip_launch<32, kMax>(a, g, cnt, part0, n, step, k == 0, d, st);
       else if (cnt <= 192)
-        e = clip_launch<192, kMax>(a, g, cnt, part0, n, step == 0, k == 0, d, st);
+        e = clip_launch<192, kMax>(a, g, cnt, part0, n, step, k == 0, d, st);
       else
-        e = clip_launch<kMaxTensors, kMax>(a, g, cnt, part0, n, step == 0, k == 0, d, st);
+        e = clip_launch<kMaxTensors, kMax>(a, g, cnt, part0, n, step, k == 0, d, st);
       if (e != cudaSuccess) return e;
-      part0 += np;
-      if (step == 1 && a.norm_only) break;
+      part0 += (int)np;
     }
-    parts = part0;
+    if (step == 0) parts = part0;
   }
-  return cudaSuccess;
+  return e;
 }
 
 }  // namespace
