@@ -191,6 +191,37 @@ def test_reproducible_stream_and_graph():
     check(grads, stats, outs, limit)
 
 
+@pytest.mark.parametrize("kind", [0, 1], ids=["l2", "max"])
+def test_many_chunks(kind):
+    # enough of them that the coefficient is formed once, before the scaling
+    n = g()
+    grads = make([9000001, 5, 12000000, 3000003], [F32, BF16], 7)
+    before = [t.clone() for t in grads]
+    limit = 0.4 * norm64(grads, kind)
+    outs = [torch.empty_like(t) for t in grads]
+    stats, ws = n.grpo_clip_grad_norm(grads, limit, out=outs, norm_type=kind)
+    assert n.grpo_check_error(ws) == 0
+    check(grads, stats, outs, limit, kind)
+    alone, _ = n.grpo_grad_norm(grads, norm_type=kind)
+    assert float(alone[0]) == float(stats[0]) and float(alone[1]) == 1.0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        n.grpo_clip_grad_norm(grads, limit, stats=stats, workspace=ws, norm_type=kind)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(grads, outs))
+    # under the limit in place; with a tensor that goes elsewhere
+    for t, b in zip(grads, before):
+        t.copy_(b)
+    outs = [grads[0], torch.empty_like(grads[1]), grads[2], torch.empty_like(grads[3])]
+    n.grpo_clip_grad_norm(grads, 1e9, out=outs, stats=stats, workspace=ws, norm_type=kind)
+    assert float(stats[1]) == 1.0 and all(torch.equal(a, b) for a, b in zip(outs, before))
+    grads[2][7] = float("nan")
+    n.grpo_clip_grad_norm(grads, limit, stats=stats, workspace=ws, norm_type=kind)
+    assert n.grpo_check_error(ws) == 9 and torch.isnan(stats).all()
+    assert all(torch.isnan(t).all() for t in grads)
+
+
 def test_refusals():
     n = g()
     t = torch.ones(10, 10, device="cuda")

@@ -291,7 +291,8 @@ __global__ void __launch_bounds__(32) grad_coef_kernel(const double* partial, in
 }
 
 // Scales the chunks last to first (what the norm kernel read last may still be
-// in L2; at 988 MB 1% of it is).  In place and under the limit there is nothing
+// in L2: of 988 MB 1% is; keeping more of it by the loads' eviction priorities
+// made this kernel slower than it saved).  In place and under the limit there is nothing
 // to write.  npartial: the partials to form the coefficient from (the same sum
 // in every CTA), or 0: it is in stats already.
 template <int CAP, bool kMax>
@@ -381,12 +382,13 @@ cudaError_t clip_launch(const ClipArgs& a, const GradTensor* g, int count, int p
                       1, t, partial + part0);
   bool copies = false;
   for (int k = 0; k < count; ++k) copies |= g[k].out != g[k].data;
-  // into other tensors: 64 CTAs per SM one after the other (442 us for 988 MB,
-  // norm included; 4 per SM, all at once, 463); in place, where there may be
-  // nothing to do, those that are resident at once
-  int64_t grid = (copies ? 64 : 4) * (int64_t)d.sms;
+  // into other tensors a CTA per chunk (1 GiB in 460 us, norm included; 64 CTAs
+  // per SM, 471); in place, where there may be nothing to do, those that are
+  // resident at once (1 GiB under the limit 154 us, over it 480; a CTA per chunk
+  // 186 and 466)
   const int64_t chunks = t.first[count];
-  if (grid > chunks) grid = chunks;
+  int64_t grid = 4 * (int64_t)d.sms;
+  if (grid > chunks || copies) grid = chunks;
   if (grid < 1) grid = 1;
   return launch_pdl(grad_scale_kernel<CAP, kMax>, dim3((unsigned)grid), dim3(kThreads), 0, st, 1,
                     t, (const double*)partial, nparts, a.max_norm, a.eps, (int)copies, a.stats,
