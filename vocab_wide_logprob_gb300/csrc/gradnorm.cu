@@ -5,7 +5,7 @@
 //   out  = coef * g                                          (per element)
 //
 // Two launches, or three: the norm kernel reads every element once and leaves
-// one float64 partial per CTA; one warp adds the partials in a fixed order; the
+// one float64 partial per CTA; they are added in a fixed order; the
 // scaling kernel scales.  The table of tensors travels in the kernels'
 // parameters (kMaxTensors of them a launch), so a call needs no copy, no device
 // table and no synchronisation, and can be captured.
@@ -257,16 +257,24 @@ __device__ __forceinline__ void chunk_scale(const void* data_, void* out_, int64
   }
 }
 
-// The partials added by one warp in a fixed order (one, since a float64
-// instruction occupies its pipe for many cycles here whatever the number of
-// warps that issue it), and the coefficient from their sum.
-template <bool kMax>
+// The partials added by kW warps in a fixed order, and the coefficient from
+// their sum, in the first warp.  Where every CTA does this it is one warp (a
+// float64 instruction occupies its pipe for many cycles here, and the CTAs of
+// an SM share it); where it is done once, eight.
+template <bool kMax, int kW>
 __device__ __forceinline__ float coefficient(const double* partial, int npartial, float max_norm,
                                              float eps, float* stats, WsHeader* hdr) {
   double s = 0.0;
 #pragma unroll 8
-  for (int k = threadIdx.x; k < npartial; k += 32) s = combine(s, partial[k], kMax);
+  for (int k = threadIdx.x; k < npartial; k += 32 * kW) s = combine(s, partial[k], kMax);
   for (int o = 16; o > 0; o >>= 1) s = combine(s, __shfl_xor_sync(0xffffffffu, s, o), kMax);
+  if (kW > 1) {
+    __shared__ double warp_sum[kW];
+    if (threadIdx.x % 32 == 0) warp_sum[threadIdx.x / 32] = s;
+    __syncthreads();
+    s = warp_sum[0];
+    for (int w = 1; w < kW; ++w) s = combine(s, warp_sum[w], kMax);
+  }
   const double norm = kMax ? s : sqrt(s);
   double c = (double)max_norm / (norm + (double)eps);
   c = c > 1.0 ? 1.0 : c;         // keeps NaN
@@ -279,15 +287,15 @@ __device__ __forceinline__ float coefficient(const double* partial, int npartial
   return (float)c;
 }
 
-// The norm and the coefficient alone (one warp): the whole second step of
+// The norm and the coefficient alone: the whole second step of
 // grpo_grad_norm, and for many chunks the scaling kernel's first.
 template <bool kMax>
-__global__ void __launch_bounds__(32) grad_coef_kernel(const double* partial, int npartial,
+__global__ void __launch_bounds__(kThreads) grad_coef_kernel(const double* partial, int npartial,
                                                        float max_norm, float eps, float* stats,
                                                        WsHeader* hdr) {
   pdl_wait();
   pdl_trigger();
-  coefficient<kMax>(partial, npartial, max_norm, eps, stats, hdr);
+  coefficient<kMax, kWarps>(partial, npartial, max_norm, eps, stats, hdr);
 }
 
 // Scales the chunks last to first (what the norm kernel read last may still be
@@ -309,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 4) grad_scale_kernel(const __grid_co
     coef = stats[1];
   } else {
     if (threadIdx.x < 32) {
-      const float c = coefficient<kMax>(partial, npartial, max_norm, eps,
+      const float c = coefficient<kMax, 1>(partial, npartial, max_norm, eps,
                                         first && blockIdx.x == 0 ? stats : nullptr, hdr);
       if (threadIdx.x == 0) s_coef = c;
     }
@@ -408,7 +416,7 @@ cudaError_t clip_run(const ClipArgs& a, const DeviceInfo& d, cudaStream_t st) {
   for (int step = 0; step < 3; ++step) {
     if (step == 1) {
       if (apart)
-        e = launch_pdl(grad_coef_kernel<kMax>, dim3(1), dim3(32), 0, st, 1,
+        e = launch_pdl(grad_coef_kernel<kMax>, dim3(1), dim3(kThreads), 0, st, 1,
                        (const double*)(static_cast<char*>(a.ws) + 256), parts, a.max_norm, a.eps,
                        a.stats, static_cast<WsHeader*>(a.ws));
       if (e != cudaSuccess || a.norm_only) return e;
