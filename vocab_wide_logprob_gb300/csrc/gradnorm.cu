@@ -407,7 +407,8 @@ template <bool kMax>
 cudaError_t clip_run(const ClipArgs& a, const DeviceInfo& d, cudaStream_t st) {
   // the norm of every group of tensors, the coefficient, the scaling of every
   // group.  With few chunks the scaling kernel's CTAs form the coefficient
-  // themselves (a launch less); with many a kernel of its own does it once.
+  // themselves (a launch less: 8 MiB into a copy 8.5 us, against 9.7); with many a
+  // kernel of its own does it once (64 MiB 30 us, against 41; 16 MiB 13.2 either way).
   int64_t all = 0;
   for (int64_t k = 0; k < a.count; ++k) all += chunks_of(a.tensors[k]);
   const bool apart = a.norm_only || all > 4 * (int64_t)d.sms;
