@@ -310,6 +310,29 @@ def test_views_of_padded_rows(dt):
         both(d)
 
 
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("offs", [(0, 0, 1), (1, 0, 0), (0, 3, 2), (5, 5, 5), (8, 8, 8)])
+@pytest.mark.parametrize("N", [3, 160])
+def test_alignments(dt, offs, N):
+    """Rows that begin anywhere relative to 16 bytes, with NaN around them, in
+    one and in several steps of the race."""
+    V = 20000
+    c = case(N, 2, V, dt, 16, err=0.4)
+    parts = {}
+    for name, t, o in zip(("z", "y", "noise"), (c["z"], c["y"], c["noise"]), offs):
+        big = torch.full((*t.shape[:-1], V + 16), math.nan, device="cuda", dtype=t.dtype)
+        parts[name] = big[..., o:o + V]
+        parts[name].copy_(t)
+    both(dict(c, **parts))
+    both(dict(c, y=None, z=parts["z"], noise=parts["noise"]))
+
+
+@pytest.mark.parametrize("dt,N,V", [(BF16, 80, 151936), (F32, 44, 150001), (BF16, 300, 40001)])
+def test_rows_behind_a_rejection(dt, N, V):
+    """So many rows that those behind a known rejection are left out."""
+    both(case(N, 4, V, dt, 17, err=0.6, ragged=True))
+
+
 def test_distribution_of_the_emitted_tokens():
     """Over many sequences of one distribution, the first emitted or accepted
     token follows the target: a chi-square bound at 7 sigma."""

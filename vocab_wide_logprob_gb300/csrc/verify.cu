@@ -11,9 +11,9 @@
 //   with T = 0: x_j is accepted while it is argmax z_j, and argmax z_a emitted.
 //
 // Two kernels.  verify_rows_kernel computes (max, sum of exponentials) of every
-// target and draft row, each row split over CTAs that work on their own; with
-// more rows than the GPU takes at once it runs position by position and leaves
-// out rows behind a rejection that is already known (the last CTA of a
+// target and draft row, each row split over CTAs that work on their own; where
+// the rows are many bytes it runs position by position and leaves out rows
+// behind a rejection that is already known (the last CTA of a
 // position's rows decides it and publishes it; nothing waits for anything, and
 // a row that was read in vain changes no result).  verify_emit_kernel, one
 // thread block cluster per sequence, takes every position's decision at once,
@@ -26,6 +26,8 @@
 // best lower bound (a handful of a row) are compared in float64.
 #include <math.h>
 #include <stddef.h>
+
+#include <atomic>
 
 #include "host_ctx.cuh"
 #include "ops.cuh"
@@ -179,10 +181,12 @@ struct RowStat {
   int64_t arg;
 };
 
-// Over the slice [v0, v1) of a row, by all warps of the CTA.
+// Over the slice [v0, v1) of a row, by all warps of the CTA; also the logit x,
+// where the slice holds it.
 template <typename T, bool kArg>
 __device__ __forceinline__ RowStat row_stats(const T* row, int64_t v0, int64_t v1,
-                                             const Temper& t, uint32_t ring) {
+                                             const Temper& t, uint32_t ring, bool holds,
+                                             int64_t x, float& picked) {
   using E = Elt<T>;
   constexpr int EPV = E::kPerVec;
   constexpr int U = kRowVecs;
@@ -263,6 +267,7 @@ __device__ __forceinline__ RowStat row_stats(const T* row, int64_t v0, int64_t v
   };
 #pragma unroll
   for (int k = 0; k < kRowStages; ++k) issue(k);
+  if (holds) picked = E::load1(row + x);
   int stage = 0;
   for (int n = 0; n < batches; ++n) {
     cp_async_wait<kRowStages - 1>();
@@ -431,22 +436,23 @@ __global__ void __launch_bounds__(kThreads, 4) verify_rows_kernel(const VerifyPa
   }
   const unsigned jq = q / (unsigned)p.N;
   const int64_t j = jq, i = q - jq * (unsigned)p.N;
+  // (loads that are in flight together: each costs a CTA's start its latency)
   uint32_t flags = 0;
-  const int32_t len = clamped_len(p, i, &flags);
+  const int32_t stop = p.lazy ? *(volatile int32_t*)(p.rejected + i) : INT32_MAX;
+  int64_t x = -1;  // the drafted token
+  if (tid == 0 && j < p.K) x = p.tokens[i * p.K + j];
   const float Ti = temperature_of(p, i);
+  const int32_t len = clamped_len(p, i, &flags);
   const bool greedy = Ti < kMinTemperature;
-  if (j > len || (is_draft && (j == len || greedy))) return;
-  if (p.lazy && *(volatile int32_t*)(p.rejected + i) < j) return;
+  if (j > len || (is_draft && (j == len || greedy)) || stop < j) return;
   const Temper t = temper(greedy ? 1.f : Ti);
   const int64_t v0 = min(p.V, s * p.part_elems), v1 = min(p.V, v0 + p.part_elems);
   const T* row = is_draft ? draft + i * p.dls + j * p.dld : target + i * p.tls + j * p.tld;
-  int64_t x = -1;  // the drafted token, if this part holds its logit
-  if (tid == 0 && j < len) x = p.tokens[i * p.K + j];
+  const bool holds = j < len && x >= v0 && x < v1;  // its logit (thread 0)
   const uint32_t ring = smem_u32(row_ring);
-  const RowStat r = greedy ? row_stats<T, true>(row, v0, v1, t, ring)
-                           : row_stats<T, false>(row, v0, v1, t, ring);
   float picked = 0.f;
-  if (x >= v0 && x < v1) picked = Elt<T>::load1(row + x);
+  const RowStat r = greedy ? row_stats<T, true>(row, v0, v1, t, ring, holds, x, picked)
+                           : row_stats<T, false>(row, v0, v1, t, ring, holds, x, picked);
   if (lane == 0) {
     s_red[warp] = make_float2(r.m, r.s);
     s_top[warp] = r.top;
@@ -470,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_rows_kernel(const VerifyPa
   uint32_t last = 0;
   if (lane == 0) {
     p.part[at] = make_float2(m, sum);
-    if (x >= v0 && x < v1) p.picked[row_at] = picked;
+    if (holds) p.picked[row_at] = picked;
     if (p.lazy && j < len) {
       const uint32_t expect = (uint32_t)(p.split * (draft != nullptr && !greedy ? 2 : 1));
       __threadfence();
@@ -575,7 +581,8 @@ __device__ __forceinline__ uint64_t race_upper2(uint64_t c2, uint64_t nt, uint64
 
 // The race streams its rows in steps of 8 elements per thread of target, draft
 // and noise: bulk copies (TMA), race_stages() steps ahead, issued by thread 0
-// when every warp has released the stage.  156 MB in 28 us of the emitting
+// when every warp has released the stage.  Copies begin at the 16-byte boundary
+// at or before an array's first element.  156 MB in 28 us of the emitting
 // kernel's 44 (128 sequences); with per-thread copies the call took 5 us more.
 constexpr int kRaceElems = 8 * kRaceThreads;
 template <typename T>
@@ -584,7 +591,7 @@ __host__ __device__ constexpr int race_stages() {
 }
 template <typename T>
 __host__ __device__ constexpr uint32_t race_stage_bytes() {
-  return (uint32_t)kRaceElems * (2 * (uint32_t)sizeof(T) + 4);
+  return (uint32_t)kRaceElems * (2 * (uint32_t)sizeof(T) + 4) + 3 * 16;
 }
 template <typename T>
 __host__ __device__ constexpr size_t race_ring() {
@@ -611,23 +618,40 @@ __device__ __forceinline__ void race_keep(Shared& sh, float hi, float bar, int64
   }
 }
 
-// 16-byte aligned rows with maxima of ordinary size: n8 groups of 8 elements
-// from v0 on, pairs of them through packed arithmetic.  `used` counts the
-// ring's steps over all calls (every thread the same).  Returns the largest
-// upper bound.
-template <typename T, bool kDraft>
+__device__ __forceinline__ float lds_logit(uint32_t at, uint16_t) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+  return bf16_bits_to_float(v);
+}
+__device__ __forceinline__ float lds_logit(uint32_t at, float) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+  return v;
+}
+
+// Rows with maxima of ordinary size: n8 groups of 8 elements from v0 on, pairs
+// of them through packed arithmetic.  kAligned: all three arrays are 16-byte
+// aligned at v0, and a thread takes 8 neighbours as vectors; otherwise it takes
+// elements kRaceThreads apart (and the row goes on for 8 elements either side,
+// which the copies may read).  `used` counts the ring's steps over all calls
+// (every thread the same).  Returns the largest upper bound.
+template <typename T, bool kDraft, bool kAligned>
 __device__ __forceinline__ float race_stream(const Racer& c, const T* tr, const T* dr,
                                              const float* nr, int64_t v0, int n8, Shared& sh,
                                              uint32_t ring, uint32_t& used) {
   using E = Elt<T>;
   constexpr int W = E::kPerVec == 8 ? 1 : 2;  // vectors of 8 logits
-  constexpr uint32_t S = race_stages<T>(), kLogits = kRaceElems * sizeof(T);
+  constexpr uint32_t S = race_stages<T>(), kLogits = kRaceElems * sizeof(T) + 16;
   const int tid = threadIdx.x, lane = tid & 31;
   const int steps = (n8 + kRaceThreads - 1) / kRaceThreads;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (*(volatile int*)&sh.abort) return;
     if (!mbar_wait(smem_u32(bar), parity)) *(volatile int*)&sh.abort = 1;
   };
+  auto past = [](const void* q) {  // bytes behind a 16-byte boundary
+    return kAligned ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(q) & 15u);
+  };
+  const uint32_t ot = past(tr + v0), od = kDraft ? past(dr + v0) : 0u, on = past(nr + v0);
   auto issue = [&](int step) {  // thread 0
     const uint32_t n = used + (uint32_t)step, st = n % S;
     wait(&sh.empty[st], ((n / S) & 1u) ^ 1u);
@@ -635,10 +659,13 @@ __device__ __forceinline__ float race_stream(const Racer& c, const T* tr, const 
     const uint32_t to = ring + st * race_stage_bytes<T>(), full = smem_u32(&sh.full[st]);
     const uint32_t count = (uint32_t)min(kRaceElems, 8 * (n8 - step * kRaceThreads));
     const int64_t v = v0 + (int64_t)step * kRaceElems;
-    mbar_arrive_expect_tx(full, count * ((kDraft ? 2 : 1) * (uint32_t)sizeof(T) + 4));
-    bulk_g2s(to, tr + v, count * (uint32_t)sizeof(T), full);
-    if (kDraft) bulk_g2s(to + kLogits, dr + v, count * (uint32_t)sizeof(T), full);
-    bulk_g2s(to + 2 * kLogits, nr + v, count * 4, full);
+    auto bytes = [&](uint32_t off, uint32_t size) { return (off + count * size + 15u) & ~15u; };
+    const uint32_t bt = bytes(ot, sizeof(T)), bd = kDraft ? bytes(od, sizeof(T)) : 0u,
+                   bn = bytes(on, 4);
+    mbar_arrive_expect_tx(full, bt + bd + bn);
+    bulk_g2s(to, reinterpret_cast<const char*>(tr + v) - ot, bt, full);
+    if (kDraft) bulk_g2s(to + kLogits, reinterpret_cast<const char*>(dr + v) - od, bd, full);
+    bulk_g2s(to + 2 * kLogits, reinterpret_cast<const char*>(nr + v) - on, bn, full);
     sh.issued = n + 1;
   };
   if (tid == 0)
@@ -659,7 +686,19 @@ __device__ __forceinline__ float race_stream(const Racer& c, const T* tr, const 
     float most = 0.f;
     float x[8], y[8], e[8];
     const uint32_t at = ring + st * race_stage_bytes<T>();
-    if (k < n8) {
+    // element q of the thread is number first + q * apart from v0 on
+    const int first = kAligned ? 8 * k : step * kRaceElems + tid;
+    constexpr int apart = kAligned ? 1 : kRaceThreads;
+    if (!kAligned) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const uint32_t o = (uint32_t)(tid + q * kRaceThreads);
+        const bool in = first + q * apart < 8 * n8;
+        x[q] = in ? lds_logit(at + ot + o * (uint32_t)sizeof(T), T()) : -INFINITY;
+        y[q] = kDraft && in ? lds_logit(at + kLogits + od + o * (uint32_t)sizeof(T), T()) : -INFINITY;
+        e[q] = in ? lds_logit(at + 2 * kLogits + on + o * 4, float()) : 1.f;
+      }
+    } else if (k < n8) {
       if (W == 1) {
         E::unpack(ld_shared_v4(at + 16 * tid), x);
         if (kDraft) E::unpack(ld_shared_v4(at + kLogits + 16 * tid), y);
@@ -676,7 +715,7 @@ __device__ __forceinline__ float race_stream(const Racer& c, const T* tr, const 
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sh.empty[st]));
-    if (k < n8) {
+    if (!kAligned || k < n8) {
 #pragma unroll
       for (int q = 0; q < 8; q += 2) {
         const uint64_t h =
@@ -695,7 +734,7 @@ __device__ __forceinline__ float race_stream(const Racer& c, const T* tr, const 
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         hi[q] = 0.f;
-        if (k < n8 && 8 * k + q != skip) {
+        if ((!kAligned || k < n8) && first + q * apart != skip) {
           float lo;
           race_bounds(c, x[q], kDraft ? y[q] : 0.f, e[q], lo, hi[q]);
           top = fmaxf(top, lo);
@@ -703,14 +742,14 @@ __device__ __forceinline__ float race_stream(const Racer& c, const T* tr, const 
       }
       bar = race_raise(sh, top);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) race_keep(sh, hi[q], bar, v0 + 8 * (int64_t)k + q);
+      for (int q = 0; q < 8; ++q) race_keep(sh, hi[q], bar, v0 + first + q * apart);
     }
   }
   used += (uint32_t)steps;
   return largest;
 }
 
-template <typename T>
+template <typename T, bool kAligned>
 __device__ Bounds race_bounds_of(const Racer& c, const T* tr, const T* dr, const float* nr,
                                  int64_t v0, int64_t v1, Shared& sh, uint32_t ring,
                                  uint32_t& used) {
@@ -724,23 +763,32 @@ __device__ Bounds race_bounds_of(const Racer& c, const T* tr, const T* dr, const
   __syncthreads();
   // upper bound (that of a skipped token too: it only asks for the exact race)
   float largest = 0.f;
-  int64_t from = v0;
-  const bool vec = (reinterpret_cast<uintptr_t>(tr + v0) | reinterpret_cast<uintptr_t>(nr + v0) |
-                    (c.has_draft ? reinterpret_cast<uintptr_t>(dr + v0) : 0)) % 16 == 0 &&
-                   !c.bigt && !(c.has_draft && c.bigd);
-  if (vec) {
-    const int n8 = (int)((v1 - v0) / 8);
-    largest = c.has_draft ? race_stream<T, true>(c, tr, dr, nr, v0, n8, sh, ring, used)
-                          : race_stream<T, false>(c, tr, dr, nr, v0, n8, sh, ring, used);
-    from = v0 + (int64_t)n8 * 8;
+  // [v0, head) and [tail, v1) are left to single loads
+  int64_t head = v0, tail = v0;
+  const bool usual = !c.bigt && !(c.has_draft && c.bigd);
+  if constexpr (kAligned) {
+    if (usual) {
+      const int n8 = (int)((v1 - v0) / 8);
+      largest = c.has_draft ? race_stream<T, true, true>(c, tr, dr, nr, v0, n8, sh, ring, used)
+                            : race_stream<T, false, true>(c, tr, dr, nr, v0, n8, sh, ring, used);
+      tail = v0 + (int64_t)n8 * 8;
+    }
+  } else if (usual && v1 - v0 >= 32) {
+    head = v0 + 8;
+    const int n8 = (int)((v1 - 8 - head) / 8);
+    largest = c.has_draft ? race_stream<T, true, false>(c, tr, dr, nr, head, n8, sh, ring, used)
+                          : race_stream<T, false, false>(c, tr, dr, nr, head, n8, sh, ring, used);
+    tail = head + (int64_t)n8 * 8;
   }
   constexpr int M = 4;
-  for (int64_t base = from; base < v1; base += kRaceThreads * M) {
+  const int64_t singles = (head - v0) + (v1 - tail);
+  auto single = [&](int64_t k) { return k < head - v0 ? v0 + k : tail + (k - (head - v0)); };
+  for (int64_t base = 0; base < singles; base += kRaceThreads * M) {
     float hi[M], top = 0.f, x[M], y[M], e[M];
 #pragma unroll
     for (int w = 0; w < M; ++w) {
-      const int64_t v = base + w * kRaceThreads + tid;
-      if (v < v1) {
+      const int64_t k = base + w * kRaceThreads + tid, v = single(k);
+      if (k < singles) {
         x[w] = E::load1(tr + v);
         y[w] = c.has_draft ? E::load1(dr + v) : 0.f;
         e[w] = __ldg(nr + v);
@@ -748,9 +796,9 @@ __device__ Bounds race_bounds_of(const Racer& c, const T* tr, const T* dr, const
     }
 #pragma unroll
     for (int w = 0; w < M; ++w) {
-      const int64_t v = base + w * kRaceThreads + tid;
+      const int64_t k = base + w * kRaceThreads + tid;
       hi[w] = 0.f;
-      if (v < v1 && v != c.skip) {
+      if (k < singles && single(k) != c.skip) {
         float lo;
         race_bounds(c, x[w], y[w], e[w], lo, hi[w]);
         top = fmaxf(top, lo);
@@ -759,7 +807,7 @@ __device__ Bounds race_bounds_of(const Racer& c, const T* tr, const T* dr, const
     }
     const float bar = race_raise(sh, top);
 #pragma unroll
-    for (int w = 0; w < M; ++w) race_keep(sh, hi[w], bar, base + w * kRaceThreads + tid);
+    for (int w = 0; w < M; ++w) race_keep(sh, hi[w], bar, single(base + w * kRaceThreads + tid));
   }
   const unsigned wlargest = __reduce_max_sync(0xffffffffu, __float_as_uint(largest));
   if (lane == 0) atomicMax(&sh.top, (int)wlargest);
@@ -864,7 +912,10 @@ __device__ __forceinline__ void cluster_or_cta_sync(uint32_t ranks) {
     __syncthreads();
 }
 
-template <typename T>
+// kAligned: every row of the three arrays, and every slice of one, begins at a
+// 16-byte boundary.  (Two kernels: with both loops in one the registers of the
+// unaligned rows' made the other spill, 102 us for 90 at 128 sequences.)
+template <typename T, bool kAligned>
 __global__ void __launch_bounds__(kRaceThreads, 2) verify_emit_kernel(
     const VerifyParams p, const T* __restrict__ target, const T* __restrict__ draft) {
   extern __shared__ __align__(16) unsigned char emit_ring[];
@@ -957,7 +1008,7 @@ __global__ void __launch_bounds__(kRaceThreads, 2) verify_emit_kernel(
   // depends on comes from what they sent one another.
   for (int round = 0; round < 2; ++round) {
     Bounds own = {0.f, 0.f, -1, 0};
-    if (d.emit == 1) own = race_bounds_of(c, trow, drow, noise, v0, v1, sh, smem_u32(emit_ring), used);
+    if (d.emit == 1) own = race_bounds_of<T, kAligned>(c, trow, drow, noise, v0, v1, sh, smem_u32(emit_ring), used);
     if (tid < (int)ranks) {
       const uint32_t to = (uint32_t)tid;
       const float4 f = make_float4(own.lo, own.hi, __int_as_float(own.token), __int_as_float(own.count));
@@ -1053,6 +1104,52 @@ VerifyLayout verify_layout(int64_t N, int64_t K) {
   return l;
 }
 
+// Clusters of C emitting CTAs that the device runs at once, asked for once.
+template <typename T, bool kAligned>
+cudaError_t clusters_at_once(int C, const DeviceInfo& d, int* n) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices][kMaxCluster + 1];
+  const bool keep = d.device >= 0 && d.device < kDevices;
+  *n = keep ? known[d.device][C].load(std::memory_order_relaxed) : 0;
+  if (*n > 0) return cudaSuccess;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)C;
+  at.val.clusterDim.y = 1;
+  at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)C);
+  cfg.blockDim = dim3(kRaceThreads);
+  cfg.dynamicSmemBytes = race_ring<T>();
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaOccupancyMaxActiveClusters(n, verify_emit_kernel<T, kAligned>, &cfg);
+  if (e == cudaSuccess && keep) known[d.device][C].store(*n < 1 ? 1 : *n, std::memory_order_relaxed);
+  return e;
+}
+
+template <typename T, bool kAligned>
+cudaError_t launch_emit(VerifyParams p, const VerifyArgs& a, const DeviceInfo& d, cudaStream_t st) {
+  cudaError_t e = ensure_dynamic_smem((const void*)verify_emit_kernel<T, kAligned>, (int)race_ring<T>());
+  if (e != cudaSuccess) return e;
+  // the emitting clusters: as many CTAs each as lets all of them run at once, of
+  // at least 8 KiB of logits each (74 clusters of 4 run at once, 36 of 8: 64
+  // sequences with 2, 4, 8 CTAs take 70, 59, 69 us, 32 sequences 56, 45, 40)
+  int C = 1;
+  while (C < kMaxCluster && a.V * (int64_t)sizeof(T) / (2 * C) >= kMinPartBytes) {
+    int fit = 0;
+    e = clusters_at_once<T, kAligned>(2 * C, d, &fit);
+    if (e != cudaSuccess) return e;
+    if (a.N > fit) break;
+    C *= 2;
+  }
+  constexpr int EPV = Elt<T>::kPerVec;
+  p.chunk = ((a.V + C - 1) / C + EPV - 1) / EPV * EPV;
+  return launch_pdl(verify_emit_kernel<T, kAligned>, dim3((unsigned)(a.N * C)), dim3(kRaceThreads),
+                    race_ring<T>(), st, (unsigned)C, p,
+                    static_cast<const T*>(a.target), static_cast<const T*>(a.draft));
+}
+
 template <typename T>
 cudaError_t launch_t(const VerifyArgs& a, const DeviceInfo& d, cudaStream_t st) {
   constexpr int EPV = Elt<T>::kPerVec;
@@ -1060,15 +1157,21 @@ cudaError_t launch_t(const VerifyArgs& a, const DeviceInfo& d, cudaStream_t st) 
   char* ws = static_cast<char*>(a.ws);
   const int64_t row_bytes = a.V * (int64_t)sizeof(T);
   const int kinds = a.draft != nullptr ? 2 : 1;
-  // parts of a row: enough that the first position's rows occupy every SM
-  // four times over, of at least 8 KiB
+  // Parts of a row.  A part costs some 3 us of latencies whatever its size, so
+  // rows are split in halves until two CTAs per SM are reached (8 KiB at least),
+  // further down to 31 KiB until seven are, and down to 96 KiB in any case.  Calls
+  // with 1, 2, 4, 8 parts a row: 144 rows of 304 KB 33.0, 28.3, 26.7, 28.3 us; 256
+  // of 128 KB 20.5, 19.7, 16.3, 18.2; 1,152 of 64 KB 33.9, 35.3, 42.8, 62.7.
+  const int64_t rows = a.N * (a.K + 1) + (kinds == 2 ? a.N * a.K : 0);
   int split = 1, split_log2 = 0;
-  while (split < kMaxSplit && a.N * kinds * split < 4 * (int64_t)d.sms &&
-         row_bytes / (2 * split) >= kMinPartBytes) {
+  while (split < kMaxSplit) {
+    const int64_t half = row_bytes / (2 * split), ctas = rows * 2 * split;
+    if (!((half >= kMinPartBytes && ctas <= 2 * (int64_t)d.sms) ||
+          (half >= 31 * 1024 && ctas <= 7 * (int64_t)d.sms) || half > 48 * 1024))
+      break;
     split *= 2;
     ++split_log2;
   }
-  const int64_t rows = a.N * (a.K + 1) + (kinds == 2 ? a.N * a.K : 0);
   if (rows > INT32_MAX / split) return cudaErrorInvalidValue;  // (refused by api.cu)
   VerifyParams p = {};
   p.N = a.N;
@@ -1098,8 +1201,9 @@ cudaError_t launch_t(const VerifyArgs& a, const DeviceInfo& d, cudaStream_t st) 
   p.split = split;
   p.split_log2 = split_log2;
   p.part_elems = ((a.V + split - 1) / split + EPV - 1) / EPV * EPV;
-  // all rows at once when the GPU takes them at once
-  p.lazy = a.K > 0 && rows * split > 4 * (int64_t)d.sms;
+  // Leaving rows out costs a launch and a ticket per part: 279 MB 54-62 us against
+  // 66 for all rows, 350 MB 89 against 96; but 74 MB 38 against 34, 175 MB the same.
+  p.lazy = a.K > 0 && rows * row_bytes > ((int64_t)192 << 20);
   cudaError_t e;
   if (p.lazy) {
     const int64_t words = a.N * (a.K + 1);
@@ -1115,17 +1219,16 @@ cudaError_t launch_t(const VerifyArgs& a, const DeviceInfo& d, cudaStream_t st) 
   e = launch_pdl(verify_rows_kernel<T>, dim3((unsigned)(rows * split)), dim3(kThreads), kRowRing,
                  st, 1, p, target, draft);
   if (e != cudaSuccess) return e;
-  // the emitting cluster: as many CTAs as the GPU takes at once (two per SM),
-  // of at least 8 KiB of logits each
-  int C = 1;
-  while (C < kMaxCluster && a.N * 2 * C <= 2 * (int64_t)d.sms &&
-         row_bytes / (2 * C) >= kMinPartBytes)
-    C *= 2;
-  p.chunk = ((a.V + C - 1) / C + EPV - 1) / EPV * EPV;
-  e = ensure_dynamic_smem((const void*)verify_emit_kernel<T>, (int)race_ring<T>());
-  if (e != cudaSuccess) return e;
-  return launch_pdl(verify_emit_kernel<T>, dim3((unsigned)(a.N * C)), dim3(kRaceThreads),
-                    race_ring<T>(), st, (unsigned)C, p, target, draft);
+  // every row of the arrays that the race reads at a 16-byte boundary
+  uintptr_t odd = reinterpret_cast<uintptr_t>(a.target) | reinterpret_cast<uintptr_t>(a.noise);
+  if (a.N > 1) odd |= (uintptr_t)a.nld * 4 | (uintptr_t)a.tls * sizeof(T);
+  if (a.K > 0) odd |= (uintptr_t)a.tld * sizeof(T);
+  if (draft != nullptr) {
+    odd |= reinterpret_cast<uintptr_t>(draft);
+    if (a.N > 1) odd |= (uintptr_t)a.dls * sizeof(T);
+    if (a.K > 1) odd |= (uintptr_t)a.dld * sizeof(T);
+  }
+  return odd % 16 == 0 ? launch_emit<T, true>(p, a, d, st) : launch_emit<T, false>(p, a, d, st);
 }
 
 }  // namespace
