@@ -235,17 +235,18 @@ struct SortPlan {
 };
 
 // Columns per thread of the summing kernel: 8 side by side of 16-byte aligned
-// rows; else 4, a row's threads apart, so that neighbours read neighbouring
-// elements.
-__host__ __device__ constexpr int sum_cols(bool vec) { return vec ? 8 : 4; }
-// Threads per row, and the columns of a row of partial sums: whole CTAs of
-// threads.
+// rows (vec); else 8 of a warp's 256, 32 apart, so that a warp's stores meet.
+constexpr int kSumCols = 8;
+constexpr int kWarpCols = 32 * kSumCols;
+// Threads per row (whole warps where rows are not aligned), and the columns of
+// a row of partial sums: whole CTAs of threads.
 int row_threads(int64_t d, bool vec) {
-  const int64_t units = (d + sum_cols(vec) - 1) / sum_cols(vec);
+  const int64_t units =
+      vec ? (d + kSumCols - 1) / kSumCols : (d + kWarpCols - 1) / kWarpCols * 32;
   return (int)(units < kThreads ? units : kThreads);
 }
 int64_t padded_cols(int64_t d, bool vec) {
-  const int64_t cols = sum_cols(vec) * (int64_t)row_threads(d, vec);
+  const int64_t cols = kSumCols * (int64_t)row_threads(d, vec);
   return (d + cols - 1) / cols * cols;
 }
 
@@ -466,12 +467,18 @@ __global__ void __launch_bounds__(kSortThreads) embed_scatter_kernel(
     const int any = __syncthreads_or((int)f);
     if (tid == 0) hdr->flags = any ? kFlagTokenRange : 0u;
   }
+  // (16 tiles' counts in flight at a time)
   int32_t before = 0, total = 0;
-#pragma unroll 8
-  for (int t = 0; t < tiles; ++t) {
-    const int32_t c = hist[(int64_t)t * kMaxBins + tid];
-    before += t < (int)blockIdx.x ? c : 0;
-    total += c;
+  for (int t0 = 0; t0 < tiles; t0 += 16) {
+    int32_t c[16];
+#pragma unroll
+    for (int u = 0; u < 16; ++u)
+      c[u] = t0 + u < tiles ? hist[(int64_t)(t0 + u) * kMaxBins + tid] : 0;
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+      before += t0 + u < (int)blockIdx.x ? c[u] : 0;
+      total += c[u];
+    }
   }
   bin_bases(sh, total, before);
   const int64_t a = (int64_t)blockIdx.x * tile, b = min(a + tile, n);
@@ -563,11 +570,12 @@ struct SegParams {
   int cols;         // columns of one CTA in y
 };
 
-// A thread's C columns of a row of dW: contiguous (8) or `step` apart (4).
+// A thread's 8 columns of a row of dW: contiguous or 32 apart, `left` of the
+// row from the first on.
 template <typename TW, bool kVec>
-__device__ __forceinline__ void write_row(TW* row, int step, int left, bool accumulate,
-                                          float scale, const float* acc) {
-  constexpr int C = sum_cols(kVec);
+__device__ __forceinline__ void write_row(TW* row, int left, bool accumulate, float scale,
+                                          const float* acc) {
+  constexpr int C = kSumCols, step = 32;
   float x[8];
 #pragma unroll
   for (int k = 0; k < C; ++k) x[k] = acc[k] * scale;
@@ -598,14 +606,31 @@ __device__ __forceinline__ void write_row(TW* row, int step, int left, bool accu
   }
 }
 
-// Bytes a thread of the summing kernel has on their way: kSumDepth rows of 8
-// columns, asynchronous copies through a ring of its own in shared memory
-// (rows of any alignment: kSumRegs rows in registers instead).
-template <typename TD>
+// What is on its way for a thread of the summing kernel: sum_depth rows of 8
+// columns, asynchronous copies through a ring in shared memory.  Of aligned rows
+// a thread copies its own columns; of others a warp copies the 16-byte pieces
+// that hold its columns (one more than they fill), and every lane reads single
+// elements of them.
+template <typename TD, bool kVec>
 __host__ __device__ constexpr int sum_depth() {
-  return sizeof(TD) == 4 ? 4 : 8;
+  return kVec && sizeof(TD) == 4 ? 4 : 8;
 }
-constexpr int kSumRegs = 8;
+// bytes of one row in the ring: of a thread's columns, or of a warp's
+template <typename TD, bool kVec>
+__host__ __device__ inline int sum_slot(int64_t d) {
+  if (kVec) return kSumCols * (int)sizeof(TD);
+  return ((int)(d < kWarpCols ? d : kWarpCols) * (int)sizeof(TD) + 30) / 16 * 16;
+}
+__device__ __forceinline__ float lds_elt(uint32_t at, uint16_t) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+  return bf16_bits_to_float(v);
+}
+__device__ __forceinline__ float lds_elt(uint32_t at, float) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+  return v;
+}
 constexpr int kMaxGroups = 32;
 
 // A group of `tpr` threads takes Q sorted entries (a tile), C columns per
@@ -616,15 +641,16 @@ constexpr int kMaxGroups = 32;
 // same keys: the id at a tile's first entry a is split iff it began before the
 // previous tile (key[a - Q - 1]) or reaches past this one (key[a + Q]).
 // HBM-bound at many tokens: 65,536 rows of 896 float32 (235 MB) in 50 us, with
-// 8 rows in registers 62 us.
+// 8 rows in registers 62 us.  Rows of 901 bfloat16 (65,172 of them): 35 us, 145 with single
+// loads into registers.
 template <typename TD, typename TW, bool kVec, bool kAcc>
 __global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const SegParams p,
                                                                 const TD* __restrict__ dout,
                                                                 TW* dw) {
-  extern __shared__ __align__(16) unsigned char sum_ring[];
+  extern __shared__ __align__(16) unsigned char sum_ring_raw[];
   __shared__ int32_t s_key[(kMaxGroups + 1) * kMaxSegEntries];
   __shared__ int32_t s_pos[(kMaxGroups + 1) * kMaxSegEntries];
-  constexpr int C = sum_cols(kVec);
+  constexpr int C = kSumCols;
   const int Q = p.seg;
   pdl_wait();
   pdl_trigger();
@@ -646,10 +672,11 @@ __global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const SegParams 
   const int32_t next2 = live && b + Q < p.n ? p.key[b + Q] : -1;
   __syncthreads();
   if (!live) return;
-  const int64_t c0 = (int64_t)blockIdx.y * p.cols + (kVec ? 8 * l : l);
-  const int left = (int)min((int64_t)p.cols, p.d - (int64_t)blockIdx.y * p.cols) - (kVec ? 8 * l : l);
-  const int step = p.tpr;
-  if (left <= 0) return;
+  // first column, and the columns of the CTA from there on
+  const int lane = tid & 31, cl = kVec ? 8 * l : l / 32 * kWarpCols + lane;
+  const int64_t c0 = (int64_t)blockIdx.y * p.cols + cl;
+  const int left = (int)min((int64_t)p.cols, p.d - (int64_t)blockIdx.y * p.cols) - cl;
+  if (left + (kVec ? 0 : lane) <= 0) return;  // (a whole warp, where rows are not aligned)
   const int32_t* key = s_key + grp * Q;
   const int32_t* pos = s_pos + grp * Q;
   const int nb = (int)(b - a);  // entries of the tile
@@ -684,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const SegParams 
     if (open)
       flush_part(0);
     else
-      write_row<TW, kVec>(dw + cur * p.ldw + c0, step, left, kAcc, p.scale, acc);
+      write_row<TW, kVec>(dw + cur * p.ldw + c0, left, kAcc, p.scale, acc);
   };
   auto take = [&](int e, const float* v) {
     const int32_t k = key[e];
@@ -702,8 +729,8 @@ __global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const SegParams 
     }
   };
   if constexpr (kVec) {
-    constexpr int kDepth = sum_depth<TD>(), kUnit = 8 * (int)sizeof(TD);
-    const uint32_t mine = smem_u32(sum_ring) + tid * kUnit;  // slot k: + k * kThreads * kUnit
+    constexpr int kDepth = sum_depth<TD, true>(), kUnit = 8 * (int)sizeof(TD);
+    const uint32_t mine = smem_u32(sum_ring_raw) + tid * kUnit;  // slot k: + k * kThreads * kUnit
     auto issue = [&](int e, int slot) {
       if (e < e1) {
         const char* src = reinterpret_cast<const char*>(dout + (int64_t)pos[e] * p.ldd + c0);
@@ -731,20 +758,46 @@ __global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const SegParams 
     }
     cp_async_wait<0>();
   } else {
-#pragma unroll 1
-    for (int e = e0; e < e1; e += kSumRegs) {
-      float v[kSumRegs][C];
+    constexpr int kDepth = sum_depth<TD, false>(), kElt = (int)sizeof(TD);
+    constexpr int kPieces = (kWarpCols * kElt + 16 + 511) / 512;  // of 16 bytes, per lane
+    const uint32_t row_bytes = (uint32_t)sum_slot<TD, false>(p.d);
+    const uint32_t ring0 = smem_u32(sum_ring_raw) + tid / 32 * (kDepth * row_bytes);
+    const uint32_t ring1 = ring0 + kDepth * row_bytes;
+    const char* col = reinterpret_cast<const char*>(dout + (c0 - lane));  // the warp's first column
+    const int width = min(kWarpCols, left + lane) * kElt;
+    const int64_t pitch = p.ldd * kElt;
+    // bytes of the row's columns behind a 16-byte boundary
+    const uint32_t col4 = (uint32_t)reinterpret_cast<uintptr_t>(col), pitch4 = (uint32_t)pitch;
+    auto past = [&](int e) { return (col4 + (uint32_t)pos[e] * pitch4) & 15u; };
+    auto issue = [&](int e, uint32_t to) {
+      if (e < e1) {
+        const int off = (int)past(e), n = off + width - 16 * lane;
+        const char* src = col + pos[e] * pitch + (16 * lane - off);
 #pragma unroll
-      for (int u = 0; u < kSumRegs; ++u) {
-        if (e + u >= e1) continue;
-        const TD* row = dout + (int64_t)pos[e + u] * p.ldd + c0;
-#pragma unroll
-        for (int c = 0; c < C; ++c) v[u][c] = c * step < left ? Elt<TD>::load1(row + c * step) : 0.f;
+        for (int q = 0; q < kPieces; ++q)
+          if (512 * q < n) cp_async16(to + 16 * lane + 512 * q, src + 512 * q);
       }
+      cp_async_commit();
+    };
 #pragma unroll
-      for (int u = 0; u < kSumRegs; ++u)
-        if (e + u < e1) take(e + u, v[u]);
+    for (int k = 0; k < kDepth; ++k) issue(e0 + k, ring0 + k * row_bytes);
+    uint32_t at = ring0;
+#pragma unroll 1
+    for (int e = e0; e < e1; ++e) {
+      cp_async_wait<kDepth - 1>();
+      __syncwarp();
+      // (columns behind the row's end: whatever is there, never written)
+      const uint32_t from = at + past(e) + lane * kElt;
+      float v[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c) v[c] = lds_elt(from + c * (32 * kElt), TD());
+      __syncwarp();
+      take(e, v);
+      issue(e + kDepth, at);
+      at += row_bytes;
+      if (at == ring1) at = ring0;
     }
+    cp_async_wait<0>();
   }
   if (split && cur == last) {
     flush_part(open ? 0 : 1);
@@ -810,7 +863,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(const SegPa
         s.w += q.w;
       }
       const float x[4] = {s.x, s.y, s.z, s.w};
-      constexpr int C = sum_cols(kVec);
+      constexpr int C = kSumCols;
       const int64_t cy = c / p.cols;               // the CTA column of embed_sum_kernel
       const int64_t unit = (c - cy * p.cols) / C;  // its thread
       const int o = (int)(c % C);
@@ -818,7 +871,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(const SegPa
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         // the partial sums hold each thread's columns side by side
-        const int64_t in = kVec ? C * unit + o + k : unit + (int64_t)(o + k) * p.tpr;
+        const int64_t in = kVec ? C * unit + o + k
+                                : unit / 32 * kWarpCols + unit % 32 + 32 * (o + k);
         if (in < ncy && unit < p.tpr) {
           TW* q = dw + v * p.ldw + cy * p.cols + in;
           float y = x[k] * p.scale;
@@ -841,7 +895,10 @@ cudaError_t launch_sums(const EmbedBwdArgs& a, SegParams p, const DeviceInfo& de
   const unsigned ny = (unsigned)((p.d + p.cols - 1) / p.cols);
   const int64_t seg_tiles = (p.n + p.seg - 1) / p.seg;
   const int64_t blocks = (seg_tiles + p.groups - 1) / p.groups;
-  const size_t ring = kVec ? (size_t)sum_depth<TD>() * kThreads * 8 * sizeof(TD) : 0;
+  // (a warp reads 256 columns of its last row whatever the width)
+  const size_t ring =
+      (size_t)sum_depth<TD, kVec>() * (kVec ? kThreads : kWarps) * sum_slot<TD, kVec>(p.d) +
+      (kVec ? 0 : kWarpCols * sizeof(TD));
   cudaError_t e = ensure_dynamic_smem((const void*)embed_sum_kernel<TD, TW, kVec, kAcc>, (int)ring);
   if (e != cudaSuccess) return e;
   e = launch_pdl(embed_sum_kernel<TD, TW, kVec, kAcc>, dim3((unsigned)blocks, ny), dim3(kThreads),
@@ -970,7 +1027,7 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, const DeviceInfo& dev, cudaS
   p.groups = kThreads / p.tpr;
   if (p.groups > kMaxGroups) p.groups = kMaxGroups;
   if (p.groups > per) p.groups = per < 1 ? 1 : (int)per;
-  p.cols = sum_cols(vec) * p.tpr;
+  p.cols = kSumCols * p.tpr;
   if (a.ddtype == 0)
     return a.wdtype == 0 ? launch_sums_t<float, float>(a, p, vec, dev, st)
                          : launch_sums_t<float, uint16_t>(a, p, vec, dev, st);
