@@ -20,83 +20,142 @@ namespace grpo {
 namespace {
 
 // ---------------------------------------------------------------------------
-// element access: 8 columns per thread
+// rows of any alignment
 // ---------------------------------------------------------------------------
 
-// A thread's 8 columns of a row of any alignment: the first at p, `step` apart,
-// `left` columns of the row from p on.
+// A warp takes 256 columns of a row at a time, 8 per lane, 32 apart (so that its
+// stores meet): the 16-byte pieces that hold them go to shared memory by
+// asynchronous copies, several rows ahead, and every lane reads single elements
+// of them.
+constexpr int kWarpCols = 256;
+// bytes of one row's pieces (one more than its columns fill), and of a CTA's
+// rings: a warp reads 256 columns of the last row whatever its width
+inline int warp_slot(int64_t d, size_t esize) {
+  return ((int)(d < kWarpCols ? d : kWarpCols) * (int)esize + 30) / 16 * 16;
+}
+inline size_t warp_rings(int64_t d, size_t esize, int depth) {
+  return (size_t)kWarps * depth * warp_slot(d, esize) + kWarpCols * esize;
+}
+__device__ __forceinline__ float lds_elt(uint32_t at, uint16_t) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+  return bf16_bits_to_float(v);
+}
+__device__ __forceinline__ float lds_elt(uint32_t at, float) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+  return v;
+}
+// The pieces of `width` bytes from p on, by the warp; `off` bytes of them lie
+// before p.
 template <typename T>
-struct Cols8 {
-  __device__ static void load(const T* p, int step, int left, float* x) {
+__device__ __forceinline__ void copy_pieces(uint32_t to, const char* p, int off, int width) {
+  constexpr int kPieces = (kWarpCols * (int)sizeof(T) + 16 + 511) / 512;
+  const int lane = threadIdx.x & 31, n = off + width - 16 * lane;
+  const char* src = p + (16 * lane - off);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = k * step < left ? Elt<T>::load1(p + k * step) : 0.f;
-  }
-  __device__ static void store(T* p, int step, int left, const float* x) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k * step < left) Elt<T>::store1(p + k * step, x[k]);
-  }
-};
+  for (int q = 0; q < kPieces; ++q)
+    if (512 * q < n) cp_async16(to + 16 * lane + 512 * q, src + 512 * q);
+}
 
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-
-// Any alignment (5,001 rows of 901 elements, float32 to bfloat16: 6 us): one
-// CTA copies `rows` rows; its threads walk the rows' units
-// of 8 columns (unit c of a row: columns c, c + nu, ... c + 7 nu), U of them
-// in flight each: first the units' ids, then the rows, then the stores.
-template <typename TW, typename TO, int U>
-__global__ void __launch_bounds__(kThreads) embed_fwd_any_kernel(
-    const int64_t* __restrict__ ids, int64_t n, const TW* __restrict__ w, int64_t V, int64_t d,
-    int64_t ldw, float scale, TO* __restrict__ out, int64_t ldo, int rows, int nu) {
-  pdl_wait();
-  pdl_trigger();
-  const int64_t row0 = (int64_t)blockIdx.x * rows;
-  const int nrows = (int)min((int64_t)rows, n - row0);
-  int r = threadIdx.x / nu, c = threadIdx.x - r * nu;
-  const int dr = kThreads / nu, dc = kThreads - dr * nu;
-  while (r < nrows) {
-    int64_t id[U];
-    int rr[U], cc[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      rr[u] = r;
-      cc[u] = c;
-      id[u] = r < nrows ? __ldg(ids + row0 + r) : 0;
-      c += dc;
-      r += dr;
-      if (c >= nu) {
-        c -= nu;
-        ++r;
-      }
-    }
-    float x[U][8];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (rr[u] >= nrows) continue;
-      if (id[u] >= 0 && id[u] < V) {
-        Cols8<TW>::load(w + id[u] * ldw + cc[u], nu, (int)d - cc[u], x[u]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[u][e] = __int_as_float(0x7fc00000);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (rr[u] >= nrows) continue;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[u][e] *= scale;
-      Cols8<TO>::store(out + (row0 + rr[u]) * ldo + cc[u], nu, (int)d - cc[u], x[u]);
-    }
-  }
-}
 
 constexpr int kFwdIds = 512;  // rows of a CTA whose ids wait in shared memory
 // units (8 columns) a thread has on their way: 128 bytes
 template <typename TW>
 __host__ __device__ constexpr int fwd_depth() {
   return sizeof(TW) == 4 ? 4 : 8;
+}
+
+// the same in rows' parts of 256 columns, of a warp
+template <typename TW>
+__host__ __device__ constexpr int any_depth() {
+  return sizeof(TW) == 4 ? 4 : 8;
+}
+
+// Rows of any alignment: a CTA takes a run of rows, its warps every eighth of
+// the rows' parts of 256 columns.  65,536 rows of 901 bfloat16 to float32 in 47 us,
+// 79 with loads straight into registers.
+template <typename TW, typename TO>
+__global__ void __launch_bounds__(kThreads) embed_fwd_any_kernel(
+    const int64_t* __restrict__ ids, int64_t n, const TW* __restrict__ w, int64_t V, int64_t d,
+    int64_t ldw, float scale, TO* __restrict__ out, int64_t ldo, int rows, int slot_bytes) {
+  constexpr int kElt = (int)sizeof(TW), kDepth = any_depth<TW>();
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ int32_t s_id[kFwdIds];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_trigger();
+  const int64_t row0 = (int64_t)blockIdx.x * rows;
+  const int nrows = (int)min((int64_t)rows, n - row0);
+  for (int k = tid; k < nrows; k += kThreads) {
+    const int64_t id = __ldg(ids + row0 + k);
+    s_id[k] = id >= 0 && id < V ? (int32_t)id : -1;
+  }
+  __syncthreads();
+  struct At {
+    int r, c;  // row of the CTA, first column
+  };
+  const int parts = (int)((d + kWarpCols - 1) / kWarpCols);
+  const int dr = kWarps / parts, dc = (kWarps - dr * parts) * kWarpCols;
+  auto step = [&](At& a) {
+    a.c += dc;
+    a.r += dr;
+    if (a.c >= parts * kWarpCols) {
+      a.c -= parts * kWarpCols;
+      ++a.r;
+    }
+  };
+  At get = {warp / parts, warp % parts * kWarpCols}, put = get;
+  const uint32_t ring0 = smem_u32(ring) + warp * (kDepth * slot_bytes);
+  const uint32_t ring1 = ring0 + kDepth * slot_bytes;
+  const int64_t pitch = ldw * kElt;
+  const char* base = reinterpret_cast<const char*>(w);
+  auto past = [&](int32_t id, int c) {
+    return ((uint32_t)reinterpret_cast<uintptr_t>(base) + (uint32_t)id * (uint32_t)pitch + c * kElt) & 15u;
+  };
+  auto issue = [&](uint32_t to) {
+    if (get.r < nrows) {
+      const int32_t id = s_id[get.r];
+      if (id >= 0)
+        copy_pieces<TW>(to, base + id * pitch + get.c * kElt, (int)past(id, get.c),
+                        (int)min((int64_t)kWarpCols, d - get.c) * kElt);
+    }
+    cp_async_commit();
+    step(get);
+  };
+#pragma unroll 1
+  for (int k = 0; k < kDepth; ++k) issue(ring0 + k * slot_bytes);
+  uint32_t at = ring0;
+  while (put.r < nrows) {
+    cp_async_wait<kDepth - 1>();
+    __syncwarp();
+    // (an id outside the table: NaN whatever is there)
+    const int32_t id = s_id[put.r];
+    const uint32_t from = at + past(id, put.c) + lane * kElt;
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = lds_elt(from + k * (32 * kElt), TW());
+    __syncwarp();
+    TO* q = out + (row0 + put.r) * ldo + put.c + lane;
+    const float f = id < 0 ? __int_as_float(0x7fc00000) : scale;
+    if (d - put.c >= kWarpCols) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) Elt<TO>::store1(q + 32 * k, x[k] * f);
+    } else {
+      const int left = (int)(d - put.c) - lane;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (32 * k < left) Elt<TO>::store1(q + 32 * k, x[k] * f);
+    }
+    step(put);
+    issue(at);
+    at += slot_bytes;
+    if (at == ring1) at = ring0;
+  }
+  cp_async_wait<0>();
 }
 
 // 16-byte aligned rows.  A CTA takes a run of rows; their ids are loaded
@@ -180,31 +239,31 @@ cudaError_t launch_fwd_t(const EmbedFwdArgs& a, const DeviceInfo& dev, cudaStrea
   const int nu = (int)((a.d + 7) / 8);
   const TW* w = static_cast<const TW*>(a.weight);
   TO* out = static_cast<TO*>(a.out);
-  if (!vec) {
-    constexpr int U = 4;
-    // a CTA's units fill one unrolled step of its threads, unless that leaves
-    // SMs without a CTA
-    int64_t rows = kThreads * U / nu;
-    const int64_t spread = a.n / (2 * (int64_t)dev.sms);
-    if (rows > spread) rows = spread;
-    if (rows < 1) rows = 1;
-    return launch_pdl(embed_fwd_any_kernel<TW, TO, U>, dim3((unsigned)((a.n + rows - 1) / rows)),
-                      dim3(kThreads), 0, st, 1, a.ids, a.n, w, a.V, a.d, a.ldw, a.scale, out, a.ldo,
-                      (int)rows, nu);
-  }
   // runs of rows: 24 CTAs per SM one after the other (31.0 us at 81,920 rows of
   // 896 bfloat16; 6 per SM, all at once, 35.8; 48, 33.5), but not below one ring
-  // of units per thread while two CTAs per SM are left
+  // per thread while two CTAs per SM are left (a warp of unaligned rows: two
+  // parts of a row, 5,001 rows of 901 floats 6.2 us; eight, 8.0)
   int64_t rows = (a.n + 24 * (int64_t)dev.sms - 1) / (24 * (int64_t)dev.sms);
-  const int64_t full = (kThreads * fwd_depth<TW>() + nu - 1) / nu;
+  const int64_t parts = (a.d + kWarpCols - 1) / kWarpCols;
+  const int64_t full = vec ? (kThreads * fwd_depth<TW>() + nu - 1) / nu
+                           : (2 * kWarps + parts - 1) / parts;
   const int64_t spread = (a.n + 2 * (int64_t)dev.sms - 1) / (2 * (int64_t)dev.sms);
   if (rows < full) rows = full < spread ? full : spread;
   if (rows > kFwdIds) rows = kFwdIds;
+  const unsigned grid = (unsigned)((a.n + rows - 1) / rows);
+  if (!vec) {
+    const size_t smem = warp_rings(a.d, sizeof(TW), any_depth<TW>());
+    const cudaError_t e = ensure_dynamic_smem((const void*)embed_fwd_any_kernel<TW, TO>, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(embed_fwd_any_kernel<TW, TO>, dim3(grid), dim3(kThreads), smem, st, 1, a.ids,
+                      a.n, w, a.V, a.d, a.ldw, a.scale, out, a.ldo, (int)rows,
+                      warp_slot(a.d, sizeof(TW)));
+  }
   // an output larger than half of L2 is not kept there for its reader
   const bool stream = (size_t)a.n * (size_t)a.d * sizeof(TO) > ((size_t)64 << 20);
   auto kern = stream ? embed_fwd_kernel<TW, TO, true> : embed_fwd_kernel<TW, TO, false>;
   const size_t smem = (size_t)fwd_depth<TW>() * kThreads * 8 * sizeof(TW);
-  return launch_pdl(kern, dim3((unsigned)((a.n + rows - 1) / rows)), dim3(kThreads), smem, st, 1,
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, 1,
                     a.ids, a.n, w, a.V, a.ldw, a.scale, out, a.ldo, (int)rows, nu);
 }
 
@@ -237,7 +296,6 @@ struct SortPlan {
 // Columns per thread of the summing kernel: 8 side by side of 16-byte aligned
 // rows (vec); else 8 of a warp's 256, 32 apart, so that a warp's stores meet.
 constexpr int kSumCols = 8;
-constexpr int kWarpCols = 32 * kSumCols;
 // Threads per row (whole warps where rows are not aligned), and the columns of
 // a row of partial sums: whole CTAs of threads.
 int row_threads(int64_t d, bool vec) {
@@ -568,6 +626,7 @@ struct SegParams {
   int seg;          // sorted entries per tile
   int tpr, groups;  // threads per row, rows side by side in a CTA
   int cols;         // columns of one CTA in y
+  int slot;         // bytes of a row in a warp's ring (rows that are not aligned)
 };
 
 // A thread's 8 columns of a row of dW: contiguous or 32 apart, `left` of the
@@ -606,31 +665,13 @@ __device__ __forceinline__ void write_row(TW* row, int left, bool accumulate, fl
   }
 }
 
-// What is on its way for a thread of the summing kernel: sum_depth rows of 8
-// columns, asynchronous copies through a ring in shared memory.  Of aligned rows
-// a thread copies its own columns; of others a warp copies the 16-byte pieces
-// that hold its columns (one more than they fill), and every lane reads single
-// elements of them.
-template <typename TD, bool kVec>
+// Aligned rows that a thread of the summing kernel has on their way, copied
+// through a ring of its own in shared memory: 128 bytes of them.
+template <typename TD>
 __host__ __device__ constexpr int sum_depth() {
-  return kVec && sizeof(TD) == 4 ? 4 : 8;
+  return sizeof(TD) == 4 ? 4 : 8;
 }
-// bytes of one row in the ring: of a thread's columns, or of a warp's
-template <typename TD, bool kVec>
-__host__ __device__ inline int sum_slot(int64_t d) {
-  if (kVec) return kSumCols * (int)sizeof(TD);
-  return ((int)(d < kWarpCols ? d : kWarpCols) * (int)sizeof(TD) + 30) / 16 * 16;
-}
-__device__ __forceinline__ float lds_elt(uint32_t at, uint16_t) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
-  return bf16_bits_to_float(v);
-}
-__device__ __forceinline__ float lds_elt(uint32_t at, float) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
-  return v;
-}
+constexpr int kSumAnyDepth = 6;  // rows of a warp, of any alignment
 constexpr int kMaxGroups = 32;
 
 // A group of `tpr` threads takes Q sorted entries (a tile), C columns per
@@ -647,7 +688,7 @@ template <typename TD, typename TW, bool kVec, bool kAcc>
 __global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const SegParams p,
                                                                 const TD* __restrict__ dout,
                                                                 TW* dw) {
-  extern __shared__ __align__(16) unsigned char sum_ring_raw[];
+  extern __shared__ __align__(16) unsigned char sum_ring[];
   __shared__ int32_t s_key[(kMaxGroups + 1) * kMaxSegEntries];
   __shared__ int32_t s_pos[(kMaxGroups + 1) * kMaxSegEntries];
   constexpr int C = kSumCols;
@@ -729,8 +770,8 @@ __global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const SegParams 
     }
   };
   if constexpr (kVec) {
-    constexpr int kDepth = sum_depth<TD, true>(), kUnit = 8 * (int)sizeof(TD);
-    const uint32_t mine = smem_u32(sum_ring_raw) + tid * kUnit;  // slot k: + k * kThreads * kUnit
+    constexpr int kDepth = sum_depth<TD>(), kUnit = 8 * (int)sizeof(TD);
+    const uint32_t mine = smem_u32(sum_ring) + tid * kUnit;  // slot k: + k * kThreads * kUnit
     auto issue = [&](int e, int slot) {
       if (e < e1) {
         const char* src = reinterpret_cast<const char*>(dout + (int64_t)pos[e] * p.ldd + c0);
@@ -758,11 +799,9 @@ __global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const SegParams 
     }
     cp_async_wait<0>();
   } else {
-    constexpr int kDepth = sum_depth<TD, false>(), kElt = (int)sizeof(TD);
-    constexpr int kPieces = (kWarpCols * kElt + 16 + 511) / 512;  // of 16 bytes, per lane
-    const uint32_t row_bytes = (uint32_t)sum_slot<TD, false>(p.d);
-    const uint32_t ring0 = smem_u32(sum_ring_raw) + tid / 32 * (kDepth * row_bytes);
-    const uint32_t ring1 = ring0 + kDepth * row_bytes;
+    constexpr int kDepth = kSumAnyDepth, kElt = (int)sizeof(TD);
+    const uint32_t ring0 = smem_u32(sum_ring) + tid / 32 * (kDepth * p.slot);
+    const uint32_t ring1 = ring0 + kDepth * p.slot;
     const char* col = reinterpret_cast<const char*>(dout + (c0 - lane));  // the warp's first column
     const int width = min(kWarpCols, left + lane) * kElt;
     const int64_t pitch = p.ldd * kElt;
@@ -770,17 +809,11 @@ __global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const SegParams 
     const uint32_t col4 = (uint32_t)reinterpret_cast<uintptr_t>(col), pitch4 = (uint32_t)pitch;
     auto past = [&](int e) { return (col4 + (uint32_t)pos[e] * pitch4) & 15u; };
     auto issue = [&](int e, uint32_t to) {
-      if (e < e1) {
-        const int off = (int)past(e), n = off + width - 16 * lane;
-        const char* src = col + pos[e] * pitch + (16 * lane - off);
-#pragma unroll
-        for (int q = 0; q < kPieces; ++q)
-          if (512 * q < n) cp_async16(to + 16 * lane + 512 * q, src + 512 * q);
-      }
+      if (e < e1) copy_pieces<TD>(to, col + pos[e] * pitch, (int)past(e), width);
       cp_async_commit();
     };
 #pragma unroll
-    for (int k = 0; k < kDepth; ++k) issue(e0 + k, ring0 + k * row_bytes);
+    for (int k = 0; k < kDepth; ++k) issue(e0 + k, ring0 + k * p.slot);
     uint32_t at = ring0;
 #pragma unroll 1
     for (int e = e0; e < e1; ++e) {
@@ -794,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const SegParams 
       __syncwarp();
       take(e, v);
       issue(e + kDepth, at);
-      at += row_bytes;
+      at += p.slot;
       if (at == ring1) at = ring0;
     }
     cp_async_wait<0>();
@@ -895,10 +928,8 @@ cudaError_t launch_sums(const EmbedBwdArgs& a, SegParams p, const DeviceInfo& de
   const unsigned ny = (unsigned)((p.d + p.cols - 1) / p.cols);
   const int64_t seg_tiles = (p.n + p.seg - 1) / p.seg;
   const int64_t blocks = (seg_tiles + p.groups - 1) / p.groups;
-  // (a warp reads 256 columns of its last row whatever the width)
   const size_t ring =
-      (size_t)sum_depth<TD, kVec>() * (kVec ? kThreads : kWarps) * sum_slot<TD, kVec>(p.d) +
-      (kVec ? 0 : kWarpCols * sizeof(TD));
+      kVec ? (size_t)sum_depth<TD>() * kThreads * kSumCols * sizeof(TD) : warp_rings(p.d, sizeof(TD), kSumAnyDepth);
   cudaError_t e = ensure_dynamic_smem((const void*)embed_sum_kernel<TD, TW, kVec, kAcc>, (int)ring);
   if (e != cudaSuccess) return e;
   e = launch_pdl(embed_sum_kernel<TD, TW, kVec, kAcc>, dim3((unsigned)blocks, ny), dim3(kThreads),
@@ -1028,6 +1059,7 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, const DeviceInfo& dev, cudaS
   if (p.groups > kMaxGroups) p.groups = kMaxGroups;
   if (p.groups > per) p.groups = per < 1 ? 1 : (int)per;
   p.cols = kSumCols * p.tpr;
+  p.slot = warp_slot(a.d, de);
   if (a.ddtype == 0)
     return a.wdtype == 0 ? launch_sums_t<float, float>(a, p, vec, dev, st)
                          : launch_sums_t<float, uint16_t>(a, p, vec, dev, st);
