@@ -647,6 +647,10 @@ __device__ __forceinline__ void write_row(TW* row, int left, bool accumulate, fl
 #pragma unroll
       for (int k = 0; k < 8; ++k) x[k] += o[k];
     }
+    if (sizeof(TW) == 4 && reinterpret_cast<uintptr_t>(row) % 32 == 0) {
+      st_32bytes<false>(row, x);
+      return;
+    }
 #pragma unroll
     for (int k = 0; k < Vec8<TW>::kWords; ++k)
       reinterpret_cast<uint4*>(row)[k] = Elt<TW>::pack(x + k * Elt<TW>::kPerVec);
