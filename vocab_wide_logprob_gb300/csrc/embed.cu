@@ -13,6 +13,8 @@
 // 81,920 rows of 896 bfloat16 looked up in 31 us (147 MB written, 46 MB of
 // distinct rows read); the gradient of 131,072 tokens (half of them padding)
 // over 151,936 ids in 140 us, 82 us of it the zeros of the 545 MB result.
+#include <type_traits>
+
 #include "host_ctx.cuh"
 #include "ops.cuh"
 
@@ -47,7 +49,12 @@ __device__ __forceinline__ float lds_elt(uint32_t at, float) {
   return v;
 }
 // The pieces of `width` bytes from p on, by the warp; `off` bytes of them lie
-// before p.
+// before p.  Through L1: neighbouring parts share a piece, and the rows of
+// frequent ids would queue at their L2 slices (130,000 rows of 130 floats of 2,979
+// ids: 20 us, 25 past L1; but 30,000 rows of 2,047 of 60,000 ids 50, 46).
+__device__ __forceinline__ void cp_async16_l1(uint32_t smem_dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(src) : "memory");
+}
 template <typename T>
 __device__ __forceinline__ void copy_pieces(uint32_t to, const char* p, int off, int width) {
   constexpr int kPieces = (kWarpCols * (int)sizeof(T) + 16 + 511) / 512;
@@ -55,7 +62,7 @@ __device__ __forceinline__ void copy_pieces(uint32_t to, const char* p, int off,
   const char* src = p + (16 * lane - off);
 #pragma unroll
   for (int q = 0; q < kPieces; ++q)
-    if (512 * q < n) cp_async16(to + 16 * lane + 512 * q, src + 512 * q);
+    if (512 * q < n) cp_async16_l1(to + 16 * lane + 512 * q, src + 512 * q);
 }
 
 // ---------------------------------------------------------------------------
@@ -135,21 +142,26 @@ __global__ void __launch_bounds__(kThreads) embed_fwd_any_kernel(
     // (an id outside the table: NaN whatever is there)
     const int32_t id = s_id[put.r];
     const uint32_t from = at + past(id, put.c) + lane * kElt;
-    float x[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = lds_elt(from + k * (32 * kElt), TW());
-    __syncwarp();
     TO* q = out + (row0 + put.r) * ldo + put.c + lane;
     const float f = id < 0 ? __int_as_float(0x7fc00000) : scale;
-    if (d - put.c >= kWarpCols) {
+    // (32 N columns, or up to as many)
+    auto copy = [&](auto cols, int left) {
+      constexpr int N = decltype(cols)::value;
+      float x[N];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) Elt<TO>::store1(q + 32 * k, x[k] * f);
-    } else {
-      const int left = (int)(d - put.c) - lane;
+      for (int k = 0; k < N; ++k) x[k] = lds_elt(from + k * (32 * kElt), TW());
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
+      for (int k = 0; k < N; ++k)
         if (32 * k < left) Elt<TO>::store1(q + 32 * k, x[k] * f);
-    }
+    };
+    const int64_t cols = d - put.c;
+    if (cols >= kWarpCols)
+      copy(std::integral_constant<int, 8>(), kWarpCols);
+    else if (cols > 160)
+      copy(std::integral_constant<int, 8>(), (int)cols - lane);
+    else
+      copy(std::integral_constant<int, 5>(), (int)cols - lane);
+    __syncwarp();
     step(put);
     issue(at);
     at += slot_bytes;
