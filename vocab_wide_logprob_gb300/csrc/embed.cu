@@ -359,7 +359,7 @@ BwdLayout bwd_layout(int64_t n, int64_t V, int64_t d) {
   for (int k = 0; k < kMaxPasses; ++k)
     l.hist[k] = take(k < s.passes ? 4 * (size_t)kMaxBins * s.tiles : 0);
   l.bad = take(4 * (size_t)s.tiles);
-  l.list = take(4 * (size_t)(s.seg_tiles + 1));
+  l.list = take(8 * (size_t)(s.seg_tiles + 1));
   const int64_t pv = padded_cols(d, true), ps = padded_cols(d, false);
   l.part = take(2 * (size_t)s.seg_tiles * (size_t)(pv > ps ? pv : ps) * 4);
   l.total = at;
@@ -469,23 +469,34 @@ __device__ __forceinline__ void bin_bases(SortShared& sh, int32_t total, int32_t
   sh.base[tid] = run;
 }
 
-// Ranks the elements [at, at + kBatch) below b in order (warp match, then a
-// prefix over the warps) and hands each its output position; sh.base moves on.
-template <typename Load, typename Emit>
-__device__ __forceinline__ void scatter_batch(SortShared& sh, int64_t at, int64_t b, int shift,
-                                              uint32_t mask, Load load, Emit emit) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int R = kPerWarp / 32;
+__device__ __forceinline__ void clear_counts(SortShared& sh) {
 #pragma unroll
-  for (int k = 0; k < kSortWarps; ++k) sh.wh[k][tid] = 0;
-  int32_t kk[R], pp[R], rank[R];
+  for (int k = 0; k < kSortWarps; ++k) sh.wh[k][threadIdx.x] = 0;
+}
+constexpr int kPerThread = kPerWarp / 32;
+
+// A thread's elements of [at, at + kBatch) below b: keys (-1: none) and positions.
+template <typename Load>
+__device__ __forceinline__ void load_batch(int64_t at, int64_t b, Load load, int32_t* kk, int32_t* pp) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
+  for (int r = 0; r < kPerThread; ++r) {
     const int64_t i = at + warp * kPerWarp + r * 32 + lane;
     kk[r] = -1;
     pp[r] = 0;
     if (i < b) load(i, kk[r], pp[r]);
   }
+}
+
+// Ranks a batch's elements in order (warp match, then a prefix over the warps)
+// and hands each its output position; sh.base moves on.  The counts are clear
+// before.
+template <typename Emit>
+__device__ __forceinline__ void scatter_batch(SortShared& sh, const int32_t* kk, const int32_t* pp,
+                                              int shift, uint32_t mask, Emit emit) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int R = kPerThread;
+  int32_t rank[R];
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -522,7 +533,7 @@ __device__ __forceinline__ void scatter_batch(SortShared& sh, int64_t at, int64_
 // same digit in earlier tiles) and scatters its elements in order.  While it
 // does, it counts the next pass's digit per destination tile (integer
 // atomics: any order gives the same counts).
-__global__ void __launch_bounds__(kSortThreads) embed_scatter_kernel(
+__global__ void __launch_bounds__(kSortThreads, 3) embed_scatter_kernel(
     const int32_t* key, const int32_t* pos, int64_t n, int64_t tile, int shift, int dbits,
     const int32_t* hist, int32_t* hist_next, int32_t* key_out, int32_t* pos_out,
     const uint32_t* bad, WsHeader* hdr, const Clear clr) {
@@ -530,15 +541,19 @@ __global__ void __launch_bounds__(kSortThreads) embed_scatter_kernel(
   const int tid = threadIdx.x;
   const int tiles = (int)clr.first;
   const uint32_t mask = (1u << dbits) - 1u;
+  if (blockIdx.x < clr.first) clear_counts(sh);
   pdl_wait();
   pdl_trigger();
   if (blockIdx.x >= clr.first) return clear_rows(clr);
-  if (bad != nullptr && blockIdx.x == 0) {
-    uint32_t f = 0;
-    for (int t = tid; t < tiles; t += kSortThreads) f |= bad[t];
-    const int any = __syncthreads_or((int)f);
-    if (tid == 0) hdr->flags = any ? kFlagTokenRange : 0u;
-  }
+  // (the first batch is on its way while the histograms are added)
+  const int64_t a = (int64_t)blockIdx.x * tile, b = min(a + tile, n);
+  auto load = [&](int64_t i, int32_t& k, int32_t& p) {
+    k = key[i];
+    p = pos != nullptr ? pos[i] : (int32_t)i;
+  };
+  int32_t kk[kPerThread], pp[kPerThread];
+  load_batch(a, b, load, kk, pp);
+  const uint32_t tile32 = (uint32_t)tile;  // (n and so tile fit)
   // (16 tiles' counts in flight at a time)
   int32_t before = 0, total = 0;
   for (int t0 = 0; t0 < tiles; t0 += 16) {
@@ -553,22 +568,26 @@ __global__ void __launch_bounds__(kSortThreads) embed_scatter_kernel(
     }
   }
   bin_bases(sh, total, before);
-  const int64_t a = (int64_t)blockIdx.x * tile, b = min(a + tile, n);
-  for (int64_t at = a; at < b; at += kBatch)
-    scatter_batch(
-        sh, at, b, shift, mask,
-        [&](int64_t i, int32_t& k, int32_t& p) {
-          k = key[i];
-          p = pos != nullptr ? pos[i] : (int32_t)i;
-        },
-        [&](int32_t k, int32_t p, int32_t to) {
-          key_out[to] = k;
-          pos_out[to] = p;
-          if (hist_next != nullptr)
-            atomicAdd(hist_next + (int64_t)(to / tile) * kMaxBins +
-                          (((uint32_t)k >> (shift + dbits)) & mask),
-                      1);
-        });
+  for (int64_t at = a;;) {
+    scatter_batch(sh, kk, pp, shift, mask, [&](int32_t k, int32_t p, int32_t to) {
+      key_out[to] = k;
+      pos_out[to] = p;
+      if (hist_next != nullptr)
+        atomicAdd(hist_next + (int64_t)((uint32_t)to / tile32) * kMaxBins +
+                      (((uint32_t)k >> (shift + dbits)) & mask),
+                  1);
+    });
+    at += kBatch;
+    if (at >= b) break;
+    clear_counts(sh);
+    load_batch(at, b, load, kk, pp);
+  }
+  if (bad != nullptr && blockIdx.x == 0) {
+    uint32_t f = 0;
+    for (int t = tid; t < tiles; t += kSortThreads) f |= bad[t];
+    const int any = __syncthreads_or((int)f);
+    if (tid == 0) hdr->flags = any ? kFlagTokenRange : 0u;
+  }
 }
 
 // The whole sort of up to kOneCta tokens by one CTA: every pass counts and
@@ -612,17 +631,21 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(
     const bool last = p + 1 == passes;
     int32_t* ko = last ? key_out : o.key[from ^ 1];
     int32_t* po = last ? pos_out : o.pos[from ^ 1];
-    for (int at = 0; at < n; at += kBatch)
-      scatter_batch(
-          o.s, at, n, shift, mask,
+    for (int at = 0; at < n; at += kBatch) {
+      int32_t kk[kPerThread], pp[kPerThread];
+      clear_counts(o.s);
+      load_batch(
+          at, n,
           [&](int64_t i, int32_t& k, int32_t& q) {
             k = o.key[from][i];
             q = o.pos[from][i];
           },
-          [&](int32_t k, int32_t q, int32_t to) {
-            ko[to] = k;
-            po[to] = q;
-          });
+          kk, pp);
+      scatter_batch(o.s, kk, pp, shift, mask, [&](int32_t k, int32_t q, int32_t to) {
+        ko[to] = k;
+        po[to] = q;
+      });
+    }
   }
 }
 
@@ -636,7 +659,7 @@ struct SegParams {
   int64_t n, V, d, ldd, ldw, dpad;
   float scale;
   float* part;    // [seg tiles][2][dpad]: an id's rows in a tile that it began before (0), goes on after (1)
-  int32_t* list;  // count, then the tiles in which a split id begins
+  int32_t* list;  // count (8 bytes), then pairs: the tile in which a split id begins, the id
   int seg;          // sorted entries per tile
   int tpr, groups;  // threads per row, rows side by side in a CTA
   int cols;         // columns of one CTA in y
@@ -852,7 +875,8 @@ __global__ void __launch_bounds__(kThreads, 4) embed_sum_kernel(const SegParams 
   }
   if (split && cur == last) {
     flush_part(open ? 0 : 1);
-    if (!open && l == 0 && blockIdx.y == 0) p.list[1 + atomicAdd(p.list, 1)] = (int32_t)t;
+    if (!open && l == 0 && blockIdx.y == 0)
+      reinterpret_cast<int2*>(p.list)[1 + atomicAdd(p.list, 1)] = make_int2((int32_t)t, last);
   } else {
     flush();
   }
@@ -875,9 +899,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embed_join_kernel(const SegPa
   const int ny = (int)((p.dpad + kJoinCols - 1) / kJoinCols);
   const int64_t items = (int64_t)count * ny;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int64_t t = p.list[1 + it / ny];
+    const int2 begin = reinterpret_cast<const int2*>(p.list)[1 + it / ny];
+    const int64_t t = begin.x;
+    const int32_t v = begin.y;
     const int64_t c = (it % ny) * kJoinCols + 4 * lane;
-    const int32_t v = p.key[(t + 1) * p.seg];
     // the last tile that begins with the id: the next 32 at once, then by
     // 32-way search (the keys are sorted)
     int64_t last = t + 1, beyond = (p.n + p.seg - 1) / p.seg, stride = 1;
