@@ -287,7 +287,6 @@ constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxBins = 512;                   // 9-bit digits
 constexpr int kBatch = 4 * kSortThreads;        // elements ranked at a time
-constexpr int kPerWarp = kBatch / kSortWarps;   // contiguous elements of one warp
 constexpr int kMaxTiles = 304;                  // CTAs of a sort pass (two per SM)
 constexpr int kMaxPasses = 4;
 static_assert(kMaxBins == kSortThreads, "one thread per bin");
@@ -473,33 +472,32 @@ __device__ __forceinline__ void clear_counts(SortShared& sh) {
 #pragma unroll
   for (int k = 0; k < kSortWarps; ++k) sh.wh[k][threadIdx.x] = 0;
 }
-constexpr int kPerThread = kPerWarp / 32;
+constexpr int kPerThread = kBatch / kSortThreads;
 
-// A thread's elements of [at, at + kBatch) below b: keys (-1: none) and positions.
-template <typename Load>
+// A thread's R elements of the batch [at, at + R kSortThreads) below b (a warp's
+// are contiguous): keys (-1: none) and positions.
+template <int R, typename Load>
 __device__ __forceinline__ void load_batch(int64_t at, int64_t b, Load load, int32_t* kk, int32_t* pp) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int r = 0; r < kPerThread; ++r) {
-    const int64_t i = at + warp * kPerWarp + r * 32 + lane;
+  for (int r = 0; r < R; ++r) {
+    const int64_t i = at + warp * (32 * R) + r * 32 + lane;
     kk[r] = -1;
     pp[r] = 0;
     if (i < b) load(i, kk[r], pp[r]);
   }
 }
 
-// Ranks a batch's elements in order (lanes with the same digit by one vote per
-// bit, then a prefix over the warps) and hands each its output position; sh.base
-// moves on.  The counts are clear before.  (The gradient of 42,115 tokens of 64
-// columns takes 28.1 us; with the warp's match instruction, which takes its time
-// for every different value, 29.3.)
-template <typename Emit>
-__device__ __forceinline__ void scatter_batch(SortShared& sh, const int32_t* kk, const int32_t* pp,
-                                              int shift, uint32_t mask, Emit emit) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int R = kPerThread;
-  int32_t rank[R];
-  uint32_t dg[R], same[R];
+// Ranks a batch's elements among those of their digit in the same warp, in order
+// (lanes with the same digit by one vote per bit), and leaves the warps' counts,
+// which are clear before.  (The gradient of 42,115 tokens of 64 columns takes 28.1
+// us; with the warp's match instruction, which takes its time for every different
+// value, 29.3.)
+template <int R>
+__device__ __forceinline__ void rank_batch(SortShared& sh, const int32_t* kk, int shift,
+                                           uint32_t mask, uint32_t* dg, int32_t* rank) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t same[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     dg[r] = ((uint32_t)kk[r] >> shift) & mask;
@@ -525,20 +523,24 @@ __device__ __forceinline__ void scatter_batch(SortShared& sh, const int32_t* kk,
     rank[r] = old + __popc(below);
   }
   __syncthreads();
-  {
-    int32_t first = sh.base[tid];
+}
+// The warps' counts of this thread's bin to first positions, from `first` on.
+__device__ __forceinline__ int32_t place_counts(SortShared& sh, int32_t first) {
 #pragma unroll
-    for (int k = 0; k < kSortWarps; ++k) {
-      const int32_t c = sh.wh[k][tid];
-      sh.wh[k][tid] = first;
-      first += c;
-    }
-    sh.base[tid] = first;
+  for (int k = 0; k < kSortWarps; ++k) {
+    const int32_t c = sh.wh[k][threadIdx.x];
+    sh.wh[k][threadIdx.x] = first;
+    first += c;
   }
+  return first;
+}
+template <int R, typename Emit>
+__device__ __forceinline__ void emit_batch(const SortShared& sh, const int32_t* kk, const int32_t* pp,
+                                           const uint32_t* dg, const int32_t* rank, Emit emit) {
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < R; ++r)
-    if (kk[r] >= 0) emit(kk[r], pp[r], sh.wh[warp][dg[r]] + rank[r]);
+    if (kk[r] >= 0) emit(kk[r], pp[r], sh.wh[threadIdx.x >> 5][dg[r]] + rank[r]);
   __syncthreads();
 }
 
@@ -566,7 +568,7 @@ __global__ void __launch_bounds__(kSortThreads, 3) embed_scatter_kernel(
     p = pos != nullptr ? pos[i] : (int32_t)i;
   };
   int32_t kk[kPerThread], pp[kPerThread];
-  load_batch(a, b, load, kk, pp);
+  load_batch<kPerThread>(a, b, load, kk, pp);
   const uint32_t tile32 = (uint32_t)tile;  // (n and so tile fit)
   // (16 tiles' counts in flight at a time)
   int32_t before = 0, total = 0;
@@ -583,7 +585,11 @@ __global__ void __launch_bounds__(kSortThreads, 3) embed_scatter_kernel(
   }
   bin_bases(sh, total, before);
   for (int64_t at = a;;) {
-    scatter_batch(sh, kk, pp, shift, mask, [&](int32_t k, int32_t p, int32_t to) {
+    uint32_t dg[kPerThread];
+    int32_t rank[kPerThread];
+    rank_batch<kPerThread>(sh, kk, shift, mask, dg, rank);
+    sh.base[tid] = place_counts(sh, sh.base[tid]);
+    emit_batch<kPerThread>(sh, kk, pp, dg, rank, [&](int32_t k, int32_t p, int32_t to) {
       key_out[to] = k;
       pos_out[to] = p;
       if (hist_next != nullptr)
@@ -594,7 +600,7 @@ __global__ void __launch_bounds__(kSortThreads, 3) embed_scatter_kernel(
     at += kBatch;
     if (at >= b) break;
     clear_counts(sh);
-    load_batch(at, b, load, kk, pp);
+    load_batch<kPerThread>(at, b, load, kk, pp);
   }
   if (bad != nullptr && blockIdx.x == 0) {
     uint32_t f = 0;
@@ -604,62 +610,66 @@ __global__ void __launch_bounds__(kSortThreads, 3) embed_scatter_kernel(
   }
 }
 
-// The whole sort of up to kOneCta tokens by one CTA: every pass counts and
-// scatters between shared-memory arrays (777 tokens: 7 us in one launch, where
-// the passes' kernels take three launches of 4 us).
+// The whole sort of up to kOneCta tokens by one CTA, R of them per thread: every
+// pass ranks all of them and scatters between shared-memory arrays.  4,096 tokens
+// of 130 columns take 19.2 us a call, 4,097 by the passes' kernels 22.
 constexpr int kOneCta = 4096;
 struct OneShared {
   SortShared s;
   int32_t key[2][kOneCta], pos[2][kOneCta];
-  int32_t hist[kMaxBins];
 };
+template <int R>
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(
     const int64_t* __restrict__ ids, int n, int64_t V, int64_t pad_id, int passes, int dbits,
     int32_t* key_out, int32_t* pos_out, int32_t* list, WsHeader* hdr, const Clear clr) {
   extern __shared__ __align__(16) unsigned char one_raw[];
   OneShared& o = *reinterpret_cast<OneShared*>(one_raw);
+  if (blockIdx.x < clr.first) clear_counts(o.s);
   pdl_wait();
   pdl_trigger();
   if (blockIdx.x >= clr.first) return clear_rows(clr);
   const int tid = threadIdx.x;
   const uint32_t mask = (1u << dbits) - 1u;
   int outside = 0;
-#pragma unroll 4
-  for (int i = tid; i < n; i += kSortThreads) {
-    o.key[0][i] = key_of(__ldg(ids + i), V, pad_id, &outside);
-    o.pos[0][i] = i;
+  int32_t kk[R], pp[R];
+  load_batch<R>(
+      0, n,
+      [&](int64_t i, int32_t& k, int32_t& q) {
+        k = key_of(__ldg(ids + i), V, pad_id, &outside);
+        q = (int32_t)i;
+      },
+      kk, pp);
+  for (int p = 0; p < passes; ++p) {
+    const int shift = p * dbits, to_buf = p & 1;
+    uint32_t dg[R];
+    int32_t rank[R];
+    rank_batch<R>(o.s, kk, shift, mask, dg, rank);
+    int32_t total = 0;
+#pragma unroll
+    for (int k = 0; k < kSortWarps; ++k) total += o.s.wh[k][tid];
+    bin_bases(o.s, total, 0);
+    place_counts(o.s, o.s.base[tid]);
+    const bool last = p + 1 == passes;
+    int32_t* ko = last ? key_out : o.key[to_buf];
+    int32_t* po = last ? pos_out : o.pos[to_buf];
+    emit_batch<R>(o.s, kk, pp, dg, rank, [&](int32_t k, int32_t q, int32_t to) {
+      ko[to] = k;
+      po[to] = q;
+    });
+    if (last) break;
+    clear_counts(o.s);
+    load_batch<R>(
+        0, n,
+        [&](int64_t i, int32_t& k, int32_t& q) {
+          k = ko[i];
+          q = po[i];
+        },
+        kk, pp);
   }
   const int any = __syncthreads_or(outside);
   if (tid == 0) {
     hdr->flags = any ? kFlagTokenRange : 0u;
     list[0] = 0;
-  }
-  for (int p = 0; p < passes; ++p) {
-    const int shift = p * dbits, from = p & 1;
-    o.hist[tid] = 0;
-    __syncthreads();
-    for (int i = tid; i < n; i += kSortThreads)
-      atomicAdd(&o.hist[((uint32_t)o.key[from][i] >> shift) & mask], 1);
-    __syncthreads();
-    bin_bases(o.s, o.hist[tid], 0);
-    const bool last = p + 1 == passes;
-    int32_t* ko = last ? key_out : o.key[from ^ 1];
-    int32_t* po = last ? pos_out : o.pos[from ^ 1];
-    for (int at = 0; at < n; at += kBatch) {
-      int32_t kk[kPerThread], pp[kPerThread];
-      clear_counts(o.s);
-      load_batch(
-          at, n,
-          [&](int64_t i, int32_t& k, int32_t& q) {
-            k = o.key[from][i];
-            q = o.pos[from][i];
-          },
-          kk, pp);
-      scatter_batch(o.s, kk, pp, shift, mask, [&](int32_t k, int32_t q, int32_t to) {
-        ko[to] = k;
-        po[to] = q;
-      });
-    }
   }
 }
 
@@ -1068,11 +1078,14 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, const DeviceInfo& dev, cudaS
   int out = s.passes & 1;
   if (one) {
     const Clear c = clear_share(0, 1);
-    e = ensure_dynamic_smem((const void*)embed_sort_kernel, (int)sizeof(OneShared));
+    auto kern = a.n <= 2 * kSortThreads   ? embed_sort_kernel<2>
+                : a.n <= 4 * kSortThreads ? embed_sort_kernel<4>
+                                          : embed_sort_kernel<kOneCta / kSortThreads>;
+    e = ensure_dynamic_smem((const void*)kern, (int)sizeof(OneShared));
     if (e != cudaSuccess) return e;
-    e = launch_pdl(embed_sort_kernel, dim3((unsigned)(1 + clear_ctas)), dim3(kSortThreads),
-                   sizeof(OneShared), st, 1, a.ids, (int)a.n, a.V, a.pad_id, s.passes, s.dbits,
-                   i32(l.key[out]), i32(l.pos[out]), i32(l.list), hdr, c);
+    e = launch_pdl(kern, dim3((unsigned)(1 + clear_ctas)), dim3(kSortThreads), sizeof(OneShared), st,
+                   1, a.ids, (int)a.n, a.V, a.pad_id, s.passes, s.dbits, i32(l.key[out]),
+                   i32(l.pos[out]), i32(l.list), hdr, c);
   } else {
     const int64_t n_rest =
         s.passes > 1 ? (int64_t)(l.hist[s.passes - 1] - l.hist[1]) / 4 + (int64_t)kMaxBins * s.tiles
