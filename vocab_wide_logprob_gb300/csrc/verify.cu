@@ -1018,23 +1018,20 @@ __global__ void __launch_bounds__(kRaceThreads, 2) verify_emit_kernel(
                          (*(volatile int*)&sh.abort ? 4 : 0));
     }
     cluster_or_cta_sync(ranks);
-    const int again = sh.again[round][0] & 3;
-    for (uint32_t k = 0; k < ranks; ++k)
-      if (sh.again[round][k] & 4) flags |= kFlagTimeout;
+    // (every warp the same: a lane looks at a CTA's part)
+    const bool in = (uint32_t)lane < ranks;
+    const int state = in ? sh.again[round][lane] : 0;
+    const Bounds b = in ? sh.bounds[round][lane] : Bounds{0.f, 0.f, -1, 0};
+    if (__any_sync(0xffffffffu, state & 4)) flags |= kFlagTimeout;
+    const int again = __shfl_sync(0xffffffffu, state, 0) & 3;
     if (again == 0) break;
-    float bar = 0.f;
-    for (uint32_t k = 0; k < ranks; ++k) bar = fmaxf(bar, sh.bounds[round][k].lo);
-    int rivals = 0;
-    int32_t winner = -1;
-    for (uint32_t k = 0; k < ranks; ++k) {
-      const Bounds b = sh.bounds[round][k];
-      if (b.count != 0 && b.hi >= bar) {
-        rivals += b.count < 0 ? 2 : b.count;
-        winner = b.token;
-      }
-    }
+    // (the bounds are not negative: their bits are in order)
+    const float bar = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(b.lo)));
+    const bool rival = b.count != 0 && b.hi >= bar;
+    const uint32_t who = __ballot_sync(0xffffffffu, rival);
+    const uint32_t rivals = __reduce_add_sync(0xffffffffu, !rival ? 0u : b.count < 0 ? 2u : (uint32_t)b.count);
     if (rivals == 1 && bar > 0.f) {  // nothing else comes near
-      token = winner;
+      token = __shfl_sync(0xffffffffu, b.token, __ffs(who) - 1);
       break;
     }
     const Bounds mine = sh.bounds[round][rank];
