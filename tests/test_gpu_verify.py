@@ -236,6 +236,28 @@ def test_no_residual_falls_back_to_the_target():
 
 
 @pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("draft", [False, True], ids=["last", "residual"])
+@pytest.mark.parametrize("V", [40000, 40003])
+def test_close_scores_far_from_zero(dt, draft, V):
+    """Logits thousands away from 0 (a shift that changes no probability): the
+    winner's score is 1e-4 of itself above that of a token before it."""
+    N, r = 64, gen(18)
+    shift = (torch.rand(N, 1, 1, generator=r, device="cuda") * 60000 + 1000).to(dt)
+    z = shift.expand(N, 2 if draft else 1, V).clone()
+    noise = torch.full((N, V), 4.0, device="cuda")
+    noise[:, 7] = 1.0
+    noise[torch.arange(N, device="cuda"), 4000 + 500 * torch.arange(N, device="cuda")] = 1 / (1 + 1e-4)
+    c = dict(z=z, x=torch.zeros(N, 0, dtype=torch.int64, device="cuda"),
+             u=torch.zeros(N, 0, device="cuda"), noise=noise, y=None, lens=None, temp=None)
+    if draft:  # the draft has all but a little of its mass on the rejected token 0
+        c["x"] = torch.zeros(N, 1, dtype=torch.int64, device="cuda")
+        c["u"] = torch.ones(N, 1, device="cuda")
+        c["y"] = shift.expand(N, 1, V).clone()
+        c["y"][:, :, 0] = (c["y"][:, :, 0].float() * 1.25 + 40).to(dt)
+    both(c)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
 @pytest.mark.parametrize("V", [40, 4099, 40000])
 def test_masks_and_nonfinite_rows(dt, V):
     low = torch.finfo(dt).min

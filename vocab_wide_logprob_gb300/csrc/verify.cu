@@ -560,21 +560,43 @@ __device__ __forceinline__ void race_bounds(const Racer& c, float x, float y, fl
   lo = fmaf(s, -kRaceMargin, d) * w;
   hi = fmaf(s, kRaceMargin, d) * w;
 }
-// The upper bounds of a pair of elements of rows whose maxima are not extreme:
-// nt and nd are minus the reference exponents and the log2 of the sums.
+// The same for rows whose maxima are not extreme.  The sums are divided out
+// after the exponentials: taken into the exponents, their logarithms would be
+// rounded at the size of the references, which may be thousands.
+struct UsualRace {
+  float c, rt, rd;       // exponents: x c - r
+  float t_up, t_lo;      // (1 +- margin) / the target's sum
+  float d_up, d_lo;      // minus (1 -+ margin) / the draft's
+};
+__device__ __forceinline__ UsualRace usual_race(const Racer& c) {
+  const float it = __fdiv_rn(1.f, c.st), id = c.has_draft ? __fdiv_rn(1.f, c.sd) : 0.f;
+  return {c.t.c,
+          c.rt,
+          c.has_draft ? c.rd : 0.f,
+          (1.f + kRaceMargin) * it,
+          (1.f - kRaceMargin) * it,
+          (kRaceMargin - 1.f) * id,
+          (-kRaceMargin - 1.f) * id};
+}
 template <bool kDraft>
-__device__ __forceinline__ uint64_t race_upper2(uint64_t c2, uint64_t nt, uint64_t nd,
-                                                float x0, float x1, float y0,
+__device__ __forceinline__ void race_bounds(const UsualRace& c, float x, float y, float e, float& lo,
+                                            float& hi) {
+  const float p = ex2(fmaf(x, c.c, -c.rt)), q = kDraft ? ex2(fmaf(y, c.c, -c.rd)) : 0.f;
+  const float w = rcp(e);
+  lo = fmaf(q, c.d_lo, p * c.t_lo) * w;
+  hi = fmaf(q, c.d_up, p * c.t_up) * w;
+}
+// The upper bounds of a pair of elements.
+template <bool kDraft>
+__device__ __forceinline__ uint64_t race_upper2(const UsualRace& c, float x0, float x1, float y0,
                                                 float y1, float e0, float e1) {
-  const uint64_t x = f2_pack(x0, x1);
-  const uint64_t p = f2_ex2(f2_fma(x, c2, nt));
+  const uint64_t c2 = f2_pack(c.c, c.c);
+  const uint64_t p = f2_ex2(f2_fma(f2_pack(x0, x1), c2, f2_pack(-c.rt, -c.rt)));
   const uint64_t w = f2_pack(rcp(e0), rcp(e1));
-  const uint64_t up = f2_pack(1.f + kRaceMargin, 1.f + kRaceMargin);
-  uint64_t h = f2_mul(p, up);  // p (1 + margin) - q (1 - margin)
+  uint64_t h = f2_mul(p, f2_pack(c.t_up, c.t_up));
   if (kDraft) {
-    const uint64_t y = f2_pack(y0, y1);
-    const uint64_t q = f2_ex2(f2_fma(y, c2, nd));
-    h = f2_fma(q, f2_pack(kRaceMargin - 1.f, kRaceMargin - 1.f), h);
+    const uint64_t q = f2_ex2(f2_fma(f2_pack(y0, y1), c2, f2_pack(-c.rd, -c.rd)));
+    h = f2_fma(q, f2_pack(c.d_up, c.d_up), h);
   }
   return f2_mul(h, w);
 }
@@ -670,9 +692,7 @@ __device__ __forceinline__ float race_stream(const Racer& c, const T* tr, const 
   };
   if (tid == 0)
     for (int k = 0; k < (int)S && k < steps; ++k) issue(k);
-  const uint64_t c2 = f2_pack(c.t.c, c.t.c);
-  const float nt1 = -(c.rt + c.lst), nd1 = -(c.rd + c.lsd);
-  const uint64_t nt = f2_pack(nt1, nt1), nd = f2_pack(nd1, nd1);
+  const UsualRace ur = usual_race(c);
   const int64_t in = c.skip - v0;  // the token left out, if it is here
   const int skip = c.skip >= 0 && in >= 0 && in < 8 * (int64_t)n8 ? (int)in : -1;
   float bar = 0.f, largest = 0.f;
@@ -719,8 +739,8 @@ __device__ __forceinline__ float race_stream(const Racer& c, const T* tr, const 
 #pragma unroll
       for (int q = 0; q < 8; q += 2) {
         const uint64_t h =
-            kDraft ? race_upper2<true>(c2, nt, nd, x[q], x[q + 1], y[q], y[q + 1], e[q], e[q + 1])
-                   : race_upper2<false>(c2, nt, nd, x[q], x[q + 1], 0.f, 0.f, e[q], e[q + 1]);
+            kDraft ? race_upper2<true>(ur, x[q], x[q + 1], y[q], y[q + 1], e[q], e[q + 1])
+                   : race_upper2<false>(ur, x[q], x[q + 1], 0.f, 0.f, e[q], e[q + 1]);
         float h0, h1;
         f2_unpack(h, h0, h1);
         most = fmaxf(most, fmaxf(h0, h1));
@@ -736,7 +756,7 @@ __device__ __forceinline__ float race_stream(const Racer& c, const T* tr, const 
         hi[q] = 0.f;
         if ((!kAligned || k < n8) && first + q * apart != skip) {
           float lo;
-          race_bounds(c, x[q], kDraft ? y[q] : 0.f, e[q], lo, hi[q]);
+          race_bounds<kDraft>(ur, x[q], kDraft ? y[q] : 0.f, e[q], lo, hi[q]);
           top = fmaxf(top, lo);
         }
       }
