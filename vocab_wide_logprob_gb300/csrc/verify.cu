@@ -1127,8 +1127,12 @@ cudaError_t clusters_at_once(int C, const DeviceInfo& d, int* n) {
   constexpr int kDevices = 64;
   static std::atomic<int> known[kDevices][kMaxCluster + 1];
   const bool keep = d.device >= 0 && d.device < kDevices;
-  *n = keep ? known[d.device][C].load(std::memory_order_relaxed) : 0;
-  if (*n > 0) return cudaSuccess;
+  // (the answer + 1; 0: not asked yet)
+  const int had = keep ? known[d.device][C].load(std::memory_order_relaxed) : 0;
+  if (had > 0) {
+    *n = had - 1;
+    return cudaSuccess;
+  }
   cudaLaunchAttribute at = {};
   at.id = cudaLaunchAttributeClusterDimension;
   at.val.clusterDim.x = (unsigned)C;
@@ -1141,7 +1145,7 @@ cudaError_t clusters_at_once(int C, const DeviceInfo& d, int* n) {
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   const cudaError_t e = cudaOccupancyMaxActiveClusters(n, verify_emit_kernel<T, kAligned>, &cfg);
-  if (e == cudaSuccess && keep) known[d.device][C].store(*n < 1 ? 1 : *n, std::memory_order_relaxed);
+  if (e == cudaSuccess && keep) known[d.device][C].store(*n + 1, std::memory_order_relaxed);
   return e;
 }
 
