@@ -167,6 +167,19 @@ def test_odd_addresses(dt):
         assert (dst[rest] == 9).all()
 
 
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_outputs_at_16_bytes(dt):
+    """Outputs that begin at a 16-byte boundary that is not one of 32."""
+    n = g()
+    grads = [torch.randn(50000, generator=gen(8), device="cuda").to(dt) for _ in range(3)]
+    limit = 0.5 * norm64(grads)
+    dst = [torch.full((50012,), 9.0, device="cuda") for _ in grads]
+    outs = [t[4:50004] for t in dst]
+    stats, _ = n.grpo_clip_grad_norm(grads, limit, out=outs)
+    check(grads, stats, outs, limit)
+    assert all((t[:4] == 9).all() and (t[50004:] == 9).all() for t in dst)
+
+
 def test_reproducible_stream_and_graph():
     n = g()
     grads = make([123457, 1000, 8], [BF16, F32], 6)

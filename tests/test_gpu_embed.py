@@ -79,6 +79,25 @@ def test_forward_views_of_wider_rows_and_odd_addresses():
         assert (out_buf[:, :5] == 7).all() and (out_buf[:, 5 + hi - lo:] == 7).all()
 
 
+@pytest.mark.parametrize("wdt,odt", [(F32, F32), (F32, BF16), (BF16, F32), (BF16, BF16)])
+@pytest.mark.parametrize("n,d", [(1, 257), (700, 33), (3001, 160), (3001, 161), (700, 515), (5000, 901),
+                                 (40, 8192), (3000, 64)])
+@pytest.mark.parametrize("lo", [1, 4, 8])
+def test_forward_at_any_alignment(n, d, lo, wdt, odt):
+    """Tables with NaN around their rows, ids outside, outputs in wider rows."""
+    V = 211
+    buf = torch.full((V, d + 16), float("nan"), device="cuda", dtype=wdt)
+    w = buf[:, lo:lo + d]
+    w.copy_(torch.randn(V, d, generator=gen(7), device="cuda"))
+    ids = draw_ids(n, V, 8)
+    ids[n // 2] = V
+    out_buf = torch.full((n, d + 16), 7.0, device="cuda", dtype=odt)
+    out = out_buf[:, lo:lo + d]
+    g().grpo_embed_fwd(ids, w, 3.5, out=out)
+    check_fwd(out, ids, w, 3.5)
+    assert (out_buf[:, :lo] == 7).all() and (out_buf[:, lo + d:] == 7).all()
+
+
 def test_forward_ids_outside_give_nan_rows():
     w = torch.randn(10, 24, device="cuda")
     ids = torch.tensor([0, -1, 9, 10, 1 << 40, -(1 << 62), 3], device="cuda")
@@ -218,6 +237,40 @@ def test_gradient_into_views_and_from_views():
         n.grpo_embed_bwd(ids, buf[:, lo:hi], 20, dweight=view)
         check_bwd(view, ids, buf[:, lo:hi])
         assert (out_buf[:, :7] == 3).all() and (out_buf[:, 7 + hi - lo:] == 3).all()
+
+
+@pytest.mark.parametrize("ddt,wdt", [(F32, F32), (BF16, F32), (F32, BF16), (BF16, BF16)])
+@pytest.mark.parametrize("n,d", [(1, 257), (900, 33), (3001, 160), (700, 515), (6000, 901), (40, 8192),
+                                 (3000, 64)])
+@pytest.mark.parametrize("lo", [1, 4])
+def test_gradient_at_any_alignment(n, d, lo, ddt, wdt):
+    """Gradients with NaN around their rows, results in wider rows."""
+    V = 97
+    buf = torch.full((n, d + 16), float("nan"), device="cuda", dtype=ddt)
+    x = buf[:, lo:lo + d]
+    x.copy_(torch.randn(n, d, generator=gen(52), device="cuda"))
+    ids = draw_ids(n, V, 53)
+    out_buf = torch.full((V, d + 16), 3.0, device="cuda", dtype=wdt)
+    view = out_buf[:, lo:lo + d]
+    g().grpo_embed_bwd(ids, x, V, dweight=view)
+    check_bwd(view, ids, x)
+    base = torch.randn(V, d, generator=gen(54), device="cuda").to(wdt)
+    view.copy_(base)
+    g().grpo_embed_bwd(ids, x, V, 0.5, dweight=view, accumulate=True)
+    check_bwd(view, ids, x, 0.5, None, base)
+    assert (out_buf[:, :lo] == 3).all() and (out_buf[:, lo + d:] == 3).all()
+
+
+@pytest.mark.parametrize("n", [1, 512, 1023, 1024, 1025, 3000])
+@pytest.mark.parametrize("V", [2, 70, 600, 300000])
+def test_gradient_of_few_tokens(n, V):
+    """Tokens sorted by one block, two to eight of them per thread."""
+    ids = draw_ids(n, V, 55)
+    ids[::7] = V + 3
+    x = torch.randn(n, 24, generator=gen(56), device="cuda")
+    dw, ws = g().grpo_embed_bwd(ids, x, V)
+    assert g().grpo_check_error(ws) == 6
+    check_bwd(dw, ids, x)
 
 
 def test_gradient_empty():

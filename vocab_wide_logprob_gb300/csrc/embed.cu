@@ -333,7 +333,9 @@ SortPlan sort_plan(int64_t n, int64_t V, int64_t d) {
   // threads on each of 152 SMs); 4 entries where 8 leave fewer than 64 (777 tokens
   // of 130 columns 11.6 us, 12.8 with 8; 42,115 of 64 columns 32.3, 30.5 with 8)
   s.seg = kMaxSegEntries;
-  while (s.seg > kMinSegEntries && (n + s.seg - 1) / s.seg * (padded_cols(d, true) / 8) < 152 * 512) s.seg /= 2;
+  while (s.seg > kMinSegEntries &&
+         (n + s.seg - 1) / s.seg * (padded_cols(d, true) / 8) < 152 * 512)
+    s.seg /= 2;
   if (s.seg == kMinSegEntries && (n + 7) / 8 * (padded_cols(d, true) / 8) < 152 * 64) s.seg /= 2;
   s.seg_tiles = (n + s.seg - 1) / s.seg;
   return s;
@@ -995,8 +997,8 @@ cudaError_t launch_sums(const EmbedBwdArgs& a, SegParams p, const DeviceInfo& de
   const unsigned ny = (unsigned)((p.d + p.cols - 1) / p.cols);
   const int64_t seg_tiles = (p.n + p.seg - 1) / p.seg;
   const int64_t blocks = (seg_tiles + p.groups - 1) / p.groups;
-  const size_t ring =
-      kVec ? (size_t)sum_depth<TD>() * kThreads * kSumCols * sizeof(TD) : warp_rings(p.d, sizeof(TD), kSumAnyDepth);
+  const size_t ring = kVec ? (size_t)sum_depth<TD>() * kThreads * kSumCols * sizeof(TD)
+                           : warp_rings(p.d, sizeof(TD), kSumAnyDepth);
   cudaError_t e = ensure_dynamic_smem((const void*)embed_sum_kernel<TD, TW, kVec, kAcc>, (int)ring);
   if (e != cudaSuccess) return e;
   e = launch_pdl(embed_sum_kernel<TD, TW, kVec, kAcc>, dim3((unsigned)blocks, ny), dim3(kThreads),

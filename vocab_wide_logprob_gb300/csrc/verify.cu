@@ -1028,7 +1028,8 @@ __global__ void __launch_bounds__(kRaceThreads, 2) verify_emit_kernel(
   // depends on comes from what they sent one another.
   for (int round = 0; round < 2; ++round) {
     Bounds own = {0.f, 0.f, -1, 0};
-    if (d.emit == 1) own = race_bounds_of<T, kAligned>(c, trow, drow, noise, v0, v1, sh, smem_u32(emit_ring), used);
+    if (d.emit == 1)
+      own = race_bounds_of<T, kAligned>(c, trow, drow, noise, v0, v1, sh, smem_u32(emit_ring), used);
     if (tid < (int)ranks) {
       const uint32_t to = (uint32_t)tid;
       const float4 f = make_float4(own.lo, own.hi, __int_as_float(own.token), __int_as_float(own.count));
@@ -1049,7 +1050,8 @@ __global__ void __launch_bounds__(kRaceThreads, 2) verify_emit_kernel(
     const float bar = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(b.lo)));
     const bool rival = b.count != 0 && b.hi >= bar;
     const uint32_t who = __ballot_sync(0xffffffffu, rival);
-    const uint32_t rivals = __reduce_add_sync(0xffffffffu, !rival ? 0u : b.count < 0 ? 2u : (uint32_t)b.count);
+    const uint32_t rivals = __reduce_add_sync(
+        0xffffffffu, !rival ? 0u : b.count < 0 ? 2u : (uint32_t)b.count);
     if (rivals == 1 && bar > 0.f) {  // nothing else comes near
       token = __shfl_sync(0xffffffffu, b.token, __ffs(who) - 1);
       break;
