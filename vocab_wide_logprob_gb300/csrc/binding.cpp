@@ -103,6 +103,21 @@ Tensor workspace_of(PyObject* o, size_t need, const c10::Device& dev) {
   }
   return make({(int64_t)need}, at::kByte, dev);
 }
+// A new workspace of `need` bytes with `count` floats behind them in the same
+// memory, as two tensors: one allocation (about 1.3 us each on the host, of the 9
+// us of a clipping call on 26 tensors).
+Tensor workspace_and(size_t need, int64_t count, const c10::Device& dev, Tensor* floats) {
+  const int64_t at = (int64_t)(need + 255) / 256 * 256;
+  Tensor w = make({at + 4 * count}, at::kByte, dev);
+  w.unsafeGetTensorImpl()->set_sizes_contiguous({(int64_t)need});
+  auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(w.storage()),
+                                                   c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                   caffe2::TypeMeta::Make<float>());
+  impl->set_storage_offset(at / 4);
+  impl->set_sizes_contiguous({count});
+  *floats = Tensor(std::move(impl));
+  return w;
+}
 size_t bytes_of(const Tensor& t) { return (size_t)t.numel() * t.element_size(); }
 
 // Rows of d elements: the pitch of the last-but-one dimension of a tensor of
@@ -311,17 +326,19 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         g.out_dtype = code(t.scalar_type(), "every out");
       }
     }
-    Tensor stats;
-    if (a[5] == Py_None) {
+    size_t need = 0;
+    check_status(grpo_grad_norm_workspace_size(n, &need), "grpo_grad_norm_workspace_size");
+    Tensor stats, ws;
+    if (a[5] == Py_None && a[6] == Py_None) {
+      ws = workspace_and(need, 2, dev, &stats);
+    } else if (a[5] == Py_None) {
       stats = make({2}, at::kFloat, dev);
     } else {
       stats = tensor(a[5], "stats");
       contiguous(stats, "stats", at::kFloat, dev);
       if (stats.numel() < 2) refuse(PyExc_ValueError, "%s must hold two values", "stats");
     }
-    size_t need = 0;
-    check_status(grpo_grad_norm_workspace_size(n, &need), "grpo_grad_norm_workspace_size");
-    const Tensor ws = workspace_of(a[6], need, dev);
+    if (!ws.defined()) ws = workspace_of(a[6], need, dev);
     const grpo_stream_t st = stream_of(a[7]);
     float* sp = (float*)stats.data_ptr();
     check_status(launch([&] {
