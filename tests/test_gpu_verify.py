@@ -257,6 +257,93 @@ def test_close_scores_far_from_zero(dt, draft, V):
     both(c)
 
 
+def far_case(dt, V, T, rows):
+    """One sequence per entry of ``rows`` (float64 [V]), nothing drafted, at temperature T."""
+    z = torch.stack([r.to(dt) for r in rows]).unsqueeze(1).cuda()
+    N, r = len(rows), gen(19)
+    return dict(z=z, x=torch.zeros(N, 0, dtype=torch.int64, device="cuda"),
+                u=torch.zeros(N, 0, device="cuda"), y=None, lens=None,
+                noise=torch.empty(N, V, device="cuda").exponential_(generator=r).clamp_(min=1e-9),
+                temp=torch.full((N,), T, device="cuda"))
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("V", [37, 4099, 40000])
+def test_every_token_at_one_far_level(dt, V):
+    """Masks of any size under every token (and the same above 0): a uniform row."""
+    levels = [s * v for s in (-1, 1) for v in (1.1e7, 1.2e7, 1e8, 1e9, 3e9, 1e10, 1e13, 1e20, 9.9e29, 1e30)]
+    out = both(far_case(dt, V, 1.0, [torch.full((V,), v, dtype=torch.float64) for v in levels]))
+    assert (out["logp"] + math.log(V)).abs().max() < 1e-4
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("level", [3e9, 1e10, -1e10, 1e20])
+def test_far_rows_of_different_values(dt, level):
+    """Random logits far from zero at temperatures that leave a distribution."""
+    V, g0 = 9001, torch.Generator().manual_seed(20)
+    rows = [level * (1 + torch.rand(V, generator=g0, dtype=torch.float64)) for _ in range(6)]
+    for T in (1.0, abs(level) / 4096, abs(level) / 20):
+        both(far_case(dt, V, T, rows))
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("T", [1.1e-6, 3e-6, 1e-5, 1e-4])
+def test_small_temperatures(dt, T):
+    V, g0 = 9001, torch.Generator().manual_seed(21)
+    base = torch.randn(V, generator=g0, dtype=torch.float64)
+    rows = [3 * base, -65504 + torch.zeros(V, dtype=torch.float64), 20 + T * base, 3000 * base,
+            torch.where(base > 3, 1.0, -65504.0), torch.where(base > 3, 1.0, -1e9)]
+    c = far_case(dt, V, T, rows)
+    both(c)
+    c["z"] = c["z"].expand(6, 3, V).contiguous()  # with drafts, accepted and not
+    c["y"] = c["z"][:, :2].clone()
+    c["x"] = c["y"].float().argmax(-1)
+    c["x"][::2, 1] = (c["x"][::2, 1] + 1) % V
+    c["y"][:, 1].scatter_(1, c["x"][:, 1:], 60000.0)
+    c["u"] = torch.full((6, 2), 0.5, device="cuda")
+    both(c)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("V", [64, 5001, 151936])
+@pytest.mark.parametrize("order", ["up", "down", "mixed"])
+def test_parts_on_both_sides_of_the_far_form(sign, V, order):
+    """A row whose parts have maxima a few units apart around 2^24 / log2(e),
+    where the weights' form changes: the parts' sums are merged exactly."""
+    edge = 2 ** 24 / math.log2(math.e)
+    step = torch.arange(V, dtype=torch.float64) * (12.0 / V)
+    if order == "down":
+        step = step.flip(0)
+    elif order == "mixed":
+        step = step[torch.randperm(V, generator=torch.Generator().manual_seed(22))]
+    rows = [torch.floor(sign * edge - 6 + k + step) for k in range(-2, 9, 2)]
+    c = far_case(F32, V, 1.0, rows)
+    both(c)
+    # drafted from a row of the other form (a shift changes nothing): accepted
+    c["x"] = torch.full((6, 1), V // 2, device="cuda")
+    c["u"] = torch.full((6, 1), 0.999, device="cuda")
+    c["y"], c["z"] = c["z"] - math.floor(sign * edge), c["z"].expand(6, 2, V).contiguous()
+    assert (both(c)["n_accepted"] == 1).all()
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("level", [-1e10, 1e10])
+def test_far_residual(dt, level):
+    """A rejected draft whose distribution is one token: the residual is the
+    rest of a uniform row far from zero."""
+    V = 4099
+    c = far_case(dt, V, 1.0, [torch.full((V,), level, dtype=torch.float64)] * 4)
+    c["z"] = c["z"].expand(4, 2, V).contiguous()
+    c["x"] = torch.tensor([[0], [5], [2048], [V - 1]], device="cuda")
+    c["u"] = torch.full((4, 1), 0.9, device="cuda")
+    c["y"] = torch.full((4, 1, V), 2 * abs(level), device="cuda").neg().to(dt)
+    c["y"].scatter_(2, c["x"].unsqueeze(-1), abs(level))
+    out = both(c)
+    assert (out["n_accepted"] == 0).all()
+    c["y"] = None
+    both(c)
+
+
 @pytest.mark.parametrize("dt", [F32, BF16])
 @pytest.mark.parametrize("V", [40, 4099, 40000])
 def test_masks_and_nonfinite_rows(dt, V):

@@ -42,10 +42,12 @@ constexpr int kMaxSplit = 32;          // CTAs per row of the rows kernel (one l
 constexpr int64_t kMinPartBytes = 8192;  // of a row, when it is split
 constexpr int kCandidates = 1024;      // race candidates a CTA can hold
 constexpr float kMinTemperature = 1e-6f;  // below it a temperature counts as 0
-constexpr float kBig = 1e30f;          // maxima beyond it take the subtracting form below
+constexpr float kFar = 0x1p24f;        // |exponents| from it on take the subtracting form below
 constexpr double kLn2 = 0.69314718055994530942;
-// relative error bound of the float32 probabilities in the race (about 2^-22
-// from the exponent's rounding at 60 bits, ex2 and the products), with room
+// Relative error bound of the float32 probabilities in the race.  An exponent
+// between 0 and -126 (ex2 gives 0 beyond) is rounded once, by 2^-18 at most: 2.6e-6
+// of the weight.  ex2 adds 2^-22 of its own, the quotients, the products and
+// the noise's reciprocal (2^-23) less than 6e-7 together: 3.5e-6 of 1e-5.
 constexpr float kRaceMargin = 1e-5f;
 
 // 1 / x on the special-function unit (2^-23; infinite for 0).
@@ -63,23 +65,33 @@ struct Temper {
 };
 __device__ __forceinline__ Temper temper(float T) { return {__fdiv_rn(1.44269504f, T)}; }
 
-// Reference exponent of a row (or part of one) with maximum m: weights are
-// 2^(x c - r).  With r the rounded product, x c - r is rounded once, at its
-// own size: near the maximum, where the weights matter, it is exact to 2^-24.
-// Where the product would leave float32's range, weights are 2^((x - m) c).
+// Weights of a row (or part of one) with maximum m.  Near rows: 2^(x c - r) with
+// r the product m c rounded.  x c - r is rounded once, at its own size: near the
+// maximum, where the weights matter, it is exact to 2^-24 but for the rounding of
+// r, which all the weights and the sum share.  That is half a step of r: 1/2 below
+// 2^24, but beyond 2^31 more than ex2's range, and the weight of the maximum
+// itself would be infinite or 0.  So rows whose |m c| reaches 2^24 are far:
+// 2^((x - m) c), where x - m is exact for every x that has a weight.
 __device__ __forceinline__ float ref_of(float m, const Temper& t) { return m * t.c; }
-__device__ __forceinline__ bool is_big(float m) { return !(fabsf(m) < kBig); }
-__device__ __forceinline__ float exponent(float x, float m, float r, bool big, const Temper& t) {
-  if (big) {
+__device__ __forceinline__ bool is_far(float m, const Temper& t) {
+  return !(fabsf(ref_of(m, t)) < kFar);  // (also m = +-inf)
+}
+__device__ __forceinline__ float exponent(float x, float m, float r, bool far, const Temper& t) {
+  if (far) {
     return (x - m) * t.c;
   }
   return fmaf(x, t.c, -r);
 }
-// 2^(reference m1 - reference m2): moves a sum from one reference to a larger one
+// 2^(reference of m1 - reference of m2), m1 <= m2: moves a sum from one reference
+// to a larger one.  A far row's reference is m c itself, a near one's the rounded
+// product: between the two the product is taken exactly.
 __device__ __forceinline__ float rescale(float m1, float m2, const Temper& t) {
   if (m1 == m2) return 1.f;
   if (m1 == -INFINITY) return 0.f;
-  if (is_big(m1) || is_big(m2)) return ex2((m1 - m2) * t.c);
+  const bool f1 = is_far(m1, t), f2 = is_far(m2, t);
+  if (f1 && f2) return ex2((m1 - m2) * t.c);
+  if (f1) return ex2(fmaf(m1, t.c, -ref_of(m2, t)));
+  if (f2) return ex2(fmaf(-m2, t.c, ref_of(m1, t)));
   return ex2(ref_of(m1, t) - ref_of(m2, t));
 }
 __device__ __forceinline__ float warp_max(float x) {
@@ -107,7 +119,8 @@ __device__ __forceinline__ void warp_merge(float& m, float& s, const Temper& t) 
 // natural log of a weight in float64 (p is weight / sum)
 __device__ __forceinline__ double log_weight(float x, float m, const Temper& t) {
   const double c = (double)t.c;
-  const double e = is_big(m) ? ((double)x - (double)m) * c : (double)x * c - (double)ref_of(m, t);
+  const double e =
+      is_far(m, t) ? ((double)x - (double)m) * c : (double)x * c - (double)ref_of(m, t);
   return e * kLn2;
 }
 // Acceptance and log-probs within this of a border are looked at in float64
@@ -211,7 +224,7 @@ __device__ __forceinline__ RowStat row_stats(const T* row, int64_t v0, int64_t v
     acc23 = f2_mul(acc23, f2_pack(sc, sc));
     edge_s *= sc;
     m = M;
-    above = is_big(M) ? M : M + __fdividef(kRefSlack, t.c);
+    above = is_far(M, t) ? M : M + __fdividef(kRefSlack, t.c);
   };
   auto consume = [&](const uint4* d, int base) {
     const float bm = E::template batch_max<U>(d);
@@ -220,7 +233,7 @@ __device__ __forceinline__ RowStat row_stats(const T* row, int64_t v0, int64_t v
       top = bm;
       where = base;
     }
-    if (!is_big(m)) {
+    if (!is_far(m, t)) {
       const float nr = -ref_of(m, t);
       const uint64_t nr2 = f2_pack(nr, nr);
 #pragma unroll
@@ -234,18 +247,20 @@ __device__ __forceinline__ RowStat row_stats(const T* row, int64_t v0, int64_t v
           acc23 = f2_add(acc23, f2_ex2(f2_fma(x23, c2, nr2)));
         }
       }
-    } else {  // extreme values, or nothing but -inf and NaN so far
+    } else {  // (nothing but -inf and NaN so far: any reference gives 0 and NaN)
+      const float nm = m == -INFINITY ? 0.f : -m;
+      const uint64_t nm2 = f2_pack(nm, nm);
 #pragma unroll 1
       for (int u = 0; u < U; ++u) {
         float x[EPV];
         E::unpack(u == 0 ? d[0] : u == 1 ? d[1] : u == 2 ? d[2] : d[3], x);
 #pragma unroll
-        for (int k = 0; k < EPV; ++k)
-          if (x[k] != -INFINITY) edge_s += ex2(exponent(x[k], m, 0.f, true, t));
+        for (int k = 0; k < EPV; k += 2)
+          acc01 = f2_add(acc01, f2_ex2(f2_mul(f2_add(f2_pack(x[k], x[k + 1]), nm2), c2)));
       }
     }
   };
-  static_assert(U == 4, "the slow path names the vectors");
+  static_assert(U == 4, "the far rows' path names the vectors");
 
   const uint32_t mine = ring + 16 * tid;  // vector u of stage s: + (s * U + u) * kThreads * 16
   const T* src = row + a + (int64_t)tid * EPV;
@@ -298,8 +313,9 @@ __device__ __forceinline__ RowStat row_stats(const T* row, int64_t v0, int64_t v
     const float bm = fmaxf(xh, xt);
     if (__any_sync(kAll, bm > above)) adopt(bm);
     const float r = ref_of(m, t);
-    if (xh != -INFINITY) edge_s += ex2(exponent(xh, m, r, is_big(m), t));
-    if (xt != -INFINITY) edge_s += ex2(exponent(xt, m, r, is_big(m), t));
+    const bool far = is_far(m, t);
+    if (xh != -INFINITY) edge_s += ex2(exponent(xh, m, r, far, t));
+    if (xt != -INFINITY) edge_s += ex2(exponent(xt, m, r, far, t));
   }
   RowStat out;
   out.arg = INT64_MAX;
@@ -519,6 +535,7 @@ struct Shared {
   double wred[kRaceWarps];
   int64_t wred_at[kRaceWarps];
   int best, top, count;
+  float off[2], low[2];  // of the race's rows: offsets, factors of the lower bounds
   int abort;        // a bounded wait gave up
   uint32_t issued;  // steps of the ring that were copied
   uint64_t full[3], empty[3];
@@ -526,12 +543,11 @@ struct Shared {
   float cand_hi[kCandidates];
 };
 
-// The row's race in this CTA's slice: best score and its lowest index.
+// The rows of a race: their maxima and sums.
 struct Racer {
   Temper t;
-  float mt, rt, md, rd;      // maxima and reference exponents
-  float st, sd, lst, lsd;    // the sums and their log2
-  bool bigt, bigd, has_draft;
+  float mt, md, st, sd;
+  bool has_draft;
   int64_t skip;  // token without mass in the residual (drafts without logits), or -1
 };
 
@@ -551,44 +567,55 @@ __device__ __forceinline__ void better(double& s, int64_t& at, double s2, int64_
   }
 }
 
-// Lower and upper bound of a score, any row.
-__device__ __forceinline__ void race_bounds(const Racer& c, float x, float y, float e, float& lo,
-                                            float& hi) {
-  const float p = ex2(exponent(x, c.mt, c.rt, c.bigt, c.t) - c.lst);
-  const float q = c.has_draft ? ex2(exponent(y, c.md, c.rd, c.bigd, c.t) - c.lsd) : 0.f;
-  const float w = rcp(e), d = p - q, s = p + q;
-  lo = fmaf(s, -kRaceMargin, d) * w;
-  hi = fmaf(s, kRaceMargin, d) * w;
-}
-// The same for rows whose maxima are not extreme.  The sums are divided out
-// after the exponentials: taken into the exponents, their logarithms would be
-// rounded at the size of the references, which may be thousands.
-struct UsualRace {
-  float c, rt, rd;       // exponents: x c - r
-  float t_up, t_lo;      // (1 +- margin) / the target's sum
-  float d_up, d_lo;      // minus (1 -+ margin) / the draft's
+// Lower and upper bounds of scores, from exponents (x - o) c - r: o = 0 and the
+// rounded reference for a near row, the maximum and r = 0 for a far one.  The
+// sums are divided out after the exponentials: taken into the exponents, their
+// logarithms would be rounded at the size of the references, which may be
+// thousands.  What is rarely asked for (the offsets of far rows, the lower bounds'
+// factors) waits in shared memory: with an offset subtracted from every element
+// 128 sequences of 9 rows took 7 us more, by its registers.
+struct RaceBounds {
+  float c, rt, rd;   // exponents: x c - r
+  float t_up, d_up;  // (1 + margin) / the target's sum, (margin - 1) / the draft's
+  bool far;          // one of the rows is
 };
-__device__ __forceinline__ UsualRace usual_race(const Racer& c) {
-  const float it = __fdiv_rn(1.f, c.st), id = c.has_draft ? __fdiv_rn(1.f, c.sd) : 0.f;
+// By every thread, before a barrier: thread 0 leaves the shared part.
+__device__ __forceinline__ RaceBounds race_bounds_for(const Racer& c, Shared& sh) {
+  const float it = rcp(c.st), id = c.has_draft ? rcp(c.sd) : 0.f;
+  const bool ft = is_far(c.mt, c.t), fd = c.has_draft && is_far(c.md, c.t);
+  if (threadIdx.x == 0) {
+    sh.off[0] = ft ? c.mt : 0.f;
+    sh.off[1] = fd ? c.md : 0.f;
+    sh.low[0] = (1.f - kRaceMargin) * it;
+    sh.low[1] = (-kRaceMargin - 1.f) * id;
+  }
   return {c.t.c,
-          c.rt,
-          c.has_draft ? c.rd : 0.f,
+          ft ? 0.f : ref_of(c.mt, c.t),
+          c.has_draft && !fd ? ref_of(c.md, c.t) : 0.f,
           (1.f + kRaceMargin) * it,
-          (1.f - kRaceMargin) * it,
           (kRaceMargin - 1.f) * id,
-          (-kRaceMargin - 1.f) * id};
+          ft || fd};
+}
+template <bool kDraft, int N>
+__device__ __forceinline__ void race_offsets(const Shared& sh, float (&x)[N], float (&y)[N]) {
+  const float ot = sh.off[0], od = sh.off[1];
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    x[q] -= ot;
+    if (kDraft) y[q] -= od;
+  }
 }
 template <bool kDraft>
-__device__ __forceinline__ void race_bounds(const UsualRace& c, float x, float y, float e, float& lo,
-                                            float& hi) {
+__device__ __forceinline__ void race_bounds(const RaceBounds& c, float t_lo, float d_lo, float x,
+                                            float y, float e, float& lo, float& hi) {
   const float p = ex2(fmaf(x, c.c, -c.rt)), q = kDraft ? ex2(fmaf(y, c.c, -c.rd)) : 0.f;
   const float w = rcp(e);
-  lo = fmaf(q, c.d_lo, p * c.t_lo) * w;
+  lo = fmaf(q, d_lo, p * t_lo) * w;
   hi = fmaf(q, c.d_up, p * c.t_up) * w;
 }
 // The upper bounds of a pair of elements.
 template <bool kDraft>
-__device__ __forceinline__ uint64_t race_upper2(const UsualRace& c, float x0, float x1, float y0,
+__device__ __forceinline__ uint64_t race_upper2(const RaceBounds& c, float x0, float x1, float y0,
                                                 float y1, float e0, float e1) {
   const uint64_t c2 = f2_pack(c.c, c.c);
   const uint64_t p = f2_ex2(f2_fma(f2_pack(x0, x1), c2, f2_pack(-c.rt, -c.rt)));
@@ -651,16 +678,16 @@ __device__ __forceinline__ float lds_logit(uint32_t at, float) {
   return v;
 }
 
-// Rows with maxima of ordinary size: n8 groups of 8 elements from v0 on, pairs
-// of them through packed arithmetic.  kAligned: all three arrays are 16-byte
-// aligned at v0, and a thread takes 8 neighbours as vectors; otherwise it takes
-// elements kRaceThreads apart (and the row goes on for 8 elements either side,
-// which the copies may read).  `used` counts the ring's steps over all calls
-// (every thread the same).  Returns the largest upper bound.
+// n8 groups of 8 elements from v0 on, pairs of them through packed arithmetic.
+// kAligned: all three arrays are 16-byte aligned at v0, and a thread takes 8
+// neighbours as vectors; otherwise it takes elements kRaceThreads apart (and
+// the row goes on for 8 elements either side, which the copies may read).  `used`
+// counts the ring's steps over all calls (every thread the same).  Returns the
+// largest upper bound.
 template <typename T, bool kDraft, bool kAligned>
-__device__ __forceinline__ float race_stream(const Racer& c, const T* tr, const T* dr,
-                                             const float* nr, int64_t v0, int n8, Shared& sh,
-                                             uint32_t ring, uint32_t& used) {
+__device__ __forceinline__ float race_stream(const RaceBounds& rb, int64_t left_out, const T* tr,
+                                             const T* dr, const float* nr, int64_t v0, int n8,
+                                             Shared& sh, uint32_t ring, uint32_t& used) {
   using E = Elt<T>;
   constexpr int W = E::kPerVec == 8 ? 1 : 2;  // vectors of 8 logits
   constexpr uint32_t S = race_stages<T>(), kLogits = kRaceElems * sizeof(T) + 16;
@@ -692,9 +719,8 @@ __device__ __forceinline__ float race_stream(const Racer& c, const T* tr, const 
   };
   if (tid == 0)
     for (int k = 0; k < (int)S && k < steps; ++k) issue(k);
-  const UsualRace ur = usual_race(c);
-  const int64_t in = c.skip - v0;  // the token left out, if it is here
-  const int skip = c.skip >= 0 && in >= 0 && in < 8 * (int64_t)n8 ? (int)in : -1;
+  const int64_t in = left_out - v0;  // the token left out, if it is here
+  const int skip = left_out >= 0 && in >= 0 && in < 8 * (int64_t)n8 ? (int)in : -1;
   float bar = 0.f, largest = 0.f;
 #pragma unroll 1
   for (int step = 0, k = tid; step < steps; ++step, k += kRaceThreads) {
@@ -735,12 +761,13 @@ __device__ __forceinline__ float race_stream(const Racer& c, const T* tr, const 
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sh.empty[st]));
+    if (rb.far) race_offsets<kDraft>(sh, x, y);
     if (!kAligned || k < n8) {
 #pragma unroll
       for (int q = 0; q < 8; q += 2) {
         const uint64_t h =
-            kDraft ? race_upper2<true>(ur, x[q], x[q + 1], y[q], y[q + 1], e[q], e[q + 1])
-                   : race_upper2<false>(ur, x[q], x[q + 1], 0.f, 0.f, e[q], e[q + 1]);
+            kDraft ? race_upper2<true>(rb, x[q], x[q + 1], y[q], y[q + 1], e[q], e[q + 1])
+                   : race_upper2<false>(rb, x[q], x[q + 1], 0.f, 0.f, e[q], e[q + 1]);
         float h0, h1;
         f2_unpack(h, h0, h1);
         most = fmaxf(most, fmaxf(h0, h1));
@@ -751,12 +778,13 @@ __device__ __forceinline__ float race_stream(const Racer& c, const T* tr, const 
     bar = fmaxf(bar, __int_as_float(*(volatile int*)&sh.best));
     if (__any_sync(0xffffffffu, most > 0.f && most >= bar)) {
       float hi[8], top = 0.f;
+      const float t_lo = sh.low[0], d_lo = sh.low[1];
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         hi[q] = 0.f;
         if ((!kAligned || k < n8) && first + q * apart != skip) {
           float lo;
-          race_bounds<kDraft>(ur, x[q], kDraft ? y[q] : 0.f, e[q], lo, hi[q]);
+          race_bounds<kDraft>(rb, t_lo, d_lo, x[q], kDraft ? y[q] : 0.f, e[q], lo, hi[q]);
           top = fmaxf(top, lo);
         }
       }
@@ -775,6 +803,7 @@ __device__ Bounds race_bounds_of(const Racer& c, const T* tr, const T* dr, const
                                  uint32_t& used) {
   using E = Elt<T>;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const RaceBounds rb = race_bounds_for(c, sh);
   if (tid == 0) {
     sh.best = 0;
     sh.top = 0;
@@ -785,22 +814,20 @@ __device__ Bounds race_bounds_of(const Racer& c, const T* tr, const T* dr, const
   float largest = 0.f;
   // [v0, head) and [tail, v1) are left to single loads
   int64_t head = v0, tail = v0;
-  const bool usual = !c.bigt && !(c.has_draft && c.bigd);
   if constexpr (kAligned) {
-    if (usual) {
-      const int n8 = (int)((v1 - v0) / 8);
-      largest = c.has_draft ? race_stream<T, true, true>(c, tr, dr, nr, v0, n8, sh, ring, used)
-                            : race_stream<T, false, true>(c, tr, dr, nr, v0, n8, sh, ring, used);
-      tail = v0 + (int64_t)n8 * 8;
-    }
-  } else if (usual && v1 - v0 >= 32) {
+    const int n8 = (int)((v1 - v0) / 8);
+    largest = c.has_draft ? race_stream<T, true, true>(rb, c.skip, tr, dr, nr, v0, n8, sh, ring, used)
+                          : race_stream<T, false, true>(rb, c.skip, tr, dr, nr, v0, n8, sh, ring, used);
+    tail = v0 + (int64_t)n8 * 8;
+  } else if (v1 - v0 >= 32) {
     head = v0 + 8;
     const int n8 = (int)((v1 - 8 - head) / 8);
-    largest = c.has_draft ? race_stream<T, true, false>(c, tr, dr, nr, head, n8, sh, ring, used)
-                          : race_stream<T, false, false>(c, tr, dr, nr, head, n8, sh, ring, used);
+    largest = c.has_draft ? race_stream<T, true, false>(rb, c.skip, tr, dr, nr, head, n8, sh, ring, used)
+                          : race_stream<T, false, false>(rb, c.skip, tr, dr, nr, head, n8, sh, ring, used);
     tail = head + (int64_t)n8 * 8;
   }
   constexpr int M = 4;
+  const float t_lo = sh.low[0], d_lo = sh.low[1];
   const int64_t singles = (head - v0) + (v1 - tail);
   auto single = [&](int64_t k) { return k < head - v0 ? v0 + k : tail + (k - (head - v0)); };
   for (int64_t base = 0; base < singles; base += kRaceThreads * M) {
@@ -814,13 +841,17 @@ __device__ Bounds race_bounds_of(const Racer& c, const T* tr, const T* dr, const
         e[w] = __ldg(nr + v);
       }
     }
+    if (rb.far) race_offsets<true>(sh, x, y);
 #pragma unroll
     for (int w = 0; w < M; ++w) {
       const int64_t k = base + w * kRaceThreads + tid;
       hi[w] = 0.f;
       if (k < singles && single(k) != c.skip) {
         float lo;
-        race_bounds(c, x[w], y[w], e[w], lo, hi[w]);
+        if (c.has_draft)
+          race_bounds<true>(rb, t_lo, d_lo, x[w], y[w], e[w], lo, hi[w]);
+        else
+          race_bounds<false>(rb, t_lo, d_lo, x[w], 0.f, e[w], lo, hi[w]);
         top = fmaxf(top, lo);
       }
       largest = fmaxf(largest, hi[w]);
@@ -1011,16 +1042,10 @@ __global__ void __launch_bounds__(kRaceThreads, 2) verify_emit_kernel(
   Racer c;
   c.t = t;
   c.mt = d.mt;
-  c.rt = ref_of(d.mt, t);
-  c.bigt = is_big(d.mt);
-  c.lst = __log2f(d.st);
   c.st = d.st;
   c.md = d.md;
-  c.rd = ref_of(d.md, t);
-  c.bigd = is_big(d.md);
   c.sd = d.sd;
   c.has_draft = drow != nullptr;
-  c.lsd = __log2f(d.sd);
   c.skip = draft == nullptr && !bonus ? d.token : -1;
   int64_t token = d.emit == 2 ? d.arg : -1;
   uint32_t used = 0;
