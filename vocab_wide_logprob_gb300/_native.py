@@ -532,7 +532,9 @@ def grpo_lmhead_loss_bwd(hidden, weight, P, input_ids, lens, lse, w, grad_loss=N
 # The operators around the loss.  Their tensors are checked and marshalled in
 # C++ (csrc/binding.cpp, module _ops): these calls are short, or take hundreds
 # of tensors.  A tensor of the wrong type raises TypeError, one of the wrong
-# shape, layout or device ValueError, a refused call GrpoError.
+# shape, layout or device ValueError, a refused call GrpoError.  With a ``stream``
+# given, what a call allocates is memory of that stream, as under
+# torch.cuda.stream(stream).
 
 
 def grpo_embed_fwd(ids, weight, scale=1.0, out=None, out_dtype=None, stream=None):

@@ -13,6 +13,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -64,15 +65,31 @@ grpo_dtype code(at::ScalarType t, const char* name) {
   if (t == at::kBFloat16) return GRPO_BF16;
   refuse(PyExc_TypeError, "%s must be float32 or bfloat16", name);
 }
-grpo_stream_t stream_of(PyObject* o) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
-  PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
-  if (h == nullptr) throw Refused();
-  void* p = PyLong_AsVoidPtr(h);
-  Py_DECREF(h);
-  if (PyErr_Occurred()) throw Refused();
-  return (grpo_stream_t)p;
-}
+// The stream of a call: the given one (anything with a `cuda_stream`), or the
+// device's current one.  Until the call returns a given stream is the current one, so
+// that what the call allocates comes from that stream's memory: a workspace that
+// the caller drops while the kernels still run is handed out to that stream only.
+class CallStream {
+ public:
+  CallStream(PyObject* o, const c10::Device& dev) {
+    if (o == Py_None) {
+      handle_ = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+      return;
+    }
+    PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
+    if (h == nullptr) throw Refused();
+    void* p = PyLong_AsVoidPtr(h);
+    Py_DECREF(h);
+    if (PyErr_Occurred()) throw Refused();
+    handle_ = (cudaStream_t)p;
+    guard_.reset_stream(c10::cuda::getStreamFromExternal(handle_, dev.index()));
+  }
+  operator grpo_stream_t() const { return (grpo_stream_t)handle_; }
+
+ private:
+  cudaStream_t handle_;
+  c10::cuda::OptionalCUDAStreamGuard guard_;
+};
 void on_device(const Tensor& t, const char* name, const c10::Device& dev) {
   if (!t.is_cuda() || t.device() != dev)
     refuse(PyExc_ValueError, "%s must be a CUDA tensor on the device of the others", name);
@@ -186,6 +203,7 @@ PyObject* embed_fwd(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const float scale = (float)number(a[2]);
     const at::ScalarType dt = dtype_or(a[4], a[3] == Py_None ? weight.scalar_type()
                                                               : tensor(a[3], "out").scalar_type());
+    const CallStream st(a[5], dev);
     Tensor out;
     int64_t ldo = d;
     if (a[3] == Py_None) {
@@ -201,7 +219,6 @@ PyObject* embed_fwd(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
       ldo = row_pitch(out, "out", n, d);
     }
     const grpo_dtype ocode = code(dt, "out");
-    const grpo_stream_t st = stream_of(a[5]);
     check_status(launch([&] {
                    return grpo_embed_fwd((const int64_t*)ids.data_ptr(), n, weight.data_ptr(),
                                          wcode, V, d, ldw, scale, out.data_ptr(), ocode, ldo, st);
@@ -243,6 +260,7 @@ PyObject* embed_bwd(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const float scale = (float)number(a[3]);
     const int64_t pad = a[4] == Py_None ? -1 : integer(a[4]);
     const int accumulate = PyObject_IsTrue(a[6]);
+    const CallStream st(a[9], dev);
     Tensor dw;
     int64_t ldw = d;
     if (a[5] == Py_None) {
@@ -263,7 +281,6 @@ PyObject* embed_bwd(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     size_t need = 0;
     check_status(grpo_embed_workspace_size(n, V, d, &need), "grpo_embed_workspace_size");
     const Tensor ws = workspace_of(a[8], need, dev);
-    const grpo_stream_t st = stream_of(a[9]);
     check_status(launch([&] {
                    return grpo_embed_bwd((const int64_t*)ids.data_ptr(), n, dout.data_ptr(), dcode,
                                          V, d, ldd, scale, pad, dw.data_ptr(), wcode, ldw,
@@ -328,6 +345,7 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     }
     size_t need = 0;
     check_status(grpo_grad_norm_workspace_size(n, &need), "grpo_grad_norm_workspace_size");
+    const CallStream st(a[7], dev);
     Tensor stats, ws;
     if (a[5] == Py_None && a[6] == Py_None) {
       ws = workspace_and(need, 2, dev, &stats);
@@ -339,7 +357,6 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
       if (stats.numel() < 2) refuse(PyExc_ValueError, "%s must hold two values", "stats");
     }
     if (!ws.defined()) ws = workspace_of(a[6], need, dev);
-    const grpo_stream_t st = stream_of(a[7]);
     float* sp = (float*)stats.data_ptr();
     check_status(launch([&] {
                    return norm_only
@@ -414,6 +431,7 @@ PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
       contiguous(*temp, "temperature", at::kFloat, dev);
       shaped(*temp, "temperature", {N});
     }
+    const CallStream st(a[9], dev);
     Tensor tokens, accepted, logp;
     PyObject* given_ws = a[8];
     if (a[7] == Py_None) {
@@ -439,7 +457,6 @@ PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     size_t need = 0;
     check_status(grpo_verify_workspace_size(N, K, &need), "grpo_verify_workspace_size");
     const Tensor ws = workspace_of(given_ws, need, dev);
-    const grpo_stream_t st = stream_of(a[9]);
     check_status(
         launch([&] {
           return grpo_verify_drafts(
