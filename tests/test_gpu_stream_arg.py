@@ -95,3 +95,62 @@ def test_results_on_a_given_stream(name):
     for a, b in zip(got, want):
         if a.dtype != torch.uint8:  # (not the workspace)
             assert torch.equal(a, b)
+
+
+def loss_calls():
+    n = g()
+    N, P, C, V, d = 4, 3, 5, 2048, 128
+    dev = dict(device="cuda")
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    logits = torch.randn(N, P + C, V, generator=gen, **dev)
+    ids = torch.randint(0, V, (N, P + C), generator=gen, **dev)
+    lens = torch.tensor([5, 0, 3, 1], dtype=torch.int32, **dev)
+    adv = torch.randn(N, generator=gen, **dev)
+    hidden = torch.randn(N, P + C, d, generator=gen, **dev).bfloat16()
+    weight = torch.randn(V, d, generator=gen, **dev).bfloat16()
+    host = logits.cpu().pin_memory()
+    f = n.grpo_loss_fwd(logits, P, ids, lens, adv)
+    torch.cuda.synchronize()
+
+    def cuda(out):
+        return tuple(out[k] for k in sorted(out))
+
+    return {
+        "mask": lambda **k: n.grpo_mask(ids, P, C, V - 1, **k),
+        "advantage": lambda **k: (n.grpo_advantage(adv, 2, **k),),
+        "advantage_ex": lambda **k: n.grpo_advantage_ex(adv, 2, count_contrast=True, **k),
+        "loss_fwd": lambda **k: cuda(n.grpo_loss_fwd(logits, P, ids, lens, adv, **k)),
+        "logprobs": lambda **k: n.grpo_logprobs(logits, P, ids, lens, **k),
+        "loss_fwd_static": lambda **k: cuda(n.grpo_loss_fwd_static(logits, P, ids, lens, adv, **k)),
+        "loss_bwd": lambda **k: (n.grpo_loss_bwd(logits, P, ids, lens, f["lse"], f["w"], **k),),
+        "loss_fwd_bwd": lambda **k: cuda(n.grpo_loss_fwd_bwd(logits, P, ids, lens, adv, **k)),
+        "loss_fwd_bwd_host": lambda **k: cuda(n.grpo_loss_fwd_bwd_host(host, P, ids, lens, adv, **k)),
+        "lmhead_logprobs": lambda **k: n.grpo_lmhead_logprobs(hidden, weight, P, ids, lens, **k),
+        "lmhead_loss_fwd": lambda **k: cuda(n.grpo_lmhead_loss_fwd(hidden, weight, P, ids, lens, adv,
+                                                                   **k)),
+        "lmhead_loss_bwd": lambda **k: n.grpo_lmhead_loss_bwd(hidden, weight, P, ids, lens, f["lse"],
+                                                              f["w"], **k),
+    }
+
+
+LOSS_NAMES = ["mask", "advantage", "advantage_ex", "loss_fwd", "logprobs", "loss_fwd_static",
+              "loss_bwd", "loss_fwd_bwd", "loss_fwd_bwd_host", "lmhead_logprobs",
+              "lmhead_loss_fwd", "lmhead_loss_bwd"]
+
+
+@pytest.mark.parametrize("name", LOSS_NAMES)
+def test_loss_calls_allocate_on_the_given_stream(name):
+    call = loss_calls()[name]
+    want = [t.clone() for t in call()]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    handle = type("Handle", (), {"cuda_stream": side.cuda_stream})()
+    for s in (side, torch.cuda.ExternalStream(side.cuda_stream), handle):
+        out = call(stream=s)
+        side.synchronize()
+        for t, b in zip(out, want):
+            assert stream_of_memory(t) == side.cuda_stream
+            if t.dtype != torch.uint8 and name != "loss_fwd_bwd_host":  # (its staging has unread rows)
+                assert torch.equal(t, b)
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()

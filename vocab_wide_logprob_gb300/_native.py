@@ -2,7 +2,8 @@
 
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels behind these calls.  Functions take PyTorch tensors for device
-memory, pass ``tensor.data_ptr()`` and the current CUDA stream, and raise
+memory, pass ``tensor.data_ptr()`` and the current CUDA stream (or the given
+``stream``, whose memory what they allocate then is), and raise
 :class:`GrpoError` on any status other than ``GRPO_OK``.  There is no CPU
 fallback: importing this module fails loudly when the library is missing.
 """
@@ -121,6 +122,18 @@ def _stream(stream=None):
     return stream.cuda_stream
 
 
+def _empty(stream, shape, dtype, device):
+    """torch.empty in the memory of the stream that the call runs on: with a
+    ``stream`` given, a workspace that the caller drops while the kernels still
+    use it goes back to that stream alone."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -156,9 +169,9 @@ def grpo_mask(input_ids: torch.Tensor, P: int, C: int, eos_id: int, mask=None, l
     _dev(input_ids, "input_ids", torch.int64)
     N = input_ids.shape[0]
     if mask is None:
-        mask = torch.empty((N, C), dtype=torch.uint8, device=input_ids.device)
+        mask = _empty(stream, (N, C), dtype=torch.uint8, device=input_ids.device)
     if len_out is None:
-        len_out = torch.empty((N,), dtype=torch.int32, device=input_ids.device)
+        len_out = _empty(stream, (N,), dtype=torch.int32, device=input_ids.device)
     _check(_lib.grpo_mask(_ptr(input_ids), N, P, C, int(eos_id), _ptr(mask), _ptr(len_out),
                           _stream(stream)), "grpo_mask")
     return mask, len_out
@@ -168,7 +181,7 @@ def grpo_advantage(rewards: torch.Tensor, G: int, adv=None, stream=None):
     """Dr. GRPO advantage: R_i minus its group's mean, float32 [B*G]."""
     _dev(rewards, "rewards", torch.float32)
     if adv is None:
-        adv = torch.empty_like(rewards)
+        adv = _empty(stream, rewards.shape, dtype=rewards.dtype, device=rewards.device)
     n = rewards.numel()
     if G < 1 or n % G:
         raise ValueError("len(rewards) must be a multiple of G >= 1")
@@ -184,11 +197,11 @@ def grpo_advantage_ex(rewards: torch.Tensor, G: int, mode: int = GRPO_ADV_DR, st
     tensor).  Returns ``(adv, n_contrast or None)``."""
     _dev(rewards, "rewards", torch.float32)
     if adv is None:
-        adv = torch.empty_like(rewards)
+        adv = _empty(stream, rewards.shape, dtype=rewards.dtype, device=rewards.device)
     n = rewards.numel()
     if G < 1 or n % G:
         raise ValueError("len(rewards) must be a multiple of G >= 1")
-    cnt = torch.empty((1,), dtype=torch.int32, device=rewards.device) if count_contrast else None
+    cnt = _empty(stream, (1,), dtype=torch.int32, device=rewards.device) if count_contrast else None
     _check(_lib.grpo_advantage_ex(_ptr(rewards), n // G, G, int(mode), float(std_eps), _ptr(adv),
                                   _ptr(cnt), _stream(stream)), "grpo_advantage_ex")
     return adv, cnt
@@ -217,13 +230,13 @@ def grpo_loss_fwd(logits, P, input_ids, lens, adv, old_logp=None, ref_logp=None,
         _dev(t, name, dt)
     dev = logits.device
     if out is None:
-        out = {"logp": torch.empty((N, C), dtype=torch.float32, device=dev),
-               "lse": torch.empty((N, C), dtype=torch.float32, device=dev),
-               "w": torch.empty((N, C), dtype=torch.float32, device=dev),
-               "loss": torch.empty((1,), dtype=torch.float32, device=dev)}
+        out = {"logp": _empty(stream, (N, C), dtype=torch.float32, device=dev),
+               "lse": _empty(stream, (N, C), dtype=torch.float32, device=dev),
+               "w": _empty(stream, (N, C), dtype=torch.float32, device=dev),
+               "loss": _empty(stream, (1,), dtype=torch.float32, device=dev)}
     need = grpo_workspace_size(N, C, V)
     if workspace is None or workspace.numel() < need:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        workspace = _empty(stream, (need,), dtype=torch.uint8, device=dev)
     out["workspace"] = workspace
     head = (_ptr(logits), _dtype_code(logits), N, P, C, V, _ptr(input_ids), _ptr(lens), _ptr(adv),
             _ptr(old_logp), _ptr(ref_logp), float(eps), float(beta), float(norm))
@@ -255,11 +268,11 @@ def grpo_logprobs(logits, P, input_ids, lens, out=None, workspace=None, stream=N
     _dev(lens, "lens", torch.int32)
     dev = logits.device
     if out is None:
-        out = (torch.empty((N, C), dtype=torch.float32, device=dev),
-               torch.empty((N, C), dtype=torch.float32, device=dev))
+        out = (_empty(stream, (N, C), dtype=torch.float32, device=dev),
+               _empty(stream, (N, C), dtype=torch.float32, device=dev))
     need = grpo_workspace_size(N, C, V)
     if workspace is None or workspace.numel() < need:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        workspace = _empty(stream, (need,), dtype=torch.uint8, device=dev)
     _check(_lib.grpo_logprobs(_ptr(logits), _dtype_code(logits), N, P, C, V, _ptr(input_ids),
                               _ptr(lens), _ptr(out[0]), _ptr(out[1]), _ptr(workspace),
                               workspace.numel(), _stream(stream)), "grpo_logprobs")
@@ -282,10 +295,10 @@ def grpo_loss_fwd_static(logits, P, input_ids, lens, adv, old_logp=None, ref_log
         _dev(t, name, dt)
     dev = logits.device
     if out is None:
-        out = {"logp": torch.empty((N, C), dtype=torch.float32, device=dev),
-               "lse": torch.empty((N, C), dtype=torch.float32, device=dev),
-               "w": torch.empty((N, C), dtype=torch.float32, device=dev),
-               "loss": torch.empty((1,), dtype=torch.float32, device=dev)}
+        out = {"logp": _empty(stream, (N, C), dtype=torch.float32, device=dev),
+               "lse": _empty(stream, (N, C), dtype=torch.float32, device=dev),
+               "w": _empty(stream, (N, C), dtype=torch.float32, device=dev),
+               "loss": _empty(stream, (1,), dtype=torch.float32, device=dev)}
     _check(_lib.grpo_loss_fwd_static(
         _ptr(logits), _dtype_code(logits), N, P, C, V, _ptr(input_ids), _ptr(lens), _ptr(adv),
         _ptr(old_logp), _ptr(ref_logp), float(eps), float(beta), float(norm), _ptr(out["logp"]),
@@ -305,7 +318,7 @@ def grpo_loss_bwd(logits, P, input_ids, lens, lse, w, grad_loss=None, dlogits=No
                         ("grad_loss", grad_loss, torch.float32)):
         _dev(t, name, dt)
     if dlogits is None:
-        dlogits = torch.empty_like(logits)
+        dlogits = _empty(stream, logits.shape, dtype=logits.dtype, device=logits.device)
     _dev(dlogits, "dlogits", logits.dtype)
     args = (_ptr(logits), _dtype_code(logits), N, P, C, V, _ptr(input_ids), _ptr(lens), _ptr(lse),
             _ptr(w), _ptr(grad_loss), _ptr(dlogits))
@@ -337,15 +350,15 @@ def grpo_loss_fwd_bwd(logits, P, input_ids, lens, adv, old_logp=None, ref_logp=N
         _dev(t, name, dt)
     dev = logits.device
     if out is None:
-        out = {"logp": torch.empty((N, C), dtype=torch.float32, device=dev),
-               "lse": torch.empty((N, C), dtype=torch.float32, device=dev),
-               "w": torch.empty((N, C), dtype=torch.float32, device=dev),
-               "loss": torch.empty((1,), dtype=torch.float32, device=dev)}
+        out = {"logp": _empty(stream, (N, C), dtype=torch.float32, device=dev),
+               "lse": _empty(stream, (N, C), dtype=torch.float32, device=dev),
+               "w": _empty(stream, (N, C), dtype=torch.float32, device=dev),
+               "loss": _empty(stream, (1,), dtype=torch.float32, device=dev)}
     need = grpo_workspace_size(N, C, V)
     if workspace is None or workspace.numel() < need:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        workspace = _empty(stream, (need,), dtype=torch.uint8, device=dev)
     if dlogits is None:
-        dlogits = torch.empty_like(logits)
+        dlogits = _empty(stream, logits.shape, dtype=logits.dtype, device=logits.device)
     _dev(dlogits, "dlogits", logits.dtype)
     out["workspace"] = workspace
     out["dlogits"] = dlogits
@@ -381,17 +394,17 @@ def grpo_loss_fwd_bwd_host(host_logits, P, input_ids, lens, adv, old_logp=None, 
         _dev(t, name, dt)
     dev = input_ids.device
     if out is None:
-        out = {"logp": torch.empty((N, C), dtype=torch.float32, device=dev),
-               "lse": torch.empty((N, C), dtype=torch.float32, device=dev),
-               "w": torch.empty((N, C), dtype=torch.float32, device=dev),
-               "loss": torch.empty((1,), dtype=torch.float32, device=dev)}
+        out = {"logp": _empty(stream, (N, C), dtype=torch.float32, device=dev),
+               "lse": _empty(stream, (N, C), dtype=torch.float32, device=dev),
+               "w": _empty(stream, (N, C), dtype=torch.float32, device=dev),
+               "loss": _empty(stream, (1,), dtype=torch.float32, device=dev)}
     need = grpo_workspace_size(N, C, V)
     if workspace is None or workspace.numel() < need:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        workspace = _empty(stream, (need,), dtype=torch.uint8, device=dev)
     if dlogits is None:
-        dlogits = torch.empty(host_logits.shape, dtype=host_logits.dtype, device=dev)
+        dlogits = _empty(stream, host_logits.shape, dtype=host_logits.dtype, device=dev)
     if staging is None:
-        staging = torch.empty(host_logits.shape, dtype=host_logits.dtype, device=dev)
+        staging = _empty(stream, host_logits.shape, dtype=host_logits.dtype, device=dev)
     if dlogits.is_cuda:
         _dev(dlogits, "dlogits", host_logits.dtype)
     elif (not dlogits.is_pinned() or not dlogits.is_contiguous()
@@ -433,13 +446,13 @@ def grpo_lmhead_logprobs(hidden, weight, P, input_ids, lens, out=None, workspace
         raise ValueError("weight must be [V, d]")
     dev = hidden.device
     if out is None:
-        out = (torch.empty((N, C), dtype=torch.float32, device=dev),
-               torch.empty((N, C), dtype=torch.float32, device=dev))
+        out = (_empty(stream, (N, C), dtype=torch.float32, device=dev),
+               _empty(stream, (N, C), dtype=torch.float32, device=dev))
     need = ctypes.c_size_t(0)
     _check(_lib.grpo_lmhead_workspace_size(N, C, V, d, ctypes.byref(need)),
            "grpo_lmhead_workspace_size")
     if workspace is None or workspace.numel() < need.value:
-        workspace = torch.empty((need.value,), dtype=torch.uint8, device=dev)
+        workspace = _empty(stream, (need.value,), dtype=torch.uint8, device=dev)
     _check(_lib.grpo_lmhead_logprobs(_ptr(hidden), _ptr(weight), N, P, C, V, d, _ptr(input_ids),
                                      _ptr(lens), _ptr(out[0]), _ptr(out[1]), _ptr(workspace),
                                      workspace.numel(), _stream(stream)), "grpo_lmhead_logprobs")
@@ -466,13 +479,13 @@ def grpo_lmhead_loss_fwd(hidden, weight, P, input_ids, lens, adv, old_logp=None,
         raise ValueError("weight must be [V, d]")
     dev = hidden.device
     if out is None:
-        out = {k: torch.empty((N, C), dtype=torch.float32, device=dev) for k in ("logp", "lse", "w")}
-        out["loss"] = torch.empty((1,), dtype=torch.float32, device=dev)
+        out = {k: _empty(stream, (N, C), dtype=torch.float32, device=dev) for k in ("logp", "lse", "w")}
+        out["loss"] = _empty(stream, (1,), dtype=torch.float32, device=dev)
     need = ctypes.c_size_t(0)
     _check(_lib.grpo_lmhead_workspace_size(N, C, V, d, ctypes.byref(need)),
            "grpo_lmhead_workspace_size")
     if workspace is None or workspace.numel() < need.value:
-        workspace = torch.empty((need.value,), dtype=torch.uint8, device=dev)
+        workspace = _empty(stream, (need.value,), dtype=torch.uint8, device=dev)
     out["workspace"] = workspace
     head = (_ptr(hidden), _ptr(weight), N, P, C, V, d, _ptr(input_ids), _ptr(lens), _ptr(adv),
             _ptr(old_logp), _ptr(ref_logp), float(eps), float(beta), float(norm))
@@ -514,11 +527,11 @@ def grpo_lmhead_loss_bwd(hidden, weight, P, input_ids, lens, lse, w, grad_loss=N
     C = T - P
     dev = hidden.device
     if out is None:
-        out = (torch.empty((N, T, d), dtype=torch.float32, device=dev),
-               torch.empty((V, d), dtype=torch.float32, device=dev))
+        out = (_empty(stream, (N, T, d), dtype=torch.float32, device=dev),
+               _empty(stream, (V, d), dtype=torch.float32, device=dev))
     if workspace is None:
         need = grpo_lmhead_bwd_workspace_size(N, C, V, d, rows_per_pass)
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        workspace = _empty(stream, (need,), dtype=torch.uint8, device=dev)
     head = (_ptr(hidden), _ptr(weight), N, P, C, V, d, _ptr(input_ids), _ptr(lens), _ptr(lse),
             _ptr(w), _ptr(grad_loss), _ptr(out[0]), _ptr(out[1]))
     tail = (_ptr(workspace), workspace.numel(), _stream(stream))
