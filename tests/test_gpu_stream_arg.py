@@ -154,3 +154,11 @@ def test_loss_calls_allocate_on_the_given_stream(name):
             if t.dtype != torch.uint8 and name != "loss_fwd_bwd_host":  # (its staging has unread rows)
                 assert torch.equal(t, b)
     assert torch.cuda.current_stream() == torch.cuda.default_stream()
+
+
+def test_a_stream_of_another_device_is_refused():
+    n = g()
+    other = type("Other", (), {"cuda_stream": 0, "device_index": 7})()
+    ids, w = torch.zeros(3, dtype=torch.int64, device="cuda"), torch.zeros(4, 8, device="cuda")
+    with pytest.raises(ValueError, match="stream"):
+        n.grpo_embed_fwd(ids, w, stream=other)

@@ -187,6 +187,26 @@ def test_binding_refuses_cpu_tensors_and_wrong_types(n):
                              torch.zeros(2, 0), torch.zeros(2, 8))
 
 
+def _on(device, *shapes, dtype=torch.float32):
+    """Tensors that say they are on ``device`` and have no memory."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    with FakeTensorMode():
+        return [torch.zeros(s, dtype=dtype, device=device) for s in shapes]
+
+
+def test_binding_refuses_tensors_of_another_device(n):
+    """The library launches on the current device: tensors that agree with one
+    another but are on a device that is not current are refused before anything
+    is allocated or launched."""
+    (ids,), (x,) = _on("cuda:7", 4, dtype=torch.int64), _on("cuda:7", (2, 2), dtype=torch.int64)
+    w, dout, z, u, e = _on("cuda:7", (8, 16), (4, 16), (2, 3, 16), (2, 2), (2, 16))
+    for call in (lambda: n.grpo_embed_fwd(ids, w), lambda: n.grpo_embed_bwd(ids, dout, 8),
+                 lambda: n.grpo_clip_grad_norm([w, dout], 1.0), lambda: n.grpo_grad_norm([w]),
+                 lambda: n.grpo_verify_drafts(z, x, u, e)):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call()
+
+
 def test_package_exports():
     import vocab_wide_logprob_gb300 as pkg
     for name in ("grpo_embed_fwd", "grpo_embed_bwd", "grpo_clip_grad_norm", "grpo_grad_norm",

@@ -13,6 +13,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -82,6 +83,15 @@ class CallStream {
     Py_DECREF(h);
     if (PyErr_Occurred()) throw Refused();
     handle_ = (cudaStream_t)p;
+    PyObject* d = PyObject_GetAttrString(o, "device_index");
+    if (d != nullptr) {
+      const int64_t index = integer(d);
+      Py_DECREF(d);
+      if (index != dev.index())
+        refuse(PyExc_ValueError, "%s must be of the tensors' device", "stream");
+    } else {
+      PyErr_Clear();  // (a bare handle)
+    }
     guard_.reset_stream(c10::cuda::getStreamFromExternal(handle_, dev.index()));
   }
   operator grpo_stream_t() const { return (grpo_stream_t)handle_; }
@@ -93,6 +103,20 @@ class CallStream {
 void on_device(const Tensor& t, const char* name, const c10::Device& dev) {
   if (!t.is_cuda() || t.device() != dev)
     refuse(PyExc_ValueError, "%s must be a CUDA tensor on the device of the others", name);
+}
+// The device of a call: its first tensor's, which has to be the current one (the
+// library launches there, on that device's streams and with its properties).
+c10::Device device_of(const Tensor& t, const char* name) {
+  const c10::Device dev = t.device();
+  on_device(t, name, dev);
+  c10::DeviceIndex current = -1;
+  if (c10::cuda::GetDevice(&current) != cudaSuccess) {
+    (void)cudaGetLastError();
+    current = -1;
+  }
+  if (dev.index() != current)
+    refuse(PyExc_ValueError, "%s must be on the current CUDA device", name);
+  return dev;
 }
 void contiguous(const Tensor& t, const char* name, at::ScalarType dtype, const c10::Device& dev) {
   on_device(t, name, dev);
@@ -192,7 +216,7 @@ PyObject* embed_fwd(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   if (!count_is(n_args, 6)) return nullptr;
   return guarded([&]() -> PyObject* {
     const Tensor& ids = tensor(a[0], "ids");
-    const c10::Device dev = ids.device();
+    const c10::Device dev = device_of(ids, "ids");
     contiguous(ids, "ids", at::kLong, dev);
     const Tensor& weight = tensor(a[1], "weight");
     on_device(weight, "weight", dev);
@@ -247,7 +271,7 @@ PyObject* embed_bwd(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   if (!count_is(n_args, 10)) return nullptr;
   return guarded([&]() -> PyObject* {
     const Tensor& ids = tensor(a[0], "ids");
-    const c10::Device dev = ids.device();
+    const c10::Device dev = device_of(ids, "ids");
     contiguous(ids, "ids", at::kLong, dev);
     const Tensor& dout = tensor(a[1], "dout");
     on_device(dout, "dout", dev);
@@ -316,7 +340,7 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const float eps = norm_only ? 0.f : (float)number(a[4]);
     const grpo_norm_type type = (grpo_norm_type)integer(a[3]);
     const c10::Device dev =
-        n > 0 ? tensor(grads.at(0), "every gradient").device()
+        n > 0 ? device_of(tensor(grads.at(0), "every gradient"), "every gradient")
               : c10::Device(c10::kCUDA, c10::cuda::getCurrentCUDAStream().device_index());
     std::vector<grpo_tensor> table((size_t)n);
     for (Py_ssize_t k = 0; k < n; ++k) {
@@ -395,8 +419,7 @@ PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   if (!count_is(n_args, 10)) return nullptr;
   return guarded([&]() -> PyObject* {
     const Tensor& z = tensor(a[0], "target_logits");
-    const c10::Device dev = z.device();
-    on_device(z, "target_logits", dev);
+    const c10::Device dev = device_of(z, "target_logits");
     if (z.dim() != 3) refuse(PyExc_ValueError, "%s must be [N, K+1, V]", "target_logits");
     const int64_t N = z.size(0), rows = z.size(1), V = z.size(2), K = rows - 1;
     if (K < 0) refuse(PyExc_ValueError, "%s must have a row per sequence", "target_logits");
