@@ -187,11 +187,20 @@ def test_binding_refuses_cpu_tensors_and_wrong_types(n):
                              torch.zeros(2, 0), torch.zeros(2, 8))
 
 
+class _Elsewhere(torch.Tensor):
+    """A tensor that says it is on a device and has no memory."""
+
+    @staticmethod
+    def __new__(cls, device, shape, dtype=torch.float32):
+        return torch.Tensor._make_wrapper_subclass(cls, shape, dtype=dtype, device=device)
+
+    @classmethod
+    def __torch_dispatch__(cls, func, types, args=(), kwargs=None):
+        raise AssertionError(f"{func} on a tensor without memory")
+
+
 def _on(device, *shapes, dtype=torch.float32):
-    """Tensors that say they are on ``device`` and have no memory."""
-    from torch._subclasses.fake_tensor import FakeTensorMode
-    with FakeTensorMode():
-        return [torch.zeros(s, dtype=dtype, device=device) for s in shapes]
+    return [_Elsewhere(device, s if isinstance(s, tuple) else (s,), dtype) for s in shapes]
 
 
 def test_binding_refuses_tensors_of_another_device(n):
