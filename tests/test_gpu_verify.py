@@ -442,6 +442,40 @@ def test_rows_behind_a_rejection(dt, N, V):
     both(case(N, 4, V, dt, 17, err=0.6, ragged=True))
 
 
+@pytest.mark.parametrize("dt,N,V", [(BF16, 300, 40001), (F32, 120, 60000), (BF16, 80, 151936)])
+@pytest.mark.parametrize("draft", [True, False], ids=["drafted", "copied"])
+def test_rows_behind_rejections_of_every_kind(dt, N, V, draft):
+    """Calls that leave rows out, with all that can stop a sequence: rejections,
+    greedy ones, undefined rows and temperatures, ids outside [0, V).  The
+    workspace holds ones before, so that a part read early shows."""
+    K = 4 if draft else 8
+    assert N * V * (2 if dt == BF16 else 4) * (2 * K + 1 if draft else K + 1) > 192 << 20
+    c = case(N, K, V, dt, 23, draft, err=0.5, temp=True, ragged=True)
+    r = gen(24)
+    c["lens"][::2] = K
+    c["temp"][torch.rand(N, generator=r, device="cuda") < 0.4] = 0.0
+    right = (torch.rand(N, K, generator=r, device="cuda") < 0.8) & (c["temp"] == 0).view(N, 1)
+    c["x"] = torch.where(right, c["z"][:, :K].float().argmax(-1), c["x"])
+    c["temp"][1::17] = -1.0
+    c["temp"][2::19] = math.nan
+    at = torch.randint(0, K, (N,), generator=r, device="cuda")
+    for i in range(0, N, 7):
+        c["x"][i, at[i]] = (-1, V, 1 << 40)[i % 3]
+    for i in range(3, N, 11):
+        c["z"][i, at[i], V // 3] = math.nan
+    for i in range(4, N, 13):
+        c["z"][i, at[i]] = -math.inf
+    if draft:
+        for i in range(5, N, 9):
+            c["y"][i, at[i], 7] = math.nan
+    need = g().grpo_verify_workspace_size(N, K)
+    want = reference(**c)
+    for _ in range(3):
+        out = run(c, workspace=torch.full((need,), 255, dtype=torch.uint8, device="cuda"))
+        assert g().grpo_check_error(out["workspace"]) == 6
+        check(out, want, V)
+
+
 def test_distribution_of_the_emitted_tokens():
     """Over many sequences of one distribution, the first emitted or accepted
     token follows the target: a chi-square bound at 7 sigma."""

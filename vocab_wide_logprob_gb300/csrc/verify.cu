@@ -454,13 +454,16 @@ __global__ void __launch_bounds__(kThreads, 4) verify_rows_kernel(const VerifyPa
   const int64_t j = jq, i = q - jq * (unsigned)p.N;
   // (loads that are in flight together: each costs a CTA's start its latency)
   uint32_t flags = 0;
-  const int32_t stop = p.lazy ? *(volatile int32_t*)(p.rejected + i) : INT32_MAX;
+  // (one thread reads it for all: other CTAs lower it meanwhile)
+  int32_t stop = INT32_MAX;
+  if (p.lazy && tid == 0) stop = *(volatile int32_t*)(p.rejected + i);
   int64_t x = -1;  // the drafted token
   if (tid == 0 && j < p.K) x = p.tokens[i * p.K + j];
   const float Ti = temperature_of(p, i);
   const int32_t len = clamped_len(p, i, &flags);
   const bool greedy = Ti < kMinTemperature;
-  if (j > len || (is_draft && (j == len || greedy)) || stop < j) return;
+  if (j > len || (is_draft && (j == len || greedy))) return;
+  if (p.lazy && __syncthreads_or(stop < j)) return;
   const Temper t = temper(greedy ? 1.f : Ti);
   const int64_t v0 = min(p.V, s * p.part_elems), v1 = min(p.V, v0 + p.part_elems);
   const T* row = is_draft ? draft + i * p.dls + j * p.dld : target + i * p.tls + j * p.tld;
