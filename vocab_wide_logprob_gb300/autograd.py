@@ -8,13 +8,34 @@ embedding lookup (grpo_embed_fwd / grpo_embed_bwd).
 Of the losses, only the logits (or the hidden states and the LM head) receive a gradient.  The advantages, old and reference
 log-probs are constants of the update step (the advantage comes from the
 rewards, the old and reference log-probs from no-grad passes), so their
-gradients are None.
+gradients are None.  The gradients are first-order: under create_graph=True they
+can be used like any, but a second derivative through them raises.
 """
 from __future__ import annotations
 
 import torch
 
 from . import _native as g
+
+
+class _FirstOrder(torch.autograd.Function):
+    """A gradient as it is, hung onto what it was computed from, so that a
+    derivative of it is refused rather than left out."""
+
+    @staticmethod
+    def forward(ctx, grad, *of):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("this gradient has no derivative: the library's backward passes are "
+                           "first-order")
+
+
+def _first_order(grad, *of):
+    """``grad`` of a backward pass that used the tensors ``of``.  (Gradients are
+    enabled in a backward pass only under create_graph=True.)"""
+    return _FirstOrder.apply(grad, *of) if torch.is_grad_enabled() else grad
 
 
 class GRPOLoss(torch.autograd.Function):
@@ -37,7 +58,7 @@ class GRPOLoss(torch.autograd.Function):
         logits, input_ids, lens, lse, w = ctx.saved_tensors
         gl = grad_loss.detach().reshape(1).to(torch.float32).contiguous()
         dlogits = g.grpo_loss_bwd(logits, ctx.P, input_ids, lens, lse, w, gl)
-        return (dlogits,) + (None,) * 10
+        return (_first_order(dlogits, logits, grad_loss),) + (None,) * 10
 
 
 def grpo_loss(logits, P, input_ids, lens, adv, old_logp=None, ref_logp=None, eps=0.2, beta=0.0,
@@ -66,7 +87,7 @@ class GRPOEmbedding(torch.autograd.Function):
         # (the gradient of a broadcast or transposed use arrives with other strides)
         dw, _ = g.grpo_embed_bwd(ids, dout.contiguous(), ctx.V, ctx.scale, ctx.pad_id,
                                  out_dtype=ctx.wdtype)
-        return None, dw, None, None, None
+        return None, _first_order(dw, dout), None, None, None
 
 
 def grpo_embed(ids, weight, scale=1.0, pad_id=None, out_dtype=None):
@@ -110,7 +131,8 @@ class GRPOLMHeadLoss(torch.autograd.Function):
             rpp = max(1, int(lens.sum().item()))
         dh, dw, _ = g.grpo_lmhead_loss_bwd(hidden, weight, ctx.P, input_ids, lens, lse, w, gl,
                                            rows_per_pass=rpp)
-        return (dh, dw) + (None,) * 11
+        of = (hidden, weight, grad_loss)
+        return (_first_order(dh, *of), _first_order(dw, *of)) + (None,) * 11
 
 
 def grpo_lmhead_loss(hidden, weight, P, input_ids, lens, adv, old_logp=None, ref_logp=None,
