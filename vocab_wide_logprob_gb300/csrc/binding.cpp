@@ -159,6 +159,11 @@ Tensor workspace_and(size_t need, int64_t count, const c10::Device& dev, Tensor*
   *floats = Tensor(std::move(impl));
   return w;
 }
+// A tensor of the caller's has new values: autograd refuses a backward pass that
+// saved the old ones.
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
 size_t bytes_of(const Tensor& t) { return (size_t)t.numel() * t.element_size(); }
 
 // Rows of d elements: the pitch of the last-but-one dimension of a tensor of
@@ -248,8 +253,9 @@ PyObject* embed_fwd(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                                          wcode, V, d, ldw, scale, out.data_ptr(), ocode, ldo, st);
                  }),
                  "grpo_embed_fwd");
-    if (a[3] != Py_None) return Py_NewRef(a[3]);
-    return THPVariable_Wrap(out);
+    if (a[3] == Py_None) return THPVariable_Wrap(out);
+    written(out);
+    return Py_NewRef(a[3]);
   });
 }
 
@@ -311,6 +317,7 @@ PyObject* embed_bwd(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                                          accumulate, ws.data_ptr(), bytes_of(ws), st);
                  }),
                  "grpo_embed_bwd");
+    if (a[5] != Py_None) written(dw);
     return pair(wrap(a[5], dw), wrap(a[8], ws));
   });
 }
@@ -352,6 +359,7 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
       g.out = nullptr;
       g.numel = t.numel();
       g.dtype = g.out_dtype = code(t.scalar_type(), "every gradient");
+      if (!norm_only && a[2] == Py_None) written(t);
     }
     if (a[2] != Py_None) {
       const Items outs(a[2], "out must be a list of tensors");
@@ -365,6 +373,7 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
           refuse(PyExc_ValueError, "%s must have its gradient's size", "every out");
         g.out = t.data_ptr();
         g.out_dtype = code(t.scalar_type(), "every out");
+        if (!norm_only) written(t);
       }
     }
     size_t need = 0;
@@ -390,6 +399,7 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
                                                     ws.data_ptr(), bytes_of(ws), st);
                  }),
                  norm_only ? "grpo_grad_norm" : "grpo_clip_grad_norm");
+    if (a[5] != Py_None) written(stats);
     return pair(wrap(a[5], stats), wrap(a[6], ws));
   });
 }
@@ -492,6 +502,8 @@ PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
               ws.data_ptr(), bytes_of(ws), st);
         }),
         "grpo_verify_drafts");
+    if (a[7] != Py_None)
+      for (const Tensor* t : {&tokens, &accepted, &logp}) written(*t);
     PyObject* out = a[7] == Py_None ? PyDict_New() : Py_NewRef(a[7]);
     if (out == nullptr) return nullptr;
     auto put = [&](const char* key, PyObject* v) {  // takes v
