@@ -216,6 +216,17 @@ def test_binding_refuses_tensors_of_another_device(n):
             call()
 
 
+def test_binding_hands_on_an_argument_without_a_truth_value(n):
+    class Neither:
+        def __bool__(self):
+            raise ZeroDivisionError("neither")
+
+    ids, = _on("cuda:7", 4, dtype=torch.int64)
+    dout, dw = _on("cuda:7", (4, 16), (8, 16))
+    with pytest.raises(ZeroDivisionError):
+        n.grpo_embed_bwd(ids, dout, 8, dweight=dw, accumulate=Neither())
+
+
 def test_package_exports():
     import vocab_wide_logprob_gb300 as pkg
     for name in ("grpo_embed_fwd", "grpo_embed_bwd", "grpo_clip_grad_norm", "grpo_grad_norm",

@@ -61,6 +61,11 @@ int64_t integer(PyObject* o) {
   if (v == -1 && PyErr_Occurred()) throw Refused();
   return v;
 }
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Refused();
+  return v != 0;
+}
 grpo_dtype code(at::ScalarType t, const char* name) {
   if (t == at::kFloat) return GRPO_F32;
   if (t == at::kBFloat16) return GRPO_BF16;
@@ -276,6 +281,7 @@ PyObject* wrap(PyObject* given, const Tensor& t) {
 PyObject* embed_bwd(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   if (!count_is(n_args, 10)) return nullptr;
   return guarded([&]() -> PyObject* {
+    const bool accumulate = truth(a[6]);
     const Tensor& ids = tensor(a[0], "ids");
     const c10::Device dev = device_of(ids, "ids");
     contiguous(ids, "ids", at::kLong, dev);
@@ -289,7 +295,6 @@ PyObject* embed_bwd(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const int64_t ldd = row_pitch(dout, "dout", n, d);
     const float scale = (float)number(a[3]);
     const int64_t pad = a[4] == Py_None ? -1 : integer(a[4]);
-    const int accumulate = PyObject_IsTrue(a[6]);
     const CallStream st(a[9], dev);
     Tensor dw;
     int64_t ldw = d;
@@ -342,7 +347,7 @@ PyObject* clip(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return guarded([&]() -> PyObject* {
     const Items grads(a[0], "grads must be a list of tensors");
     const Py_ssize_t n = grads.size();
-    const bool norm_only = PyObject_IsTrue(a[8]) == 1;
+    const bool norm_only = truth(a[8]);
     const float max_norm = norm_only ? 0.f : (float)number(a[1]);
     const float eps = norm_only ? 0.f : (float)number(a[4]);
     const grpo_norm_type type = (grpo_norm_type)integer(a[3]);
