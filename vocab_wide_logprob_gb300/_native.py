@@ -105,9 +105,34 @@ def _load():
 
 _lib = _load()
 
-from . import _ops  # noqa: E402  (the operators around the loss; linked to libgrpo.so)
 
-_ops.set_error(GrpoError)
+class _NoOps:
+    """Stands for the module _ops where it cannot be used: the loss calls do
+    without it, the operators around the loss raise."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{self._why}: build it with `python -m vocab_wide_logprob_gb300.build`")
+
+
+def _load_ops():
+    """The module _ops (csrc/binding.cpp, linked to libgrpo.so), if it is there
+    and was compiled against this PyTorch and this Python."""
+    from .build import binding_target
+    try:
+        from . import _ops as ops
+    except ImportError as e:
+        return _NoOps(f"the binding _ops.so of the operators around the loss does not load ({e})")
+    have, want = getattr(ops, "built_for", None), binding_target()
+    if have != want:
+        return _NoOps(f"_ops.so was compiled against {have}, not {want}")
+    ops.set_error(GrpoError)
+    return ops
+
+
+_ops = _load_ops()
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 

@@ -12,6 +12,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import glob
 import os
+import runpy
 import shutil
 import subprocess
 import sys
@@ -82,18 +83,39 @@ def _torch_dir() -> str:
     return os.path.dirname(importlib.util.find_spec("torch").origin)
 
 
+def binding_target() -> str:
+    """What ``_ops.so`` has to be compiled against: this PyTorch and this Python."""
+    version = runpy.run_path(os.path.join(_torch_dir(), "version.py"))["__version__"]
+    return f"torch {version}, {sys.implementation.cache_tag}"
+
+
+def _binding_stale(obj: str) -> bool:
+    """Whether the object is older than its sources or was compiled against
+    another PyTorch or Python (noted in a file beside it)."""
+    if _stale(obj, [BINDING_SOURCE, *glob.glob(os.path.join(INCLUDE, "*.h"))]):
+        return True
+    try:
+        with open(obj + ".target") as f:
+            return f.read() != binding_target()
+    except OSError:
+        return True
+
+
 def _compile_binding() -> str:
     obj = os.path.join(BUILD, "binding.o")
-    if _stale(obj, [BINDING_SOURCE, *glob.glob(os.path.join(INCLUDE, "*.h"))]):
-        inc = os.path.join(_torch_dir(), "include")
+    if _binding_stale(obj):
+        target, inc = binding_target(), os.path.join(_torch_dir(), "include")
         dirs = [INCLUDE, inc, os.path.join(inc, "torch", "csrc", "api", "include"),
                 sysconfig.get_paths()["include"], os.path.join(cuda_home(), "include")]
         cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+               f'-DGRPO_BUILT_FOR="{target}"',
                *[x for d in dirs for x in ("-isystem" if d != INCLUDE else "-I", d)],
                "-c", BINDING_SOURCE, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"g++ failed on {BINDING_SOURCE}:\n{r.stderr}")
+        with open(obj + ".target", "w") as f:
+            f.write(target)
     return obj
 
 
@@ -120,7 +142,6 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True) 
     with cf.ThreadPoolExecutor(max_workers=min(9, len(srcs) + 1)) as ex:
         binding = ex.submit(_compile_binding)
         results = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
-        binding = binding.result()
     objs = [o for o, _ in results]
     if verbose_ptxas and not quiet:
         for _, log in results:
@@ -134,7 +155,8 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True) 
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIBRARY)
-    _link_binding(binding, force)
+    # (after the library: the loss calls work without the binding)
+    _link_binding(binding.result(), force)
     return LIBRARY
 
 

@@ -546,4 +546,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__ops() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__ops() {
+  PyObject* m = PyModule_Create(&module);
+  // what it was compiled against; _native.py compares
+  if (m != nullptr && PyModule_AddStringConstant(m, "built_for", GRPO_BUILT_FOR) != 0) Py_CLEAR(m);
+  return m;
+}
