@@ -38,16 +38,6 @@ inline int warp_slot(int64_t d, size_t esize) {
 inline size_t warp_rings(int64_t d, size_t esize, int depth) {
   return (size_t)kWarps * depth * warp_slot(d, esize) + kWarpCols * esize;
 }
-__device__ __forceinline__ float lds_elt(uint32_t at, uint16_t) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
-  return bf16_bits_to_float(v);
-}
-__device__ __forceinline__ float lds_elt(uint32_t at, float) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
-  return v;
-}
 // The pieces of `width` bytes from p on, by the warp; `off` bytes of them lie
 // before p.  Through L1: neighbouring parts share a piece, and the rows of
 // frequent ids would queue at their L2 slices (130,000 rows of 130 floats of 2,979
@@ -144,7 +134,9 @@ __global__ void __launch_bounds__(kThreads) embed_fwd_any_kernel(
     const uint32_t from = at + past(id, put.c) + lane * kElt;
     TO* q = out + (row0 + put.r) * ldo + put.c + lane;
     const float f = id < 0 ? __int_as_float(0x7fc00000) : scale;
-    // (32 N columns, or up to as many)
+    // (32 N columns, or up to as many.  Up to 160 columns five loads per lane, above
+    // that eight: 130,000 rows of 130 floats 18.9 us, of 33 18.6, with eight 19.9 and
+    // 19.5; 65,536 rows of 901 bfloat16, 133 of them in a row's last part, 37.5 and 38.5)
     auto copy = [&](auto cols, int left) {
       constexpr int N = decltype(cols)::value;
       float x[N];
@@ -330,13 +322,13 @@ SortPlan sort_plan(int64_t n, int64_t V, int64_t d) {
   if (s.tile < kBatch) s.tile = kBatch;
   s.tiles = (int)((n + s.tile - 1) / s.tile);
   // few tokens: shorter groups, so that there are enough of them (about 512
-  // threads on each of 152 SMs); 4 entries where 8 leave fewer than 64 (777 tokens
+  // threads on each SM); 4 entries where 8 leave fewer than 64 (777 tokens
   // of 130 columns 11.6 us, 12.8 with 8; 42,115 of 64 columns 32.3, 30.5 with 8)
   s.seg = kMaxSegEntries;
   while (s.seg > kMinSegEntries &&
-         (n + s.seg - 1) / s.seg * (padded_cols(d, true) / 8) < 152 * 512)
+         (n + s.seg - 1) / s.seg * (padded_cols(d, true) / 8) < kPlanSms * 512)
     s.seg /= 2;
-  if (s.seg == kMinSegEntries && (n + 7) / 8 * (padded_cols(d, true) / 8) < 152 * 64) s.seg /= 2;
+  if (s.seg == kMinSegEntries && (n + 7) / 8 * (padded_cols(d, true) / 8) < kPlanSms * 64) s.seg /= 2;
   s.seg_tiles = (n + s.seg - 1) / s.seg;
   return s;
 }

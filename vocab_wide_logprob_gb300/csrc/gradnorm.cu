@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 4) grad_scale_kernel(const __grid_co
 // ---------------------------------------------------------------------------
 
 constexpr int kMaxTensors = 768;     // tensors of one launch: the parameters stay below 32 KiB
-constexpr int kMaxPartials = 152 * 8;  // CTAs of one norm launch
+constexpr int kMaxPartials = kPlanSms * 8;  // CTAs of one norm launch
 static_assert(sizeof(Table<kMaxTensors>) < 32000, "kernel parameters");
 
 template <int CAP>

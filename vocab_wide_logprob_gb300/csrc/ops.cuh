@@ -20,6 +20,18 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// One element at a shared-memory address, as float.
+__device__ __forceinline__ float lds_elt(uint32_t at, uint16_t) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+  return bf16_bits_to_float(v);
+}
+__device__ __forceinline__ float lds_elt(uint32_t at, float) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+  return v;
+}
+
 template <bool kStream>
 __device__ __forceinline__ void st_32bytes(void* p, const float* x) {
   if (kStream)
@@ -40,11 +52,6 @@ struct Vec8 {
   __device__ __forceinline__ void load(const TI* p) {
 #pragma unroll
     for (int k = 0; k < kWords; ++k) v[k] = reinterpret_cast<const uint4*>(p)[k];
-  }
-  // through the read-only path, not kept in L1
-  __device__ __forceinline__ void load_stream(const TI* p) {
-#pragma unroll
-    for (int k = 0; k < kWords; ++k) v[k] = ld_stream(reinterpret_cast<const uint4*>(p) + k);
   }
   __device__ __forceinline__ void fill(uint32_t word) {
 #pragma unroll
@@ -78,6 +85,10 @@ struct Vec8 {
     }
   }
 };
+
+// SMs that plans are made for which the workspace's size depends on (its size is
+// asked for without a device).
+constexpr int kPlanSms = 152;
 
 // ---- embedding lookup and its gradient (embed.cu) ---------------------------
 

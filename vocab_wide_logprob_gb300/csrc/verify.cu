@@ -670,17 +670,6 @@ __device__ __forceinline__ void race_keep(Shared& sh, float hi, float bar, int64
   }
 }
 
-__device__ __forceinline__ float lds_logit(uint32_t at, uint16_t) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
-  return bf16_bits_to_float(v);
-}
-__device__ __forceinline__ float lds_logit(uint32_t at, float) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
-  return v;
-}
-
 // n8 groups of 8 elements from v0 on, pairs of them through packed arithmetic.
 // kAligned: all three arrays are 16-byte aligned at v0, and a thread takes 8
 // neighbours as vectors; otherwise it takes elements kRaceThreads apart (and
@@ -743,9 +732,9 @@ __device__ __forceinline__ float race_stream(const RaceBounds& rb, int64_t left_
       for (int q = 0; q < 8; ++q) {
         const uint32_t o = (uint32_t)(tid + q * kRaceThreads);
         const bool in = first + q * apart < 8 * n8;
-        x[q] = in ? lds_logit(at + ot + o * (uint32_t)sizeof(T), T()) : -INFINITY;
-        y[q] = kDraft && in ? lds_logit(at + kLogits + od + o * (uint32_t)sizeof(T), T()) : -INFINITY;
-        e[q] = in ? lds_logit(at + 2 * kLogits + on + o * 4, float()) : 1.f;
+        x[q] = in ? lds_elt(at + ot + o * (uint32_t)sizeof(T), T()) : -INFINITY;
+        y[q] = kDraft && in ? lds_elt(at + kLogits + od + o * (uint32_t)sizeof(T), T()) : -INFINITY;
+        e[q] = in ? lds_elt(at + 2 * kLogits + on + o * 4, float()) : 1.f;
       }
     } else if (k < n8) {
       if (W == 1) {
