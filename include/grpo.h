@@ -489,9 +489,10 @@ grpo_status grpo_embed_fwd(const int64_t *ids, int64_t n, const void *weight, gr
  * `wdtype`, ldw apart.  The tokens are sorted by id (stable) and each id's
  * rows added in float32 in a fixed order that depends on the ids alone, so
  * results are bitwise reproducible; one rounding to `wdtype`.
- * workspace: at least grpo_embed_workspace_size(n, V, d) bytes (about 16
- * bytes per token, 2 * d * 4 / 32 bytes per token of partial sums, one byte
- * per id).
+ * workspace: at least grpo_embed_workspace_size(n, V, d) bytes: 16 bytes per
+ * token, partial sums of 8 bytes per column for every group of 4 to 32 tokens
+ * (32 where there are many; d padded to a multiple of 256, above 2,048 of 2,048)
+ * and the sort's histograms, 2 KB per pass for every 2,048 tokens or more.
  */
 grpo_status grpo_embed_workspace_size(int64_t n, int64_t V, int64_t d, size_t *bytes);
 grpo_status grpo_embed_bwd(const int64_t *ids, int64_t n, const void *dout, grpo_dtype ddtype,
@@ -525,9 +526,10 @@ typedef enum {
  * another except out == data).  stats: two float32 in device memory, norm and
  * coef.  In place with coef = 1 nothing is written; with another output
  * everything is.  max_norm >= 0 (infinity: no limit), eps >= 0.
- * Squares are summed in float32 per thread and batch and in float64 beyond,
- * scaled by a power of two where they would leave float32's range, in a fixed
- * order: results are bitwise reproducible.  A norm that is not finite is
+ * Squares are summed in float32 per thread and batch and as pairs of floats
+ * (about 2^-47) beyond; batches whose squares would leave float32's range are scaled by a
+ * power of two and summed in float64, as are the thread blocks' totals, in a
+ * fixed order: results are bitwise reproducible.  A norm that is not finite is
  * reported by grpo_check_error as GRPO_ERR_VALUE; the formula is followed
  * (an infinite norm gives coef 0, NaN stays NaN).
  * workspace: at least grpo_grad_norm_workspace_size(count) bytes.
@@ -570,7 +572,10 @@ grpo_status grpo_grad_norm(const grpo_tensor *tensors, int64_t count, grpo_norm_
  * target_logits: row j of sequence i starts at element i * target_seq + j *
  * target_row; draft_logits the same with its strides (ignored when NULL);
  * both of `dtype`, aligned to their element.  draft_tokens [N, K] int64, u
- * [N, K] float32, noise float32 rows noise_row apart, positive and finite.
+ * [N, K] float32, noise float32 rows noise_row apart, of values from 2^-60 to
+ * 2^30 (exponential samples are; p / noise is held in float32 until few tokens
+ * are left).  The outputs and the workspace overlap neither one another nor an
+ * input.
  * Outputs: tokens [N, K+1] int64 (the accepted ones, the emitted one, then
  * -1), n_accepted [N] int32, logp [N, K+1] float32 (log p_j of tokens[i, j],
  * then 0).

@@ -257,6 +257,22 @@ def test_close_scores_far_from_zero(dt, draft, V):
     both(c)
 
 
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("at", [0, 17, 2501, 5002])
+def test_noise_at_the_ends_of_its_range(dt, at):
+    """An improbable token (2^-99) whose noise is 2^-60 beats, or not, the rest."""
+    V = 5003
+    c = case(4, 0, V, dt, 25)
+    c["z"].zero_()
+    c["z"][:, :, at] = -60.0
+    for rest, wins in ((2.0 ** 30, True), (1.0, False)):
+        c["noise"] = rest * (1 + torch.rand(4, V, generator=gen(26), device="cuda") / 2)
+        c["noise"].clamp_(max=2.0 ** 30)
+        c["noise"][:, at] = 2.0 ** -60
+        out = both(c)
+        assert ((out["tokens"] == at).all()) == wins
+
+
 def far_case(dt, V, T, rows):
     """One sequence per entry of ``rows`` (float64 [V]), nothing drafted, at temperature T."""
     z = torch.stack([r.to(dt) for r in rows]).unsqueeze(1).cuda()

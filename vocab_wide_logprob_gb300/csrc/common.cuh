@@ -180,13 +180,16 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 // writes to be visible, so no ordering is lost, while the launch and the
 // shared-memory prologue overlap the previous kernel's tail.  pdl_trigger()
 // lets the next kernel start launching; it is issued once this kernel's
-// CTAs are all resident, so it cannot take their slots.  Two exceptions:
+// CTAs are all resident, so it cannot take their slots.  Three exceptions:
 // the backward, launched right after the loss forward on the same stream,
 // writes the rows that score nothing before its wait (dlogits.cu); and the
 // loss forward's log-sum-exp kernel, launched right after prep (which waits
 // before it triggers, so every kernel before prep has completed when it
 // starts), reads the raw lengths and the logits before its wait, and waits
-// only before it touches what prep writes (the workspace header).
+// only before it touches what prep writes (the workspace header); likewise the
+// kernel that ends a verification of drafts, launched after a kernel that waits
+// before it triggers, reads lengths and temperatures and prefetches the noise
+// (verify.cu).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -175,7 +175,7 @@ struct Decision {
 // The rows kernel streams a row through shared memory: every thread copies its
 // own 16-byte vectors kRowStages batches ahead (asynchronous copies, read back
 // by the thread that issued them: no barrier, no registers).  The ring alone
-// reads 6.2 TB/s; with the exponentials 4.6 TB/s (242 MB in 52 us at 128
+// reads 6.2 TB/s; with the exponentials 4.8 TB/s (247 MB in 51 us at 128
 // sequences of 5 rows of 151,936 bfloat16 and their drafts), bound by issue
 // slots: one unpack, half a packed FMA and one ex2 per element, and some 600
 // instructions per warp and part around them.
@@ -423,7 +423,7 @@ __device__ __forceinline__ void decide(const VerifyParams& p, bool has_draft, in
 
 // One row part per CTA.  Grid order: positions, then sequences, then kinds
 // (target, draft), then parts, so that a position's decision is known before
-// most of the next position's CTAs begin: 242 of 350 MB are read at 128 x 4
+// most of the next position's CTAs begin: 247 of 350 MB are read at 128 x 4
 // drafts of which 73% are accepted, where 207 MB are needed.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) verify_rows_kernel(const VerifyParams p,
@@ -634,8 +634,9 @@ __device__ __forceinline__ uint64_t race_upper2(const RaceBounds& c, float x0, f
 // The race streams its rows in steps of 8 elements per thread of target, draft
 // and noise: bulk copies (TMA), race_stages() steps ahead, issued by thread 0
 // when every warp has released the stage.  Copies begin at the 16-byte boundary
-// at or before an array's first element.  156 MB in 28 us of the emitting
-// kernel's 44 (128 sequences); with per-thread copies the call took 5 us more.
+// at or before an array's first element.  156 MB in the emitting kernel's 41 us,
+// decisions included (128 sequences); with per-thread copies the call took 5 us
+// more.
 constexpr int kRaceElems = 8 * kRaceThreads;
 template <typename T>
 __host__ __device__ constexpr int race_stages() {
@@ -956,8 +957,9 @@ __device__ __forceinline__ void cluster_or_cta_sync(uint32_t ranks) {
 }
 
 // kAligned: every row of the three arrays, and every slice of one, begins at a
-// 16-byte boundary.  (Two kernels: with both loops in one the registers of the
-// unaligned rows' made the other spill, 102 us for 90 at 128 sequences.)
+// 16-byte boundary.  (Two kernels: with both loops in one 102 us instead of 90 at
+// 128 sequences.  At two CTAs per SM there are 64 registers per thread; the
+// aligned rows' kernel keeps 120 bytes on its stack, the other 8 to 16.)
 template <typename T, bool kAligned>
 __global__ void __launch_bounds__(kRaceThreads, 2) verify_emit_kernel(
     const VerifyParams p, const T* __restrict__ target, const T* __restrict__ draft) {
