@@ -216,6 +216,26 @@ def test_binding_refuses_tensors_of_another_device(n):
             call()
 
 
+def test_loss_calls_refuse_tensors_of_another_device(n, monkeypatch):
+    monkeypatch.setattr(n, "_current_device", lambda: 0)
+    i64, i32 = dict(dtype=torch.int64), dict(dtype=torch.int32)
+    (ids,), (lens,) = _on("cuda:7", (2, 8), **i64), _on("cuda:7", 2, **i32)
+    logits, adv, lse = _on("cuda:7", (2, 8, 100), (2,), (2, 4))
+    hidden, weight = _on("cuda:7", (2, 8, 128), (100, 128), dtype=torch.bfloat16)
+    for call in (lambda: n.grpo_mask(ids, 4, 4, 9), lambda: n.grpo_advantage(adv, 2),
+                 lambda: n.grpo_advantage_ex(adv, 2),
+                 lambda: n.grpo_loss_fwd(logits, 4, ids, lens, adv),
+                 lambda: n.grpo_loss_fwd_static(logits, 4, ids, lens, adv),
+                 lambda: n.grpo_loss_fwd_bwd(logits, 4, ids, lens, adv),
+                 lambda: n.grpo_loss_bwd(logits, 4, ids, lens, lse, lse),
+                 lambda: n.grpo_logprobs(logits, 4, ids, lens),
+                 lambda: n.grpo_lmhead_logprobs(hidden, weight, 4, ids, lens),
+                 lambda: n.grpo_lmhead_loss_fwd(hidden, weight, 4, ids, lens, adv),
+                 lambda: n.grpo_lmhead_loss_bwd(hidden, weight, 4, ids, lens, lse, lse)):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call()
+
+
 def test_binding_hands_on_an_argument_without_a_truth_value(n):
     class Neither:
         def __bool__(self):

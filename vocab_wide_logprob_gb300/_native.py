@@ -134,6 +134,7 @@ def _load_ops():
 
 _ops = _load_ops()
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 def library() -> ctypes.CDLL:
@@ -143,7 +144,7 @@ def library() -> ctypes.CDLL:
 def _stream(stream=None):
     """Handle of ``stream``, or of the current device's current stream."""
     if stream is None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_current_device())
     return stream.cuda_stream
 
 
@@ -179,8 +180,11 @@ def _dtype_code(t: torch.Tensor) -> int:
 def _dev(t, name, dtype=None):
     if t is None:
         return
-    if not t.is_cuda:
+    device = t.get_device()  # (-1: host memory)
+    if device < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if device != _current_device():  # (the library launches there)
+        raise ValueError(f"{name} must be on the current CUDA device")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
