@@ -599,9 +599,129 @@ grpo_status grpo_verify_drafts(const void *target_logits, const void *draft_logi
                                size_t workspace_bytes, grpo_stream_t stream);
 
 /*
+ * grpo_token_stats -- log-probs of given tokens, the entropy and the likeliest
+ * alternatives of every row of logits: what a rollout reports of its tokens
+ * and what an update watches or rewards.  For row j < L_i of sequence i (L_i =
+ * len[i]; NULL: R) with logits z, given token y and T = temperature[i] (NULL: 1;
+ * below 1e-6, a greedy sequence: 1, as in grpo_verify_drafts):
+ *   m = max_v z_v,  L = ln sum_v exp((z_v - m) / T)
+ *   logp    = (z_y - m) / T - L
+ *   entropy = L - sum_v p_v (z_v - m) / T,   p_v = exp((z_v - m) / T - L)
+ *   norm    = (m, L)     (what grpo_token_stats_bwd takes; their sum at T = 1
+ *                         is the log-sum-exp)
+ *   top_tokens, top_logp: the `top` largest z_v, largest first, the lowest v of
+ *             equal ones first, and their log-probs
+ * -inf logits (banned tokens) have probability 0 and add nothing to the
+ * entropy.  Rows j >= L_i are not read; they get logp, entropy, norm and
+ * top_logp 0 and top_tokens -1.
+ *
+ * logits: row j of sequence i starts at element i * logits_seq + j *
+ * logits_row (rows of [N, P+C, V] logits: logits + (P-1) * V, logits_seq =
+ * (P+C) * V), `dtype`, aligned to its element; tokens: row j of sequence i at
+ * i * token_seq + j, int64.  logp, entropy [N, R], norm [N, R, 2] float32;
+ * top_tokens [N, R, top] int64, top_logp [N, R, top] float32 (NULL with top
+ * 0).  0 <= top <= 32, top <= V; N * R <= 2^26, V < 2^31 - 2^16.  The outputs and the
+ * workspace overlap neither one another nor an input.
+ * A row without a distribution (NaN or +inf in it, nothing but -inf; a
+ * temperature that is negative, NaN or infinite) gets NaN and top_tokens -1,
+ * GRPO_ERR_VALUE by grpo_check_error; a token outside [0, V) logp NaN
+ * (GRPO_ERR_TOKEN_RANGE); a length outside [0, R] is clamped
+ * (GRPO_ERR_LENGTH_RANGE).
+ * Sums are float32 per thread, added in a fixed order: results are bitwise
+ * reproducible.  workspace: at least grpo_token_stats_workspace_size(N, R)
+ * bytes (a word per row).
+ */
+grpo_status grpo_token_stats_workspace_size(int64_t N, int64_t R, size_t *bytes);
+grpo_status grpo_token_stats(const void *logits, grpo_dtype dtype, int64_t N, int64_t R, int64_t V,
+                             int64_t logits_seq, int64_t logits_row, const int64_t *tokens,
+                             int64_t token_seq, const int32_t *len, const float *temperature,
+                             int64_t top, float *logp, float *entropy, float *norm,
+                             int64_t *top_tokens, float *top_logp, void *workspace,
+                             size_t workspace_bytes, grpo_stream_t stream);
+
+/*
+ * grpo_token_stats_bwd -- gradient of grpo_token_stats' logp and entropy with
+ * respect to the logits, from its norm and entropy and the upstream gradients
+ * g = grad_logp, h = grad_entropy [N, R] float32 (either may be NULL: 0):
+ *   dlogits_v = (g ([v = y] - p_v) - h p_v (ln p_v + entropy)) / T
+ * in `dtype`, one rounding.  Every row j < R of every sequence is written:
+ * zeros for rows j >= L_i and for rows whose g and h are both 0 (neither kind's
+ * logits are read).  A row without a distribution, or with g != 0 and a token
+ * outside [0, V), gets NaN.
+ * dlogits: row j of sequence i at i * dlogits_seq + j * dlogits_row (so rows of a
+ * larger buffer can be written where they lie; what is between them stays).
+ * It overlaps no input.  tokens are needed with grad_logp only, entropy with
+ * grad_entropy only.  Rows of logits and dlogits that share their address's remainder by
+ * 16 stream fastest.
+ */
+grpo_status grpo_token_stats_bwd(const void *logits, grpo_dtype dtype, int64_t N, int64_t R,
+                                 int64_t V, int64_t logits_seq, int64_t logits_row,
+                                 const int64_t *tokens, int64_t token_seq, const int32_t *len,
+                                 const float *temperature, const float *norm,
+                                 const float *entropy, const float *grad_logp,
+                                 const float *grad_entropy, void *dlogits, int64_t dlogits_seq,
+                                 int64_t dlogits_row, grpo_stream_t stream);
+
+/* One tensor of an AdamW step: `numel` dense elements in each array. */
+typedef struct {
+    void *param;          /* float32 or bfloat16 */
+    float *master;        /* float32 copy that bfloat16 params are updated in; or NULL */
+    const void *grad;     /* float32 or bfloat16; NULL: the tensor is left as it is */
+    void *exp_avg;        /* float32, or with 8-bit states e4m3 codes */
+    void *exp_avg_sq;     /* float32, or with 8-bit states e4m3 codes of its root */
+    float *scales;        /* 8-bit states: [ceil(numel / 256)][2]; else NULL */
+    int64_t numel;
+    grpo_dtype param_dtype;
+    grpo_dtype grad_dtype;
+} grpo_adamw_tensor;
+
+typedef struct {
+    int64_t step;            /* number of this step, from 1 */
+    const int64_t *step_dev; /* or where it lies in device memory; NULL: `step` */
+    double lr;
+    const float *lr_dev;     /* or where it lies in device memory; NULL: `lr` */
+    double beta1, beta2, eps, weight_decay;
+    const float *norm;       /* the gradients' global norm (grpo_grad_norm's stats), or NULL */
+    double max_norm, norm_eps;
+} grpo_adamw_hyper;
+
+/*
+ * grpo_adamw_step -- one AdamW step over `count` tensors, the step behind the
+ * backward and the gradients' norm.  Per element, in float32:
+ *   g  = c * grad,        c = min(1, max_norm / (norm + norm_eps)), or 1 without norm
+ *   m' = beta1 m + (1 - beta1) g
+ *   v' = beta2 v + (1 - beta2) g^2
+ *   w' = w - lr (m' / (1 - beta1^t) / (sqrt(v' / (1 - beta2^t)) + eps) + weight_decay w)
+ * with w the master where there is one, else the param; a bfloat16 param is
+ * w' rounded to nearest (without a master, changes below half a step of it are lost).  With
+ * `norm` the gradients are clipped as grpo_clip_grad_norm clips them, without
+ * being written; a norm that is not finite skips the step: nothing is written.
+ *
+ * state_bits 32: m and v are float32.  state_bits 8: every 256 consecutive
+ * elements of a tensor share two float32 scales, and m = code * scales[block][0],
+ * sqrt(v) = code * scales[block][1] with codes in e4m3, scale = the block's largest
+ * magnitude / 448, rounded to nearest after the step (the update itself uses the unrounded
+ * m' and v').  The root is what is stored because its range is half that of v
+ * in powers of two; a positive root never becomes 0 (the smallest code, 2^-9,
+ * instead), since it divides.  A block whose largest |m'| is below 2^-80 is
+ * stored as 0.  Everything up to the codes is rounded operation by operation as written.  Zeroed states and scales are those of the first step.
+ *
+ * tensors: HOST array (read before the call returns; the pointers in it are
+ * device pointers, aligned to their element, and what is written overlaps nothing
+ * else; params that overlap one another are refused).  Arrays that are all
+ * 16-byte aligned (e4m3 codes: 8) move in wide accesses.
+ * beta1, beta2 in [0, 1), lr, eps, weight_decay, norm_eps >= 0 and finite,
+ * max_norm >= 0 (infinity: no limit), step >= 1 (step_dev's value too).
+ * With step_dev and lr_dev a captured call can be replayed with other values.
+ */
+grpo_status grpo_adamw_step(const grpo_adamw_tensor *tensors, int64_t count, int state_bits,
+                            const grpo_adamw_hyper *hyper, grpo_stream_t stream);
+
+/*
  * grpo_check_error -- synchronises `stream`, then reports what the kernels of
  * the most recent call on `workspace` (grpo_loss_fwd and its relatives,
- * grpo_embed_bwd, grpo_clip_grad_norm, grpo_verify_drafts) recorded: GRPO_OK,
+ * grpo_embed_bwd, grpo_clip_grad_norm, grpo_verify_drafts, grpo_token_stats)
+ * recorded: GRPO_OK,
  * GRPO_ERR_TOKEN_RANGE (a scored id outside [0, V); its logp and lse are NaN),
  * GRPO_ERR_LENGTH_RANGE (a length outside [0, C]; it was clamped),
  * GRPO_ERR_TIMEOUT, or GRPO_ERR_VALUE.  GRPO_ERR_CUDA if the synchronisation itself failed.

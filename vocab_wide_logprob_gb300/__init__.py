@@ -14,13 +14,17 @@ _NAMES = ("grpo_mask", "grpo_advantage", "grpo_advantage_ex", "grpo_workspace_si
           "grpo_lmhead_logprobs", "grpo_lmhead_loss_fwd", "grpo_lmhead_loss_bwd",
           "grpo_embed_fwd", "grpo_embed_bwd", "grpo_embed_workspace_size", "grpo_clip_grad_norm",
           "grpo_grad_norm", "grpo_grad_norm_workspace_size", "grpo_verify_drafts",
-          "grpo_verify_workspace_size", "grpo_check_error", "grpo_selftest_timeout", "grpo_set_early_start", "grpo_copy", "GrpoError")
+          "grpo_verify_workspace_size", "grpo_token_stats", "grpo_token_stats_bwd",
+          "grpo_token_stats_workspace_size", "grpo_adamw_state", "grpo_adamw_step",
+          "grpo_check_error", "grpo_selftest_timeout", "grpo_set_early_start", "grpo_copy",
+          "GrpoError")
 
 
 def __getattr__(name):
     if name in _NAMES:
         from . import _native as module
-    elif name in ("GRPOLoss", "grpo_loss", "GRPOEmbedding", "grpo_embed"):
+    elif name in ("GRPOLoss", "grpo_loss", "GRPOEmbedding", "grpo_embed", "GRPOTokenStats",
+                  "grpo_logp_entropy"):
         from . import autograd as module
     else:
         raise AttributeError(name)

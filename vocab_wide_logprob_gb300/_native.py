@@ -93,6 +93,12 @@ def _load():
         "grpo_verify_workspace_size": ([I64, I64, ctypes.POINTER(SZ)], INT),
         "grpo_verify_drafts": ([P, P, INT, I64, I64, I64, I64, I64, I64, I64, P, P, P, P, I64, P,
                                 P, P, P, P, SZ, P], INT),
+        "grpo_token_stats_workspace_size": ([I64, I64, ctypes.POINTER(SZ)], INT),
+        "grpo_token_stats": ([P, INT, I64, I64, I64, I64, I64, P, I64, P, P, I64, P, P, P, P, P, P,
+                              SZ, P], INT),
+        "grpo_token_stats_bwd": ([P, INT, I64, I64, I64, I64, I64, P, I64, P, P, P, P, P, P, P, I64,
+                                  I64, P], INT),
+        "grpo_adamw_step": ([P, I64, INT, P, P], INT),
         "grpo_lmhead_loss_bwd": ([P, P, I64, I64, I64, I64, I64, P, P, P, P, P, P, P, P, SZ, P],
                                  INT),
     }
@@ -646,6 +652,77 @@ def grpo_verify_drafts(target_logits, draft_tokens, u, noise, draft_logits=None,
     reuse the buffers."""
     return _ops.verify(target_logits, draft_tokens, u, noise, draft_logits, draft_lens,
                        temperature, out, workspace, stream)
+
+
+def grpo_token_stats_workspace_size(N: int, R: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(_lib.grpo_token_stats_workspace_size(N, R, ctypes.byref(out)),
+           "grpo_token_stats_workspace_size")
+    return int(out.value)
+
+
+def grpo_token_stats(logits, tokens, lens=None, temperature=None, top=0, out=None, workspace=None,
+                     stream=None):
+    """Log-probs of ``tokens`` [N, R] int64 under ``logits`` [N, R, V] float32 or
+    bfloat16 (views of padded rows or sequences included, such as ``logits[:,
+    P-1:-1]`` with ``input_ids[:, P:]``), the entropy of every row and its ``top``
+    (at most 32) likeliest tokens.  ``lens`` [N] int32: rows of each sequence that
+    count (None: all); ``temperature`` [N] float32 (None: 1).  Returns a dict with
+    ``logp`` and ``entropy`` [N, R], ``norm`` [N, R, 2] (largest logit, log-sum) in
+    float32, with ``top`` also ``top_tokens`` [N, R, top] int64 and ``top_logp``,
+    and ``workspace``; pass it as ``out`` to reuse the buffers.  New outputs and
+    workspace share one allocation."""
+    return _ops.token_stats(logits, tokens, lens, temperature, top, out, workspace, stream)
+
+
+def grpo_token_stats_bwd(logits, tokens, norm, entropy, grad_logp=None, grad_entropy=None,
+                         lens=None, temperature=None, out=None, stream=None):
+    """Gradient with respect to the logits of :func:`grpo_token_stats`' log-probs
+    (upstream ``grad_logp`` [N, R]) and entropies (``grad_entropy``), from its
+    ``norm`` and ``entropy``.  Returns dlogits [N, R, V] in the logits' dtype, or
+    ``out`` (which may be a view of padded rows); rows behind a sequence's length are zeros."""
+    return _ops.token_stats_bwd(logits, tokens, norm, entropy, grad_logp, grad_entropy, lens,
+                                temperature, out, stream)
+
+
+def grpo_adamw_state(params, bits=32, master=False):
+    """Zeroed AdamW states of ``params`` for :func:`grpo_adamw_step`: a dict of
+    lists, one tensor per param.  bits 32: ``exp_avg`` and ``exp_avg_sq`` float32;
+    bits 8: ``exp_avg`` and ``exp_avg_root`` (of the second moment's root)
+    float8_e4m3fn and ``scales`` [blocks of 256 elements, 2] float32, value = code
+    * scale.  ``master``: also float32 copies of the bfloat16 params (None for
+    the others), which are then what is updated."""
+    if bits not in (8, 32):
+        raise ValueError("bits must be 8 or 32")
+    kind = torch.float32 if bits == 32 else torch.float8_e4m3fn
+
+    def zeros():
+        # (the codes' zero is the zero byte)
+        return [torch.zeros(p.shape, dtype=torch.uint8, device=p.device).view(kind) if bits == 8
+                else torch.zeros(p.shape, dtype=kind, device=p.device) for p in params]
+
+    state = {"exp_avg": zeros(), "exp_avg_sq" if bits == 32 else "exp_avg_root": zeros()}
+    if bits == 8:
+        state["scales"] = [torch.zeros((p.numel() + 255) // 256, 2, device=p.device)
+                           for p in params]
+    if master:
+        state["master"] = [p.detach().float().contiguous() if p.dtype == torch.bfloat16 else None
+                           for p in params]
+    return state
+
+
+def grpo_adamw_step(params, grads, state, step, lr, beta1=0.9, beta2=0.999, eps=1e-8,
+                    weight_decay=0.01, norm=None, max_norm=float("inf"), norm_eps=1e-6,
+                    stream=None):
+    """One AdamW step of ``params`` (dense float32 or bfloat16, any mixture) with
+    ``grads`` (of either type; None leaves a param as it is) and ``state`` (of
+    :func:`grpo_adamw_state`), all updated in place.  ``step``: the number of this
+    step from 1, an int or an int64 tensor on the device; ``lr`` a number or a
+    float32 tensor on the device (for captured calls).  With ``norm`` (the stats
+    of :func:`grpo_grad_norm`) the gradients are clipped to ``max_norm`` on the
+    way, and a norm that is not finite skips the step."""
+    _ops.adamw(params, grads, state, step, lr, beta1, beta2, eps, weight_decay, norm, max_norm,
+               norm_eps, stream)
 
 
 def grpo_set_early_start(enable: bool) -> None:

@@ -3,7 +3,9 @@ backward grpo_loss_bwd (d loss / d logits, "loss.backward()" of "Making Dr
 GRPO go brrr", salahadawi.com), both through the C ABI; torch only holds
 the tensors.  GRPOLMHeadLoss does the same from hidden states and the LM head
 (grpo_lmhead_loss_fwd / grpo_lmhead_loss_bwd).  GRPOEmbedding is the
-embedding lookup (grpo_embed_fwd / grpo_embed_bwd).
+embedding lookup (grpo_embed_fwd / grpo_embed_bwd), GRPOTokenStats the
+log-probs and entropies of a caller's own loss (grpo_token_stats /
+grpo_token_stats_bwd).
 
 Of the losses, only the logits (or the hidden states and the LM head) receive a gradient.  The advantages, old and reference
 log-probs are constants of the update step (the advantage comes from the
@@ -94,6 +96,37 @@ def grpo_embed(ids, weight, scale=1.0, pad_id=None, out_dtype=None):
     """Functional form of :class:`GRPOEmbedding` (differentiable in
     ``weight``)."""
     return GRPOEmbedding.apply(ids, weight, scale, pad_id, out_dtype)
+
+
+class GRPOTokenStats(torch.autograd.Function):
+    """logp, entropy = GRPOTokenStats.apply(logits, tokens, lens, temperature):
+    grpo_token_stats of logits [N, R, V], both [N, R] float32 and differentiable
+    in ``logits``; the backward is grpo_token_stats_bwd."""
+
+    @staticmethod
+    def forward(ctx, logits, tokens, lens=None, temperature=None):
+        out = g.grpo_token_stats(logits, tokens, lens, temperature)
+        ctx.save_for_backward(logits, tokens, out["norm"], out["entropy"], lens, temperature)
+        ctx.set_materialize_grads(False)
+        return out["logp"], out["entropy"]
+
+    @staticmethod
+    def backward(ctx, grad_logp, grad_entropy):
+        if grad_logp is None and grad_entropy is None:
+            return None, None, None, None
+        logits, tokens, norm, entropy, lens, temperature = ctx.saved_tensors
+        # (the gradient of a sum arrives expanded)
+        gl, gh = (None if t is None else t.detach().float().contiguous()
+                  for t in (grad_logp, grad_entropy))
+        dz = g.grpo_token_stats_bwd(logits, tokens, norm, entropy, gl, gh, lens, temperature)
+        of = [t for t in (logits, grad_logp, grad_entropy) if t is not None]
+        return _first_order(dz, *of), None, None, None
+
+
+def grpo_logp_entropy(logits, tokens, lens=None, temperature=None):
+    """Functional form of :class:`GRPOTokenStats` (differentiable in
+    ``logits``)."""
+    return GRPOTokenStats.apply(logits, tokens, lens, temperature)
 
 
 class GRPOLMHeadLoss(torch.autograd.Function):

@@ -4,6 +4,7 @@
 #include <math.h>
 #include <stdlib.h>
 
+#include <algorithm>
 #include <atomic>
 #include <map>
 #include <memory>
@@ -923,6 +924,25 @@ bool verify_fits(int64_t N, int64_t K) {
   return K <= (int64_t)1 << 20 && N <= ((int64_t)1 << 26) / (K + 1);
 }
 
+// Rows of logits of a token statistics call.
+bool rows_fit(int64_t N, int64_t R) {
+  return N == 0 || R == 0 || N <= ((int64_t)1 << 26) / R;
+}
+// Checks shared by those calls: rows of V elements at i * seq + j * row, apart.
+grpo_status check_rows(grpo_dtype dtype, int64_t N, int64_t R, int64_t V, int64_t seq,
+                       int64_t row) {
+  if (!known_dtype(dtype)) return GRPO_ERR_UNSUPPORTED;
+  if (N < 0 || R < 0 || V < 1) return GRPO_ERR_INVALID_ARG;
+  if (!rows_fit(N, R) || V > INT32_MAX - 65536) return GRPO_ERR_UNSUPPORTED;
+  if ((R > 1 && row < V) || row < 0 || seq < 0) return GRPO_ERR_INVALID_ARG;
+  if (mul3(R, row, 8) < 0 || mul3(N, seq, 8) < 0) return GRPO_ERR_UNSUPPORTED;
+  if (N > 1 && R > 0 && seq < (R - 1) * row + V) return GRPO_ERR_INVALID_ARG;
+  return GRPO_OK;
+}
+size_t rows_bytes(int64_t N, int64_t R, int64_t V, int64_t seq, int64_t row, grpo_dtype t) {
+  return ((size_t)(N - 1) * (size_t)seq + (size_t)(R - 1) * (size_t)row + (size_t)V) * esize_of(t);
+}
+
 constexpr int64_t kMaxEmbedDim = (int64_t)1 << 24;
 
 // Shape checks shared by the embedding calls.
@@ -1179,6 +1199,199 @@ grpo_status grpo_verify_drafts(const void* target_logits, const void* draft_logi
   a.logp = logp;
   a.ws = workspace;
   return from_cuda(launch_verify(a, dev, (cudaStream_t)stream));
+}
+
+grpo_status grpo_token_stats_workspace_size(int64_t N, int64_t R, size_t* bytes) {
+  if (bytes == nullptr || N < 0 || R < 0) return GRPO_ERR_INVALID_ARG;
+  if (!rows_fit(N, R)) return GRPO_ERR_UNSUPPORTED;
+  *bytes = token_stats_workspace_bytes(N, R);
+  return GRPO_OK;
+}
+
+grpo_status grpo_token_stats(const void* logits, grpo_dtype dtype, int64_t N, int64_t R, int64_t V,
+                             int64_t logits_seq, int64_t logits_row, const int64_t* tokens,
+                             int64_t token_seq, const int32_t* len, const float* temperature,
+                             int64_t top, float* logp, float* entropy, float* norm,
+                             int64_t* top_tokens, float* top_logp, void* workspace,
+                             size_t workspace_bytes, grpo_stream_t stream) {
+  const grpo_status s = check_rows(dtype, N, R, V, logits_seq, logits_row);
+  if (s != GRPO_OK) return s;
+  if (token_seq < 0 || top < 0 || top > V) return GRPO_ERR_INVALID_ARG;
+  if (top > kMaxTop || mul3(N, token_seq, 8) < 0) return GRPO_ERR_UNSUPPORTED;
+  if (workspace == nullptr) return GRPO_ERR_INVALID_ARG;
+  const int64_t rows = N * R;
+  if (rows > 0) {
+    if (logits == nullptr || tokens == nullptr || logp == nullptr || entropy == nullptr ||
+        norm == nullptr)
+      return GRPO_ERR_INVALID_ARG;
+    if (top > 0 && (top_tokens == nullptr || top_logp == nullptr)) return GRPO_ERR_INVALID_ARG;
+  }
+  if (!aligned(logits, esize_of(dtype)) || !aligned(tokens, 8) || !aligned(len, 4) ||
+      !aligned(temperature, 4) || !aligned(logp, 4) || !aligned(entropy, 4) || !aligned(norm, 4) ||
+      (top > 0 && (!aligned(top_tokens, 8) || !aligned(top_logp, 4))) || !aligned(workspace, 256))
+    return GRPO_ERR_MISALIGNED;
+  if (workspace_bytes < token_stats_workspace_bytes(N, R)) return GRPO_ERR_WORKSPACE;
+  DeviceInfo dev;
+  if (current_device(&dev) != cudaSuccess) return GRPO_ERR_CUDA;
+  stream_take_last(stream);
+  TokenStatsArgs a;
+  a.logits = logits;
+  a.dtype = dtype == GRPO_F32 ? 0 : 1;
+  a.N = N;
+  a.R = R;
+  a.V = V;
+  a.seq = logits_seq;
+  a.row = logits_row;
+  a.tokens = tokens;
+  a.token_seq = token_seq;
+  a.lens = len;
+  a.temperature = temperature;
+  a.top = (int)top;
+  a.logp = logp;
+  a.entropy = entropy;
+  a.norm = norm;
+  a.top_tokens = top_tokens;
+  a.top_logp = top_logp;
+  a.ws = workspace;
+  return from_cuda(launch_token_stats(a, dev, (cudaStream_t)stream));
+}
+
+grpo_status grpo_token_stats_bwd(const void* logits, grpo_dtype dtype, int64_t N, int64_t R,
+                                 int64_t V, int64_t logits_seq, int64_t logits_row,
+                                 const int64_t* tokens, int64_t token_seq, const int32_t* len,
+                                 const float* temperature, const float* norm,
+                                 const float* entropy, const float* grad_logp,
+                                 const float* grad_entropy, void* dlogits, int64_t dlogits_seq,
+                                 int64_t dlogits_row, grpo_stream_t stream) {
+  grpo_status s = check_rows(dtype, N, R, V, logits_seq, logits_row);
+  if (s == GRPO_OK) s = check_rows(dtype, N, R, V, dlogits_seq, dlogits_row);
+  if (s != GRPO_OK) return s;
+  if (token_seq < 0) return GRPO_ERR_INVALID_ARG;
+  if (mul3(N, token_seq, 8) < 0) return GRPO_ERR_UNSUPPORTED;
+  const int64_t rows = N * R;
+  if (rows == 0) return GRPO_OK;
+  if (logits == nullptr || norm == nullptr || dlogits == nullptr ||
+      (grad_logp != nullptr && tokens == nullptr) ||
+      (grad_entropy != nullptr && entropy == nullptr))
+    return GRPO_ERR_INVALID_ARG;
+  if (!aligned(logits, esize_of(dtype)) || !aligned(dlogits, esize_of(dtype)) ||
+      !aligned(tokens, 8) || !aligned(len, 4) || !aligned(temperature, 4) || !aligned(norm, 4) ||
+      !aligned(entropy, 4) || !aligned(grad_logp, 4) || !aligned(grad_entropy, 4))
+    return GRPO_ERR_MISALIGNED;
+  const size_t nd = rows_bytes(N, R, V, dlogits_seq, dlogits_row, dtype);
+  if (overlap(dlogits, nd, logits, rows_bytes(N, R, V, logits_seq, logits_row, dtype)) ||
+      overlap(dlogits, nd, norm, 8 * (size_t)rows) ||
+      (entropy != nullptr && overlap(dlogits, nd, entropy, 4 * (size_t)rows)) ||
+      (grad_logp != nullptr && overlap(dlogits, nd, grad_logp, 4 * (size_t)rows)) ||
+      (grad_entropy != nullptr && overlap(dlogits, nd, grad_entropy, 4 * (size_t)rows)) ||
+      (tokens != nullptr &&
+       overlap(dlogits, nd, tokens, 8 * (size_t)((N - 1) * token_seq + R))))
+    return GRPO_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  if (current_device(&dev) != cudaSuccess) return GRPO_ERR_CUDA;
+  stream_take_last(stream);
+  TokenStatsBwdArgs a;
+  a.logits = logits;
+  a.dtype = dtype == GRPO_F32 ? 0 : 1;
+  a.N = N;
+  a.R = R;
+  a.V = V;
+  a.seq = logits_seq;
+  a.row = logits_row;
+  a.tokens = tokens;
+  a.token_seq = token_seq;
+  a.lens = len;
+  a.temperature = temperature;
+  a.norm = norm;
+  a.entropy = entropy;
+  a.grad_logp = grad_logp;
+  a.grad_entropy = grad_entropy;
+  a.dlogits = dlogits;
+  a.dseq = dlogits_seq;
+  a.drow = dlogits_row;
+  return from_cuda(launch_token_stats_bwd(a, dev, (cudaStream_t)stream));
+}
+
+grpo_status grpo_adamw_step(const grpo_adamw_tensor* tensors, int64_t count, int state_bits,
+                            const grpo_adamw_hyper* hyper, grpo_stream_t stream) {
+  if (state_bits != 8 && state_bits != 32) return GRPO_ERR_UNSUPPORTED;
+  if (count < 0 || hyper == nullptr || (count > 0 && tensors == nullptr))
+    return GRPO_ERR_INVALID_ARG;
+  if (count > INT32_MAX) return GRPO_ERR_UNSUPPORTED;
+  const grpo_adamw_hyper& h = *hyper;
+  const auto size = [](double x) { return x >= 0.0 && x <= 3e38; };  // a float32 magnitude
+  if (!(h.beta1 >= 0.0 && h.beta1 < 1.0) || !(h.beta2 >= 0.0 && h.beta2 < 1.0) || !size(h.eps) ||
+      !size(h.weight_decay) || (h.lr_dev == nullptr && !size(h.lr)) ||
+      (h.step_dev == nullptr && h.step < 1))
+    return GRPO_ERR_INVALID_ARG;
+  if (h.norm != nullptr && (!(h.max_norm >= 0.0) || !size(h.norm_eps))) return GRPO_ERR_INVALID_ARG;
+  if (!aligned(h.step_dev, 8) || !aligned(h.lr_dev, 4) || !aligned(h.norm, 4))
+    return GRPO_ERR_MISALIGNED;
+  const bool eight = state_bits == 8;
+  const size_t state = eight ? 1 : 4;
+  // (room for the table and for the order of its params)
+  std::unique_ptr<AdamwTensor[]> table(new (std::nothrow) AdamwTensor[(size_t)count + 1]);
+  std::unique_ptr<Span[]> spans(new (std::nothrow) Span[(size_t)count + 1]);
+  if (!table || !spans) return GRPO_ERR_UNSUPPORTED;
+  int64_t n = 0, all = 0;
+  for (int64_t k = 0; k < count; ++k) {
+    const grpo_adamw_tensor& t = tensors[k];
+    if (!known_dtype(t.param_dtype) || !known_dtype(t.grad_dtype)) return GRPO_ERR_UNSUPPORTED;
+    if (t.numel < 0) return GRPO_ERR_INVALID_ARG;
+    if (t.numel == 0 || t.grad == nullptr) continue;  // left as it is
+    if (t.param == nullptr || t.exp_avg == nullptr || t.exp_avg_sq == nullptr ||
+        (eight != (t.scales != nullptr)) ||
+        (t.master != nullptr && t.param_dtype != GRPO_BF16))
+      return GRPO_ERR_INVALID_ARG;
+    if (t.numel > INT64_MAX / 16 - all) return GRPO_ERR_UNSUPPORTED;
+    all += t.numel;
+    if (!aligned(t.param, esize_of(t.param_dtype)) || !aligned(t.grad, esize_of(t.grad_dtype)) ||
+        !aligned(t.exp_avg, state) || !aligned(t.exp_avg_sq, state) || !aligned(t.scales, 4) ||
+        !aligned(t.master, 4))
+      return GRPO_ERR_MISALIGNED;
+    const size_t e = (size_t)t.numel;
+    const Span own[6] = {span(t.param, e * esize_of(t.param_dtype)), span(t.exp_avg, e * state),
+                         span(t.exp_avg_sq, e * state), span(t.master, 4 * e),
+                         span(t.scales, 8 * ((e + kStateBlock - 1) / kStateBlock)),
+                         span(t.grad, e * esize_of(t.grad_dtype))};
+    for (int x = 1; x < 6; ++x)
+      if (overlaps(own, x, own[x])) return GRPO_ERR_INVALID_ARG;
+    spans[(size_t)n] = own[0];
+    AdamwTensor& o = table[(size_t)n++];
+    o.param = t.param;
+    o.master = t.master;
+    o.grad = t.grad;
+    o.avg = t.exp_avg;
+    o.sq = t.exp_avg_sq;
+    o.scales = t.scales;
+    o.numel = t.numel;
+    o.dt = (t.param_dtype == GRPO_BF16 ? 1 : 0) | (t.grad_dtype == GRPO_BF16 ? 2 : 0);
+  }
+  if (n == 0) return GRPO_OK;
+  // a param listed twice (tied weights) would be updated twice, by blocks that run
+  // at the same time
+  std::sort(spans.get(), spans.get() + n, [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  for (int64_t k = 1; k < n; ++k)
+    if (spans[(size_t)k].lo < spans[(size_t)k - 1].hi) return GRPO_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  if (current_device(&dev) != cudaSuccess) return GRPO_ERR_CUDA;
+  stream_take_last(stream);
+  AdamwArgs a;
+  a.tensors = table.get();
+  a.count = n;
+  a.eight = eight;
+  a.step = h.step;
+  a.step_dev = h.step_dev;
+  a.lr = h.lr;
+  a.lr_dev = h.lr_dev;
+  a.beta1 = h.beta1;
+  a.beta2 = h.beta2;
+  a.eps = h.eps;
+  a.decay = h.weight_decay;
+  a.norm = h.norm;
+  a.max_norm = h.max_norm;
+  a.norm_eps = h.norm_eps;
+  return from_cuda(launch_adamw(a, dev, (cudaStream_t)stream));
 }
 
 grpo_status grpo_check_error(const void* workspace, grpo_stream_t stream) {

@@ -1,5 +1,6 @@
 // Tensor marshalling of the operators around the loss (embedding, gradient
-// clipping, draft verification): the module vocab_wide_logprob_gb300._ops.
+// clipping, draft verification, token statistics, AdamW): the module
+// vocab_wide_logprob_gb300._ops.
 //
 // It checks the tensors, allocates what the caller did not pass, and calls the
 // C ABI of include/grpo.h on the current CUDA stream -- what _native.py does
@@ -9,6 +10,7 @@
 // _native.py documents the functions and gives them their keywords.
 #include <Python.h>
 
+#include <optional>
 #include <vector>
 
 #include <ATen/core/Tensor.h>
@@ -528,6 +530,331 @@ PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   });
 }
 
+// Several outputs behind a workspace in one allocation (1.3 us each on the host).
+// add() in any order, then place() them.
+class Arena {
+ public:
+  Arena(size_t need, const c10::Device& dev) : dev_(dev), need_(need), at_(round(need)) {}
+  void add(Tensor* t, std::initializer_list<int64_t> shape, at::ScalarType dtype) {
+    int64_t n = 1;
+    for (const int64_t s : shape) n *= s;
+    parts_.push_back({t, {shape}, dtype, at_});
+    at_ += round((size_t)n * c10::elementSize(dtype));
+  }
+  // All of them; returns the workspace.
+  Tensor place() {
+    Tensor w = make({(int64_t)at_}, at::kByte, dev_);
+    for (const Piece& p : parts_) {
+      auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(w.storage()),
+                                                       c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                       c10::scalarTypeToTypeMeta(p.dtype));
+      impl->set_storage_offset((int64_t)(p.at / c10::elementSize(p.dtype)));
+      impl->set_sizes_contiguous(p.shape);
+      *p.to = Tensor(std::move(impl));
+    }
+    w.unsafeGetTensorImpl()->set_sizes_contiguous({(int64_t)need_});
+    return w;
+  }
+
+ private:
+  struct Piece {
+    Tensor* to;
+    c10::SmallVector<int64_t, 4> shape;
+    at::ScalarType dtype;
+    size_t at;
+  };
+  static size_t round(size_t n) { return (n + 255) / 256 * 256; }
+  c10::Device dev_;
+  size_t need_, at_;
+  c10::SmallVector<Piece, 6> parts_;
+};
+
+// Tokens [N, R] int64 whose rows may be part of wider ones: the pitch of the sequences.
+int64_t token_pitch(const Tensor& t, int64_t N, int64_t R, const c10::Device& dev) {
+  on_device(t, "tokens", dev);
+  if (t.scalar_type() != at::kLong) refuse(PyExc_TypeError, "%s has the wrong dtype", "tokens");
+  shaped(t, "tokens", {N, R});
+  if (R > 1 && t.stride(1) != 1) refuse(PyExc_ValueError, "%s must have dense rows", "tokens");
+  return t.stride(0);
+}
+// An [N, R, ...] or [N] input of one dtype, or none.
+const Tensor* maybe_input(PyObject* o, const char* name, at::ScalarType dtype,
+                          at::IntArrayRef shape, const c10::Device& dev) {
+  const Tensor* t = maybe_tensor(o, name);
+  if (t == nullptr) return nullptr;
+  contiguous(*t, name, dtype, dev);
+  shaped(*t, name, shape);
+  return t;
+}
+template <typename T>
+T* data_or_null(const Tensor* t) {
+  return t != nullptr ? (T*)t->data_ptr() : nullptr;
+}
+
+// token_stats(logits, tokens, lens, temperature, top, out, workspace, stream) -> out
+PyObject* token_stats(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  if (!count_is(n_args, 8)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Tensor& z = tensor(a[0], "logits");
+    const c10::Device dev = device_of(z, "logits");
+    if (z.dim() != 3) refuse(PyExc_ValueError, "%s must be [N, R, V]", "logits");
+    const int64_t N = z.size(0), R = z.size(1), V = z.size(2);
+    const grpo_dtype dt = code(z.scalar_type(), "logits");
+    int64_t seq, row;
+    logit_strides(z, "logits", N, R, V, &seq, &row);
+    const Tensor& x = tensor(a[1], "tokens");
+    const int64_t token_seq = token_pitch(x, N, R, dev);
+    const Tensor* lens = maybe_input(a[2], "lens", at::kInt, {N}, dev);
+    const Tensor* temp = maybe_input(a[3], "temperature", at::kFloat, {N}, dev);
+    const int64_t top = integer(a[4]);
+    if (top < 0) refuse(PyExc_ValueError, "%s must not be negative", "top");
+    size_t need = 0;
+    check_status(grpo_token_stats_workspace_size(N, R, &need), "grpo_token_stats_workspace_size");
+    const CallStream st(a[7], dev);
+    Tensor logp, entropy, norm, top_tokens, top_logp, ws;
+    PyObject* given_ws = a[6];
+    if (a[5] == Py_None) {
+      if (top > 32 || top > V) check_status(top > V ? GRPO_ERR_INVALID_ARG : GRPO_ERR_UNSUPPORTED,
+                                            "grpo_token_stats");
+      Arena arena(given_ws == Py_None ? need : 0, dev);
+      arena.add(&logp, {N, R}, at::kFloat);
+      arena.add(&entropy, {N, R}, at::kFloat);
+      arena.add(&norm, {N, R, 2}, at::kFloat);
+      if (top > 0) {
+        arena.add(&top_tokens, {N, R, top}, at::kLong);
+        arena.add(&top_logp, {N, R, top}, at::kFloat);
+      }
+      ws = arena.place();
+    } else {
+      if (!PyDict_Check(a[5])) refuse(PyExc_TypeError, "%s must be a dict", "out");
+      const auto given = [&](const char* key, at::ScalarType t, at::IntArrayRef shape) {
+        const Tensor& o = entry(a[5], key);
+        contiguous(o, key, t, dev);
+        shaped(o, key, shape);
+        return o;
+      };
+      logp = given("logp", at::kFloat, {N, R});
+      entropy = given("entropy", at::kFloat, {N, R});
+      norm = given("norm", at::kFloat, {N, R, 2});
+      if (top > 0) {
+        top_tokens = given("top_tokens", at::kLong, {N, R, top});
+        top_logp = given("top_logp", at::kFloat, {N, R, top});
+      }
+      if (given_ws == Py_None) {
+        PyObject* w = PyDict_GetItemString(a[5], "workspace");
+        if (w != nullptr) given_ws = w;
+      }
+    }
+    if (given_ws != Py_None || !ws.defined()) ws = workspace_of(given_ws, need, dev);
+    check_status(launch([&] {
+                   return grpo_token_stats(
+                       z.data_ptr(), dt, N, R, V, seq, row, (const int64_t*)x.data_ptr(),
+                       token_seq, data_or_null<const int32_t>(lens),
+                       data_or_null<const float>(temp), top, (float*)logp.data_ptr(),
+                       (float*)entropy.data_ptr(), (float*)norm.data_ptr(),
+                       top > 0 ? (int64_t*)top_tokens.data_ptr() : nullptr,
+                       top > 0 ? (float*)top_logp.data_ptr() : nullptr, ws.data_ptr(),
+                       bytes_of(ws), st);
+                 }),
+                 "grpo_token_stats");
+    if (a[5] != Py_None)
+      for (const Tensor* t : {&logp, &entropy, &norm, &top_tokens, &top_logp})
+        if (t->defined()) written(*t);
+    PyObject* out = a[5] == Py_None ? PyDict_New() : Py_NewRef(a[5]);
+    if (out == nullptr) return nullptr;
+    const auto put = [&](const char* key, PyObject* v) {  // takes v
+      const bool ok = v != nullptr && PyDict_SetItemString(out, key, v) == 0;
+      Py_XDECREF(v);
+      return ok;
+    };
+    bool ok = put("workspace", wrap(given_ws, ws));
+    if (a[5] == Py_None) {
+      ok = ok && put("logp", THPVariable_Wrap(logp)) && put("entropy", THPVariable_Wrap(entropy)) &&
+           put("norm", THPVariable_Wrap(norm));
+      if (top > 0)
+        ok = ok && put("top_tokens", THPVariable_Wrap(top_tokens)) &&
+             put("top_logp", THPVariable_Wrap(top_logp));
+    }
+    if (!ok) {
+      Py_DECREF(out);
+      return nullptr;
+    }
+    return out;
+  });
+}
+
+// token_stats_bwd(logits, tokens, norm, entropy, grad_logp, grad_entropy, lens, temperature,
+//                 out, stream) -> out
+PyObject* token_stats_bwd(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  if (!count_is(n_args, 10)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Tensor& z = tensor(a[0], "logits");
+    const c10::Device dev = device_of(z, "logits");
+    if (z.dim() != 3) refuse(PyExc_ValueError, "%s must be [N, R, V]", "logits");
+    const int64_t N = z.size(0), R = z.size(1), V = z.size(2);
+    const grpo_dtype dt = code(z.scalar_type(), "logits");
+    int64_t seq, row, dseq, drow, token_seq = 0;
+    logit_strides(z, "logits", N, R, V, &seq, &row);
+    const Tensor* x = maybe_tensor(a[1], "tokens");
+    if (x != nullptr) token_seq = token_pitch(*x, N, R, dev);
+    const Tensor* norm = maybe_input(a[2], "norm", at::kFloat, {N, R, 2}, dev);
+    if (norm == nullptr) refuse(PyExc_TypeError, "%s must be a tensor", "norm");
+    const Tensor* entropy = maybe_input(a[3], "entropy", at::kFloat, {N, R}, dev);
+    const Tensor* gl = maybe_input(a[4], "grad_logp", at::kFloat, {N, R}, dev);
+    const Tensor* gh = maybe_input(a[5], "grad_entropy", at::kFloat, {N, R}, dev);
+    if (gl != nullptr && x == nullptr) refuse(PyExc_ValueError, "%s are needed", "tokens");
+    if (gh != nullptr && entropy == nullptr) refuse(PyExc_ValueError, "%s is needed", "entropy");
+    const Tensor* lens = maybe_input(a[6], "lens", at::kInt, {N}, dev);
+    const Tensor* temp = maybe_input(a[7], "temperature", at::kFloat, {N}, dev);
+    const CallStream st(a[9], dev);
+    Tensor out;
+    if (a[8] == Py_None) {
+      out = make({N, R, V}, z.scalar_type(), dev);
+    } else {
+      out = tensor(a[8], "out");
+      on_device(out, "out", dev);
+      if (out.scalar_type() != z.scalar_type())
+        refuse(PyExc_TypeError, "%s must have logits' dtype", "out");
+    }
+    logit_strides(out, "out", N, R, V, &dseq, &drow);
+    check_status(launch([&] {
+                   return grpo_token_stats_bwd(
+                       z.data_ptr(), dt, N, R, V, seq, row, data_or_null<const int64_t>(x),
+                       token_seq, data_or_null<const int32_t>(lens),
+                       data_or_null<const float>(temp), data_or_null<const float>(norm),
+                       data_or_null<const float>(entropy), data_or_null<const float>(gl),
+                       data_or_null<const float>(gh), out.data_ptr(), dseq, drow, st);
+                 }),
+                 "grpo_token_stats_bwd");
+    if (a[8] != Py_None) written(out);
+    return wrap(a[8], out);
+  });
+}
+
+// A list of the state's dict, as long as the params; none where it may be absent.
+PyObject* state_list(PyObject* state, const char* key, bool needed) {
+  PyObject* o = PyDict_GetItemString(state, key);
+  if (o == nullptr || o == Py_None) {
+    if (needed) refuse(PyExc_ValueError, "state has no %s", key);
+    return nullptr;
+  }
+  return o;
+}
+
+// adamw(params, grads, state, step, lr, beta1, beta2, eps, weight_decay, norm, max_norm, norm_eps,
+//       stream)
+PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  if (!count_is(n_args, 13)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Items params(a[0], "params must be a list of tensors");
+    const Items grads(a[1], "grads must be a list of tensors");
+    if (!PyDict_Check(a[2])) refuse(PyExc_TypeError, "%s must be a dict", "state");
+    const Py_ssize_t n = params.size();
+    const bool eight = state_list(a[2], "scales", false) != nullptr;
+    const Items avg(state_list(a[2], "exp_avg", true), "exp_avg must be a list of tensors");
+    const char* second = eight ? "exp_avg_root" : "exp_avg_sq";
+    const Items sq(state_list(a[2], second, true), "exp_avg_sq must be a list of tensors");
+    PyObject* empty = PyTuple_New(0);
+    if (empty == nullptr) throw Refused();
+    const Items none(empty, "");
+    Py_DECREF(empty);
+    PyObject* masters = state_list(a[2], "master", false);
+    const Items master(masters != nullptr ? masters : none.seq, "master must be a list of tensors");
+    const Items scales(eight ? state_list(a[2], "scales", true) : none.seq,
+                       "scales must be a list of tensors");
+    const auto as_long = [&](const Items& l, const char* name) {
+      if (l.size() != n) refuse(PyExc_ValueError, "%s must have one tensor per param", name);
+    };
+    as_long(grads, "grads");
+    as_long(avg, "exp_avg");
+    as_long(sq, second);
+    if (masters != nullptr) as_long(master, "master");
+    if (eight) as_long(scales, "scales");
+    const c10::Device dev = n > 0 ? device_of(tensor(params.at(0), "every param"), "every param")
+                                  : c10::Device(c10::kCUDA, 0);
+    const auto dense = [&](const Tensor& t, const char* name) {
+      on_device(t, name, dev);
+      if (!t.is_contiguous()) refuse(PyExc_ValueError, "%s must be contiguous", name);
+    };
+    // float32 (or e4m3) values, one for every element of the param
+    const auto like = [&](PyObject* o, const char* name, at::ScalarType dtype, int64_t numel) {
+      const Tensor& t = tensor(o, name);
+      dense(t, name);
+      if (t.scalar_type() != dtype) refuse(PyExc_TypeError, "%s has the wrong dtype", name);
+      if (t.numel() != numel) refuse(PyExc_ValueError, "%s must have its param's size", name);
+      return t.data_ptr();
+    };
+    const at::ScalarType kept = eight ? at::kFloat8_e4m3fn : at::kFloat;
+    std::vector<grpo_adamw_tensor> table((size_t)n);
+    std::vector<Tensor> changed;  // (held: the call lets other threads run)
+    changed.reserve((size_t)n * 5);
+    for (Py_ssize_t k = 0; k < n; ++k) {
+      const Tensor& t = tensor(params.at(k), "every param");
+      dense(t, "every param");
+      grpo_adamw_tensor& e = table[(size_t)k];
+      e = {};
+      e.param = t.data_ptr();
+      e.numel = t.numel();
+      e.param_dtype = code(t.scalar_type(), "every param");
+      e.exp_avg = like(avg.at(k), "every exp_avg", kept, e.numel);
+      e.exp_avg_sq = like(sq.at(k), "every exp_avg_sq", kept, e.numel);
+      if (eight)
+        e.scales = (float*)like(scales.at(k), "every scales", at::kFloat,
+                                2 * ((e.numel + 255) / 256));
+      if (masters != nullptr && master.at(k) != Py_None)
+        e.master = (float*)like(master.at(k), "every master", at::kFloat, e.numel);
+      if (e.master != nullptr && e.param_dtype != GRPO_BF16)
+        refuse(PyExc_TypeError, "%s belongs to a bfloat16 param", "a master");
+      if (grads.at(k) == Py_None) continue;
+      const Tensor& g = tensor(grads.at(k), "every gradient");
+      dense(g, "every gradient");
+      if (g.numel() != e.numel)
+        refuse(PyExc_ValueError, "%s must have its param's size", "every gradient");
+      e.grad = g.data_ptr();
+      e.grad_dtype = code(g.scalar_type(), "every gradient");
+      changed.push_back(t);
+      changed.push_back(THPVariable_Unpack(avg.at(k)));
+      changed.push_back(THPVariable_Unpack(sq.at(k)));
+      if (eight) changed.push_back(THPVariable_Unpack(scales.at(k)));
+      if (e.master != nullptr) changed.push_back(THPVariable_Unpack(master.at(k)));
+    }
+    grpo_adamw_hyper h = {};
+    // a number of the host, or a tensor of one value on the device
+    const auto on_gpu = [&](PyObject* o, const char* name, at::ScalarType dtype, int64_t least) {
+      const Tensor& t = THPVariable_Unpack(o);
+      contiguous(t, name, dtype, dev);
+      if (t.numel() < least) refuse(PyExc_ValueError, "%s must hold its value", name);
+      return t.data_ptr();
+    };
+    if (THPVariable_Check(a[3]))
+      h.step_dev = (const int64_t*)on_gpu(a[3], "step", at::kLong, 1);
+    else
+      h.step = integer(a[3]);
+    if (THPVariable_Check(a[4]))
+      h.lr_dev = (const float*)on_gpu(a[4], "lr", at::kFloat, 1);
+    else
+      h.lr = number(a[4]);
+    h.beta1 = number(a[5]);
+    h.beta2 = number(a[6]);
+    h.eps = number(a[7]);
+    h.weight_decay = number(a[8]);
+    if (a[9] != Py_None) {
+      tensor(a[9], "norm");
+      h.norm = (const float*)on_gpu(a[9], "norm", at::kFloat, 1);
+    }
+    h.max_norm = number(a[10]);
+    h.norm_eps = number(a[11]);
+    std::optional<CallStream> st;
+    if (n > 0) st.emplace(a[12], dev);  // (without params nothing is launched)
+    const grpo_stream_t stream = st ? (grpo_stream_t)*st : nullptr;
+    check_status(
+        launch([&] { return grpo_adamw_step(table.data(), n, eight ? 8 : 32, &h, stream); }),
+        "grpo_adamw_step");
+    for (const Tensor& t : changed) written(t);
+    Py_RETURN_NONE;
+  });
+}
+
 // set_error(GrpoError): the exception of a status other than GRPO_OK
 PyObject* set_error(PyObject*, PyObject* type) {
   Py_XSETREF(g_error, Py_NewRef(type));
@@ -539,6 +866,9 @@ PyMethodDef methods[] = {{"embed_fwd", FAST(embed_fwd), nullptr},
                          {"embed_bwd", FAST(embed_bwd), nullptr},
                          {"clip", FAST(clip), nullptr},
                          {"verify", FAST(verify), nullptr},
+                         {"token_stats", FAST(token_stats), nullptr},
+                         {"token_stats_bwd", FAST(token_stats_bwd), nullptr},
+                         {"adamw", FAST(adamw), nullptr},
                          {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, methods,

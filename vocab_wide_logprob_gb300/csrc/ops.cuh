@@ -1,6 +1,6 @@
 // Launchers of the operators around the loss (embedding, gradient clipping,
-// draft verification); defined in embed.cu, gradnorm.cu and verify.cu, called
-// by api.cu.  Internal header.
+// draft verification, token statistics, AdamW); defined in embed.cu, gradnorm.cu,
+// verify.cu, token_stats.cu and adamw.cu, called by api.cu.  Internal header.
 #pragma once
 
 #include "common.cuh"
@@ -162,5 +162,74 @@ struct VerifyArgs {
 };
 size_t verify_workspace_bytes(int64_t N, int64_t K);
 cudaError_t launch_verify(const VerifyArgs& a, const DeviceInfo& d, cudaStream_t st);
+
+// ---- token statistics of logits and their gradient (token_stats.cu) -------------
+
+constexpr int kMaxTop = 32;  // alternatives per row
+
+struct TokenStatsArgs {
+  const void* logits;
+  int dtype;                           // 0 f32, 1 bf16
+  int64_t N, R, V, seq, row;           // rows at i * seq + j * row
+  const int64_t* tokens;               // at i * token_seq + j
+  int64_t token_seq;
+  const int32_t* lens;                 // [N] or null (R each)
+  const float* temperature;            // [N] or null (1)
+  int top;
+  float* logp;                         // [N, R]
+  float* entropy;                      // [N, R]
+  float* norm;                         // [N, R, 2]: largest logit, log of the sum
+  int64_t* top_tokens;                 // [N, R, top]
+  float* top_logp;
+  void* ws;
+};
+size_t token_stats_workspace_bytes(int64_t N, int64_t R);
+cudaError_t launch_token_stats(const TokenStatsArgs& a, const DeviceInfo& d, cudaStream_t st);
+
+struct TokenStatsBwdArgs {
+  const void* logits;
+  int dtype;
+  int64_t N, R, V, seq, row;
+  const int64_t* tokens;  // null without grad_logp
+  int64_t token_seq;
+  const int32_t* lens;
+  const float* temperature;
+  const float* norm;
+  const float* entropy;       // null without grad_entropy
+  const float* grad_logp;     // or null
+  const float* grad_entropy;  // or null
+  void* dlogits;
+  int64_t dseq, drow;
+};
+cudaError_t launch_token_stats_bwd(const TokenStatsBwdArgs& a, const DeviceInfo& d,
+                                   cudaStream_t st);
+
+// ---- AdamW over many tensors (adamw.cu) -------------------------------------------
+
+constexpr int kStateBlock = 256;  // elements that share the scales of 8-bit states
+
+struct AdamwTensor {
+  void* param;
+  float* master;
+  const void* grad;
+  void* avg;
+  void* sq;
+  float* scales;
+  int64_t numel;
+  int dt;  // bit 0: param is bf16, bit 1: grad is bf16
+};
+struct AdamwArgs {
+  const AdamwTensor* tensors;  // host
+  int64_t count;
+  bool eight;  // states in 8 bits
+  int64_t step;
+  const int64_t* step_dev;
+  double lr;
+  const float* lr_dev;
+  double beta1, beta2, eps, decay;
+  const float* norm;  // [norm, ...] or null
+  double max_norm, norm_eps;
+};
+cudaError_t launch_adamw(const AdamwArgs& a, const DeviceInfo& d, cudaStream_t st);
 
 }  // namespace grpo

@@ -1,0 +1,650 @@
+// Log-probs of given tokens, entropy and likeliest alternatives of rows of
+// logits, and the gradient of the first two.
+//
+// Forward, with c = log2(e) / T and every thread's running reference r:
+//   t_v = (z_v - r) c,  w_v = 2^t_v,  S = sum w_v,  E = sum w_v t_v
+// in one pass.  At the end everything is moved to the row's maximum m (S' = S
+// 2^d, E' = 2^d (E + d S) with d = (r - m) c) and added in a fixed order:
+//   L = ln S,  logp = (z_y - m) / T - L,  entropy = L - ln2 E / S.
+// Differences are taken before they are scaled, so no rounding is of the size of
+// the logits (rows of lowest values, temperatures near 0); t is held above
+// -150, where w is 0, so that -inf adds 0 to E.
+//
+// Alternatives: each thread also keeps the maximum of every group of vectors it
+// reads.  The top-th largest of the maxima of 64 sets of threads is a lower
+// bound of the top-th largest logit, which about 1.1 (top 5) to 1.4 (top 32)
+// times top logits reach in rows without an order: only the groups whose maximum
+// reaches it are read again.
+//
+// Backward: dz_v = p_v (A + B lg p_v) (+ g / T at the token) with lg p = (z - m) c
+// - L log2(e), A = -(g + h H) / T, B = -h ln2 / T.
+#include <math.h>
+
+#include "ops.cuh"
+
+namespace grpo {
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kMinTemperature = 1e-6f;  // below it a temperature counts as 0: greedy
+constexpr float kLowest = -150.f;         // 2^kLowest is 0 in ex2's range
+constexpr float kSlack = 8.f;             // sums may grow to 2^8 of their reference
+
+// max that keeps NaN
+__device__ __forceinline__ float max_keep_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// The temperature of sequence i: 1 for greedy ones, NaN for one that is none.
+__device__ __forceinline__ float warmth_of(const float* temperature, int64_t i) {
+  const float T = temperature != nullptr ? __ldg(temperature + i) : 1.f;
+  if (!(T >= 0.f) || isinf(T)) return NAN;
+  return T < kMinTemperature ? 1.f : T;
+}
+
+// Values in the order of unsigned integers (-0 and +0 are one value), above the
+// id's complement: larger keys come first among the alternatives.
+__device__ __forceinline__ uint64_t key_of(float x, int64_t v) {
+  const uint32_t u = __float_as_uint(x + 0.f);
+  const uint32_t o = (u & 0x80000000u) ? ~u : u | 0x80000000u;
+  return (uint64_t)o << 32 | (uint32_t)~(uint32_t)v;
+}
+__device__ __forceinline__ float key_value(uint64_t k) {
+  const uint32_t o = (uint32_t)(k >> 32);
+  return __uint_as_float((o & 0x80000000u) ? o & 0x7fffffffu : ~o);
+}
+__device__ __forceinline__ int64_t key_id(uint64_t k) { return (int64_t)(uint32_t)~(uint32_t)k; }
+
+// ---------------------------------------------------------------------------
+// forward
+// ---------------------------------------------------------------------------
+
+template <typename T>
+struct StatsParams {
+  const T* logits;
+  int64_t N, R, V, seq, row;
+  const int64_t* tokens;
+  int64_t token_seq;
+  const int32_t* lens;
+  const float* temperature;
+  int top;
+  float* logp;
+  float* entropy;
+  float* norm;
+  int64_t* top_tokens;
+  float* top_logp;
+  WsHeader* hdr;
+};
+
+constexpr int kSlots = 32;      // groups of a thread whose maxima are kept, the last for a ragged end
+constexpr int kCandidates = 512;
+constexpr int kHits = 256;
+
+// Running sums of one thread, two lanes of each packed.
+struct Sums {
+  float ref = 0.f, lim = -INFINITY;  // lim: a larger value moves the reference
+  float top = -INFINITY;
+  uint64_t s = 0, e = 0;
+
+  __device__ __forceinline__ void make_room(float largest, float c) {
+    if (!(largest > lim)) return;
+    if (lim != -INFINITY) {
+      const float d = fmaxf((ref - largest) * c, kLowest), f = ex2(d);
+      const uint64_t f2 = f2_pack(f, f);
+      e = f2_mul(f2, f2_fma(f2_pack(d, d), s, e));
+      s = f2_mul(f2, s);
+    }
+    ref = largest;
+    lim = largest + __fdividef(kSlack, c);
+  }
+  __device__ __forceinline__ void add(uint64_t x, uint64_t nref, uint64_t c) {
+    float a, b;
+    f2_unpack(f2_mul(f2_add(x, nref), c), a, b);
+    a = max_keep_nan(a, kLowest);
+    b = max_keep_nan(b, kLowest);
+    const uint64_t w = f2_pack(ex2(a), ex2(b));
+    s = f2_add(s, w);
+    e = f2_fma(w, f2_pack(a, b), e);
+  }
+};
+
+template <typename T>
+struct StatsShared {
+  float warp_max[kWarps];
+  float2 warp_sum[kWarps];
+  float4 total;  // m, S, E
+};
+struct TopShared {
+  float slot[kSlots][kThreads];
+  float quad[64];
+  uint64_t key[kCandidates];
+  int hit[kHits];
+  float bound;
+  int hits, keys, ties;
+};
+
+// Whether a vector's elements are worth a look, and those that are: above the
+// bound, or (ties) equal to it.
+__device__ __forceinline__ void push_key(TopShared& sh, float x, int64_t v) {
+  const int at = atomicAdd(&sh.keys, 1);
+  if (at < kCandidates) sh.key[at] = key_of(x, v);
+}
+
+template <typename T>
+struct Part {  // elements [v0, v1) of a row; vectors of 16 bytes in [a, b)
+  const T* z;
+  int64_t v0, v1, a, b;
+  int nvec;
+  int groups, per;  // groups of `per` batches of U vectors
+};
+
+// The best `top` of the part's elements, as keys in sh.key[0 .. top) sorted, with
+// the elements' count in the return value.  Called by the whole CTA after the
+// stream; `own_max` is the thread's largest element.
+template <typename T>
+__device__ int best_of_part(TopShared& sh, const Part<T>& p, float own_max, int top) {
+  using E = Elt<T>;
+  constexpr int EPV = E::kPerVec, U = E::kUnroll;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t n = p.v1 - p.v0;
+  __shared__ uint64_t s_sorted[kMaxTop];
+  if (tid == 0) sh.hits = sh.keys = sh.ties = 0;
+  bool listed = false;
+  if (n <= kCandidates) {
+    __syncthreads();
+    for (int64_t v = tid; v < n; v += kThreads) sh.key[v] = key_of(E::load1(p.z + p.v0 + v), p.v0 + v);
+    if (tid == 0) sh.keys = (int)n;
+    __syncthreads();
+    listed = true;
+  } else {
+    float q = fmaxf(own_max, __shfl_xor_sync(0xffffffffu, own_max, 1));
+    q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 2));
+    if (lane % 4 == 0) sh.quad[tid / 4] = q;
+    __syncthreads();
+    if (warp == 0) {
+      // the top-th largest of the 64, lower indices first
+      const float mine[2] = {sh.quad[lane], sh.quad[lane + 32]};
+      int before[2] = {0, 0};
+#pragma unroll 8
+      for (int k = 0; k < 64; ++k) {
+        const float x = sh.quad[k];
+        before[0] += x > mine[0] || (x == mine[0] && k < lane);
+        before[1] += x > mine[1] || (x == mine[1] && k < lane + 32);
+      }
+      if (before[0] == top - 1) sh.bound = mine[0];
+      if (before[1] == top - 1) sh.bound = mine[1];
+    }
+    __syncthreads();
+    const float bound = sh.bound;
+    // with the ties at the bound, or (where they are too many) without them
+    for (int strict = 0; strict < 2 && !listed; ++strict) {
+      for (int g = 0; g <= p.groups; ++g) {
+        const float x = sh.slot[g][tid];
+        if (strict ? x > bound : x >= bound) {
+          const int at = atomicAdd(&sh.hits, 1);
+          if (at < kHits) sh.hit[at] = g * kThreads + tid;
+        }
+      }
+      __syncthreads();
+      const int hits = sh.hits;
+      if (hits <= kHits) {
+        const int each = p.per * U;
+        for (int w = tid; w < hits * each; w += kThreads) {
+          const int h = sh.hit[w / each], t = h % kThreads, g = h / kThreads;
+          if (g == p.groups) {  // a ragged end's element
+            if (w % each == 0) {
+              const int64_t v = t < 32 ? p.v0 + t : p.b + t - 32;
+              push_key(sh, E::load1(p.z + v), v);
+            }
+            continue;
+          }
+          const int k = (g * each + w % each) * kThreads + t;
+          if (k >= p.nvec) continue;
+          float x[EPV];
+          E::unpack(ld_stream(p.z + p.a + (int64_t)k * EPV), x);
+#pragma unroll
+          for (int e = 0; e < EPV; ++e)
+            if (strict ? x[e] > bound : x[e] >= bound) push_key(sh, x[e], p.a + (int64_t)k * EPV + e);
+        }
+      }
+      __syncthreads();
+      listed = hits <= kHits && sh.keys <= kCandidates - (strict ? kMaxTop : 0);
+      const int have = sh.keys;
+      __syncthreads();
+      if (!listed) {
+        if (tid == 0) sh.hits = sh.keys = 0;
+        __syncthreads();
+      } else if (strict && have < top) {
+        // the first ties in the order of their ids
+        for (int64_t at = p.v0; at < p.v1; at += kThreads) {
+          const int64_t v = at + tid;
+          const bool tie = v < p.v1 && E::load1(p.z + v) == bound;
+          const uint32_t votes = __ballot_sync(0xffffffffu, tie);
+          if (lane == 0) sh.hit[warp] = __popc(votes);
+          __syncthreads();
+          int before = sh.ties, all = sh.ties;
+          for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) before += sh.hit[w];
+            all += sh.hit[w];
+          }
+          before += __popc(votes & ((1u << lane) - 1));
+          if (tie && have + before < top) sh.key[have + before] = key_of(bound, v);
+          __syncthreads();
+          if (tid == 0) sh.ties = all;
+          if (have + all >= top) break;
+        }
+        if (tid == 0) sh.keys = top;
+        __syncthreads();
+      }
+    }
+  }
+  if (!listed) {
+    // rows whose largest elements crowd in few threads' groups: every warp keeps
+    // the best 32 of its share, one per lane, best first
+    uint64_t mine = 0, last = 0;
+    for (int64_t at = p.v0 + warp * 32; at < p.v1; at += kThreads) {
+      const int64_t v = at + lane;
+      const uint64_t k = v < p.v1 ? key_of(E::load1(p.z + v), v) : 0;
+      uint32_t better = __ballot_sync(0xffffffffu, k > last);
+      while (better != 0) {
+        const int from = __ffs(better) - 1;
+        better &= better - 1;
+        const uint64_t x = __shfl_sync(0xffffffffu, k, from);
+        const uint64_t up = __shfl_up_sync(0xffffffffu, mine, 1);
+        if (x > mine) mine = lane > 0 && x > up ? up : x;
+        last = __shfl_sync(0xffffffffu, mine, top - 1);
+      }
+    }
+    sh.key[tid] = mine;
+    if (tid == 0) sh.keys = kThreads;
+    __syncthreads();
+  }
+  // sorted by counting the keys before each (they are all different, but for
+  // the zeros of empty lanes)
+  const int have = sh.keys;
+  uint64_t mine[kCandidates / kThreads];
+  int rank[kCandidates / kThreads];
+#pragma unroll
+  for (int u = 0; u < kCandidates / kThreads; ++u) {
+    const int k = tid + u * kThreads;
+    mine[u] = k < have ? sh.key[k] : 0;
+    rank[u] = kMaxTop;
+    if (mine[u] != 0) {
+      rank[u] = 0;
+      for (int j = 0; j < have; ++j) rank[u] += sh.key[j] > mine[u];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kCandidates / kThreads; ++u)
+    if (rank[u] < top) s_sorted[rank[u]] = mine[u];
+  __syncthreads();
+  const int got = (int)min(n, (int64_t)top);
+  if (tid < got) sh.key[tid] = s_sorted[tid];
+  __syncthreads();
+  return got;
+}
+
+template <typename T, bool kTop>
+__global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsParams<T> p) {
+  using E = Elt<T>;
+  constexpr int EPV = E::kPerVec, U = E::kUnroll;
+  extern __shared__ char s_dyn[];
+  TopShared& top = *reinterpret_cast<TopShared*>(s_dyn);
+  __shared__ StatsShared<T> sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_trigger();
+  const int64_t rows = p.N * p.R, r = blockIdx.x;
+  if (r == 0 && tid == 0) {
+    p.hdr->flags = kFlagIndirect;
+    p.hdr->status_count = (uint32_t)rows;
+    p.hdr->status_check = ~(uint32_t)rows;
+  }
+  if (r >= rows) return;
+  const int64_t i = r / p.R, j = r - i * p.R;
+  uint32_t* status = reinterpret_cast<uint32_t*>(p.hdr) + 64 + r;
+  uint32_t flags = 0;
+  if (p.lens != nullptr) {
+    const int64_t len = __ldg(p.lens + i);
+    if ((len < 0 || len > p.R) && j == 0) flags = kFlagLengthRange;
+    if (j >= len) {  // behind the sequence's end
+      if (tid == 0) {
+        p.logp[r] = p.entropy[r] = p.norm[2 * r] = p.norm[2 * r + 1] = 0.f;
+        *status = flags;
+      }
+      if (kTop && tid < p.top) {
+        p.top_tokens[r * p.top + tid] = -1;
+        p.top_logp[r * p.top + tid] = 0.f;
+      }
+      return;
+    }
+  }
+  const float Ti = warmth_of(p.temperature, i);
+  const float c = kLog2e / Ti;
+  Part<T> part;
+  part.z = p.logits + i * p.seq + j * p.row;
+  part.v0 = 0;
+  part.v1 = p.V;
+  const unsigned phase = (unsigned)(reinterpret_cast<uintptr_t>(part.z + part.v0) & 15u);
+  part.a = min(part.v0 + (int64_t)(((16u - phase) & 15u) / sizeof(T)), part.v1);
+  part.nvec = (int)((part.v1 - part.a) / EPV);
+  part.b = part.a + (int64_t)part.nvec * EPV;
+  const int batches = (part.nvec + kThreads * U - 1) / (kThreads * U);
+  part.per = (batches + kSlots - 2) / (kSlots - 1);
+  part.groups = part.per > 0 ? (batches + part.per - 1) / part.per : 0;
+
+  Sums sum;
+  const uint64_t c2 = f2_pack(c, c);
+  const uint4* vec = reinterpret_cast<const uint4*>(part.z + part.a);
+  int k0 = tid;
+  for (int g = 0; g < part.groups; ++g) {
+    float group_max = -INFINITY;
+    for (int q = 0; q < part.per; ++q, k0 += kThreads * U) {
+      uint4 d[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = k0 + u * kThreads;
+        d[u] = k < part.nvec ? ld_stream(vec + k)
+                             : make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf);
+      }
+      const float largest = E::template batch_max<U>(d);
+      group_max = fmaxf(group_max, largest);
+      sum.make_room(largest, c);
+      const uint64_t nref = f2_pack(-sum.ref, -sum.ref);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float x[EPV];
+        E::unpack(d[u], x);
+#pragma unroll
+        for (int e = 0; e < EPV; e += 2) sum.add(f2_pack(x[e], x[e + 1]), nref, c2);
+      }
+    }
+    sum.top = fmaxf(sum.top, group_max);
+    if (kTop) top.slot[g][tid] = group_max;
+  }
+  {  // a ragged end's element
+    int64_t v = -1;
+    if (tid < part.a - part.v0)
+      v = part.v0 + tid;
+    else if (tid >= 32 && tid - 32 < part.v1 - part.b)
+      v = part.b + tid - 32;
+    float x = -INFINITY;
+    if (v >= 0) {
+      x = E::load1(part.z + v);
+      sum.make_room(x, c);
+      sum.top = fmaxf(sum.top, x);
+      sum.add(f2_pack(x, -INFINITY), f2_pack(-sum.ref, -sum.ref), c2);
+    }
+    if (kTop) top.slot[part.groups][tid] = v >= 0 ? x : NAN;
+  }
+  // the row's maximum, then its sums relative to it
+  float m = sum.top;
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) sh.warp_max[warp] = m;
+  __syncthreads();
+  m = sh.warp_max[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) m = fmaxf(m, sh.warp_max[w]);
+  float s, e, s1, e1;
+  f2_unpack(sum.s, s, s1);
+  f2_unpack(sum.e, e, e1);
+  s += s1;
+  e += e1;
+  if (sum.lim != -INFINITY) {
+    const float d = fmaxf((sum.ref - m) * c, kLowest), f = ex2(d);
+    e = f * fmaf(d, s, e);
+    s *= f;
+  }
+  for (int o = 16; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    e += __shfl_xor_sync(0xffffffffu, e, o);
+  }
+  if (lane == 0) sh.warp_sum[warp] = make_float2(s, e);
+  __syncthreads();
+  s = e = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    s += sh.warp_sum[w].x;
+    e += sh.warp_sum[w].y;
+  }
+  // (a comparison with NaN is false)
+  const bool defined = s > 0.f && s < INFINITY && fabsf(m) < INFINITY && c > 0.f;
+  const float L = logf(s);
+  if (tid == 0) {
+    float lp = NAN, H = NAN;
+    if (defined) {
+      H = L - kLn2 * (e / s);
+      const int64_t y = __ldg(p.tokens + i * p.token_seq + j);
+      if (y >= 0 && y < p.V)
+        lp = (E::load1(part.z + y) - m) / Ti - L;
+      else
+        flags |= kFlagTokenRange;
+    } else {
+      flags |= kFlagValue;
+    }
+    p.logp[r] = lp;
+    p.entropy[r] = H;
+    p.norm[2 * r] = defined ? m : NAN;
+    p.norm[2 * r + 1] = defined ? L : NAN;
+    *status = flags;
+  }
+  if (!kTop) return;
+  if (!defined) {
+    if (tid < p.top) {
+      p.top_tokens[r * p.top + tid] = -1;
+      p.top_logp[r * p.top + tid] = NAN;
+    }
+    return;
+  }
+  best_of_part(top, part, sum.top, p.top);
+  if (tid < p.top) {
+    const uint64_t k = top.key[tid];
+    p.top_tokens[r * p.top + tid] = key_id(k);
+    p.top_logp[r * p.top + tid] = (key_value(k) - m) / Ti - L;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// backward
+// ---------------------------------------------------------------------------
+
+template <typename T>
+struct StatsBwdParams {
+  const T* logits;
+  int64_t N, R, V, seq, row;
+  const int64_t* tokens;
+  int64_t token_seq;
+  const int32_t* lens;
+  const float* temperature;
+  const float* norm;
+  const float* entropy;
+  const float* grad_logp;
+  const float* grad_entropy;
+  T* dlogits;
+  int64_t dseq, drow;
+  int64_t chunk, split;  // elements per work item, work items per row
+};
+
+// The gradient of one element.
+struct RowGrad {
+  float m, c, L2, A, B, g;  // g: of the log-prob, divided by T
+  __device__ __forceinline__ float at(float x) const {
+    const float l = max_keep_nan(fmaf(x - m, c, -L2), kLowest);
+    return ex2(l) * fmaf(B, l, A);
+  }
+  // at the token: g (1 - p) without cancellation
+  __device__ __forceinline__ float at_token(float x) const {
+    const float l = max_keep_nan(fmaf(x - m, c, -L2), kLowest);
+    return ex2(l) * fmaf(B, l, A + g) - g * expm1f(l * kLn2);
+  }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) token_stats_bwd_kernel(
+    const StatsBwdParams<T> p) {
+  using E = Elt<T>;
+  constexpr int EPV = E::kPerVec, U = E::kUnroll;
+  const int tid = threadIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  const int64_t items = p.N * p.R * p.split;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t r = item / p.split, i = r / p.R, j = r - i * p.R;
+    const int64_t v0 = (item - r * p.split) * p.chunk, v1 = min(p.V, v0 + p.chunk);
+    if (v0 >= v1) continue;
+    const T* z = p.logits + i * p.seq + j * p.row;
+    T* out = p.dlogits + i * p.dseq + j * p.drow;
+    // 16-byte vectors of the output in [a, b)
+    const unsigned phase = (unsigned)(reinterpret_cast<uintptr_t>(out + v0) & 15u);
+    const int64_t a = min(v0 + (int64_t)(((16u - phase) & 15u) / sizeof(T)), v1);
+    const int nvec = (int)((v1 - a) / EPV);
+    const int64_t b = a + (int64_t)nvec * EPV;
+    uint4* ovec = reinterpret_cast<uint4*>(out + a);
+    const bool inside = p.lens == nullptr || j < __ldg(p.lens + i);
+    const float g = inside && p.grad_logp != nullptr ? __ldg(p.grad_logp + r) : 0.f;
+    const float h = inside && p.grad_entropy != nullptr ? __ldg(p.grad_entropy + r) : 0.f;
+    int64_t edge = -1;
+    if (tid < a - v0)
+      edge = v0 + tid;
+    else if (tid >= 32 && tid - 32 < v1 - b)
+      edge = b + tid - 32;
+    if (g == 0.f && h == 0.f) {  // zeros, logits not read
+      for (int k = tid; k < nvec; k += kThreads) st_stream(ovec + k, zero);
+      if (edge >= 0) E::store1(out + edge, 0.f);
+      continue;
+    }
+    const float Ti = warmth_of(p.temperature, i);
+    RowGrad q;
+    q.m = __ldg(p.norm + 2 * r);
+    q.L2 = __ldg(p.norm + 2 * r + 1) * kLog2e;
+    q.c = kLog2e / Ti;
+    q.g = g / Ti;
+    const float H = h != 0.f ? __ldg(p.entropy + r) : 0.f;
+    q.A = -(q.g + h / Ti * H);
+    q.B = -h / Ti * kLn2;
+    int64_t y = -1;
+    if (g != 0.f) {
+      y = __ldg(p.tokens + i * p.token_seq + j);
+      if (y < 0 || y >= p.V) q.A = NAN;
+    }
+    const T* zin = z + a;
+    if (((reinterpret_cast<uintptr_t>(zin) ^ reinterpret_cast<uintptr_t>(ovec)) & 15u) == 0) {
+      const uint4* zvec = reinterpret_cast<const uint4*>(zin);
+      const int ky = y >= a && y < b ? (int)((y - a) / EPV) : -1;
+      const int ey = ky >= 0 ? (int)((y - a) % EPV) : 0;
+      for (int k0 = tid; k0 < nvec; k0 += kThreads * U) {
+        uint4 d[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int k = k0 + u * kThreads;
+          if (k < nvec) d[u] = ld_stream(zvec + k);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int k = k0 + u * kThreads;
+          if (k >= nvec) break;
+          float x[EPV], o[EPV];
+          E::unpack(d[u], x);
+#pragma unroll
+          for (int e = 0; e < EPV; ++e) o[e] = q.at(x[e]);
+          if (k == ky) {
+            const float zy = E::extract(d[u], ey);
+#pragma unroll
+            for (int e = 0; e < EPV; ++e)
+              if (e == ey) o[e] = q.at_token(zy);
+          }
+          st_stream(ovec + k, E::pack(o));
+        }
+      }
+    } else {
+      for (int64_t v = a + tid; v < b; v += kThreads) {
+        const float x = E::load1(z + v);
+        E::store1(out + v, v == y ? q.at_token(x) : q.at(x));
+      }
+    }
+    if (edge >= 0) {
+      const float x = E::load1(z + edge);
+      E::store1(out + edge, edge == y ? q.at_token(x) : q.at(x));
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// launch
+// ---------------------------------------------------------------------------
+
+template <typename T>
+cudaError_t stats_run(const TokenStatsArgs& a, const DeviceInfo&, cudaStream_t st) {
+  StatsParams<T> p;
+  p.logits = static_cast<const T*>(a.logits);
+  p.N = a.N;
+  p.R = a.R;
+  p.V = a.V;
+  p.seq = a.seq;
+  p.row = a.row;
+  p.tokens = a.tokens;
+  p.token_seq = a.token_seq;
+  p.lens = a.lens;
+  p.temperature = a.temperature;
+  p.top = a.top;
+  p.logp = a.logp;
+  p.entropy = a.entropy;
+  p.norm = a.norm;
+  p.top_tokens = a.top_tokens;
+  p.top_logp = a.top_logp;
+  p.hdr = static_cast<WsHeader*>(a.ws);
+  const int64_t rows = a.N * a.R;
+  const dim3 grid((unsigned)(rows < 1 ? 1 : rows));
+  if (a.top == 0) return launch_pdl(token_stats_kernel<T, false>, grid, dim3(kThreads), 0, st, 1, p);
+  return launch_pdl(token_stats_kernel<T, true>, grid, dim3(kThreads), sizeof(TopShared), st, 1, p);
+}
+
+template <typename T>
+cudaError_t bwd_run(const TokenStatsBwdArgs& a, const DeviceInfo& d, cudaStream_t st) {
+  constexpr int EPV = Elt<T>::kPerVec;
+  StatsBwdParams<T> p;
+  p.logits = static_cast<const T*>(a.logits);
+  p.N = a.N;
+  p.R = a.R;
+  p.V = a.V;
+  p.seq = a.seq;
+  p.row = a.row;
+  p.tokens = a.tokens;
+  p.token_seq = a.token_seq;
+  p.lens = a.lens;
+  p.temperature = a.temperature;
+  p.norm = a.norm;
+  p.entropy = a.entropy;
+  p.grad_logp = a.grad_logp;
+  p.grad_entropy = a.grad_entropy;
+  p.dlogits = static_cast<T*>(a.dlogits);
+  p.dseq = a.dseq;
+  p.drow = a.drow;
+  p.split = row_split(a.V * (int64_t)sizeof(T), nullptr, 8);
+  p.chunk = ((a.V + p.split - 1) / p.split + EPV - 1) / EPV * EPV;
+  const int64_t items = a.N * a.R * p.split;
+  int64_t grid = 256 * (int64_t)d.sms;
+  if (grid > items) grid = items;
+  return launch_pdl(token_stats_bwd_kernel<T>, dim3((unsigned)grid), dim3(kThreads), 0, st, 1, p);
+}
+
+}  // namespace
+
+size_t token_stats_workspace_bytes(int64_t N, int64_t R) {
+  return align_up(256 + 4 * (size_t)N * (size_t)R, 256);
+}
+
+cudaError_t launch_token_stats(const TokenStatsArgs& a, const DeviceInfo& d, cudaStream_t st) {
+  return a.dtype == 0 ? stats_run<float>(a, d, st) : stats_run<uint16_t>(a, d, st);
+}
+
+cudaError_t launch_token_stats_bwd(const TokenStatsBwdArgs& a, const DeviceInfo& d,
+                                   cudaStream_t st) {
+  if (a.N * a.R == 0) return cudaSuccess;
+  return a.dtype == 0 ? bwd_run<float>(a, d, st) : bwd_run<uint16_t>(a, d, st);
+}
+
+}  // namespace grpo
