@@ -76,6 +76,7 @@ struct StatsParams {
   int64_t* top_tokens;
   float* top_logp;
   WsHeader* hdr;
+  int64_t chunk;  // elements of a row per CTA of its cluster
 };
 
 constexpr int kSlots = 32;      // groups of a thread whose maxima are kept, the last for a ragged end
@@ -110,13 +111,16 @@ struct Sums {
   }
 };
 
-template <typename T>
+constexpr int kMaxSplit = 8;  // CTAs of a cluster that share a row
+
 struct StatsShared {
   float warp_max[kWarps];
   float2 warp_sum[kWarps];
-  float4 total;  // m, S, E
+  float4 part[kMaxSplit];  // of the cluster's CTAs, in the first one: m, S, E
 };
 struct TopShared {
+  uint64_t part_key[kMaxSplit][kMaxTop];  // likewise: their best keys, sorted
+
   float slot[kSlots][kThreads];
   float quad[64];
   uint64_t key[kCandidates];
@@ -140,11 +144,11 @@ struct Part {  // elements [v0, v1) of a row; vectors of 16 bytes in [a, b)
   int groups, per;  // groups of `per` batches of U vectors
 };
 
-// The best `top` of the part's elements, as keys in sh.key[0 .. top) sorted, with
-// the elements' count in the return value.  Called by the whole CTA after the
-// stream; `own_max` is the thread's largest element.
+// The best `top` of the part's elements (all of them if it has fewer), as keys in
+// sh.key[0 ..) sorted, zeros behind them.  Called by the whole CTA after the stream;
+// `own_max` is the thread's largest element.
 template <typename T>
-__device__ int best_of_part(TopShared& sh, const Part<T>& p, float own_max, int top) {
+__device__ void best_of_part(TopShared& sh, const Part<T>& p, float own_max, int top) {
   using E = Elt<T>;
   constexpr int EPV = E::kPerVec, U = E::kUnroll;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -281,9 +285,38 @@ __device__ int best_of_part(TopShared& sh, const Part<T>& p, float own_max, int 
     if (rank[u] < top) s_sorted[rank[u]] = mine[u];
   __syncthreads();
   const int got = (int)min(n, (int64_t)top);
-  if (tid < got) sh.key[tid] = s_sorted[tid];
+  if (tid < kMaxTop) sh.key[tid] = tid < got ? s_sorted[tid] : 0;
   __syncthreads();
-  return got;
+}
+
+// The best `top` of the cluster's sorted lists, in sh.key[0 .. top): a key comes
+// behind those before it in its own list and the larger ones of every other.
+__device__ __forceinline__ void merge_parts(TopShared& sh, int parts, int top) {
+  const int list = threadIdx.x / kMaxTop, at = threadIdx.x % kMaxTop;
+  const uint64_t mine = list < parts && at < top ? sh.part_key[list][at] : 0;
+  if (mine != 0) {
+    int rank = at;
+    for (int other = 0; other < parts; ++other) {
+      if (other == list) continue;
+      int lo = 0;  // keys of the other list that are larger
+#pragma unroll
+      for (int step = kMaxTop / 2; step > 0; step /= 2)
+        if (sh.part_key[other][lo + step - 1] > mine) lo += step;
+      if (sh.part_key[other][lo] > mine) ++lo;
+      rank += lo;
+    }
+    if (rank < top) sh.key[rank] = mine;
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
 }
 
 template <typename T, bool kTop>
@@ -292,12 +325,13 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
   constexpr int EPV = E::kPerVec, U = E::kUnroll;
   extern __shared__ char s_dyn[];
   TopShared& top = *reinterpret_cast<TopShared*>(s_dyn);
-  __shared__ StatsShared<T> sh;
+  __shared__ StatsShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
-  const int64_t rows = p.N * p.R, r = blockIdx.x;
-  if (r == 0 && tid == 0) {
+  const uint32_t parts = cluster_size(), rank = cluster_ctarank();
+  const int64_t rows = p.N * p.R, r = cluster_id_x();
+  if (r == 0 && rank == 0 && tid == 0) {
     p.hdr->flags = kFlagIndirect;
     p.hdr->status_count = (uint32_t)rows;
     p.hdr->status_check = ~(uint32_t)rows;
@@ -310,6 +344,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
     const int64_t len = __ldg(p.lens + i);
     if ((len < 0 || len > p.R) && j == 0) flags = kFlagLengthRange;
     if (j >= len) {  // behind the sequence's end
+      if (rank != 0) return;
       if (tid == 0) {
         p.logp[r] = p.entropy[r] = p.norm[2 * r] = p.norm[2 * r + 1] = 0.f;
         *status = flags;
@@ -325,8 +360,16 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
   const float c = kLog2e / Ti;
   Part<T> part;
   part.z = p.logits + i * p.seq + j * p.row;
-  part.v0 = 0;
-  part.v1 = p.V;
+  part.v0 = min(p.V, rank * p.chunk);
+  part.v1 = min(p.V, part.v0 + p.chunk);
+  if (parts > 1) cluster_arrive_relaxed();  // (the first CTA runs before it is written to)
+  // the token's logit, in time for the end
+  int64_t y = -1;
+  float zy = 0.f;
+  if (rank == 0 && tid == 0) {
+    y = __ldg(p.tokens + i * p.token_seq + j);
+    if (y >= 0 && y < p.V) zy = E::load1(part.z + y);
+  }
   const unsigned phase = (unsigned)(reinterpret_cast<uintptr_t>(part.z + part.v0) & 15u);
   part.a = min(part.v0 + (int64_t)(((16u - phase) & 15u) / sizeof(T)), part.v1);
   part.nvec = (int)((part.v1 - part.a) / EPV);
@@ -409,23 +452,38 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
     s += sh.warp_sum[w].x;
     e += sh.warp_sum[w].y;
   }
+  if (parts > 1) {
+    if (kTop) best_of_part(top, part, sum.top, p.top);
+    __syncwarp();  // (the cluster's barriers want whole warps)
+    cluster_wait();
+    if (tid == 0)
+      st_cluster_f32x4(map_to_rank(smem_u32(&sh.part[rank]), 0), make_float4(m, s, e, 0.f));
+    if (kTop && tid < kMaxTop)
+      st_cluster_u64(map_to_rank(smem_u32(&top.part_key[rank][tid]), 0), top.key[tid]);
+    __syncwarp();
+    cluster_sync();
+    if (rank != 0) return;
+    m = sh.part[0].x;
+    for (int k = 1; k < (int)parts; ++k) m = fmaxf(m, sh.part[k].x);
+    s = e = 0.f;
+    for (int k = 0; k < (int)parts; ++k) {
+      const float4 q = sh.part[k];
+      // (a part of nothing but -inf has sums 0)
+      const float d = fmaxf((q.x - m) * c, kLowest), f = ex2(d);
+      s += f * q.y;
+      e += f * fmaf(d, q.y, q.z);
+    }
+  }
   // (a comparison with NaN is false)
   const bool defined = s > 0.f && s < INFINITY && fabsf(m) < INFINITY && c > 0.f;
   const float L = logf(s);
   if (tid == 0) {
-    float lp = NAN, H = NAN;
-    if (defined) {
-      H = L - kLn2 * (e / s);
-      const int64_t y = __ldg(p.tokens + i * p.token_seq + j);
-      if (y >= 0 && y < p.V)
-        lp = (E::load1(part.z + y) - m) / Ti - L;
-      else
-        flags |= kFlagTokenRange;
-    } else {
+    if (!defined)
       flags |= kFlagValue;
-    }
-    p.logp[r] = lp;
-    p.entropy[r] = H;
+    else if (y < 0 || y >= p.V)
+      flags |= kFlagTokenRange;
+    p.logp[r] = defined && y >= 0 && y < p.V ? (zy - m) / Ti - L : NAN;
+    p.entropy[r] = defined ? L - kLn2 * (e / s) : NAN;
     p.norm[2 * r] = defined ? m : NAN;
     p.norm[2 * r + 1] = defined ? L : NAN;
     *status = flags;
@@ -438,7 +496,10 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
     }
     return;
   }
-  best_of_part(top, part, sum.top, p.top);
+  if (parts > 1)
+    merge_parts(top, (int)parts, p.top);
+  else
+    best_of_part(top, part, sum.top, p.top);
   if (tid < p.top) {
     const uint64_t k = top.key[tid];
     p.top_tokens[r * p.top + tid] = key_id(k);
@@ -481,11 +542,70 @@ struct RowGrad {
   }
 };
 
+// The 16 bytes that begin `shift` bytes (a multiple of 2) into lo and hi.
+__device__ __forceinline__ uint4 from_two(uint4 lo, uint4 hi, unsigned shift) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  if (shift & 8) {
+#pragma unroll
+    for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+  }
+  if (shift & 4) {
+#pragma unroll
+    for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
+  }
+  const unsigned bits = (shift & 2) * 8;
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
+// nvec vectors of gradients; z: the first one's logits (kShift: `shift` bytes
+// behind a 16-byte boundary), y: the token relative to it.
+template <typename T, bool kShift>
+__device__ __forceinline__ void grad_vectors(const T* z, uint4* out, int nvec, unsigned shift,
+                                             const RowGrad& q, int64_t y) {
+  using E = Elt<T>;
+  constexpr int EPV = E::kPerVec, U = kShift ? E::kUnroll / 2 : E::kUnroll;
+  const uint4* zvec = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(z) - shift);
+  const int ky = y >= 0 && y < (int64_t)nvec * EPV ? (int)(y / EPV) : -1;
+  const int ey = ky >= 0 ? (int)(y % EPV) : 0;
+  for (int k0 = threadIdx.x; k0 < nvec; k0 += kThreads * U) {
+    uint4 d[U], next[kShift ? U : 1];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * kThreads;
+      if (k >= nvec) break;
+      if (kShift) {  // (the neighbour's first is this one's second: through L1)
+        d[u] = __ldg(zvec + k);
+        next[u] = __ldg(zvec + k + 1);
+      } else {
+        d[u] = ld_stream(zvec + k);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * kThreads;
+      if (k >= nvec) break;
+      if (kShift) d[u] = from_two(d[u], next[u], shift);
+      float x[EPV], o[EPV];
+      E::unpack(d[u], x);
+#pragma unroll
+      for (int e = 0; e < EPV; ++e) o[e] = q.at(x[e]);
+      if (k == ky) {
+        const float zy = E::extract(d[u], ey);
+#pragma unroll
+        for (int e = 0; e < EPV; ++e)
+          if (e == ey) o[e] = q.at_token(zy);
+      }
+      st_stream(out + k, E::pack(o));
+    }
+  }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) token_stats_bwd_kernel(
     const StatsBwdParams<T> p) {
   using E = Elt<T>;
-  constexpr int EPV = E::kPerVec, U = E::kUnroll;
+  constexpr int EPV = E::kPerVec;
   const int tid = threadIdx.x;
   pdl_wait();
   pdl_trigger();
@@ -497,10 +617,18 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) token_stats_
     if (v0 >= v1) continue;
     const T* z = p.logits + i * p.seq + j * p.row;
     T* out = p.dlogits + i * p.dseq + j * p.drow;
-    // 16-byte vectors of the output in [a, b)
+    // 16-byte vectors of the output in [a, b); the input lies `shift` bytes behind
+    // such a boundary there
     const unsigned phase = (unsigned)(reinterpret_cast<uintptr_t>(out + v0) & 15u);
-    const int64_t a = min(v0 + (int64_t)(((16u - phase) & 15u) / sizeof(T)), v1);
-    const int nvec = (int)((v1 - a) / EPV);
+    int64_t a = min(v0 + (int64_t)(((16u - phase) & 15u) / sizeof(T)), v1);
+    int nvec = (int)((v1 - a) / EPV);
+    const unsigned shift = (unsigned)(reinterpret_cast<uintptr_t>(z + a) & 15u);
+    if (shift != 0 && nvec > 0) {
+      // a vector is put together from the two of the input that it lies in: both inside
+      // the row
+      if (a * (int64_t)sizeof(T) < shift) a += EPV, --nvec;
+      if (nvec > 0 && (p.V - a - (int64_t)nvec * EPV) * (int64_t)sizeof(T) < 16 - shift) --nvec;
+    }
     const int64_t b = a + (int64_t)nvec * EPV;
     uint4* ovec = reinterpret_cast<uint4*>(out + a);
     const bool inside = p.lens == nullptr || j < __ldg(p.lens + i);
@@ -530,41 +658,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) token_stats_
       y = __ldg(p.tokens + i * p.token_seq + j);
       if (y < 0 || y >= p.V) q.A = NAN;
     }
-    const T* zin = z + a;
-    if (((reinterpret_cast<uintptr_t>(zin) ^ reinterpret_cast<uintptr_t>(ovec)) & 15u) == 0) {
-      const uint4* zvec = reinterpret_cast<const uint4*>(zin);
-      const int ky = y >= a && y < b ? (int)((y - a) / EPV) : -1;
-      const int ey = ky >= 0 ? (int)((y - a) % EPV) : 0;
-      for (int k0 = tid; k0 < nvec; k0 += kThreads * U) {
-        uint4 d[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int k = k0 + u * kThreads;
-          if (k < nvec) d[u] = ld_stream(zvec + k);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int k = k0 + u * kThreads;
-          if (k >= nvec) break;
-          float x[EPV], o[EPV];
-          E::unpack(d[u], x);
-#pragma unroll
-          for (int e = 0; e < EPV; ++e) o[e] = q.at(x[e]);
-          if (k == ky) {
-            const float zy = E::extract(d[u], ey);
-#pragma unroll
-            for (int e = 0; e < EPV; ++e)
-              if (e == ey) o[e] = q.at_token(zy);
-          }
-          st_stream(ovec + k, E::pack(o));
-        }
-      }
-    } else {
-      for (int64_t v = a + tid; v < b; v += kThreads) {
-        const float x = E::load1(z + v);
-        E::store1(out + v, v == y ? q.at_token(x) : q.at(x));
-      }
-    }
+    if (shift == 0)
+      grad_vectors<T, false>(z + a, ovec, nvec, 0, q, y - a);
+    else
+      grad_vectors<T, true>(z + a, ovec, nvec, shift, q, y - a);
     if (edge >= 0) {
       const float x = E::load1(z + edge);
       E::store1(out + edge, edge == y ? q.at_token(x) : q.at(x));
@@ -577,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) token_stats_
 // ---------------------------------------------------------------------------
 
 template <typename T>
-cudaError_t stats_run(const TokenStatsArgs& a, const DeviceInfo&, cudaStream_t st) {
+cudaError_t stats_run(const TokenStatsArgs& a, const DeviceInfo& d, cudaStream_t st) {
   StatsParams<T> p;
   p.logits = static_cast<const T*>(a.logits);
   p.N = a.N;
@@ -597,9 +694,14 @@ cudaError_t stats_run(const TokenStatsArgs& a, const DeviceInfo&, cudaStream_t s
   p.top_logp = a.top_logp;
   p.hdr = static_cast<WsHeader*>(a.ws);
   const int64_t rows = a.N * a.R;
-  const dim3 grid((unsigned)(rows < 1 ? 1 : rows));
-  if (a.top == 0) return launch_pdl(token_stats_kernel<T, false>, grid, dim3(kThreads), 0, st, 1, p);
-  return launch_pdl(token_stats_kernel<T, true>, grid, dim3(kThreads), sizeof(TopShared), st, 1, p);
+  const int split = lse_split(a.V * (int64_t)sizeof(T), rows, d.sms, "GRPO_STATS_SPLIT");
+  constexpr int EPV = Elt<T>::kPerVec;
+  p.chunk = ((a.V + split - 1) / split + EPV - 1) / EPV * EPV;
+  const dim3 grid((unsigned)(rows < 1 ? split : rows * split));
+  if (a.top == 0)
+    return launch_pdl(token_stats_kernel<T, false>, grid, dim3(kThreads), 0, st, split, p);
+  return launch_pdl(token_stats_kernel<T, true>, grid, dim3(kThreads), sizeof(TopShared), st,
+                    split, p);
 }
 
 template <typename T>
