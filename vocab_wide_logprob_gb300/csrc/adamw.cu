@@ -16,6 +16,7 @@
 // operation (no fused products, the root and the quotients correctly rounded): the codes
 // are those of the same float32 formula anywhere.
 #include <math.h>
+#include <stdlib.h>
 
 #include <type_traits>
 
@@ -24,12 +25,11 @@
 namespace grpo {
 namespace {
 
-constexpr int kChunk = 2048;  // elements of a thread block's piece of a tensor
-constexpr int kUnits = kChunk / 8 / kThreads;  // of 8 elements, per thread
+constexpr int kUnit = 8 * kThreads;  // elements that a thread block takes at once
+constexpr int kMaxUnits = 4;         // at most so many in turn
 constexpr float kF8Max = 448.f;                // e4m3's largest value
-constexpr float kF8Tiny = 0x1p-9f;             // and its smallest positive one
 constexpr float kNothing = 0x1p-80f;           // a block of smaller |m| is stored as 0
-static_assert(kChunk % kStateBlock == 0 && kStateBlock == 8 * 32, "a warp holds a block");
+static_assert(kUnit % kStateBlock == 0 && kStateBlock == 8 * 32, "a warp holds a block");
 
 template <int CAP>
 struct Table {
@@ -43,6 +43,7 @@ struct Table {
   int64_t first[CAP + 1];  // the chunk that a tensor begins with
   uint8_t dt[CAP];         // bit 0: param is bf16, bit 1: grad is bf16
   int count;
+  int units;  // of a chunk
 };
 
 struct Hyper {
@@ -53,6 +54,7 @@ struct Hyper {
   const float* lr_dev;
   const float* norm;
   float max_norm, norm_eps;
+  float minus_zero;
 };
 
 // What a step takes from device memory where the caller has it there.
@@ -75,91 +77,130 @@ __device__ __forceinline__ int find_tensor(const Table<CAP>& t, int64_t chunk) {
 
 // ---- 8 consecutive elements ------------------------------------------------------
 
-__device__ __forceinline__ void ld8(const float* p, float* x) {
-  if (reinterpret_cast<uintptr_t>(p) % 32 == 0) {
-    asm volatile("ld.global.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]),
-                   "=f"(x[6]), "=f"(x[7])
-                 : "l"(p));
-    return;
-  }
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void ld8(const uint16_t* p, float* x) {
-  Elt<uint16_t>::unpack(*reinterpret_cast<const uint4*>(p), x);
-}
-__device__ __forceinline__ void st8(float* p, const float* x) {
-  if (reinterpret_cast<uintptr_t>(p) % 32 == 0) {
-    st_32bytes<false>(p, x);
-    return;
-  }
-  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-__device__ __forceinline__ void st8(uint16_t* p, const float* x) {
-  *reinterpret_cast<uint4*>(p) = Elt<uint16_t>::pack(x);
-}
+// As they are stored, in registers.
+template <typename T>
+struct Raw8;
 
-// e4m3 codes
-struct F8 {
-  uint8_t bits;
+template <>
+struct Raw8<float> {
+  float x[8];
+  __device__ __forceinline__ void load(const float* p) {
+    if (reinterpret_cast<uintptr_t>(p) % 32 == 0) {
+      asm volatile("ld.global.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]),
+                     "=f"(x[6]), "=f"(x[7])
+                   : "l"(p));
+      return;
+    }
+    const float4 a = reinterpret_cast<const float4*>(p)[0];
+    const float4 b = reinterpret_cast<const float4*>(p)[1];
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+  __device__ __forceinline__ void load_some(const float* p, int n) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = k < n ? p[k] : 0.f;
+  }
+  __device__ __forceinline__ uint64_t pair(int k) const { return f2_pack(x[2 * k], x[2 * k + 1]); }
+  __device__ __forceinline__ void set(int k, uint64_t v) { f2_unpack(v, x[2 * k], x[2 * k + 1]); }
+  __device__ __forceinline__ void store(float* p) const {
+    if (reinterpret_cast<uintptr_t>(p) % 32 == 0) {
+      st_32bytes<false>(p, x);
+      return;
+    }
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
+  __device__ __forceinline__ void store_some(float* p, int n) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) p[k] = x[k];
+  }
 };
-__device__ __forceinline__ uint32_t f8_pack2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ void f8_unpack2(uint32_t w, float& lo, float& hi) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-      : "=f"(lo), "=f"(hi)
-      : "r"(h));
-}
-__device__ __forceinline__ void ld8(const F8* p, float* x) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  f8_unpack2(w.x & 0xffffu, x[0], x[1]);
-  f8_unpack2(w.x >> 16, x[2], x[3]);
-  f8_unpack2(w.y & 0xffffu, x[4], x[5]);
-  f8_unpack2(w.y >> 16, x[6], x[7]);
-}
-__device__ __forceinline__ void st8(F8* p, const float* x) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(f8_pack2(x[0], x[1]) | f8_pack2(x[2], x[3]) << 16,
-                                            f8_pack2(x[4], x[5]) | f8_pack2(x[6], x[7]) << 16);
-}
 
-__device__ __forceinline__ float ld1(const float* p) { return *p; }
-__device__ __forceinline__ float ld1(const uint16_t* p) { return bf16_bits_to_float(*p); }
-__device__ __forceinline__ float ld1(const F8* p) {
-  float x, y;
-  f8_unpack2(p->bits, x, y);
-  return x;
-}
-__device__ __forceinline__ void st1(float* p, float x) { *p = x; }
-__device__ __forceinline__ void st1(uint16_t* p, float x) { Elt<uint16_t>::store1(p, x); }
-__device__ __forceinline__ void st1(F8* p, float x) { p->bits = (uint8_t)f8_pack2(x, 0.f); }
+template <>
+struct Raw8<uint16_t> {  // bfloat16
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  }
+  __device__ __forceinline__ void load_some(const uint16_t* p, int n) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      w[k] = (2 * k < n ? (uint32_t)p[2 * k] : 0u) |
+             (2 * k + 1 < n ? (uint32_t)p[2 * k + 1] << 16 : 0u);
+  }
+  __device__ __forceinline__ uint64_t pair(int k) const {
+    return f2_pack(bf16_lo(w[k]), bf16_hi(w[k]));
+  }
+  __device__ __forceinline__ void set(int k, uint64_t v) {
+    float a, b;
+    f2_unpack(v, a, b);
+    w[k] = pack_bf16x2(a, b);
+  }
+  __device__ __forceinline__ void store(uint16_t* p) const {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void store_some(uint16_t* p, int n) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) p[k] = (uint16_t)(w[k / 2] >> (k % 2 * 16));
+  }
+};
 
-// n of 8 elements (zeros behind them); wide: all 8, aligned
-template <typename T>
-__device__ __forceinline__ void load(const T* p, float* x, bool wide, int n) {
-  if (wide) {
-    ld8(p, x);
-    return;
+template <>
+struct Raw8<uint8_t> {  // e4m3 codes
+  uint32_t w[2];
+  __device__ __forceinline__ void load(const uint8_t* p) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
   }
+  __device__ __forceinline__ void load_some(const uint8_t* p, int n) {
+    w[0] = w[1] = 0;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) x[k] = k < n ? ld1(p + k) : 0.f;
+    for (int k = 0; k < 8; ++k)
+      if (k < n) w[k / 4] |= (uint32_t)p[k] << (k % 4 * 8);
+  }
+  __device__ __forceinline__ uint64_t pair(int k) const {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[k / 2] >> (k % 2 * 16))));
+    float a, b;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+        : "=f"(a), "=f"(b)
+        : "r"(h));
+    return f2_pack(a, b);
+  }
+  __device__ __forceinline__ void set(int k, uint64_t v) {  // k in order
+    float a, b;
+    f2_unpack(v, a, b);
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+    w[k / 2] = k % 2 == 0 ? (uint32_t)r : w[k / 2] | (uint32_t)r << 16;
+  }
+  __device__ __forceinline__ void store(uint8_t* p) const {
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  }
+  __device__ __forceinline__ void store_some(uint8_t* p, int n) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < n) p[k] = (uint8_t)(w[k / 4] >> (k % 4 * 8));
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void load(Raw8<T>& r, const T* p, bool wide, int n) {
+  if (wide)
+    r.load(p);
+  else
+    r.load_some(p, n);
 }
 template <typename T>
-__device__ __forceinline__ void store(T* p, const float* x, bool wide, int n) {
-  if (wide) {
-    st8(p, x);
-    return;
-  }
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    if (k < n) st1(p + k, x[k]);
+__device__ __forceinline__ void store(const Raw8<T>& r, T* p, bool wide, int n) {
+  if (wide)
+    r.store(p);
+  else
+    r.store_some(p, n);
 }
 
 __device__ __forceinline__ float max_keep_nan(float a, float b) {
@@ -176,12 +217,47 @@ __device__ __forceinline__ float block_scale(float largest, float& inverse) {
   inverse = any ? __frcp_rn(scale) : 0.f;
   return scale;
 }
+__device__ __forceinline__ uint64_t both(float x) { return f2_pack(x, x); }
+
+// Products that stay products: an addition behind f2_mul becomes one fused
+// instruction with it (seen in the sums' last bits); behind x y + z, with a z that is -0
+// but not known to be when this is compiled, it cannot.
+__device__ __forceinline__ uint64_t product(uint64_t x, uint64_t y, const Hyper& h) {
+  return f2_fma(x, y, both(h.minus_zero));
+}
+
 // x / s correctly rounded, from the correctly rounded 1 / s (P. Markstein's
 // theorem: an estimate within one step, its remainder by a fused product, one correction).
 // s is above 2^-89, so that the remainder of a quotient that has a code is exact.
-__device__ __forceinline__ float quotient(float x, float s, float inverse) {
-  const float q = __fmul_rn(x, inverse);
-  return __fmaf_rn(__fmaf_rn(-q, s, x), inverse, q);
+__device__ __forceinline__ uint64_t quotient(uint64_t x, uint64_t minus_s, uint64_t inverse) {
+  const uint64_t q = f2_mul(x, inverse);
+  return f2_fma(f2_fma(q, minus_s, x), inverse, q);
+}
+// The square root by one Newton step (Heron's, on the reciprocal root's
+// estimate): v y = sqrt(v) (1 + d) with |d| below 2^-22, and the remainder v - (v y)^2 is
+// exact, so that what is rounded at the end is off by 2^-44: the nearest float32 but in one of a
+// million cases.
+__device__ __forceinline__ uint64_t root_of(uint64_t v) {
+  float a, b, ya, yb;
+  f2_unpack(v, a, b);
+  asm("rsqrt.approx.f32 %0, %1;" : "=f"(ya) : "f"(a));
+  asm("rsqrt.approx.f32 %0, %1;" : "=f"(yb) : "f"(b));
+  const uint64_t y = f2_pack(ya, yb), s = f2_mul(v, y);
+  float ra, rb, sa, sb;
+  f2_unpack(s, sa, sb);
+  const uint64_t rest = f2_fma(f2_pack(-sa, -sb), s, v);
+  f2_unpack(f2_fma(rest, f2_mul(y, both(0.5f)), s), ra, rb);
+  // (0 and infinity are their own roots)
+  ra = a == 0.f || a == INFINITY ? a : ra;
+  rb = b == 0.f || b == INFINITY ? b : rb;
+  return f2_pack(ra, rb);
+}
+__device__ __forceinline__ uint64_t reciprocals(uint64_t x) {
+  float a, b;
+  f2_unpack(x, a, b);
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+  return f2_pack(a, b);
 }
 
 // ---- the step ------------------------------------------------------------------------
@@ -190,81 +266,111 @@ __device__ __forceinline__ float quotient(float x, float s, float inverse) {
 template <typename W, typename G, bool kMaster, bool kEight>
 __device__ __forceinline__ void chunk_step(W* param, float* master, const G* grad, void* avg_,
                                            void* sq_, float* scales, int64_t numel, int64_t e0,
-                                           const Hyper& h, const Now& now) {
-  using State = std::conditional_t<kEight, F8, float>;
+                                           int units, const Hyper& h, const Now& now) {
+  using State = std::conditional_t<kEight, uint8_t, float>;
+  using Value = std::conditional_t<kMaster, float, W>;
   State* avg = static_cast<State*>(avg_);
   State* sq = static_cast<State*>(sq_);
+  Value* value;
+  if constexpr (kMaster)
+    value = master;
+  else
+    value = param;
   const int lane = threadIdx.x & 31;
   const uintptr_t states = reinterpret_cast<uintptr_t>(avg) | reinterpret_cast<uintptr_t>(sq);
   const uintptr_t others = reinterpret_cast<uintptr_t>(param) | reinterpret_cast<uintptr_t>(grad) |
-                           (kMaster ? reinterpret_cast<uintptr_t>(master) : 0);
+                           reinterpret_cast<uintptr_t>(value);
   const bool aligned = (others & 15) == 0 && (states & (kEight ? 7 : 15)) == 0;
-  float g[kUnits][8], m[kUnits][8], v[kUnits][8], w[kUnits][8];
-  float2 sc[kUnits];
-#pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    const int64_t e = e0 + (int64_t)(u * kThreads + threadIdx.x) * 8;
-    const int n = (int)min((int64_t)8, numel - e);  // (none or fewer behind the end)
+  int64_t e = e0 + threadIdx.x * 8;
+#pragma unroll 1
+  for (int unit = 0; unit < units; ++unit, e += kUnit) {
+    // (a warp that has elements stays whole: it shares a block's scales)
+    if (e - lane * 8 >= numel) break;
+    const int n = (int)max((int64_t)0, min((int64_t)8, numel - e));
     const bool wide = aligned && n == 8;
-    load(grad + e, g[u], wide, n);
-    load(avg + e, m[u], wide, n);
-    load(sq + e, v[u], wide, n);
-    if (kMaster)
-      load(master + e, w[u], wide, n);
-    else
-      load(param + e, w[u], wide, n);
-    if (kEight) {
-      const int64_t block = (e - lane * 8) / kStateBlock;
-      sc[u] = block * kStateBlock < numel ? make_float2(scales[2 * block], scales[2 * block + 1])
-                                          : make_float2(0.f, 0.f);
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    const int64_t e = e0 + (int64_t)(u * kThreads + threadIdx.x) * 8;
-    const int n = (int)min((int64_t)8, numel - e);
-    const bool wide = aligned && n == 8;
+    Raw8<G> g;
+    Raw8<State> m, v;
+    Raw8<Value> w;
+    load(g, grad + e, wide, n);
+    load(m, avg + e, wide, n);
+    load(v, sq + e, wide, n);
+    load(w, value + e, wide, n);
+    float2 sc = make_float2(0.f, 0.f);
+    const int64_t block = (e - lane * 8) / kStateBlock;
+    if (kEight) sc = make_float2(scales[2 * block], scales[2 * block + 1]);
+    uint64_t new_m[4], new_v[4];
     float most_m = 0.f, most_r = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float gk = __fmul_rn(g[u][k], now.coef);
-      float mk = m[u][k], vk = v[u][k];
+    for (int k = 0; k < 4; ++k) {
+      const uint64_t gk = f2_mul(g.pair(k), both(now.coef));
+      uint64_t mk = m.pair(k), vk = v.pair(k);
       if (kEight) {
-        mk = __fmul_rn(mk, sc[u].x);
-        vk = __fmul_rn(vk, sc[u].y);
-        vk = __fmul_rn(vk, vk);
+        mk = f2_mul(mk, both(sc.x));
+        vk = f2_mul(vk, both(sc.y));
+        vk = f2_mul(vk, vk);
       }
-      mk = __fadd_rn(__fmul_rn(mk, h.beta1), __fmul_rn(gk, h.one_minus1));
-      vk = __fadd_rn(__fmul_rn(vk, h.beta2), __fmul_rn(__fmul_rn(gk, gk), h.one_minus2));
-      const float root = __fsqrt_rn(vk);
-      const float up = __fdividef(mk * now.inv_c1, fmaf(root, now.inv_root_c2, h.eps));
-      w[u][k] = fmaf(-now.lr, fmaf(h.decay, w[u][k], up), w[u][k]);
-      m[u][k] = mk;
-      v[u][k] = kEight ? root : vk;
+      mk = f2_add(product(mk, both(h.beta1), h), product(gk, both(h.one_minus1), h));
+      vk = f2_add(product(vk, both(h.beta2), h),
+                  product(f2_mul(gk, gk), both(h.one_minus2), h));
+      const uint64_t root = root_of(vk);
+      const uint64_t over = reciprocals(f2_fma(root, both(now.inv_root_c2), both(h.eps)));
+      const uint64_t wk = w.pair(k);
+      // lr (m' / c1 / (..) + decay w)
+      const uint64_t change = f2_fma(f2_mul(mk, both(now.inv_c1)), over, f2_mul(wk, both(h.decay)));
+      const uint64_t next = f2_fma(change, both(-now.lr), wk);
+      w.set(k, next);
+      new_m[k] = mk;
+      new_v[k] = kEight ? root : vk;
       if (kEight) {
-        most_m = max_keep_nan(most_m, fabsf(mk));
-        most_r = max_keep_nan(most_r, root);
+        float a, b;
+        f2_unpack(mk, a, b);
+        most_m = max_keep_nan(most_m, max_keep_nan(fabsf(a), fabsf(b)));
+        f2_unpack(root, a, b);
+        most_r = max_keep_nan(most_r, max_keep_nan(a, b));
       }
     }
     if (kEight) {
       float im, ir;
       const float sm = block_scale(most_m, im), sr = block_scale(most_r, ir);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        m[u][k] = quotient(m[u][k], sm, im);
-        const float r = quotient(v[u][k], sr, ir);
-        v[u][k] = r > 0.f ? fmaxf(r, kF8Tiny) : r;
+      for (int k = 0; k < 4; ++k) {
+        m.set(k, quotient(new_m[k], both(-sm), both(im)));
+        v.set(k, quotient(new_v[k], both(-sr), both(ir)));
       }
-      if (lane == 0 && n > 0) {
-        const int64_t block = e / kStateBlock;
+      // a positive root stays positive: codes that are 0 (found four at a time)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if constexpr (kEight) {
+          if (((v.w[j] - 0x01010101u) & ~v.w[j] & 0x80808080u) != 0) {
+            float r[4];
+            f2_unpack(new_v[2 * j], r[0], r[1]);
+            f2_unpack(new_v[2 * j + 1], r[2], r[3]);
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+              if ((v.w[j] >> (8 * b) & 0xffu) == 0 && r[b] > 0.f && ir > 0.f) v.w[j] |= 1u << (8 * b);
+          }
+        }
+      }
+      if (lane == 0) {
         scales[2 * block] = sm;
         scales[2 * block + 1] = sr;
       }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        m.set(k, new_m[k]);
+        v.set(k, new_v[k]);
+      }
     }
-    store(avg + e, m[u], wide, n);
-    store(sq + e, v[u], wide, n);
-    if (kMaster) store(master + e, w[u], wide, n);
-    store(param + e, w[u], wide, n);
+    store(m, avg + e, wide, n);
+    store(v, sq + e, wide, n);
+    store(w, value + e, wide, n);
+    if constexpr (kMaster) {
+      Raw8<W> rounded;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) rounded.set(k, w.pair(k));
+      store(rounded, param + e, wide, n);
+    }
   }
 }
 
@@ -287,13 +393,13 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
   }
   const int64_t chunk = blockIdx.x;
   const int k = find_tensor(t, chunk);
-  const int64_t e0 = (chunk - t.first[k]) * kChunk, n = t.numel[k];
+  const int64_t e0 = (chunk - t.first[k]) * t.units * kUnit, n = t.numel[k];
   const int dt = t.dt[k] | (t.master[k] != nullptr ? 4 : 0);
   using B = uint16_t;
 #define STEP(W, G, MASTER)                                                                 \
   chunk_step<W, G, MASTER, kEight>(static_cast<W*>(t.param[k]), t.master[k],               \
                                    static_cast<const G*>(t.grad[k]), t.avg[k], t.sq[k],    \
-                                   t.scales[k], n, e0, h, now)
+                                   t.scales[k], n, e0, t.units, h, now)
   switch (dt) {
     case 0:
       STEP(float, float, false);
@@ -321,13 +427,17 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
 constexpr int kMaxTensors = 480;  // of one launch: the parameters stay below 32 KiB
 static_assert(sizeof(Table<kMaxTensors>) + sizeof(Hyper) < 32000, "kernel parameters");
 
-int64_t chunks_of(const AdamwTensor& t) { return (t.numel + kChunk - 1) / kChunk; }
+int64_t chunks_of(const AdamwTensor& t, int units) {
+  const int64_t size = (int64_t)units * kUnit;
+  return (t.numel + size - 1) / size;
+}
 
 template <int CAP>
-cudaError_t launch_group(const AdamwTensor* g, int count, bool eight, const Hyper& h,
+cudaError_t launch_group(const AdamwTensor* g, int count, int units, bool eight, const Hyper& h,
                          cudaStream_t st) {
   Table<CAP> t;
   t.count = count;
+  t.units = units;
   int64_t at = 0;
   for (int k = 0; k < count; ++k) {
     t.param[k] = g[k].param;
@@ -339,7 +449,7 @@ cudaError_t launch_group(const AdamwTensor* g, int count, bool eight, const Hype
     t.numel[k] = g[k].numel;
     t.dt[k] = (uint8_t)g[k].dt;
     t.first[k] = at;
-    at += chunks_of(g[k]);
+    at += chunks_of(g[k], units);
   }
   t.first[count] = at;
   const dim3 grid((unsigned)at), block(kThreads);
@@ -349,7 +459,7 @@ cudaError_t launch_group(const AdamwTensor* g, int count, bool eight, const Hype
 
 }  // namespace
 
-cudaError_t launch_adamw(const AdamwArgs& a, const DeviceInfo&, cudaStream_t st) {
+cudaError_t launch_adamw(const AdamwArgs& a, const DeviceInfo& d, cudaStream_t st) {
   Hyper h;
   h.lr = (float)a.lr;
   h.beta1 = (float)a.beta1;
@@ -367,18 +477,26 @@ cudaError_t launch_adamw(const AdamwArgs& a, const DeviceInfo&, cudaStream_t st)
   h.norm = a.norm;
   h.max_norm = (float)a.max_norm;
   h.norm_eps = (float)a.norm_eps;
+  h.minus_zero = -0.f;
+  // A chunk of several units finds its tensor and its numbers once; where that
+  // would leave fewer than eight chunks per SM, smaller ones run side by side.
+  int64_t all = 0;
+  for (int64_t k = 0; k < a.count; ++k) all += a.tensors[k].numel;
+  int units = kMaxUnits;
+  if (const char* s = getenv("GRPO_ADAMW_UNITS")) units = atoi(s);
+  while (units > 1 && all / (units * kUnit) < 8 * (int64_t)d.sms) units /= 2;
   // tensors in launches of at most kMaxTensors and 2^30 chunks
   int64_t k = 0;
   while (k < a.count) {
     int n = 0;
     int64_t chunks = 0;
     while (k + n < a.count && n < kMaxTensors &&
-           (n == 0 || chunks + chunks_of(a.tensors[k + n]) < (int64_t)1 << 30))
-      chunks += chunks_of(a.tensors[k + n++]);
+           (n == 0 || chunks + chunks_of(a.tensors[k + n], units) < (int64_t)1 << 30))
+      chunks += chunks_of(a.tensors[k + n++], units);
     const AdamwTensor* g = a.tensors + k;
-    const cudaError_t e = n <= 32    ? launch_group<32>(g, n, a.eight, h, st)
-                          : n <= 128 ? launch_group<128>(g, n, a.eight, h, st)
-                                     : launch_group<kMaxTensors>(g, n, a.eight, h, st);
+    const cudaError_t e = n <= 32    ? launch_group<32>(g, n, units, a.eight, h, st)
+                          : n <= 128 ? launch_group<128>(g, n, units, a.eight, h, st)
+                                     : launch_group<kMaxTensors>(g, n, units, a.eight, h, st);
     if (e != cudaSuccess) return e;
     k += n;
   }
