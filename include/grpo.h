@@ -669,7 +669,7 @@ typedef struct {
     const void *grad;     /* float32 or bfloat16; NULL: the tensor is left as it is */
     void *exp_avg;        /* float32, or with 8-bit states e4m3 codes */
     void *exp_avg_sq;     /* float32, or with 8-bit states e4m3 codes of its root */
-    float *scales;        /* 8-bit states: [ceil(numel / 256)][2]; else NULL */
+    float *scales;        /* 8-bit states: [ceil(numel / 256)][2], 8-byte aligned; else NULL */
     int64_t numel;
     grpo_dtype param_dtype;
     grpo_dtype grad_dtype;

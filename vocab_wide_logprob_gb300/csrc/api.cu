@@ -1346,7 +1346,7 @@ grpo_status grpo_adamw_step(const grpo_adamw_tensor* tensors, int64_t count, int
     if (t.numel > INT64_MAX / 16 - all) return GRPO_ERR_UNSUPPORTED;
     all += t.numel;
     if (!aligned(t.param, esize_of(t.param_dtype)) || !aligned(t.grad, esize_of(t.grad_dtype)) ||
-        !aligned(t.exp_avg, state) || !aligned(t.exp_avg_sq, state) || !aligned(t.scales, 4) ||
+        !aligned(t.exp_avg, state) || !aligned(t.exp_avg_sq, state) || !aligned(t.scales, 8) ||
         !aligned(t.master, 4))
       return GRPO_ERR_MISALIGNED;
     const size_t e = (size_t)t.numel;
