@@ -20,6 +20,7 @@
 // - L log2(e), A = -(g + h H) / T, B = -h ln2 / T.
 #include <math.h>
 
+#include "host_ctx.cuh"
 #include "ops.cuh"
 
 namespace grpo {
@@ -79,7 +80,11 @@ struct StatsParams {
   int64_t chunk;  // elements of a row per CTA of its cluster
 };
 
-constexpr int kSlots = 32;      // groups of a thread whose maxima are kept, the last for a ragged end
+constexpr int kBatch = 4;       // vectors of 16 bytes that a thread takes at once
+constexpr int kStageVecs = kBatch * kThreads;
+constexpr int kStageBytes = 16 * kStageVecs;
+constexpr int kStages = 3;      // of the ring that bulk copies fill
+constexpr int kSlots = 16;      // groups of a thread whose maxima are kept, the last for a ragged end
 constexpr int kCandidates = 512;
 constexpr int kHits = 256;
 
@@ -111,18 +116,36 @@ struct Sums {
   }
 };
 
+// The elements of a vector in pairs.  (bf16's low halves by byte permutations: as shifts
+// they would go to the pipe that the packed arithmetic fills.)
+__device__ __forceinline__ void pairs_of(const uint4& d, uint64_t* x, float) {
+  x[0] = f2_pack(__uint_as_float(d.x), __uint_as_float(d.y));
+  x[1] = f2_pack(__uint_as_float(d.z), __uint_as_float(d.w));
+}
+__device__ __forceinline__ void pairs_of(const uint4& d, uint64_t* x, uint16_t) {
+  const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t lo;
+    asm("prmt.b32 %0, %1, 0, 0x1044;" : "=r"(lo) : "r"(w[k]));
+    x[k] = f2_pack(__uint_as_float(lo), bf16_hi(w[k]));
+  }
+}
+
 constexpr int kMaxSplit = 8;  // CTAs of a cluster that share a row
 
 struct StatsShared {
+  uint64_t full[kStages], empty[kStages];
+  int abort;  // a bounded wait gave up
   float warp_max[kWarps];
   float2 warp_sum[kWarps];
-  float4 part[kMaxSplit];  // of the cluster's CTAs, in the first one: m, S, E
+  float4 part[kMaxSplit];  // of the cluster's CTAs, in the first one: m, S, E, whether it gave up
 };
 struct TopShared {
   uint64_t part_key[kMaxSplit][kMaxTop];  // likewise: their best keys, sorted
 
   float slot[kSlots][kThreads];
-  float quad[64];
+  alignas(16) float quad[64];
   uint64_t key[kCandidates];
   int hit[kHits];
   float bound;
@@ -150,7 +173,7 @@ struct Part {  // elements [v0, v1) of a row; vectors of 16 bytes in [a, b)
 template <typename T>
 __device__ void best_of_part(TopShared& sh, const Part<T>& p, float own_max, int top) {
   using E = Elt<T>;
-  constexpr int EPV = E::kPerVec, U = E::kUnroll;
+  constexpr int EPV = E::kPerVec, U = kBatch;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t n = p.v1 - p.v0;
   __shared__ uint64_t s_sorted[kMaxTop];
@@ -167,18 +190,19 @@ __device__ void best_of_part(TopShared& sh, const Part<T>& p, float own_max, int
     q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 2));
     if (lane % 4 == 0) sh.quad[tid / 4] = q;
     __syncthreads();
-    if (warp == 0) {
+    if (tid < 64) {
       // the top-th largest of the 64, lower indices first
-      const float mine[2] = {sh.quad[lane], sh.quad[lane + 32]};
-      int before[2] = {0, 0};
-#pragma unroll 8
-      for (int k = 0; k < 64; ++k) {
-        const float x = sh.quad[k];
-        before[0] += x > mine[0] || (x == mine[0] && k < lane);
-        before[1] += x > mine[1] || (x == mine[1] && k < lane + 32);
+      const float mine = sh.quad[tid];
+      int before = 0;
+#pragma unroll 4
+      for (int k = 0; k < 64; k += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(&sh.quad[k]);
+        before += (x.x > mine || (x.x == mine && k < tid)) +
+                  (x.y > mine || (x.y == mine && k + 1 < tid)) +
+                  (x.z > mine || (x.z == mine && k + 2 < tid)) +
+                  (x.w > mine || (x.w == mine && k + 3 < tid));
       }
-      if (before[0] == top - 1) sh.bound = mine[0];
-      if (before[1] == top - 1) sh.bound = mine[1];
+      if (before == top - 1) sh.bound = mine;
     }
     __syncthreads();
     const float bound = sh.bound;
@@ -319,12 +343,14 @@ __device__ __forceinline__ uint32_t cluster_size() {
   return r;
 }
 
+// Thread blocks per SM: as many as have room for their ring in shared memory.  Three
+// stages on their way in each keep HBM busy while some of the blocks begin or end a row.
 template <typename T, bool kTop>
-__global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsParams<T> p) {
+__global__ void __launch_bounds__(kThreads, kTop ? 3 : 4) token_stats_kernel(const StatsParams<T> p) {
   using E = Elt<T>;
-  constexpr int EPV = E::kPerVec, U = E::kUnroll;
-  extern __shared__ char s_dyn[];
-  TopShared& top = *reinterpret_cast<TopShared*>(s_dyn);
+  constexpr int EPV = E::kPerVec, U = kBatch;
+  extern __shared__ __align__(128) char s_dyn[];
+  TopShared& top = *reinterpret_cast<TopShared*>(s_dyn + kStages * kStageBytes);
   __shared__ StatsShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
@@ -374,23 +400,64 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
   part.a = min(part.v0 + (int64_t)(((16u - phase) & 15u) / sizeof(T)), part.v1);
   part.nvec = (int)((part.v1 - part.a) / EPV);
   part.b = part.a + (int64_t)part.nvec * EPV;
-  const int batches = (part.nvec + kThreads * U - 1) / (kThreads * U);
+  const int batches = (part.nvec + kStageVecs - 1) / kStageVecs;
   part.per = (batches + kSlots - 2) / (kSlots - 1);
   part.groups = part.per > 0 ? (batches + part.per - 1) / part.per : 0;
 
+  // batch b goes through stage b % kStages; thread 0 orders the copies
+  const uint32_t ring = smem_u32(s_dyn), full = smem_u32(sh.full), empty = smem_u32(sh.empty);
+  const char* source = reinterpret_cast<const char*>(part.z + part.a);
+  const auto order = [&](int b) {
+    const int st = b % kStages;
+    const uint32_t bytes = 16u * (uint32_t)min(kStageVecs, part.nvec - b * kStageVecs);
+    mbar_arrive_expect_tx(full + 8 * st, bytes);
+    bulk_g2s(ring + st * kStageBytes, source + (int64_t)b * kStageBytes, bytes, full + 8 * st);
+  };
+  int ordered = 0;  // (thread 0's)
+  if (tid == 0) {
+    sh.abort = 0;
+    for (int k = 0; k < kStages; ++k) {
+      mbar_init(full + 8 * k, 1);
+      mbar_init(empty + 8 * k, kWarps);
+    }
+    mbar_init_fence();
+    for (; ordered < min(kStages, batches); ++ordered) order(ordered);
+  }
+  __syncthreads();
   Sums sum;
   const uint64_t c2 = f2_pack(c, c);
-  const uint4* vec = reinterpret_cast<const uint4*>(part.z + part.a);
-  int k0 = tid;
+  int batch = 0;
   for (int g = 0; g < part.groups; ++g) {
     float group_max = -INFINITY;
-    for (int q = 0; q < part.per; ++q, k0 += kThreads * U) {
+    for (int q = 0; q < part.per && batch < batches; ++q, ++batch) {
+      const int st = batch % kStages;
+      if (!mbar_wait(full + 8 * st, batch / kStages & 1)) {
+        *(volatile int*)&sh.abort = 1;
+        batch = batches;
+        break;
+      }
+      const int n = min(kStageVecs, part.nvec - batch * kStageVecs);
       uint4 d[U];
+      if (n == kStageVecs) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = k0 + u * kThreads;
-        d[u] = k < part.nvec ? ld_stream(vec + k)
-                             : make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf);
+        for (int u = 0; u < U; ++u)
+          d[u] = ld_shared_v4(ring + st * kStageBytes + 16 * (tid + u * kThreads));
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          d[u] = make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf);
+          if (tid + u * kThreads < n)
+            d[u] = ld_shared_v4(ring + st * kStageBytes + 16 * (tid + u * kThreads));
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + 8 * st);
+      // the stage of the batch before this one is free once every warp has read it
+      if (tid == 0 && batch >= 1 && batch - 1 + kStages < batches) {
+        if (mbar_wait(empty + 8 * ((batch - 1) % kStages), (batch - 1) / kStages & 1))
+          order(ordered++);
+        else
+          *(volatile int*)&sh.abort = 1;  // (nothing more arrives: every wait ends)
       }
       const float largest = E::template batch_max<U>(d);
       group_max = fmaxf(group_max, largest);
@@ -398,10 +465,10 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
       const uint64_t nref = f2_pack(-sum.ref, -sum.ref);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        float x[EPV];
-        E::unpack(d[u], x);
+        uint64_t x[EPV / 2];
+        pairs_of(d[u], x, T());
 #pragma unroll
-        for (int e = 0; e < EPV; e += 2) sum.add(f2_pack(x[e], x[e + 1]), nref, c2);
+        for (int e = 0; e < EPV / 2; ++e) sum.add(x[e], nref, c2);
       }
     }
     sum.top = fmaxf(sum.top, group_max);
@@ -452,12 +519,19 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
     s += sh.warp_sum[w].x;
     e += sh.warp_sum[w].y;
   }
+  if (sh.abort != 0) {  // some of the row is missing: no distribution, and the reason
+    s = NAN;
+    flags |= kFlagTimeout;
+    if (tid == 0)  // (what may still be on its way)
+      for (int b = max(0, ordered - kStages); b < ordered; ++b)
+        mbar_wait(full + 8 * (b % kStages), b / kStages & 1);
+  }
   if (parts > 1) {
     if (kTop) best_of_part(top, part, sum.top, p.top);
     __syncwarp();  // (the cluster's barriers want whole warps)
     cluster_wait();
     if (tid == 0)
-      st_cluster_f32x4(map_to_rank(smem_u32(&sh.part[rank]), 0), make_float4(m, s, e, 0.f));
+      st_cluster_f32x4(map_to_rank(smem_u32(&sh.part[rank]), 0), make_float4(m, s, e, sh.abort != 0 ? 1.f : 0.f));
     if (kTop && tid < kMaxTop)
       st_cluster_u64(map_to_rank(smem_u32(&top.part_key[rank][tid]), 0), top.key[tid]);
     __syncwarp();
@@ -472,6 +546,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
       const float d = fmaxf((q.x - m) * c, kLowest), f = ex2(d);
       s += f * q.y;
       e += f * fmaf(d, q.y, q.z);
+      if (q.w != 0.f) flags |= kFlagTimeout;
     }
   }
   // (a comparison with NaN is false)
@@ -698,10 +773,12 @@ cudaError_t stats_run(const TokenStatsArgs& a, const DeviceInfo& d, cudaStream_t
   constexpr int EPV = Elt<T>::kPerVec;
   p.chunk = ((a.V + split - 1) / split + EPV - 1) / EPV * EPV;
   const dim3 grid((unsigned)(rows < 1 ? split : rows * split));
-  if (a.top == 0)
-    return launch_pdl(token_stats_kernel<T, false>, grid, dim3(kThreads), 0, st, split, p);
-  return launch_pdl(token_stats_kernel<T, true>, grid, dim3(kThreads), sizeof(TopShared), st,
-                    split, p);
+  constexpr int kRing = kStages * kStageBytes;
+  const int smem = a.top == 0 ? kRing : kRing + (int)sizeof(TopShared);
+  const auto kern = a.top == 0 ? token_stats_kernel<T, false> : token_stats_kernel<T, true>;
+  const cudaError_t e = ensure_dynamic_smem((const void*)kern, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, grid, dim3(kThreads), smem, st, split, p);
 }
 
 template <typename T>
