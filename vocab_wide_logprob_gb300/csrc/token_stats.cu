@@ -84,7 +84,7 @@ constexpr int kBatch = 4;       // vectors of 16 bytes that a thread takes at on
 constexpr int kStageVecs = kBatch * kThreads;
 constexpr int kStageBytes = 16 * kStageVecs;
 constexpr int kStages = 3;      // of the ring that bulk copies fill
-constexpr int kSlots = 16;      // groups of a thread whose maxima are kept, the last for a ragged end
+constexpr int kSlots = 8;       // groups of a thread whose maxima are kept, the last for a ragged end
 constexpr int kCandidates = 512;
 constexpr int kHits = 256;
 
@@ -141,22 +141,22 @@ struct StatsShared {
   float2 warp_sum[kWarps];
   float4 part[kMaxSplit];  // of the cluster's CTAs, in the first one: m, S, E, whether it gave up
 };
+// What the choice of the alternatives keeps in shared memory; `Late` lies over the ring,
+// which is free by then.
 struct TopShared {
-  uint64_t part_key[kMaxSplit][kMaxTop];  // likewise: their best keys, sorted
-
-  float slot[kSlots][kThreads];
-  alignas(16) float quad[64];
-  uint64_t key[kCandidates];
-  int hit[kHits];
+  uint64_t part_key[kMaxSplit][kMaxTop];  // of the cluster's CTAs, in the first one: best keys, sorted
+  alignas(16) float quad[64];             // maxima of sets of four threads
   float bound;
   int hits, keys, ties;
 };
+struct Late {
+  uint64_t key[kCandidates];
+  int hit[kHits];
+};
 
-// Whether a vector's elements are worth a look, and those that are: above the
-// bound, or (ties) equal to it.
-__device__ __forceinline__ void push_key(TopShared& sh, float x, int64_t v) {
+__device__ __forceinline__ void push_key(TopShared& sh, Late& late, float x, int64_t v) {
   const int at = atomicAdd(&sh.keys, 1);
-  if (at < kCandidates) sh.key[at] = key_of(x, v);
+  if (at < kCandidates) late.key[at] = key_of(x, v);
 }
 
 template <typename T>
@@ -167,105 +167,113 @@ struct Part {  // elements [v0, v1) of a row; vectors of 16 bytes in [a, b)
   int groups, per;  // groups of `per` batches of U vectors
 };
 
-// The best `top` of the part's elements (all of them if it has fewer), as keys in
-// sh.key[0 ..) sorted, zeros behind them.  Called by the whole CTA after the stream;
-// `own_max` is the thread's largest element.
-template <typename T>
-__device__ void best_of_part(TopShared& sh, const Part<T>& p, float own_max, int top) {
+// A logit's own bits, from its float, and back.
+__device__ __forceinline__ float bits_of(float x, float) { return x; }
+__device__ __forceinline__ uint16_t bits_of(float x, uint16_t) {
+  return (uint16_t)(__float_as_uint(x) >> 16);
+}
+__device__ __forceinline__ float value_of(float x) { return x; }
+__device__ __forceinline__ float value_of(uint16_t x) { return bf16_bits_to_float(x); }
+
+// The bound: the top-th largest of the 64 sets' maxima, lower sets first.  By the first
+// 64 threads, behind a barrier; another one makes it known.
+__device__ __forceinline__ void find_bound(TopShared& sh, int top) {
+  const int tid = threadIdx.x;
+  if (tid >= 64) return;
+  const float mine = sh.quad[tid];
+  int before = 0;
+#pragma unroll 4
+  for (int k = 0; k < 64; k += 4) {
+    const float4 x = *reinterpret_cast<const float4*>(&sh.quad[k]);
+    before += (x.x > mine || (x.x == mine && k < tid)) + (x.y > mine || (x.y == mine && k + 1 < tid)) +
+              (x.z > mine || (x.z == mine && k + 2 < tid)) +
+              (x.w > mine || (x.w == mine && k + 3 < tid));
+  }
+  if (before == top - 1) sh.bound = mine;
+}
+
+// The best `top` of the part's elements (all of them if it has fewer): emit(place, key)
+// for each, by the thread that found it.  Called by the whole CTA after the stream, with
+// the bound known.  slot[g][thread]: maxima of groups.
+template <typename T, typename Emit>
+__device__ __forceinline__ void best_of_part(TopShared& sh, Late& late, const T (*slot)[kThreads],
+                                             const Part<T>& p, int top, Emit emit) {
   using E = Elt<T>;
   constexpr int EPV = E::kPerVec, U = kBatch;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t n = p.v1 - p.v0;
-  __shared__ uint64_t s_sorted[kMaxTop];
-  if (tid == 0) sh.hits = sh.keys = sh.ties = 0;
   bool listed = false;
   if (n <= kCandidates) {
-    __syncthreads();
-    for (int64_t v = tid; v < n; v += kThreads) sh.key[v] = key_of(E::load1(p.z + p.v0 + v), p.v0 + v);
+    for (int64_t v = tid; v < n; v += kThreads) late.key[v] = key_of(E::load1(p.z + p.v0 + v), p.v0 + v);
     if (tid == 0) sh.keys = (int)n;
     __syncthreads();
     listed = true;
-  } else {
-    float q = fmaxf(own_max, __shfl_xor_sync(0xffffffffu, own_max, 1));
-    q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 2));
-    if (lane % 4 == 0) sh.quad[tid / 4] = q;
-    __syncthreads();
-    if (tid < 64) {
-      // the top-th largest of the 64, lower indices first
-      const float mine = sh.quad[tid];
-      int before = 0;
-#pragma unroll 4
-      for (int k = 0; k < 64; k += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(&sh.quad[k]);
-        before += (x.x > mine || (x.x == mine && k < tid)) +
-                  (x.y > mine || (x.y == mine && k + 1 < tid)) +
-                  (x.z > mine || (x.z == mine && k + 2 < tid)) +
-                  (x.w > mine || (x.w == mine && k + 3 < tid));
+  }
+  const float bound = sh.bound;
+  // with the ties at the bound, or (where they are too many) without them
+#pragma unroll 1
+  for (int strict = 0; strict < 2 && !listed; ++strict) {
+#pragma unroll 1
+    for (int g = 0; g <= p.groups; ++g) {
+      const float x = value_of(slot[g][tid]);
+      if (strict ? x > bound : x >= bound) {
+        const int at = atomicAdd(&sh.hits, 1);
+        if (at < kHits) late.hit[at] = g * kThreads + tid;
       }
-      if (before == top - 1) sh.bound = mine;
     }
     __syncthreads();
-    const float bound = sh.bound;
-    // with the ties at the bound, or (where they are too many) without them
-    for (int strict = 0; strict < 2 && !listed; ++strict) {
-      for (int g = 0; g <= p.groups; ++g) {
-        const float x = sh.slot[g][tid];
-        if (strict ? x > bound : x >= bound) {
-          const int at = atomicAdd(&sh.hits, 1);
-          if (at < kHits) sh.hit[at] = g * kThreads + tid;
-        }
-      }
-      __syncthreads();
-      const int hits = sh.hits;
-      if (hits <= kHits) {
-        const int each = p.per * U;
-        for (int w = tid; w < hits * each; w += kThreads) {
-          const int h = sh.hit[w / each], t = h % kThreads, g = h / kThreads;
-          if (g == p.groups) {  // a ragged end's element
-            if (w % each == 0) {
-              const int64_t v = t < 32 ? p.v0 + t : p.b + t - 32;
-              push_key(sh, E::load1(p.z + v), v);
-            }
-            continue;
+    const int hits = sh.hits;
+    if (hits <= kHits) {
+      const int each = p.per * U;
+#pragma unroll 1
+      for (int w = tid; w < hits * each; w += kThreads) {
+        const int h = late.hit[w / each], t = h % kThreads, g = h / kThreads;
+        if (g == p.groups) {  // a ragged end's element
+          if (w % each == 0) {
+            const int64_t v = t < 32 ? p.v0 + t : p.b + t - 32;
+            push_key(sh, late, E::load1(p.z + v), v);
           }
-          const int k = (g * each + w % each) * kThreads + t;
-          if (k >= p.nvec) continue;
-          float x[EPV];
-          E::unpack(ld_stream(p.z + p.a + (int64_t)k * EPV), x);
+          continue;
+        }
+        const int k = (g * each + w % each) * kThreads + t;
+        if (k >= p.nvec) continue;
+        float x[EPV];
+        E::unpack(ld_stream(p.z + p.a + (int64_t)k * EPV), x);
 #pragma unroll
-          for (int e = 0; e < EPV; ++e)
-            if (strict ? x[e] > bound : x[e] >= bound) push_key(sh, x[e], p.a + (int64_t)k * EPV + e);
-        }
+        for (int e = 0; e < EPV; ++e)
+          if (strict ? x[e] > bound : x[e] >= bound)
+            push_key(sh, late, x[e], p.a + (int64_t)k * EPV + e);
       }
+    }
+    __syncthreads();
+    const int have = sh.keys;
+    listed = hits <= kHits && have <= kCandidates - (strict ? kMaxTop : 0);
+    if (listed && (!strict || have >= top)) break;
+    __syncthreads();
+    if (!listed) {
+      if (tid == 0) sh.hits = sh.keys = 0;
       __syncthreads();
-      listed = hits <= kHits && sh.keys <= kCandidates - (strict ? kMaxTop : 0);
-      const int have = sh.keys;
-      __syncthreads();
-      if (!listed) {
-        if (tid == 0) sh.hits = sh.keys = 0;
+    } else {
+      // the first ties in the order of their ids
+      for (int64_t at = p.v0; at < p.v1; at += kThreads) {
+        const int64_t v = at + tid;
+        const bool tie = v < p.v1 && E::load1(p.z + v) == bound;
+        const uint32_t votes = __ballot_sync(0xffffffffu, tie);
+        if (lane == 0) late.hit[warp] = __popc(votes);
         __syncthreads();
-      } else if (strict && have < top) {
-        // the first ties in the order of their ids
-        for (int64_t at = p.v0; at < p.v1; at += kThreads) {
-          const int64_t v = at + tid;
-          const bool tie = v < p.v1 && E::load1(p.z + v) == bound;
-          const uint32_t votes = __ballot_sync(0xffffffffu, tie);
-          if (lane == 0) sh.hit[warp] = __popc(votes);
-          __syncthreads();
-          int before = sh.ties, all = sh.ties;
-          for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) before += sh.hit[w];
-            all += sh.hit[w];
-          }
-          before += __popc(votes & ((1u << lane) - 1));
-          if (tie && have + before < top) sh.key[have + before] = key_of(bound, v);
-          __syncthreads();
-          if (tid == 0) sh.ties = all;
-          if (have + all >= top) break;
+        int before = sh.ties, all = sh.ties;
+        for (int w = 0; w < kWarps; ++w) {
+          if (w < warp) before += late.hit[w];
+          all += late.hit[w];
         }
-        if (tid == 0) sh.keys = top;
+        before += __popc(votes & ((1u << lane) - 1));
+        if (tie && have + before < top) late.key[have + before] = key_of(bound, v);
         __syncthreads();
+        if (tid == 0) sh.ties = all;
+        if (have + all >= top) break;
       }
+      if (tid == 0) sh.keys = top;
+      __syncthreads();
     }
   }
   if (!listed) {
@@ -285,53 +293,42 @@ __device__ void best_of_part(TopShared& sh, const Part<T>& p, float own_max, int
         last = __shfl_sync(0xffffffffu, mine, top - 1);
       }
     }
-    sh.key[tid] = mine;
+    late.key[tid] = mine;
     if (tid == 0) sh.keys = kThreads;
     __syncthreads();
   }
-  // sorted by counting the keys before each (they are all different, but for
-  // the zeros of empty lanes)
+  // the place of a key is the number of keys before it (they are all different, but
+  // for the zeros of empty lanes)
   const int have = sh.keys;
-  uint64_t mine[kCandidates / kThreads];
-  int rank[kCandidates / kThreads];
-#pragma unroll
-  for (int u = 0; u < kCandidates / kThreads; ++u) {
-    const int k = tid + u * kThreads;
-    mine[u] = k < have ? sh.key[k] : 0;
-    rank[u] = kMaxTop;
-    if (mine[u] != 0) {
-      rank[u] = 0;
-      for (int j = 0; j < have; ++j) rank[u] += sh.key[j] > mine[u];
-    }
+#pragma unroll 1
+  for (int k = tid; k < have; k += kThreads) {
+    const uint64_t mine = late.key[k];
+    if (mine == 0) continue;
+    int place = 0;
+    for (int j = 0; j < have; ++j) place += late.key[j] > mine;
+    if (place < top) emit(place, mine);
   }
-#pragma unroll
-  for (int u = 0; u < kCandidates / kThreads; ++u)
-    if (rank[u] < top) s_sorted[rank[u]] = mine[u];
-  __syncthreads();
-  const int got = (int)min(n, (int64_t)top);
-  if (tid < kMaxTop) sh.key[tid] = tid < got ? s_sorted[tid] : 0;
-  __syncthreads();
 }
 
-// The best `top` of the cluster's sorted lists, in sh.key[0 .. top): a key comes
-// behind those before it in its own list and the larger ones of every other.
-__device__ __forceinline__ void merge_parts(TopShared& sh, int parts, int top) {
+// The best `top` of the cluster's sorted lists: a key comes behind those before it in
+// its own list and the larger ones of every other.
+template <typename Emit>
+__device__ __forceinline__ void merge_parts(const TopShared& sh, int parts, int top, Emit emit) {
   const int list = threadIdx.x / kMaxTop, at = threadIdx.x % kMaxTop;
   const uint64_t mine = list < parts && at < top ? sh.part_key[list][at] : 0;
-  if (mine != 0) {
-    int rank = at;
-    for (int other = 0; other < parts; ++other) {
-      if (other == list) continue;
-      int lo = 0;  // keys of the other list that are larger
+  if (mine == 0) return;
+  int place = at;
+#pragma unroll 1
+  for (int other = 0; other < parts; ++other) {
+    if (other == list) continue;
+    int lo = 0;  // keys of the other list that are larger
 #pragma unroll
-      for (int step = kMaxTop / 2; step > 0; step /= 2)
-        if (sh.part_key[other][lo + step - 1] > mine) lo += step;
-      if (sh.part_key[other][lo] > mine) ++lo;
-      rank += lo;
-    }
-    if (rank < top) sh.key[rank] = mine;
+    for (int step = kMaxTop / 2; step > 0; step /= 2)
+      if (sh.part_key[other][lo + step - 1] > mine) lo += step;
+    if (sh.part_key[other][lo] > mine) ++lo;
+    place += lo;
   }
-  __syncthreads();
+  if (place < top) emit(place, mine);
 }
 
 __device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
@@ -346,12 +343,14 @@ __device__ __forceinline__ uint32_t cluster_size() {
 // Thread blocks per SM: as many as have room for their ring in shared memory.  Three
 // stages on their way in each keep HBM busy while some of the blocks begin or end a row.
 template <typename T, bool kTop>
-__global__ void __launch_bounds__(kThreads, kTop ? 3 : 4) token_stats_kernel(const StatsParams<T> p) {
+__global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsParams<T> p) {
   using E = Elt<T>;
   constexpr int EPV = E::kPerVec, U = kBatch;
   extern __shared__ __align__(128) char s_dyn[];
-  TopShared& top = *reinterpret_cast<TopShared*>(s_dyn + kStages * kStageBytes);
+  Late& late = *reinterpret_cast<Late*>(s_dyn);
+  T(*slot)[kThreads] = reinterpret_cast<T(*)[kThreads]>(s_dyn + kStages * kStageBytes);
   __shared__ StatsShared sh;
+  __shared__ TopShared top;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
@@ -472,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, kTop ? 3 : 4) token_stats_kernel(con
       }
     }
     sum.top = fmaxf(sum.top, group_max);
-    if (kTop) top.slot[g][tid] = group_max;
+    if (kTop) slot[g][tid] = bits_of(group_max, T());
   }
   {  // a ragged end's element
     int64_t v = -1;
@@ -487,13 +486,20 @@ __global__ void __launch_bounds__(kThreads, kTop ? 3 : 4) token_stats_kernel(con
       sum.top = fmaxf(sum.top, x);
       sum.add(f2_pack(x, -INFINITY), f2_pack(-sum.ref, -sum.ref), c2);
     }
-    if (kTop) top.slot[part.groups][tid] = v >= 0 ? x : NAN;
+    if (kTop) slot[part.groups][tid] = v >= 0 ? bits_of(x, T()) : bits_of(NAN, T());
   }
   // the row's maximum, then its sums relative to it
   float m = sum.top;
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) sh.warp_max[warp] = m;
+  if (kTop) {
+    float q = fmaxf(sum.top, __shfl_xor_sync(0xffffffffu, sum.top, 1));
+    q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, 2));
+    if (lane % 4 == 0) top.quad[tid / 4] = q;
+    if (tid == 0) top.hits = top.keys = top.ties = 0;
+  }
   __syncthreads();
+  if (kTop) find_bound(top, p.top);
   m = sh.warp_max[0];
 #pragma unroll
   for (int w = 1; w < kWarps; ++w) m = fmaxf(m, sh.warp_max[w]);
@@ -527,13 +533,18 @@ __global__ void __launch_bounds__(kThreads, kTop ? 3 : 4) token_stats_kernel(con
         mbar_wait(full + 8 * (b % kStages), b / kStages & 1);
   }
   if (parts > 1) {
-    if (kTop) best_of_part(top, part, sum.top, p.top);
     __syncwarp();  // (the cluster's barriers want whole warps)
     cluster_wait();
+    if (kTop) {
+      const int got = sh.abort != 0 ? 0 : (int)min(part.v1 - part.v0, (int64_t)p.top);
+      const uint32_t to = map_to_rank(smem_u32(&top.part_key[rank][0]), 0);
+      if (got > 0)
+        best_of_part(top, late, slot, part, p.top,
+                     [&](int place, uint64_t key) { st_cluster_u64(to + 8 * place, key); });
+      if (tid >= got && tid < kMaxTop) st_cluster_u64(to + 8 * tid, 0);
+    }
     if (tid == 0)
       st_cluster_f32x4(map_to_rank(smem_u32(&sh.part[rank]), 0), make_float4(m, s, e, sh.abort != 0 ? 1.f : 0.f));
-    if (kTop && tid < kMaxTop)
-      st_cluster_u64(map_to_rank(smem_u32(&top.part_key[rank][tid]), 0), top.key[tid]);
     __syncwarp();
     cluster_sync();
     if (rank != 0) return;
@@ -571,15 +582,14 @@ __global__ void __launch_bounds__(kThreads, kTop ? 3 : 4) token_stats_kernel(con
     }
     return;
   }
+  const auto write = [&](int place, uint64_t key) {
+    p.top_tokens[r * p.top + place] = key_id(key);
+    p.top_logp[r * p.top + place] = (key_value(key) - m) / Ti - L;
+  };
   if (parts > 1)
-    merge_parts(top, (int)parts, p.top);
+    merge_parts(top, (int)parts, p.top, write);
   else
-    best_of_part(top, part, sum.top, p.top);
-  if (tid < p.top) {
-    const uint64_t k = top.key[tid];
-    p.top_tokens[r * p.top + tid] = key_id(k);
-    p.top_logp[r * p.top + tid] = (key_value(k) - m) / Ti - L;
-  }
+    best_of_part(top, late, slot, part, p.top, write);
 }
 
 // ---------------------------------------------------------------------------
@@ -774,7 +784,7 @@ cudaError_t stats_run(const TokenStatsArgs& a, const DeviceInfo& d, cudaStream_t
   p.chunk = ((a.V + split - 1) / split + EPV - 1) / EPV * EPV;
   const dim3 grid((unsigned)(rows < 1 ? split : rows * split));
   constexpr int kRing = kStages * kStageBytes;
-  const int smem = a.top == 0 ? kRing : kRing + (int)sizeof(TopShared);
+  const int smem = a.top == 0 ? kRing : kRing + kSlots * kThreads * (int)sizeof(T);
   const auto kern = a.top == 0 ? token_stats_kernel<T, false> : token_stats_kernel<T, true>;
   const cudaError_t e = ensure_dynamic_smem((const void*)kern, smem);
   if (e != cudaSuccess) return e;
