@@ -175,20 +175,22 @@ __device__ __forceinline__ uint16_t bits_of(float x, uint16_t) {
 __device__ __forceinline__ float value_of(float x) { return x; }
 __device__ __forceinline__ float value_of(uint16_t x) { return bf16_bits_to_float(x); }
 
-// The bound: the top-th largest of the 64 sets' maxima, lower sets first.  By the first
-// 64 threads, behind a barrier; another one makes it known.
+// The bound: the top-th largest of the 64 sets' maxima, lower sets first; four threads
+// count what is before one.  Between two barriers.
 __device__ __forceinline__ void find_bound(TopShared& sh, int top) {
-  const int tid = threadIdx.x;
-  if (tid >= 64) return;
-  const float mine = sh.quad[tid];
+  const int set = threadIdx.x / 4, quarter = threadIdx.x % 4 * 16;
+  const float mine = sh.quad[set];
   int before = 0;
-#pragma unroll 4
-  for (int k = 0; k < 64; k += 4) {
-    const float4 x = *reinterpret_cast<const float4*>(&sh.quad[k]);
-    before += (x.x > mine || (x.x == mine && k < tid)) + (x.y > mine || (x.y == mine && k + 1 < tid)) +
-              (x.z > mine || (x.z == mine && k + 2 < tid)) +
-              (x.w > mine || (x.w == mine && k + 3 < tid));
+#pragma unroll
+  for (int k = 0; k < 16; k += 4) {
+    const float4 x = *reinterpret_cast<const float4*>(&sh.quad[quarter + k]);
+    const int at = quarter + k;
+    before += (x.x > mine || (x.x == mine && at < set)) + (x.y > mine || (x.y == mine && at + 1 < set)) +
+              (x.z > mine || (x.z == mine && at + 2 < set)) +
+              (x.w > mine || (x.w == mine && at + 3 < set));
   }
+  before += __shfl_xor_sync(0xffffffffu, before, 1);
+  before += __shfl_xor_sync(0xffffffffu, before, 2);
   if (before == top - 1) sh.bound = mine;
 }
 
@@ -213,36 +215,59 @@ __device__ __forceinline__ void best_of_part(TopShared& sh, Late& late, const T 
   // with the ties at the bound, or (where they are too many) without them
 #pragma unroll 1
   for (int strict = 0; strict < 2 && !listed; ++strict) {
-#pragma unroll 1
-    for (int g = 0; g <= p.groups; ++g) {
-      const float x = value_of(slot[g][tid]);
-      if (strict ? x > bound : x >= bound) {
-        const int at = atomicAdd(&sh.hits, 1);
-        if (at < kHits) late.hit[at] = g * kThreads + tid;
+    uint32_t votes[kSlots];
+    int mine = 0;
+#pragma unroll
+    for (int g = 0; g < kSlots; ++g) {
+      const float x = g <= p.groups ? value_of(slot[g][tid]) : NAN;
+      votes[g] = __ballot_sync(0xffffffffu, strict ? x > bound : x >= bound);
+      mine += __popc(votes[g]);
+    }
+    if (mine > 0) {  // (one addition a warp)
+      int at = 0;
+      if (lane == 0) at = atomicAdd(&sh.hits, mine);
+      at = __shfl_sync(0xffffffffu, at, 0);
+#pragma unroll
+      for (int g = 0; g < kSlots; ++g) {
+        const int k = at + __popc(votes[g] & ((1u << lane) - 1));
+        if ((votes[g] >> lane & 1) && k < kHits) late.hit[k] = g * kThreads + tid;
+        at += __popc(votes[g]);
       }
     }
     __syncthreads();
     const int hits = sh.hits;
     if (hits <= kHits) {
-      const int each = p.per * U;
+      const unsigned each = (unsigned)p.per * U, items = (unsigned)hits * each;
+      constexpr int kAhead = 2;
 #pragma unroll 1
-      for (int w = tid; w < hits * each; w += kThreads) {
-        const int h = late.hit[w / each], t = h % kThreads, g = h / kThreads;
-        if (g == p.groups) {  // a ragged end's element
-          if (w % each == 0) {
-            const int64_t v = t < 32 ? p.v0 + t : p.b + t - 32;
-            push_key(sh, late, E::load1(p.z + v), v);
-          }
-          continue;
-        }
-        const int k = (g * each + w % each) * kThreads + t;
-        if (k >= p.nvec) continue;
-        float x[EPV];
-        E::unpack(ld_stream(p.z + p.a + (int64_t)k * EPV), x);
+      for (unsigned w0 = tid; w0 < items; w0 += kAhead * kThreads) {
+        uint4 d[kAhead];
+        int at[kAhead];  // the vector, or none
 #pragma unroll
-        for (int e = 0; e < EPV; ++e)
-          if (strict ? x[e] > bound : x[e] >= bound)
-            push_key(sh, late, x[e], p.a + (int64_t)k * EPV + e);
+        for (int u = 0; u < kAhead; ++u) {
+          const unsigned w = w0 + u * kThreads, q = w / each, rest = w - q * each;
+          at[u] = INT32_MAX;
+          if (w < items) {
+            const int h = late.hit[q], t = h % kThreads, g = h / kThreads;
+            if (g < p.groups) {
+              at[u] = (g * (int)each + (int)rest) * kThreads + t;
+            } else if (rest == 0) {  // a ragged end's element
+              const int64_t v = t < 32 ? p.v0 + t : p.b + t - 32;
+              push_key(sh, late, E::load1(p.z + v), v);
+            }
+          }
+          if (at[u] < p.nvec) d[u] = ld_stream(p.z + p.a + (int64_t)at[u] * EPV);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          if (at[u] >= p.nvec) continue;
+          float x[EPV];
+          E::unpack(d[u], x);
+#pragma unroll
+          for (int e = 0; e < EPV; ++e)
+            if (strict ? x[e] > bound : x[e] >= bound)
+              push_key(sh, late, x[e], p.a + (int64_t)at[u] * EPV + e);
+        }
       }
     }
     __syncthreads();
@@ -298,36 +323,39 @@ __device__ __forceinline__ void best_of_part(TopShared& sh, Late& late, const T 
     __syncthreads();
   }
   // the place of a key is the number of keys before it (they are all different, but
-  // for the zeros of empty lanes)
+  // for the zeros of empty lanes); eight threads count for one
   const int have = sh.keys;
 #pragma unroll 1
-  for (int k = tid; k < have; k += kThreads) {
-    const uint64_t mine = late.key[k];
-    if (mine == 0) continue;
+  for (int k0 = 0; k0 < have; k0 += kThreads / 8) {
+    const int k = k0 + tid / 8;
+    const uint64_t mine = k < have ? late.key[k] : 0;
     int place = 0;
-    for (int j = 0; j < have; ++j) place += late.key[j] > mine;
-    if (place < top) emit(place, mine);
+#pragma unroll 4
+    for (int j = tid % 8; j < have; j += 8) place += late.key[j] > mine;
+    place += __shfl_xor_sync(0xffffffffu, place, 1);
+    place += __shfl_xor_sync(0xffffffffu, place, 2);
+    place += __shfl_xor_sync(0xffffffffu, place, 4);
+    if (tid % 8 == 0 && mine != 0 && place < top) emit(place, mine);
   }
 }
 
-// The best `top` of the cluster's sorted lists: a key comes behind those before it in
-// its own list and the larger ones of every other.
+// The best `top` of the cluster's sorted lists: a key comes behind the larger ones of
+// every list, its own too.
 template <typename Emit>
 __device__ __forceinline__ void merge_parts(const TopShared& sh, int parts, int top, Emit emit) {
   const int list = threadIdx.x / kMaxTop, at = threadIdx.x % kMaxTop;
   const uint64_t mine = list < parts && at < top ? sh.part_key[list][at] : 0;
   if (mine == 0) return;
-  int place = at;
-#pragma unroll 1
-  for (int other = 0; other < parts; ++other) {
-    if (other == list) continue;
-    int lo = 0;  // keys of the other list that are larger
+  int lo[kMaxSplit] = {};  // keys of every list that are larger
 #pragma unroll
-    for (int step = kMaxTop / 2; step > 0; step /= 2)
-      if (sh.part_key[other][lo + step - 1] > mine) lo += step;
-    if (sh.part_key[other][lo] > mine) ++lo;
-    place += lo;
-  }
+  for (int step = kMaxTop / 2; step > 0; step /= 2)
+#pragma unroll
+    for (int other = 0; other < kMaxSplit; ++other)
+      if (other < parts && sh.part_key[other][lo[other] + step - 1] > mine) lo[other] += step;
+  int place = 0;
+#pragma unroll
+  for (int other = 0; other < kMaxSplit; ++other)
+    if (other < parts) place += lo[other] + (sh.part_key[other][lo[other]] > mine);
   if (place < top) emit(place, mine);
 }
 
@@ -388,13 +416,6 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
   part.v0 = min(p.V, rank * p.chunk);
   part.v1 = min(p.V, part.v0 + p.chunk);
   if (parts > 1) cluster_arrive_relaxed();  // (the first CTA runs before it is written to)
-  // the token's logit, in time for the end
-  int64_t y = -1;
-  float zy = 0.f;
-  if (rank == 0 && tid == 0) {
-    y = __ldg(p.tokens + i * p.token_seq + j);
-    if (y >= 0 && y < p.V) zy = E::load1(part.z + y);
-  }
   const unsigned phase = (unsigned)(reinterpret_cast<uintptr_t>(part.z + part.v0) & 15u);
   part.a = min(part.v0 + (int64_t)(((16u - phase) & 15u) / sizeof(T)), part.v1);
   part.nvec = (int)((part.v1 - part.a) / EPV);
@@ -422,6 +443,8 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
     mbar_init_fence();
     for (; ordered < min(kStages, batches); ++ordered) order(ordered);
   }
+  // (used behind the stream)
+  const int64_t y = rank == 0 && tid == 0 ? __ldg(p.tokens + i * p.token_seq + j) : -1;
   __syncthreads();
   Sums sum;
   const uint64_t c2 = f2_pack(c, c);
@@ -473,6 +496,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
     sum.top = fmaxf(sum.top, group_max);
     if (kTop) slot[g][tid] = bits_of(group_max, T());
   }
+  const float at_token = y >= 0 && y < p.V ? E::load1(part.z + y) : 0.f;
   {  // a ragged end's element
     int64_t v = -1;
     if (tid < part.a - part.v0)
@@ -568,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
       flags |= kFlagValue;
     else if (y < 0 || y >= p.V)
       flags |= kFlagTokenRange;
-    p.logp[r] = defined && y >= 0 && y < p.V ? (zy - m) / Ti - L : NAN;
+    p.logp[r] = defined && y >= 0 && y < p.V ? (at_token - m) / Ti - L : NAN;
     p.entropy[r] = defined ? L - kLn2 * (e / s) : NAN;
     p.norm[2 * r] = defined ? m : NAN;
     p.norm[2 * r + 1] = defined ? L : NAN;
