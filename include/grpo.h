@@ -618,7 +618,7 @@ grpo_status grpo_verify_drafts(const void *target_logits, const void *draft_logi
  * logits: row j of sequence i starts at element i * logits_seq + j *
  * logits_row (rows of [N, P+C, V] logits: logits + (P-1) * V, logits_seq =
  * (P+C) * V), `dtype`, aligned to its element; tokens: row j of sequence i at
- * i * token_seq + j, int64.  logp, entropy [N, R], norm [N, R, 2] float32;
+ * i * token_seq + j, int64.  logp, entropy [N, R], norm [N, R, 2] float32 (8-byte aligned);
  * top_tokens [N, R, top] int64, top_logp [N, R, top] float32 (NULL with top
  * 0).  0 <= top <= 32, top <= V; N * R <= 2^26, V < 2^31 - 2^16.  The outputs and the
  * workspace overlap neither one another nor an input.

@@ -1227,7 +1227,7 @@ grpo_status grpo_token_stats(const void* logits, grpo_dtype dtype, int64_t N, in
     if (top > 0 && (top_tokens == nullptr || top_logp == nullptr)) return GRPO_ERR_INVALID_ARG;
   }
   if (!aligned(logits, esize_of(dtype)) || !aligned(tokens, 8) || !aligned(len, 4) ||
-      !aligned(temperature, 4) || !aligned(logp, 4) || !aligned(entropy, 4) || !aligned(norm, 4) ||
+      !aligned(temperature, 4) || !aligned(logp, 4) || !aligned(entropy, 4) || !aligned(norm, 8) ||
       (top > 0 && (!aligned(top_tokens, 8) || !aligned(top_logp, 4))) || !aligned(workspace, 256))
     return GRPO_ERR_MISALIGNED;
   if (workspace_bytes < token_stats_workspace_bytes(N, R)) return GRPO_ERR_WORKSPACE;
@@ -1275,7 +1275,7 @@ grpo_status grpo_token_stats_bwd(const void* logits, grpo_dtype dtype, int64_t N
       (grad_entropy != nullptr && entropy == nullptr))
     return GRPO_ERR_INVALID_ARG;
   if (!aligned(logits, esize_of(dtype)) || !aligned(dlogits, esize_of(dtype)) ||
-      !aligned(tokens, 8) || !aligned(len, 4) || !aligned(temperature, 4) || !aligned(norm, 4) ||
+      !aligned(tokens, 8) || !aligned(len, 4) || !aligned(temperature, 4) || !aligned(norm, 8) ||
       !aligned(entropy, 4) || !aligned(grad_logp, 4) || !aligned(grad_entropy, 4))
     return GRPO_ERR_MISALIGNED;
   const size_t nd = rows_bytes(N, R, V, dlogits_seq, dlogits_row, dtype);

@@ -673,7 +673,7 @@ template <typename T, bool kShift>
 __device__ __forceinline__ void grad_vectors(const T* z, uint4* out, int nvec, unsigned shift,
                                              const RowGrad& q, int64_t y) {
   using E = Elt<T>;
-  constexpr int EPV = E::kPerVec, U = kShift ? E::kUnroll / 2 : E::kUnroll;
+  constexpr int EPV = E::kPerVec, U = kShift ? 2 : 4;
   const uint4* zvec = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(z) - shift);
   const int ky = y >= 0 && y < (int64_t)nvec * EPV ? (int)(y / EPV) : -1;
   const int ey = ky >= 0 ? (int)(y % EPV) : 0;
@@ -710,9 +710,11 @@ __device__ __forceinline__ void grad_vectors(const T* z, uint4* out, int nvec, u
   }
 }
 
+// HBM-bound: 8,192 rows of 151,936 bf16, half of them scored, 554 us (99% of the copy
+// rate); rows whose gradient lies at another alignment 5.4 TB/s (2,000 of 151,935: 226 us).
+// Five thread blocks per SM: 99 us for 1,024 rows, 104 with four.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) token_stats_bwd_kernel(
-    const StatsBwdParams<T> p) {
+__global__ void __launch_bounds__(kThreads, 5) token_stats_bwd_kernel(const StatsBwdParams<T> p) {
   using E = Elt<T>;
   constexpr int EPV = E::kPerVec;
   const int tid = threadIdx.x;
@@ -740,9 +742,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) token_stats_
     }
     const int64_t b = a + (int64_t)nvec * EPV;
     uint4* ovec = reinterpret_cast<uint4*>(out + a);
+    // (loaded together: one latency)
     const bool inside = p.lens == nullptr || j < __ldg(p.lens + i);
-    const float g = inside && p.grad_logp != nullptr ? __ldg(p.grad_logp + r) : 0.f;
-    const float h = inside && p.grad_entropy != nullptr ? __ldg(p.grad_entropy + r) : 0.f;
+    const float2 norm = __ldg(reinterpret_cast<const float2*>(p.norm) + r);
+    const float Ti = warmth_of(p.temperature, i);
+    const float gr = p.grad_logp != nullptr ? __ldg(p.grad_logp + r) : 0.f;
+    const float hr = p.grad_entropy != nullptr ? __ldg(p.grad_entropy + r) : 0.f;
+    const float Hr = p.grad_entropy != nullptr ? __ldg(p.entropy + r) : 0.f;
+    const int64_t yr = p.grad_logp != nullptr ? __ldg(p.tokens + i * p.token_seq + j) : -1;
+    const float g = inside ? gr : 0.f, h = inside ? hr : 0.f;
     int64_t edge = -1;
     if (tid < a - v0)
       edge = v0 + tid;
@@ -753,18 +761,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4) token_stats_
       if (edge >= 0) E::store1(out + edge, 0.f);
       continue;
     }
-    const float Ti = warmth_of(p.temperature, i);
     RowGrad q;
-    q.m = __ldg(p.norm + 2 * r);
-    q.L2 = __ldg(p.norm + 2 * r + 1) * kLog2e;
+    q.m = norm.x;
+    q.L2 = norm.y * kLog2e;
     q.c = kLog2e / Ti;
     q.g = g / Ti;
-    const float H = h != 0.f ? __ldg(p.entropy + r) : 0.f;
-    q.A = -(q.g + h / Ti * H);
+    q.A = -(q.g + (h != 0.f ? h / Ti * Hr : 0.f));
     q.B = -h / Ti * kLn2;
     int64_t y = -1;
     if (g != 0.f) {
-      y = __ldg(p.tokens + i * p.token_seq + j);
+      y = yr;
       if (y < 0 || y >= p.V) q.A = NAN;
     }
     if (shift == 0)
@@ -803,7 +809,13 @@ cudaError_t stats_run(const TokenStatsArgs& a, const DeviceInfo& d, cudaStream_t
   p.top_logp = a.top_logp;
   p.hdr = static_cast<WsHeader*>(a.ws);
   const int64_t rows = a.N * a.R;
-  const int split = lse_split(a.V * (int64_t)sizeof(T), rows, d.sms, "GRPO_STATS_SPLIT");
+  // whole rows where there are more than SMs for them (256 rows of 304 KB 19 us, in halves
+  // 20); below that as many CTAs as leave two per SM (64 rows 7.3 us in quarters, 12.4
+  // whole, 8.7 in eighths; one row 4.5 us in eighths, 11.9 whole) of a batch each
+  int split = 1;
+  while (split < kMaxSplit && 2 * split * rows <= 2 * (int64_t)d.sms &&
+         a.V * (int64_t)sizeof(T) >= 2 * split * kStageBytes)
+    split *= 2;
   constexpr int EPV = Elt<T>::kPerVec;
   p.chunk = ((a.V + split - 1) / split + EPV - 1) / EPV * EPV;
   const dim3 grid((unsigned)(rows < 1 ? split : rows * split));
@@ -836,7 +848,13 @@ cudaError_t bwd_run(const TokenStatsBwdArgs& a, const DeviceInfo& d, cudaStream_
   p.dlogits = static_cast<T*>(a.dlogits);
   p.dseq = a.dseq;
   p.drow = a.drow;
-  p.split = row_split(a.V * (int64_t)sizeof(T), nullptr, 8);
+  // parts of a row of 32 KB or more (1,024 rows of 304 KB 99 us, whole rows 107); where
+  // that leaves few, down to 8 KB (8 rows 3.2 us in 32 parts each, 6.3 in 4), but no more than
+  // the SMs hold at once (1,024 rows of 64 KB 25 us whole, 40 in 8 parts)
+  const int64_t row_bytes = a.V * (int64_t)sizeof(T);
+  p.split = row_split(row_bytes, nullptr, 8);
+  while (a.N * a.R * p.split < 4 * (int64_t)d.sms && row_bytes / (2 * p.split) >= 8192) p.split *= 2;
+
   p.chunk = ((a.V + p.split - 1) / p.split + EPV - 1) / EPV * EPV;
   const int64_t items = a.N * a.R * p.split;
   int64_t grid = 256 * (int64_t)d.sms;
