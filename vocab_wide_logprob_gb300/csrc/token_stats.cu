@@ -78,12 +78,13 @@ struct StatsParams {
   float* top_logp;
   WsHeader* hdr;
   int64_t chunk;  // elements of a row per CTA of its cluster
+  int stages;     // of the ring
 };
 
 constexpr int kBatch = 4;       // vectors of 16 bytes that a thread takes at once
 constexpr int kStageVecs = kBatch * kThreads;
 constexpr int kStageBytes = 16 * kStageVecs;
-constexpr int kStages = 3;      // of the ring that bulk copies fill
+constexpr int kMaxStages = 12;  // of the ring that bulk copies fill (as many as there is room for)
 constexpr int kSlots = 8;       // groups of a thread whose maxima are kept, the last for a ragged end
 constexpr int kCandidates = 512;
 constexpr int kHits = 256;
@@ -135,7 +136,7 @@ __device__ __forceinline__ void pairs_of(const uint4& d, uint64_t* x, uint16_t) 
 constexpr int kMaxSplit = 8;  // CTAs of a cluster that share a row
 
 struct StatsShared {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[kMaxStages], empty[kMaxStages];
   int abort;  // a bounded wait gave up
   float warp_max[kWarps];
   float2 warp_sum[kWarps];
@@ -196,10 +197,11 @@ __device__ __forceinline__ void find_bound(TopShared& sh, int top) {
 
 // The best `top` of the part's elements (all of them if it has fewer): emit(place, key)
 // for each, by the thread that found it.  Called by the whole CTA after the stream, with
-// the bound known.  slot[g][thread]: maxima of groups.
+// the bound known.  slot[g][thread]: maxima of groups.  kept: where the part's vectors still
+// lie in shared memory, or 0.
 template <typename T, typename Emit>
 __device__ __forceinline__ void best_of_part(TopShared& sh, Late& late, const T (*slot)[kThreads],
-                                             const Part<T>& p, int top, Emit emit) {
+                                             const Part<T>& p, uint32_t kept, int top, Emit emit) {
   using E = Elt<T>;
   constexpr int EPV = E::kPerVec, U = kBatch;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -256,7 +258,9 @@ __device__ __forceinline__ void best_of_part(TopShared& sh, Late& late, const T 
               push_key(sh, late, E::load1(p.z + v), v);
             }
           }
-          if (at[u] < p.nvec) d[u] = ld_stream(p.z + p.a + (int64_t)at[u] * EPV);
+          if (at[u] < p.nvec)
+            d[u] = kept != 0 ? ld_shared_v4(kept + 16 * at[u])
+                             : ld_stream(p.z + p.a + (int64_t)at[u] * EPV);
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
@@ -375,8 +379,9 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
   using E = Elt<T>;
   constexpr int EPV = E::kPerVec, U = kBatch;
   extern __shared__ __align__(128) char s_dyn[];
-  Late& late = *reinterpret_cast<Late*>(s_dyn);
-  T(*slot)[kThreads] = reinterpret_cast<T(*)[kThreads]>(s_dyn + kStages * kStageBytes);
+  // (behind what a part that fits into the ring leaves there)
+  Late& late = *reinterpret_cast<Late*>(s_dyn + p.stages * kStageBytes - sizeof(Late));
+  T(*slot)[kThreads] = reinterpret_cast<T(*)[kThreads]>(s_dyn + p.stages * kStageBytes);
   __shared__ StatsShared sh;
   __shared__ TopShared top;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -416,19 +421,19 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
   part.v0 = min(p.V, rank * p.chunk);
   part.v1 = min(p.V, part.v0 + p.chunk);
   if (parts > 1) cluster_arrive_relaxed();  // (the first CTA runs before it is written to)
-  const unsigned phase = (unsigned)(reinterpret_cast<uintptr_t>(part.z + part.v0) & 15u);
-  part.a = min(part.v0 + (int64_t)(((16u - phase) & 15u) / sizeof(T)), part.v1);
+  const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(part.z + part.v0) & 15u);
+  part.a = min(part.v0 + (int64_t)(((16u - off) & 15u) / sizeof(T)), part.v1);
   part.nvec = (int)((part.v1 - part.a) / EPV);
   part.b = part.a + (int64_t)part.nvec * EPV;
   const int batches = (part.nvec + kStageVecs - 1) / kStageVecs;
   part.per = (batches + kSlots - 2) / (kSlots - 1);
   part.groups = part.per > 0 ? (batches + part.per - 1) / part.per : 0;
 
-  // batch b goes through stage b % kStages; thread 0 orders the copies
+  // batch b goes through stage b % stages; thread 0 orders the copies
+  const int stages = p.stages;
   const uint32_t ring = smem_u32(s_dyn), full = smem_u32(sh.full), empty = smem_u32(sh.empty);
   const char* source = reinterpret_cast<const char*>(part.z + part.a);
-  const auto order = [&](int b) {
-    const int st = b % kStages;
+  const auto order = [&](int b, int st) {
     const uint32_t bytes = 16u * (uint32_t)min(kStageVecs, part.nvec - b * kStageVecs);
     mbar_arrive_expect_tx(full + 8 * st, bytes);
     bulk_g2s(ring + st * kStageBytes, source + (int64_t)b * kStageBytes, bytes, full + 8 * st);
@@ -436,24 +441,25 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
   int ordered = 0;  // (thread 0's)
   if (tid == 0) {
     sh.abort = 0;
-    for (int k = 0; k < kStages; ++k) {
+    const int n = min(stages, batches);
+    for (int k = 0; k < n; ++k) {
       mbar_init(full + 8 * k, 1);
       mbar_init(empty + 8 * k, kWarps);
     }
     mbar_init_fence();
-    for (; ordered < min(kStages, batches); ++ordered) order(ordered);
+    for (; ordered < n; ++ordered) order(ordered, ordered);
   }
   // (used behind the stream)
   const int64_t y = rank == 0 && tid == 0 ? __ldg(p.tokens + i * p.token_seq + j) : -1;
   __syncthreads();
   Sums sum;
   const uint64_t c2 = f2_pack(c, c);
-  int batch = 0;
+  int batch = 0, st = 0, last = 0;  // the batch's stage, and the one before
+  uint32_t phase = 0, last_phase = 0;
   for (int g = 0; g < part.groups; ++g) {
     float group_max = -INFINITY;
     for (int q = 0; q < part.per && batch < batches; ++q, ++batch) {
-      const int st = batch % kStages;
-      if (!mbar_wait(full + 8 * st, batch / kStages & 1)) {
+      if (!mbar_wait(full + 8 * st, phase)) {
         *(volatile int*)&sh.abort = 1;
         batch = batches;
         break;
@@ -475,11 +481,17 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + 8 * st);
       // the stage of the batch before this one is free once every warp has read it
-      if (tid == 0 && batch >= 1 && batch - 1 + kStages < batches) {
-        if (mbar_wait(empty + 8 * ((batch - 1) % kStages), (batch - 1) / kStages & 1))
-          order(ordered++);
+      if (tid == 0 && batch >= 1 && ordered < batches) {
+        if (mbar_wait(empty + 8 * last, last_phase))
+          order(ordered++, last);
         else
           *(volatile int*)&sh.abort = 1;  // (nothing more arrives: every wait ends)
+      }
+      last = st;
+      last_phase = phase;
+      if (++st == stages) {
+        st = 0;
+        phase ^= 1;
       }
       const float largest = E::template batch_max<U>(d);
       group_max = fmaxf(group_max, largest);
@@ -549,12 +561,13 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
     s += sh.warp_sum[w].x;
     e += sh.warp_sum[w].y;
   }
+  const uint32_t kept = 16 * part.nvec <= stages * kStageBytes - (int)sizeof(Late) ? ring : 0;
   if (sh.abort != 0) {  // some of the row is missing: no distribution, and the reason
     s = NAN;
     flags |= kFlagTimeout;
     if (tid == 0)  // (what may still be on its way)
-      for (int b = max(0, ordered - kStages); b < ordered; ++b)
-        mbar_wait(full + 8 * (b % kStages), b / kStages & 1);
+      for (int b = max(0, ordered - stages); b < ordered; ++b)
+        mbar_wait(full + 8 * (b % stages), b / stages & 1);
   }
   if (parts > 1) {
     __syncwarp();  // (the cluster's barriers want whole warps)
@@ -563,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
       const int got = sh.abort != 0 ? 0 : (int)min(part.v1 - part.v0, (int64_t)p.top);
       const uint32_t to = map_to_rank(smem_u32(&top.part_key[rank][0]), 0);
       if (got > 0)
-        best_of_part(top, late, slot, part, p.top,
+        best_of_part(top, late, slot, part, kept, p.top,
                      [&](int place, uint64_t key) { st_cluster_u64(to + 8 * place, key); });
       if (tid >= got && tid < kMaxTop) st_cluster_u64(to + 8 * tid, 0);
     }
@@ -613,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
   if (parts > 1)
     merge_parts(top, (int)parts, p.top, write);
   else
-    best_of_part(top, late, slot, part, p.top, write);
+    best_of_part(top, late, slot, part, kept, p.top, write);
 }
 
 // ---------------------------------------------------------------------------
@@ -819,10 +832,19 @@ cudaError_t stats_run(const TokenStatsArgs& a, const DeviceInfo& d, cudaStream_t
   constexpr int EPV = Elt<T>::kPerVec;
   p.chunk = ((a.V + split - 1) / split + EPV - 1) / EPV * EPV;
   const dim3 grid((unsigned)(rows < 1 ? split : rows * split));
-  constexpr int kRing = kStages * kStageBytes;
-  const int smem = a.top == 0 ? kRing : kRing + kSlots * kThreads * (int)sizeof(T);
+  // The ring: three stages, with which four CTAs fill an SM's shared memory; more where
+  // fewer CTAs come to an SM, up to the whole part and room behind it.
+  const int slots = a.top == 0 ? 0 : kSlots * kThreads * (int)sizeof(T);
+  const int64_t per_sm = (rows * split + d.sms - 1) / d.sms;
+  const int64_t batches = (p.chunk * (int64_t)sizeof(T) + kStageBytes - 1) / kStageBytes;
+  p.stages = 3;
+  while (p.stages < kMaxStages && p.stages <= batches &&
+         per_sm * ((p.stages + 1) * kStageBytes + slots + 4096) <= 224 * 1024)
+    ++p.stages;
+  const int smem = p.stages * kStageBytes + slots;
   const auto kern = a.top == 0 ? token_stats_kernel<T, false> : token_stats_kernel<T, true>;
-  const cudaError_t e = ensure_dynamic_smem((const void*)kern, smem);
+  const cudaError_t e =
+      ensure_dynamic_smem((const void*)kern, kMaxStages * kStageBytes + kSlots * kThreads * 4);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, grid, dim3(kThreads), smem, st, split, p);
 }
