@@ -195,6 +195,26 @@ __device__ __forceinline__ void find_bound(TopShared& sh, int top) {
   if (before == top - 1) sh.bound = mine;
 }
 
+// emit(place, key) for the first `top` of late.key[0 .. have): a key's place is the number
+// of keys before it (they are all different, but for zeros, which are none); eight threads
+// count for one.
+template <typename Emit>
+__device__ __forceinline__ void emit_places(const Late& late, int have, int top, Emit emit) {
+  const int tid = threadIdx.x;
+#pragma unroll 1
+  for (int k0 = 0; k0 < have; k0 += kThreads / 8) {
+    const int k = k0 + tid / 8;
+    const uint64_t mine = k < have ? late.key[k] : 0;
+    int place = 0;
+#pragma unroll 4
+    for (int j = tid % 8; j < have; j += 8) place += late.key[j] > mine;
+    place += __shfl_xor_sync(0xffffffffu, place, 1);
+    place += __shfl_xor_sync(0xffffffffu, place, 2);
+    place += __shfl_xor_sync(0xffffffffu, place, 4);
+    if (tid % 8 == 0 && mine != 0 && place < top) emit(place, mine);
+  }
+}
+
 // The best `top` of the part's elements (all of them if it has fewer): emit(place, key)
 // for each, by the thread that found it.  Called by the whole CTA after the stream, with
 // the bound known.  slot[g][thread]: maxima of groups.  kept: where the part's vectors still
@@ -326,41 +346,26 @@ __device__ __forceinline__ void best_of_part(TopShared& sh, Late& late, const T 
     if (tid == 0) sh.keys = kThreads;
     __syncthreads();
   }
-  // the place of a key is the number of keys before it (they are all different, but
-  // for the zeros of empty lanes); eight threads count for one
-  const int have = sh.keys;
-#pragma unroll 1
-  for (int k0 = 0; k0 < have; k0 += kThreads / 8) {
-    const int k = k0 + tid / 8;
-    const uint64_t mine = k < have ? late.key[k] : 0;
-    int place = 0;
-#pragma unroll 4
-    for (int j = tid % 8; j < have; j += 8) place += late.key[j] > mine;
-    place += __shfl_xor_sync(0xffffffffu, place, 1);
-    place += __shfl_xor_sync(0xffffffffu, place, 2);
-    place += __shfl_xor_sync(0xffffffffu, place, 4);
-    if (tid % 8 == 0 && mine != 0 && place < top) emit(place, mine);
-  }
+  emit_places(late, sh.keys, top, emit);
 }
 
-// The best `top` of the cluster's sorted lists: a key comes behind the larger ones of
-// every list, its own too.
+// The best `top` of the cluster's lists, each sorted: the last of a list of `top` keys has
+// as many before it, so that only what reaches the largest of the lasts is looked at.
 template <typename Emit>
-__device__ __forceinline__ void merge_parts(const TopShared& sh, int parts, int top, Emit emit) {
+__device__ __forceinline__ void merge_parts(TopShared& sh, Late& late, int parts, int top, Emit emit) {
   const int list = threadIdx.x / kMaxTop, at = threadIdx.x % kMaxTop;
+  uint64_t least = 1;  // (of a key)
+#pragma unroll
+  for (int k = 0; k < kMaxSplit; ++k)
+    if (k < parts) least = max(least, sh.part_key[k][top - 1]);
   const uint64_t mine = list < parts && at < top ? sh.part_key[list][at] : 0;
-  if (mine == 0) return;
-  int lo[kMaxSplit] = {};  // keys of every list that are larger
-#pragma unroll
-  for (int step = kMaxTop / 2; step > 0; step /= 2)
-#pragma unroll
-    for (int other = 0; other < kMaxSplit; ++other)
-      if (other < parts && sh.part_key[other][lo[other] + step - 1] > mine) lo[other] += step;
-  int place = 0;
-#pragma unroll
-  for (int other = 0; other < kMaxSplit; ++other)
-    if (other < parts) place += lo[other] + (sh.part_key[other][lo[other]] > mine);
-  if (place < top) emit(place, mine);
+  const uint32_t votes = __ballot_sync(0xffffffffu, mine >= least);
+  int first = 0;
+  if (at == 0 && votes != 0) first = atomicAdd(&sh.ties, __popc(votes));
+  first = __shfl_sync(0xffffffffu, first, 0);
+  if (mine >= least) late.key[first + __popc(votes & ((1u << at) - 1))] = mine;
+  __syncthreads();
+  emit_places(late, sh.ties, top, emit);
 }
 
 __device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
@@ -370,6 +375,12 @@ __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
+}
+
+__device__ __forceinline__ void write_header(WsHeader* hdr, uint32_t rows) {
+  hdr->flags = kFlagIndirect;
+  hdr->status_count = rows;
+  hdr->status_check = ~rows;
 }
 
 // Thread blocks per SM: as many as have room for their ring in shared memory.  Three
@@ -385,50 +396,39 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
   __shared__ StatsShared sh;
   __shared__ TopShared top;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_wait();
-  pdl_trigger();
   const uint32_t parts = cluster_size(), rank = cluster_ctarank();
-  const int64_t rows = p.N * p.R, r = cluster_id_x();
-  if (r == 0 && rank == 0 && tid == 0) {
-    p.hdr->flags = kFlagIndirect;
-    p.hdr->status_count = (uint32_t)rows;
-    p.hdr->status_check = ~(uint32_t)rows;
-  }
-  if (r >= rows) return;
-  const int64_t i = r / p.R, j = r - i * p.R;
+  const uint32_t rows = (uint32_t)(p.N * p.R), r32 = cluster_id_x();  // (below 2^26)
+  const int64_t r = r32, i = r32 / max((uint32_t)p.R, 1u), j = r - i * p.R;
+  const bool writer = rank == 0 && warp == kWarps - 1 && lane == 0;  // of the row's results
   uint32_t* status = reinterpret_cast<uint32_t*>(p.hdr) + 64 + r;
   uint32_t flags = 0;
-  if (p.lens != nullptr) {
+  if (p.lens != nullptr && r < rows) {
+    pdl_wait();
+    pdl_trigger();
     const int64_t len = __ldg(p.lens + i);
     if ((len < 0 || len > p.R) && j == 0) flags = kFlagLengthRange;
     if (j >= len) {  // behind the sequence's end
-      if (rank != 0) return;
-      if (tid == 0) {
+      if (r == 0 && writer) write_header(p.hdr, rows);
+      if (writer) {
         p.logp[r] = p.entropy[r] = p.norm[2 * r] = p.norm[2 * r + 1] = 0.f;
         *status = flags;
       }
-      if (kTop && tid < p.top) {
+      if (kTop && rank == 0 && tid < p.top) {
         p.top_tokens[r * p.top + tid] = -1;
         p.top_logp[r * p.top + tid] = 0.f;
       }
       return;
     }
   }
-  const float Ti = warmth_of(p.temperature, i);
-  const float c = kLog2e / Ti;
   Part<T> part;
   part.z = p.logits + i * p.seq + j * p.row;
   part.v0 = min(p.V, rank * p.chunk);
   part.v1 = min(p.V, part.v0 + p.chunk);
-  if (parts > 1) cluster_arrive_relaxed();  // (the first CTA runs before it is written to)
   const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(part.z + part.v0) & 15u);
   part.a = min(part.v0 + (int64_t)(((16u - off) & 15u) / sizeof(T)), part.v1);
   part.nvec = (int)((part.v1 - part.a) / EPV);
   part.b = part.a + (int64_t)part.nvec * EPV;
   const int batches = (part.nvec + kStageVecs - 1) / kStageVecs;
-  part.per = (batches + kSlots - 2) / (kSlots - 1);
-  part.groups = part.per > 0 ? (batches + part.per - 1) / part.per : 0;
-
   // batch b goes through stage b % stages; thread 0 orders the copies
   const int stages = p.stages;
   const uint32_t ring = smem_u32(s_dyn), full = smem_u32(sh.full), empty = smem_u32(sh.empty);
@@ -438,20 +438,30 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
     mbar_arrive_expect_tx(full + 8 * st, bytes);
     bulk_g2s(ring + st * kStageBytes, source + (int64_t)b * kStageBytes, bytes, full + 8 * st);
   };
-  int ordered = 0;  // (thread 0's)
   if (tid == 0) {
     sh.abort = 0;
-    const int n = min(stages, batches);
-    for (int k = 0; k < n; ++k) {
+    for (int k = 0; k < min(stages, batches); ++k) {
       mbar_init(full + 8 * k, 1);
       mbar_init(empty + 8 * k, kWarps);
     }
     mbar_init_fence();
-    for (; ordered < n; ++ordered) order(ordered, ordered);
   }
-  // (used behind the stream)
-  const int64_t y = rank == 0 && tid == 0 ? __ldg(p.tokens + i * p.token_seq + j) : -1;
+  // (without lengths nothing of the caller's memory was read this far)
+  pdl_wait();
+  pdl_trigger();
+  if (r == 0 && writer) write_header(p.hdr, rows);
+  if (r >= rows) return;
+  if (parts > 1) cluster_arrive_relaxed();  // (the first CTA runs before it is written to)
+  int ordered = 0;                          // (thread 0's)
+  if (tid == 0)
+    for (; ordered < min(stages, batches); ++ordered) order(ordered, ordered);
   __syncthreads();
+  part.per = (batches + kSlots - 2) / (kSlots - 1);
+  part.groups = part.per > 0 ? (batches + part.per - 1) / part.per : 0;
+  const float Ti = warmth_of(p.temperature, i);
+  const float c = kLog2e / Ti;
+  // (used behind the stream)
+  const int64_t y = writer ? __ldg(p.tokens + i * p.token_seq + j) : -1;
   Sums sum;
   const uint64_t c2 = f2_pack(c, c);
   int batch = 0, st = 0, last = 0;  // the batch's stage, and the one before
@@ -579,6 +589,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
         best_of_part(top, late, slot, part, kept, p.top,
                      [&](int place, uint64_t key) { st_cluster_u64(to + 8 * place, key); });
       if (tid >= got && tid < kMaxTop) st_cluster_u64(to + 8 * tid, 0);
+      if (tid == 0) top.ties = 0;  // (counts the lists' keys next)
     }
     if (tid == 0)
       st_cluster_f32x4(map_to_rank(smem_u32(&sh.part[rank]), 0), make_float4(m, s, e, sh.abort != 0 ? 1.f : 0.f));
@@ -600,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
   // (a comparison with NaN is false)
   const bool defined = s > 0.f && s < INFINITY && fabsf(m) < INFINITY && c > 0.f;
   const float L = logf(s);
-  if (tid == 0) {
+  if (writer) {
     if (!defined)
       flags |= kFlagValue;
     else if (y < 0 || y >= p.V)
@@ -624,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
     p.top_logp[r * p.top + place] = (key_value(key) - m) / Ti - L;
   };
   if (parts > 1)
-    merge_parts(top, (int)parts, p.top, write);
+    merge_parts(top, late, (int)parts, p.top, write);
   else
     best_of_part(top, late, slot, part, kept, p.top, write);
 }
