@@ -786,8 +786,6 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     };
     const at::ScalarType kept = eight ? at::kFloat8_e4m3fn : at::kFloat;
     std::vector<grpo_adamw_tensor> table((size_t)n);
-    std::vector<Tensor> changed;  // (held: the call lets other threads run)
-    changed.reserve((size_t)n * 5);
     for (Py_ssize_t k = 0; k < n; ++k) {
       const Tensor& t = tensor(params.at(k), "every param");
       dense(t, "every param");
@@ -812,11 +810,10 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         refuse(PyExc_ValueError, "%s must have its param's size", "every gradient");
       e.grad = g.data_ptr();
       e.grad_dtype = code(g.scalar_type(), "every gradient");
-      changed.push_back(t);
-      changed.push_back(THPVariable_Unpack(avg.at(k)));
-      changed.push_back(THPVariable_Unpack(sq.at(k)));
-      if (eight) changed.push_back(THPVariable_Unpack(scales.at(k)));
-      if (e.master != nullptr) changed.push_back(THPVariable_Unpack(master.at(k)));
+      for (const Tensor* w : {&t, &THPVariable_Unpack(avg.at(k)), &THPVariable_Unpack(sq.at(k))})
+        written(*w);
+      if (eight) written(THPVariable_Unpack(scales.at(k)));
+      if (e.master != nullptr) written(THPVariable_Unpack(master.at(k)));
     }
     grpo_adamw_hyper h = {};
     // a number of the host, or a tensor of one value on the device
@@ -850,7 +847,6 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     check_status(
         launch([&] { return grpo_adamw_step(table.data(), n, eight ? 8 : 32, &h, stream); }),
         "grpo_adamw_step");
-    for (const Tensor& t : changed) written(t);
     Py_RETURN_NONE;
   });
 }
