@@ -617,8 +617,9 @@ grpo_status grpo_verify_drafts(const void *target_logits, const void *draft_logi
  *
  * logits: row j of sequence i starts at element i * logits_seq + j *
  * logits_row (rows of [N, P+C, V] logits: logits + (P-1) * V, logits_seq =
- * (P+C) * V), `dtype`, aligned to its element; tokens: row j of sequence i at
- * i * token_seq + j, int64.  logp, entropy [N, R], norm [N, R, 2] float32 (8-byte aligned);
+ * (P+C) * V; [R, N, V] logits: logits_seq = V, logits_row = N * V), `dtype`, aligned to its
+ * element; tokens: that of row j of sequence i at i * token_seq + j * token_row,
+ * int64; no stride is negative.  logp, entropy [N, R], norm [N, R, 2] float32 (8-byte aligned);
  * top_tokens [N, R, top] int64, top_logp [N, R, top] float32 (NULL with top
  * 0).  0 <= top <= 32, top <= V; N * R <= 2^26, V < 2^31 - 2^16.  The outputs and the
  * workspace overlap neither one another nor an input.
@@ -634,9 +635,9 @@ grpo_status grpo_verify_drafts(const void *target_logits, const void *draft_logi
 grpo_status grpo_token_stats_workspace_size(int64_t N, int64_t R, size_t *bytes);
 grpo_status grpo_token_stats(const void *logits, grpo_dtype dtype, int64_t N, int64_t R, int64_t V,
                              int64_t logits_seq, int64_t logits_row, const int64_t *tokens,
-                             int64_t token_seq, const int32_t *len, const float *temperature,
-                             int64_t top, float *logp, float *entropy, float *norm,
-                             int64_t *top_tokens, float *top_logp, void *workspace,
+                             int64_t token_seq, int64_t token_row, const int32_t *len,
+                             const float *temperature, int64_t top, float *logp, float *entropy,
+                             float *norm, int64_t *top_tokens, float *top_logp, void *workspace,
                              size_t workspace_bytes, grpo_stream_t stream);
 
 /*
@@ -649,15 +650,15 @@ grpo_status grpo_token_stats(const void *logits, grpo_dtype dtype, int64_t N, in
  * logits are read).  A row without a distribution, or with g != 0 and a token
  * outside [0, V), gets NaN.
  * dlogits: row j of sequence i at i * dlogits_seq + j * dlogits_row (so rows of a
- * larger buffer can be written where they lie; what is between them stays).
- * It overlaps no input.  tokens are needed with grad_logp only, entropy with
+ * larger buffer can be written where they lie; what is between them stays); the
+ * rows are apart, sequence by sequence or row by row.  It overlaps no input.  tokens are needed with grad_logp only, entropy with
  * grad_entropy only.  Rows of logits and dlogits that share their address's remainder by
  * 16 stream fastest.
  */
 grpo_status grpo_token_stats_bwd(const void *logits, grpo_dtype dtype, int64_t N, int64_t R,
                                  int64_t V, int64_t logits_seq, int64_t logits_row,
-                                 const int64_t *tokens, int64_t token_seq, const int32_t *len,
-                                 const float *temperature, const float *norm,
+                                 const int64_t *tokens, int64_t token_seq, int64_t token_row,
+                                 const int32_t *len, const float *temperature, const float *norm,
                                  const float *entropy, const float *grad_logp,
                                  const float *grad_entropy, void *dlogits, int64_t dlogits_seq,
                                  int64_t dlogits_row, grpo_stream_t stream);
@@ -710,7 +711,8 @@ typedef struct {
  * device pointers, aligned to their element, and what is written overlaps nothing
  * else; params that overlap one another are refused).  Arrays that are all
  * 16-byte aligned (e4m3 codes: 8) move in wide accesses.
- * beta1, beta2 in [0, 1), lr, eps, weight_decay, norm_eps >= 0 and finite,
+ * beta1, beta2 in [0, 1), lr, eps, weight_decay, norm_eps >= 0 and finite (with eps 0 an
+ * element that never had a gradient is 0 / 0),
  * max_norm >= 0 (infinity: no limit), step >= 1 (step_dev's value too).
  * With step_dev and lr_dev a captured call can be replayed with other values.
  */

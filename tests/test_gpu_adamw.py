@@ -261,6 +261,18 @@ def test_values_that_are_not_finite_stay_visible():
             assert not m[700].isfinite() and not root[700].isfinite()
 
 
+def test_shapes_that_do_not_fit_are_refused():
+    n = g()
+    p, gr, st = make([(6, 10), 50], [F32], [F32], 32, False, 20)
+    for bad in ([gr[0].t().contiguous(), gr[1]], [gr[0], gr[1][:49].contiguous()], [gr[0].t(), gr[1]]):
+        with pytest.raises(ValueError):
+            n.grpo_adamw_step(p, bad, st, 1, 1e-3)
+    with pytest.raises(ValueError):
+        n.grpo_adamw_step([p[0].t(), p[1]], gr, st, 1, 1e-3)
+    with pytest.raises(n.GrpoError):
+        n.grpo_adamw_step([p[0], p[0]], [gr[0], gr[0]], {k: [v[0], v[0].clone()] for k, v in st.items()}, 1, 1e-3)
+
+
 def test_params_without_gradients_and_empty_ones():
     n = g()
     for bits in (32, 8):

@@ -134,6 +134,42 @@ def test_views_of_wider_buffers(dt):
         check(z[:, -1:], ids[:, -1:], out, 6)
 
 
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_time_major_rows(dt):
+    """[R, N, V] logits and [R, N] tokens, transposed; the gradient in the same layout."""
+    n = g()
+    N, R, V = 5, 7, 2001
+    z, y = draw(R, N, V, dt, 40)
+    z, y = z.transpose(0, 1), y.t()
+    lens = torch.tensor([7, 0, 3, 1, 7], dtype=torch.int32, device="cuda")
+    out = n.grpo_token_stats(z, y, lens, top=5)
+    check(z, y, out, 5, lens)
+    gl, gh = (torch.randn(N, R, generator=gen(s), device="cuda") for s in (41, 42))
+    dz = torch.empty(R, N, V, dtype=dt, device="cuda").transpose(0, 1)
+    n.grpo_token_stats_bwd(z, y, out["norm"], out["entropy"], gl, gh, lens, out=dz)
+    check_grad(z, y, gl, gh, dz, lens)
+    # one row for all sequences (read only)
+    one = z[:1].expand(N, R, V)
+    out = n.grpo_token_stats(one, y, lens)
+    check(one, y, out, 0, lens)
+    with pytest.raises(n.GrpoError):
+        n.grpo_token_stats_bwd(z, y, out["norm"], out["entropy"], gl, out=dz[:1].expand(N, R, V))
+
+
+@pytest.mark.parametrize("V", [100_000_007, 50_331_648])
+def test_a_long_row(V):
+    """Vectors and batches far beyond a vocabulary's."""
+    n = g()
+    z, y = draw(1, 2, V, BF16, 43)
+    z[0, 1, V - 1] = 30.0
+    out = n.grpo_token_stats(z, y, top=11)
+    check(z, y, out, 11)
+    gl = torch.ones(1, 2, device="cuda")
+    dz = n.grpo_token_stats_bwd(z, y, out["norm"], out["entropy"], gl, gl)
+    for j in range(2):
+        check_grad(z[:, j:j + 1], y[:, j:j + 1], gl[:, :1], gl[:, :1], dz[:, j:j + 1])
+
+
 def test_lengths_and_what_lies_behind():
     n = g()
     z, y = draw(5, 6, 3001, BF16, 3)

@@ -28,7 +28,7 @@ def A(addr):
 
 
 def _stats(lib, **kw):
-    a = dict(z=A(0x100000), dt=1, N=2, R=3, V=100, seq=300, row=100, tokens=A(0x20000), tseq=3,
+    a = dict(z=A(0x100000), dt=1, N=2, R=3, V=100, seq=300, row=100, tokens=A(0x20000), tseq=3, trow=1,
              lens=None, temp=None, top=2, logp=A(0x30000), H=A(0x40000), norm=A(0x50000),
              top_tokens=A(0x60000), top_logp=A(0x70000), ws=A(0x80000), ws_bytes=1 << 16, stream=None)
     a.update(kw)
@@ -42,11 +42,14 @@ def test_token_stats_refusals(lib):
     assert _stats(lib, V=0) == INVALID
     assert _stats(lib, V=1 << 31, row=1 << 31, seq=1 << 33) == UNSUPPORTED
     assert _stats(lib, N=1 << 24, R=1 << 10) == UNSUPPORTED
-    assert _stats(lib, row=99) == INVALID        # rows overlap
-    assert _stats(lib, seq=299) == INVALID       # sequences overlap
+    assert _stats(lib, row=-1) == INVALID
     assert _stats(lib, seq=-1) == INVALID
     assert _stats(lib, seq=1 << 62) == UNSUPPORTED
+    assert _stats(lib, row=1 << 62) == UNSUPPORTED
     assert _stats(lib, tseq=-1) == INVALID
+    assert _stats(lib, trow=-1) == INVALID
+    assert _stats(lib, tseq=1 << 62) == UNSUPPORTED
+    assert _stats(lib, trow=1 << 61) == UNSUPPORTED
     assert _stats(lib, top=-1) == INVALID
     assert _stats(lib, top=33) == UNSUPPORTED
     assert _stats(lib, top=5, V=4) == INVALID
@@ -66,7 +69,7 @@ def test_token_stats_refusals(lib):
 
 
 def _bwd(lib, **kw):
-    a = dict(z=A(0x100000), dt=1, N=2, R=3, V=100, seq=300, row=100, tokens=A(0x20000), tseq=3,
+    a = dict(z=A(0x100000), dt=1, N=2, R=3, V=100, seq=300, row=100, tokens=A(0x20000), tseq=3, trow=1,
              lens=None, temp=None, norm=A(0x30000), H=A(0x40000), gl=A(0x50000), gh=A(0x60000),
              dz=A(0x200000), dseq=300, drow=100, stream=None)
     a.update(kw)
@@ -77,9 +80,12 @@ def test_token_stats_bwd_refusals(lib):
     assert _bwd(lib, dt=-1) == UNSUPPORTED
     assert _bwd(lib, N=-1) == INVALID
     assert _bwd(lib, V=0) == INVALID
-    assert _bwd(lib, row=99) == INVALID
-    assert _bwd(lib, dseq=299) == INVALID
-    assert _bwd(lib, drow=99) == INVALID
+    assert _bwd(lib, row=-1) == INVALID
+    assert _bwd(lib, trow=-1) == INVALID
+    assert _bwd(lib, dseq=299) == INVALID          # sequences overlap
+    assert _bwd(lib, drow=99) == INVALID           # rows overlap
+    assert _bwd(lib, dseq=100, drow=199) == INVALID
+    assert _bwd(lib, dseq=99, drow=200) == INVALID
     assert _bwd(lib, dseq=1 << 62) == UNSUPPORTED
     for name in ("z", "norm", "dz", "tokens", "H"):
         assert _bwd(lib, **{name: None}) == INVALID, name

@@ -94,10 +94,10 @@ def _load():
         "grpo_verify_drafts": ([P, P, INT, I64, I64, I64, I64, I64, I64, I64, P, P, P, P, I64, P,
                                 P, P, P, P, SZ, P], INT),
         "grpo_token_stats_workspace_size": ([I64, I64, ctypes.POINTER(SZ)], INT),
-        "grpo_token_stats": ([P, INT, I64, I64, I64, I64, I64, P, I64, P, P, I64, P, P, P, P, P, P,
-                              SZ, P], INT),
-        "grpo_token_stats_bwd": ([P, INT, I64, I64, I64, I64, I64, P, I64, P, P, P, P, P, P, P, I64,
-                                  I64, P], INT),
+        "grpo_token_stats": ([P, INT, I64, I64, I64, I64, I64, P, I64, I64, P, P, I64, P, P, P, P, P,
+                              P, SZ, P], INT),
+        "grpo_token_stats_bwd": ([P, INT, I64, I64, I64, I64, I64, P, I64, I64, P, P, P, P, P, P, P,
+                                  I64, I64, P], INT),
         "grpo_adamw_step": ([P, I64, INT, P, P], INT),
         "grpo_lmhead_loss_bwd": ([P, P, I64, I64, I64, I64, I64, P, P, P, P, P, P, P, P, SZ, P],
                                  INT),
@@ -665,7 +665,7 @@ def grpo_token_stats(logits, tokens, lens=None, temperature=None, top=0, out=Non
                      stream=None):
     """Log-probs of ``tokens`` [N, R] int64 under ``logits`` [N, R, V] float32 or
     bfloat16 (views of padded rows or sequences included, such as ``logits[:,
-    P-1:-1]`` with ``input_ids[:, P:]``), the entropy of every row and its ``top``
+    P-1:-1]`` with ``input_ids[:, P:]``, and rows of [R, N, V] logits transposed), the entropy of every row and its ``top``
     (at most 32) likeliest tokens.  ``lens`` [N] int32: rows of each sequence that
     count (None: all); ``temperature`` [N] float32 (None: 1).  Returns a dict with
     ``logp`` and ``entropy`` [N, R], ``norm`` [N, R, 2] (largest logit, log-sum) in

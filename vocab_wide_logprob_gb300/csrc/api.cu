@@ -928,16 +928,27 @@ bool verify_fits(int64_t N, int64_t K) {
 bool rows_fit(int64_t N, int64_t R) {
   return N == 0 || R == 0 || N <= ((int64_t)1 << 26) / R;
 }
-// Checks shared by those calls: rows of V elements at i * seq + j * row, apart.
+// Checks shared by those calls: rows of V elements at i * seq + j * row.
 grpo_status check_rows(grpo_dtype dtype, int64_t N, int64_t R, int64_t V, int64_t seq,
                        int64_t row) {
   if (!known_dtype(dtype)) return GRPO_ERR_UNSUPPORTED;
   if (N < 0 || R < 0 || V < 1) return GRPO_ERR_INVALID_ARG;
   if (!rows_fit(N, R) || V > INT32_MAX - 65536) return GRPO_ERR_UNSUPPORTED;
-  if ((R > 1 && row < V) || row < 0 || seq < 0) return GRPO_ERR_INVALID_ARG;
-  if (mul3(R, row, 8) < 0 || mul3(N, seq, 8) < 0) return GRPO_ERR_UNSUPPORTED;
-  if (N > 1 && R > 0 && seq < (R - 1) * row + V) return GRPO_ERR_INVALID_ARG;
+  if (row < 0 || seq < 0) return GRPO_ERR_INVALID_ARG;
+  const int64_t across = mul3(N, seq, 16), along = mul3(R, row, 16);
+  if (across < 0 || along < 0 || across > INT64_MAX / 2 || along > INT64_MAX / 2)
+    return GRPO_ERR_UNSUPPORTED;
   return GRPO_OK;
+}
+// Whether no two of them share an element: sequences behind one another, or rows.
+bool rows_apart(int64_t N, int64_t R, int64_t V, int64_t seq, int64_t row) {
+  if (N < 1 || R < 1) return true;
+  if ((R > 1 && row < V) || (N > 1 && seq < V)) return false;
+  return N == 1 || R == 1 || seq >= (R - 1) * row + V || row >= (N - 1) * seq + V;
+}
+bool tokens_fit(int64_t N, int64_t R, int64_t seq, int64_t row) {
+  const int64_t across = mul3(N, seq, 16), along = mul3(R, row, 16);
+  return across >= 0 && along >= 0 && across <= INT64_MAX / 2 && along <= INT64_MAX / 2;
 }
 size_t rows_bytes(int64_t N, int64_t R, int64_t V, int64_t seq, int64_t row, grpo_dtype t) {
   return ((size_t)(N - 1) * (size_t)seq + (size_t)(R - 1) * (size_t)row + (size_t)V) * esize_of(t);
@@ -1210,14 +1221,14 @@ grpo_status grpo_token_stats_workspace_size(int64_t N, int64_t R, size_t* bytes)
 
 grpo_status grpo_token_stats(const void* logits, grpo_dtype dtype, int64_t N, int64_t R, int64_t V,
                              int64_t logits_seq, int64_t logits_row, const int64_t* tokens,
-                             int64_t token_seq, const int32_t* len, const float* temperature,
-                             int64_t top, float* logp, float* entropy, float* norm,
-                             int64_t* top_tokens, float* top_logp, void* workspace,
+                             int64_t token_seq, int64_t token_row, const int32_t* len,
+                             const float* temperature, int64_t top, float* logp, float* entropy,
+                             float* norm, int64_t* top_tokens, float* top_logp, void* workspace,
                              size_t workspace_bytes, grpo_stream_t stream) {
   const grpo_status s = check_rows(dtype, N, R, V, logits_seq, logits_row);
   if (s != GRPO_OK) return s;
-  if (token_seq < 0 || top < 0 || top > V) return GRPO_ERR_INVALID_ARG;
-  if (top > kMaxTop || mul3(N, token_seq, 8) < 0) return GRPO_ERR_UNSUPPORTED;
+  if (token_seq < 0 || token_row < 0 || top < 0 || top > V) return GRPO_ERR_INVALID_ARG;
+  if (top > kMaxTop || !tokens_fit(N, R, token_seq, token_row)) return GRPO_ERR_UNSUPPORTED;
   if (workspace == nullptr) return GRPO_ERR_INVALID_ARG;
   const int64_t rows = N * R;
   if (rows > 0) {
@@ -1244,6 +1255,7 @@ grpo_status grpo_token_stats(const void* logits, grpo_dtype dtype, int64_t N, in
   a.row = logits_row;
   a.tokens = tokens;
   a.token_seq = token_seq;
+  a.token_row = token_row;
   a.lens = len;
   a.temperature = temperature;
   a.top = (int)top;
@@ -1258,16 +1270,17 @@ grpo_status grpo_token_stats(const void* logits, grpo_dtype dtype, int64_t N, in
 
 grpo_status grpo_token_stats_bwd(const void* logits, grpo_dtype dtype, int64_t N, int64_t R,
                                  int64_t V, int64_t logits_seq, int64_t logits_row,
-                                 const int64_t* tokens, int64_t token_seq, const int32_t* len,
-                                 const float* temperature, const float* norm,
+                                 const int64_t* tokens, int64_t token_seq, int64_t token_row,
+                                 const int32_t* len, const float* temperature, const float* norm,
                                  const float* entropy, const float* grad_logp,
                                  const float* grad_entropy, void* dlogits, int64_t dlogits_seq,
                                  int64_t dlogits_row, grpo_stream_t stream) {
   grpo_status s = check_rows(dtype, N, R, V, logits_seq, logits_row);
   if (s == GRPO_OK) s = check_rows(dtype, N, R, V, dlogits_seq, dlogits_row);
   if (s != GRPO_OK) return s;
-  if (token_seq < 0) return GRPO_ERR_INVALID_ARG;
-  if (mul3(N, token_seq, 8) < 0) return GRPO_ERR_UNSUPPORTED;
+  if (token_seq < 0 || token_row < 0 || !rows_apart(N, R, V, dlogits_seq, dlogits_row))
+    return GRPO_ERR_INVALID_ARG;
+  if (!tokens_fit(N, R, token_seq, token_row)) return GRPO_ERR_UNSUPPORTED;
   const int64_t rows = N * R;
   if (rows == 0) return GRPO_OK;
   if (logits == nullptr || norm == nullptr || dlogits == nullptr ||
@@ -1285,7 +1298,7 @@ grpo_status grpo_token_stats_bwd(const void* logits, grpo_dtype dtype, int64_t N
       (grad_logp != nullptr && overlap(dlogits, nd, grad_logp, 4 * (size_t)rows)) ||
       (grad_entropy != nullptr && overlap(dlogits, nd, grad_entropy, 4 * (size_t)rows)) ||
       (tokens != nullptr &&
-       overlap(dlogits, nd, tokens, 8 * (size_t)((N - 1) * token_seq + R))))
+       overlap(dlogits, nd, tokens, 8 * (size_t)((N - 1) * token_seq + (R - 1) * token_row + 1))))
     return GRPO_ERR_INVALID_ARG;
   DeviceInfo dev;
   if (current_device(&dev) != cudaSuccess) return GRPO_ERR_CUDA;
@@ -1300,6 +1313,7 @@ grpo_status grpo_token_stats_bwd(const void* logits, grpo_dtype dtype, int64_t N
   a.row = logits_row;
   a.tokens = tokens;
   a.token_seq = token_seq;
+  a.token_row = token_row;
   a.lens = len;
   a.temperature = temperature;
   a.norm = norm;

@@ -569,13 +569,22 @@ class Arena {
   c10::SmallVector<Piece, 6> parts_;
 };
 
-// Tokens [N, R] int64 whose rows may be part of wider ones: the pitch of the sequences.
-int64_t token_pitch(const Tensor& t, int64_t N, int64_t R, const c10::Device& dev) {
+// Strides of [N, R, V] rows that are dense each.
+void row_strides(const Tensor& t, const char* name, int64_t N, int64_t R, int64_t V, int64_t* seq,
+                 int64_t* row) {
+  shaped(t, name, {N, R, V});
+  if (V > 1 && t.stride(2) != 1) refuse(PyExc_ValueError, "%s must have dense rows", name);
+  *seq = N > 1 ? t.stride(0) : 0;
+  *row = R > 1 ? t.stride(1) : 0;
+}
+// Strides of tokens [N, R] int64.
+void token_strides(const Tensor& t, int64_t N, int64_t R, const c10::Device& dev, int64_t* seq,
+                   int64_t* row) {
   on_device(t, "tokens", dev);
   if (t.scalar_type() != at::kLong) refuse(PyExc_TypeError, "%s has the wrong dtype", "tokens");
   shaped(t, "tokens", {N, R});
-  if (R > 1 && t.stride(1) != 1) refuse(PyExc_ValueError, "%s must have dense rows", "tokens");
-  return t.stride(0);
+  *seq = N > 1 ? t.stride(0) : 0;
+  *row = R > 1 ? t.stride(1) : 0;
 }
 // An [N, R, ...] or [N] input of one dtype, or none.
 const Tensor* maybe_input(PyObject* o, const char* name, at::ScalarType dtype,
@@ -601,9 +610,10 @@ PyObject* token_stats(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const int64_t N = z.size(0), R = z.size(1), V = z.size(2);
     const grpo_dtype dt = code(z.scalar_type(), "logits");
     int64_t seq, row;
-    logit_strides(z, "logits", N, R, V, &seq, &row);
+    row_strides(z, "logits", N, R, V, &seq, &row);
     const Tensor& x = tensor(a[1], "tokens");
-    const int64_t token_seq = token_pitch(x, N, R, dev);
+    int64_t token_seq, token_row;
+    token_strides(x, N, R, dev, &token_seq, &token_row);
     const Tensor* lens = maybe_input(a[2], "lens", at::kInt, {N}, dev);
     const Tensor* temp = maybe_input(a[3], "temperature", at::kFloat, {N}, dev);
     const int64_t top = integer(a[4]);
@@ -649,7 +659,7 @@ PyObject* token_stats(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     check_status(launch([&] {
                    return grpo_token_stats(
                        z.data_ptr(), dt, N, R, V, seq, row, (const int64_t*)x.data_ptr(),
-                       token_seq, data_or_null<const int32_t>(lens),
+                       token_seq, token_row, data_or_null<const int32_t>(lens),
                        data_or_null<const float>(temp), top, (float*)logp.data_ptr(),
                        (float*)entropy.data_ptr(), (float*)norm.data_ptr(),
                        top > 0 ? (int64_t*)top_tokens.data_ptr() : nullptr,
@@ -693,10 +703,10 @@ PyObject* token_stats_bwd(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     if (z.dim() != 3) refuse(PyExc_ValueError, "%s must be [N, R, V]", "logits");
     const int64_t N = z.size(0), R = z.size(1), V = z.size(2);
     const grpo_dtype dt = code(z.scalar_type(), "logits");
-    int64_t seq, row, dseq, drow, token_seq = 0;
-    logit_strides(z, "logits", N, R, V, &seq, &row);
+    int64_t seq, row, dseq, drow, token_seq = 0, token_row = 0;
+    row_strides(z, "logits", N, R, V, &seq, &row);
     const Tensor* x = maybe_tensor(a[1], "tokens");
-    if (x != nullptr) token_seq = token_pitch(*x, N, R, dev);
+    if (x != nullptr) token_strides(*x, N, R, dev, &token_seq, &token_row);
     const Tensor* norm = maybe_input(a[2], "norm", at::kFloat, {N, R, 2}, dev);
     if (norm == nullptr) refuse(PyExc_TypeError, "%s must be a tensor", "norm");
     const Tensor* entropy = maybe_input(a[3], "entropy", at::kFloat, {N, R}, dev);
@@ -716,11 +726,11 @@ PyObject* token_stats_bwd(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
       if (out.scalar_type() != z.scalar_type())
         refuse(PyExc_TypeError, "%s must have logits' dtype", "out");
     }
-    logit_strides(out, "out", N, R, V, &dseq, &drow);
+    row_strides(out, "out", N, R, V, &dseq, &drow);
     check_status(launch([&] {
                    return grpo_token_stats_bwd(
                        z.data_ptr(), dt, N, R, V, seq, row, data_or_null<const int64_t>(x),
-                       token_seq, data_or_null<const int32_t>(lens),
+                       token_seq, token_row, data_or_null<const int32_t>(lens),
                        data_or_null<const float>(temp), data_or_null<const float>(norm),
                        data_or_null<const float>(entropy), data_or_null<const float>(gl),
                        data_or_null<const float>(gh), out.data_ptr(), dseq, drow, st);
@@ -806,8 +816,8 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
       if (grads.at(k) == Py_None) continue;
       const Tensor& g = tensor(grads.at(k), "every gradient");
       dense(g, "every gradient");
-      if (g.numel() != e.numel)
-        refuse(PyExc_ValueError, "%s must have its param's size", "every gradient");
+      if (g.sizes() != t.sizes())
+        refuse(PyExc_ValueError, "%s must have its param's shape", "every gradient");
       e.grad = g.data_ptr();
       e.grad_dtype = code(g.scalar_type(), "every gradient");
       for (const Tensor* w : {&t, &THPVariable_Unpack(avg.at(k)), &THPVariable_Unpack(sq.at(k))})

@@ -171,8 +171,8 @@ struct TokenStatsArgs {
   const void* logits;
   int dtype;                           // 0 f32, 1 bf16
   int64_t N, R, V, seq, row;           // rows at i * seq + j * row
-  const int64_t* tokens;               // at i * token_seq + j
-  int64_t token_seq;
+  const int64_t* tokens;               // at i * token_seq + j * token_row
+  int64_t token_seq, token_row;
   const int32_t* lens;                 // [N] or null (R each)
   const float* temperature;            // [N] or null (1)
   int top;
@@ -191,7 +191,7 @@ struct TokenStatsBwdArgs {
   int dtype;
   int64_t N, R, V, seq, row;
   const int64_t* tokens;  // null without grad_logp
-  int64_t token_seq;
+  int64_t token_seq, token_row;
   const int32_t* lens;
   const float* temperature;
   const float* norm;

@@ -67,7 +67,7 @@ struct StatsParams {
   const T* logits;
   int64_t N, R, V, seq, row;
   const int64_t* tokens;
-  int64_t token_seq;
+  int64_t token_seq, token_row;
   const int32_t* lens;
   const float* temperature;
   int top;
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
   const float Ti = warmth_of(p.temperature, i);
   const float c = kLog2e / Ti;
   // (used behind the stream)
-  const int64_t y = writer ? __ldg(p.tokens + i * p.token_seq + j) : -1;
+  const int64_t y = writer ? __ldg(p.tokens + i * p.token_seq + j * p.token_row) : -1;
   Sums sum;
   const uint64_t c2 = f2_pack(c, c);
   int batch = 0, st = 0, last = 0;  // the batch's stage, and the one before
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
     s += sh.warp_sum[w].x;
     e += sh.warp_sum[w].y;
   }
-  const uint32_t kept = 16 * part.nvec <= stages * kStageBytes - (int)sizeof(Late) ? ring : 0;
+  const uint32_t kept = part.nvec <= (stages * kStageBytes - (int)sizeof(Late)) / 16 ? ring : 0;
   if (sh.abort != 0) {  // some of the row is missing: no distribution, and the reason
     s = NAN;
     flags |= kFlagTimeout;
@@ -649,7 +649,7 @@ struct StatsBwdParams {
   const T* logits;
   int64_t N, R, V, seq, row;
   const int64_t* tokens;
-  int64_t token_seq;
+  int64_t token_seq, token_row;
   const int32_t* lens;
   const float* temperature;
   const float* norm;
@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 5) token_stats_bwd_kernel(const Stat
     const float gr = p.grad_logp != nullptr ? __ldg(p.grad_logp + r) : 0.f;
     const float hr = p.grad_entropy != nullptr ? __ldg(p.grad_entropy + r) : 0.f;
     const float Hr = p.grad_entropy != nullptr ? __ldg(p.entropy + r) : 0.f;
-    const int64_t yr = p.grad_logp != nullptr ? __ldg(p.tokens + i * p.token_seq + j) : -1;
+    const int64_t yr = p.grad_logp != nullptr ? __ldg(p.tokens + i * p.token_seq + j * p.token_row) : -1;
     const float g = inside ? gr : 0.f, h = inside ? hr : 0.f;
     int64_t edge = -1;
     if (tid < a - v0)
@@ -823,6 +823,7 @@ cudaError_t stats_run(const TokenStatsArgs& a, const DeviceInfo& d, cudaStream_t
   p.row = a.row;
   p.tokens = a.tokens;
   p.token_seq = a.token_seq;
+  p.token_row = a.token_row;
   p.lens = a.lens;
   p.temperature = a.temperature;
   p.top = a.top;
@@ -872,6 +873,7 @@ cudaError_t bwd_run(const TokenStatsBwdArgs& a, const DeviceInfo& d, cudaStream_
   p.row = a.row;
   p.tokens = a.tokens;
   p.token_seq = a.token_seq;
+  p.token_row = a.token_row;
   p.lens = a.lens;
   p.temperature = a.temperature;
   p.norm = a.norm;
