@@ -166,6 +166,7 @@ struct Part {  // elements [v0, v1) of a row; vectors of 16 bytes in [a, b)
   int64_t v0, v1, a, b;
   int nvec;
   int groups, per;  // groups of `per` batches of U vectors
+  unsigned inverse;  // 2^32 / (per U), rounded up: quotients of what is below 2^32 / (per U)
 };
 
 // A logit's own bits, from its float, and back.
@@ -260,6 +261,8 @@ __device__ __forceinline__ void best_of_part(TopShared& sh, Late& late, const T 
     const int hits = sh.hits;
     if (hits <= kHits) {
       const unsigned each = (unsigned)p.per * U, items = (unsigned)hits * each;
+      const bool divide = each > 4096;  // (items reach kHits each: the product with the inverse is
+                                        // exact while items each are below 2^32)
       constexpr int kAhead = 2;
 #pragma unroll 1
       for (unsigned w0 = tid; w0 < items; w0 += kAhead * kThreads) {
@@ -267,9 +270,11 @@ __device__ __forceinline__ void best_of_part(TopShared& sh, Late& late, const T 
         int at[kAhead];  // the vector, or none
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-          const unsigned w = w0 + u * kThreads, q = w / each, rest = w - q * each;
+          const unsigned w = w0 + u * kThreads;
           at[u] = INT32_MAX;
+          if (u > 0 && w0 - tid + u * kThreads >= items) break;
           if (w < items) {
+            const unsigned q = divide ? w / each : __umulhi(w, p.inverse), rest = w - q * each;
             const int h = late.hit[q], t = h % kThreads, g = h / kThreads;
             if (g < p.groups) {
               at[u] = (g * (int)each + (int)rest) * kThreads + t;
@@ -284,6 +289,7 @@ __device__ __forceinline__ void best_of_part(TopShared& sh, Late& late, const T 
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
+          if (u > 0 && w0 - tid + u * kThreads >= items) break;
           if (at[u] >= p.nvec) continue;
           float x[EPV];
           E::unpack(d[u], x);
@@ -349,15 +355,21 @@ __device__ __forceinline__ void best_of_part(TopShared& sh, Late& late, const T 
   emit_places(late, sh.keys, top, emit);
 }
 
-// The best `top` of the cluster's lists, each sorted: the last of a list of `top` keys has
-// as many before it, so that only what reaches the largest of the lasts is looked at.
+// The best `top` of the cluster's lists, each sorted.  The last of a list of `top` keys has
+// as many before it, and so have together the lists' keys at the place top / parts: only
+// what reaches the larger of the two is looked at.
 template <typename Emit>
 __device__ __forceinline__ void merge_parts(TopShared& sh, Late& late, int parts, int top, Emit emit) {
   const int list = threadIdx.x / kMaxTop, at = threadIdx.x % kMaxTop;
-  uint64_t least = 1;  // (of a key)
+  const int share = (top + parts - 1) / parts;
+  uint64_t least = 1, all = ~0ull;  // (of a key)
 #pragma unroll
   for (int k = 0; k < kMaxSplit; ++k)
-    if (k < parts) least = max(least, sh.part_key[k][top - 1]);
+    if (k < parts) {
+      least = max(least, sh.part_key[k][top - 1]);
+      all = min(all, sh.part_key[k][share - 1]);
+    }
+  least = max(least, all);
   const uint64_t mine = list < parts && at < top ? sh.part_key[list][at] : 0;
   const uint32_t votes = __ballot_sync(0xffffffffu, mine >= least);
   int first = 0;
@@ -458,6 +470,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
   __syncthreads();
   part.per = (batches + kSlots - 2) / (kSlots - 1);
   part.groups = part.per > 0 ? (batches + part.per - 1) / part.per : 0;
+  part.inverse = 0xffffffffu / (unsigned)max(part.per * U, 1) + 1;
   const float Ti = warmth_of(p.temperature, i);
   const float c = kLog2e / Ti;
   // (used behind the stream)
