@@ -155,11 +155,6 @@ struct Late {
   int hit[kHits];
 };
 
-__device__ __forceinline__ void push_key(TopShared& sh, Late& late, float x, int64_t v) {
-  const int at = atomicAdd(&sh.keys, 1);
-  if (at < kCandidates) late.key[at] = key_of(x, v);
-}
-
 template <typename T>
 struct Part {  // elements [v0, v1) of a row; vectors of 16 bytes in [a, b)
   const T* z;
@@ -265,38 +260,53 @@ __device__ __forceinline__ void best_of_part(TopShared& sh, Late& late, const T 
                                         // exact while items each are below 2^32)
       constexpr int kAhead = 2;
 #pragma unroll 1
-      for (unsigned w0 = tid; w0 < items; w0 += kAhead * kThreads) {
+      for (unsigned first = 0; first < items; first += kAhead * kThreads) {
         uint4 d[kAhead];
-        int at[kAhead];  // the vector, or none
+        int64_t id[kAhead];  // of the vector's first element, or none; a ragged end's alone
+        bool alone[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-          const unsigned w = w0 + u * kThreads;
-          at[u] = INT32_MAX;
-          if (u > 0 && w0 - tid + u * kThreads >= items) break;
-          if (w < items) {
-            const unsigned q = divide ? w / each : __umulhi(w, p.inverse), rest = w - q * each;
-            const int h = late.hit[q], t = h % kThreads, g = h / kThreads;
-            if (g < p.groups) {
-              at[u] = (g * (int)each + (int)rest) * kThreads + t;
-            } else if (rest == 0) {  // a ragged end's element
-              const int64_t v = t < 32 ? p.v0 + t : p.b + t - 32;
-              push_key(sh, late, E::load1(p.z + v), v);
-            }
+          const unsigned w = first + u * kThreads + tid;
+          id[u] = -1;
+          alone[u] = false;
+          if (u > 0 && first + u * kThreads >= items) break;
+          if (w >= items) continue;
+          const unsigned q = divide ? w / each : __umulhi(w, p.inverse), rest = w - q * each;
+          const int h = late.hit[q], t = h % kThreads, g = h / kThreads;
+          const int at = (g * (int)each + (int)rest) * kThreads + t;
+          if (g == p.groups) {
+            if (rest != 0) continue;
+            alone[u] = true;
+            id[u] = t < 32 ? p.v0 + t : p.b + t - 32;
+          } else if (at < p.nvec) {
+            id[u] = p.a + (int64_t)at * EPV;
+            d[u] = kept != 0 ? ld_shared_v4(kept + 16 * at) : ld_stream(p.z + id[u]);
           }
-          if (at[u] < p.nvec)
-            d[u] = kept != 0 ? ld_shared_v4(kept + 16 * at[u])
-                             : ld_stream(p.z + p.a + (int64_t)at[u] * EPV);
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-          if (u > 0 && w0 - tid + u * kThreads >= items) break;
-          if (at[u] >= p.nvec) continue;
+          if (u > 0 && first + u * kThreads >= items) break;
           float x[EPV];
           E::unpack(d[u], x);
+          if (alone[u]) x[0] = E::load1(p.z + id[u]);
+          uint32_t votes[EPV];
+          int mine = 0;
 #pragma unroll
-          for (int e = 0; e < EPV; ++e)
-            if (strict ? x[e] > bound : x[e] >= bound)
-              push_key(sh, late, x[e], p.a + (int64_t)at[u] * EPV + e);
+          for (int e = 0; e < EPV; ++e) {
+            const bool there = id[u] >= 0 && (e == 0 || !alone[u]);
+            votes[e] = __ballot_sync(0xffffffffu, there && (strict ? x[e] > bound : x[e] >= bound));
+            mine += __popc(votes[e]);
+          }
+          if (mine == 0) continue;  // (one addition a warp)
+          int at = 0;
+          if (lane == 0) at = atomicAdd(&sh.keys, mine);
+          at = __shfl_sync(0xffffffffu, at, 0);
+#pragma unroll
+          for (int e = 0; e < EPV; ++e) {
+            const int k = at + __popc(votes[e] & ((1u << lane) - 1));
+            if ((votes[e] >> lane & 1) && k < kCandidates) late.key[k] = key_of(x[e], id[u] + e);
+            at += __popc(votes[e]);
+          }
         }
       }
     }
