@@ -664,6 +664,184 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
 }
 
 // ---------------------------------------------------------------------------
+// forward, short rows: a warp per row
+// ---------------------------------------------------------------------------
+
+// A warp's best keys so far, one per lane, best first.
+struct Best {
+  uint64_t mine = 0, last = 0;  // last: the top-th
+
+  // Takes the lanes' x where `wanted`.
+  __device__ __forceinline__ void take(bool wanted, float x, int64_t v, int top) {
+    const uint64_t k = wanted ? key_of(x, v) : 0;
+    uint32_t better = __ballot_sync(0xffffffffu, k > last);
+    const int lane = threadIdx.x & 31;
+    while (better != 0) {
+      const int from = __ffs(better) - 1;
+      better &= better - 1;
+      const uint64_t y = __shfl_sync(0xffffffffu, k, from);
+      const uint64_t up = __shfl_up_sync(0xffffffffu, mine, 1);
+      if (y > mine) mine = lane > 0 && y > up ? up : y;
+      last = __shfl_sync(0xffffffffu, mine, top - 1);
+    }
+  }
+};
+
+// The top-th largest of 64 values, two a lane: a warp's lower bound of the top-th
+// largest element where each is the largest of a set.
+__device__ __forceinline__ float warp_bound(float set0, float set1, int top) {
+  const auto ordered = [](float x) { return (uint32_t)(key_of(x, 0) >> 32); };
+  uint32_t hi = ordered(fmaxf(set0, set1)), lo = ordered(fminf(set0, set1)), best = 0;
+#pragma unroll 1
+  for (int k = 0; k < top; ++k) {
+    best = __reduce_max_sync(0xffffffffu, hi);
+    if ((threadIdx.x & 31) == __ffs(__ballot_sync(0xffffffffu, hi == best)) - 1) {
+      hi = lo;
+      lo = 0;  // (below every value)
+    }
+  }
+  return best == 0 ? -INFINITY : key_value((uint64_t)best << 32);
+}
+
+// What token_stats_kernel computes.  A row takes one warp longer than a thread block, but
+// 32 of them share an SM, without barriers and with a tenth of the instructions that a row costs
+// beside its elements (which kernel where: at the launch).
+template <typename T, bool kTop>
+__global__ void __launch_bounds__(kThreads, 4) token_stats_short_kernel(const StatsParams<T> p) {
+  using E = Elt<T>;
+  constexpr int EPV = E::kPerVec, U = 4;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rows = (uint32_t)(p.N * p.R), r = blockIdx.x * kWarps + threadIdx.x / 32;
+  pdl_wait();
+  pdl_trigger();
+  if (r == 0 && lane == 0) write_header(p.hdr, rows);
+  if (r >= rows) return;
+  const int64_t i = r / (uint32_t)p.R, j = r - i * p.R;
+  uint32_t* status = reinterpret_cast<uint32_t*>(p.hdr) + 64 + r;
+  uint32_t flags = 0;
+  float* const norm = p.norm + 2 * (int64_t)r;
+  int64_t* const top_tokens = p.top_tokens + (int64_t)r * p.top;
+  float* const top_logp = p.top_logp + (int64_t)r * p.top;
+  if (p.lens != nullptr) {
+    const int64_t len = __ldg(p.lens + i);
+    if ((len < 0 || len > p.R) && j == 0) flags = kFlagLengthRange;
+    if (j >= len) {  // behind the sequence's end
+      if (lane == 0) {
+        p.logp[r] = p.entropy[r] = norm[0] = norm[1] = 0.f;
+        *status = flags;
+      }
+      if (kTop && lane < p.top) {
+        top_tokens[lane] = -1;
+        top_logp[lane] = 0.f;
+      }
+      return;
+    }
+  }
+  const int64_t y = lane == 0 ? __ldg(p.tokens + i * p.token_seq + j * p.token_row) : -1;
+  const T* z = p.logits + i * p.seq + j * p.row;
+  const float Ti = warmth_of(p.temperature, i);
+  const float c = kLog2e / Ti;
+  // (short: 32-bit indexes)
+  const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(z) & 15u);
+  const int V = (int)p.V, a = min((int)(((16u - off) & 15u) / sizeof(T)), V);
+  const int nvec = (V - a) / EPV, b = a + nvec * EPV;
+  const uint4* vec = reinterpret_cast<const uint4*>(z + a);
+  const auto load = [&](uint4* d, int k0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      d[u] = make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf);
+      if (k0 + 32 * u < nvec) d[u] = __ldg(vec + k0 + 32 * u);
+    }
+  };
+  const int ragged = lane < 16 ? (lane < a ? lane : -1) : (lane - 16 < V - b ? b + lane - 16 : -1);
+  const float end = ragged >= 0 ? E::load1(z + ragged) : -INFINITY;
+
+  Sums sum;
+  const uint64_t c2 = f2_pack(c, c);
+  float set0 = -INFINITY, set1 = end;
+#pragma unroll 1
+  for (int k0 = lane; k0 - lane < nvec; k0 += 32 * U) {
+    uint4 d[U];
+    load(d, k0);
+    const float even = E::template batch_max<U / 2>(d), odd = E::template batch_max<U / 2>(d + U / 2);
+    set0 = fmaxf(set0, even);
+    set1 = fmaxf(set1, odd);
+    sum.make_room(fmaxf(even, odd), c);
+    const uint64_t nref = f2_pack(-sum.ref, -sum.ref);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      uint64_t x[EPV / 2];
+      pairs_of(d[u], x, T());
+#pragma unroll
+      for (int e = 0; e < EPV / 2; ++e) sum.add(x[e], nref, c2);
+    }
+  }
+  if (ragged >= 0) {
+    sum.make_room(end, c);
+    sum.add(f2_pack(end, -INFINITY), f2_pack(-sum.ref, -sum.ref), c2);
+  }
+  const float at_token = y >= 0 && y < V ? E::load1(z + y) : 0.f;
+  float m = fmaxf(set0, set1);
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float s, e, s1, e1;
+  f2_unpack(sum.s, s, s1);
+  f2_unpack(sum.e, e, e1);
+  s += s1;
+  e += e1;
+  if (sum.lim != -INFINITY) {
+    const float d = fmaxf((sum.ref - m) * c, kLowest), f = ex2(d);
+    e = f * fmaf(d, s, e);
+    s *= f;
+  }
+  for (int o = 16; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    e += __shfl_xor_sync(0xffffffffu, e, o);
+  }
+  // (a comparison with NaN is false)
+  const bool defined = s > 0.f && s < INFINITY && fabsf(m) < INFINITY && c > 0.f;
+  const float L = logf(s);
+  if (lane == 0) {
+    if (!defined)
+      flags |= kFlagValue;
+    else if (y < 0 || y >= V)
+      flags |= kFlagTokenRange;
+    p.logp[r] = defined && y >= 0 && y < V ? (at_token - m) / Ti - L : NAN;
+    p.entropy[r] = defined ? L - kLn2 * (e / s) : NAN;
+    norm[0] = defined ? m : NAN;
+    norm[1] = defined ? L : NAN;
+    *status = flags;
+  }
+  if (!kTop) return;
+  Best best;
+  if (defined) {
+    const float bound = warp_bound(set0, set1, p.top);
+    best.take(ragged >= 0 && end >= bound, end, ragged, p.top);
+#pragma unroll 1
+    for (int k0 = lane; k0 - lane < nvec; k0 += 32 * U) {
+      uint4 d[U];
+      load(d, k0);
+      if (!__any_sync(0xffffffffu, E::template batch_max<U>(d) >= bound)) continue;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool there = k0 + 32 * u < nvec;
+        float x[EPV];
+        E::unpack(d[u], x);
+#pragma unroll
+        for (int q = 0; q < EPV; ++q) {
+          const bool wanted = there && x[q] >= bound;
+          if (__any_sync(0xffffffffu, wanted))
+            best.take(wanted, x[q], a + (int64_t)(k0 + 32 * u) * EPV + q, p.top);
+        }
+      }
+    }
+  }
+  if (lane < p.top) {
+    top_tokens[lane] = defined ? key_id(best.mine) : -1;
+    top_logp[lane] = defined ? (key_value(best.mine) - m) / Ti - L : NAN;
+  }
+}
+
+// ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
 
@@ -714,9 +892,9 @@ __device__ __forceinline__ uint4 from_two(uint4 lo, uint4 hi, unsigned shift) {
                     __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
 }
 
-// nvec vectors of gradients; z: the first one's logits (kShift: `shift` bytes
+// nvec vectors of gradients by kStep threads; z: the first one's logits (kShift: `shift` bytes
 // behind a 16-byte boundary), y: the token relative to it.
-template <typename T, bool kShift>
+template <typename T, bool kShift, int kStep>
 __device__ __forceinline__ void grad_vectors(const T* z, uint4* out, int nvec, unsigned shift,
                                              const RowGrad& q, int64_t y) {
   using E = Elt<T>;
@@ -724,11 +902,11 @@ __device__ __forceinline__ void grad_vectors(const T* z, uint4* out, int nvec, u
   const uint4* zvec = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(z) - shift);
   const int ky = y >= 0 && y < (int64_t)nvec * EPV ? (int)(y / EPV) : -1;
   const int ey = ky >= 0 ? (int)(y % EPV) : 0;
-  for (int k0 = threadIdx.x; k0 < nvec; k0 += kThreads * U) {
+  for (int k0 = threadIdx.x % kStep; k0 < nvec; k0 += kStep * U) {
     uint4 d[U], next[kShift ? U : 1];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = k0 + u * kThreads;
+      const int k = k0 + u * kStep;
       if (k >= nvec) break;
       if (kShift) {  // (the neighbour's first is this one's second: through L1)
         d[u] = __ldg(zvec + k);
@@ -739,7 +917,7 @@ __device__ __forceinline__ void grad_vectors(const T* z, uint4* out, int nvec, u
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = k0 + u * kThreads;
+      const int k = k0 + u * kStep;
       if (k >= nvec) break;
       if (kShift) d[u] = from_two(d[u], next[u], shift);
       float x[EPV], o[EPV];
@@ -760,18 +938,21 @@ __device__ __forceinline__ void grad_vectors(const T* z, uint4* out, int nvec, u
 // HBM-bound: 8,192 rows of 151,936 bf16, half of them scored, 554 us (99% of the copy
 // rate); rows whose gradient lies at another alignment 5.4 TB/s (2,000 of 151,935: 226 us).
 // Five thread blocks per SM: 99 us for 1,024 rows, 104 with four.
-template <typename T>
+// kStep: threads to an item, a block's or a warp's.
+template <typename T, int kStep>
 __global__ void __launch_bounds__(kThreads, 5) token_stats_bwd_kernel(const StatsBwdParams<T> p) {
   using E = Elt<T>;
-  constexpr int EPV = E::kPerVec;
-  const int tid = threadIdx.x;
+  constexpr int EPV = E::kPerVec, kTeams = kThreads / kStep;
+  const int tid = threadIdx.x % kStep;
   pdl_wait();
   pdl_trigger();
-  const int64_t items = p.N * p.R * p.split;
+  const uint32_t items = (uint32_t)(p.N * p.R) * (uint32_t)p.split;  // (below 2^31)
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int64_t r = item / p.split, i = r / p.R, j = r - i * p.R;
-    const int64_t v0 = (item - r * p.split) * p.chunk, v1 = min(p.V, v0 + p.chunk);
+  for (uint32_t item = blockIdx.x * kTeams + threadIdx.x / kStep; item < items;
+       item += gridDim.x * kTeams) {
+    const uint32_t row = item / (uint32_t)p.split, seq = row / (uint32_t)p.R;
+    const int64_t r = row, i = seq, j = row - seq * (uint32_t)p.R;
+    const int64_t v0 = (item - row * (uint32_t)p.split) * p.chunk, v1 = min(p.V, v0 + p.chunk);
     if (v0 >= v1) continue;
     const T* z = p.logits + i * p.seq + j * p.row;
     T* out = p.dlogits + i * p.dseq + j * p.drow;
@@ -799,12 +980,12 @@ __global__ void __launch_bounds__(kThreads, 5) token_stats_bwd_kernel(const Stat
     const int64_t yr = p.grad_logp != nullptr ? __ldg(p.tokens + i * p.token_seq + j * p.token_row) : -1;
     const float g = inside ? gr : 0.f, h = inside ? hr : 0.f;
     int64_t edge = -1;
-    if (tid < a - v0)
+    if (tid < 16 && tid < a - v0)  // (at most 15 on either side)
       edge = v0 + tid;
-    else if (tid >= 32 && tid - 32 < v1 - b)
-      edge = b + tid - 32;
+    else if (tid >= 16 && tid - 16 < v1 - b)
+      edge = b + tid - 16;
     if (g == 0.f && h == 0.f) {  // zeros, logits not read
-      for (int k = tid; k < nvec; k += kThreads) st_stream(ovec + k, zero);
+      for (int k = tid; k < nvec; k += kStep) st_stream(ovec + k, zero);
       if (edge >= 0) E::store1(out + edge, 0.f);
       continue;
     }
@@ -821,9 +1002,9 @@ __global__ void __launch_bounds__(kThreads, 5) token_stats_bwd_kernel(const Stat
       if (y < 0 || y >= p.V) q.A = NAN;
     }
     if (shift == 0)
-      grad_vectors<T, false>(z + a, ovec, nvec, 0, q, y - a);
+      grad_vectors<T, false, kStep>(z + a, ovec, nvec, 0, q, y - a);
     else
-      grad_vectors<T, true>(z + a, ovec, nvec, shift, q, y - a);
+      grad_vectors<T, true, kStep>(z + a, ovec, nvec, shift, q, y - a);
     if (edge >= 0) {
       const float x = E::load1(z + edge);
       E::store1(out + edge, edge == y ? q.at_token(x) : q.at(x));
@@ -857,6 +1038,17 @@ cudaError_t stats_run(const TokenStatsArgs& a, const DeviceInfo& d, cudaStream_t
   p.top_logp = a.top_logp;
   p.hdr = static_cast<WsHeader*>(a.ws);
   const int64_t rows = a.N * a.R;
+  // A warp per row where the rows are short and many (top alternatives take a warp longer):
+  // 32,768 rows of 1,000 bf16 22 us, 175 with a thread block each (with 5 alternatives 47
+  // and 349); 1,024 of 4,096 4.6 and 7.6 us, 300 of them 4.5 and 3.8; 4,096 of 16,384 with 5
+  // alternatives 49 and 57, 1,024 of them 23 and 17.
+  const int64_t row_bytes = a.V * (int64_t)sizeof(T);
+  if (row_bytes <= 1024 || (row_bytes <= 32768 && rows * 2048 >= row_bytes * d.sms * (a.top > 0 ? 2 : 1))) {
+    const dim3 blocks((unsigned)((rows + kWarps - 1) / kWarps + (rows == 0)));
+    return a.top == 0
+               ? launch_pdl(token_stats_short_kernel<T, false>, blocks, dim3(kThreads), 0, st, 1, p)
+               : launch_pdl(token_stats_short_kernel<T, true>, blocks, dim3(kThreads), 0, st, 1, p);
+  }
   // whole rows where there are more than SMs for them (256 rows of 304 KB 19 us, in halves
   // 20); below that as many CTAs as leave two per SM (64 rows 7.3 us in quarters, 12.4
   // whole, 8.7 in eighths; one row 4.5 us in eighths, 11.9 whole) of a batch each
@@ -906,18 +1098,26 @@ cudaError_t bwd_run(const TokenStatsBwdArgs& a, const DeviceInfo& d, cudaStream_
   p.dlogits = static_cast<T*>(a.dlogits);
   p.dseq = a.dseq;
   p.drow = a.drow;
+  const int64_t row_bytes = a.V * (int64_t)sizeof(T), rows = a.N * a.R;
+  // A warp per row where the rows are short and many: 32,768 rows of 1,000 bf16 29 us, 108
+  // with a thread block each; 4,096 of 4,096 16 and 20 us, 1,024 of them 8.2 and 7.2.
+  if (row_bytes <= 8192 && rows * 1024 >= row_bytes * d.sms) {
+    p.split = 1;
+    p.chunk = a.V;
+    const int64_t blocks = (rows + kWarps - 1) / kWarps, most = 32 * (int64_t)d.sms;
+    return launch_pdl(token_stats_bwd_kernel<T, 32>, dim3((unsigned)(blocks < most ? blocks : most)),
+                      dim3(kThreads), 0, st, 1, p);
+  }
   // parts of a row of 32 KB or more (1,024 rows of 304 KB 99 us, whole rows 107); where
   // that leaves few, down to 8 KB (8 rows 3.2 us in 32 parts each, 6.3 in 4), but no more than
   // the SMs hold at once (1,024 rows of 64 KB 25 us whole, 40 in 8 parts)
-  const int64_t row_bytes = a.V * (int64_t)sizeof(T);
   p.split = row_split(row_bytes, nullptr, 8);
-  while (a.N * a.R * p.split < 4 * (int64_t)d.sms && row_bytes / (2 * p.split) >= 8192) p.split *= 2;
-
+  while (rows * p.split < 4 * (int64_t)d.sms && row_bytes / (2 * p.split) >= 8192) p.split *= 2;
   p.chunk = ((a.V + p.split - 1) / p.split + EPV - 1) / EPV * EPV;
-  const int64_t items = a.N * a.R * p.split;
+  const int64_t items = rows * p.split;
   int64_t grid = 256 * (int64_t)d.sms;
   if (grid > items) grid = items;
-  return launch_pdl(token_stats_bwd_kernel<T>, dim3((unsigned)grid), dim3(kThreads), 0, st, 1, p);
+  return launch_pdl(token_stats_bwd_kernel<T, kThreads>, dim3((unsigned)grid), dim3(kThreads), 0, st, 1, p);
 }
 
 }  // namespace
