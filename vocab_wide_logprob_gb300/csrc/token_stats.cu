@@ -820,10 +820,10 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_short_kernel(const St
     for (int k0 = lane; k0 - lane < nvec; k0 += 32 * U) {
       uint4 d[U];
       load(d, k0);
-      if (!__any_sync(0xffffffffu, E::template batch_max<U>(d) >= bound)) continue;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const bool there = k0 + 32 * u < nvec;
+        if (!__any_sync(0xffffffffu, there && E::template batch_max<1>(d + u) >= bound)) continue;
         float x[EPV];
         E::unpack(d[u], x);
 #pragma unroll
