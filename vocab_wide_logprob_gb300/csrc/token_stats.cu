@@ -1,7 +1,8 @@
 // Log-probs of given tokens, entropy and likeliest alternatives of rows of
 // logits, and the gradient of the first two.
 //
-// Forward, with c = log2(e) / T and every thread's running reference r:
+// Forward, with c = log2(e) / T and every thread's running reference r (a maximum, moved
+// when a value exceeds it by 8 / c):
 //   t_v = (z_v - r) c,  w_v = 2^t_v,  S = sum w_v,  E = sum w_v t_v
 // in one pass.  At the end everything is moved to the row's maximum m (S' = S
 // 2^d, E' = 2^d (E + d S) with d = (r - m) c) and added in a fixed order:
@@ -492,7 +493,8 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
   for (int g = 0; g < part.groups; ++g) {
     float group_max = -INFINITY;
     for (int q = 0; q < part.per && batch < batches; ++q, ++batch) {
-      if (!mbar_wait(full + 8 * st, phase)) {
+      // (a warp gives up as a whole: what follows wants all its lanes)
+      if (!__all_sync(0xffffffffu, mbar_wait(full + 8 * st, phase))) {
         *(volatile int*)&sh.abort = 1;
         batch = batches;
         break;
