@@ -400,6 +400,33 @@ def test_gradient_of_views_into_views(dt):
         assert (rows[:, :, V:] == 9).all()
 
 
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 3, 40011), (2, 3, 16390), (2, 1, 16385), (3, 7, 65537),
+                                   (4, 100, 100), (2, 700, 1001), (1, 2, 9)], ids=str)
+def test_gradient_of_rows_at_another_alignment(shape, dt):
+    """Every phase of the input against every phase of the output, in long rows of several
+    parts and in short ones; what lies around the rows stays."""
+    n = g()
+    N, R, V = shape
+    r = gen(14)
+    gl = torch.randn(N, R, generator=r, device="cuda")
+    gh = torch.randn(N, R, generator=r, device="cuda")
+    y = torch.randint(0, V, (N, R), generator=r, device="cuda")
+    y.view(-1)[0], y.view(-1)[-1] = 0, V - 1
+    plain = (torch.randn(N, R, V, generator=r, device="cuda") * 2).to(dt)
+    for at in range(16 // plain.element_size()):
+        for pad_in, pad_out in ((0, 1), (1, 0), (8, 8)):
+            buf = torch.full((N * R * (V + pad_in) + at,), math.inf, dtype=dt, device="cuda")
+            z = buf[at:].view(N, R, V + pad_in)[:, :, :V]
+            z.copy_(plain)
+            out = n.grpo_token_stats(z, y)
+            full = torch.full((N * R * (V + pad_out) + 16,), 9.0, dtype=dt, device="cuda")
+            rows = full[8:-8].view(N, R, V + pad_out)
+            n.grpo_token_stats_bwd(z, y, out["norm"], out["entropy"], gl, gh, out=rows[:, :, :V])
+            check_grad(z, y, gl, gh, rows[:, :, :V])
+            assert (rows[:, :, V:] == 9).all() and (full[:8] == 9).all() and (full[-8:] == 9).all()
+
+
 def test_gradient_against_differences():
     """Central differences of the float64 definition, every entry."""
     n = g()

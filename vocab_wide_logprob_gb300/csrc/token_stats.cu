@@ -937,14 +937,75 @@ __device__ __forceinline__ void grad_vectors(const T* z, uint4* out, int nvec, u
   }
 }
 
+// At most kStagedVecs vectors of gradients by a thread block, of logits at any alignment,
+// through shared memory: all copies are on their way at once, and a vector is put together
+// from two there.
+constexpr int kPieceVecs = 2 * kThreads, kPieces = 4, kStagedVecs = kPieces * kPieceVecs;
+template <typename T>
+__device__ __forceinline__ void grad_staged(uint4* stage, const T* z, uint4* out, int nvec,
+                                            unsigned shift, const RowGrad& q, int64_t y) {
+  using E = Elt<T>;
+  constexpr int EPV = E::kPerVec;
+  const uint4* zvec = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(z) - shift);
+  const int ky = y >= 0 && y < (int64_t)nvec * EPV ? (int)(y / EPV) : -1;
+  const int ey = ky >= 0 ? (int)(y % EPV) : 0;
+  const int tid = threadIdx.x, in = nvec + (nvec > 0 && shift != 0);
+  const uint32_t to = smem_u32(stage);
+#pragma unroll
+  for (int piece = 0; piece < kPieces; ++piece) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int k = piece * kPieceVecs + u * kThreads + tid;
+      if (k < in) cp_async16(to + 16 * k, zvec + k);
+    }
+    if (piece == kPieces - 1 && tid == 0 && in > kStagedVecs)
+      cp_async16(to + 16 * kStagedVecs, zvec + kStagedVecs);
+    cp_async_commit();
+  }
+#pragma unroll 1
+  for (int piece = 0; piece * kPieceVecs < nvec; ++piece) {
+    // this piece, and the next one's first vector
+    if (piece == 0)
+      cp_async_wait<kPieces - 2>();
+    else if (piece == 1)
+      cp_async_wait<kPieces - 3>();
+    else
+      cp_async_wait<0>();
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int k = piece * kPieceVecs + u * kThreads + tid;
+      if (k >= nvec) break;
+      uint4 d = ld_shared_v4(to + 16 * k);
+      if (shift != 0) d = from_two(d, ld_shared_v4(to + 16 * (k + 1)), shift);
+      float x[EPV], o[EPV];
+      E::unpack(d, x);
+#pragma unroll
+      for (int e = 0; e < EPV; ++e) o[e] = q.at(x[e]);
+      if (k == ky) {
+        const float zy = E::extract(d, ey);
+#pragma unroll
+        for (int e = 0; e < EPV; ++e)
+          if (e == ey) o[e] = q.at_token(zy);
+      }
+      st_stream(out + k, E::pack(o));
+    }
+  }
+  __syncthreads();  // (the stage is free)
+}
+
 // HBM-bound: 8,192 rows of 151,936 bf16, half of them scored, 554 us (99% of the copy
-// rate); rows whose gradient lies at another alignment 5.4 TB/s (2,000 of 151,935: 226 us).
-// Five thread blocks per SM: 99 us for 1,024 rows, 104 with four.
+// rate); rows whose gradient lies at another alignment 5.7 TB/s (2,000 of 151,935: 214 us;
+// 227 with two loads a vector instead of the stage, 32,768 rows of 9,001 216 and 271).
+// Five thread blocks per SM: 99 us for 1,024 rows, 104 with four; staged six: 222 with five.
 // kStep: threads to an item, a block's or a warp's.
-template <typename T, int kStep>
-__global__ void __launch_bounds__(kThreads, 5) token_stats_bwd_kernel(const StatsBwdParams<T> p) {
+// kStaged: through shared memory.
+template <typename T, int kStep, bool kStaged>
+__global__ void __launch_bounds__(kThreads, kStaged ? 6 : 5) token_stats_bwd_kernel(
+    const StatsBwdParams<T> p) {
   using E = Elt<T>;
   constexpr int EPV = E::kPerVec, kTeams = kThreads / kStep;
+  __shared__ uint4 stage[kStaged ? kStagedVecs + 1 : 1];
   const int tid = threadIdx.x % kStep;
   pdl_wait();
   pdl_trigger();
@@ -1003,10 +1064,13 @@ __global__ void __launch_bounds__(kThreads, 5) token_stats_bwd_kernel(const Stat
       y = yr;
       if (y < 0 || y >= p.V) q.A = NAN;
     }
-    if (shift == 0)
+    if constexpr (kStaged) {
+      grad_staged(stage, z + a, ovec, nvec, shift, q, y - a);
+    } else if (kStep == kThreads || shift == 0) {  // (blocks: shifted rows are staged)
       grad_vectors<T, false, kStep>(z + a, ovec, nvec, 0, q, y - a);
-    else
+    } else {
       grad_vectors<T, true, kStep>(z + a, ovec, nvec, shift, q, y - a);
+    }
     if (edge >= 0) {
       const float x = E::load1(z + edge);
       E::store1(out + edge, edge == y ? q.at_token(x) : q.at(x));
@@ -1107,7 +1171,7 @@ cudaError_t bwd_run(const TokenStatsBwdArgs& a, const DeviceInfo& d, cudaStream_
     p.split = 1;
     p.chunk = a.V;
     const int64_t blocks = (rows + kWarps - 1) / kWarps, most = 32 * (int64_t)d.sms;
-    return launch_pdl(token_stats_bwd_kernel<T, 32>, dim3((unsigned)(blocks < most ? blocks : most)),
+    return launch_pdl(token_stats_bwd_kernel<T, 32, false>, dim3((unsigned)(blocks < most ? blocks : most)),
                       dim3(kThreads), 0, st, 1, p);
   }
   // parts of a row of 32 KB or more (1,024 rows of 304 KB 99 us, whole rows 107); where
@@ -1116,10 +1180,27 @@ cudaError_t bwd_run(const TokenStatsBwdArgs& a, const DeviceInfo& d, cudaStream_
   p.split = row_split(row_bytes, nullptr, 8);
   while (rows * p.split < 4 * (int64_t)d.sms && row_bytes / (2 * p.split) >= 8192) p.split *= 2;
   p.chunk = ((a.V + p.split - 1) / p.split + EPV - 1) / EPV * EPV;
+  // Rows whose gradients lie at another alignment go through shared memory in parts that
+  // fit there.
+  const auto differ = [](int64_t x) { return x * (int64_t)sizeof(T) % 16 != 0; };
+  const bool staged =
+      ((reinterpret_cast<uintptr_t>(a.logits) ^ reinterpret_cast<uintptr_t>(a.dlogits)) & 15) != 0 ||
+      (a.N > 1 && differ(a.seq - a.dseq)) || (a.R > 1 && differ(a.row - a.drow));
+  if (staged) {
+    const int64_t most = (int64_t)kStagedVecs * EPV;
+    while (p.chunk > most) {
+      p.split *= 2;
+      p.chunk = ((a.V + p.split - 1) / p.split + EPV - 1) / EPV * EPV;
+    }
+  }
   const int64_t items = rows * p.split;
   int64_t grid = 256 * (int64_t)d.sms;
   if (grid > items) grid = items;
-  return launch_pdl(token_stats_bwd_kernel<T, kThreads>, dim3((unsigned)grid), dim3(kThreads), 0, st, 1, p);
+  if (staged)
+    return launch_pdl(token_stats_bwd_kernel<T, kThreads, true>, dim3((unsigned)grid),
+                      dim3(kThreads), 0, st, 1, p);
+  return launch_pdl(token_stats_bwd_kernel<T, kThreads, false>, dim3((unsigned)grid),
+                    dim3(kThreads), 0, st, 1, p);
 }
 
 }  // namespace
