@@ -1115,13 +1115,17 @@ cudaError_t stats_run(const TokenStatsArgs& a, const DeviceInfo& d, cudaStream_t
                ? launch_pdl(token_stats_short_kernel<T, false>, blocks, dim3(kThreads), 0, st, 1, p)
                : launch_pdl(token_stats_short_kernel<T, true>, blocks, dim3(kThreads), 0, st, 1, p);
   }
-  // whole rows where there are more than SMs for them (256 rows of 304 KB 19 us, in halves
-  // 20); below that as many CTAs as leave two per SM (64 rows 7.3 us in quarters, 12.4
-  // whole, 8.7 in eighths; one row 4.5 us in eighths, 11.9 whole) of a batch each
+  // whole rows where there are more than SMs for them (296 rows of 304 KB 18.0 us, in halves
+  // 18.9); below that as many CTAs as leave two per SM (64 rows 7.3 us in quarters, 12.4
+  // whole, 8.7 in eighths; one row 4.5 us in eighths, 11.9 whole) of a batch each, or three
+  // where each still has 128 KB (224 rows in halves 15.6 us, whole 17.6; of 128 KB rows 8.0
+  // and 7.9, of 64 KB 6.3 and 5.1; 80 rows of 1.2 MB in quarters 23.6, in halves 30.5)
   int split = 1;
-  while (split < kMaxSplit && 2 * split * rows <= 2 * (int64_t)d.sms &&
-         a.V * (int64_t)sizeof(T) >= 2 * split * kStageBytes)
+  while (split < kMaxSplit) {
+    const int64_t part = row_bytes / (2 * split);
+    if (part < kStageBytes || 2 * split * rows > (part >= 128 * 1024 ? 3 : 2) * (int64_t)d.sms) break;
     split *= 2;
+  }
   constexpr int EPV = Elt<T>::kPerVec;
   p.chunk = ((a.V + split - 1) / split + EPV - 1) / EPV * EPV;
   const dim3 grid((unsigned)(rows < 1 ? split : rows * split));
