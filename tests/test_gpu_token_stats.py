@@ -402,7 +402,7 @@ def test_gradient_of_views_into_views(dt):
 
 @pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("shape", [(1, 3, 40011), (2, 3, 16390), (2, 1, 16385), (3, 7, 65537),
-                                   (4, 100, 100), (2, 700, 1001), (1, 2, 9)], ids=str)
+                                   (4, 100, 100), (2, 700, 1001), (2, 800, 2503), (1, 2, 9)], ids=str)
 def test_gradient_of_rows_at_another_alignment(shape, dt):
     """Every phase of the input against every phase of the output, in long rows of several
     parts and in short ones; what lies around the rows stays."""

@@ -878,7 +878,42 @@ struct RowGrad {
   }
 };
 
-// The 16 bytes that begin `shift` bytes (a multiple of 2) into lo and hi.
+// Of one vector, two elements of a packed operation each; ey: the token's element, or -1.
+template <typename T>
+__device__ __forceinline__ uint4 grad_vector(const uint4& d, const RowGrad& q, int ey) {
+  using E = Elt<T>;
+  constexpr int EPV = E::kPerVec;
+  uint64_t x[EPV / 2];
+  pairs_of(d, x, T());
+  float o[EPV];
+#pragma unroll
+  for (int e = 0; e < EPV / 2; ++e) {
+    float a, b;
+    f2_unpack(f2_fma(f2_add(x[e], f2_pack(-q.m, -q.m)), f2_pack(q.c, q.c), f2_pack(-q.L2, -q.L2)), a, b);
+    a = max_keep_nan(a, kLowest);
+    b = max_keep_nan(b, kLowest);
+    const uint64_t f = f2_fma(f2_pack(q.B, q.B), f2_pack(a, b), f2_pack(q.A, q.A));
+    f2_unpack(f2_mul(f2_pack(ex2(a), ex2(b)), f), o[2 * e], o[2 * e + 1]);
+  }
+  if (ey >= 0) {
+    const float zy = E::extract(d, ey);
+#pragma unroll
+    for (int e = 0; e < EPV; ++e)
+      if (e == ey) o[e] = q.at_token(zy);
+  }
+  return E::pack(o);
+}
+
+// The 16 bytes that begin kWords words and `bits` bits into lo and hi.
+template <int kWords>
+__device__ __forceinline__ uint4 from_two(uint4 lo, uint4 hi, unsigned bits) {
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  return make_uint4(__funnelshift_r(w[kWords], w[kWords + 1], bits),
+                    __funnelshift_r(w[kWords + 1], w[kWords + 2], bits),
+                    __funnelshift_r(w[kWords + 2], w[kWords + 3], bits),
+                    __funnelshift_r(w[kWords + 3], w[kWords + 4], bits));
+}
+// `shift`: bytes, a multiple of 2.
 __device__ __forceinline__ uint4 from_two(uint4 lo, uint4 hi, unsigned shift) {
   uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
   if (shift & 8) {
@@ -889,9 +924,7 @@ __device__ __forceinline__ uint4 from_two(uint4 lo, uint4 hi, unsigned shift) {
 #pragma unroll
     for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
   }
-  const unsigned bits = (shift & 2) * 8;
-  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
-                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+  return from_two<0>(make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]), (shift & 2) * 8);
 }
 
 // nvec vectors of gradients by kStep threads; z: the first one's logits (kShift: `shift` bytes
@@ -903,7 +936,7 @@ __device__ __forceinline__ void grad_vectors(const T* z, uint4* out, int nvec, u
   constexpr int EPV = E::kPerVec, U = kShift ? 2 : 4;
   const uint4* zvec = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(z) - shift);
   const int ky = y >= 0 && y < (int64_t)nvec * EPV ? (int)(y / EPV) : -1;
-  const int ey = ky >= 0 ? (int)(y % EPV) : 0;
+  const int ey = ky >= 0 ? (int)(y % EPV) : -1;
   for (int k0 = threadIdx.x % kStep; k0 < nvec; k0 += kStep * U) {
     uint4 d[U], next[kShift ? U : 1];
 #pragma unroll
@@ -922,17 +955,7 @@ __device__ __forceinline__ void grad_vectors(const T* z, uint4* out, int nvec, u
       const int k = k0 + u * kStep;
       if (k >= nvec) break;
       if (kShift) d[u] = from_two(d[u], next[u], shift);
-      float x[EPV], o[EPV];
-      E::unpack(d[u], x);
-#pragma unroll
-      for (int e = 0; e < EPV; ++e) o[e] = q.at(x[e]);
-      if (k == ky) {
-        const float zy = E::extract(d[u], ey);
-#pragma unroll
-        for (int e = 0; e < EPV; ++e)
-          if (e == ey) o[e] = q.at_token(zy);
-      }
-      st_stream(out + k, E::pack(o));
+      st_stream(out + k, grad_vector<T>(d[u], q, k == ky ? ey : -1));
     }
   }
 }
@@ -941,14 +964,37 @@ __device__ __forceinline__ void grad_vectors(const T* z, uint4* out, int nvec, u
 // through shared memory: all copies are on their way at once, and a vector is put together
 // from two there.
 constexpr int kPieceVecs = 2 * kThreads, kPieces = 4, kStagedVecs = kPieces * kPieceVecs;
+template <typename T, int kWords>
+__device__ __forceinline__ void grad_of_stage(uint32_t from, uint4* out, int nvec, unsigned bits,
+                                              const RowGrad& q, int ky, int ey) {
+#pragma unroll 1
+  for (int piece = 0; piece * kPieceVecs < nvec; ++piece) {
+    // this piece, and the next one's first vector
+    if (piece == 0)
+      cp_async_wait<kPieces - 2>();
+    else if (piece == 1)
+      cp_async_wait<kPieces - 3>();
+    else
+      cp_async_wait<0>();
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int k = piece * kPieceVecs + u * kThreads + (int)threadIdx.x;
+      if (k >= nvec) break;
+      // (rows that agree take nothing of the second, whatever it holds)
+      const uint4 d = from_two<kWords>(ld_shared_v4(from + 16 * k), ld_shared_v4(from + 16 * (k + 1)), bits);
+      st_stream(out + k, grad_vector<T>(d, q, k == ky ? ey : -1));
+    }
+  }
+  __syncthreads();  // (the stage is free)
+}
 template <typename T>
 __device__ __forceinline__ void grad_staged(uint4* stage, const T* z, uint4* out, int nvec,
                                             unsigned shift, const RowGrad& q, int64_t y) {
-  using E = Elt<T>;
-  constexpr int EPV = E::kPerVec;
+  constexpr int EPV = Elt<T>::kPerVec;
   const uint4* zvec = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(z) - shift);
   const int ky = y >= 0 && y < (int64_t)nvec * EPV ? (int)(y / EPV) : -1;
-  const int ey = ky >= 0 ? (int)(y % EPV) : 0;
+  const int ey = ky >= 0 ? (int)(y % EPV) : -1;
   const int tid = threadIdx.x, in = nvec + (nvec > 0 && shift != 0);
   const uint32_t to = smem_u32(stage);
 #pragma unroll
@@ -962,46 +1008,27 @@ __device__ __forceinline__ void grad_staged(uint4* stage, const T* z, uint4* out
       cp_async16(to + 16 * kStagedVecs, zvec + kStagedVecs);
     cp_async_commit();
   }
-#pragma unroll 1
-  for (int piece = 0; piece * kPieceVecs < nvec; ++piece) {
-    // this piece, and the next one's first vector
-    if (piece == 0)
-      cp_async_wait<kPieces - 2>();
-    else if (piece == 1)
-      cp_async_wait<kPieces - 3>();
-    else
-      cp_async_wait<0>();
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int k = piece * kPieceVecs + u * kThreads + tid;
-      if (k >= nvec) break;
-      uint4 d = ld_shared_v4(to + 16 * k);
-      if (shift != 0) d = from_two(d, ld_shared_v4(to + 16 * (k + 1)), shift);
-      float x[EPV], o[EPV];
-      E::unpack(d, x);
-#pragma unroll
-      for (int e = 0; e < EPV; ++e) o[e] = q.at(x[e]);
-      if (k == ky) {
-        const float zy = E::extract(d, ey);
-#pragma unroll
-        for (int e = 0; e < EPV; ++e)
-          if (e == ey) o[e] = q.at_token(zy);
-      }
-      st_stream(out + k, E::pack(o));
-    }
-  }
-  __syncthreads();  // (the stage is free)
+  // (a loop for each of the four: none selects words)
+  const unsigned bits = shift % 4 * 8;
+  if (shift < 4)
+    grad_of_stage<T, 0>(to, out, nvec, bits, q, ky, ey);
+  else if (shift < 8)
+    grad_of_stage<T, 1>(to, out, nvec, bits, q, ky, ey);
+  else if (shift < 12)
+    grad_of_stage<T, 2>(to, out, nvec, bits, q, ky, ey);
+  else
+    grad_of_stage<T, 3>(to, out, nvec, bits, q, ky, ey);
 }
 
-// HBM-bound: 8,192 rows of 151,936 bf16, half of them scored, 554 us (99% of the copy
-// rate); rows whose gradient lies at another alignment 5.7 TB/s (2,000 of 151,935: 214 us;
-// 227 with two loads a vector instead of the stage, 32,768 rows of 9,001 216 and 271).
-// Five thread blocks per SM: 99 us for 1,024 rows, 104 with four; staged six: 222 with five.
-// kStep: threads to an item, a block's or a warp's.
+// HBM-bound: 8,192 rows of 151,936 bf16, half of them scored, 545 us (the copy rate); rows
+// whose gradient lies at another alignment 6.6 TB/s (2,000 of 151,935: 183 us, 227 with two
+// loads a vector instead of the stage).
+// Five thread blocks per SM: 99 us for 1,024 rows, 104 with four; staged six, 4% before five;
+// a warp per row four: 32,768 rows of 1,001 38 us, 41 with five, which spill.
+// kStep: threads to an item: a block's, or one or two warps'.
 // kStaged: through shared memory.
 template <typename T, int kStep, bool kStaged>
-__global__ void __launch_bounds__(kThreads, kStaged ? 6 : 5) token_stats_bwd_kernel(
+__global__ void __launch_bounds__(kThreads, kStaged ? 6 : kStep < kThreads ? 4 : 5) token_stats_bwd_kernel(
     const StatsBwdParams<T> p) {
   using E = Elt<T>;
   constexpr int EPV = E::kPerVec, kTeams = kThreads / kStep;
@@ -1169,34 +1196,33 @@ cudaError_t bwd_run(const TokenStatsBwdArgs& a, const DeviceInfo& d, cudaStream_
   p.dseq = a.dseq;
   p.drow = a.drow;
   const int64_t row_bytes = a.V * (int64_t)sizeof(T), rows = a.N * a.R;
-  // A warp per row where the rows are short and many: 32,768 rows of 1,000 bf16 29 us, 108
-  // with a thread block each; 4,096 of 4,096 16 and 20 us, 1,024 of them 8.2 and 7.2.
-  if (row_bytes <= 8192 && rows * 1024 >= row_bytes * d.sms) {
+  // A warp per row where the rows are short and many, two for somewhat longer ones: 32,768 rows
+  // of 1,000 bf16 28 us by warps, 40 by pairs, 97 by thread blocks; 4,001 105, 109 and 140;
+  // 2,048 rows of 1,000 3.8, 4.6 and 8.0, of 4,000 9.9, 8.8 and 10.3, of 8,000 16.8, 13.6 and
+  // 13.2; 600 rows of 2,000 4.0, 3.2 and 4.1, of 6,000 9.7, 6.5 and 5.2.
+  if (row_bytes <= 12288 && rows * 1024 >= row_bytes * d.sms) {
     p.split = 1;
     p.chunk = a.V;
-    const int64_t blocks = (rows + kWarps - 1) / kWarps, most = 32 * (int64_t)d.sms;
-    return launch_pdl(token_stats_bwd_kernel<T, 32, false>, dim3((unsigned)(blocks < most ? blocks : most)),
-                      dim3(kThreads), 0, st, 1, p);
+    const bool one = row_bytes <= 4096 && rows * 256 >= row_bytes * d.sms;
+    const int64_t teams = one ? kWarps : kWarps / 2;
+    const int64_t blocks = (rows + teams - 1) / teams, most = 32 * (int64_t)d.sms;
+    return launch_pdl(one ? token_stats_bwd_kernel<T, 32, false> : token_stats_bwd_kernel<T, 64, false>,
+                      dim3((unsigned)(blocks < most ? blocks : most)), dim3(kThreads), 0, st, 1, p);
   }
   // parts of a row of 32 KB or more (1,024 rows of 304 KB 99 us, whole rows 107); where
   // that leaves few, down to 8 KB (8 rows 3.2 us in 32 parts each, 6.3 in 4), but no more than
   // the SMs hold at once (1,024 rows of 64 KB 25 us whole, 40 in 8 parts)
   p.split = row_split(row_bytes, nullptr, 8);
   while (rows * p.split < 4 * (int64_t)d.sms && row_bytes / (2 * p.split) >= 8192) p.split *= 2;
-  p.chunk = ((a.V + p.split - 1) / p.split + EPV - 1) / EPV * EPV;
   // Rows whose gradients lie at another alignment go through shared memory in parts that
-  // fit there.
+  // fit there, as large as that (2,000 rows of 151,935 bf16 in 10 parts 183 us, in 16 199).
   const auto differ = [](int64_t x) { return x * (int64_t)sizeof(T) % 16 != 0; };
   const bool staged =
       ((reinterpret_cast<uintptr_t>(a.logits) ^ reinterpret_cast<uintptr_t>(a.dlogits)) & 15) != 0 ||
       (a.N > 1 && differ(a.seq - a.dseq)) || (a.R > 1 && differ(a.row - a.drow));
-  if (staged) {
-    const int64_t most = (int64_t)kStagedVecs * EPV;
-    while (p.chunk > most) {
-      p.split *= 2;
-      p.chunk = ((a.V + p.split - 1) / p.split + EPV - 1) / EPV * EPV;
-    }
-  }
+  constexpr int64_t kMost = (int64_t)kStagedVecs * EPV;
+  if (staged && p.split * kMost < a.V) p.split = (a.V + kMost - 1) / kMost;
+  p.chunk = ((a.V + p.split - 1) / p.split + EPV - 1) / EPV * EPV;
   const int64_t items = rows * p.split;
   int64_t grid = 256 * (int64_t)d.sms;
   if (grid > items) grid = items;
