@@ -537,6 +537,43 @@ def test_another_stream_and_a_graph():
         assert torch.equal(dout, dwant)
 
 
+def test_graphs_that_share_a_workspace_and_streams_side_by_side():
+    """Two captured graphs with the same outputs and workspace, replayed in turn; then
+    calls of different sizes on two streams at once, each with its own."""
+    n = g()
+    cases = [(draw(6, 3, 9001, BF16, 30), 8), (draw(3, 2, 40011, F32, 31), 8)]
+    names = ("logp", "entropy", "norm", "top_tokens", "top_logp")
+    want = [n.grpo_token_stats(z, y, top=top) for (z, y), top in cases]
+    ws = torch.empty(n.grpo_token_stats_workspace_size(6, 3), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for k, ((z, y), top) in enumerate(cases):
+        outs.append({x: torch.empty_like(want[k][x]) for x in names})
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[k]):
+            n.grpo_token_stats(z, y, top=top, out=outs[k], workspace=ws)
+    for k in (0, 1, 1, 0, 1, 0):
+        for o in outs[k].values():
+            if isinstance(o, torch.Tensor) and o is not ws:
+                o.zero_()
+        graphs[k].replay()
+        torch.cuda.synchronize()
+        assert n.grpo_check_error(ws) == 0
+        for x in names:
+            assert torch.equal(outs[k][x], want[k][x]), (k, x)
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(8):
+        for k, ((z, y), top) in enumerate(cases):
+            with torch.cuda.stream(side[k]):
+                got[k].append(n.grpo_token_stats(z, y, top=top))
+    torch.cuda.synchronize()
+    for k in (0, 1):
+        for o in got[k]:
+            for x in names:
+                assert torch.equal(o[x], want[k][x]), (k, x)
+
+
 def test_rows_beyond_two_to_the_31_elements():
     """The last sequence's rows start past 2^32 elements' bytes."""
     n = g()

@@ -60,6 +60,15 @@ def test_token_stats_refusals(lib):
                       ("top_logp", 0x70002), ("ws", 0x80010)):
         assert _stats(lib, **{name: A(bad)}) == MISALIGNED, name
     assert _stats(lib, ws_bytes=256) == WORKSPACE
+    outs = ("logp", "H", "norm", "top_tokens", "top_logp", "ws")
+    for name in outs:  # over an input, over another output
+        for at in (0x100000, 0x20000):
+            assert _stats(lib, **{name: A(at)}) == INVALID, name
+        assert _stats(lib, **{name: A(0x90000), "lens": A(0x90004)}) == INVALID, name
+        assert _stats(lib, **{name: A(0x90000), "temp": A(0x90004)}) == INVALID, name
+        for other in outs:
+            if other != name:
+                assert _stats(lib, **{name: A(0x90000), other: A(0x90000)}) == INVALID, (name, other)
     out = ctypes.c_size_t(0)
     assert lib.grpo_token_stats_workspace_size(4, 3, ctypes.byref(out)) == OK
     assert out.value >= 256 + 4 * 12
@@ -95,7 +104,7 @@ def test_token_stats_bwd_refusals(lib):
         assert _bwd(lib, **{name: A(bad)}) == MISALIGNED, name
     assert _bwd(lib, dz=A(0x100000)) == INVALID           # in place
     assert _bwd(lib, dz=A(0x100000 + 2 * 599)) == INVALID  # over the last element
-    for name in ("norm", "H", "gl", "gh", "tokens"):
+    for name in ("norm", "H", "gl", "gh", "tokens", "lens", "temp"):
         assert _bwd(lib, **{name: A(0x200000 + 8)}) == INVALID, name
     assert _bwd(lib, N=0) == OK                            # nothing to do
 

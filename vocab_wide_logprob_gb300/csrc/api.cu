@@ -950,8 +950,12 @@ bool tokens_fit(int64_t N, int64_t R, int64_t seq, int64_t row) {
   const int64_t across = mul3(N, seq, 16), along = mul3(R, row, 16);
   return across >= 0 && along >= 0 && across <= INT64_MAX / 2 && along <= INT64_MAX / 2;
 }
+// (of one row or more)
 size_t rows_bytes(int64_t N, int64_t R, int64_t V, int64_t seq, int64_t row, grpo_dtype t) {
   return ((size_t)(N - 1) * (size_t)seq + (size_t)(R - 1) * (size_t)row + (size_t)V) * esize_of(t);
+}
+Span token_span(const int64_t* tokens, int64_t N, int64_t R, int64_t seq, int64_t row) {
+  return span(tokens, 8 * (size_t)((N - 1) * seq + (R - 1) * row + 1));
 }
 
 constexpr int64_t kMaxEmbedDim = (int64_t)1 << 24;
@@ -1242,6 +1246,19 @@ grpo_status grpo_token_stats(const void* logits, grpo_dtype dtype, int64_t N, in
       (top > 0 && (!aligned(top_tokens, 8) || !aligned(top_logp, 4))) || !aligned(workspace, 256))
     return GRPO_ERR_MISALIGNED;
   if (workspace_bytes < token_stats_workspace_bytes(N, R)) return GRPO_ERR_WORKSPACE;
+  if (rows > 0) {
+    const size_t n = (size_t)rows, alternatives = n * (size_t)top;
+    const Span writes[6] = {span(workspace, token_stats_workspace_bytes(N, R)), span(logp, 4 * n),
+                            span(entropy, 4 * n), span(norm, 8 * n),
+                            span(top_tokens, 8 * alternatives), span(top_logp, 4 * alternatives)};
+    for (int k = 1; k < 6; ++k)
+      if (overlaps(writes, k, writes[k])) return GRPO_ERR_INVALID_ARG;
+    const Span reads[4] = {span(logits, rows_bytes(N, R, V, logits_seq, logits_row, dtype)),
+                           token_span(tokens, N, R, token_seq, token_row),
+                           span(len, 4 * (size_t)N), span(temperature, 4 * (size_t)N)};
+    for (const Span& r : reads)
+      if (overlaps(writes, 6, r)) return GRPO_ERR_INVALID_ARG;
+  }
   DeviceInfo dev;
   if (current_device(&dev) != cudaSuccess) return GRPO_ERR_CUDA;
   stream_take_last(stream);
@@ -1291,15 +1308,17 @@ grpo_status grpo_token_stats_bwd(const void* logits, grpo_dtype dtype, int64_t N
       !aligned(tokens, 8) || !aligned(len, 4) || !aligned(temperature, 4) || !aligned(norm, 8) ||
       !aligned(entropy, 4) || !aligned(grad_logp, 4) || !aligned(grad_entropy, 4))
     return GRPO_ERR_MISALIGNED;
-  const size_t nd = rows_bytes(N, R, V, dlogits_seq, dlogits_row, dtype);
-  if (overlap(dlogits, nd, logits, rows_bytes(N, R, V, logits_seq, logits_row, dtype)) ||
-      overlap(dlogits, nd, norm, 8 * (size_t)rows) ||
-      (entropy != nullptr && overlap(dlogits, nd, entropy, 4 * (size_t)rows)) ||
-      (grad_logp != nullptr && overlap(dlogits, nd, grad_logp, 4 * (size_t)rows)) ||
-      (grad_entropy != nullptr && overlap(dlogits, nd, grad_entropy, 4 * (size_t)rows)) ||
-      (tokens != nullptr &&
-       overlap(dlogits, nd, tokens, 8 * (size_t)((N - 1) * token_seq + (R - 1) * token_row + 1))))
-    return GRPO_ERR_INVALID_ARG;
+  const Span out = span(dlogits, rows_bytes(N, R, V, dlogits_seq, dlogits_row, dtype));
+  const size_t n = (size_t)rows;
+  const Span reads[8] = {span(logits, rows_bytes(N, R, V, logits_seq, logits_row, dtype)),
+                         token_span(tokens, N, R, token_seq, token_row),
+                         span(len, 4 * (size_t)N),
+                         span(temperature, 4 * (size_t)N),
+                         span(norm, 8 * n),
+                         span(entropy, 4 * n),
+                         span(grad_logp, 4 * n),
+                         span(grad_entropy, 4 * n)};
+  if (overlaps(reads, 8, out)) return GRPO_ERR_INVALID_ARG;
   DeviceInfo dev;
   if (current_device(&dev) != cudaSuccess) return GRPO_ERR_CUDA;
   stream_take_last(stream);
