@@ -39,6 +39,24 @@ __device__ __forceinline__ float max_keep_nan(float a, float b) {
   return r;
 }
 
+// Loads that are issued here (the compiler moves others down to where their value is
+// wanted, which is at the end of a row's chain).
+__device__ __forceinline__ int64_t load_now(const int64_t* p) {
+  int64_t x;
+  asm volatile("ld.global.nc.s64 %0, [%1];" : "=l"(x) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ float load_now(const float* p) {
+  float x;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(x) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ float load_now(const uint16_t* p) {
+  uint16_t x;
+  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(x) : "l"(p));
+  return bf16_bits_to_float(x);
+}
+
 // The temperature of sequence i: 1 for greedy ones, NaN for one that is none.
 __device__ __forceinline__ float warmth_of(const float* temperature, int64_t i) {
   const float T = temperature != nullptr ? __ldg(temperature + i) : 1.f;
@@ -173,6 +191,14 @@ __device__ __forceinline__ uint16_t bits_of(float x, uint16_t) {
 __device__ __forceinline__ float value_of(float x) { return x; }
 __device__ __forceinline__ float value_of(uint16_t x) { return bf16_bits_to_float(x); }
 
+__device__ __forceinline__ uint32_t raw_of(float x) { return __float_as_uint(x); }
+__device__ __forceinline__ uint32_t raw_of(uint16_t x) { return x; }
+// The float behind x.
+__device__ __forceinline__ float next_above(float x) {
+  const int b = __float_as_int(x + 0.f);
+  return __int_as_float(b >= 0 ? b + 1 : b - 1);
+}
+
 // The bound: the top-th largest of the 64 sets' maxima, lower sets first; four threads
 // count what is before one.  Between two barriers.
 __device__ __forceinline__ void find_bound(TopShared& sh, int top) {
@@ -193,22 +219,22 @@ __device__ __forceinline__ void find_bound(TopShared& sh, int top) {
 }
 
 // emit(place, key) for the first `top` of late.key[0 .. have): a key's place is the number
-// of keys before it (they are all different, but for zeros, which are none); eight threads
-// count for one.
+// of keys before it (they are all different, but for zeros, which are none); up to eight
+// threads count for one.
 template <typename Emit>
 __device__ __forceinline__ void emit_places(const Late& late, int have, int top, Emit emit) {
   const int tid = threadIdx.x;
+  int team = 8;
+  while (team > 1 && have * team > kThreads) team /= 2;
 #pragma unroll 1
-  for (int k0 = 0; k0 < have; k0 += kThreads / 8) {
-    const int k = k0 + tid / 8;
+  for (int k0 = 0; k0 < have; k0 += kThreads / team) {
+    const int k = k0 + tid / team;
     const uint64_t mine = k < have ? late.key[k] : 0;
     int place = 0;
 #pragma unroll 4
-    for (int j = tid % 8; j < have; j += 8) place += late.key[j] > mine;
-    place += __shfl_xor_sync(0xffffffffu, place, 1);
-    place += __shfl_xor_sync(0xffffffffu, place, 2);
-    place += __shfl_xor_sync(0xffffffffu, place, 4);
-    if (tid % 8 == 0 && mine != 0 && place < top) emit(place, mine);
+    for (int j = tid % team; j < have; j += team) place += late.key[j] > mine;
+    for (int o = 1; o < team; o *= 2) place += __shfl_xor_sync(0xffffffffu, place, o);
+    if (tid % team == 0 && mine != 0 && place < top) emit(place, mine);
   }
 }
 
@@ -221,6 +247,7 @@ __device__ __forceinline__ void best_of_part(TopShared& sh, Late& late, const T 
                                              const Part<T>& p, uint32_t kept, int top, Emit emit) {
   using E = Elt<T>;
   constexpr int EPV = E::kPerVec, U = kBatch;
+  constexpr uint32_t kNan = sizeof(T) == 2 ? 0x7fc07fc0u : 0x7fc00000u;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t n = p.v1 - p.v0;
   bool listed = false;
@@ -231,28 +258,28 @@ __device__ __forceinline__ void best_of_part(TopShared& sh, Late& late, const T 
     listed = true;
   }
   const float bound = sh.bound;
+  // Appends one of each lane's chosen at a time: store(place, which), `chosen` a bit each.
+  const auto append = [&](uint32_t chosen, int* count, auto store) {
+    uint32_t votes;
+    while ((votes = __ballot_sync(0xffffffffu, chosen != 0)) != 0) {
+      int at = 0;
+      if (lane == 0) at = atomicAdd(count, __popc(votes));  // (one addition a warp)
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(votes & ((1u << lane) - 1));
+      if (chosen != 0) store(at, __ffs(chosen) - 1);
+      chosen &= chosen - 1;
+    }
+  };
   // with the ties at the bound, or (where they are too many) without them
 #pragma unroll 1
   for (int strict = 0; strict < 2 && !listed; ++strict) {
-    uint32_t votes[kSlots];
-    int mine = 0;
+    const float least = strict ? next_above(bound) : bound;
+    uint32_t groups = 0;
 #pragma unroll
-    for (int g = 0; g < kSlots; ++g) {
-      const float x = g <= p.groups ? value_of(slot[g][tid]) : NAN;
-      votes[g] = __ballot_sync(0xffffffffu, strict ? x > bound : x >= bound);
-      mine += __popc(votes[g]);
-    }
-    if (mine > 0) {  // (one addition a warp)
-      int at = 0;
-      if (lane == 0) at = atomicAdd(&sh.hits, mine);
-      at = __shfl_sync(0xffffffffu, at, 0);
-#pragma unroll
-      for (int g = 0; g < kSlots; ++g) {
-        const int k = at + __popc(votes[g] & ((1u << lane) - 1));
-        if ((votes[g] >> lane & 1) && k < kHits) late.hit[k] = g * kThreads + tid;
-        at += __popc(votes[g]);
-      }
-    }
+    for (int g = 0; g < kSlots; ++g)
+      if (g <= p.groups && value_of(slot[g][tid]) >= least) groups |= 1u << g;
+    append(groups, &sh.hits, [&](int at, int g) {
+      if (at < kHits) late.hit[at] = g * kThreads + tid;
+    });
     __syncthreads();
     const int hits = sh.hits;
     if (hits <= kHits) {
@@ -263,51 +290,38 @@ __device__ __forceinline__ void best_of_part(TopShared& sh, Late& late, const T 
 #pragma unroll 1
       for (unsigned first = 0; first < items; first += kAhead * kThreads) {
         uint4 d[kAhead];
-        int64_t id[kAhead];  // of the vector's first element, or none; a ragged end's alone
-        bool alone[kAhead];
+        int64_t id[kAhead];  // of the vector's first element
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
           const unsigned w = first + u * kThreads + tid;
-          id[u] = -1;
-          alone[u] = false;
-          if (u > 0 && first + u * kThreads >= items) break;
+          id[u] = 0;
+          d[u] = make_uint4(kNan, kNan, kNan, kNan);  // (never chosen)
           if (w >= items) continue;
           const unsigned q = divide ? w / each : __umulhi(w, p.inverse), rest = w - q * each;
           const int h = late.hit[q], t = h % kThreads, g = h / kThreads;
           const int at = (g * (int)each + (int)rest) * kThreads + t;
-          if (g == p.groups) {
+          if (g == p.groups) {  // a ragged end's element alone
             if (rest != 0) continue;
-            alone[u] = true;
             id[u] = t < 32 ? p.v0 + t : p.b + t - 32;
+            d[u].x = (sizeof(T) == 2 ? kNan << 16 : 0u) | raw_of(p.z[id[u]]);
           } else if (at < p.nvec) {
             id[u] = p.a + (int64_t)at * EPV;
             d[u] = kept != 0 ? ld_shared_v4(kept + 16 * at) : ld_stream(p.z + id[u]);
           }
         }
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          if (u > 0 && first + u * kThreads >= items) break;
+#pragma unroll 1
+        for (int u = 0; u < kAhead && first + u * kThreads < items; ++u) {
           float x[EPV];
-          E::unpack(d[u], x);
-          if (alone[u]) x[0] = E::load1(p.z + id[u]);
-          uint32_t votes[EPV];
-          int mine = 0;
+          E::unpack(d[0], x);
+          uint32_t chosen = 0;
 #pragma unroll
-          for (int e = 0; e < EPV; ++e) {
-            const bool there = id[u] >= 0 && (e == 0 || !alone[u]);
-            votes[e] = __ballot_sync(0xffffffffu, there && (strict ? x[e] > bound : x[e] >= bound));
-            mine += __popc(votes[e]);
-          }
-          if (mine == 0) continue;  // (one addition a warp)
-          int at = 0;
-          if (lane == 0) at = atomicAdd(&sh.keys, mine);
-          at = __shfl_sync(0xffffffffu, at, 0);
-#pragma unroll
-          for (int e = 0; e < EPV; ++e) {
-            const int k = at + __popc(votes[e] & ((1u << lane) - 1));
-            if ((votes[e] >> lane & 1) && k < kCandidates) late.key[k] = key_of(x[e], id[u] + e);
-            at += __popc(votes[e]);
-          }
+          for (int e = 0; e < EPV; ++e)
+            if (x[e] >= least) chosen |= 1u << e;
+          append(chosen, &sh.keys, [&](int at, int e) {
+            if (at < kCandidates) late.key[at] = key_of(E::extract(d[0], e), id[0] + e);
+          });
+          d[0] = d[1];
+          id[0] = id[1];
         }
       }
     }
@@ -366,29 +380,38 @@ __device__ __forceinline__ void best_of_part(TopShared& sh, Late& late, const T 
   emit_places(late, sh.keys, top, emit);
 }
 
-// The best `top` of the cluster's lists, each sorted.  The last of a list of `top` keys has
-// as many before it, and so have together the lists' keys at the place top / parts: only
-// what reaches the larger of the two is looked at.
+// Sorts a warp's keys, whose lanes first rise and then fall (or the other way): largest
+// first, or last.
+__device__ __forceinline__ uint64_t sort_merged(uint64_t key, bool first) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
+    key = ((lane & o) == 0) == first ? max(key, other) : min(key, other);
+  }
+  return key;
+}
+
+// The best `top` of the cluster's lists, each sorted and filled up with zeros: one warp merges
+// them two by two, a lane a place.  (Of a list that falls and one that rises, the larger one at
+// each place are the best 32 of both; K. Batcher's merge sorts them.)
 template <typename Emit>
-__device__ __forceinline__ void merge_parts(TopShared& sh, Late& late, int parts, int top, Emit emit) {
-  const int list = threadIdx.x / kMaxTop, at = threadIdx.x % kMaxTop;
-  const int share = (top + parts - 1) / parts;
-  uint64_t least = 1, all = ~0ull;  // (of a key)
+__device__ __forceinline__ void merge_parts(const TopShared& sh, int parts, int top, Emit emit) {
+  const int lane = threadIdx.x;
+  if (lane >= 32) return;
+  static_assert(kMaxSplit == 8 && kMaxTop == 32, "a place per lane, three rounds");
+  uint64_t key[kMaxSplit];
 #pragma unroll
   for (int k = 0; k < kMaxSplit; ++k)
-    if (k < parts) {
-      least = max(least, sh.part_key[k][top - 1]);
-      all = min(all, sh.part_key[k][share - 1]);
-    }
-  least = max(least, all);
-  const uint64_t mine = list < parts && at < top ? sh.part_key[list][at] : 0;
-  const uint32_t votes = __ballot_sync(0xffffffffu, mine >= least);
-  int first = 0;
-  if (at == 0 && votes != 0) first = atomicAdd(&sh.ties, __popc(votes));
-  first = __shfl_sync(0xffffffffu, first, 0);
-  if (mine >= least) late.key[first + __popc(votes & ((1u << at) - 1))] = mine;
-  __syncthreads();
-  emit_places(late, sh.ties, top, emit);
+    key[k] = k < parts ? sh.part_key[k][k % 2 == 0 ? lane : 31 - lane] : 0;
+#pragma unroll
+  for (int far = 1; far < kMaxSplit; far *= 2) {
+    if (far >= parts) break;
+#pragma unroll
+    for (int k = 0; k < kMaxSplit; k += 2 * far)
+      key[k] = sort_merged(max(key[k], key[k + far]), k / (2 * far) % 2 == 0);
+  }
+  if (key[0] != 0 && lane < top) emit(lane, key[0]);
 }
 
 __device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
@@ -485,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
   const float Ti = warmth_of(p.temperature, i);
   const float c = kLog2e / Ti;
   // (used behind the stream)
-  const int64_t y = writer ? __ldg(p.tokens + i * p.token_seq + j * p.token_row) : -1;
+  const int64_t y = writer ? load_now(p.tokens + i * p.token_seq + j * p.token_row) : -1;
   Sums sum;
   const uint64_t c2 = f2_pack(c, c);
   int batch = 0, st = 0, last = 0;  // the batch's stage, and the one before
@@ -543,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
     sum.top = fmaxf(sum.top, group_max);
     if (kTop) slot[g][tid] = bits_of(group_max, T());
   }
-  const float at_token = y >= 0 && y < p.V ? E::load1(part.z + y) : 0.f;
+  const float at_token = y >= 0 && y < p.V ? load_now(part.z + y) : 0.f;
   {  // a ragged end's element
     int64_t v = -1;
     if (tid < part.a - part.v0)
@@ -614,24 +637,27 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
         best_of_part(top, late, slot, part, kept, p.top,
                      [&](int place, uint64_t key) { st_cluster_u64(to + 8 * place, key); });
       if (tid >= got && tid < kMaxTop) st_cluster_u64(to + 8 * tid, 0);
-      if (tid == 0) top.ties = 0;  // (counts the lists' keys next)
     }
     if (tid == 0)
       st_cluster_f32x4(map_to_rank(smem_u32(&sh.part[rank]), 0), make_float4(m, s, e, sh.abort != 0 ? 1.f : 0.f));
     __syncwarp();
     cluster_sync();
     if (rank != 0) return;
-    m = sh.part[0].x;
-    for (int k = 1; k < (int)parts; ++k) m = fmaxf(m, sh.part[k].x);
-    s = e = 0.f;
-    for (int k = 0; k < (int)parts; ++k) {
-      const float4 q = sh.part[k];
-      // (a part of nothing but -inf has sums 0)
-      const float d = fmaxf((q.x - m) * c, kLowest), f = ex2(d);
-      s += f * q.y;
-      e += f * fmaf(d, q.y, q.z);
-      if (q.w != 0.f) flags |= kFlagTimeout;
+    // (a lane a part, in every eight; a part of nothing but -inf has sums 0)
+    const int k = lane % kMaxSplit;
+    const float4 q = sh.part[min(k, (int)parts - 1)];
+    m = q.x;
+#pragma unroll
+    for (int o = kMaxSplit / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float d = fmaxf((q.x - m) * c, kLowest), f = k < (int)parts ? ex2(d) : 0.f;
+    s = f * q.y;
+    e = f * fmaf(d, q.y, q.z);
+#pragma unroll
+    for (int o = kMaxSplit / 2; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      e += __shfl_xor_sync(0xffffffffu, e, o);
     }
+    if (__any_sync(0xffffffffu, q.w != 0.f)) flags |= kFlagTimeout;
   }
   // (a comparison with NaN is false)
   const bool defined = s > 0.f && s < INFINITY && fabsf(m) < INFINITY && c > 0.f;
@@ -660,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
     p.top_logp[r * p.top + place] = (key_value(key) - m) / Ti - L;
   };
   if (parts > 1)
-    merge_parts(top, late, (int)parts, p.top, write);
+    merge_parts(top, (int)parts, p.top, write);
   else
     best_of_part(top, late, slot, part, kept, p.top, write);
 }
