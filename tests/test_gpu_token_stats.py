@@ -42,7 +42,7 @@ def warmth(T):
 class Ref:
     """The statistics of one sequence's rows [n, V] in float64."""
 
-    def __init__(self, z, T=1.0):
+    def __init__(self, z, T=1.0, lanes=512):
         z = z.double()
         self.T = float(T)
         self.m = z.amax(-1, keepdim=True)
@@ -56,14 +56,14 @@ class Ref:
         self.D = -px.sum(-1, keepdim=True)
         self.H = self.L + self.D
         self.x = x
-        self.delta = (4 * self.D + 28 + z.shape[-1] / 512) * U
+        self.delta = (4 * self.D + 28 + z.shape[-1] / lanes) * U
 
 
 def order(z, top):
     return z.double().sort(dim=-1, descending=True, stable=True).indices[..., :top]
 
 
-def check(z, tokens, out, top=0, lens=None, T=None, rows=None):
+def check(z, tokens, out, top=0, lens=None, T=None, lanes=512):
     N, R, V = z.shape
     for i in range(N):
         n = R if lens is None else max(0, min(R, int(lens[i])))
@@ -73,7 +73,7 @@ def check(z, tokens, out, top=0, lens=None, T=None, rows=None):
             assert (out["top_tokens"][i, n:] == -1).all()
         if n == 0:
             continue
-        r = Ref(z[i, :n], 1.0 if T is None else warmth(T[i:i + 1]).item())
+        r = Ref(z[i, :n], 1.0 if T is None else warmth(T[i:i + 1]).item(), lanes)
         y = tokens[i, :n].unsqueeze(-1)
 
         def near(have, lp, at):
@@ -116,6 +116,24 @@ def test_stats(shape, dt, top):
     assert n.grpo_check_error(out["workspace"]) == 0
     assert ("top_tokens" in out) == (k > 0)
     check(z, y, out, k)
+
+
+@pytest.mark.parametrize("shape, dt, top", [((8, 510, 16411), F32, 0), ((16, 300, 8191), BF16, 5),
+                                            ((5, 900, 31999), BF16, 0), ((9, 150, 8003), F32, 9)],
+                         ids=str)
+def test_many_rows(shape, dt, top):
+    """Rows enough that longer ones take a warp each, whose lanes add V / 64 numbers: every
+    97th against float64, and all of them bit for bit with a second call's."""
+    n = g()
+    z, y = draw(*shape, dt, 3)
+    out = n.grpo_token_stats(z, y, top=top)
+    assert n.grpo_check_error(out["workspace"]) == 0
+    some = torch.arange(0, shape[0] * shape[1], 97, device="cuda")
+    flat = {k: v.flatten(0, 1)[some][None] for k, v in out.items() if k != "workspace"}
+    check(z.flatten(0, 1)[some][None], y.flatten()[some][None], flat, top, lanes=64)
+    again = n.grpo_token_stats(z, y, top=top)
+    for k in flat:
+        assert torch.equal(out[k], again[k]), k
 
 
 @pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])

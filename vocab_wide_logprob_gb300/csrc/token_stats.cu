@@ -238,7 +238,7 @@ __device__ __forceinline__ void emit_places(const Late& late, int have, int top,
   }
 }
 
-// The best `top` of the part's elements (all of them if it has fewer): emit(place, key)
+// The best `top` of the part's elements (it has as many): emit(place, key)
 // for each, by the thread that found it.  Called by the whole CTA after the stream, with
 // the bound known.  slot[g][thread]: maxima of groups.  kept: where the part's vectors still
 // lie in shared memory, or 0.
@@ -249,14 +249,7 @@ __device__ __forceinline__ void best_of_part(TopShared& sh, Late& late, const T 
   constexpr int EPV = E::kPerVec, U = kBatch;
   constexpr uint32_t kNan = sizeof(T) == 2 ? 0x7fc07fc0u : 0x7fc00000u;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t n = p.v1 - p.v0;
   bool listed = false;
-  if (n <= kCandidates) {
-    for (int64_t v = tid; v < n; v += kThreads) late.key[v] = key_of(E::load1(p.z + p.v0 + v), p.v0 + v);
-    if (tid == 0) sh.keys = (int)n;
-    __syncthreads();
-    listed = true;
-  }
   const float bound = sh.bound;
   // Appends one of each lane's chosen at a time: store(place, which), `chosen` a bit each.
   const auto append = [&](uint32_t chosen, int* count, auto store) {
@@ -631,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_kernel(const StatsPar
     __syncwarp();  // (the cluster's barriers want whole warps)
     cluster_wait();
     if (kTop) {
-      const int got = sh.abort != 0 ? 0 : (int)min(part.v1 - part.v0, (int64_t)p.top);
+      const int got = sh.abort != 0 ? 0 : p.top;
       const uint32_t to = map_to_rank(smem_u32(&top.part_key[rank][0]), 0);
       if (got > 0)
         best_of_part(top, late, slot, part, kept, p.top,
@@ -1157,12 +1150,16 @@ cudaError_t stats_run(const TokenStatsArgs& a, const DeviceInfo& d, cudaStream_t
   p.top_logp = a.top_logp;
   p.hdr = static_cast<WsHeader*>(a.ws);
   const int64_t rows = a.N * a.R;
-  // A warp per row where the rows are short and many (top alternatives take a warp longer):
-  // 32,768 rows of 1,000 bf16 22 us, 175 with a thread block each (with 5 alternatives 47
-  // and 349); 1,024 of 4,096 4.6 and 7.6 us, 300 of them 4.5 and 3.8; 4,096 of 16,384 with 5
-  // alternatives 49 and 57, 1,024 of them 23 and 17.
+  // A warp per row where the rows are short and many; by warps and by thread blocks, without
+  // alternatives, with 5 and with 20 (bf16, us): 600 rows of 2 KB 2.5 and 4.2, 4.8 and 7.8, 7.3
+  // and 8.4; 1,200 of 8 KB 4.0 and 7.7, 8.1 and 14.3, 12.4 and 15.0; 300 of 8 KB 3.9 and 3.1,
+  // 7.4 and 5.5, 11.8 and 5.8; 2,400 of 32 KB 17.9 and 21.6, 26.4 and 33.1, 34.4 and 34.6; 4,800
+  // of 64 KB 50.7 and 61.2, 93 and 87, 97 and 90; 3,600 of 128 KB 85 and 76.  Rows of which a
+  // block's sets have a few elements each always (8 rows of 1 KB 2.3 and 2.7, 4.0 and 4.7, 6.8
+  // and 20).
   const int64_t row_bytes = a.V * (int64_t)sizeof(T);
-  if (row_bytes <= 1024 || (row_bytes <= 32768 && rows * 2048 >= row_bytes * d.sms * (a.top > 0 ? 2 : 1))) {
+  if (row_bytes <= 1024 || (row_bytes <= (a.top == 0 ? 131072 : 32768) &&
+                            rows * 2560 >= row_bytes * d.sms * (a.top > 8 ? 2 : 1))) {
     const dim3 blocks((unsigned)((rows + kWarps - 1) / kWarps + (rows == 0)));
     return a.top == 0
                ? launch_pdl(token_stats_short_kernel<T, false>, blocks, dim3(kThreads), 0, st, 1, p)
