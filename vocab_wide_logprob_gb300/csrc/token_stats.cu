@@ -374,20 +374,34 @@ __device__ __forceinline__ void best_of_part(TopShared& sh, Late& late, const T 
 }
 
 // Sorts a warp's keys, whose lanes first rise and then fall (or the other way): largest
-// first, or last.
-__device__ __forceinline__ uint64_t sort_merged(uint64_t key, bool first) {
-  const int lane = threadIdx.x & 31;
+// first, or last.  (K. Batcher's merge.)
+template <typename K>
+__device__ __forceinline__ K exchanged(K key, int o, bool first) {
+  const K other = __shfl_xor_sync(0xffffffffu, key, o);
+  return ((threadIdx.x & o) == 0) == first ? max(key, other) : min(key, other);
+}
+template <typename K>
+__device__ __forceinline__ K sort_merged(K key, bool first) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
-    key = ((lane & o) == 0) == first ? max(key, other) : min(key, other);
+  for (int o = 16; o > 0; o >>= 1) key = exchanged(key, o, first);
+  return key;
+}
+// In any order before, in the first `count` lanes (the others' are 0).
+template <typename K>
+__device__ __forceinline__ K sort_keys(K key, bool first, int count = 32) {
+#pragma unroll
+  for (int size = 2; size <= 32; size *= 2) {
+    if (size / 2 >= count) break;  // (sorted, the largest first)
+#pragma unroll
+    for (int o = size / 2; o > 0; o >>= 1)
+      key = exchanged(key, o, size == 32 ? first : (threadIdx.x & size) == 0);
   }
   return key;
 }
 
 // The best `top` of the cluster's lists, each sorted and filled up with zeros: one warp merges
 // them two by two, a lane a place.  (Of a list that falls and one that rises, the larger one at
-// each place are the best 32 of both; K. Batcher's merge sorts them.)
+// each place are the best 32 of both.)
 template <typename Emit>
 __device__ __forceinline__ void merge_parts(const TopShared& sh, int parts, int top, Emit emit) {
   const int lane = threadIdx.x;
@@ -710,18 +724,25 @@ struct Best {
 
 // The top-th largest of 64 values, two a lane: a warp's lower bound of the top-th
 // largest element where each is the largest of a set.
+// (By repeated maxima, or for more of them sorted: 32,768 rows of 1,000 bf16 with 20 53 us by
+// sorting and 58 by maxima, with 5 44 and 42.)
 __device__ __forceinline__ float warp_bound(float set0, float set1, int top) {
   const auto ordered = [](float x) { return (uint32_t)(key_of(x, 0) >> 32); };
   uint32_t hi = ordered(fmaxf(set0, set1)), lo = ordered(fminf(set0, set1)), best = 0;
+  if (top > 8) {
+    best = sort_merged(max(sort_keys(hi, true), sort_keys(lo, false)), true);
+    best = __shfl_sync(0xffffffffu, best, top - 1);
+  } else {
 #pragma unroll 1
-  for (int k = 0; k < top; ++k) {
-    best = __reduce_max_sync(0xffffffffu, hi);
-    if ((threadIdx.x & 31) == __ffs(__ballot_sync(0xffffffffu, hi == best)) - 1) {
-      hi = lo;
-      lo = 0;  // (below every value)
+    for (int k = 0; k < top; ++k) {
+      best = __reduce_max_sync(0xffffffffu, hi);
+      if ((threadIdx.x & 31) == __ffs(__ballot_sync(0xffffffffu, hi == best)) - 1) {
+        hi = lo;
+        lo = 0;  // (below every value)
+      }
     }
   }
-  return best == 0 ? -INFINITY : key_value((uint64_t)best << 32);
+  return key_value((uint64_t)best << 32);
 }
 
 // What token_stats_kernel computes.  A row takes one warp longer than a thread block, but
@@ -833,27 +854,67 @@ __global__ void __launch_bounds__(kThreads, 4) token_stats_short_kernel(const St
     *status = flags;
   }
   if (!kTop) return;
+  // The candidates as a list that the warp sorts, up to two keys a lane; where there are more
+  // (ties, crowds in few sets), by insertion of one after the other (32,768 rows of 1,000 bf16
+  // with 20 72 us, 58 as lists; with 5 46 and 42).
+  constexpr int kList = 64;
+  __shared__ uint64_t lists[kTop ? kWarps : 1][kList];
+  uint64_t* const list = lists[kTop ? threadIdx.x / 32 : 0];
   Best best;
   if (defined) {
     const float bound = warp_bound(set0, set1, p.top);
-    best.take(ragged >= 0 && end >= bound, end, ragged, p.top);
+    int count = 0;
+    const auto append = [&](uint32_t chosen, auto key) {
+      uint32_t votes;
+      while ((votes = __ballot_sync(0xffffffffu, chosen != 0)) != 0) {
+        const int at = count + __popc(votes & ((1u << lane) - 1));
+        if (chosen != 0 && at < kList) list[at] = key(__ffs(chosen) - 1);
+        count += __popc(votes);
+        chosen &= chosen - 1;
+      }
+    };
+    // each(vector, its first element, whether it is one) where one of the warp's has candidates
+    const auto second_look = [&](auto each) {
 #pragma unroll 1
-    for (int k0 = lane; k0 - lane < nvec; k0 += 32 * U) {
-      uint4 d[U];
-      load(d, k0);
+      for (int k0 = lane; k0 - lane < nvec; k0 += 32 * U) {
+        uint4 d[U];
+        load(d, k0);
+        if (!__any_sync(0xffffffffu, E::template batch_max<U>(d) >= bound)) continue;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const bool there = k0 + 32 * u < nvec;
-        if (!__any_sync(0xffffffffu, there && E::template batch_max<1>(d + u) >= bound)) continue;
+        for (int u = 0; u < U; ++u) {
+          const bool there = k0 + 32 * u < nvec;
+          if (__any_sync(0xffffffffu, there && E::template batch_max<1>(d + u) >= bound))
+            each(d[u], a + (k0 + 32 * u) * EPV, there);
+        }
+      }
+    };
+    append(ragged >= 0 && end >= bound, [&](int) { return key_of(end, ragged); });
+    second_look([&](const uint4& d, int v, bool there) {
+      float x[EPV];
+      E::unpack(d, x);
+      uint32_t chosen = 0;
+#pragma unroll
+      for (int q = 0; q < EPV; ++q)
+        if (there && x[q] >= bound) chosen |= 1u << q;
+      append(chosen, [&](int q) { return key_of(E::extract(d, q), v + q); });
+    });
+    __syncwarp();
+    if (count <= kList) {
+      best.mine = sort_keys(lane < count ? list[lane] : 0, true, count);
+      if (count > 32)
+        best.mine = sort_merged(
+            max(best.mine, sort_keys(lane + 32 < count ? list[lane + 32] : 0, false)), true);
+    } else {
+      best.take(ragged >= 0 && end >= bound, end, ragged, p.top);
+      second_look([&](const uint4& d, int v, bool there) {
         float x[EPV];
-        E::unpack(d[u], x);
+        E::unpack(d, x);
 #pragma unroll
         for (int q = 0; q < EPV; ++q) {
           const bool wanted = there && x[q] >= bound;
-          if (__any_sync(0xffffffffu, wanted))
-            best.take(wanted, x[q], a + (int64_t)(k0 + 32 * u) * EPV + q, p.top);
+          if (__any_sync(0xffffffffu, wanted)) best.take(wanted, x[q], v + q, p.top);
         }
-      }
+      });
     }
   }
   if (lane < p.top) {
@@ -1151,12 +1212,12 @@ cudaError_t stats_run(const TokenStatsArgs& a, const DeviceInfo& d, cudaStream_t
   p.hdr = static_cast<WsHeader*>(a.ws);
   const int64_t rows = a.N * a.R;
   // A warp per row where the rows are short and many; by warps and by thread blocks, without
-  // alternatives, with 5 and with 20 (bf16, us): 600 rows of 2 KB 2.5 and 4.2, 4.8 and 7.8, 7.3
-  // and 8.4; 1,200 of 8 KB 4.0 and 7.7, 8.1 and 14.3, 12.4 and 15.0; 300 of 8 KB 3.9 and 3.1,
-  // 7.4 and 5.5, 11.8 and 5.8; 2,400 of 32 KB 17.9 and 21.6, 26.4 and 33.1, 34.4 and 34.6; 4,800
-  // of 64 KB 50.7 and 61.2, 93 and 87, 97 and 90; 3,600 of 128 KB 85 and 76.  Rows of which a
-  // block's sets have a few elements each always (8 rows of 1 KB 2.3 and 2.7, 4.0 and 4.7, 6.8
-  // and 20).
+  // alternatives, with 5 and with 20 (bf16, us): 600 rows of 2 KB 2.5 and 4.2, 4.4 and 7.8, 5.6
+  // and 8.3; 1,200 of 8 KB 4.0 and 7.7, 7.1 and 14.2, 9.7 and 14.8; 300 of 8 KB 3.8 and 3.2,
+  // 6.8 and 5.4, 9.4 and 5.8; 2,400 of 32 KB 18.1 and 21.6, 25.3 and 32.8, 31.2 and 34.3 (with
+  // 32 44 and 36); 4,800 of 64 KB 51 and 61, 93 and 86, 96 and 89; 3,600 of 128 KB 85 and 76.
+  // Rows of which a block's sets have a few elements each always (8 rows of 1 KB 2.3 and 2.6,
+  // 3.9 and 4.7, 5.2 and 20).
   const int64_t row_bytes = a.V * (int64_t)sizeof(T);
   if (row_bytes <= 1024 || (row_bytes <= (a.top == 0 ? 131072 : 32768) &&
                             rows * 2560 >= row_bytes * d.sms * (a.top > 8 ? 2 : 1))) {
