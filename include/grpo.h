@@ -628,9 +628,10 @@ grpo_status grpo_verify_drafts(const void *target_logits, const void *draft_logi
  * GRPO_ERR_VALUE by grpo_check_error; a token outside [0, V) logp NaN
  * (GRPO_ERR_TOKEN_RANGE); a length outside [0, R] is clamped
  * (GRPO_ERR_LENGTH_RANGE).
- * Sums are float32 per thread, added in a fixed order: results are bitwise
- * reproducible.  workspace: at least grpo_token_stats_workspace_size(N, R)
- * bytes (a word per row).
+ * Sums are float32 per thread, added in a fixed order: a call repeated gives the same
+ * bits.  (That order follows the sizes and a row's address modulo 16 bytes: the same row in
+ * another batch may differ in its last bits.)  workspace: at least
+ * grpo_token_stats_workspace_size(N, R) bytes (a word per row).
  */
 grpo_status grpo_token_stats_workspace_size(int64_t N, int64_t R, size_t *bytes);
 grpo_status grpo_token_stats(const void *logits, grpo_dtype dtype, int64_t N, int64_t R, int64_t V,

@@ -274,6 +274,52 @@ def test_masks(dt, V):
     check(z, y, out, 7)
 
 
+@pytest.mark.parametrize("V, copies", [(33, 1), (250, 1), (250, 400), (2039, 300)])
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_masks_of_short_rows(dt, V, copies):
+    """Rows that a warp takes, with more candidates than its list holds and with
+    hardly any."""
+    n = g()
+    inf, low = float("inf"), LOWEST[dt]
+    r = gen(40)
+    rows = []
+    base = (torch.randn(V, generator=r, device="cuda") * 3).to(dt)
+    for fill in (-inf, low):
+        rows.append(base.masked_fill(torch.rand(V, generator=r, device="cuda") < 0.9, fill))
+        few = torch.full((V,), fill, device="cuda", dtype=dt)
+        few[torch.randint(0, V, (3,), generator=r, device="cuda")] = 1.5
+        rows.append(few)
+    one = torch.full((V,), -inf, device="cuda", dtype=dt)
+    one[V - 1] = -7.0
+    rows.append(one)
+    zeros = torch.zeros(V, device="cuda", dtype=dt)
+    zeros[::3] = -0.0
+    rows += [zeros, torch.full((V,), 3.25, device="cuda", dtype=dt),
+             base.sort().values, base.sort(descending=True).values]
+    for k in (20, 31, 32, 33, 63, 64, 65):  # equal ones at the border, over and under the list's size
+        ties = torch.full((V,), 1.0, device="cuda", dtype=dt)
+        ties[torch.randperm(V, generator=r, device="cuda")[:k]] = 2.0
+        rows.append(ties)
+    crowd = base.clone()  # in the vectors of one lane
+    for k in range(0, V - 8, 256):
+        crowd[k:k + 8] = 20.0 + torch.rand(8, generator=r, device="cuda").to(dt)
+    rows.append(crowd)
+    z = torch.stack(rows).unsqueeze(1)
+    y = z.float().argmax(-1)
+    for top in (1, 8, 9, 32):
+        out = n.grpo_token_stats(z.repeat(copies, 1, 1), y.repeat(copies, 1), top=top)
+        assert n.grpo_check_error(out["workspace"]) == 0
+        N = z.shape[0]
+        # (the order of a row's sums follows its address's remainder by 16 bytes: copies 16 apart
+        # share it, others agree to the tolerance only)
+        for c in range(min(copies, 16)):
+            check(z, y, {k: v[c * N:(c + 1) * N] for k, v in out.items() if k != "workspace"}, top,
+                  lanes=64)
+            for k in ("logp", "entropy", "norm", "top_tokens", "top_logp"):
+                v = out[k].view(copies, N, -1)[c::16]
+                assert torch.equal(v, v[:1].expand_as(v)), k
+
+
 @pytest.mark.parametrize("V", [9, 700, 40000])
 @pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
 def test_rows_without_a_distribution(dt, V):
