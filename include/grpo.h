@@ -708,6 +708,10 @@ typedef struct {
  * instead), since it divides.  A block whose largest |m'| is below 2^-80 is
  * stored as 0.  Everything up to the codes is rounded operation by operation as written.  Zeroed states and scales are those of the first step.
  *
+ * A finite gradient whose square leaves float32 (above some 10^19) makes v' infinite and its
+ * quotient 0: the element only decays.  With 8-bit states its root is then stored as the
+ * larger of 2^64 (the float below it) and |m'|, so that its block keeps a finite scale.
+ *
  * tensors: HOST array (read before the call returns; the pointers in it are
  * device pointers, aligned to their element, and what is written overlaps nothing
  * else; params that overlap one another are refused).  Arrays that are all
