@@ -151,3 +151,25 @@ def test_from_both_ends_at_once(bits):
     was = keep(params, state)
     n.grpo_adamw_step(params, grads, state, 1, LR, beta1=B1, beta2=B2, eps=0.0, weight_decay=DECAY)
     check(was, params, grads, state, 1, 0.0)
+
+
+def test_unused_rows_keep_the_code_zero():
+    """What never had a gradient keeps the zero bytes that it began with, alone or beside
+    others of its block."""
+    n = g()
+    r = torch.Generator(device="cuda")
+    r.manual_seed(4)
+    for pt in (F32, BF16):
+        p = [torch.randn(s, generator=r, device="cuda").to(pt) for s in (4096, 100, 2500)]
+        state = n.grpo_adamw_state(p, 8)
+        grads = [torch.randn(x.shape, generator=r, device="cuda") for x in p]
+        used = [torch.rand(x.shape, generator=r, device="cuda") < 0.5 for x in p]
+        used[0][1024:2048] = False
+        for x, u in zip(grads, used):
+            x.mul_(u)
+        for step in (1, 2, 3):
+            n.grpo_adamw_step(p, grads, state, step, LR, weight_decay=DECAY)
+            for key in ("exp_avg", "exp_avg_root"):
+                for code, u in zip(state[key], used):
+                    assert not code.view(torch.uint8)[~u].any(), key
+            assert all((c.view(torch.uint8)[u] > 0).all() for c, u in zip(state["exp_avg_root"], used))

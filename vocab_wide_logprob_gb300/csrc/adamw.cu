@@ -393,18 +393,14 @@ __device__ __forceinline__ void step8(const Arrays<W, G, State, Value>& t, int e
       x.m.set(k, quotient(new_m[k], both(-sm), both(im)));
       x.v.set(k, quotient(new_v[k], both(sr), both(-ir)));
     }
-    // a positive root stays positive: codes that are 0 (found four at a time)
+    // a positive root stays positive: a code that is 0 becomes 1 (a root of 0 has the code of
+    // -0 this far, which its sign gives away)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       uint32_t& w = x.v.w[j];
-      if (((w - 0x01010101u) & ~w & 0x80808080u) != 0) {
-        float r[4];
-        f2_unpack(new_v[2 * j], r[0], r[1]);
-        f2_unpack(new_v[2 * j + 1], r[2], r[3]);
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          if ((w >> (8 * b) & 0xffu) == 0 && r[b] < 0.f && ir > 0.f) w |= 1u << (8 * b);
-      }
+      // (0x80 in the bytes that are 0: no byte's sum passes into the next)
+      const uint32_t zero = ~(((w & 0x7f7f7f7fu) + 0x7f7f7f7fu) | w) & 0x80808080u;
+      w = (w & 0x7f7f7f7fu) | zero >> 7;
     }
     if ((threadIdx.x & 31) == 0) t.scales[e / kStateBlock] = make_float2(sm, sr);
   } else {
