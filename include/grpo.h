@@ -717,7 +717,8 @@ typedef struct {
  * else; params that overlap one another are refused).  Arrays that are all
  * 16-byte aligned (e4m3 codes: 8) move in wide accesses.
  * beta1, beta2 in [0, 1), lr, eps, weight_decay, norm_eps >= 0 and finite (with eps 0 an
- * element that never had a gradient is 0 / 0),
+ * element that never had a gradient is 0 / 0; an eps between 0 and 2^-126 counts as 2^-126,
+ * none is above 2^126),
  * max_norm >= 0 (infinity: no limit), step >= 1 (step_dev's value too).
  * With step_dev and lr_dev a captured call can be replayed with other values.
  */

@@ -173,3 +173,19 @@ def test_unused_rows_keep_the_code_zero():
                 for code, u in zip(state[key], used):
                     assert not code.view(torch.uint8)[~u].any(), key
             assert all((c.view(torch.uint8)[u] > 0).all() for c, u in zip(state["exp_avg_root"], used))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-50, 1e-40, 2.0 ** -127, 2.0 ** -126, 1e-30])
+def test_an_eps_below_the_normal_range(eps, bits):
+    """Keeps elements that never had a gradient from 0 / 0, as any other does."""
+    n = g()
+    params, state, gradients = start(n, [3000], "f32", [F32], bits, 5, (-9, -3))
+    for step in (1, 2):
+        grads = gradients()
+        grads[0][::3] = 0.0
+        grads[0][512:1024] = 0.0
+        was = keep(params, state)
+        n.grpo_adamw_step(params, grads, state, step, LR, beta1=B1, beta2=B2, eps=eps, weight_decay=DECAY)
+        # (beside roots of 10^-11 and more all of these are nothing)
+        check(was, params, grads, state, step, max(eps, 2.0 ** -126))

@@ -244,3 +244,9 @@ def test_package_exports():
     for name in ("grpo_token_stats", "grpo_token_stats_bwd", "grpo_adamw_state", "grpo_adamw_step",
                  "GRPOTokenStats", "grpo_logp_entropy"):
         assert callable(getattr(pkg, name))
+
+
+def test_adamw_eps_without_a_reciprocal(lib):
+    assert _adamw(lib, [], eps=2.0 ** 126) == OK
+    for x in (2.0 ** 126 * 1.01, 3e38):
+        assert _adamw(lib, [], eps=x) == INVALID, x

@@ -558,7 +558,8 @@ cudaError_t launch_adamw(const AdamwArgs& a, const DeviceInfo& d, cudaStream_t s
   h.beta2 = (float)a.beta2;
   h.one_minus1 = (float)(1.0 - a.beta1);
   h.one_minus2 = (float)(1.0 - a.beta2);
-  h.eps = (float)a.eps;
+  // (what is below float32's normal numbers would be 0 to the reciprocal, and 0 / 0 a NaN)
+  h.eps = a.eps > 0.0 ? fmaxf((float)a.eps, 0x1p-126f) : 0.f;
   h.decay = (float)a.decay;
   h.ln_beta1 = (float)log(a.beta1);
   h.ln_beta2 = (float)log(a.beta2);

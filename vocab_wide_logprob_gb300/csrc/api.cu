@@ -1353,7 +1353,8 @@ grpo_status grpo_adamw_step(const grpo_adamw_tensor* tensors, int64_t count, int
   if (count > INT32_MAX) return GRPO_ERR_UNSUPPORTED;
   const grpo_adamw_hyper& h = *hyper;
   const auto size = [](double x) { return x >= 0.0 && x <= 3e38; };  // a float32 magnitude
-  if (!(h.beta1 >= 0.0 && h.beta1 < 1.0) || !(h.beta2 >= 0.0 && h.beta2 < 1.0) || !size(h.eps) ||
+  if (!(h.beta1 >= 0.0 && h.beta1 < 1.0) || !(h.beta2 >= 0.0 && h.beta2 < 1.0) ||
+      !(h.eps >= 0.0 && h.eps <= 0x1p126) ||  // (its reciprocal is a normal number)
       !size(h.weight_decay) || (h.lr_dev == nullptr && !size(h.lr)) ||
       (h.step_dev == nullptr && h.step < 1))
     return GRPO_ERR_INVALID_ARG;
