@@ -149,3 +149,41 @@ def test_the_update_in_a_graph():
     torch.cuda.synchronize()
     assert torch.equal(param, eager)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_each_step_with_8_bit_states():
+    """Every element of every step, from the states that it found: the update takes them as the
+    numbers they are and uses its own moments unrounded, so that the bound is that of states in
+    float32 (off by some 1e-6 of a step's size, and by half a step of float32 at 1)."""
+    import vocab_wide_logprob_gb300 as grpo
+    from vocab_wide_logprob_gb300 import autograd
+    ids, lens, adv, embed, head = inputs(4)
+    params = [embed, head]
+    state = grpo.grpo_adamw_state(params, 8)
+
+    def value(codes, k, j):
+        n = codes.numel()
+        each = state["scales"][k][:, j].double().repeat_interleave(256)[:n]
+        return (codes.reshape(-1).float().double() * each).view(codes.shape)
+
+    for step in range(1, 5):
+        embed.requires_grad_()
+        head.requires_grad_()
+        logits = autograd.grpo_embed(ids, embed) @ head.t()
+        logp, entropy = autograd.grpo_logp_entropy(logits[:, P - 1:-1], ids[:, P:], lens)
+        grads = list(torch.autograd.grad(loss_of(logp, entropy, lens, adv), (embed, head)))
+        embed.requires_grad_(False)
+        head.requires_grad_(False)
+        stats, _ = grpo.grpo_grad_norm(grads)
+        coef = min(1.0, LIMIT / (float(stats[0]) + 1e-6))
+        want = []
+        for k, p in enumerate(params):
+            g = grads[k].double() * coef
+            m = BETA1 * value(state["exp_avg"][k], k, 0) + (1 - BETA1) * g
+            v = BETA2 * value(state["exp_avg_root"][k], k, 1) ** 2 + (1 - BETA2) * g * g
+            up = m / (1 - BETA1 ** step) / ((v / (1 - BETA2 ** step)).sqrt() + EPS)
+            want.append(p.double() - LR * (up + DECAY * p.double()))
+        grpo.grpo_adamw_step(params, grads, state, step, LR, beta1=BETA1, beta2=BETA2, eps=EPS,
+                             weight_decay=DECAY, norm=stats, max_norm=LIMIT)
+        for p, w in zip(params, want):
+            assert (p.double() - w).abs().max() <= 3e-5 * LR
