@@ -61,19 +61,6 @@ struct Now {
   float coef, lr, inv_c1, inv_root_c2;
 };
 
-template <int CAP>
-__device__ __forceinline__ int find_tensor(const Table<CAP>& t, int64_t chunk) {
-  int lo = 0, hi = t.count;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (t.first[mid] <= chunk)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  return lo;
-}
-
 // ---- 8 consecutive elements ------------------------------------------------------
 
 // As they are stored, in registers.
@@ -202,11 +189,6 @@ __device__ __forceinline__ void store(const Raw8<T>& r, T* p, bool wide, int n) 
     r.store_some(p, n);
 }
 
-__device__ __forceinline__ float max_keep_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 // The block's scale from a lane's largest value (not negative: its bits are ordered
 // as it is, NaN above all), and its reciprocal by one Newton step.
 __device__ __forceinline__ float block_scale(float largest, float& inverse) {

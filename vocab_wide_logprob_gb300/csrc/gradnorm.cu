@@ -35,19 +35,6 @@ struct Table {
   int count;
 };
 
-template <int CAP>
-__device__ __forceinline__ int find_tensor(const Table<CAP>& t, int64_t chunk) {
-  int lo = 0, hi = t.count;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (t.first[mid] <= chunk)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  return lo;
-}
-
 // ---------------------------------------------------------------------------
 // norm
 // ---------------------------------------------------------------------------
@@ -89,11 +76,6 @@ __device__ __forceinline__ void add_squares(Acc& a, const float* x, float top) {
   pair_add(a.hi, a.lo, (s0 + s1) + (s2 + s3));
 }
 
-// max that keeps NaN
-__device__ __forceinline__ float max_nan(float a, float b) {
-  return a != a ? a : (b != b ? b : fmaxf(a, b));
-}
-
 template <typename T, bool kMax>
 __device__ __forceinline__ void chunk_norm(Acc& acc, const T* data, int64_t numel, int64_t e0) {
   using E = Elt<T>;
@@ -116,7 +98,7 @@ __device__ __forceinline__ void chunk_norm(Acc& acc, const T* data, int64_t nume
   if (tid < a - e0) edge = E::load1(data + e0 + tid);
   if (tid >= 32 && tid - 32 < e1 - b) edge = E::load1(data + b + tid - 32);
   if (kMax) {
-    acc.hi = max_nan(acc.hi, fabsf(edge));
+    acc.hi = max_keep_nan(acc.hi, fabsf(edge));
   } else if (edge != 0.f) {
     const float ed[4] = {edge, 0.f, 0.f, 0.f};
     add_squares<4>(acc, ed, fabsf(edge));
@@ -129,7 +111,7 @@ __device__ __forceinline__ void chunk_norm(Acc& acc, const T* data, int64_t nume
     for (int u = 0; u < kVecs / 2; ++u) E::unpack(d[h * (kVecs / 2) + u], x + u * EPV);
     if (kMax) {
 #pragma unroll
-      for (int k = 0; k < kVecs / 2 * EPV; ++k) acc.hi = max_nan(acc.hi, fabsf(x[k]));
+      for (int k = 0; k < kVecs / 2 * EPV; ++k) acc.hi = max_keep_nan(acc.hi, fabsf(x[k]));
     } else {
       float top = 0.f;
 #pragma unroll
@@ -155,7 +137,7 @@ __device__ __forceinline__ double block_total(Acc a) {
       const float hi = __shfl_xor_sync(0xffffffffu, a.hi, o);
       const float lo = __shfl_xor_sync(0xffffffffu, a.lo, o);
       if (kMax) {
-        a.hi = max_nan(a.hi, hi);
+        a.hi = max_keep_nan(a.hi, hi);
       } else {
         // (the smaller lane's value first in both, so that both get the same bits)
         float h = (lane & o) ? hi : a.hi, l = ((lane & o) ? lo : a.lo) + ((lane & o) ? a.lo : lo);

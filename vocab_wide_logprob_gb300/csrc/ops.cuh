@@ -20,6 +20,27 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// max that keeps NaN
+__device__ __forceinline__ float max_keep_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// The tensor of a table (first[k]: the chunk that tensor k begins with) that a chunk is of.
+template <typename Table>
+__device__ __forceinline__ int find_tensor(const Table& t, int64_t chunk) {
+  int lo = 0, hi = t.count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (t.first[mid] <= chunk)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
 // One element at a shared-memory address, as float.
 __device__ __forceinline__ float lds_elt(uint32_t at, uint16_t) {
   uint16_t v;

@@ -32,13 +32,6 @@ constexpr float kMinTemperature = 1e-6f;  // below it a temperature counts as 0:
 constexpr float kLowest = -150.f;         // 2^kLowest is 0 in ex2's range
 constexpr float kSlack = 8.f;             // sums may grow to 2^8 of their reference
 
-// max that keeps NaN
-__device__ __forceinline__ float max_keep_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 // Loads that are issued here (the compiler moves others down to where their value is
 // wanted, which is at the end of a row's chain).
 __device__ __forceinline__ int64_t load_now(const int64_t* p) {
