@@ -1,5 +1,6 @@
-"""AdamW steps so large that a thread block takes two units of a tensor: tensors that
-end in either unit, at any alignment, beside a large one.  Tolerances as for small ones."""
+"""AdamW steps so large that a thread block may take two units of a tensor (where params and
+gradients differ in type): tensors that end in either unit, at any alignment, beside a
+large one.  Tolerances as for small ones."""
 import pytest
 import torch
 
@@ -19,10 +20,11 @@ def sizes():
 
 
 @pytest.mark.parametrize("phases", [(0,), (1, 8, 3, 0)], ids=["aligned", "mixed"])
+@pytest.mark.parametrize("gts", [[F32], [BF16], [F32, BF16]], ids=["g32", "g16", "gmix"])
 @pytest.mark.parametrize("kind", small.KINDS, ids=[k[0] for k in small.KINDS])
-def test_two_units_a_block(kind, phases):
+def test_large_steps(kind, gts, phases):
     n = small.g()
-    was = small.make(sizes(), kind[1], [F32, BF16], 8, kind[2], 30, phases)
+    was = small.make(sizes(), kind[1], gts, 8, kind[2], 30, phases)
     place = lambda k, t: None if t is None else small.at_phase(t, phases[k % len(phases)])
     now = ([place(k, t) for k, t in enumerate(was[0])], [place(k, t) for k, t in enumerate(was[1])],
            {key: [t.clone() if key == "scales" else place(k, t) for k, t in enumerate(v)]
@@ -34,7 +36,7 @@ def test_two_units_a_block(kind, phases):
 def test_a_second_unit_with_squares_outside_float32s_range():
     """Each unit's v' that is infinite or tiny is its own affair."""
     n = small.g()
-    was = small.make(sizes(), [F32], [F32], 8, False, 31)
+    was = small.make(sizes(), [BF16], [F32], 8, False, 31)
     big = max(range(len(ENDS) + 1), key=lambda k: was[1][k].numel())
     grad = was[1][big]
     grad[UNIT + 5] = 1e25
@@ -43,7 +45,7 @@ def test_a_second_unit_with_squares_outside_float32s_range():
     n.grpo_adamw_step(*now, 7, 1e-3, **small.HYPER)
     # (an infinite v': the weight only decays)
     w = was[0][big][UNIT + 5].double()
-    assert (now[0][big][UNIT + 5].double() - w * (1 - 1e-3 * small.HYPER["weight_decay"])).abs() <= 2.0 ** -23 * w.abs()
+    assert (now[0][big][UNIT + 5].double() - w * (1 - 1e-3 * small.HYPER["weight_decay"])).abs() <= 2.0 ** -8 * 1.001 * w.abs()
     assert now[2]["scales"][big].isfinite().all() and now[0][big].isfinite().all()
     # everything but that element's block as ever
     cut = lambda t, size: torch.cat([t[:UNIT // 256 * size], t[(UNIT // 256 + 1) * size:]])

@@ -443,11 +443,13 @@ __device__ __forceinline__ void chunk_step(W* param, float* master, const G* gra
   }
 }
 
-// Thread blocks per SM: with 8-bit states the arithmetic (48 instructions an element)
+// Thread blocks per SM: with 8-bit states the arithmetic (some 50 instructions an element)
 // fills half the issue slots, and what hides the loads and the two reductions is other
-// warps: 494 M elements take 1,035 us with six blocks (some registers spilled), 1,104 with
-// five, 1,167 with four; 1,084 with four that fetch a unit ahead, 1,245 with a ring of
-// asynchronous copies.  With 32-bit states four blocks keep HBM busy.
+// warps: 494 M elements take 994 us with six blocks (some registers spilled), 1,155 with
+// five, 1,263 with four (with masters five and six are within 2%).  Loads ahead of their use cost
+// more than they hide: before the root took any v', 1,084 us with four blocks that fetch a unit
+// ahead and 1,245 with a ring of asynchronous copies, where six blocks took 1,035.  With 32-bit
+// states four blocks keep HBM busy.
 template <int CAP, bool kEight>
 __global__ void __launch_bounds__(kThreads, kEight ? 6 : 4) adamw_kernel(const __grid_constant__ Table<CAP> t,
                                                             const __grid_constant__ Hyper h) {
@@ -553,13 +555,20 @@ cudaError_t launch_adamw(const AdamwArgs& a, const DeviceInfo& d, cudaStream_t s
   h.max_norm = (float)a.max_norm;
   h.norm_eps = (float)a.norm_eps;
   h.minus_zero = -0.f;
-  // A chunk of two units finds its tensor and its numbers once: 386 us for 183 M
-  // elements with 8-bit states, 399 with one.  Where that leaves fewer than 64 chunks
-  // per SM, chunks of one: 43.3 us for 19 M elements, 45.2 with two; also with 32-bit
-  // states, which the arithmetic does not bound (494 M: 1,949 us, 1,970 with two).
+  // Chunks of two units, which find their tensor and their numbers once, where params and
+  // gradients are of different types and no master is kept (8-bit states, 494 M elements:
+  // float32 params 988 us, 1,008 with one unit; bfloat16 931 and 961), and one for the others
+  // (float32 alone 1,127 us, 1,266 with two; bfloat16 alone 946 and 984; masters 1,262 and 1,432,
+  // 1,175 and 1,329; 32-bit states 1,941 and 1,964).  Where that leaves fewer than 64 chunks per
+  // SM, one: 11.6 M elements 29.0 us, 30.1 with two.
   int64_t all = 0;
-  for (int64_t k = 0; k < a.count; ++k) all += a.tensors[k].numel;
-  const int units = a.eight && all / (2 * kUnit) >= 64 * (int64_t)d.sms ? 2 : 1;
+  bool differ = true;
+  for (int64_t k = 0; k < a.count; ++k) {
+    const AdamwTensor& t = a.tensors[k];
+    all += t.numel;
+    differ = differ && t.master == nullptr && (t.dt == 1 || t.dt == 2);
+  }
+  const int units = a.eight && differ && all / (2 * kUnit) >= 64 * (int64_t)d.sms ? 2 : 1;
   // tensors in launches of at most kMaxTensors and 2^30 chunks
   int64_t k = 0;
   while (k < a.count) {
