@@ -612,7 +612,7 @@ grpo_status grpo_verify_drafts(const void *target_logits, const void *draft_logi
  *   top_tokens, top_logp: the `top` largest z_v, largest first, the lowest v of
  *             equal ones first, and their log-probs
  * -inf logits (banned tokens) have probability 0 and add nothing to the
- * entropy.  Rows j >= L_i are not read; they get logp, entropy, norm and
+ * entropy; so does a finite one whose z_v - m has no place in float32.  Rows j >= L_i are not read; they get logp, entropy, norm and
  * top_logp 0 and top_tokens -1.
  *
  * logits: row j of sequence i starts at element i * logits_seq + j *
@@ -706,7 +706,9 @@ typedef struct {
  * m' and v').  The root is what is stored because its range is half that of v
  * in powers of two; a positive root never becomes 0 (the smallest code, 2^-9,
  * instead), since it divides.  A block whose largest |m'| is below 2^-80 is
- * stored as 0.  Everything up to the codes is rounded operation by operation as written.  Zeroed states and scales are those of the first step.
+ * stored as 0.  Up to the codes every operation is rounded to float32 as written, products
+ * and sums apart (c and the scales are products with rounded reciprocals; the root is the nearest
+ * float32 but in about one of a million cases).  Zeroed states and scales are those of the first step.
  *
  * A finite gradient whose square leaves float32 (above some 10^19) makes v' infinite and its
  * quotient 0: the element only decays.  With 8-bit states its root is then stored as the

@@ -671,7 +671,8 @@ def grpo_token_stats(logits, tokens, lens=None, temperature=None, top=0, out=Non
     ``logp`` and ``entropy`` [N, R], ``norm`` [N, R, 2] (largest logit, log-sum) in
     float32, with ``top`` also ``top_tokens`` [N, R, top] int64 and ``top_logp``,
     and ``workspace``; pass it as ``out`` to reuse the buffers.  New outputs and
-    workspace share one allocation."""
+    workspace share one allocation: one that is kept keeps all of it (20 bytes a row and 12
+    per alternative), and ``torch.save`` of one writes all; ``clone()`` what outlives the rest."""
     return _ops.token_stats(logits, tokens, lens, temperature, top, out, workspace, stream)
 
 

@@ -13,8 +13,9 @@
 // a value, which the step itself never sees (it uses the unrounded m' and v').
 // A value next to a border between codes goes to one or the other by its last bit, so
 // everything up to the codes is rounded as the formula is written, operation by
-// operation (no fused products, the root and the quotients correctly rounded): the codes
-// are those of the same float32 formula anywhere.
+// operation: no fused products, the quotients correctly rounded, the root but in one of a
+// million cases, c and the scales as products with rounded reciprocals.  So the codes are
+// those of the same float32 formula anywhere, but for about as few.
 #include <math.h>
 
 #include <type_traits>

@@ -1097,7 +1097,8 @@ __device__ __forceinline__ void grad_staged(uint4* stage, const T* z, uint4* out
 // whose gradient lies at another alignment 6.6 TB/s (2,000 of 151,935: 183 us, 227 with two
 // loads a vector instead of the stage).
 // Five thread blocks per SM: 99 us for 1,024 rows, 104 with four; staged six, 4% before five;
-// a warp per row four: 32,768 rows of 1,001 38 us, 41 with five, which spill.
+// one or two warps per row four, which spill a little (52 bytes a thread): 32,768 rows of 1,000
+// 27.3 us, 28.2 with five, which spill more, 33.5 with three, which do not.
 // kStep: threads to an item: a block's, or one or two warps'.
 // kStaged: through shared memory.
 template <typename T, int kStep, bool kStaged>
@@ -1207,8 +1208,10 @@ cudaError_t stats_run(const TokenStatsArgs& a, const DeviceInfo& d, cudaStream_t
   // A warp per row where the rows are short and many; by warps and by thread blocks, without
   // alternatives, with 5 and with 20 (bf16, us): 600 rows of 2 KB 2.5 and 4.2, 4.4 and 7.8, 5.6
   // and 8.3; 1,200 of 8 KB 4.0 and 7.7, 7.1 and 14.2, 9.7 and 14.8; 300 of 8 KB 3.8 and 3.2,
-  // 6.8 and 5.4, 9.4 and 5.8; 2,400 of 32 KB 18.1 and 21.6, 25.3 and 32.8, 31.2 and 34.3 (with
-  // 32 44 and 36); 4,800 of 64 KB 51 and 61, 93 and 86, 96 and 89; 3,600 of 128 KB 85 and 76.
+  // 6.8 and 5.4, 9.4 and 5.8; 2,400 of 32 KB 18.1 and 21.6, 25.3 and 32.8, 31.2 and 34.3;
+  // 4,800 of 64 KB 51 and 61, 93 and 86, 96 and 89; 3,600 of 128 KB 85 and 76.  With 32
+  // alternatives, which more of the rows' candidates reach: 1,200 of 8 KB 10.9 and 15.7; 2,400 of
+  // 16 KB 28 and 30; 4,000 of 32 KB 62 and 57, 8,000 102 and 108, 16,000 183 and 212.
   // Rows of which a block's sets have a few elements each always (8 rows of 1 KB 2.3 and 2.6,
   // 3.9 and 4.7, 5.2 and 20).
   const int64_t row_bytes = a.V * (int64_t)sizeof(T);
