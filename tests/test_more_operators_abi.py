@@ -250,3 +250,11 @@ def test_adamw_eps_without_a_reciprocal(lib):
     assert _adamw(lib, [], eps=2.0 ** 126) == OK
     for x in (2.0 ** 126 * 1.01, 3e38):
         assert _adamw(lib, [], eps=x) == INVALID, x
+
+
+def test_states_of_a_modules_parameters(n):
+    """parameters() is a generator: every list of the states has an entry for each."""
+    m = torch.nn.Linear(300, 5).bfloat16()
+    for bits in (32, 8):
+        s = n.grpo_adamw_state(m.parameters(), bits, master=True)
+        assert all(len(v) == 2 for v in s.values()), {k: len(v) for k, v in s.items()}

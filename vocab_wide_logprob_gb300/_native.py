@@ -695,6 +695,7 @@ def grpo_adamw_state(params, bits=32, master=False):
     the others), which are then what is updated."""
     if bits not in (8, 32):
         raise ValueError("bits must be 8 or 32")
+    params = list(params)  # (a module's parameters() can be gone through once)
     kind = torch.float32 if bits == 32 else torch.float8_e4m3fn
 
     def zeros():
