@@ -444,8 +444,8 @@ __device__ __forceinline__ void chunk_step(W* param, float* master, const G* gra
   }
 }
 
-// Thread blocks per SM: with 8-bit states the arithmetic (some 50 instructions an element)
-// fills half the issue slots, and what hides the loads and the two reductions is other
+// Thread blocks per SM: with 8-bit states the arithmetic (53 to 73 instructions an element,
+// by the types) fills 60 to 70% of the issue slots, and what hides the loads and the two reductions is other
 // warps: 494 M elements take 994 us with six blocks (some registers spilled), 1,155 with
 // five, 1,263 with four (with masters five and six are within 2%).  Loads ahead of their use cost
 // more than they hide: before the root took any v', 1,084 us with four blocks that fetch a unit
